@@ -384,6 +384,28 @@ int pa_decode_append(void *out, const void *q, const void *key, const void *valu
                      size_t workspace_bytes, void *stream);
 
 /*
+ * pa_decode_window -- decode under a sliding window with a few first tokens
+ * that stay visible (sinks): pa_decode's attention over the keys j of
+ * sequence s with
+ *   j < seq_lens[s]  and  (j < sinks  or  j >= seq_lens[s] - window).
+ * Only the blocks that hold a visible key are read, and only their entries of
+ * block_tables: a cache manager may free the blocks between the sinks and the
+ * window and leave anything in their entries.  Slots without a visible key
+ * may hold anything, NaN included.
+ *   window  >= 1 (the query's own key counts); sinks >= 0; together they may
+ *           exceed the sequence, which is then attended whole
+ * Head dims 64 and 128, groups, outputs and device errors as pa_decode.  No
+ * workspace: the split over the keys is joined inside the launch's clusters,
+ * always in the same order, so equal calls give equal bits and calls may
+ * overlap freely.
+ */
+int pa_decode_window(void *out, const void *q, const void *k_cache, const void *v_cache,
+                     const int32_t *block_tables, int max_blocks_per_seq,
+                     const int32_t *seq_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+                     int head_dim, int block_size, int64_t num_blocks, int window, int sinks,
+                     float scale, float *out_lse, void *stream);
+
+/*
  * Size of the static device scratch behind pa_decode_noalloc (8 MiB).
  */
 #define PA_NOALLOC_SCRATCH_BYTES (8u << 20)

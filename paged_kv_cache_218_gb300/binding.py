@@ -69,6 +69,8 @@ _SIGS = {
     "pa_hybrid_attention_append": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _P,
                                     _P, _P, _P, _P, _P, _I, _P, _I, _P, _L, _L,
                                     _P, _P, _I, _I, _I, _I, _L, _F, _I, _P, _S, _P], _I),
+    "pa_decode_window": ([_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _L, _I, _I, _F, _P, _P],
+                         _I),
     "pa_test_decode_stalled": ([_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _L, _F, _I, _P,
                                 _S, ctypes.c_uint, _P], _I),
     "pa_test_prefill_stalled": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
@@ -114,6 +116,29 @@ def _need(t: torch.Tensor, name: str, dtype, dims: Optional[int] = None, contigu
         raise ValueError(f"{name} must have {dims} dims, got {t.dim()}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+
+
+def _same(name: str, t: torch.Tensor, shape) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _int32(name: str, v, least: int) -> int:
+    """An int argument of the C call: ctypes would wrap a larger one silently."""
+    v = int(v)
+    if not least <= v <= 0x7FFFFFFF:
+        raise ValueError(f"{name} must be in [{least}, 2**31 - 1], got {v}")
+    return v
+
+
+def _one_device(first: torch.Tensor, *others) -> None:
+    """Every tensor on the device of the first, and that the current one (the
+    call is queued on a stream of the current device)."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors on {first.device}, current device {torch.cuda.current_device()}")
 
 
 def pa_status_string(status: int) -> str:
@@ -297,6 +322,33 @@ def pa_decode_append(out, q, key, value, k_cache, v_cache, block_tables, seq_len
         _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
         block_tables.shape[1], _ptr(seq_lens), S, Hq, Hkv, D, bs, nb, float(scale),
         int(partition_tokens), _ptr(out_lse), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def pa_decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, window, sinks, scale,
+                     out_lse=None, stream=None) -> None:
+    """Decode over each sequence's last `window` keys and first `sinks` keys;
+    table entries of blocks without a visible key are not read."""
+    _need(out, "out", torch.bfloat16, 3)
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    S, Hq, D = q.shape
+    nb, bs, Hkv, Dk = k_cache.shape
+    _same("out", out, q.shape)
+    _same("v_cache", v_cache, k_cache.shape)
+    if Dk != D or block_tables.shape[0] != S or seq_lens.shape[0] != S:
+        raise ValueError("q, k_cache, block_tables and seq_lens do not fit together")
+    if out_lse is not None:
+        _need(out_lse, "out_lse", torch.float32, 2)
+        _same("out_lse", out_lse, (S, Hq))
+    _one_device(q, out, k_cache, v_cache, block_tables, seq_lens, out_lse)
+    _check("pa_decode_window", _lib.pa_decode_window(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+        block_tables.shape[1], _ptr(seq_lens), S, Hq, Hkv, D, bs, nb,
+        _int32("window", window, 1), _int32("sinks", sinks, 0), float(scale), _ptr(out_lse),
+        _stream(stream)))
 
 
 def pa_decode_noalloc(out, q, k_cache, v_cache, block_tables, seq_lens, scale, out_lse=None,

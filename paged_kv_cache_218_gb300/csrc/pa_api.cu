@@ -1224,6 +1224,50 @@ int pa_hybrid_attention_append(
              : PA_ERR_CUDA;
 }
 
+int pa_decode_window(void* out, const void* q, const void* k_cache, const void* v_cache,
+                     const int32_t* block_tables, int max_blocks_per_seq,
+                     const int32_t* seq_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+                     int head_dim, int block_size, int64_t num_blocks, int window, int sinks,
+                     float scale, float* out_lse, void* stream) {
+  if (int rc = check_shape(num_q_heads, num_kv_heads, head_dim, block_size)) return rc;
+  if (num_seqs < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || window < 1 || sinks < 0)
+    return PA_ERR_INVALID;
+  if (num_blocks * kBlockSize > (int64_t)INT32_MAX || max_blocks_per_seq > INT32_MAX / kBlockSize)
+    return PA_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || !isfinite(scale)) return PA_ERR_INVALID;
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens) return PA_ERR_INVALID;
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(block_tables, 4) || !aligned(seq_lens, 4) || (out_lse && !aligned(out_lse, 4)))
+    return PA_ERR_INVALID;
+  if (static_cast<int64_t>(num_seqs) * num_kv_heads > INT32_MAX / kMaxWindowSplit)
+    return PA_ERR_UNSUPPORTED;
+  DeviceInfo* d;
+  if (int rc = current_device_info(&d)) return rc;
+  WindowDecodeArgs a{};
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k_cache);
+  a.v = static_cast<const __nv_bfloat16*>(v_cache);
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.out_lse = out_lse;
+  a.err = d->err;
+  a.num_blocks = num_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = num_q_heads / num_kv_heads;
+  a.window = window;
+  a.sinks = sinks;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  return launch_decode_window(a, head_dim, d->num_sms, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
 int pa_test_decode_stalled(void* out, const void* q, const void* k_cache, const void* v_cache,
                            const int32_t* block_tables, int max_blocks_per_seq,
                            const int32_t* seq_lens, int num_seqs, int num_q_heads,

@@ -1,0 +1,382 @@
+// pa_window_decode.cu -- paged decode attention over a sliding window and a
+// few first tokens that stay visible (sm_103a).
+//
+// One query per sequence, GQA group G <= 8.  With n = seq_len, window W and S
+// sinks, query head h sees the keys j < n with j < S or j >= n - W:
+//
+//   out = sum_j 2^(c x_j - m) v_j / sum_j 2^(c x_j - m),  x_j = <q, k_j>,
+//   c = scale * log2(e), m a running reference maximum.
+//
+// What bounds it: HBM.  Every visible K/V row is read once (4 D bytes per key
+// and kv head against 4 D G multiply-adds), so the kernel's job is to keep
+// enough bytes in flight.  A warp owns one kv head and walks 16-token blocks;
+// the block's K and V rows go from global memory straight into registers (16
+// bytes per lane and load, 64 registers = 8 KB per warp in flight at head_dim
+// 128), with the next block's K loads issued as soon as this block's scores
+// are done and its V loads as soon as its P V is.  There is no shared-memory
+// staging, because the contraction order of a dot product is free: a lane
+// hands the tensor core the 16-byte pieces it loaded, and the query operand
+// is permuted the same way.
+//
+//   scores  S^T (16 keys x 8 heads) = K (A, 16 keys x 16 d) Q^T (B)
+//           lane (g, t) = (lane / 4, lane % 4) holds keys g and g + 8, columns
+//           [8 (4 j + t), + 8) for j < D / 32;
+//   output  O^T (16 d x 8 heads) = V^T (A, 16 d x 16 keys) P^T (B)
+//           lane (g, t) holds keys 2t, 2t + 1, 2t + 8, 2t + 9, columns
+//           [8 (8 h + g), + 8) for h < D / 64; byte permutes pair two keys of
+//           one column into an A register.
+//
+// P enters the tensor core as a sum of two bf16 numbers (p = hi + lo, relative
+// error 2^-17), so that the output is rounded to bf16 once, at the end; the
+// second product costs 8 of 24 MMAs of a block that waits for memory anyway.
+// Scores, statistics and accumulators are fp32.
+//
+// Split over the key axis: the warps of a CTA, and the CTAs of a cluster (up
+// to kMaxSplit), take a sequence's blocks in turn; their (m, l, O) are joined
+// in shared memory, then across the cluster through distributed shared memory.
+// So the call needs no workspace, and its result does not depend on timing.
+#include <math.h>
+
+#include <algorithm>
+
+#include "../../include/pa.h"
+#include "pa_internal.h"
+#include "pa_ptx.cuh"
+
+namespace pa {
+namespace {
+
+// Lowest reference maximum (log2 units): a row whose scores are all -inf keeps
+// it, so its weights are 0 rather than NaN.
+constexpr float kFloor = -1e30f;
+// The reference maximum moves only when a score passes it by this much (log2
+// units): p stays below 2^8 and most blocks need no cross-lane maximum.
+constexpr float kMoveThreshold = 8.f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(reinterpret_cast<uint64_t>(p)));
+  return v;
+}
+
+__device__ __forceinline__ float ld_dsmem(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float bf16_round(float x) {
+  return __bfloat162float(__float2bfloat16(x));
+}
+
+// Shared memory: the warps' partial outputs [warps][8 heads][D], their maxima
+// and sums [warps][8] each, then the CTA's joined output [8][D], maxima [8]
+// and sums [8] (read by the cluster's other CTAs).
+template <int D>
+__host__ __device__ constexpr int window_smem_floats(int warps) {
+  return warps * (8 * D + 16) + 8 * D + 16;
+}
+
+template <int D, int W>
+__global__ void __launch_bounds__(32 * W, 16 / W) decode_window_kernel(const WindowDecodeArgs a) {
+  constexpr int KJ = D / 32;  // 16-byte pieces of a K row per lane
+  constexpr int VH = D / 64;  // 16-byte pieces of a V row per lane
+  extern __shared__ __align__(16) float sm[];
+  float* const sm_o = sm;
+  float* const sm_m = sm_o + W * 8 * D;
+  float* const sm_l = sm_m + W * 8;
+  float* const cta_o = sm_l + W * 8;
+  float* const cta_m = cta_o + 8 * D;
+  float* const cta_l = cta_m + 8;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int splits = a.splits;
+  const int rank = static_cast<int>(blockIdx.x) % splits;
+  const int unit = static_cast<int>(blockIdx.x) / splits;
+  const int kvh = unit % a.num_kv_heads;
+  const int s = unit / a.num_kv_heads;
+  const int G = a.group;
+
+  griddep_launch_dependents();
+  griddep_wait();
+
+  // q: head g of the group, the columns of this lane's K pieces
+  uint4 qf[KJ];
+  const __nv_bfloat16* qrow =
+      a.q + (static_cast<int64_t>(s) * a.num_q_heads + kvh * G + (g < G ? g : 0)) * D;
+#pragma unroll
+  for (int j = 0; j < KJ; ++j) {
+    qf[j] = *reinterpret_cast<const uint4*>(qrow + 8 * (4 * j + t));
+    if (g >= G) qf[j] = make_uint4(0, 0, 0, 0);
+  }
+
+  int n = a.seq_lens[s];
+  const int cap = a.max_blocks * kBlockSize;
+  if (n < 0 || n > cap) {
+    if (threadIdx.x == 0 && rank == 0 && kvh == 0) atomicOr(a.err, PA_DEVERR_SEQ_LEN);
+    n = n < 0 ? 0 : cap;
+  }
+  const int lo = n > a.window ? n - a.window : 0;  // first key of the window
+  const int ns = a.sinks < n ? a.sinks : n;        // visible sinks
+  const int nsb = (ns + kBlockSize - 1) / kBlockSize;
+  const int b_first = max(lo / kBlockSize, nsb);   // first block behind the sinks'
+  const int nb = (n + kBlockSize - 1) / kBlockSize;
+  const int nv = nsb + (nb > b_first ? nb - b_first : 0);  // visible blocks
+  const int stride = splits * W;
+  const int first = rank * W + warp;
+
+  const int64_t tok_bytes = static_cast<int64_t>(a.num_kv_heads) * D * 2;
+  const char* const kbase = reinterpret_cast<const char*>(a.k) + kvh * (D * 2) + t * 16;
+  const char* const vbase = reinterpret_cast<const char*>(a.v) + kvh * (D * 2) + g * 16;
+  const int32_t* const table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks;
+
+  float o[4 * VH][4];
+#pragma unroll
+  for (int i = 0; i < 4 * VH; ++i)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
+  float m0 = kFloor, m1 = kFloor, l0 = 0.f, l1 = 0.f;  // heads 2t, 2t + 1
+
+  // The block of visible index vb; its id, read 32 of this warp's blocks at a
+  // time (lane i holds the id of its block first + i * stride).
+  auto real_block = [&](int vb) { return vb < nsb ? vb : vb - nsb + b_first; };
+  int ids = 0;
+  auto read_ids = [&](int vb) {
+    const int mine = vb + lane * stride;
+    ids = 0;
+    if (mine < nv) {
+      ids = table[real_block(mine)];
+      if (ids < 0 || ids >= a.num_blocks) {
+        atomicOr(a.err, PA_DEVERR_BLOCK_ID);
+        ids = -1;  // reads as zeros
+      }
+    }
+  };
+  uint4 kr[2][KJ], vr[4][VH];
+  auto load_k = [&](int id) {
+    const char* p = kbase + (static_cast<int64_t>(id) * kBlockSize + g) * tok_bytes;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int j = 0; j < KJ; ++j)
+        kr[r][j] = id < 0 ? make_uint4(0, 0, 0, 0) : ld_stream(p + r * 8 * tok_bytes + j * 64);
+  };
+  auto load_v = [&](int id) {
+    const char* p = vbase + (static_cast<int64_t>(id) * kBlockSize + 2 * t) * tok_bytes;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int h = 0; h < VH; ++h)
+        vr[r][h] = id < 0 ? make_uint4(0, 0, 0, 0)
+                          : ld_stream(p + ((r & 1) + (r >> 1) * 8) * tok_bytes + h * 128);
+  };
+
+  if (first < nv) {
+    read_ids(first);
+    int id = __shfl_sync(0xffffffffu, ids, 0);
+    load_k(id);
+    load_v(id);
+  }
+  int it = 0;  // position of this block's id in the batch of 32
+  for (int vb = first; vb < nv; vb += stride) {
+    const int j0 = real_block(vb) * kBlockSize;
+    // ---- scores of 16 keys x 8 heads
+    float sc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < KJ; ++j) {
+      const uint32_t a0[4] = {kr[0][j].x, kr[1][j].x, kr[0][j].y, kr[1][j].y};
+      mma_bf16_16816(sc, a0, qf[j].x, qf[j].y);
+      const uint32_t a1[4] = {kr[0][j].z, kr[1][j].z, kr[0][j].w, kr[1][j].w};
+      mma_bf16_16816(sc, a1, qf[j].z, qf[j].w);
+    }
+    // ---- the next block's K
+    const int next = vb + stride;
+    int id = 0;
+    if (next < nv) {
+      if (++it == 32) {
+        read_ids(next);
+        it = 0;
+      }
+      id = __shfl_sync(0xffffffffu, ids, it);
+      load_k(id);
+    }
+    // ---- mask (first or last block of the window, last block of the sinks):
+    // hidden keys get weight 0 and their V rows, which may hold anything, 0
+    const bool edge = !(j0 + kBlockSize <= n && (j0 >= lo || j0 + kBlockSize <= ns));
+    float x0 = sc[0] * a.scale_log2, x1 = sc[1] * a.scale_log2;
+    float x2 = sc[2] * a.scale_log2, x3 = sc[3] * a.scale_log2;
+    if (edge) {
+      auto seen = [&](int j) { return j < n && (j >= lo || j < ns); };
+      if (!seen(j0 + g)) x0 = x1 = -INFINITY;
+      if (!seen(j0 + g + 8)) x2 = x3 = -INFINITY;
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (!seen(j0 + 2 * t + (r & 1) + (r >> 1) * 8))
+#pragma unroll
+          for (int h = 0; h < VH; ++h) vr[r][h] = make_uint4(0, 0, 0, 0);
+    }
+    // ---- reference maximum
+    float b0 = fmaxf(x0, x2), b1 = fmaxf(x1, x3);
+    if (__any_sync(0xffffffffu, b0 > m0 + kMoveThreshold || b1 > m1 + kMoveThreshold)) {
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) {
+        b0 = fmaxf(b0, __shfl_xor_sync(0xffffffffu, b0, off));
+        b1 = fmaxf(b1, __shfl_xor_sync(0xffffffffu, b1, off));
+      }
+      b0 = fmaxf(b0, m0);
+      b1 = fmaxf(b1, m1);
+      const float s0 = fast_exp2(m0 - b0), s1 = fast_exp2(m1 - b1);
+      m0 = b0;
+      m1 = b1;
+      l0 *= s0;
+      l1 *= s1;
+#pragma unroll
+      for (int i = 0; i < 4 * VH; ++i) {
+        o[i][0] *= s0;
+        o[i][1] *= s1;
+        o[i][2] *= s0;
+        o[i][3] *= s1;
+      }
+    }
+    const float p0 = fast_exp2(x0 - m0), p1 = fast_exp2(x1 - m1);
+    const float p2 = fast_exp2(x2 - m0), p3 = fast_exp2(x3 - m1);
+    l0 += p0 + p2;
+    l1 += p1 + p3;
+    // P^T as the B operand: keys 2t, 2t + 1 (and + 8) of head g
+    const uint32_t hi0 = movmatrix_trans(pack_bf16x2(p0, p1));
+    const uint32_t hi1 = movmatrix_trans(pack_bf16x2(p2, p3));
+    const uint32_t lo0 = movmatrix_trans(pack_bf16x2(p0 - bf16_round(p0), p1 - bf16_round(p1)));
+    const uint32_t lo1 = movmatrix_trans(pack_bf16x2(p2 - bf16_round(p2), p3 - bf16_round(p3)));
+#pragma unroll
+    for (int h = 0; h < VH; ++h) {
+      const uint32_t r0[4] = {vr[0][h].x, vr[0][h].y, vr[0][h].z, vr[0][h].w};
+      const uint32_t r1[4] = {vr[1][h].x, vr[1][h].y, vr[1][h].z, vr[1][h].w};
+      const uint32_t r2[4] = {vr[2][h].x, vr[2][h].y, vr[2][h].z, vr[2][h].w};
+      const uint32_t r3[4] = {vr[3][h].x, vr[3][h].y, vr[3][h].z, vr[3][h].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t av[4] = {prmt(r0[i], r1[i], 0x5410), prmt(r0[i], r1[i], 0x7632),
+                                prmt(r2[i], r3[i], 0x5410), prmt(r2[i], r3[i], 0x7632)};
+        mma_bf16_16816(o[4 * h + i], av, hi0, hi1);
+        mma_bf16_16816(o[4 * h + i], av, lo0, lo1);
+      }
+    }
+    // ---- the next block's V
+    if (next < nv) load_v(id);
+  }
+
+  // ---- join the CTA's warps
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    l0 += __shfl_xor_sync(0xffffffffu, l0, off);
+    l1 += __shfl_xor_sync(0xffffffffu, l1, off);
+  }
+  if (g == 0) {
+    sm_m[warp * 8 + 2 * t] = m0;
+    sm_m[warp * 8 + 2 * t + 1] = m1;
+    sm_l[warp * 8 + 2 * t] = l0;
+    sm_l[warp * 8 + 2 * t + 1] = l1;
+  }
+#pragma unroll
+  for (int h = 0; h < VH; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // rows g, g + 8 of the tile are columns 8 (8 h + g) + 2 i, + 1
+      const int d = 8 * (8 * h + g) + 2 * i;
+      float2* dst = reinterpret_cast<float2*>(sm_o + (warp * 8 + 2 * t) * D + d);
+      dst[0] = make_float2(o[4 * h + i][0], o[4 * h + i][2]);
+      dst[D / 2] = make_float2(o[4 * h + i][1], o[4 * h + i][3]);
+    }
+  __syncthreads();
+  for (int e = threadIdx.x; e < G * D; e += 32 * W) {
+    const int h = e / D, d = e % D;
+    float m = kFloor;
+#pragma unroll
+    for (int w = 0; w < W; ++w) m = fmaxf(m, sm_m[w * 8 + h]);
+    float acc = 0.f, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float f = fast_exp2(sm_m[w * 8 + h] - m);
+      acc += f * sm_o[(w * 8 + h) * D + d];
+      l += f * sm_l[w * 8 + h];
+    }
+    if (splits == 1) {
+      const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + kvh * G + h;
+      a.out[row * D + d] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
+      if (d == 0 && a.out_lse) a.out_lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    } else {
+      cta_o[e] = acc;
+      if (d == 0) {
+        cta_m[h] = m;
+        cta_l[h] = l;
+      }
+    }
+  }
+  if (splits == 1) return;
+
+  // ---- join the cluster's CTAs: CTA r writes every splits-th element
+  cluster_sync();
+  const uint32_t ro = smem_u32(cta_o), rm = smem_u32(cta_m), rl = smem_u32(cta_l);
+  for (int e = rank * 32 * W + threadIdx.x; e < G * D; e += splits * 32 * W) {
+    const int h = e / D, d = e % D;
+    float m = kFloor;
+    for (int c = 0; c < splits; ++c) m = fmaxf(m, ld_dsmem(mapa_shared(rm + 4 * h, c)));
+    float acc = 0.f, l = 0.f;
+    for (int c = 0; c < splits; ++c) {
+      const float f = fast_exp2(ld_dsmem(mapa_shared(rm + 4 * h, c)) - m);
+      acc += f * ld_dsmem(mapa_shared(ro + 4 * e, c));
+      l += f * ld_dsmem(mapa_shared(rl + 4 * h, c));
+    }
+    const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + kvh * G + h;
+    a.out[row * D + d] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
+    if (d == 0 && a.out_lse) a.out_lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+  cluster_sync();  // no CTA leaves while another may still read its shared memory
+}
+
+template <int D, int W>
+cudaError_t launch(const WindowDecodeArgs& a, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * a.num_kv_heads *
+                                           a.splits));
+  cfg.blockDim = dim3(32 * W);
+  cfg.dynamicSmemBytes = window_smem_floats<D>(W) * sizeof(float);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = a.splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.splits > 1 ? 2 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_window_kernel<D, W>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_decode_window(WindowDecodeArgs a, int head_dim, int num_sms,
+                                 cudaStream_t stream) {
+  // Blocks that a sequence can attend at most, and how many warps each
+  // (sequence, kv head) gets: enough that all of them fill the SMs' 16 warp
+  // slots (128 registers a thread), no more than there are blocks.
+  const int64_t visible = std::min<int64_t>(
+      a.max_blocks, (static_cast<int64_t>(a.sinks) + kBlockSize - 1) / kBlockSize +
+                        (static_cast<int64_t>(a.window) + kBlockSize - 1) / kBlockSize + 1);
+  const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+  const int64_t want = std::min<int64_t>(visible, (static_cast<int64_t>(num_sms) * 16 + units - 1) / units);
+  const bool wide = want > 4;
+  const int w = wide ? 8 : 4;
+  a.splits = 1;
+  while (a.splits < kMaxWindowSplit && a.splits * w < want) a.splits *= 2;
+  if (head_dim == 128) return wide ? launch<128, 8>(a, stream) : launch<128, 4>(a, stream);
+  return wide ? launch<64, 8>(a, stream) : launch<64, 4>(a, stream);
+}
+
+}  // namespace pa
