@@ -406,6 +406,98 @@ int pa_decode_window(void *out, const void *q, const void *k_cache, const void *
                      float scale, float *out_lse, void *stream);
 
 /*
+ * Rotary frequencies for pa_qk_norm_rope_cache, computed on the host (host
+ * pointers): increments[i], i < rot_dim / 2, is pair i's frequency as a
+ * fixed-point number of turns per position, in units of 2^-64 turn, so that
+ * position * increment modulo 2^64 is the exact phase of any position.  The
+ * caller copies them to the device once.  Base frequencies are
+ * f_i = base^(-2 i / rot_dim) radians per position; `scaling` stretches them
+ * for contexts `factor` times longer:
+ *   PA_ROPE_NONE        f_i (factor ignored)
+ *   PA_ROPE_LINEAR      f_i / factor (position interpolation)
+ *   PA_ROPE_NTK         f_i with base * factor^(rot_dim / (rot_dim - 2))
+ *   PA_ROPE_YARN        by parts (Peng et al., "YaRN"): f_i (1 - r_i) +
+ *                       f_i / factor r_i, r_i rising linearly from 0 to 1 over
+ *                       the pairs that make param0 (usually 32) to param1
+ *                       (usually 1) turns over original_context positions;
+ *                       the rotated values are scaled by 0.1 ln(factor) + 1
+ *   PA_ROPE_WAVELENGTH  by parts over the turns t_i = original_context f_i /
+ *                       (2 pi): f_i / factor for t_i <= param0 (usually 1),
+ *                       f_i for t_i >= param1 (usually 4), linear in t_i between
+ * *rope_factor is the scale of the rotated values (1 except for YARN).
+ * rot_dim: a multiple of 16 up to 256; base > 1; factor >= 1; the last three
+ * arguments are read by YARN (param0 > param1 > 0) and WAVELENGTH (param1 >
+ * param0 > 0) only.
+ */
+typedef enum pa_rope_scaling {
+  PA_ROPE_NONE = 0,
+  PA_ROPE_LINEAR = 1,
+  PA_ROPE_NTK = 2,
+  PA_ROPE_YARN = 3,
+  PA_ROPE_WAVELENGTH = 4
+} pa_rope_scaling;
+int pa_rope_increments(int64_t *increments, float *rope_factor, int rot_dim, double base,
+                       int scaling, double factor, double original_context, double param0,
+                       double param1);
+
+/*
+ * Norms of queries and keys for each head, the position rotation, and the
+ * slot scatter, in one pass over the projections' output:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight   for each query / key head (the
+ *       mean over head_dim; a NULL weight: no norm, y = x)
+ *   rotation of y's first rot_dim columns by u_i = positions[t] * freq_i:
+ *       (a, b) -> rope_factor * (a cos u_i - b sin u_i, b cos u_i + a sin u_i),
+ *       pairs (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved is non-zero;
+ *       the other columns pass through
+ *   queries -> q_out; keys -> their slot of k_cache (and k_out); values, as
+ *       they are -> their slot of v_cache.
+ * All arithmetic is fp32 with one rounding to bf16 at the end (sums of
+ * squares must stay finite in fp32).
+ *   q_out      device bf16 [num_tokens, num_q_heads, head_dim]; may be q
+ *              itself where q is contiguous
+ *   k_out      device bf16 [num_tokens, num_kv_heads, head_dim] or NULL: the
+ *              rotated keys, as pa_decode_append and pa_hybrid_attention_append
+ *              take them; may be k itself where k is contiguous
+ *   q, k, v    device bf16, row t at + t * token stride (elements, a multiple
+ *              of 8; heads contiguous), so one fused projection's output serves
+ *   q_weight, k_weight  device fp32 [head_dim] (16-byte aligned) or NULL
+ *   positions  device int64 [num_tokens], any value
+ *   increments device int64 [rot_dim / 2] (pa_rope_increments); rot_dim 0: no
+ *              rotation, positions and increments unused (may be NULL)
+ *   k_cache, v_cache, slot_mapping  as pa_reshape_and_cache (a negative slot
+ *              is padding: q_out and k_out are written, the pools are not).
+ *              Both pools NULL: no scatter (v and slot_mapping unused), and
+ *              k_out is required
+ * head_dim: a multiple of 16 up to 256; rot_dim: a multiple of 16 up to
+ * head_dim; any head counts.  Outputs may not overlap inputs otherwise than
+ * as stated (PA_ERR_INVALID).
+ */
+int pa_qk_norm_rope_cache(void *q_out, void *k_out, const void *q, const void *k, const void *v,
+                          int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                          const float *q_weight, const float *k_weight, float eps,
+                          const int64_t *positions, const int64_t *increments, int rot_dim,
+                          int interleaved, float rope_factor, void *k_cache, void *v_cache,
+                          const int64_t *slot_mapping, int num_tokens, int num_q_heads,
+                          int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                          void *stream);
+
+/*
+ * The same into E4M3 pools (uint8, as pa_reshape_and_cache_fp8): code =
+ * E4M3(y / k_scales[h]) of the fp32 key y (not rounded to bf16 in between),
+ * E4M3(v / v_scales[h]) of the value.  The pools are required.
+ */
+int pa_qk_norm_rope_cache_fp8(void *q_out, void *k_out, const void *q, const void *k,
+                              const void *v, int64_t q_token_stride, int64_t k_token_stride,
+                              int64_t v_token_stride, const float *q_weight,
+                              const float *k_weight, float eps, const int64_t *positions,
+                              const int64_t *increments, int rot_dim, int interleaved,
+                              float rope_factor, void *k_cache, void *v_cache,
+                              const int64_t *slot_mapping, const float *k_scales,
+                              const float *v_scales, int num_tokens, int num_q_heads,
+                              int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                              void *stream);
+
+/*
  * Size of the static device scratch behind pa_decode_noalloc (8 MiB).
  */
 #define PA_NOALLOC_SCRATCH_BYTES (8u << 20)

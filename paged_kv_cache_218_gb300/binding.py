@@ -38,6 +38,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _L = ctypes.c_int64
 _F = ctypes.c_float
+_D = ctypes.c_double
 _S = ctypes.c_size_t
 
 _SIGS = {
@@ -69,6 +70,11 @@ _SIGS = {
     "pa_hybrid_attention_append": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _P,
                                     _P, _P, _P, _P, _P, _I, _P, _I, _P, _L, _L,
                                     _P, _P, _I, _I, _I, _I, _L, _F, _I, _P, _S, _P], _I),
+    "pa_rope_increments": ([_P, ctypes.POINTER(_F), _I, _D, _I, _D, _D, _D, _D], _I),
+    "pa_qk_norm_rope_cache": ([_P, _P, _P, _P, _P, _L, _L, _L, _P, _P, _F, _P, _P, _I, _I, _F,
+                               _P, _P, _P, _I, _I, _I, _I, _I, _L, _P], _I),
+    "pa_qk_norm_rope_cache_fp8": ([_P, _P, _P, _P, _P, _L, _L, _L, _P, _P, _F, _P, _P, _I, _I, _F,
+                                   _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _L, _P], _I),
     "pa_decode_window": ([_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _L, _I, _I, _F, _P, _P],
                          _I),
     "pa_test_decode_stalled": ([_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _L, _F, _I, _P,
@@ -322,6 +328,107 @@ def pa_decode_append(out, q, key, value, k_cache, v_cache, block_tables, seq_len
         _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
         block_tables.shape[1], _ptr(seq_lens), S, Hq, Hkv, D, bs, nb, float(scale),
         int(partition_tokens), _ptr(out_lse), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
+
+
+def pa_rope_increments(rot_dim, base=10000.0, scaling="none", factor=1.0, original_context=0.0,
+                       params=None):
+    """Rotary frequencies as fixed-point turns: (int64 CPU tensor [rot_dim / 2],
+    the factor of the rotated values).  `params` defaults to (32, 1) turns for
+    "yarn" and (1, 4) for "wavelength".  Needs no GPU."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
+    p0, p1 = params if params is not None else {"yarn": (32.0, 1.0), "wavelength": (1.0, 4.0)}.get(
+        scaling, (0.0, 0.0))
+    rot_dim = _int32("rot_dim", rot_dim, 0)
+    inc = torch.empty(rot_dim // 2, dtype=torch.int64)
+    f = _F(0.0)
+    _check("pa_rope_increments", _lib.pa_rope_increments(
+        inc.data_ptr(), ctypes.byref(f), rot_dim, float(base), ROPE_SCALINGS[scaling],
+        float(factor), float(original_context), float(p0), float(p1)))
+    return inc, float(f.value)
+
+
+def _norm_rope(fn, pool_dtype, q_out, q, k, v, positions, increments, k_cache, v_cache,
+               slot_mapping, scales, q_weight, k_weight, eps, interleaved, rope_factor, k_out,
+               stream):
+    _need(q, "q", torch.bfloat16, 3, contiguous=False)
+    _need(k, "k", torch.bfloat16, 3, contiguous=False)
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    _need(q_out, "q_out", torch.bfloat16, 3)
+    _same("q_out", q_out, q.shape)
+    _same("k", k, (T, Hkv, D))
+    rows = [(q, "q"), (k, "k")]
+    if k_cache is not None or v_cache is not None or scales:
+        _need(v, "v", torch.bfloat16, 3, contiguous=False)
+        _same("v", v, k.shape)
+        rows.append((v, "v"))
+        _need(k_cache, "k_cache", pool_dtype, 4)
+        _need(v_cache, "v_cache", pool_dtype, 4)
+        _same("v_cache", v_cache, k_cache.shape)
+        _same("k_cache", k_cache, (*k_cache.shape[:2], Hkv, D))
+        _need(slot_mapping, "slot_mapping", torch.int64, 1)
+        _same("slot_mapping", slot_mapping, (T,))
+        nb, bs = k_cache.shape[:2]
+        vp, v_stride = v.data_ptr(), v.stride(0)
+    else:
+        slot_mapping, nb, bs, vp, v_stride = None, 0, 0, None, 0
+    for t, n in rows:
+        if t.stride(2) != 1 or (t.stride(1) != D and t.shape[1] > 1):
+            raise ValueError(f"{n} must be contiguous within a token")
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _need(t, n, torch.float32, 1)
+            _same(n, t, (D,))
+    if k_out is not None:
+        _need(k_out, "k_out", torch.bfloat16, 3)
+        _same("k_out", k_out, k.shape)
+    rot = 0
+    if increments is not None:
+        _need(increments, "increments", torch.int64, 1)
+        _need(positions, "positions", torch.int64, 1)
+        _same("positions", positions, (T,))
+        rot = 2 * increments.shape[0]
+    else:
+        positions = None
+    for t, n in zip(scales, ("k_scales", "v_scales")):
+        _need(t, n, torch.float32, 1)
+        _same(n, t, (Hkv,))
+    _one_device(q, k, v if vp else None, q_out, k_out, k_cache, v_cache, slot_mapping, q_weight,
+                k_weight, positions, increments, *scales)
+    # a single token's stride is never used: any view of one row will do
+    one = T <= 1
+    _check(fn, getattr(_lib, fn)(
+        _ptr(q_out), _ptr(k_out), _ptr(q), _ptr(k), vp, Hq * D if one else q.stride(0),
+        Hkv * D if one else k.stride(0), Hkv * D if one else v_stride, _ptr(q_weight),
+        _ptr(k_weight), float(eps), _ptr(positions), _ptr(increments), rot, int(bool(interleaved)),
+        float(rope_factor), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
+        *(_ptr(t) for t in scales), T, Hq, Hkv, D, bs, nb, _stream(stream)))
+
+
+def pa_qk_norm_rope_cache(q_out, q, k, v, positions, increments, k_cache, v_cache, slot_mapping,
+                          q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                          rope_factor=1.0, k_out=None, stream=None) -> None:
+    """Norms of q [T, Hq, D] and k [T, Hkv, D] per head (weights fp32 [D], None:
+    no norm), rotation of the first 2 * len(increments) columns (None: none),
+    q -> q_out, k -> its slots of k_cache and k_out, v -> its slots of v_cache.
+    With both pools None: no scatter, k_out required."""
+    _norm_rope("pa_qk_norm_rope_cache", torch.bfloat16, q_out, q, k, v, positions, increments,
+               k_cache, v_cache, slot_mapping, (), q_weight, k_weight, eps, interleaved,
+               rope_factor, k_out, stream)
+
+
+def pa_qk_norm_rope_cache_fp8(q_out, q, k, v, positions, increments, k_cache, v_cache,
+                              slot_mapping, k_scales, v_scales, q_weight=None, k_weight=None,
+                              eps=1e-6, interleaved=False, rope_factor=1.0, k_out=None,
+                              stream=None) -> None:
+    """pa_qk_norm_rope_cache into uint8 E4M3 pools with per-kv-head fp32 scales."""
+    _norm_rope("pa_qk_norm_rope_cache_fp8", torch.uint8, q_out, q, k, v, positions, increments,
+               k_cache, v_cache, slot_mapping, (k_scales, v_scales), q_weight, k_weight, eps,
+               interleaved, rope_factor, k_out, stream)
 
 
 def pa_decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, window, sinks, scale,

@@ -1224,6 +1224,155 @@ int pa_hybrid_attention_append(
              : PA_ERR_CUDA;
 }
 
+// Bytes from a tensor's first to one past its last element, rows of `row`
+// elements of `elem` bytes at a token stride.
+static int64_t span_bytes(int64_t rows, int64_t stride, int64_t row, int elem) {
+  return ((rows - 1) * stride + row) * elem;
+}
+
+static bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const char* x = static_cast<const char*>(a);
+  const char* y = static_cast<const char*>(b);
+  return x < y + bn && y < x + an;
+}
+
+static int norm_rope_impl(void* q_out, void* k_out, const void* q, const void* k, const void* v,
+                          int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                          const float* q_weight, const float* k_weight, float eps,
+                          const int64_t* positions, const int64_t* increments, int rot_dim,
+                          int interleaved, float rope_factor, void* k_cache, void* v_cache,
+                          const int64_t* slots, bool fp8, const float* k_scales,
+                          const float* v_scales, int num_tokens, int Hq, int Hkv, int D,
+                          int block_size, int64_t num_blocks, void* stream) {
+  if (num_tokens < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || rot_dim < 0 || rot_dim > D)
+    return PA_ERR_INVALID;
+  if (D % 16 != 0 || D > 256 || rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
+  if (Hq > (1 << 20) || Hkv > (1 << 20)) return PA_ERR_UNSUPPORTED;
+  if ((q_weight || k_weight) && (!(eps >= 0.f) || !isfinite(eps))) return PA_ERR_INVALID;
+  if (rot_dim > 0 && !isfinite(rope_factor)) return PA_ERR_INVALID;
+  const bool pools = k_cache || v_cache;
+  if (pools || fp8) {
+    if (block_size <= 0 || num_blocks <= 0) return PA_ERR_INVALID;
+    if (block_size != kBlockSize) return PA_ERR_UNSUPPORTED;
+    if (num_blocks > INT64_MAX / 16 / (static_cast<int64_t>(Hkv) * D * 2)) return PA_ERR_INVALID;
+  }
+  if (num_tokens == 0) return PA_OK;
+  if (!q_out || !q || !k || (!pools && !k_out)) return PA_ERR_INVALID;
+  if ((pools || fp8) && (!k_cache || !v_cache || !v || !slots)) return PA_ERR_INVALID;
+  if (fp8 && (!k_scales || !v_scales || !aligned(k_scales, 4) || !aligned(v_scales, 4)))
+    return PA_ERR_INVALID;
+  if (rot_dim > 0 && (!positions || !increments || !aligned(positions, 8) ||
+                      !aligned(increments, 8)))
+    return PA_ERR_INVALID;
+  const int64_t q_row = static_cast<int64_t>(Hq) * D, k_row = static_cast<int64_t>(Hkv) * D;
+  // (a stride bound keeps every offset below within 64 bits)
+  const int64_t most = int64_t{1} << 30;
+  if (q_stride < q_row || k_stride < k_row || q_stride % 8 || k_stride % 8 || q_stride > most ||
+      k_stride > most)
+    return PA_ERR_INVALID;
+  if (pools && (v_stride < k_row || v_stride % 8 || v_stride > most)) return PA_ERR_INVALID;
+  if (!aligned(q_out, 16) || !aligned(q, 16) || !aligned(k, 16) || (k_out && !aligned(k_out, 16)) ||
+      (q_weight && !aligned(q_weight, 16)) || (k_weight && !aligned(k_weight, 16)))
+    return PA_ERR_INVALID;
+  if (pools && (!aligned(v, 16) || !aligned(slots, 8) || !aligned(k_cache, fp8 ? 8 : 16) ||
+                !aligned(v_cache, fp8 ? 8 : 16)))
+    return PA_ERR_INVALID;
+  // outputs may be an input in place (row for row), and otherwise touch none
+  struct Span {
+    const void* p;
+    int64_t bytes, stride;
+  };
+  const Span in[3] = {{q, span_bytes(num_tokens, q_stride, q_row, 2), q_stride},
+                      {k, span_bytes(num_tokens, k_stride, k_row, 2), k_stride},
+                      {v, pools ? span_bytes(num_tokens, v_stride, k_row, 2) : 0, v_stride}};
+  const Span out[2] = {{q_out, num_tokens * q_row * 2, q_row},
+                       {k_out, k_out ? num_tokens * k_row * 2 : 0, k_row}};
+  for (int o = 0; o < 2; ++o)
+    for (int i = 0; i < 3; ++i) {
+      if (out[o].bytes == 0 || in[i].bytes == 0) continue;
+      const bool in_place = o == i && out[o].p == in[i].p &&
+                            (num_tokens == 1 || in[i].stride == out[o].stride);
+      if (!in_place && overlap(out[o].p, out[o].bytes, in[i].p, in[i].bytes))
+        return PA_ERR_INVALID;
+    }
+  if (k_out && overlap(q_out, out[0].bytes, k_out, out[1].bytes)) return PA_ERR_INVALID;
+  if (pools) {
+    const int64_t pool = num_blocks * kBlockSize * k_row * (fp8 ? 1 : 2);
+    for (const void* p : {k_cache, v_cache}) {
+      for (const Span& x : in)
+        if (x.bytes && overlap(p, pool, x.p, x.bytes)) return PA_ERR_INVALID;
+      for (const Span& x : out)
+        if (x.bytes && overlap(p, pool, x.p, x.bytes)) return PA_ERR_INVALID;
+    }
+    if (overlap(k_cache, pool, v_cache, pool)) return PA_ERR_INVALID;
+  }
+  DeviceInfo* d;
+  if (int rc = current_device_info(&d)) return rc;
+  RopeArgs a{};
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.positions = positions;
+  a.increments = increments;
+  a.slots = slots;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.err = d->err;
+  a.num_slots = num_blocks * kBlockSize;
+  a.eps = eps;
+  a.rope_factor = rope_factor;
+  a.num_tokens = num_tokens;
+  a.num_q_heads = Hq;
+  a.num_kv_heads = Hkv;
+  a.head_dim = D;
+  a.rot_dim = rot_dim;
+  return launch_norm_rope(a, interleaved != 0, fp8, d->num_sms,
+                          static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+int pa_qk_norm_rope_cache(void* q_out, void* k_out, const void* q, const void* k, const void* v,
+                          int64_t q_token_stride, int64_t k_token_stride, int64_t v_token_stride,
+                          const float* q_weight, const float* k_weight, float eps,
+                          const int64_t* positions, const int64_t* increments, int rot_dim,
+                          int interleaved, float rope_factor, void* k_cache, void* v_cache,
+                          const int64_t* slot_mapping, int num_tokens, int num_q_heads,
+                          int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                          void* stream) {
+  return norm_rope_impl(q_out, k_out, q, k, v, q_token_stride, k_token_stride, v_token_stride,
+                        q_weight, k_weight, eps, positions, increments, rot_dim, interleaved,
+                        rope_factor, k_cache, v_cache, slot_mapping, false, nullptr, nullptr,
+                        num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                        stream);
+}
+
+int pa_qk_norm_rope_cache_fp8(void* q_out, void* k_out, const void* q, const void* k,
+                              const void* v, int64_t q_token_stride, int64_t k_token_stride,
+                              int64_t v_token_stride, const float* q_weight,
+                              const float* k_weight, float eps, const int64_t* positions,
+                              const int64_t* increments, int rot_dim, int interleaved,
+                              float rope_factor, void* k_cache, void* v_cache,
+                              const int64_t* slot_mapping, const float* k_scales,
+                              const float* v_scales, int num_tokens, int num_q_heads,
+                              int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                              void* stream) {
+  return norm_rope_impl(q_out, k_out, q, k, v, q_token_stride, k_token_stride, v_token_stride,
+                        q_weight, k_weight, eps, positions, increments, rot_dim, interleaved,
+                        rope_factor, k_cache, v_cache, slot_mapping, true, k_scales, v_scales,
+                        num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, num_blocks,
+                        stream);
+}
+
 int pa_decode_window(void* out, const void* q, const void* k_cache, const void* v_cache,
                      const int32_t* block_tables, int max_blocks_per_seq,
                      const int32_t* seq_lens, int num_seqs, int num_q_heads, int num_kv_heads,

@@ -44,3 +44,110 @@ DECODE_T = dict(zip(DECODE, [V, V, V, V, V, I, V, I, I, I, I, I, L, I, I, F, V, 
     (dict(lse=P + 2), INVALID)])
 def test_decode_window_refuses(lib, change, want):
     assert call(lib.pa_decode_window, DECODE, DECODE_T, **change) == want
+
+
+B = 1 << 20  # stand-ins far enough apart
+ROPE = dict(q_out=B, k_out=None, q=2 * B, k=3 * B, v=4 * B, qs=1024, ks=256, vs=256, qw=None,
+            kw=None, eps=1e-6, pos=5 * B, inc=6 * B, rot=128, il=0, factor=1.0, kc=7 * B,
+            vc=20 * B, slots=40 * B, T=4, Hq=8, Hkv=2, D=128, bs=16, nb=64, stream=None)
+ROPE_T = dict(zip(ROPE, [V, V, V, V, V, L, L, L, V, V, F, V, V, I, I, F, V, V, V, I, I, I, I, I, L,
+                         V]))
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(T=-1), INVALID), (dict(Hq=0), INVALID), (dict(Hkv=-1), INVALID), (dict(D=0), INVALID),
+    (dict(rot=-16), INVALID), (dict(rot=144), INVALID), (dict(D=72, rot=16), UNSUPPORTED),
+    (dict(D=272), UNSUPPORTED), (dict(rot=24), UNSUPPORTED), (dict(bs=8), UNSUPPORTED),
+    (dict(nb=0), INVALID), (dict(nb=1 << 62), INVALID), (dict(qw=B, eps=-1.0), INVALID),
+    (dict(kw=B, eps=float("inf")), INVALID), (dict(factor=float("nan")), INVALID),
+    (dict(T=0), OK), (dict(T=0, q=None, q_out=None), OK),
+    (dict(q=None), INVALID), (dict(k=None), INVALID), (dict(q_out=None), INVALID),
+    (dict(v=None), INVALID), (dict(slots=None), INVALID), (dict(kc=None), INVALID),
+    (dict(vc=None), INVALID), (dict(pos=None), INVALID), (dict(inc=None), INVALID),
+    (dict(kc=None, vc=None), INVALID),
+    (dict(qs=1016), INVALID), (dict(qs=1028), INVALID), (dict(ks=128), INVALID),
+    (dict(vs=12), INVALID), (dict(qs=1 << 40), INVALID),
+    (dict(q=2 * B + 8), INVALID), (dict(q_out=B + 2), INVALID), (dict(kc=7 * B + 8), INVALID),
+    (dict(qw=B + 4), INVALID), (dict(pos=5 * B + 4), INVALID), (dict(slots=40 * B + 4), INVALID),
+    # overlaps: q_out inside q, over k, half in place, with the pools; the pools with each other
+    (dict(q_out=2 * B + 2048), INVALID), (dict(q_out=3 * B), INVALID),
+    (dict(q_out=2 * B, qs=2048), INVALID), (dict(q_out=7 * B + 4096), INVALID),
+    (dict(k_out=B), INVALID), (dict(vc=7 * B + 16), INVALID), (dict(v=20 * B), INVALID)])
+def test_norm_rope_refuses(lib, change, want):
+    assert call(lib.pa_qk_norm_rope_cache, ROPE, ROPE_T, **change) == want
+
+
+def test_norm_rope_fp8_refuses_missing_scales_and_pools(lib):
+    names = list(ROPE)
+    at = names.index("slots") + 1
+    args = dict(ROPE)
+    full = {k: args[k] for k in names[:at]} | {"kscale": B, "vscale": B} | {
+        k: args[k] for k in names[at:]}
+    types = {**ROPE_T, "kscale": V, "vscale": V}
+    for change in (dict(kscale=None), dict(vscale=None), dict(kscale=B + 2), dict(kc=None),
+                   dict(kc=None, vc=None, k_out=60 * B), dict(kc=7 * B + 4)):
+        assert call(lib.pa_qk_norm_rope_cache_fp8, full, types, **change) == INVALID
+
+
+def _increments(lib, rot, base=10000.0, scaling=0, factor=1.0, ctx=0.0, p0=0.0, p1=0.0):
+    out = (ctypes.c_int64 * max(rot // 2, 1))()
+    f = ctypes.c_float(0)
+    fn = lib.pa_rope_increments
+    fn.argtypes = [V, V, I] + [ctypes.c_double, I] + [ctypes.c_double] * 4
+    fn.restype = ctypes.c_int
+    rc = fn(out, ctypes.byref(f), rot, base, scaling, factor, ctx, p0, p1)
+    return rc, [x / 2.0**64 * 2 * 3.141592653589793 for x in out], f.value
+
+
+def test_rope_increments_follow_their_formulas(lib):
+    import math
+    rot, base = 64, 10000.0
+    plain = [base ** (-2 * i / rot) for i in range(rot // 2)]
+
+    def near(got, want):
+        # doubles: pow and the quotient by 2 pi, a few steps of 2^-52; and the
+        # rounding to whole units of 2^-64 turn: 2 pi 2^-65 = 1.7e-19 radians
+        assert all(abs(a - b) <= 1e-14 * b + 2 * math.pi * 2.0**-65 for a, b in zip(got, want))
+
+    rc, f, s = _increments(lib, rot)
+    assert rc == OK and s == 1.0
+    near(f, plain)
+    near(_increments(lib, rot, scaling=1, factor=4.0)[1], [x / 4 for x in plain])
+    ntk = base * 4.0 ** (rot / (rot - 2))
+    near(_increments(lib, rot, scaling=2, factor=4.0)[1],
+         [ntk ** (-2 * i / rot) for i in range(rot // 2)])
+    rc, f, s = _increments(lib, rot, scaling=3, factor=16.0, ctx=4096.0, p0=32.0, p1=1.0)
+    assert abs(s - (0.1 * math.log(16) + 1)) < 1e-7
+    for i, (x, p) in enumerate(zip(f, plain)):
+        turns = 4096 * p / (2 * math.pi)
+        step = 1e-14 * p + 2 * math.pi * 2.0**-65
+        assert p / 16 - step <= x <= p + step
+        if turns > 32 * 2:  # well inside either part: kept, or interpolated whole
+            near([x], [p])
+        if turns < 0.5:
+            near([x], [p / 16])
+    assert f == sorted(f, reverse=True)
+    rc, f, s = _increments(lib, rot, scaling=4, factor=8.0, ctx=8192.0, p0=1.0, p1=4.0)
+    assert s == 1.0
+    for x, p in zip(f, plain):
+        wave = 2 * math.pi / p
+        if wave < 8192 / 4:
+            want = p
+        elif wave > 8192:
+            want = p / 8
+        else:
+            smooth = (8192 / wave - 1.0) / 3.0
+            want = (1 - smooth) * p / 8 + smooth * p
+        near([x], [want])
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rot=0), UNSUPPORTED), (dict(rot=24), UNSUPPORTED), (dict(rot=512), UNSUPPORTED),
+    (dict(rot=64, base=1.0), INVALID), (dict(rot=64, base=float("nan")), INVALID),
+    (dict(rot=64, scaling=5), INVALID), (dict(rot=64, scaling=-1), INVALID),
+    (dict(rot=64, scaling=1, factor=0.5), INVALID),
+    (dict(rot=64, scaling=3, factor=2.0), INVALID),
+    (dict(rot=64, scaling=3, factor=2.0, ctx=4096.0, p0=1.0, p1=32.0), INVALID),
+    (dict(rot=64, scaling=4, factor=2.0, ctx=4096.0, p0=4.0, p1=1.0), INVALID)])
+def test_rope_increments_refuse(lib, kw, want):
+    assert _increments(lib, **kw)[0] == want
