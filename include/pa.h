@@ -406,6 +406,25 @@ int pa_decode_window(void *out, const void *q, const void *k_cache, const void *
                      float scale, float *out_lse, void *stream);
 
 /*
+ * pa_prefill_window -- pa_prefill_chunk under a sliding window with a few
+ * first tokens that stay visible: the query at position p sees the keys j with
+ *   j <= p  and  (j < sinks  or  p - j < window).
+ * Only the blocks that hold a key some query of the call sees are read, and
+ * only their entries of block_tables; slots in them that no query of a chunk
+ * sees may hold anything (the K/V of keys that some see must be finite).
+ * Arguments, shapes (head_dim 128, a group dividing 128), outputs and the
+ * treatment of inconsistent chunks as pa_prefill_chunk; window and sinks as
+ * pa_decode_window.  No workspace; equal calls give equal bits.
+ */
+int pa_prefill_window(void *out, const void *q, const void *k_cache, const void *v_cache,
+                      const int32_t *block_tables, int max_blocks_per_seq,
+                      const int32_t *cu_q_lens, const int32_t *q_start_pos,
+                      const int32_t *seq_lens, int num_chunks, int total_q_tokens, int max_q_len,
+                      int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                      int64_t num_blocks, int window, int sinks, float scale, float *out_lse,
+                      void *stream);
+
+/*
  * Rotary frequencies for pa_qk_norm_rope_cache, computed on the host (host
  * pointers): increments[i], i < rot_dim / 2, is pair i's frequency as a
  * fixed-point number of turns per position, in units of 2^-64 turn, so that
@@ -554,8 +573,8 @@ int pa_device_error_flags(unsigned int *flags, int reset);
 /*
  * Test entry points of the failure path (no product call needs them).  Each
  * makes one launch of the kernel its name gives, with the same arguments as
- * pa_decode (workspace and mode included; no lse) / pa_prefill_chunk (no
- * lse), in which the producer / loader warps issue no load at all and every
+ * pa_decode (workspace and mode included; no lse) / pa_prefill_chunk /
+ * pa_prefill_window (no lse), in which the producer / loader warps issue no load at all and every
  * mbarrier wait is bounded by wait_limit_us (1 .. 2,000,000 us) instead of
  * the default two seconds.  Every wait therefore runs out with no copy in
  * flight: the kernel sets PA_DEVERR_TIMEOUT, skips the rest of its waits,
@@ -579,6 +598,14 @@ int pa_test_prefill_stalled(void *out, const void *q, const void *k_cache, const
                             int max_q_len, int num_q_heads, int num_kv_heads, int head_dim,
                             int block_size, int64_t num_blocks, float scale,
                             unsigned int wait_limit_us, void *stream);
+int pa_test_prefill_window_stalled(void *out, const void *q, const void *k_cache,
+                                   const void *v_cache, const int32_t *block_tables,
+                                   int max_blocks_per_seq, const int32_t *cu_q_lens,
+                                   const int32_t *q_start_pos, const int32_t *seq_lens,
+                                   int num_chunks, int total_q_tokens, int max_q_len,
+                                   int num_q_heads, int num_kv_heads, int head_dim,
+                                   int block_size, int64_t num_blocks, int window, int sinks,
+                                   float scale, unsigned int wait_limit_us, void *stream);
 
 #ifdef __cplusplus
 }

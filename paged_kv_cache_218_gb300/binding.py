@@ -70,6 +70,10 @@ _SIGS = {
     "pa_hybrid_attention_append": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _P,
                                     _P, _P, _P, _P, _P, _I, _P, _I, _P, _L, _L,
                                     _P, _P, _I, _I, _I, _I, _L, _F, _I, _P, _S, _P], _I),
+    "pa_prefill_window": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _L, _I,
+                           _I, _F, _P, _P], _I),
+    "pa_test_prefill_window_stalled": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I,
+                                        _I, _L, _I, _I, _F, ctypes.c_uint, _P], _I),
     "pa_rope_increments": ([_P, ctypes.POINTER(_F), _I, _D, _I, _D, _D, _D, _D], _I),
     "pa_qk_norm_rope_cache": ([_P, _P, _P, _P, _P, _L, _L, _L, _P, _P, _F, _P, _P, _I, _I, _F,
                                _P, _P, _P, _I, _I, _I, _I, _I, _L, _P], _I),
@@ -328,6 +332,38 @@ def pa_decode_append(out, q, key, value, k_cache, v_cache, block_tables, seq_len
         _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
         block_tables.shape[1], _ptr(seq_lens), S, Hq, Hkv, D, bs, nb, float(scale),
         int(partition_tokens), _ptr(out_lse), _ptr(workspace), ws_bytes, _stream(stream)))
+
+
+def pa_prefill_window(out, q, k_cache, v_cache, block_tables, cu_q_lens, q_start_pos, seq_lens,
+                      max_q_len, window, sinks, scale, out_lse=None, stream=None) -> None:
+    """pa_prefill_chunk under a sliding window: the query at position p sees keys
+    j <= p with j < sinks or p - j < window."""
+    _need(out, "out", torch.bfloat16, 3)
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    _need(cu_q_lens, "cu_q_lens", torch.int32, 1)
+    _need(q_start_pos, "q_start_pos", torch.int32, 1)
+    _need(seq_lens, "seq_lens", torch.int32, 1)
+    T, Hq, D = q.shape
+    nb, bs, Hkv, Dk = k_cache.shape
+    C = q_start_pos.shape[0]
+    _same("out", out, q.shape)
+    _same("v_cache", v_cache, k_cache.shape)
+    if (Dk != D or block_tables.shape[0] != C or seq_lens.shape[0] != C or
+            cu_q_lens.shape[0] != C + 1):
+        raise ValueError("q, k_cache, block_tables, cu_q_lens, q_start_pos and seq_lens do not "
+                         "fit together")
+    if out_lse is not None:
+        _need(out_lse, "out_lse", torch.float32, 2)
+        _same("out_lse", out_lse, (T, Hq))
+    _one_device(q, out, k_cache, v_cache, block_tables, cu_q_lens, q_start_pos, seq_lens, out_lse)
+    _check("pa_prefill_window", _lib.pa_prefill_window(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+        block_tables.shape[1], _ptr(cu_q_lens), _ptr(q_start_pos), _ptr(seq_lens), C, T,
+        _int32("max_q_len", max_q_len, 0), Hq, Hkv, D, bs, nb, _int32("window", window, 1),
+        _int32("sinks", sinks, 0), float(scale), _ptr(out_lse), _stream(stream)))
 
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
@@ -667,3 +703,25 @@ def pa_test_prefill_stalled(out, q, k_cache, v_cache, block_tables, cu_q_lens, q
         _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
         block_tables.shape[1], _ptr(cu_q_lens), _ptr(q_start_pos), _ptr(seq_lens), C, T,
         int(max_q_len), Hq, Hkv, D, bs, nb, float(scale), int(wait_limit_us), _stream(stream)))
+
+
+def pa_test_prefill_window_stalled(out, q, k_cache, v_cache, block_tables, cu_q_lens, q_start_pos,
+                                   seq_lens, max_q_len, window, sinks, scale, wait_limit_us=1000,
+                                   stream=None) -> None:
+    """One windowed prefill launch whose loaders issue no load, every wait
+    bounded by wait_limit_us: the kernel must report PA_DEVERR_TIMEOUT."""
+    _need(out, "out", torch.bfloat16, 3)
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    for t, name in ((cu_q_lens, "cu_q_lens"), (q_start_pos, "q_start_pos"),
+                    (seq_lens, "seq_lens")):
+        _need(t, name, torch.int32, 1)
+    T, Hq, D = q.shape
+    nb, bs, Hkv, _ = k_cache.shape
+    _check("pa_test_prefill_window_stalled", _lib.pa_test_prefill_window_stalled(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+        block_tables.shape[1], _ptr(cu_q_lens), _ptr(q_start_pos), _ptr(seq_lens),
+        q_start_pos.shape[0], T, int(max_q_len), Hq, Hkv, D, bs, nb, int(window), int(sinks),
+        float(scale), int(wait_limit_us), _stream(stream)))

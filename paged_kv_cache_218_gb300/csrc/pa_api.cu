@@ -1417,6 +1417,90 @@ int pa_decode_window(void* out, const void* q, const void* k_cache, const void* 
              : PA_ERR_CUDA;
 }
 
+static int prefill_window_impl(void* out, const void* q, const void* k_cache, const void* v_cache,
+                               const int32_t* block_tables, int max_blocks_per_seq,
+                               const int32_t* cu_q_lens, const int32_t* q_start_pos,
+                               const int32_t* seq_lens, int num_chunks, int total_q_tokens, int max_q_len,
+                               int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                               int64_t num_blocks, int window, int sinks, float scale, float* out_lse,
+                               void* stream, int stall_loads = 0, uint64_t wait_ns = 0) {
+  if (window < 1 || sinks < 0) return PA_ERR_INVALID;
+  if (max_blocks_per_seq > INT32_MAX / kBlockSize) return PA_ERR_UNSUPPORTED;
+  bool done = false;
+  if (int rc = prefill_check(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                                      cu_q_lens, q_start_pos, seq_lens, num_chunks, total_q_tokens,
+                                      max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                                      num_blocks, scale, &done))
+    return rc;
+  if (done) return PA_OK;
+  if (!aligned(block_tables, 4) || !aligned(cu_q_lens, 4) || !aligned(q_start_pos, 4) ||
+      !aligned(seq_lens, 4) || (out_lse && !aligned(out_lse, 4)))
+    return PA_ERR_INVALID;
+  DeviceInfo* d;
+  if (int rc = current_device_info(&d)) return rc;
+  WindowPrefillArgs a{};
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.block_tables = block_tables;
+  a.cu_q_lens = cu_q_lens;
+  a.q_start_pos = q_start_pos;
+  a.seq_lens = seq_lens;
+  a.out_lse = out_lse;
+  a.err = d->err;
+  a.num_blocks = num_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_chunks = num_chunks;
+  a.total_q = total_q_tokens;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = num_q_heads / num_kv_heads;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.window = window;
+  a.sinks = sinks;
+  a.stall_loads = stall_loads;
+  a.wait_ns = wait_ns;  // 0: the default limit
+  const int tokens_per_tile = 128 / a.group;
+  CUtensorMap tm_q, tm_k, tm_v;
+  if (encode_q_map(&tm_q, q, total_q_tokens, num_q_heads, head_dim, a.group, tokens_per_tile) ||
+      encode_pool_map(&tm_k, k_cache, num_blocks, num_kv_heads, head_dim, kPoolKeyTile) ||
+      encode_pool_map(&tm_v, v_cache, num_blocks, num_kv_heads, head_dim, kPool2D))
+    return PA_ERR_CUDA;
+  const int64_t items = (static_cast<int64_t>(max_q_len) + 2 * tokens_per_tile - 1) /
+                                 (2 * tokens_per_tile) * num_chunks * num_kv_heads;
+  return launch_prefill_window(a, &tm_q, &tm_k, &tm_v, items, d->num_sms,
+                                        static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+int pa_prefill_window(void* out, const void* q, const void* k_cache, const void* v_cache,
+                      const int32_t* block_tables, int max_blocks_per_seq,
+                      const int32_t* cu_q_lens, const int32_t* q_start_pos,
+                      const int32_t* seq_lens, int num_chunks, int total_q_tokens, int max_q_len,
+                      int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                      int64_t num_blocks, int window, int sinks, float scale, float* out_lse,
+                      void* stream) {
+  return prefill_window_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                             cu_q_lens, q_start_pos, seq_lens, num_chunks, total_q_tokens,
+                             max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                             num_blocks, window, sinks, scale, out_lse, stream);
+}
+
+int pa_test_prefill_window_stalled(void* out, const void* q, const void* k_cache,
+                                   const void* v_cache, const int32_t* block_tables,
+                                   int max_blocks_per_seq, const int32_t* cu_q_lens,
+                                   const int32_t* q_start_pos, const int32_t* seq_lens,
+                                   int num_chunks, int total_q_tokens, int max_q_len,
+                                   int num_q_heads, int num_kv_heads, int head_dim,
+                                   int block_size, int64_t num_blocks, int window, int sinks,
+                                   float scale, unsigned int wait_limit_us, void* stream) {
+  if (wait_limit_us == 0 || wait_limit_us > 2000000u) return PA_ERR_INVALID;
+  return prefill_window_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                             cu_q_lens, q_start_pos, seq_lens, num_chunks, total_q_tokens,
+                             max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                             num_blocks, window, sinks, scale, nullptr, stream, 1,
+                             static_cast<uint64_t>(wait_limit_us) * 1000u);
+}
+
 int pa_test_decode_stalled(void* out, const void* q, const void* k_cache, const void* v_cache,
                            const int32_t* block_tables, int max_blocks_per_seq,
                            const int32_t* seq_lens, int num_seqs, int num_q_heads,

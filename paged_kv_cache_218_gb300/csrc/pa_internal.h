@@ -114,6 +114,12 @@ struct PrefillArgs {
   __nv_bfloat16* v_pool;
 };
 
+// Prefill chunks under a sliding window and sinks (pa_prefill_window).
+struct WindowPrefillArgs : PrefillArgs {
+  int window;  // a query at p sees keys (p - window, p]
+  int sinks;   // and keys [0, sinks)
+};
+
 struct CascadeArgs {
   const __nv_bfloat16* q;        // [S, Hq, 128]
   const int32_t* seq_lens;       // [S]
@@ -210,6 +216,9 @@ bool decode_supported(int head_dim, int num_kv_heads, int num_q_heads, int mode,
 cudaError_t launch_merge(const MergeArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
                            const CUtensorMap* tm_v, int grid_tiles, cudaStream_t stream);
+cudaError_t launch_prefill_window(const WindowPrefillArgs& a, const CUtensorMap* tm_q,
+                                  const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                                  int64_t max_items, int num_sms, cudaStream_t stream);
 size_t prefill_smem_bytes();
 bool cascade_shape(int num_kv_heads, int group, int max_group, int* kv_per_cta, int* warps_per_kv,
                    int* stages);

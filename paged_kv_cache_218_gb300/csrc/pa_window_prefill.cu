@@ -1,0 +1,743 @@
+// pa_window_prefill.cu -- causal paged prefill chunks under a sliding window
+// and a few first tokens that stay visible, on tcgen05 tensor cores (sm_103a).
+//
+// A query at position p sees the keys j <= p with j < sinks or p - j < window.
+// The tensor-core pipeline of a tile is pa_prefill_body.cuh's: CTA pairs
+// (cta_group::2) on two consecutive query tiles of a kv head, K and V halves
+// loaded by each CTA, three score buffers in tensor memory, online softmax
+// with P written back over its scores.  What a window changes:
+//
+//  * Key tiles run over a list of blocks, not over positions: the sinks'
+//    blocks [0, nsb), then the blocks from the one that holds the first key
+//    of the pair's first row's window on.  A list index is a "virtual" block;
+//    virtual key = key - shift behind the sinks, where shift is 16 times the
+//    blocks left out.  So a few sinks cost a few rows of the first tile, and
+//    blocks that no row sees are neither loaded nor looked up.
+//  * A row's mask over a 64-column half of a tile is
+//    vk <= hi && (vk < sinks || vk >= lo): one 64-bit mask per row and half,
+//    built from three counts; halves that all rows of a warp see whole skip
+//    it, halves that none sees skip the exponentials.
+//  * V rows that no row of the pair may see (ends of the sinks' and of the
+//    window's first block, slots behind the last key) are zeroed in shared
+//    memory before the product: they may hold anything, and 0 * NaN is NaN.
+//  * Work per query tile is short (window / 128 key tiles), so setting up and
+//    draining a pipeline per tile would cost as much as the tile.  The launch
+//    is persistent: one CTA pair per two SMs walks (chunk, query tile, kv head)
+//    items; barriers, rings and phases run on across items, Q has two buffers,
+//    and the loaders and the score products of the next item run while the
+//    softmax finishes the last one.  A pair's items are every pairs-th of the
+//    list, found with a warp-wide scan over the chunks' lengths, so ragged
+//    chunks leave no empty items.
+//
+// What bounds it: the tensor pipe and, at 128 x 128 tiles, the softmax that
+// feeds it (one exponential per score).
+// Every mbarrier wait is bounded, as in pa_prefill_body.cuh.
+#include <mutex>
+
+#include "pa_prefill_body.cuh"
+
+namespace pa {
+namespace pre {
+namespace {
+
+constexpr uint64_t kSettleNs = 1000000;  // far longer than any copy takes
+constexpr float kFloor = -1e30f;  // reference maximum of a row that saw nothing yet
+
+// Shared memory of one CTA of a pair: two Q tiles, four K and four V half
+// tiles, block ids of both loaders, the softmax's exchange, barriers.
+struct WPlan {
+  static constexpr int kNK = 4, kNV = 4;
+  static constexpr int kKSlot = kHalf, kVSlot = kHalf;
+  static constexpr int kQOff = 0;  // [2][2 * kHalf]
+  static constexpr int kKOff = kQOff + 4 * kHalf;
+  static constexpr int kVOff = kKOff + kNK * kKSlot;
+  static constexpr int kIdsOff = kVOff + kNV * kVSlot;
+  static constexpr int kRedOff = kIdsOff + 2 * kIdRing * 8 * 4;
+  static constexpr int kRedOff2 = kRedOff + 2 * 2 * 128 * 4;
+  static constexpr int kBarOff = kRedOff2 + 2 * 128 * 4;
+  static constexpr int kSmemBytes = kBarOff + 320;
+};
+static_assert(WPlan::kSmemBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
+
+// One work item of a pair: query tiles 2 mg, 2 mg + 1 of a chunk, one kv head.
+struct Item {
+  int c, kvh;
+  int q0, qlen, p0, n;  // the chunk's rows and positions
+  int tc0;              // first query token of the pair
+  int kmax;             // keys [0, kmax) are visible to some row, window and sinks aside
+  int lo;               // first key of the first row's window
+  int nsb, b_first;     // the sinks' blocks; first block behind them
+  int nvb;              // virtual blocks
+  int nkt;              // key tiles
+};
+
+// Walks a pair's items (every `stride`-th of the list); each warp keeps its own.
+struct Cursor {
+  int64_t want;    // list index of the next item
+  int64_t before;  // items of the chunks before `chunk`
+  int chunk;
+};
+
+__device__ __forceinline__ bool chunk_ok(const WindowPrefillArgs& a, int q0, int q1, int p0, int n) {
+  return q0 >= 0 && q1 <= a.total_q && q1 >= q0 && p0 >= 0 && n >= 0 && q1 - q0 <= n &&
+         p0 <= n - (q1 - q0) && n <= a.max_blocks * kBlockSize;
+}
+
+// The next item; false at the end of the list.  Called by whole warps.  The
+// caller that passes flag = true reports chunks with inconsistent metadata.
+__device__ __forceinline__ bool next_item(const WindowPrefillArgs& a, Cursor& cur, int stride,
+                                          int lane, bool flag, Item& it) {
+  const int rows = 2 * (kTileKeys / a.group);  // query tokens per item
+  for (;;) {
+    if (cur.chunk >= a.num_chunks) return false;
+    // items of 32 chunks at a time, and their inclusive sums
+    const int c = cur.chunk + lane;
+    int64_t items = 0;
+    if (c < a.num_chunks) {
+      const int q0 = a.cu_q_lens[c], q1 = a.cu_q_lens[c + 1];
+      if (chunk_ok(a, q0, q1, a.q_start_pos[c], a.seq_lens[c]))
+        items = static_cast<int64_t>((q1 - q0 + rows - 1) / rows) * a.num_kv_heads;
+      else if (flag)
+        atomicOr(a.err, PA_DEVERR_CHUNK);
+    }
+    int64_t sum = items;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += o;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, cur.before + sum > cur.want);
+    if (past == 0) {
+      cur.before += __shfl_sync(0xffffffffu, sum, 31);
+      cur.chunk += 32;
+      continue;
+    }
+    const int w = __ffs(past) - 1;
+    const int64_t start = cur.before + __shfl_sync(0xffffffffu, sum - items, w);
+    const int64_t at = cur.want - start;
+    const int64_t count = __shfl_sync(0xffffffffu, items, w);
+    cur.before = start;
+    cur.chunk += w;
+    cur.want += stride;
+    it.c = cur.chunk;
+    it.kvh = static_cast<int>(at % a.num_kv_heads);
+    // last query tiles first: where the window has not closed they are longest
+    const int mg = static_cast<int>(count / a.num_kv_heads - 1 - at / a.num_kv_heads);
+    it.q0 = a.cu_q_lens[it.c];
+    it.qlen = a.cu_q_lens[it.c + 1] - it.q0;
+    it.p0 = a.q_start_pos[it.c];
+    it.n = a.seq_lens[it.c];
+    it.tc0 = mg * rows;
+    it.kmax = it.p0 + min(it.qlen, it.tc0 + rows);
+    it.lo = max(0, it.p0 + it.tc0 - (a.window - 1));
+    const int ns = min(a.sinks, it.kmax);
+    it.nsb = (ns + kBlockSize - 1) / kBlockSize;
+    it.b_first = max(it.lo / kBlockSize, it.nsb);
+    const int nb = (it.kmax + kBlockSize - 1) / kBlockSize;
+    it.nvb = it.nsb + max(0, nb - it.b_first);
+    it.nkt = (it.nvb + 7) / 8;
+    return true;
+  }
+}
+
+// Rows of virtual blocks that no row of the pair sees: at most three ranges.
+struct Hidden {
+  int vb[3], r0[3], r1[3];  // rows [r0, r1) of block vb; vb < 0: none
+  __device__ __forceinline__ Hidden(const Item& it, int sinks) {
+#pragma unroll
+    for (int e = 0; e < 3; ++e) vb[e] = -1;
+    auto set = [&](int e, int b, int from, int to) {
+      if (from < to) {
+        vb[e] = b;
+        r0[e] = from;
+        r1[e] = to;
+      }
+    };
+    // between the sinks and the window, in the sinks' last block
+    if (it.nsb > 0) {
+      const int base = (it.nsb - 1) * kBlockSize;
+      set(0, it.nsb - 1, min(sinks, it.kmax) - base, min(kBlockSize, it.lo - base));
+    }
+    // before the window, in its first block
+    if (it.lo / kBlockSize >= it.nsb) set(1, it.nsb, 0, it.lo % kBlockSize);
+    // behind the last key
+    if (it.kmax % kBlockSize) set(2, it.nvb - 1, it.kmax % kBlockSize, kBlockSize);
+  }
+  __device__ __forceinline__ bool in_tile(int j) const {
+    return (vb[0] >= 0 && vb[0] / 8 == j) || (vb[1] >= 0 && vb[1] / 8 == j) ||
+           (vb[2] >= 0 && vb[2] / 8 == j);
+  }
+};
+
+// Bits [0, k) of 64.
+__device__ __forceinline__ uint64_t low_bits(int k) {
+  return k <= 0 ? 0ull : (k >= 64 ? ~0ull : (1ull << k) - 1);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
+                          const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const WindowPrefillArgs a) {
+  using P = WPlan;
+  constexpr int kNK = P::kNK, kNV = P::kNV;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar_q = sbase + P::kBarOff;         // [2]: Q of the pair landed
+  const uint32_t bar_q_empty = bar_q + 16;           // [2]: its score products are done
+  const uint32_t bar_k_full = bar_q_empty + 16;      // [kNK]
+  const uint32_t bar_k_empty = bar_k_full + 8 * kNK;
+  const uint32_t bar_v_full = bar_k_empty + 8 * kNK;   // [kNV]: this CTA's V landed (edge tiles)
+  const uint32_t bar_v_ready = bar_v_full + 8 * kNV;   // [kNV]: V of the pair ready
+  const uint32_t bar_v_empty = bar_v_ready + 8 * kNV;
+  const uint32_t bar_s_full = bar_v_empty + 8 * kNV;   // [kNS]: scores of a tile
+  const uint32_t bar_p_full = bar_s_full + 8 * kNS;    // [kNS]: softmax done
+  const uint32_t bar_o_done = bar_p_full + 8 * kNS;    // [kNS]: PV done
+  static_assert(32 + 8 * (2 * kNK + 3 * kNV + 3 * kNS) <= 288, "barrier area");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P::kBarOff + 288);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 292);
+  int* ids_smem = reinterpret_cast<int*>(smem + P::kIdsOff) +
+                  ((threadIdx.x >> 5) == kLoadVWarp ? kIdRing * 8 : 0);
+  float* red_max = reinterpret_cast<float*>(smem + P::kRedOff);
+  float* red_sum = reinterpret_cast<float*>(smem + P::kRedOff2);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int Hkv = a.num_kv_heads, G = a.group;
+  const int tpt = kTileKeys / G;
+  const int rank = static_cast<int>(blockIdx.x) & 1;
+  const bool issuer = rank == 0;
+  const int stride = static_cast<int>(gridDim.x) / 2;
+  Cursor cur{static_cast<int64_t>(blockIdx.x) / 2, 0, 0};
+  Item it;
+
+  if (tid == 0) {
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(bar_q + 8 * k, 1);
+      mbar_init(bar_q_empty + 8 * k, 1);
+    }
+    for (int k = 0; k < kNK; ++k) {
+      mbar_init(bar_k_full + 8 * k, 1);
+      mbar_init(bar_k_empty + 8 * k, 1);
+    }
+    for (int k = 0; k < kNV; ++k) {
+      mbar_init(bar_v_full + 8 * k, 1);
+      mbar_init(bar_v_ready + 8 * k, 2);
+      mbar_init(bar_v_empty + 8 * k, 1);
+    }
+    for (int k = 0; k < kNS; ++k) {
+      mbar_init(bar_s_full + 8 * k, 1);
+      mbar_init(bar_p_full + 8 * k, kSoftmaxWarps * 2);
+      mbar_init(bar_o_done + 8 * k, 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc<2>(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish<2>();
+  }
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers exist before either reports to the other
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == kLoadKWarp || warp == kLoadVWarp) {
+    // ------------------------------------------------------------ loaders
+    const uint64_t pol = l2_policy_evict_last();
+    IdleClock clk(a.wait_ns);
+    auto timed_out = [&](bool progressed) {
+      if (progressed) {
+        clk.progress();
+        return false;
+      }
+      if (!clk.expired()) return false;
+      if (lane == 0) {
+        *abort_flag = 1;
+        atomicOr(a.err, PA_DEVERR_TIMEOUT);
+      }
+      return true;
+    };
+    // ids of the item's virtual blocks [8 t_first, + 8 kIdBatch); a slot of
+    // the ring is rewritten once its tile's loads have been issued (by this
+    // warp).  Ids past the list read as zeros (-1: a box outside the pool).
+    auto fetch_ids = [&](int t_first) {
+      int v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int vb = t_first * 8 + lane + 32 * i;
+        const int b = vb < it.nsb ? vb : vb - it.nsb + it.b_first;
+        v[i] = vb < it.nvb ? a.block_tables[static_cast<int64_t>(it.c) * a.max_blocks + b] : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int vb = t_first * 8 + lane + 32 * i;
+        if (vb < it.nvb && (v[i] < 0 || v[i] >= a.num_blocks)) {
+          atomicOr(a.err, PA_DEVERR_BLOCK_ID);
+          v[i] = -1;
+        }
+        ids_smem[vb % (kIdRing * 8)] = v[i];
+      }
+      __syncwarp();
+    };
+    int total = 0;  // tiles loaded by this warp, over all items
+    // after a timeout: let the copies in flight land before the CTA may exit
+    auto settle = [&]() {
+      if (!*abort_flag) return;
+      const uint64_t t = global_ns();
+      while (global_ns() - t < kSettleNs) __nanosleep(1000);
+    };
+    if (warp == kLoadKWarp) {
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+      }
+      int qi = 0;  // items
+      bool stop = a.stall_loads != 0;  // a stalled test launch issues no load
+      while (!stop && next_item(a, cur, stride, lane, blockIdx.x == 0, it)) {
+        fetch_ids(0);
+        int jf = kIdBatch, jk = 0;
+        bool q_loaded = false;
+        while (jk < it.nkt && !stop) {
+          bool progressed = false;
+          if (!q_loaded) {
+            const int qb = qi & 1;
+            bool ok = qi < 2;
+            if (!ok && lane == 0) ok = mbar_test_wait(bar_q_empty + 8 * qb, ((qi >> 1) - 1) & 1);
+            if (__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
+              if (lane == 0) {
+                const uint32_t bar = bar_q + 8 * qb;
+                if (issuer) mbar_arrive_expect_tx(bar, 4 * kHalf);  // both Q tiles of the pair
+                for (int h = 0; h < 2; ++h) {
+                  const uint32_t dst = sbase + P::kQOff + (2 * qb + h) * kHalf;
+                  const int row = it.q0 + it.tc0 + rank * tpt;
+                  if (issuer)
+                    tma_load_3d(dst, &tm_q, h * 64, it.kvh * G, row, bar, pol);
+                  else
+                    tma_load_3d_pair(dst, &tm_q, h * 64, it.kvh * G, row, mapa_shared(bar, 0), pol);
+                }
+              }
+              __syncwarp();
+              q_loaded = true;
+              progressed = true;
+            }
+          }
+          if (jf < it.nkt && jk + kIdBatch / 2 >= jf) {
+            fetch_ids(jf);
+            jf += kIdBatch;
+            progressed = true;
+          }
+          const int slot = total % kNK;
+          bool free_slot = total < kNK;
+          if (!free_slot && lane == 0)
+            free_slot = mbar_test_wait(bar_k_empty + 8 * slot, ((total / kNK) - 1) & 1);
+          if (q_loaded && jk < jf && __shfl_sync(0xffffffffu, free_slot ? 1 : 0, 0)) {
+            const uint32_t bar = bar_k_full + 8 * slot;
+            if (lane == 0 && issuer) mbar_arrive_expect_tx(bar, 2 * kHalf);
+            __syncwarp();
+            if (lane < 4) {  // CTA r takes keys 64 r .. 64 r + 63: blocks 4 r .. 4 r + 3
+              const int id = ids_smem[(jk % kIdRing) * 8 + 4 * rank + lane];
+              const uint32_t dst = sbase + P::kKOff + slot * P::kKSlot + lane * 2 * kBlockBytes;
+              if (issuer)
+                tma_load_4d(dst, &tm_k, 0, 0, 2 * it.kvh, 2 * id, bar, pol);
+              else
+                tma_load_4d_pair(dst, &tm_k, 0, 0, 2 * it.kvh, 2 * id, mapa_shared(bar, 0), pol);
+            }
+            __syncwarp();
+            ++jk;
+            ++total;
+            progressed = true;
+          }
+          stop = timed_out(progressed) || warp_flag(abort_flag);
+        }
+        ++qi;
+      }
+      // every load's slot has been released, and so has landed, before exit
+      if (lane == 0)
+        for (int sl = 0; sl < kNK && sl < total; ++sl)
+          wait_or_abort<2>(bar_k_empty + 8 * sl, ((total - 1 - sl) / kNK) & 1, abort_flag, a);
+      settle();
+    } else {
+      if (lane == 0) tma_prefetch_desc(&tm_v);
+      unsigned full_phase = 0;  // bit s: parity of v_full[s]'s next use
+      int edge_slot = -1;       // slot of the edge tile whose rows are still to be zeroed
+      int edge_tile = 0;
+      bool stop = a.stall_loads != 0;
+      while (!stop && next_item(a, cur, stride, lane, false, it)) {
+        fetch_ids(0);
+        const Hidden hid(it, a.sinks);
+        int jf = kIdBatch, jv = 0;
+        while ((jv < it.nkt || edge_slot >= 0) && !stop) {
+          bool progressed = false;
+          if (jf < it.nkt && jv + kIdBatch / 2 >= jf) {
+            fetch_ids(jf);
+            jf += kIdBatch;
+            progressed = true;
+          }
+          const bool edge = hid.in_tile(jv);
+          if (jv < it.nkt && jv < jf && !(edge && edge_slot >= 0)) {
+            const int slot = total % kNV;
+            bool free_slot = total < kNV;
+            if (!free_slot && lane == 0)
+              free_slot = mbar_test_wait(bar_v_empty + 8 * slot, ((total / kNV) - 1) & 1);
+            if (__shfl_sync(0xffffffffu, free_slot ? 1 : 0, 0)) {
+              const bool remote = !issuer && !edge;
+              const uint32_t bar = edge ? bar_v_full + 8 * slot
+                                        : (remote ? mapa_shared(bar_v_ready + 8 * slot, 0)
+                                                  : bar_v_ready + 8 * slot);
+              if (lane == 0) {
+                if (remote)
+                  mbar_arrive_expect_tx_remote(bar, P::kVSlot);
+                else
+                  mbar_arrive_expect_tx(bar, P::kVSlot);
+              }
+              __syncwarp();
+              if (lane < 8) {  // CTA r takes columns 64 r .. 64 r + 63 of every key
+                const int id = ids_smem[(jv % kIdRing) * 8 + lane];
+                const uint32_t dst = sbase + P::kVOff + slot * P::kVSlot + lane * kBlockBytes;
+                const int x = it.kvh * 128 + rank * 64, y = id * kBlockSize;
+                if (remote)
+                  tma_load_2d_pair(dst, &tm_v, x, y, bar, pol);
+                else
+                  tma_load_2d(dst, &tm_v, x, y, bar, pol);
+              }
+              __syncwarp();
+              if (edge) {
+                edge_slot = slot;
+                edge_tile = jv;
+              }
+              ++jv;
+              ++total;
+              progressed = true;
+            }
+          }
+          if (edge_slot >= 0) {
+            bool landed = false;
+            if (lane == 0)
+              landed = mbar_test_wait(bar_v_full + 8 * edge_slot, (full_phase >> edge_slot) & 1);
+            if (__shfl_sync(0xffffffffu, landed ? 1 : 0, 0)) {
+              const uint32_t vt = sbase + P::kVOff + edge_slot * P::kVSlot;
+#pragma unroll
+              for (int h = 0; h < 3; ++h) {
+                if (hid.vb[h] < 0 || hid.vb[h] / 8 != edge_tile) continue;
+                const uint32_t blk = vt + (hid.vb[h] % 8) * kBlockBytes;
+                for (int e = lane + 8 * hid.r0[h]; e < 8 * hid.r1[h]; e += 32)
+                  st_shared_zero16(blk + e * 16);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (!issuer)
+                  mbar_arrive_remote_release(mapa_shared(bar_v_ready + 8 * edge_slot, 0));
+                else
+                  mbar_arrive(bar_v_ready + 8 * edge_slot);
+              }
+              full_phase ^= 1u << edge_slot;
+              edge_slot = -1;
+              progressed = true;
+            }
+          }
+          stop = timed_out(progressed) || warp_flag(abort_flag);
+        }
+      }
+      if (lane == 0)
+        for (int sl = 0; sl < kNV && sl < total; ++sl)
+          wait_or_abort<2>(bar_v_empty + 8 * sl, ((total - 1 - sl) / kNV) & 1, abort_flag, a);
+      settle();
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp || warp == kPvWarp) {
+    // ------------------------------------------------------------ tensor-core issue
+    auto commit = [&](uint32_t bar) {
+      tc_commit<2>(mapa_shared(bar, 1));
+      tc_commit<2>(bar);
+    };
+    IdleClock clk(a.wait_ns);
+    bool ok = true;
+    // give up: flag it once, so that every role leaves its loops
+    auto stuck = [&]() {
+      if (*abort_flag) return true;
+      if (!clk.expired()) return false;
+      *abort_flag = 1;
+      atomicOr(a.err, PA_DEVERR_TIMEOUT);
+      return true;
+    };
+    if (warp == kMmaWarp) {
+      const uint32_t idesc_s = instr_desc(0, 256);
+      const uint64_t dk0 = smem_desc(sbase + P::kKOff, 16, kKGroupStride);
+      int s_buf = 0, s_round = 0, s_kslot = 0, s_kphase = 0, qi = 0;
+      while (issuer && next_item(a, cur, stride, lane, false, it)) {
+        if (lane == 0) {
+          const uint64_t dq = smem_desc(sbase + P::kQOff + 2 * (qi & 1) * kHalf, 16, 1024);
+          bool q_there = false;
+          int js = 0;
+          while (ok && js < it.nkt) {
+            if (!q_there) q_there = mbar_test_wait(bar_q + 8 * (qi & 1), (qi >> 1) & 1);
+            if (q_there && mbar_test_wait(bar_k_full + 8 * s_kslot, s_kphase) &&
+                (s_round == 0 || mbar_test_wait(bar_o_done + 8 * s_buf, (s_round + 1) & 1))) {
+              tc_fence_after();
+              const uint64_t dk = dk0 + static_cast<uint64_t>((s_kslot * P::kKSlot) >> 4);
+              const uint32_t dst = tmem + s_buf * 128;
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                tc_mma_f16<2>(dst, dq + (((ks >> 2) * kHalf + (ks & 3) * 32) >> 4),
+                              dk + (((ks >> 2) * kKHalfOffset + (ks & 3) * 32) >> 4), idesc_s,
+                              ks > 0);
+              commit(bar_s_full + 8 * s_buf);
+              commit(bar_k_empty + 8 * s_kslot);
+              ++js;
+              if (js == it.nkt) commit(bar_q_empty + 8 * (qi & 1));
+              if (++s_buf == kNS) {
+                s_buf = 0;
+                ++s_round;
+              }
+              if (++s_kslot == kNK) {
+                s_kslot = 0;
+                s_kphase ^= 1;
+              }
+              clk.progress();
+            } else if (stuck()) {
+              ok = false;
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+        ++qi;
+      }
+    } else {
+      const uint32_t idesc_o = instr_desc(1, 256);
+      const uint64_t dv0 = smem_desc(sbase + P::kVOff, kHalf, 1024);
+      int p_buf = 0, p_phase = 0, p_vslot = 0, p_vphase = 0;
+      while (issuer && next_item(a, cur, stride, lane, false, it)) {
+        if (lane == 0) {
+          const Hidden hid(it, a.sinks);
+          int jp = 0;
+          while (ok && jp < it.nkt) {
+            if (mbar_test_wait(bar_p_full + 8 * p_buf, p_phase) &&
+                mbar_test_wait(bar_v_ready + 8 * p_vslot, p_vphase)) {
+              if (hid.in_tile(jp)) fence_acq_rel_cluster();  // the peer's zeroed rows
+              tc_fence_after();
+              const uint64_t dv = dv0 + static_cast<uint64_t>((p_vslot * P::kVSlot) >> 4);
+              const uint32_t ta = tmem + p_buf * 128;
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                tc_mma_f16_tmem_a<2>(tmem + kTmemO, ta + (ks >> 2) * 64 + (ks & 3) * 8,
+                                     dv + ((ks * kBlockBytes) >> 4), idesc_o,
+                                     (jp > 0 || ks > 0) ? 1u : 0u);
+              commit(bar_o_done + 8 * p_buf);
+              commit(bar_v_empty + 8 * p_vslot);
+              ++jp;
+              if (++p_buf == kNS) {
+                p_buf = 0;
+                p_phase ^= 1;
+              }
+              if (++p_vslot == kNV) {
+                p_vslot = 0;
+                p_vphase ^= 1;
+              }
+              clk.progress();
+            } else if (stuck()) {
+              ok = false;
+            }
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+        if (!ok) break;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax warps
+    const int qd = warp & 3, hc = warp >> 2;
+    const int r = qd * 32 + lane;  // query row = tensor-memory lane
+    const uint32_t lane_off = static_cast<uint32_t>(qd * 32) << 16;
+    const float sl = a.scale_log2;
+    const uint32_t ocol = tmem + lane_off + kTmemO + hc * 64;
+    uint32_t v[64];
+    int jt = 0;                    // tiles, over all items
+    int b3 = 0, s_phase = 0;       // score buffer of tile jt and its parity
+    while (next_item(a, cur, stride, lane, false, it)) {
+      const int t0 = it.tc0 + rank * tpt;
+      const int tv = min(it.qlen - t0, tpt);  // valid tokens here (<= 0: none)
+      const int shift = (it.b_first - it.nsb) * kBlockSize;
+      const int pos = it.p0 + t0 + r / G;
+      // last and first visible virtual key of the row's window
+      const int hi = min(pos, it.kmax - 1) - shift;
+      const int lo = max(0, pos - (a.window - 1)) - shift;
+      float m_run = kFloor, l_run = 0.f;
+      for (int j = 0; j < it.nkt; ++j, ++jt) {
+        const int b = jt & 1;
+        wait_or_abort_warp<2>(bar_s_full + 8 * b3, s_phase, abort_flag, a);
+        tc_fence_after();
+        const int kb = j * kTileKeys + hc * 64;
+        const bool whole = hi >= kb + 63 && (lo <= kb || a.sinks >= kb + 64);
+        const bool full = __all_sync(0xffffffffu, whole);
+        uint64_t seen = ~0ull;
+        if (!full)
+          seen = low_bits(hi - kb + 1) & (low_bits(a.sinks > kb ? min(a.sinks - kb, 64) : 0) |
+                                          ~low_bits(lo - kb));
+        const uint32_t seen0 = static_cast<uint32_t>(seen), seen1 = static_cast<uint32_t>(seen >> 32);
+        const bool any = full || __any_sync(0xffffffffu, seen != 0);
+        float mloc = -INFINITY;
+        if (full) {
+          tmem_ld64_max(tmem + lane_off + b3 * 128 + hc * 64, v, mloc);
+        } else if (any) {
+          tmem_ld64(tmem + lane_off + b3 * 128 + hc * 64, v);
+          float mp[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mp[k] = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            // a hidden score, whatever it holds, becomes -inf
+            if (!(((i < 32 ? seen0 : seen1) >> (i & 31)) & 1u)) v[i] = 0xff800000u;
+            mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(v[i]));
+          }
+          mloc = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
+                       fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
+        }
+        mloc = mloc * sl;  // scale > 0 keeps the order
+        red_max[(b * 2 + hc) * 128 + r] = mloc;
+        named_barrier(1 + qd, 64);
+        const float mx = fmaxf(mloc, red_max[(b * 2 + (hc ^ 1)) * 128 + r]);
+        const float m_new = fmaxf(m_run, mx);
+        const bool move = m_new > m_run + kRescaleThreshold;
+        const float m_use = move ? m_new : m_run;
+        const float alpha = move ? fast_exp2(m_run - m_use) : 1.f;
+        uint32_t pk[32];
+        float rs = 0.f;
+        if (any) {
+          float rsp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            // -inf (hidden) gives exactly 0: m_use is finite
+            const float e0 = fast_exp2(fmaf(__uint_as_float(v[i]), sl, -m_use));
+            const float e1 = fast_exp2(fmaf(__uint_as_float(v[i + 1]), sl, -m_use));
+            rsp[(i >> 1) & 3] += e0 + e1;
+            pk[i / 2] = pack_bf16x2(e0, e1);
+          }
+          rs = (rsp[0] + rsp[1]) + (rsp[2] + rsp[3]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) pk[i] = 0;
+        }
+        l_run = l_run * alpha + rs;
+        m_run = m_use;
+        // O is rescaled only when a row maximum moved; PV of the previous
+        // tile must have landed first (tile 0's PV overwrites O)
+        if (j >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+          const int pb = b3 == 0 ? kNS - 1 : b3 - 1;
+          wait_or_abort_warp<2>(bar_o_done + 8 * pb, b3 == 0 ? s_phase ^ 1 : s_phase, abort_flag,
+                                a);
+          tc_fence_after();
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t (&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32 * cc]);
+            tmem_ld32(ocol + 32 * cc, w);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+            tmem_st32(ocol + 32 * cc, w);
+          }
+        }
+        tmem_st32(tmem + lane_off + b3 * 128 + hc * 64, pk);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (!issuer)
+            mbar_arrive_remote(mapa_shared(bar_p_full + 8 * b3, 0));
+          else
+            mbar_arrive(bar_p_full + 8 * b3);
+        }
+        if (++b3 == kNS) {
+          b3 = 0;
+          s_phase ^= 1;
+        }
+      }
+
+      // ---- epilogue: O / l -> bf16, and lse.  The next item's first PV waits
+      // for this warp's next arrival on p_full, behind these loads of O.
+      const int pb = b3 == 0 ? kNS - 1 : b3 - 1;
+      wait_or_abort_warp<2>(bar_o_done + 8 * pb, b3 == 0 ? s_phase ^ 1 : s_phase, abort_flag, a);
+      tc_fence_after();
+      red_sum[hc * 128 + r] = l_run;
+      named_barrier(1 + qd, 64);
+      const float l_tot = l_run + red_sum[(hc ^ 1) * 128 + r];
+      const int tok = r / G, g = r % G;
+      const bool store = tok < tv && !*abort_flag;
+      const float inv = l_tot == 0.f ? 0.f : 1.f / l_tot;  // a NaN sum stays visible
+      const int64_t row = static_cast<int64_t>(it.q0 + t0 + tok) * a.num_q_heads + it.kvh * G + g;
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        uint32_t (&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32 * cc]);
+        tmem_ld32(ocol + 32 * cc, w);
+        if (store) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            pk[i / 2] = pack_bf16x2(__uint_as_float(w[i]) * inv, __uint_as_float(w[i + 1]) * inv);
+          uint4* dst = reinterpret_cast<uint4*>(a.out + row * 128 + hc * 64 + cc * 32);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            dst[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+        }
+      }
+      if (store && hc == 0 && a.out_lse)
+        a.out_lse[row] = l_tot == 0.f ? -INFINITY : (m_run + __log2f(l_tot)) * kLn2;
+      // (after a timeout every softmax warp still walks every item, its waits
+      // skipped: a pair of warps meets at its named barrier to the end)
+    }
+  }
+  tc_fence_before();
+  cluster_sync();  // neither CTA leaves while the other may still report to it
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc<2>(tmem, kTmemCols);
+}
+
+}  // namespace
+}  // namespace pre
+
+using namespace pre;
+
+cudaError_t launch_prefill_window(const WindowPrefillArgs& args, const CUtensorMap* tm_q,
+                                  const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                                  int64_t max_items, int num_sms, cudaStream_t stream) {
+  WindowPrefillArgs a = args;
+  if (a.wait_ns == 0) a.wait_ns = kWaitLimitNs;
+  constexpr int smem = WPlan::kSmemBytes + 1024;
+  static std::mutex mu;
+  static bool set_for[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set_for[dev]) {
+      e = cudaFuncSetAttribute(prefill_window_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               smem);
+      if (e != cudaSuccess) return e;
+      set_for[dev] = true;
+    }
+  }
+  const int pairs = num_sms / 2 < 1 ? 1 : num_sms / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(max_items < pairs ? max_items : pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, prefill_window_kernel, *tm_q, *tm_k, *tm_v, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace pa

@@ -1,0 +1,136 @@
+"""A sliding-window attention layer served end to end: prompts in chunks, then
+decode steps, each step pa_qk_norm_rope_cache followed by pa_prefill_window or
+pa_decode_window, with blocks that left the window given back and reused.
+Every output row is compared with dense fp64 attention over the whole
+sequence's rotated keys, kept aside from k_out."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from tests import window_ref as R
+
+pytestmark = pytest.mark.gpu
+D = 128
+
+
+@pytest.fixture(scope="module")
+def pa(cuda_device):
+    from paged_kv_cache_218_gb300 import binding
+    return binding
+
+
+class Manager:
+    """Blocks of each sequence under a window: those without a key that a later
+    query can see are freed, and the next block taken is the last one freed."""
+
+    def __init__(self, blocks, width, seqs, window, sinks):
+        self.free = list(range(blocks))
+        self.tables = np.full((seqs, width), -1, dtype=np.int32)
+        self.window, self.sinks = window, sinks
+
+    def slots(self, s, start, count):
+        out = []
+        for p in range(start, start + count):
+            if self.tables[s, p // 16] < 0:
+                self.tables[s, p // 16] = self.free.pop()
+            out.append(int(self.tables[s, p // 16]) * 16 + p % 16)
+        return out
+
+    def trim(self, s, length):
+        """The next query stands at `length`."""
+        for b in range(self.tables.shape[1]):
+            last = b * 16 + 15
+            if self.tables[s, b] >= 0 and b * 16 >= self.sinks and last <= length - self.window:
+                self.free.append(int(self.tables[s, b]))
+                self.tables[s, b] = -1
+
+
+@pytest.mark.parametrize("Hq,Hkv,window,sinks,interleaved", [
+    (8, 2, 100, 4, False), (4, 4, 33, 0, True), (8, 1, 64, 20, False), (2, 1, 1, 1, False)])
+def test_chunks_then_decode_steps(pa, cuda_device, Hq, Hkv, window, sinks, interleaved):
+    dev = cuda_device
+    rng = np.random.default_rng(Hq + window)
+    g = torch.Generator(device=dev)
+    g.manual_seed(window)
+    prompts = [333, 1, 150]
+    steps, chunk = 20, 128
+    S, scale = len(prompts), 1.0 / math.sqrt(D)
+    inc, factor = pa.pa_rope_increments(64, base=10000.0, scaling="yarn", factor=4.0,
+                                        original_context=256)
+    inc = inc.to(dev)
+    qw, kw = (1 + 0.1 * torch.randn(D, generator=g, device=dev) for _ in range(2))
+    per_seq = (window + chunk + 31) // 16 + (sinks + 15) // 16 + 2
+    man = Manager(S * per_seq, 32, S, window, sinks)
+    kc, vc = (torch.full((S * per_seq, 16, Hkv, D), float("nan"), dtype=torch.bfloat16, device=dev)
+              for _ in range(2))
+    keys = [[] for _ in range(S)]
+    values = [[] for _ in range(S)]
+    done = [0] * S
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=dev)  # noqa: E731
+
+    def project(parts):
+        """(sequence, first position, count) of the step's rows: norms, rotation, scatter."""
+        T = sum(n for _, _, n in parts)
+        qkv = torch.randn(T, Hq + 2 * Hkv, D, generator=g, device=dev).bfloat16()
+        slots = [x for s, p, n in parts for x in man.slots(s, p, n)]
+        pos = [x for _, p, n in parts for x in range(p, p + n)]
+        q = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+        k = torch.empty(T, Hkv, D, dtype=torch.bfloat16, device=dev)
+        pa.pa_qk_norm_rope_cache(q, qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:],
+                                 torch.tensor(pos, device=dev), inc, kc, vc,
+                                 torch.tensor(slots, device=dev), q_weight=qw, k_weight=kw,
+                                 interleaved=interleaved, rope_factor=factor, k_out=k)
+        return q, k, qkv[:, Hq + Hkv:]
+
+    def keep(parts, k, v):
+        row = 0
+        for s, _, n in parts:
+            keys[s] += list(R.to64(k[row:row + n]))
+            values[s] += list(R.to64(v[row:row + n]))
+            row += n
+
+    def check(parts, q, out, p_step):
+        q, row = R.to64(q), 0
+        got = R.to64(out)
+        for s, p, n in parts:
+            k, v = np.array(keys[s]), np.array(values[s])
+            for i in range(n):
+                j = R.visible(p + i, window, sinks)
+                for h in range(Hq):
+                    o, _, tol, _ = R.attend(q[row, h], k[j, h * Hkv // Hq], v[j, h * Hkv // Hq],
+                                            scale, p_step)
+                    R.assert_within(got[row, h], o, tol, (s, p + i, h))
+                row += 1
+
+    while any(d < n for d, n in zip(done, prompts)):
+        parts = [(s, done[s], min(int(rng.integers(1, chunk + 1)), n - done[s]))
+                 for s, n in enumerate(prompts) if done[s] < n]
+        q, k, v = project(parts)
+        out = torch.full_like(q, float("nan"))
+        pa.pa_prefill_window(
+            out, q, kc, vc, torch.from_numpy(man.tables[[s for s, _, _ in parts]]).to(dev),
+            i32(np.cumsum([0] + [n for _, _, n in parts]).tolist()), i32([p for _, p, _ in parts]),
+            i32([p + n for _, p, n in parts]), max(n for _, _, n in parts), window, sinks, scale)
+        torch.cuda.synchronize()
+        keep(parts, k, v)
+        check(parts, q, out, 2.0**-8)
+        for s, p, n in parts:
+            done[s] += n
+            man.trim(s, done[s])
+    for _ in range(steps):
+        parts = [(s, done[s], 1) for s in range(S)]
+        q, k, v = project(parts)
+        out = torch.full_like(q, float("nan"))
+        pa.pa_decode_window(out, q, kc, vc, torch.from_numpy(man.tables).to(dev),
+                            i32([d + 1 for d in done]), window, sinks, scale)
+        torch.cuda.synchronize()
+        keep(parts, k, v)
+        check(parts, q, out, 2.0**-16)
+        for s in range(S):
+            done[s] += 1
+            man.trim(s, done[s])
+    assert pa.pa_device_error_flags() == 0
+    # the prompts' middles were given back on the way
+    assert (man.tables[0, :(done[0] - window) // 16] < 0).sum() > 0

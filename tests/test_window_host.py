@@ -151,3 +151,32 @@ def test_rope_increments_follow_their_formulas(lib):
     (dict(rot=64, scaling=4, factor=2.0, ctx=4096.0, p0=4.0, p1=1.0), INVALID)])
 def test_rope_increments_refuse(lib, kw, want):
     assert _increments(lib, **kw)[0] == want
+
+
+PREFILL = dict(out=P, q=P, k=P, v=P, bt=P, mb=4, cu=P, start=P, sl=P, C=2, T=64, max_q=40, Hq=8,
+               Hkv=2, D=128, bs=16, nb=64, window=100, sinks=4, scale=0.1, lse=None, stream=None)
+PREFILL_T = dict(zip(PREFILL, [V, V, V, V, V, I, V, V, V, I, I, I, I, I, I, I, L, I, I, F, V, V]))
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(window=0), INVALID), (dict(sinks=-1), INVALID), (dict(scale=-1.0), INVALID),
+    (dict(C=-1), INVALID), (dict(T=-1), INVALID), (dict(max_q=-1), INVALID), (dict(mb=0), INVALID),
+    (dict(nb=0), INVALID), (dict(Hq=9), INVALID), (dict(D=64), UNSUPPORTED),
+    (dict(bs=8), UNSUPPORTED), (dict(Hq=6), UNSUPPORTED), (dict(nb=1 << 28), UNSUPPORTED),
+    (dict(mb=1 << 28), UNSUPPORTED), (dict(C=0), OK), (dict(T=0), OK), (dict(max_q=0), OK),
+    (dict(out=None), INVALID), (dict(q=None), INVALID), (dict(k=None), INVALID),
+    (dict(v=None), INVALID), (dict(bt=None), INVALID), (dict(cu=None), INVALID),
+    (dict(start=None), INVALID), (dict(sl=None), INVALID), (dict(out=P + 8), INVALID),
+    (dict(q=P + 8), INVALID), (dict(k=P + 8), INVALID), (dict(v=P + 8), INVALID),
+    (dict(bt=P + 1), INVALID), (dict(cu=P + 2), INVALID), (dict(start=P + 2), INVALID),
+    (dict(sl=P + 2), INVALID), (dict(lse=P + 1), INVALID)])
+def test_prefill_window_refuses(lib, change, want):
+    assert call(lib.pa_prefill_window, PREFILL, PREFILL_T, **change) == want
+
+
+@pytest.mark.parametrize("limit", [0, 2000001])
+def test_stalled_prefill_refuses_its_limit(lib, limit):
+    names = [n for n in PREFILL if n not in ("lse", "stream")]
+    args = {n: PREFILL[n] for n in names} | {"limit": limit, "stream": None}
+    types = {n: PREFILL_T[n] for n in names} | {"limit": ctypes.c_uint, "stream": V}
+    assert call(lib.pa_test_prefill_window_stalled, args, types) == INVALID

@@ -62,6 +62,44 @@ def decode(q, kc, vc, tables, lens, window, sinks, scale):
     return out, lse, tol, tol_l
 
 
+def prefill(q, kc, vc, tables, cu, start, window, sinks, scale):
+    """As decode, for chunks.  Weights are rounded to bf16 before the product with V: each is off
+    by at most 2^-8 of itself, so an output by at most 2^-8 sum w |v| / sum w more."""
+    q, kc, vc = to64(q), to64(kc), to64(vc)
+    tables, cu, start = tables.cpu().numpy(), cu.cpu().numpy(), start.cpu().numpy()
+    T, Hq, D = q.shape
+    G = Hq // kc.shape[2]
+    out, tol = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
+    lse, tol_l = np.zeros((T, Hq)), np.zeros((T, Hq))
+    for c in range(len(start)):
+        rows = np.arange(cu[c], cu[c + 1])
+        if len(rows) == 0:
+            continue
+        pos = start[c] + np.arange(len(rows))
+        keys = np.union1d(np.arange(max(0, pos[0] - window + 1), pos[-1] + 1),
+                          np.arange(min(sinks, pos[-1] + 1)))
+        gap = pos[:, None] - keys
+        seen = (gap >= 0) & ((keys < sinks) | (gap < window))
+        at = tables[c, keys // 16], keys % 16
+        for h in range(Hq):
+            k, v = kc[at[0], at[1], h // G], vc[at[0], at[1], h // G]
+            qh = q[rows, h]
+            x = np.where(seen, scale * (qh @ k.T), -np.inf)
+            m = x.max(1, keepdims=True)
+            w = np.exp(x - m)
+            l = w.sum(1, keepdims=True)
+            out[rows, h] = w @ v / l
+            lse[rows, h] = (m + np.log(l))[:, 0]
+            size = np.where(seen, np.abs(qh) @ np.abs(k).T, 0).max(1, keepdims=True)
+            dp = (D * 2.0**-23 * scale * size + 2.0**-21 +
+                  2.0**-22 * np.where(seen, np.abs(x), 0).max(1, keepdims=True))
+            sums = seen.sum(1, keepdims=True) * 2.0**-23
+            tol[rows, h] = (2.0**-8 * np.abs(out[rows, h]) + (2 * dp + sums) * np.abs(v).max() +
+                            2.0**-8 * (w @ np.abs(v)) / l)
+            tol_l[rows, h] = (dp + sums)[:, 0] + 2.0**-22 * np.abs(lse[rows, h])
+    return out, lse, tol, tol_l
+
+
 def assert_within(got, ref, tol, what):
     got = to64(got) if isinstance(got, torch.Tensor) else got
     same = (got == ref) | (np.abs(got - ref) <= tol)
