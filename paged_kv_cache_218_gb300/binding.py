@@ -128,27 +128,56 @@ def _need(t: torch.Tensor, name: str, dtype, dims: Optional[int] = None, contigu
         raise ValueError(f"{name} must be contiguous")
 
 
-def _same(name: str, t: torch.Tensor, shape) -> None:
+def _refuse(t, name: str, dtype, shape, device: int) -> None:
+    """The reason why _arg takes this tensor for no such argument."""
+    _need(t, name, dtype, len(shape))
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} is on {t.device}, and other arguments on cuda:{device}")
+
+
+def _arg(t, name: str, dtype, shape, device: int) -> int:
+    """The address of a contiguous tensor of this type and shape on this device.
+    (One pass of cheap checks: a small call spends most of its time here.)"""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and
+            t.shape == shape and t.is_contiguous()):
+        return t.data_ptr()
+    return _refuse(t, name, dtype, shape, device)
+
+
+def _rows(t, name: str, shape, device: int) -> int:
+    """_arg for bf16 rows [tokens, heads, head_dim] at any token stride."""
+    if (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == device and
+            t.shape == shape):
+        st = t.stride()
+        if st[2] == 1 and (st[1] == shape[2] or shape[1] == 1):
+            return t.data_ptr()
+        raise ValueError(f"{name} must be contiguous within a token")
+    _need(t, name, torch.bfloat16, 3, contiguous=False)
+    return _refuse(t.contiguous(), name, torch.bfloat16, shape, device)
+
+
+def _queue(first, device: int, stream) -> int:
+    """The stream of a call whose tensors are on `device`, which has to be the
+    current one."""
+    if device != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {first.device}, current device "
+                         f"cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def _status(fn: str, rc: int) -> None:
+    if rc:
+        raise PAError(fn, rc)
 
 
 def _int32(name: str, v, least: int) -> int:
     """An int argument of the C call: ctypes would wrap a larger one silently."""
-    v = int(v)
+    if type(v) is not int:
+        v = int(v)
     if not least <= v <= 0x7FFFFFFF:
         raise ValueError(f"{name} must be in [{least}, 2**31 - 1], got {v}")
     return v
-
-
-def _one_device(first: torch.Tensor, *others) -> None:
-    """Every tensor on the device of the first, and that the current one (the
-    call is queued on a stream of the current device)."""
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
-    if first.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors on {first.device}, current device {torch.cuda.current_device()}")
 
 
 def pa_status_string(status: int) -> str:
@@ -338,32 +367,31 @@ def pa_prefill_window(out, q, k_cache, v_cache, block_tables, cu_q_lens, q_start
                       max_q_len, window, sinks, scale, out_lse=None, stream=None) -> None:
     """pa_prefill_chunk under a sliding window: the query at position p sees keys
     j <= p with j < sinks or p - j < window."""
-    _need(out, "out", torch.bfloat16, 3)
     _need(q, "q", torch.bfloat16, 3)
-    _need(k_cache, "k_cache", torch.bfloat16, 4)
-    _need(v_cache, "v_cache", torch.bfloat16, 4)
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(cu_q_lens, "cu_q_lens", torch.int32, 1)
-    _need(q_start_pos, "q_start_pos", torch.int32, 1)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    T, Hq, D = q.shape
-    nb, bs, Hkv, Dk = k_cache.shape
-    C = q_start_pos.shape[0]
-    _same("out", out, q.shape)
-    _same("v_cache", v_cache, k_cache.shape)
-    if (Dk != D or block_tables.shape[0] != C or seq_lens.shape[0] != C or
-            cu_q_lens.shape[0] != C + 1):
-        raise ValueError("q, k_cache, block_tables, cu_q_lens, q_start_pos and seq_lens do not "
-                         "fit together")
-    if out_lse is not None:
-        _need(out_lse, "out_lse", torch.float32, 2)
-        _same("out_lse", out_lse, (T, Hq))
-    _one_device(q, out, k_cache, v_cache, block_tables, cu_q_lens, q_start_pos, seq_lens, out_lse)
-    _check("pa_prefill_window", _lib.pa_prefill_window(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-        block_tables.shape[1], _ptr(cu_q_lens), _ptr(q_start_pos), _ptr(seq_lens), C, T,
-        _int32("max_q_len", max_q_len, 0), Hq, Hkv, D, bs, nb, _int32("window", window, 1),
-        _int32("sinks", sinks, 0), float(scale), _ptr(out_lse), _stream(stream)))
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        _need(k_cache, "k_cache", torch.bfloat16, 4)
+    if not isinstance(cu_q_lens, torch.Tensor) or cu_q_lens.dim() != 1:
+        _need(cu_q_lens, "cu_q_lens", torch.int32, 1)
+    T, Hq, D = shape = q.shape
+    nb, bs, Hkv, _ = k_cache.shape
+    C = cu_q_lens.shape[0] - 1
+    dev = q.get_device()
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
+        _need(block_tables, "block_tables", torch.int32, 2)
+    mb = block_tables.shape[1]
+    if C < 0:
+        raise ValueError("cu_q_lens must hold one more entry than there are chunks")
+    args = (_arg(out, "out", torch.bfloat16, shape, dev), q.data_ptr(),
+            _arg(k_cache, "k_cache", torch.bfloat16, (nb, bs, Hkv, D), dev),
+            _arg(v_cache, "v_cache", torch.bfloat16, (nb, bs, Hkv, D), dev),
+            _arg(block_tables, "block_tables", torch.int32, (C, mb), dev), mb,
+            _arg(cu_q_lens, "cu_q_lens", torch.int32, (C + 1,), dev),
+            _arg(q_start_pos, "q_start_pos", torch.int32, (C,), dev),
+            _arg(seq_lens, "seq_lens", torch.int32, (C,), dev), C, T,
+            _int32("max_q_len", max_q_len, 0), Hq, Hkv, D, bs, nb, _int32("window", window, 1),
+            _int32("sinks", sinks, 0), scale,
+            None if out_lse is None else _arg(out_lse, "out_lse", torch.float32, (T, Hq), dev))
+    _status("pa_prefill_window", _lib.pa_prefill_window(*args, _queue(q, dev, stream)))
 
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
@@ -390,59 +418,44 @@ def pa_rope_increments(rot_dim, base=10000.0, scaling="none", factor=1.0, origin
 def _norm_rope(fn, pool_dtype, q_out, q, k, v, positions, increments, k_cache, v_cache,
                slot_mapping, scales, q_weight, k_weight, eps, interleaved, rope_factor, k_out,
                stream):
-    _need(q, "q", torch.bfloat16, 3, contiguous=False)
-    _need(k, "k", torch.bfloat16, 3, contiguous=False)
-    T, Hq, D = q.shape
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        _need(q, "q", torch.bfloat16, 3, contiguous=False)
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        _need(k, "k", torch.bfloat16, 3, contiguous=False)
+    T, Hq, D = shape = q.shape
     Hkv = k.shape[1]
-    _need(q_out, "q_out", torch.bfloat16, 3)
-    _same("q_out", q_out, q.shape)
-    _same("k", k, (T, Hkv, D))
-    rows = [(q, "q"), (k, "k")]
+    kv_shape = (T, Hkv, D)
+    dev = q.get_device()
+    qp, kp = _rows(q, "q", shape, dev), _rows(k, "k", kv_shape, dev)
+    q_row, k_row = Hq * D, Hkv * D
+    # (a single token's stride is never used: any view of one row will do)
+    q_stride, k_stride = (q.stride(0), k.stride(0)) if T > 1 else (q_row, k_row)
+    vp, v_stride, kcp, vcp, slots, bs, nb = None, k_row, None, None, None, 0, 0
     if k_cache is not None or v_cache is not None or scales:
-        _need(v, "v", torch.bfloat16, 3, contiguous=False)
-        _same("v", v, k.shape)
-        rows.append((v, "v"))
-        _need(k_cache, "k_cache", pool_dtype, 4)
-        _need(v_cache, "v_cache", pool_dtype, 4)
-        _same("v_cache", v_cache, k_cache.shape)
-        _same("k_cache", k_cache, (*k_cache.shape[:2], Hkv, D))
-        _need(slot_mapping, "slot_mapping", torch.int64, 1)
-        _same("slot_mapping", slot_mapping, (T,))
+        if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+            _need(k_cache, "k_cache", pool_dtype, 4)
         nb, bs = k_cache.shape[:2]
-        vp, v_stride = v.data_ptr(), v.stride(0)
-    else:
-        slot_mapping, nb, bs, vp, v_stride = None, 0, 0, None, 0
-    for t, n in rows:
-        if t.stride(2) != 1 or (t.stride(1) != D and t.shape[1] > 1):
-            raise ValueError(f"{n} must be contiguous within a token")
-    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _need(t, n, torch.float32, 1)
-            _same(n, t, (D,))
-    if k_out is not None:
-        _need(k_out, "k_out", torch.bfloat16, 3)
-        _same("k_out", k_out, k.shape)
-    rot = 0
+        vp = _rows(v, "v", kv_shape, dev)
+        if T > 1:
+            v_stride = v.stride(0)
+        kcp = _arg(k_cache, "k_cache", pool_dtype, (nb, bs, Hkv, D), dev)
+        vcp = _arg(v_cache, "v_cache", pool_dtype, (nb, bs, Hkv, D), dev)
+        slots = _arg(slot_mapping, "slot_mapping", torch.int64, (T,), dev)
+    rot, pp, ip = 0, None, None
     if increments is not None:
         _need(increments, "increments", torch.int64, 1)
-        _need(positions, "positions", torch.int64, 1)
-        _same("positions", positions, (T,))
         rot = 2 * increments.shape[0]
-    else:
-        positions = None
+        ip = _arg(increments, "increments", torch.int64, (rot // 2,), dev)
+        pp = _arg(positions, "positions", torch.int64, (T,), dev)
+    args = [_arg(q_out, "q_out", torch.bfloat16, shape, dev),
+            None if k_out is None else _arg(k_out, "k_out", torch.bfloat16, kv_shape, dev),
+            qp, kp, vp, q_stride, k_stride, v_stride,
+            None if q_weight is None else _arg(q_weight, "q_weight", torch.float32, (D,), dev),
+            None if k_weight is None else _arg(k_weight, "k_weight", torch.float32, (D,), dev),
+            eps, pp, ip, rot, 1 if interleaved else 0, rope_factor, kcp, vcp, slots]
     for t, n in zip(scales, ("k_scales", "v_scales")):
-        _need(t, n, torch.float32, 1)
-        _same(n, t, (Hkv,))
-    _one_device(q, k, v if vp else None, q_out, k_out, k_cache, v_cache, slot_mapping, q_weight,
-                k_weight, positions, increments, *scales)
-    # a single token's stride is never used: any view of one row will do
-    one = T <= 1
-    _check(fn, getattr(_lib, fn)(
-        _ptr(q_out), _ptr(k_out), _ptr(q), _ptr(k), vp, Hq * D if one else q.stride(0),
-        Hkv * D if one else k.stride(0), Hkv * D if one else v_stride, _ptr(q_weight),
-        _ptr(k_weight), float(eps), _ptr(positions), _ptr(increments), rot, int(bool(interleaved)),
-        float(rope_factor), _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping),
-        *(_ptr(t) for t in scales), T, Hq, Hkv, D, bs, nb, _stream(stream)))
+        args.append(_arg(t, n, torch.float32, (Hkv,), dev))
+    _status(fn.__name__, fn(*args, T, Hq, Hkv, D, bs, nb, _queue(q, dev, stream)))
 
 
 def pa_qk_norm_rope_cache(q_out, q, k, v, positions, increments, k_cache, v_cache, slot_mapping,
@@ -452,7 +465,7 @@ def pa_qk_norm_rope_cache(q_out, q, k, v, positions, increments, k_cache, v_cach
     no norm), rotation of the first 2 * len(increments) columns (None: none),
     q -> q_out, k -> its slots of k_cache and k_out, v -> its slots of v_cache.
     With both pools None: no scatter, k_out required."""
-    _norm_rope("pa_qk_norm_rope_cache", torch.bfloat16, q_out, q, k, v, positions, increments,
+    _norm_rope(_lib.pa_qk_norm_rope_cache, torch.bfloat16, q_out, q, k, v, positions, increments,
                k_cache, v_cache, slot_mapping, (), q_weight, k_weight, eps, interleaved,
                rope_factor, k_out, stream)
 
@@ -462,7 +475,7 @@ def pa_qk_norm_rope_cache_fp8(q_out, q, k, v, positions, increments, k_cache, v_
                               eps=1e-6, interleaved=False, rope_factor=1.0, k_out=None,
                               stream=None) -> None:
     """pa_qk_norm_rope_cache into uint8 E4M3 pools with per-kv-head fp32 scales."""
-    _norm_rope("pa_qk_norm_rope_cache_fp8", torch.uint8, q_out, q, k, v, positions, increments,
+    _norm_rope(_lib.pa_qk_norm_rope_cache_fp8, torch.uint8, q_out, q, k, v, positions, increments,
                k_cache, v_cache, slot_mapping, (k_scales, v_scales), q_weight, k_weight, eps,
                interleaved, rope_factor, k_out, stream)
 
@@ -471,27 +484,23 @@ def pa_decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, window, s
                      out_lse=None, stream=None) -> None:
     """Decode over each sequence's last `window` keys and first `sinks` keys;
     table entries of blocks without a visible key are not read."""
-    _need(out, "out", torch.bfloat16, 3)
     _need(q, "q", torch.bfloat16, 3)
-    _need(k_cache, "k_cache", torch.bfloat16, 4)
-    _need(v_cache, "v_cache", torch.bfloat16, 4)
-    _need(block_tables, "block_tables", torch.int32, 2)
-    _need(seq_lens, "seq_lens", torch.int32, 1)
-    S, Hq, D = q.shape
-    nb, bs, Hkv, Dk = k_cache.shape
-    _same("out", out, q.shape)
-    _same("v_cache", v_cache, k_cache.shape)
-    if Dk != D or block_tables.shape[0] != S or seq_lens.shape[0] != S:
-        raise ValueError("q, k_cache, block_tables and seq_lens do not fit together")
-    if out_lse is not None:
-        _need(out_lse, "out_lse", torch.float32, 2)
-        _same("out_lse", out_lse, (S, Hq))
-    _one_device(q, out, k_cache, v_cache, block_tables, seq_lens, out_lse)
-    _check("pa_decode_window", _lib.pa_decode_window(
-        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-        block_tables.shape[1], _ptr(seq_lens), S, Hq, Hkv, D, bs, nb,
-        _int32("window", window, 1), _int32("sinks", sinks, 0), float(scale), _ptr(out_lse),
-        _stream(stream)))
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        _need(k_cache, "k_cache", torch.bfloat16, 4)
+    S, Hq, D = shape = q.shape
+    nb, bs, Hkv, _ = k_cache.shape
+    dev = q.get_device()
+    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
+        _need(block_tables, "block_tables", torch.int32, 2)
+    mb = block_tables.shape[1]
+    args = (_arg(out, "out", torch.bfloat16, shape, dev), q.data_ptr(),
+            _arg(k_cache, "k_cache", torch.bfloat16, (nb, bs, Hkv, D), dev),
+            _arg(v_cache, "v_cache", torch.bfloat16, (nb, bs, Hkv, D), dev),
+            _arg(block_tables, "block_tables", torch.int32, (S, mb), dev), mb,
+            _arg(seq_lens, "seq_lens", torch.int32, (S,), dev), S, Hq, Hkv, D, bs, nb,
+            _int32("window", window, 1), _int32("sinks", sinks, 0), scale,
+            None if out_lse is None else _arg(out_lse, "out_lse", torch.float32, (S, Hq), dev))
+    _status("pa_decode_window", _lib.pa_decode_window(*args, _queue(q, dev, stream)))
 
 
 def pa_decode_noalloc(out, q, k_cache, v_cache, block_tables, seq_lens, scale, out_lse=None,

@@ -1247,7 +1247,7 @@ static int norm_rope_impl(void* q_out, void* k_out, const void* q, const void* k
   if (num_tokens < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || rot_dim < 0 || rot_dim > D)
     return PA_ERR_INVALID;
   if (D % 16 != 0 || D > 256 || rot_dim % 16 != 0) return PA_ERR_UNSUPPORTED;
-  if (Hq > (1 << 20) || Hkv > (1 << 20)) return PA_ERR_UNSUPPORTED;
+  if (Hq > (1 << 15) || Hkv > (1 << 15)) return PA_ERR_UNSUPPORTED;  // the grid's second axis
   if ((q_weight || k_weight) && (!(eps >= 0.f) || !isfinite(eps))) return PA_ERR_INVALID;
   if (rot_dim > 0 && !isfinite(rope_factor)) return PA_ERR_INVALID;
   const bool pools = k_cache || v_cache;
@@ -1335,8 +1335,8 @@ static int norm_rope_impl(void* q_out, void* k_out, const void* q, const void* k
   a.num_kv_heads = Hkv;
   a.head_dim = D;
   a.rot_dim = rot_dim;
-  return launch_norm_rope(a, interleaved != 0, fp8, d->num_sms,
-                          static_cast<cudaStream_t>(stream)) == cudaSuccess
+  a.interleaved = interleaved != 0;
+  return launch_norm_rope(a, fp8, d->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
 }

@@ -195,7 +195,7 @@ struct RopeArgs {
   int num_kv_heads;
   int head_dim;
   int rot_dim;
-  int slices;                // warps per token; set by the launcher
+  int interleaved;
 };
 
 constexpr int kMaxWindowSplit = 8;  // portable cluster size
@@ -224,8 +224,7 @@ bool cascade_shape(int num_kv_heads, int group, int max_group, int* kv_per_cta, 
                    int* stages);
 cudaError_t launch_cascade_prefix(const CascadeArgs& a, const CUtensorMap* tm_k,
                                   const CUtensorMap* tm_v, cudaStream_t stream);
-cudaError_t launch_norm_rope(const RopeArgs& a, bool interleaved, bool kv_fp8, int num_sms,
-                             cudaStream_t stream);
+cudaError_t launch_norm_rope(const RopeArgs& a, bool kv_fp8, int num_sms, cudaStream_t stream);
 cudaError_t launch_decode_window(WindowDecodeArgs a, int head_dim, int num_sms,
                                  cudaStream_t stream);
 // One launch for a hybrid batch: the balanced decode (bf16, head_dim 128) on

@@ -13,15 +13,20 @@
 // Angles.  A frequency comes as a 64-bit fixed-point number of turns per
 // position, so that position * increment mod 2^64 is the exact phase: one
 // integer multiply, with no loss at far positions (in fp32, position 10^6
-// would be off by 0.06 rad).  The top 32 bits, as a signed number of half
-// turns, go to sincospif.
+// would be off by 0.06 rad).  The top 32 bits, as a signed angle in [-pi, pi],
+// go to the special-function unit, whose sine and cosine are within 2^-21
+// there: 1/8000 of a bf16 step of a value of the pair's size.
 //
 // What bounds it: HBM at large batches (each element is read and written
-// once), latency at a decode step's.  A warp takes one token and a run of its
-// rows; each lane keeps 8 columns (16 bytes) and the sines and cosines of its
-// columns, which all heads of the token share, in registers.  Rows of a head
-// take 8, 16 or 32 lanes (head_dim to 64, 128, 256), so the sum of squares is
-// a few shuffles and the partner of a half-layout pair another one.
+// once), latency at a decode step's.  A warp takes one token and a few steps
+// of 32 / LPR rows of one kind (queries, keys or values), all of whose loads
+// it issues at once.  A lane keeps 16 columns of a row, as two 16-byte pieces
+// that hold both members of its eight pairs (half layout: columns [8 i, + 8)
+// and [R / 2 + 8 i, + 8); otherwise 16 columns in a row), so a rotation needs
+// no other lane.  A row takes LPR = 4, 8 or 16 lanes (head_dim to 64, 128,
+// 256); the lanes with the same columns share the work on the angles.  Norm
+// weights and sines are multiplied together once per warp, and the arithmetic
+// runs on pairs of fp32 values.
 #include <math.h>
 
 #include "../../include/pa.h"
@@ -31,187 +36,286 @@
 namespace pa {
 namespace {
 
-constexpr int kRows = 4;  // rows in flight per lane
+constexpr float kPiOver2to31 = 3.14159265358979f / 2147483648.f;
 
-__device__ __forceinline__ void unpack8(uint4 u, float (&x)[8]) {
+__device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// A lane's two pieces of a row as the members (a, b) of its pairs: as loaded,
+// or, interleaved, with the even columns in the first piece and the odd ones
+// in the second.  The same exchange puts a result's pieces back.
+__device__ __forceinline__ void deinterleave(uint4& u, uint4& v) {
+  const uint4 p = u, q = v;
+  u = make_uint4(prmt(p.x, p.y, 0x5410), prmt(p.z, p.w, 0x5410), prmt(q.x, q.y, 0x5410),
+                 prmt(q.z, q.w, 0x5410));
+  v = make_uint4(prmt(p.x, p.y, 0x7632), prmt(p.z, p.w, 0x7632), prmt(q.x, q.y, 0x7632),
+                 prmt(q.z, q.w, 0x7632));
+}
+
+__device__ __forceinline__ void interleave(uint4& u, uint4& v) {
+  const uint4 p = u, q = v;
+  u = make_uint4(prmt(p.x, q.x, 0x5410), prmt(p.x, q.x, 0x7632), prmt(p.y, q.y, 0x5410),
+                 prmt(p.y, q.y, 0x7632));
+  v = make_uint4(prmt(p.z, q.z, 0x5410), prmt(p.z, q.z, 0x7632), prmt(p.w, q.w, 0x5410),
+                 prmt(p.w, q.w, 0x7632));
+}
+
+// Bytes of E4M3 codes: 8 columns a piece, the same exchange.
+__device__ __forceinline__ void interleave(uint2& u, uint2& v) {
+  const uint2 p = u, q = v;
+  u = make_uint2(prmt(p.x, q.x, 0x5140), prmt(p.x, q.x, 0x7362));
+  v = make_uint2(prmt(p.y, q.y, 0x5140), prmt(p.y, q.y, 0x7362));
+}
+
+// Eight bf16 columns as four pairs of fp32, and back.
+__device__ __forceinline__ void unpack(const uint4& u, uint64_t (&x)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = f32x2(lo_f32(w[i]), hi_f32(w[i]));
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                    pack_bf16x2(x[6], x[7]));
-}
-
-// E4M3(x / scale), the division in IEEE fp32: the codes of pa_reshape_and_cache_fp8.
-__device__ __forceinline__ uint2 quant8(const float (&x)[8], float scale) {
-  uint32_t r[2];
+__device__ __forceinline__ uint4 pack(const uint64_t (&x)[4]) {
+  uint32_t w[4];
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const uint32_t a = f32x2_to_e4m3x2(__fdiv_rn(x[4 * k], scale), __fdiv_rn(x[4 * k + 1], scale));
-    const uint32_t b =
-        f32x2_to_e4m3x2(__fdiv_rn(x[4 * k + 2], scale), __fdiv_rn(x[4 * k + 3], scale));
-    r[k] = a | (b << 16);
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = f32x2_parts(x[i]);
+    w[i] = pack_bf16x2(f.x, f.y);
   }
-  return make_uint2(r[0], r[1]);
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// LPR lanes per row; IL: interleaved pairs; F8: E4M3 pools.
-template <int LPR, bool IL, bool F8>
-__global__ void __launch_bounds__(128) norm_rope_kernel(const RopeArgs a) {
-  constexpr int HW = 32 / LPR;  // heads a warp takes at once
+// 16 fp32 weights at w + c0 and w + c1, split the same way.
+__device__ __forceinline__ void load_weights(const float* w, int c0, int c1, bool interleaved,
+                                             uint64_t (&a)[4], uint64_t (&b)[4]) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float4 u = *reinterpret_cast<const float4*>(w + c0 + 4 * e);
+    const float4 t = *reinterpret_cast<const float4*>(w + c1 + 4 * e);
+    if (interleaved) {
+      a[e] = f32x2(u.x, u.z);
+      b[e] = f32x2(u.y, u.w);
+      a[2 + e] = f32x2(t.x, t.z);
+      b[2 + e] = f32x2(t.y, t.w);
+    } else {
+      a[2 * e] = f32x2(u.x, u.y);
+      a[2 * e + 1] = f32x2(u.z, u.w);
+      b[2 * e] = f32x2(t.x, t.y);
+      b[2 * e + 1] = f32x2(t.z, t.w);
+    }
+  }
+}
+
+// E4M3(x / scale) of 8 columns, the division in IEEE fp32: the codes of
+// pa_reshape_and_cache_fp8.  The product with the reciprocal is within 2^-22
+// of that quotient, and rounding to E4M3 is monotone: where the codes of the
+// product a little lower and a little higher agree, they are the quotient's
+// code, and the division (eight times the work) is left out.  `inv` 0: a
+// scale whose reciprocal is not a normal number; divide.
+__device__ __forceinline__ uint2 quant(const uint64_t (&x)[4], float scale, float inv) {
+  uint32_t lo[2] = {0, 0}, hi[2] = {0, 0};
+  const uint64_t inv_lo = f32x2(inv * (1.f - 0x1p-21f), inv * (1.f - 0x1p-21f));
+  const uint64_t inv_hi = f32x2(inv * (1.f + 0x1p-21f), inv * (1.f + 0x1p-21f));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 l = f32x2_parts(mul2(x[i], inv_lo)), h = f32x2_parts(mul2(x[i], inv_hi));
+    lo[i / 2] |= static_cast<uint32_t>(f32x2_to_e4m3x2(l.x, l.y)) << (16 * (i & 1));
+    hi[i / 2] |= static_cast<uint32_t>(f32x2_to_e4m3x2(h.x, h.y)) << (16 * (i & 1));
+  }
+  if (lo[0] != hi[0] || lo[1] != hi[1] || inv == 0.f) {
+    lo[0] = lo[1] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = f32x2_parts(x[i]);
+      lo[i / 2] |= static_cast<uint32_t>(
+                       f32x2_to_e4m3x2(__fdiv_rn(f.x, scale), __fdiv_rn(f.y, scale)))
+                   << (16 * (i & 1));
+    }
+  }
+  return make_uint2(lo[0], lo[1]);
+}
+
+__device__ __forceinline__ float reciprocal(float scale) {
+  return scale >= 0x1p-100f && scale <= 0x1p100f ? __frcp_rn(scale) : 0.f;
+}
+
+// LPR lanes per row; R: steps of 32 / LPR rows per warp; F8: E4M3 pools; NORM:
+// at least one of the norms; EVEN: rows fill their lanes (head_dim = 16 LPR)
+// and heads fill their steps.
+template <int LPR, int R, bool F8, bool NORM, bool EVEN>
+__global__ void __launch_bounds__(128, 6) norm_rope_kernel(const RopeArgs a) {
+  constexpr int HW = 32 / LPR;  // rows of a step
   griddep_launch_dependents();
   griddep_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t wid = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int64_t tok = wid / a.slices;
+  const int64_t tok = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (tok >= a.num_tokens) return;
-  const int slice = static_cast<int>(wid % a.slices);
+  const int sub = lane / LPR, i = lane % LPR;  // row of the step, lane of the row
+  const int D = EVEN ? 16 * LPR : a.head_dim;
+  const bool live = EVEN || i * 16 < D;
+  const bool rot = i * 16 < a.rot_dim;
+  const bool split = !a.interleaved && rot;  // the pieces are half a rotary width apart
+  const int c0 = split ? i * 8 : i * 16;
+  const int c1 = split ? i * 8 + a.rot_dim / 2 : i * 16 + 8;
 
-  const int sub = lane / LPR, c = lane % LPR;  // head within the step, 16-byte column piece
-  const int D = a.head_dim, half = a.rot_dim / 2;
-  const bool live = c * 8 < D;
-  const bool rot = c * 8 < a.rot_dim;
-  const int64_t pos = a.rot_dim > 0 ? a.positions[tok] : 0;
-  // the lane's angles: half layout, its 8 columns' (sine negated in the lower
-  // half, whose partner is c + half / 8; the upper half's is c - half / 8);
-  // interleaved, its 4 pairs'
-  constexpr int NA = IL ? 4 : 8;
-  float cs[NA], sn[NA];
+  // blockIdx.y: the queries' warps of a token, the keys', the values'
+  constexpr int per = HW * R;  // rows of a warp
+  const int uq = (a.num_q_heads + per - 1) / per, uk = (a.num_kv_heads + per - 1) / per;
+  const int u = blockIdx.y;
+  const int kind = u < uq ? 0 : (u < uq + uk ? 1 : 2);
+  const int h0 = (kind == 0 ? u : (kind == 1 ? u - uq : u - uq - uk)) * per;
+  const int heads = kind == 0 ? a.num_q_heads : a.num_kv_heads;
+  const int steps = min(R, (heads - h0 + HW - 1) / HW);  // >= 1
+  auto mine = [&](int r) { return EVEN || (live && h0 + r * HW + sub < heads); };
+  const __nv_bfloat16* const src = (kind == 0 ? a.q + tok * a.q_stride
+                                              : (kind == 1 ? a.k + tok * a.k_stride
+                                                           : a.v + tok * a.v_stride)) +
+                                   (h0 + sub) * D;
+  uint4 raw[R][2];
 #pragma unroll
-  for (int i = 0; i < NA; ++i) {
-    cs[i] = 1.f;
-    sn[i] = 0.f;
-  }
-  int partner = lane;
-  if (rot) {
-    const bool lower = c * 8 < half;
-    if (!IL) partner = lower ? lane + half / 8 : lane - half / 8;
-    const int i0 = IL ? c * 4 : (lower ? c * 8 : c * 8 - half);
-#pragma unroll
-    for (int i = 0; i < NA; ++i) {
-      const uint64_t phase = static_cast<uint64_t>(pos) * static_cast<uint64_t>(a.increments[i0 + i]);
-      const float turns2 = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
-      float sv, cv;
-      sincospif(turns2, &sv, &cv);
-      cs[i] = cv * a.rope_factor;
-      sn[i] = (!IL && lower ? -sv : sv) * a.rope_factor;
+  for (int r = 0; r < R; ++r) {
+    raw[r][0] = raw[r][1] = make_uint4(0, 0, 0, 0);
+    if (r < steps && mine(r)) {
+      raw[r][0] = *reinterpret_cast<const uint4*>(src + r * HW * D + c0);
+      raw[r][1] = *reinterpret_cast<const uint4*>(src + r * HW * D + c1);
     }
   }
-  const int64_t slot = a.k_cache ? a.slots[tok] : -1;
-  bool cached = slot >= 0;
-  if (cached && slot >= a.num_slots) {
-    if (slice == 0 && lane == 0) atomicOr(a.err, PA_DEVERR_SLOT);
-    cached = false;
+  int64_t slot = -1;
+  if (kind > 0 && a.k_cache) {
+    slot = a.slots[tok];
+    if (slot >= a.num_slots) {
+      if (lane == 0 && u == uq) atomicOr(a.err, PA_DEVERR_SLOT);
+      slot = -1;
+    }
+  }
+  // where this lane's first row goes: bf16 outputs y0 and (bf16 pools) y1, codes z
+  const int64_t in_cache = slot * a.num_kv_heads * D + (h0 + sub) * D;
+  void* const pool = kind == 1 ? a.k_cache : a.v_cache;
+  __nv_bfloat16* y0 = kind == 0 ? a.q_out : (kind == 1 ? a.k_out : nullptr);
+  if (y0) y0 += (tok * heads + h0 + sub) * D;
+  __nv_bfloat16* const y1 =
+      !F8 && slot >= 0 ? static_cast<__nv_bfloat16*>(pool) + in_cache : nullptr;
+  uint8_t* const z = F8 && slot >= 0 ? static_cast<uint8_t*>(pool) + in_cache : nullptr;
+
+  if (kind == 2 && !F8) {  // values pass through
+    if (!y1) return;
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      if (r < steps && mine(r)) {
+        *reinterpret_cast<uint4*>(y1 + r * HW * D + c0) = raw[r][0];
+        *reinterpret_cast<uint4*>(y1 + r * HW * D + c1) = raw[r][1];
+      }
+    return;
   }
 
-  // row groups of HW heads: queries, keys, values
-  const int gq = (a.num_q_heads + HW - 1) / HW, gk = (a.num_kv_heads + HW - 1) / HW;
-  const int groups = gq + gk + (a.k_cache ? gk : 0);
-  const int per = (groups + a.slices - 1) / a.slices;
-  const int g1 = min(groups, (slice + 1) * per);
+  // Coefficients of this lane's pairs: a' = rs (ac a + bs b), b' = rs (bc b + as a),
+  // with rs = 1 / rms, ac = wa cos, bs = -wb sin, bc = wb cos, as = wa sin.
+  uint64_t ac[4], as[4], bc[4], bs[4];
+  const float* const w = kind == 0 ? a.q_weight : (kind == 1 ? a.k_weight : nullptr);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) ac[e] = bc[e] = f32x2(1.f, 1.f);
+  const bool turn = rot && kind < 2;
+  if (NORM && w && live) load_weights(w, c0, c1, a.interleaved && turn, ac, bc);
+  if (kind < 2 && a.rot_dim > 0) {
+    // the HW lanes with the same columns compute 8 / HW angles each
+    const int64_t pos = a.positions[tok];
+    constexpr int NA = HW >= 8 ? 1 : 8 / HW;
+    float c[NA], s[NA];
+#pragma unroll
+    for (int e = 0; e < NA; ++e) {
+      const uint64_t inc = rot ? static_cast<uint64_t>(a.increments[i * 8 + (sub * NA + e) % 8]) : 0;
+      const uint64_t phase = static_cast<uint64_t>(pos) * inc;
+      __sincosf(static_cast<float>(static_cast<int32_t>(phase >> 32)) * kPiOver2to31, &s[e], &c[e]);
+      c[e] *= a.rope_factor;
+      s[e] *= a.rope_factor;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float cc[2], ss[2];
+#pragma unroll
+      for (int f = 0; f < 2; ++f) {
+        const int from = (2 * e + f) / NA * LPR + i;
+        cc[f] = __shfl_sync(0xffffffffu, c[(2 * e + f) % NA], from);
+        ss[f] = __shfl_sync(0xffffffffu, s[(2 * e + f) % NA], from);
+      }
+      as[e] = mul2(ac[e], f32x2(ss[0], ss[1]));
+      bs[e] = mul2(bc[e], f32x2(-ss[0], -ss[1]));
+      if (rot) {
+        ac[e] = mul2(ac[e], f32x2(cc[0], cc[1]));
+        bc[e] = mul2(bc[e], f32x2(cc[0], cc[1]));
+      }
+    }
+  }
   const float inv_d = 1.f / static_cast<float>(D);
-
-  for (int g0 = slice * per; g0 < g1; g0 += kRows) {
-    uint4 raw[kRows];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int g = g0 + r;
-      const int kind = g < gq ? 0 : (g < gq + gk ? 1 : 2);
-      const int h = (g - (kind == 0 ? 0 : (kind == 1 ? gq : gq + gk))) * HW + sub;
-      const __nv_bfloat16* src = kind == 0 ? a.q + tok * a.q_stride
-                                           : (kind == 1 ? a.k + tok * a.k_stride
-                                                        : a.v + tok * a.v_stride);
-      raw[r] = make_uint4(0, 0, 0, 0);
-      if (g < g1 && live && h < (kind == 0 ? a.num_q_heads : a.num_kv_heads))
-        raw[r] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(h) * D + c * 8);
+  for (int r = 0; r < R; ++r) {
+    if (r >= steps) break;
+    if (a.interleaved && turn) deinterleave(raw[r][0], raw[r][1]);
+    uint64_t xa[4], xb[4];
+    unpack(raw[r][0], xa);
+    unpack(raw[r][1], xb);
+    if (NORM) {
+      uint64_t s2 = mul2(xa[0], xa[0]);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (e) s2 = fma2(xa[e], xa[e], s2);
+        s2 = fma2(xb[e], xb[e], s2);
+      }
+      const float2 sp = f32x2_parts(s2);
+      float ss = sp.x + sp.y;
+#pragma unroll
+      for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+      const float rs = w ? rsqrtf(fmaf(ss, inv_d, a.eps)) : 1.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        xa[e] = mul2(xa[e], f32x2(rs, rs));
+        xb[e] = mul2(xb[e], f32x2(rs, rs));
+      }
     }
+    if (turn) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int g = g0 + r;
-      if (g >= g1) break;
-      const int kind = g < gq ? 0 : (g < gq + gk ? 1 : 2);
-      const int h = (g - (kind == 0 ? 0 : (kind == 1 ? gq : gq + gk))) * HW + sub;
-      const bool mine = live && h < (kind == 0 ? a.num_q_heads : a.num_kv_heads);
-      float x[8];
-      unpack8(raw[r], x);
-      if (kind < 2) {
-        const float* w = kind == 0 ? a.q_weight : a.k_weight;
-        if (w) {
-          float ss = 0.f;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-          for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-          const float rs = rsqrtf(fmaf(ss, inv_d, a.eps));
-          if (live) {
-            const float4 w0 = *reinterpret_cast<const float4*>(w + c * 8);
-            const float4 w1 = *reinterpret_cast<const float4*>(w + c * 8 + 4);
-            x[0] *= rs * w0.x;
-            x[1] *= rs * w0.y;
-            x[2] *= rs * w0.z;
-            x[3] *= rs * w0.w;
-            x[4] *= rs * w1.x;
-            x[5] *= rs * w1.y;
-            x[6] *= rs * w1.z;
-            x[7] *= rs * w1.w;
-          }
-        }
-        if constexpr (IL) {
-          if (rot) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float p = x[2 * i], q = x[2 * i + 1];
-              x[2 * i] = p * cs[i] - q * sn[i];
-              x[2 * i + 1] = q * cs[i] + p * sn[i];
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float o = __shfl_sync(0xffffffffu, x[i], partner);
-            if (rot) x[i] = x[i] * cs[i] + o * sn[i];
-          }
-        }
+      for (int e = 0; e < 4; ++e) {
+        const uint64_t p = xa[e];
+        xa[e] = fma2(ac[e], p, mul2(bs[e], xb[e]));
+        xb[e] = fma2(bc[e], xb[e], mul2(as[e], p));
       }
-      if (!mine) continue;
-      const int64_t col = static_cast<int64_t>(h) * D + c * 8;
-      if (kind == 0) {
-        *reinterpret_cast<uint4*>(a.q_out + tok * a.num_q_heads * D + col) = pack8(x);
-        continue;
+    } else if (NORM) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        xa[e] = mul2(xa[e], ac[e]);
+        xb[e] = mul2(xb[e], bc[e]);
       }
-      if (kind == 1 && a.k_out)
-        *reinterpret_cast<uint4*>(a.k_out + tok * a.num_kv_heads * D + col) = pack8(x);
-      if (!cached) continue;
-      const int64_t at = slot * a.num_kv_heads * D + col;
-      void* pool = kind == 1 ? a.k_cache : a.v_cache;
-      if constexpr (F8)
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + at) =
-            quant8(x, (kind == 1 ? a.k_scales : a.v_scales)[h]);
-      else
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pool) + at) =
-            kind == 1 ? pack8(x) : raw[r];
+    }
+    if (!mine(r)) continue;
+    if (!F8 || y0) {
+      uint4 p = pack(xa), q = pack(xb);
+      if (a.interleaved && turn) interleave(p, q);
+      if (y0) {
+        *reinterpret_cast<uint4*>(y0 + r * HW * D + c0) = p;
+        *reinterpret_cast<uint4*>(y0 + r * HW * D + c1) = q;
+      }
+      if (y1) {
+        *reinterpret_cast<uint4*>(y1 + r * HW * D + c0) = p;
+        *reinterpret_cast<uint4*>(y1 + r * HW * D + c1) = q;
+      }
+    }
+    if (F8 && z) {
+      const float scale = (kind == 1 ? a.k_scales : a.v_scales)[h0 + r * HW + sub];
+      const float inv = reciprocal(scale);
+      uint2 p = quant(xa, scale, inv), q = quant(xb, scale, inv);
+      if (a.interleaved && turn) interleave(p, q);
+      *reinterpret_cast<uint2*>(z + r * HW * D + c0) = p;
+      *reinterpret_cast<uint2*>(z + r * HW * D + c1) = q;
     }
   }
 }
 
-template <int LPR, bool IL, bool F8>
-cudaError_t launch(RopeArgs a, int num_sms, cudaStream_t stream) {
-  constexpr int HW = 32 / LPR;
-  const int gk = (a.num_kv_heads + HW - 1) / HW;
-  const int groups = (a.num_q_heads + HW - 1) / HW + gk + (a.k_cache ? gk : 0);
-  // few tokens: a token's rows go to several warps, kRows row groups each at
-  // least, until the SMs hold about 16 warps each
-  const int64_t want = static_cast<int64_t>(num_sms) * 16 / a.num_tokens;
-  const int most = (groups + kRows - 1) / kRows;
-  a.slices = want < 1 ? 1 : (want > most ? most : static_cast<int>(want));
-  const int64_t warps = static_cast<int64_t>(a.num_tokens) * a.slices;
+template <int LPR, int R, bool F8, bool NORM, bool EVEN>
+cudaError_t launch(const RopeArgs& a, cudaStream_t stream) {
+  constexpr int per = 32 / LPR * R;
+  const int uk = (a.num_kv_heads + per - 1) / per;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((warps + 3) / 4));
+  cfg.gridDim = dim3(static_cast<unsigned>((static_cast<int64_t>(a.num_tokens) + 3) / 4),
+                     (a.num_q_heads + per - 1) / per + uk + (a.k_cache ? uk : 0));
   cfg.blockDim = dim3(128);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -219,24 +323,40 @@ cudaError_t launch(RopeArgs a, int num_sms, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_rope_kernel<LPR, IL, F8>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, norm_rope_kernel<LPR, R, F8, NORM, EVEN>, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <int LPR, bool F8, bool NORM>
+cudaError_t pick_steps(const RopeArgs& a, int num_sms, cudaStream_t st) {
+  constexpr int HW = 32 / LPR;
+  const bool even = a.head_dim == 16 * LPR && a.num_q_heads % HW == 0 && a.num_kv_heads % HW == 0;
+  if (!even) return launch<LPR, 2, F8, NORM, false>(a, st);
+  // four steps per warp share the angles' cost; two, where four would leave
+  // the SMs' schedulers with fewer than two warps each
+  constexpr int per = HW * 4;
+  const int64_t warps = static_cast<int64_t>(a.num_tokens) *
+                        ((a.num_q_heads + per - 1) / per + 2 * ((a.num_kv_heads + per - 1) / per));
+  return warps >= num_sms * 8 ? launch<LPR, 4, F8, NORM, true>(a, st)
+                              : launch<LPR, 2, F8, NORM, true>(a, st);
+}
+
 template <int LPR>
-cudaError_t pick(const RopeArgs& a, bool interleaved, bool f8, int num_sms, cudaStream_t st) {
-  if (interleaved)
-    return f8 ? launch<LPR, true, true>(a, num_sms, st) : launch<LPR, true, false>(a, num_sms, st);
-  return f8 ? launch<LPR, false, true>(a, num_sms, st) : launch<LPR, false, false>(a, num_sms, st);
+cudaError_t pick(const RopeArgs& a, bool f8, int num_sms, cudaStream_t st) {
+  const bool norm = a.q_weight || a.k_weight;
+  if (norm)
+    return f8 ? pick_steps<LPR, true, true>(a, num_sms, st)
+              : pick_steps<LPR, false, true>(a, num_sms, st);
+  return f8 ? pick_steps<LPR, true, false>(a, num_sms, st)
+            : pick_steps<LPR, false, false>(a, num_sms, st);
 }
 
 }  // namespace
 
-cudaError_t launch_norm_rope(const RopeArgs& a, bool interleaved, bool kv_fp8, int num_sms,
-                             cudaStream_t stream) {
-  if (a.head_dim <= 64) return pick<8>(a, interleaved, kv_fp8, num_sms, stream);
-  if (a.head_dim <= 128) return pick<16>(a, interleaved, kv_fp8, num_sms, stream);
-  return pick<32>(a, interleaved, kv_fp8, num_sms, stream);
+cudaError_t launch_norm_rope(const RopeArgs& a, bool kv_fp8, int num_sms, cudaStream_t stream) {
+  if (a.head_dim <= 64) return pick<4>(a, kv_fp8, num_sms, stream);
+  if (a.head_dim <= 128) return pick<8>(a, kv_fp8, num_sms, stream);
+  return pick<16>(a, kv_fp8, num_sms, stream);
 }
 
 }  // namespace pa
