@@ -1459,6 +1459,9 @@ static int prefill_window_impl(void* out, const void* q, const void* k_cache, co
   a.stall_loads = stall_loads;
   a.wait_ns = wait_ns;  // 0: the default limit
   const int tokens_per_tile = 128 / a.group;
+  if ((static_cast<int64_t>(total_q_tokens) + 2 * tokens_per_tile - 1) / (2 * tokens_per_tile) *
+          num_kv_heads > INT32_MAX)
+    return PA_ERR_UNSUPPORTED;
   CUtensorMap tm_q, tm_k, tm_v;
   if (encode_q_map(&tm_q, q, total_q_tokens, num_q_heads, head_dim, a.group, tokens_per_tile) ||
       encode_pool_map(&tm_k, k_cache, num_blocks, num_kv_heads, head_dim, kPoolKeyTile) ||

@@ -23,11 +23,14 @@
 //  * Work per query tile is short (window / 128 key tiles), so setting up and
 //    draining a pipeline per tile would cost as much as the tile.  The launch
 //    is persistent: one CTA pair per two SMs walks (chunk, query tile, kv head)
-//    items; barriers, rings and phases run on across items, Q has two buffers,
-//    and the loaders and the score products of the next item run while the
-//    softmax finishes the last one.  A pair's items are every pairs-th of the
-//    list, found with a warp-wide scan over the chunks' lengths, so ragged
-//    chunks leave no empty items.
+//    items; barriers, rings and phases run on across items, and Q has two
+//    buffers.  A pair's items are every pairs-th of the list; the K loader finds
+//    them with a warp-wide scan over the chunks' lengths (so ragged chunks leave
+//    no empty items) and publishes them, one ahead of its loads, in a ring that
+//    the other roles read.  Block ids of the next item are fetched while the
+//    last one's tiles load, and the softmax writes P of an item's first tile
+//    before it turns to the output of the item before, whose last product is
+//    then done.
 //
 // What bounds it: the tensor pipe and, at 128 x 128 tiles, the softmax that
 // feeds it (one exponential per score).
@@ -55,23 +58,27 @@ struct WPlan {
   static constexpr int kRedOff = kIdsOff + 2 * kIdRing * 8 * 4;
   static constexpr int kRedOff2 = kRedOff + 2 * 2 * 128 * 4;
   static constexpr int kBarOff = kRedOff2 + 2 * 128 * 4;
-  static constexpr int kSmemBytes = kBarOff + 320;
+  static constexpr int kItemsOff = kBarOff + 384;  // [kItemRing]
+  static constexpr int kSmemBytes = kItemsOff + 8 * 64;
 };
 static_assert(WPlan::kSmemBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
 
 // One work item of a pair: query tiles 2 mg, 2 mg + 1 of a chunk, one kv head.
 struct Item {
+  int nkt;          // key tiles; 0 ends the list
   int c, kvh;
-  int q0, qlen, p0, n;  // the chunk's rows and positions
-  int tc0;              // first query token of the pair
-  int kmax;             // keys [0, kmax) are visible to some row, window and sinks aside
-  int lo;               // first key of the first row's window
-  int nsb, b_first;     // the sinks' blocks; first block behind them
-  int nvb;              // virtual blocks
-  int nkt;              // key tiles
+  int q0, qlen, p0; // the chunk's rows and first position
+  int tc0;          // first query token of the pair
+  int kmax;         // keys [0, kmax) are visible to some row, window and sinks aside
+  int lo;           // first key of the first row's window
+  int nsb, b_first; // the sinks' blocks; first block behind them
+  int nvb;          // virtual blocks
+  int edge[3];      // tiles with rows that no row of the pair sees, or -1
 };
+constexpr int kItemRing = 8;
+static_assert(sizeof(Item) <= 64, "ring slot");
 
-// Walks a pair's items (every `stride`-th of the list); each warp keeps its own.
+// Walks a pair's items: every `stride`-th of the list.
 struct Cursor {
   int64_t want;    // list index of the next item
   int64_t before;  // items of the chunks before `chunk`
@@ -81,63 +88,6 @@ struct Cursor {
 __device__ __forceinline__ bool chunk_ok(const WindowPrefillArgs& a, int q0, int q1, int p0, int n) {
   return q0 >= 0 && q1 <= a.total_q && q1 >= q0 && p0 >= 0 && n >= 0 && q1 - q0 <= n &&
          p0 <= n - (q1 - q0) && n <= a.max_blocks * kBlockSize;
-}
-
-// The next item; false at the end of the list.  Called by whole warps.  The
-// caller that passes flag = true reports chunks with inconsistent metadata.
-__device__ __forceinline__ bool next_item(const WindowPrefillArgs& a, Cursor& cur, int stride,
-                                          int lane, bool flag, Item& it) {
-  const int rows = 2 * (kTileKeys / a.group);  // query tokens per item
-  for (;;) {
-    if (cur.chunk >= a.num_chunks) return false;
-    // items of 32 chunks at a time, and their inclusive sums
-    const int c = cur.chunk + lane;
-    int64_t items = 0;
-    if (c < a.num_chunks) {
-      const int q0 = a.cu_q_lens[c], q1 = a.cu_q_lens[c + 1];
-      if (chunk_ok(a, q0, q1, a.q_start_pos[c], a.seq_lens[c]))
-        items = static_cast<int64_t>((q1 - q0 + rows - 1) / rows) * a.num_kv_heads;
-      else if (flag)
-        atomicOr(a.err, PA_DEVERR_CHUNK);
-    }
-    int64_t sum = items;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, sum, off);
-      if (lane >= off) sum += o;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, cur.before + sum > cur.want);
-    if (past == 0) {
-      cur.before += __shfl_sync(0xffffffffu, sum, 31);
-      cur.chunk += 32;
-      continue;
-    }
-    const int w = __ffs(past) - 1;
-    const int64_t start = cur.before + __shfl_sync(0xffffffffu, sum - items, w);
-    const int64_t at = cur.want - start;
-    const int64_t count = __shfl_sync(0xffffffffu, items, w);
-    cur.before = start;
-    cur.chunk += w;
-    cur.want += stride;
-    it.c = cur.chunk;
-    it.kvh = static_cast<int>(at % a.num_kv_heads);
-    // last query tiles first: where the window has not closed they are longest
-    const int mg = static_cast<int>(count / a.num_kv_heads - 1 - at / a.num_kv_heads);
-    it.q0 = a.cu_q_lens[it.c];
-    it.qlen = a.cu_q_lens[it.c + 1] - it.q0;
-    it.p0 = a.q_start_pos[it.c];
-    it.n = a.seq_lens[it.c];
-    it.tc0 = mg * rows;
-    it.kmax = it.p0 + min(it.qlen, it.tc0 + rows);
-    it.lo = max(0, it.p0 + it.tc0 - (a.window - 1));
-    const int ns = min(a.sinks, it.kmax);
-    it.nsb = (ns + kBlockSize - 1) / kBlockSize;
-    it.b_first = max(it.lo / kBlockSize, it.nsb);
-    const int nb = (it.kmax + kBlockSize - 1) / kBlockSize;
-    it.nvb = it.nsb + max(0, nb - it.b_first);
-    it.nkt = (it.nvb + 7) / 8;
-    return true;
-  }
 }
 
 // Rows of virtual blocks that no row of the pair sees: at most three ranges.
@@ -163,11 +113,69 @@ struct Hidden {
     // behind the last key
     if (it.kmax % kBlockSize) set(2, it.nvb - 1, it.kmax % kBlockSize, kBlockSize);
   }
-  __device__ __forceinline__ bool in_tile(int j) const {
-    return (vb[0] >= 0 && vb[0] / 8 == j) || (vb[1] >= 0 && vb[1] / 8 == j) ||
-           (vb[2] >= 0 && vb[2] / 8 == j);
-  }
 };
+
+// The next item (nkt 0 at the end of the list).  Called by a whole warp.  The
+// caller that passes flag = true reports chunks with inconsistent metadata.
+__device__ __forceinline__ Item next_item(const WindowPrefillArgs& a, Cursor& cur, int stride,
+                                          int lane, bool flag) {
+  Item it;
+  it.nkt = 0;
+  const int rows = 2 * (kTileKeys / a.group);  // query tokens per item
+  while (cur.chunk < a.num_chunks) {
+    // items of 32 chunks at a time, and their inclusive sums
+    const int c = cur.chunk + lane;
+    int items = 0, q0 = 0, q1 = 0, p0 = 0;
+    if (c < a.num_chunks) {
+      q0 = a.cu_q_lens[c];
+      q1 = a.cu_q_lens[c + 1];
+      p0 = a.q_start_pos[c];
+      if (chunk_ok(a, q0, q1, p0, a.seq_lens[c]))
+        items = (q1 - q0 + rows - 1) / rows * a.num_kv_heads;
+      else if (flag)
+        atomicOr(a.err, PA_DEVERR_CHUNK);
+    }
+    int64_t sum = items;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, sum, off);
+      if (lane >= off) sum += o;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, cur.before + sum > cur.want);
+    if (past == 0) {
+      cur.before += __shfl_sync(0xffffffffu, sum, 31);
+      cur.chunk += 32;
+      continue;
+    }
+    const int w = __ffs(past) - 1;
+    cur.before += __shfl_sync(0xffffffffu, sum - items, w);
+    const int at = static_cast<int>(cur.want - cur.before);
+    const int count = __shfl_sync(0xffffffffu, items, w);
+    cur.chunk += w;
+    cur.want += stride;
+    it.c = cur.chunk;
+    it.q0 = __shfl_sync(0xffffffffu, q0, w);
+    it.qlen = __shfl_sync(0xffffffffu, q1 - q0, w);
+    it.p0 = __shfl_sync(0xffffffffu, p0, w);
+    const int tile = at / a.num_kv_heads;
+    it.kvh = at - tile * a.num_kv_heads;
+    // last query tiles first: where the window has not closed they are longest
+    it.tc0 = (count / a.num_kv_heads - 1 - tile) * rows;
+    it.kmax = it.p0 + min(it.qlen, it.tc0 + rows);
+    it.lo = max(0, it.p0 + it.tc0 - (a.window - 1));
+    const int ns = min(a.sinks, it.kmax);
+    it.nsb = (ns + kBlockSize - 1) / kBlockSize;
+    it.b_first = max(it.lo / kBlockSize, it.nsb);
+    const int nb = (it.kmax + kBlockSize - 1) / kBlockSize;
+    it.nvb = it.nsb + max(0, nb - it.b_first);
+    it.nkt = (it.nvb + 7) / 8;
+    const Hidden hid(it, a.sinks);
+#pragma unroll
+    for (int e = 0; e < 3; ++e) it.edge[e] = hid.vb[e] < 0 ? -1 : hid.vb[e] / 8;
+    break;
+  }
+  return it;
+}
 
 // Bits [0, k) of 64.
 __device__ __forceinline__ uint64_t low_bits(int k) {
@@ -194,22 +202,24 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_s_full = bar_v_empty + 8 * kNV;   // [kNS]: scores of a tile
   const uint32_t bar_p_full = bar_s_full + 8 * kNS;    // [kNS]: softmax done
   const uint32_t bar_o_done = bar_p_full + 8 * kNS;    // [kNS]: PV done
-  static_assert(32 + 8 * (2 * kNK + 3 * kNV + 3 * kNS) <= 288, "barrier area");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P::kBarOff + 288);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 292);
+  const uint32_t bar_item = bar_o_done + 8 * kNS;      // [kItemRing]: item published
+  static_assert(32 + 8 * (2 * kNK + 3 * kNV + 3 * kNS + kItemRing) <= 336, "barrier area");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P::kBarOff + 336);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 340);
+  volatile int* go_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 352);  // [2][4]
+  auto ring_item = [&](int k) {
+    return reinterpret_cast<Item*>(smem + P::kItemsOff + 64 * (k % kItemRing));
+  };
   int* ids_smem = reinterpret_cast<int*>(smem + P::kIdsOff) +
                   ((threadIdx.x >> 5) == kLoadVWarp ? kIdRing * 8 : 0);
   float* red_max = reinterpret_cast<float*>(smem + P::kRedOff);
   float* red_sum = reinterpret_cast<float*>(smem + P::kRedOff2);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int Hkv = a.num_kv_heads, G = a.group;
+  const int G = a.group;
   const int tpt = kTileKeys / G;
   const int rank = static_cast<int>(blockIdx.x) & 1;
   const bool issuer = rank == 0;
-  const int stride = static_cast<int>(gridDim.x) / 2;
-  Cursor cur{static_cast<int64_t>(blockIdx.x) / 2, 0, 0};
-  Item it;
 
   if (tid == 0) {
     for (int k = 0; k < 2; ++k) {
@@ -230,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar_p_full + 8 * k, kSoftmaxWarps * 2);
       mbar_init(bar_o_done + 8 * k, 1);
     }
+    for (int k = 0; k < kItemRing; ++k) mbar_init(bar_item + 8 * k, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -260,29 +271,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    // ids of the item's virtual blocks [8 t_first, + 8 kIdBatch); a slot of
-    // the ring is rewritten once its tile's loads have been issued (by this
-    // warp).  Ids past the list read as zeros (-1: a box outside the pool).
-    auto fetch_ids = [&](int t_first) {
+    // ids of virtual blocks [8 t_first, + 8 kIdBatch) of an item whose tile 0
+    // is this warp's tile `base`, into the ring (tile T at slot T % kIdRing);
+    // a slot is rewritten only when its tile's loads have been issued.  Ids
+    // past the list read as zeros (-1: a box outside the pool).
+    auto fetch_ids = [&](const Item& x, int t_first, int base) {
       int v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int vb = t_first * 8 + lane + 32 * i;
-        const int b = vb < it.nsb ? vb : vb - it.nsb + it.b_first;
-        v[i] = vb < it.nvb ? a.block_tables[static_cast<int64_t>(it.c) * a.max_blocks + b] : -1;
+        const int b = vb < x.nsb ? vb : vb - x.nsb + x.b_first;
+        v[i] = vb < x.nvb ? a.block_tables[static_cast<int64_t>(x.c) * a.max_blocks + b] : -1;
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int vb = t_first * 8 + lane + 32 * i;
-        if (vb < it.nvb && (v[i] < 0 || v[i] >= a.num_blocks)) {
+        if (vb < x.nvb && (v[i] < 0 || v[i] >= a.num_blocks)) {
           atomicOr(a.err, PA_DEVERR_BLOCK_ID);
           v[i] = -1;
         }
-        ids_smem[vb % (kIdRing * 8)] = v[i];
+        ids_smem[(static_cast<unsigned>(base) * 8 + vb) % (kIdRing * 8)] = v[i];
       }
       __syncwarp();
     };
-    int total = 0;  // tiles loaded by this warp, over all items
+    unsigned total = 0;  // tiles loaded by this warp, over all items
     // after a timeout: let the copies in flight land before the CTA may exit
     auto settle = [&]() {
       if (!*abort_flag) return;
@@ -294,16 +306,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
       }
-      int qi = 0;  // items
+      Cursor cur{static_cast<int64_t>(blockIdx.x) / 2, 0, 0};
+      int published = 0;
+      auto publish = [&]() {
+        const Item x = next_item(a, cur, static_cast<int>(gridDim.x) / 2, lane, blockIdx.x == 0);
+        if (lane == 0) {
+          *ring_item(published) = x;
+          mbar_arrive(bar_item + 8 * (published % kItemRing));
+        }
+        ++published;
+        return x;
+      };
+      Item it = publish();
+      if (it.nkt) fetch_ids(it, 0, 0);
       bool stop = a.stall_loads != 0;  // a stalled test launch issues no load
-      while (!stop && next_item(a, cur, stride, lane, blockIdx.x == 0, it)) {
-        fetch_ids(0);
+      for (int qi = 0; it.nkt && !stop; ++qi) {
+        const int qb = qi & 1;
         int jf = kIdBatch, jk = 0;
-        bool q_loaded = false;
+        bool q_loaded = false, next_known = false, next_ids = false;
+        Item next = it;
         while (jk < it.nkt && !stop) {
           bool progressed = false;
           if (!q_loaded) {
-            const int qb = qi & 1;
             bool ok = qi < 2;
             if (!ok && lane == 0) ok = mbar_test_wait(bar_q_empty + 8 * qb, ((qi >> 1) - 1) & 1);
             if (__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
@@ -325,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (jf < it.nkt && jk + kIdBatch / 2 >= jf) {
-            fetch_ids(jf);
+            fetch_ids(it, jf, total - jk);
             jf += kIdBatch;
             progressed = true;
           }
@@ -338,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0 && issuer) mbar_arrive_expect_tx(bar, 2 * kHalf);
             __syncwarp();
             if (lane < 4) {  // CTA r takes keys 64 r .. 64 r + 63: blocks 4 r .. 4 r + 3
-              const int id = ids_smem[(jk % kIdRing) * 8 + 4 * rank + lane];
+              const int id = ids_smem[(total % kIdRing) * 8 + 4 * rank + lane];
               const uint32_t dst = sbase + P::kKOff + slot * P::kKSlot + lane * 2 * kBlockBytes;
               if (issuer)
                 tma_load_4d(dst, &tm_k, 0, 0, 2 * it.kvh, 2 * id, bar, pol);
@@ -349,10 +373,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++jk;
             ++total;
             progressed = true;
+          } else if (q_loaded && !next_known) {
+            next = publish();
+            next_known = progressed = true;
+          } else if (next_known && !next_ids && next.nkt && jf >= it.nkt &&
+                     it.nkt - jk <= kIdBatch) {
+            fetch_ids(next, 0, total + it.nkt - jk);
+            next_ids = progressed = true;
           }
           stop = timed_out(progressed) || warp_flag(abort_flag);
         }
-        ++qi;
+        if (stop) break;
+        if (!next_known) next = publish();
+        if (!next_ids && next.nkt) fetch_ids(next, 0, total);
+        it = next;
       }
       // every load's slot has been released, and so has landed, before exit
       if (lane == 0)
@@ -365,18 +399,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       int edge_slot = -1;       // slot of the edge tile whose rows are still to be zeroed
       int edge_tile = 0;
       bool stop = a.stall_loads != 0;
-      while (!stop && next_item(a, cur, stride, lane, false, it)) {
-        fetch_ids(0);
+      bool have_ids = false;
+      for (int k = 0; !stop; ++k) {
+        if (!wait_or_abort_warp<2>(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1, abort_flag,
+                                   a))
+          break;
+        const Item it = *ring_item(k);
+        if (it.nkt == 0) break;
+        if (!have_ids) fetch_ids(it, 0, total);
+        have_ids = false;
         const Hidden hid(it, a.sinks);
+        const uint32_t next_bar = bar_item + 8 * ((k + 1) % kItemRing);
+        const uint32_t next_phase = ((k + 1) / kItemRing) & 1;
         int jf = kIdBatch, jv = 0;
         while ((jv < it.nkt || edge_slot >= 0) && !stop) {
           bool progressed = false;
           if (jf < it.nkt && jv + kIdBatch / 2 >= jf) {
-            fetch_ids(jf);
+            fetch_ids(it, jf, total - jv);
             jf += kIdBatch;
             progressed = true;
           }
-          const bool edge = hid.in_tile(jv);
+          const bool edge = jv == it.edge[0] || jv == it.edge[1] || jv == it.edge[2];
           if (jv < it.nkt && jv < jf && !(edge && edge_slot >= 0)) {
             const int slot = total % kNV;
             bool free_slot = total < kNV;
@@ -395,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               __syncwarp();
               if (lane < 8) {  // CTA r takes columns 64 r .. 64 r + 63 of every key
-                const int id = ids_smem[(jv % kIdRing) * 8 + lane];
+                const int id = ids_smem[(total % kIdRing) * 8 + lane];
                 const uint32_t dst = sbase + P::kVOff + slot * P::kVSlot + lane * kBlockBytes;
                 const int x = it.kvh * 128 + rank * 64, y = id * kBlockSize;
                 if (remote)
@@ -421,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t vt = sbase + P::kVOff + edge_slot * P::kVSlot;
 #pragma unroll
               for (int h = 0; h < 3; ++h) {
-                if (hid.vb[h] < 0 || hid.vb[h] / 8 != edge_tile) continue;
+                if (it.edge[h] != edge_tile) continue;
                 const uint32_t blk = vt + (hid.vb[h] % 8) * kBlockBytes;
                 for (int e = lane + 8 * hid.r0[h]; e < 8 * hid.r1[h]; e += 32)
                   st_shared_zero16(blk + e * 16);
@@ -439,6 +482,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               progressed = true;
             }
           }
+          if (!progressed && !have_ids && jf >= it.nkt && it.nkt - jv <= kIdBatch) {
+            bool there = false;
+            if (lane == 0) there = mbar_test_wait(next_bar, next_phase);
+            if (__shfl_sync(0xffffffffu, there ? 1 : 0, 0)) {
+              const Item next = *ring_item(k + 1);
+              if (next.nkt) fetch_ids(next, 0, total + it.nkt - jv);
+              have_ids = progressed = true;
+            }
+          }
           stop = timed_out(progressed) || warp_flag(abort_flag);
         }
       }
@@ -450,32 +502,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   } else if (warp == kMmaWarp || warp == kPvWarp) {
     // ------------------------------------------------------------ tensor-core issue
-    auto commit = [&](uint32_t bar) {
-      tc_commit<2>(mapa_shared(bar, 1));
-      tc_commit<2>(bar);
-    };
-    IdleClock clk(a.wait_ns);
-    bool ok = true;
-    // give up: flag it once, so that every role leaves its loops
-    auto stuck = [&]() {
-      if (*abort_flag) return true;
-      if (!clk.expired()) return false;
-      *abort_flag = 1;
-      atomicOr(a.err, PA_DEVERR_TIMEOUT);
-      return true;
-    };
-    if (warp == kMmaWarp) {
-      const uint32_t idesc_s = instr_desc(0, 256);
-      const uint64_t dk0 = smem_desc(sbase + P::kKOff, 16, kKGroupStride);
-      int s_buf = 0, s_round = 0, s_kslot = 0, s_kphase = 0, qi = 0;
-      while (issuer && next_item(a, cur, stride, lane, false, it)) {
-        if (lane == 0) {
-          const uint64_t dq = smem_desc(sbase + P::kQOff + 2 * (qi & 1) * kHalf, 16, 1024);
-          bool q_there = false;
+    // Two threads of the even CTA, as in pa_prefill_body.cuh.
+    if (lane == 0 && issuer) {
+      auto commit = [&](uint32_t bar) {
+        tc_commit<2>(mapa_shared(bar, 1));
+        tc_commit<2>(bar);
+      };
+      IdleClock clk(a.wait_ns);
+      auto give_up = [&]() {
+        if (!*abort_flag) {
+          *abort_flag = 1;
+          atomicOr(a.err, PA_DEVERR_TIMEOUT);
+        }
+      };
+      bool ok = true;
+      if (warp == kMmaWarp) {
+        const uint32_t idesc_s = instr_desc(0, 256);
+        const uint64_t dk0 = smem_desc(sbase + P::kKOff, 16, kKGroupStride);
+        const uint64_t dq0 = smem_desc(sbase + P::kQOff, 16, 1024);
+        int s_buf = 0, s_round = 0, s_kslot = 0, s_kphase = 0;
+        for (int k = 0; ok; ++k) {
+          ok = wait_or_abort<2>(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1, abort_flag, a);
+          const int nkt = ok ? ring_item(k)->nkt : 0;
+          if (nkt == 0) break;
+          const uint64_t dq = dq0 + static_cast<uint64_t>(((k & 1) * 2 * kHalf) >> 4);
+          ok = wait_or_abort<2>(bar_q + 8 * (k & 1), (k >> 1) & 1, abort_flag, a);
           int js = 0;
-          while (ok && js < it.nkt) {
-            if (!q_there) q_there = mbar_test_wait(bar_q + 8 * (qi & 1), (qi >> 1) & 1);
-            if (q_there && mbar_test_wait(bar_k_full + 8 * s_kslot, s_kphase) &&
+          while (ok && js < nkt) {
+            if (mbar_test_wait(bar_k_full + 8 * s_kslot, s_kphase) &&
                 (s_round == 0 || mbar_test_wait(bar_o_done + 8 * s_buf, (s_round + 1) & 1))) {
               tc_fence_after();
               const uint64_t dk = dk0 + static_cast<uint64_t>((s_kslot * P::kKSlot) >> 4);
@@ -488,7 +542,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               commit(bar_s_full + 8 * s_buf);
               commit(bar_k_empty + 8 * s_kslot);
               ++js;
-              if (js == it.nkt) commit(bar_q_empty + 8 * (qi & 1));
               if (++s_buf == kNS) {
                 s_buf = 0;
                 ++s_round;
@@ -498,27 +551,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s_kphase ^= 1;
               }
               clk.progress();
-            } else if (stuck()) {
+            } else if (*abort_flag || clk.expired()) {
+              give_up();
               ok = false;
             }
           }
+          if (ok) commit(bar_q_empty + 8 * (k & 1));
         }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-        ++qi;
-      }
-    } else {
-      const uint32_t idesc_o = instr_desc(1, 256);
-      const uint64_t dv0 = smem_desc(sbase + P::kVOff, kHalf, 1024);
-      int p_buf = 0, p_phase = 0, p_vslot = 0, p_vphase = 0;
-      while (issuer && next_item(a, cur, stride, lane, false, it)) {
-        if (lane == 0) {
-          const Hidden hid(it, a.sinks);
+      } else {
+        const uint32_t idesc_o = instr_desc(1, 256);
+        const uint64_t dv0 = smem_desc(sbase + P::kVOff, kHalf, 1024);
+        int p_buf = 0, p_phase = 0, p_vslot = 0, p_vphase = 0;
+        for (int k = 0; ok; ++k) {
+          ok = wait_or_abort<2>(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1, abort_flag, a);
+          const int nkt = ok ? ring_item(k)->nkt : 0;
+          if (nkt == 0) break;
+          const int e0 = ring_item(k)->edge[0], e1 = ring_item(k)->edge[1],
+                    e2 = ring_item(k)->edge[2];
           int jp = 0;
-          while (ok && jp < it.nkt) {
+          while (ok && jp < nkt) {
             if (mbar_test_wait(bar_p_full + 8 * p_buf, p_phase) &&
                 mbar_test_wait(bar_v_ready + 8 * p_vslot, p_vphase)) {
-              if (hid.in_tile(jp)) fence_acq_rel_cluster();  // the peer's zeroed rows
+              if (jp == e0 || jp == e1 || jp == e2) fence_acq_rel_cluster();  // the peer's zeroed rows
               tc_fence_after();
               const uint64_t dv = dv0 + static_cast<uint64_t>((p_vslot * P::kVSlot) >> 4);
               const uint32_t ta = tmem + p_buf * 128;
@@ -539,13 +593,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p_vphase ^= 1;
               }
               clk.progress();
-            } else if (stuck()) {
+            } else if (*abort_flag || clk.expired()) {
+              give_up();
               ok = false;
             }
           }
         }
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
       }
     }
     __syncwarp();
@@ -557,46 +610,100 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float sl = a.scale_log2;
     const uint32_t ocol = tmem + lane_off + kTmemO + hc * 64;
     uint32_t v[64];
-    int jt = 0;                    // tiles, over all items
-    int b3 = 0, s_phase = 0;       // score buffer of tile jt and its parity
-    while (next_item(a, cur, stride, lane, false, it)) {
-      const int t0 = it.tc0 + rank * tpt;
-      const int tv = min(it.qlen - t0, tpt);  // valid tokens here (<= 0: none)
+    int jt = 0;                // tiles, over all items
+    int b3 = 0, s_phase = 0;   // score buffer of tile jt and its parity
+
+    // The output of an item, written once its last PV is done: O / l -> bf16,
+    // and lse.  The next item's first PV, which overwrites O, waits for this
+    // warp's arrival on p_full behind these loads of O.
+    bool pending = false;
+    int64_t out_row = 0;       // of the pending item's row; < 0: not stored
+    float out_m = 0.f, out_l = 0.f;
+    uint32_t out_bar = 0, out_phase = 0;
+    auto write_out = [&]() {
+      wait_or_abort_warp<2>(out_bar, out_phase, abort_flag, a);
+      tc_fence_after();
+      red_sum[hc * 128 + r] = out_l;
+      named_barrier(1 + qd, 64);
+      const float l_tot = out_l + red_sum[(hc ^ 1) * 128 + r];
+      const bool store = out_row >= 0 && !*abort_flag;
+      const float inv = l_tot == 0.f ? 0.f : 1.f / l_tot;  // a NaN sum stays visible
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        uint32_t (&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32 * cc]);
+        tmem_ld32(ocol + 32 * cc, w);
+        if (store) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            pk[i / 2] = pack_bf16x2(__uint_as_float(w[i]) * inv, __uint_as_float(w[i + 1]) * inv);
+          uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * 128 + hc * 64 + cc * 32);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            dst[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+        }
+      }
+      if (store && hc == 0 && a.out_lse)
+        a.out_lse[out_row] = l_tot == 0.f ? -INFINITY : (out_m + __log2f(l_tot)) * kLn2;
+    };
+
+    for (int k = 0;; ++k) {
+      // Both warps of a quadrant act on what the first one found: they meet at
+      // a named barrier for every tile, also after a timeout (when the waits
+      // are skipped and what they compute is not stored).
+      if (hc == 0) {
+        const bool got =
+            wait_or_abort_warp<2>(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1, abort_flag, a);
+        if (lane == 0) go_flag[(k & 1) * 4 + qd] = got ? ring_item(k)->nkt : 0;
+      }
+      named_barrier(1 + qd, 64);
+      const int nkt = go_flag[(k & 1) * 4 + qd];
+      if (nkt == 0) break;
+      const Item& it = *ring_item(k);
+      const int kmax = it.kmax, p0 = it.p0, t0 = it.tc0 + rank * tpt;
       const int shift = (it.b_first - it.nsb) * kBlockSize;
-      const int pos = it.p0 + t0 + r / G;
+      const int tok = r / G;
+      const int pos = p0 + t0 + tok;
+      const int64_t row = tok < min(it.qlen - t0, tpt)
+                              ? static_cast<int64_t>(it.q0 + t0 + tok) * a.num_q_heads +
+                                    it.kvh * G + r % G
+                              : -1;
       // last and first visible virtual key of the row's window
-      const int hi = min(pos, it.kmax - 1) - shift;
+      const int hi = min(pos, kmax - 1) - shift;
       const int lo = max(0, pos - (a.window - 1)) - shift;
       float m_run = kFloor, l_run = 0.f;
-      for (int j = 0; j < it.nkt; ++j, ++jt) {
+      for (int j = 0; j < nkt; ++j, ++jt) {
         const int b = jt & 1;
         wait_or_abort_warp<2>(bar_s_full + 8 * b3, s_phase, abort_flag, a);
         tc_fence_after();
         const int kb = j * kTileKeys + hc * 64;
         const bool whole = hi >= kb + 63 && (lo <= kb || a.sinks >= kb + 64);
         const bool full = __all_sync(0xffffffffu, whole);
-        uint64_t seen = ~0ull;
-        if (!full)
-          seen = low_bits(hi - kb + 1) & (low_bits(a.sinks > kb ? min(a.sinks - kb, 64) : 0) |
-                                          ~low_bits(lo - kb));
-        const uint32_t seen0 = static_cast<uint32_t>(seen), seen1 = static_cast<uint32_t>(seen >> 32);
-        const bool any = full || __any_sync(0xffffffffu, seen != 0);
+        bool any = true;
         float mloc = -INFINITY;
         if (full) {
           tmem_ld64_max(tmem + lane_off + b3 * 128 + hc * 64, v, mloc);
-        } else if (any) {
-          tmem_ld64(tmem + lane_off + b3 * 128 + hc * 64, v);
-          float mp[8];
+        } else {
+          const uint64_t seen =
+              low_bits(hi - kb + 1) &
+              (low_bits(a.sinks > kb ? min(a.sinks - kb, 64) : 0) | ~low_bits(lo - kb));
+          const uint32_t seen0 = static_cast<uint32_t>(seen);
+          const uint32_t seen1 = static_cast<uint32_t>(seen >> 32);
+          any = __any_sync(0xffffffffu, seen != 0);
+          if (any) {
+            tmem_ld64(tmem + lane_off + b3 * 128 + hc * 64, v);
+            float mp[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mp[k] = -INFINITY;
+            for (int k = 0; k < 8; ++k) mp[k] = -INFINITY;
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            // a hidden score, whatever it holds, becomes -inf
-            if (!(((i < 32 ? seen0 : seen1) >> (i & 31)) & 1u)) v[i] = 0xff800000u;
-            mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(v[i]));
+            for (int i = 0; i < 64; ++i) {
+              // a hidden score, whatever it holds, becomes -inf
+              if (!(((i < 32 ? seen0 : seen1) >> (i & 31)) & 1u)) v[i] = 0xff800000u;
+              mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(v[i]));
+            }
+            mloc = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
+                         fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
           }
-          mloc = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
-                       fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
         }
         mloc = mloc * sl;  // scale > 0 keeps the order
         red_max[(b * 2 + hc) * 128 + r] = mloc;
@@ -606,10 +713,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool move = m_new > m_run + kRescaleThreshold;
         const float m_use = move ? m_new : m_run;
         const float alpha = move ? fast_exp2(m_run - m_use) : 1.f;
+        float rsp[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t pk[32];
-        float rs = 0.f;
-        if (any) {
-          float rsp[4] = {0.f, 0.f, 0.f, 0.f};
+        // (two copies of the loop: sharing one between the paths measured 3 %
+        // slower per tile)
+        auto weights = [&]() {
 #pragma unroll
           for (int i = 0; i < 64; i += 2) {
             // -inf (hidden) gives exactly 0: m_use is finite
@@ -618,12 +726,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             rsp[(i >> 1) & 3] += e0 + e1;
             pk[i / 2] = pack_bf16x2(e0, e1);
           }
-          rs = (rsp[0] + rsp[1]) + (rsp[2] + rsp[3]);
+        };
+        if (full) {
+          weights();
+        } else if (any) {
+          weights();
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) pk[i] = 0;
         }
-        l_run = l_run * alpha + rs;
+        l_run = l_run * alpha + ((rsp[0] + rsp[1]) + (rsp[2] + rsp[3]));
         m_run = m_use;
         // O is rescaled only when a row maximum moved; PV of the previous
         // tile must have landed first (tile 0's PV overwrites O)
@@ -642,6 +754,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tmem_st32(tmem + lane_off + b3 * 128 + hc * 64, pk);
+        if (j == 0 && pending) write_out();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -650,44 +763,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             mbar_arrive(bar_p_full + 8 * b3);
         }
+        if (j + 1 == nkt) {
+          out_bar = bar_o_done + 8 * b3;
+          out_phase = s_phase;
+        }
         if (++b3 == kNS) {
           b3 = 0;
           s_phase ^= 1;
         }
       }
-
-      // ---- epilogue: O / l -> bf16, and lse.  The next item's first PV waits
-      // for this warp's next arrival on p_full, behind these loads of O.
-      const int pb = b3 == 0 ? kNS - 1 : b3 - 1;
-      wait_or_abort_warp<2>(bar_o_done + 8 * pb, b3 == 0 ? s_phase ^ 1 : s_phase, abort_flag, a);
-      tc_fence_after();
-      red_sum[hc * 128 + r] = l_run;
-      named_barrier(1 + qd, 64);
-      const float l_tot = l_run + red_sum[(hc ^ 1) * 128 + r];
-      const int tok = r / G, g = r % G;
-      const bool store = tok < tv && !*abort_flag;
-      const float inv = l_tot == 0.f ? 0.f : 1.f / l_tot;  // a NaN sum stays visible
-      const int64_t row = static_cast<int64_t>(it.q0 + t0 + tok) * a.num_q_heads + it.kvh * G + g;
-#pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        uint32_t (&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32 * cc]);
-        tmem_ld32(ocol + 32 * cc, w);
-        if (store) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            pk[i / 2] = pack_bf16x2(__uint_as_float(w[i]) * inv, __uint_as_float(w[i + 1]) * inv);
-          uint4* dst = reinterpret_cast<uint4*>(a.out + row * 128 + hc * 64 + cc * 32);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            dst[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
-        }
-      }
-      if (store && hc == 0 && a.out_lse)
-        a.out_lse[row] = l_tot == 0.f ? -INFINITY : (m_run + __log2f(l_tot)) * kLn2;
-      // (after a timeout every softmax warp still walks every item, its waits
-      // skipped: a pair of warps meets at its named barrier to the end)
+      pending = true;
+      out_row = row;
+      out_m = m_run;
+      out_l = l_run;
     }
+    if (pending) write_out();
   }
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may still report to it
