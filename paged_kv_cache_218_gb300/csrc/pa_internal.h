@@ -218,7 +218,8 @@ cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap* tm_q, const 
                            const CUtensorMap* tm_v, int grid_tiles, cudaStream_t stream);
 cudaError_t launch_prefill_window(const WindowPrefillArgs& a, const CUtensorMap* tm_q,
                                   const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                  int64_t max_items, int num_sms, cudaStream_t stream);
+                                  const CUtensorMap* tm_o, int64_t max_items, int num_sms,
+                                  cudaStream_t stream);
 size_t prefill_smem_bytes();
 bool cascade_shape(int num_kv_heads, int group, int max_group, int* kv_per_cta, int* warps_per_kv,
                    int* stages);

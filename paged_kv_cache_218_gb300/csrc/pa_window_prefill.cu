@@ -30,12 +30,15 @@
 //    the other roles read.  Block ids of the next item are fetched while the
 //    last one's tiles load, and the softmax writes P of an item's first tile
 //    before it turns to the output of the item before, whose last product is
-//    then done.
+//    then done.  Outputs leave through shared memory and a tensor store per warp
+//    (written straight from the registers, a row per lane, they took 1.6 us per
+//    item).
 //
 // What bounds it: the tensor pipe and, at 128 x 128 tiles, the softmax that
 // feeds it (one exponential per score).
 // Every mbarrier wait is bounded, as in pa_prefill_body.cuh.
 #include <mutex>
+#include <type_traits>
 
 #include "pa_prefill_body.cuh"
 
@@ -46,19 +49,20 @@ namespace {
 constexpr uint64_t kSettleNs = 1000000;  // far longer than any copy takes
 constexpr float kFloor = -1e30f;  // reference maximum of a row that saw nothing yet
 
-// Shared memory of one CTA of a pair: two Q tiles, four K and four V half
-// tiles, block ids of both loaders, the softmax's exchange, barriers.
+// Shared memory of one CTA of a pair: two Q tiles, four K and three V half
+// tiles, an output tile, block ids of both loaders, the softmax's exchange, barriers.
 struct WPlan {
-  static constexpr int kNK = 4, kNV = 4;
+  static constexpr int kNK = 4, kNV = 3;
   static constexpr int kKSlot = kHalf, kVSlot = kHalf;
   static constexpr int kQOff = 0;  // [2][2 * kHalf]
   static constexpr int kKOff = kQOff + 4 * kHalf;
   static constexpr int kVOff = kKOff + kNK * kKSlot;
-  static constexpr int kIdsOff = kVOff + kNV * kVSlot;
+  static constexpr int kOutOff = kVOff + kNV * kVSlot;  // [2 halves][128 rows][64 columns]
+  static constexpr int kIdsOff = kOutOff + 2 * kHalf;
   static constexpr int kRedOff = kIdsOff + 2 * kIdRing * 8 * 4;
   static constexpr int kRedOff2 = kRedOff + 2 * 2 * 128 * 4;
   static constexpr int kBarOff = kRedOff2 + 2 * 128 * 4;
-  static constexpr int kItemsOff = kBarOff + 384;  // [kItemRing]
+  static constexpr int kItemsOff = kBarOff + 448;  // [kItemRing]
   static constexpr int kSmemBytes = kItemsOff + 8 * 64;
 };
 static_assert(WPlan::kSmemBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
@@ -185,7 +189,8 @@ __device__ __forceinline__ uint64_t low_bits(int k) {
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
-                          const __grid_constant__ CUtensorMap tm_v, const WindowPrefillArgs a) {
+                          const __grid_constant__ CUtensorMap tm_v,
+                          const __grid_constant__ CUtensorMap tm_o, const WindowPrefillArgs a) {
   using P = WPlan;
   constexpr int kNK = P::kNK, kNV = P::kNV;
   extern __shared__ uint8_t smem_raw[];
@@ -198,15 +203,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_k_empty = bar_k_full + 8 * kNK;
   const uint32_t bar_v_full = bar_k_empty + 8 * kNK;   // [kNV]: this CTA's V landed (edge tiles)
   const uint32_t bar_v_ready = bar_v_full + 8 * kNV;   // [kNV]: V of the pair ready
-  const uint32_t bar_v_empty = bar_v_ready + 8 * kNV;
-  const uint32_t bar_s_full = bar_v_empty + 8 * kNV;   // [kNS]: scores of a tile
+  const uint32_t bar_s_full = bar_v_ready + 8 * kNV;   // [kNS]: scores of a tile
   const uint32_t bar_p_full = bar_s_full + 8 * kNS;    // [kNS]: softmax done
-  const uint32_t bar_o_done = bar_p_full + 8 * kNS;    // [kNS]: PV done
+  const uint32_t bar_o_done = bar_p_full + 8 * kNS;    // [kNS]: PV done, and so V slot free
   const uint32_t bar_item = bar_o_done + 8 * kNS;      // [kItemRing]: item published
-  static_assert(32 + 8 * (2 * kNK + 3 * kNV + 3 * kNS + kItemRing) <= 336, "barrier area");
+  static_assert(32 + 8 * (2 * kNK + 2 * kNV + 3 * kNS + kItemRing) <= 336, "barrier area");
+  static_assert(kNV == kNS, "V slot of a tile = its score buffer");
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P::kBarOff + 336);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 340);
-  volatile int* go_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 352);  // [2][4]
+  volatile int* go_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 352);
   auto ring_item = [&](int k) {
     return reinterpret_cast<Item*>(smem + P::kItemsOff + 64 * (k % kItemRing));
   };
@@ -233,7 +238,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k < kNV; ++k) {
       mbar_init(bar_v_full + 8 * k, 1);
       mbar_init(bar_v_ready + 8 * k, 2);
-      mbar_init(bar_v_empty + 8 * k, 1);
     }
     for (int k = 0; k < kNS; ++k) {
       mbar_init(bar_s_full + 8 * k, 1);
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int slot = total % kNV;
             bool free_slot = total < kNV;
             if (!free_slot && lane == 0)
-              free_slot = mbar_test_wait(bar_v_empty + 8 * slot, ((total / kNV) - 1) & 1);
+              free_slot = mbar_test_wait(bar_o_done + 8 * slot, ((total / kNV) - 1) & 1);
             if (__shfl_sync(0xffffffffu, free_slot ? 1 : 0, 0)) {
               const bool remote = !issuer && !edge;
               const uint32_t bar = edge ? bar_v_full + 8 * slot
@@ -496,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane == 0)
         for (int sl = 0; sl < kNV && sl < total; ++sl)
-          wait_or_abort<2>(bar_v_empty + 8 * sl, ((total - 1 - sl) / kNV) & 1, abort_flag, a);
+          wait_or_abort<2>(bar_o_done + 8 * sl, ((total - 1 - sl) / kNV) & 1, abort_flag, a);
       settle();
     }
     __syncwarp();
@@ -582,7 +586,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      dv + ((ks * kBlockBytes) >> 4), idesc_o,
                                      (jp > 0 || ks > 0) ? 1u : 0u);
               commit(bar_o_done + 8 * p_buf);
-              commit(bar_v_empty + 8 * p_vslot);
               ++jp;
               if (++p_buf == kNS) {
                 p_buf = 0;
@@ -615,64 +618,95 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // The output of an item, written once its last PV is done: O / l -> bf16,
     // and lse.  The next item's first PV, which overwrites O, waits for this
-    // warp's arrival on p_full behind these loads of O.
+    // warp's arrival on p_full behind these loads of O.  A warp's 32 rows, if
+    // all are tokens of the chunk, go to its part of the staging tile and from
+    // there by one tensor store.  The barrier in it also hands over the key
+    // tiles of the item after the one at hand (go_flag 0 .. 7; -1: not
+    // published yet).
+    const int tok = r / G, warp_toks = 32 / G;
+    const uint32_t stage = sbase + P::kOutOff + hc * kHalf + qd * 32 * 128;
     bool pending = false;
     int64_t out_row = 0;       // of the pending item's row; < 0: not stored
+    bool out_whole = false;    // all rows of this warp are
+    int out_y = 0, out_z = 0;  // first head and token of this warp's rows
     float out_m = 0.f, out_l = 0.f;
-    uint32_t out_bar = 0, out_phase = 0;
-    auto write_out = [&]() {
+    uint32_t out_bar = 0, out_phase = 0;  // PV of its last tile
+    auto write_out = [&](int k) {
+      volatile int* go = go_flag + (k & 1) * 4 + qd;
+      if (hc == 0 && lane == 0)
+        *go = mbar_test_wait(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1)
+                  ? ring_item(k)->nkt
+                  : -1;
       wait_or_abort_warp<2>(out_bar, out_phase, abort_flag, a);
       tc_fence_after();
       red_sum[hc * 128 + r] = out_l;
+      tmem_ld64(ocol, v);
       named_barrier(1 + qd, 64);
       const float l_tot = out_l + red_sum[(hc ^ 1) * 128 + r];
-      const bool store = out_row >= 0 && !*abort_flag;
       const float inv = l_tot == 0.f ? 0.f : 1.f / l_tot;  // a NaN sum stays visible
+      uint32_t pk[32];
 #pragma unroll
-      for (int cc = 0; cc < 2; ++cc) {
-        uint32_t (&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32 * cc]);
-        tmem_ld32(ocol + 32 * cc, w);
-        if (store) {
-          uint32_t pk[16];
+      for (int i = 0; i < 64; i += 2)
+        pk[i / 2] = pack_bf16x2(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
+      const bool good = !warp_flag(abort_flag);
+      if (out_whole && good) {
+        if (lane == 0) bulk_wait_read();  // the last item's store, long done
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            pk[i / 2] = pack_bf16x2(__uint_as_float(w[i]) * inv, __uint_as_float(w[i + 1]) * inv);
-          uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * 128 + hc * 64 + cc * 32);
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            dst[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+        for (int q = 0; q < 8; ++q)  // 16-byte columns in the 128-byte swizzle
+          sts128(stage + lane * 128 + ((q ^ (lane & 7)) << 4),
+                 make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&tm_o, hc * 64, out_y, out_z, stage);
+          bulk_commit_group();
         }
+      } else if (out_row >= 0 && good) {
+        uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * 128 + hc * 64);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          dst[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
       }
-      if (store && hc == 0 && a.out_lse)
+      if (out_row >= 0 && good && hc == 0 && a.out_lse)
         a.out_lse[out_row] = l_tot == 0.f ? -INFINITY : (out_m + __log2f(l_tot)) * kLn2;
+      return *go;
     };
 
+    // Both warps of a quadrant act on what the first one found of the next
+    // item: they meet at a named barrier for every tile, also after a timeout
+    // (when the waits are skipped and what they compute is not stored).
+    int nkt = -1;
     for (int k = 0;; ++k) {
-      // Both warps of a quadrant act on what the first one found: they meet at
-      // a named barrier for every tile, also after a timeout (when the waits
-      // are skipped and what they compute is not stored).
-      if (hc == 0) {
-        const bool got =
-            wait_or_abort_warp<2>(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1, abort_flag, a);
-        if (lane == 0) go_flag[(k & 1) * 4 + qd] = got ? ring_item(k)->nkt : 0;
+      const uint32_t item_bar = bar_item + 8 * (k % kItemRing);
+      if (nkt < 0) {
+        volatile int* go = go_flag + 8 + (k & 1) * 4 + qd;
+        if (hc == 0) {
+          const bool got = wait_or_abort_warp<2>(item_bar, (k / kItemRing) & 1, abort_flag, a);
+          if (lane == 0) *go = got ? ring_item(k)->nkt : 0;
+        }
+        named_barrier(1 + qd, 64);
+        nkt = *go;
       }
-      named_barrier(1 + qd, 64);
-      const int nkt = go_flag[(k & 1) * 4 + qd];
       if (nkt == 0) break;
+      int next_nkt = -1;
       const Item& it = *ring_item(k);
       const int kmax = it.kmax, p0 = it.p0, t0 = it.tc0 + rank * tpt;
       const int shift = (it.b_first - it.nsb) * kBlockSize;
-      const int tok = r / G;
       const int pos = p0 + t0 + tok;
-      const int64_t row = tok < min(it.qlen - t0, tpt)
-                              ? static_cast<int64_t>(it.q0 + t0 + tok) * a.num_q_heads +
-                                    it.kvh * G + r % G
-                              : -1;
+      const int tv = min(it.qlen - t0, tpt);  // tokens of this tile (<= 0: none)
+      const int row_y = it.kvh * G, row_z = it.q0 + t0 + qd * warp_toks;
+      const int64_t row =
+          tok < tv ? static_cast<int64_t>(it.q0 + t0 + tok) * a.num_q_heads + row_y + (r - tok * G)
+                   : -1;
       // last and first visible virtual key of the row's window
       const int hi = min(pos, kmax - 1) - shift;
       const int lo = max(0, pos - (a.window - 1)) - shift;
       float m_run = kFloor, l_run = 0.f;
-      for (int j = 0; j < nkt; ++j, ++jt) {
+      // (the first tile apart: what only it does stays out of the loop, whose
+      // every instruction counts)
+      auto tile = [&](int j, auto is_first) {
+        constexpr bool first = decltype(is_first)::value;
         const int b = jt & 1;
         wait_or_abort_warp<2>(bar_s_full + 8 * b3, s_phase, abort_flag, a);
         tc_fence_after();
@@ -713,17 +747,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool move = m_new > m_run + kRescaleThreshold;
         const float m_use = move ? m_new : m_run;
         const float alpha = move ? fast_exp2(m_run - m_use) : 1.f;
-        float rsp[4] = {0.f, 0.f, 0.f, 0.f};
+        uint64_t rsp[2] = {0, 0};
         uint32_t pk[32];
         // (two copies of the loop: sharing one between the paths measured 3 %
         // slower per tile)
+        const uint64_t sl2 = f32x2(sl, sl), nm2 = f32x2(-m_use, -m_use);
         auto weights = [&]() {
 #pragma unroll
           for (int i = 0; i < 64; i += 2) {
             // -inf (hidden) gives exactly 0: m_use is finite
-            const float e0 = fast_exp2(fmaf(__uint_as_float(v[i]), sl, -m_use));
-            const float e1 = fast_exp2(fmaf(__uint_as_float(v[i + 1]), sl, -m_use));
-            rsp[(i >> 1) & 3] += e0 + e1;
+            const float2 x =
+                f32x2_parts(fma2(f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sl2, nm2));
+            const float e0 = fast_exp2(x.x), e1 = fast_exp2(x.y);
+            rsp[(i >> 1) & 1] = add2(rsp[(i >> 1) & 1], f32x2(e0, e1));
             pk[i / 2] = pack_bf16x2(e0, e1);
           }
         };
@@ -735,11 +771,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) pk[i] = 0;
         }
-        l_run = l_run * alpha + ((rsp[0] + rsp[1]) + (rsp[2] + rsp[3]));
+        const float2 rs = f32x2_parts(add2(rsp[0], rsp[1]));
+        l_run = l_run * alpha + (rs.x + rs.y);
         m_run = m_use;
         // O is rescaled only when a row maximum moved; PV of the previous
         // tile must have landed first (tile 0's PV overwrites O)
-        if (j >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
           const int pb = b3 == 0 ? kNS - 1 : b3 - 1;
           wait_or_abort_warp<2>(bar_o_done + 8 * pb, b3 == 0 ? s_phase ^ 1 : s_phase, abort_flag,
                                 a);
@@ -754,7 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         tmem_st32(tmem + lane_off + b3 * 128 + hc * 64, pk);
-        if (j == 0 && pending) write_out();
+        if (first && pending) next_nkt = write_out(k + 1);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -763,21 +800,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           else
             mbar_arrive(bar_p_full + 8 * b3);
         }
-        if (j + 1 == nkt) {
-          out_bar = bar_o_done + 8 * b3;
-          out_phase = s_phase;
-        }
         if (++b3 == kNS) {
           b3 = 0;
           s_phase ^= 1;
         }
-      }
+        ++jt;
+      };
+      tile(0, std::true_type{});
+      for (int j = 1; j < nkt; ++j) tile(j, std::false_type{});
+      out_bar = bar_o_done + 8 * (b3 == 0 ? kNS - 1 : b3 - 1);
+      out_phase = b3 == 0 ? s_phase ^ 1 : s_phase;
       pending = true;
       out_row = row;
+      out_whole = (qd + 1) * warp_toks <= tv;
+      out_y = row_y;
+      out_z = row_z;
       out_m = m_run;
       out_l = l_run;
+      nkt = next_nkt;
     }
-    if (pending) write_out();
+    if (pending) write_out(0);
+    if (lane == 0) bulk_wait_done();
   }
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may still report to it
@@ -792,7 +835,7 @@ using namespace pre;
 
 cudaError_t launch_prefill_window(const WindowPrefillArgs& args, const CUtensorMap* tm_q,
                                   const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                  int64_t max_items, int num_sms, cudaStream_t stream) {
+                                  const CUtensorMap* tm_o, int64_t max_items, int num_sms, cudaStream_t stream) {
   WindowPrefillArgs a = args;
   if (a.wait_ns == 0) a.wait_ns = kWaitLimitNs;
   constexpr int smem = WPlan::kSmemBytes + 1024;
@@ -826,7 +869,7 @@ cudaError_t launch_prefill_window(const WindowPrefillArgs& args, const CUtensorM
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, prefill_window_kernel, *tm_q, *tm_k, *tm_v, a);
+  e = cudaLaunchKernelEx(&cfg, prefill_window_kernel, *tm_q, *tm_k, *tm_v, *tm_o, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
