@@ -16,7 +16,7 @@
 //  * A row's mask over a 64-column half of a tile is
 //    vk <= hi && (vk < sinks || vk >= lo): one 64-bit mask per row and half,
 //    built from three counts; halves that all rows of a warp see whole skip
-//    it, halves that none sees skip the exponentials.
+//    it.
 //  * V rows that no row of the pair may see (ends of the sinks' and of the
 //    window's first block, slots behind the last key) are zeroed in shared
 //    memory before the product: they may hold anything, and 0 * NaN is NaN.
@@ -703,8 +703,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int hi = min(pos, kmax - 1) - shift;
       const int lo = max(0, pos - (a.window - 1)) - shift;
       float m_run = kFloor, l_run = 0.f;
-      // (the first tile apart: what only it does stays out of the loop, whose
-      // every instruction counts)
+      // (The first tile apart, and one copy of the exponentials in each body:
+      // instruction fetches bound this loop.  Everything in one body measured
+      // 0.85 us a tile, two more copies 0.78, this 0.755; a first tile is
+      // masked in nearly every item, so it takes the masks always.)
       auto tile = [&](int j, auto is_first) {
         constexpr bool first = decltype(is_first)::value;
         const int b = jt & 1;
@@ -712,9 +714,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int kb = j * kTileKeys + hc * 64;
         const bool whole = hi >= kb + 63 && (lo <= kb || a.sinks >= kb + 64);
-        const bool full = __all_sync(0xffffffffu, whole);
-        bool any = true;
-        float mloc = -INFINITY;
+        const bool full = !first && __all_sync(0xffffffffu, whole);
+        float mloc;
         if (full) {
           tmem_ld64_max(tmem + lane_off + b3 * 128 + hc * 64, v, mloc);
         } else {
@@ -723,21 +724,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               (low_bits(a.sinks > kb ? min(a.sinks - kb, 64) : 0) | ~low_bits(lo - kb));
           const uint32_t seen0 = static_cast<uint32_t>(seen);
           const uint32_t seen1 = static_cast<uint32_t>(seen >> 32);
-          any = __any_sync(0xffffffffu, seen != 0);
-          if (any) {
-            tmem_ld64(tmem + lane_off + b3 * 128 + hc * 64, v);
-            float mp[8];
+          tmem_ld64(tmem + lane_off + b3 * 128 + hc * 64, v);
+          float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int k = 0; k < 8; ++k) mp[k] = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 64; ++i) {
-              // a hidden score, whatever it holds, becomes -inf
-              if (!(((i < 32 ? seen0 : seen1) >> (i & 31)) & 1u)) v[i] = 0xff800000u;
-              mp[i & 7] = fmaxf(mp[i & 7], __uint_as_float(v[i]));
-            }
-            mloc = fmaxf(fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3])),
-                         fmaxf(fmaxf(mp[4], mp[5]), fmaxf(mp[6], mp[7])));
+          for (int i = 0; i < 64; ++i) {
+            // a hidden score, whatever it holds, becomes -inf
+            v[i] = (((i < 32 ? seen0 : seen1) >> (i & 31)) & 1u) ? v[i] : 0xff800000u;
+            mp[i & 3] = fmaxf(mp[i & 3], __uint_as_float(v[i]));
           }
+          mloc = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
         }
         mloc = mloc * sl;  // scale > 0 keeps the order
         red_max[(b * 2 + hc) * 128 + r] = mloc;
@@ -749,27 +744,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float alpha = move ? fast_exp2(m_run - m_use) : 1.f;
         uint64_t rsp[2] = {0, 0};
         uint32_t pk[32];
-        // (two copies of the loop: sharing one between the paths measured 3 %
-        // slower per tile)
         const uint64_t sl2 = f32x2(sl, sl), nm2 = f32x2(-m_use, -m_use);
-        auto weights = [&]() {
 #pragma unroll
-          for (int i = 0; i < 64; i += 2) {
-            // -inf (hidden) gives exactly 0: m_use is finite
-            const float2 x =
-                f32x2_parts(fma2(f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sl2, nm2));
-            const float e0 = fast_exp2(x.x), e1 = fast_exp2(x.y);
-            rsp[(i >> 1) & 1] = add2(rsp[(i >> 1) & 1], f32x2(e0, e1));
-            pk[i / 2] = pack_bf16x2(e0, e1);
-          }
-        };
-        if (full) {
-          weights();
-        } else if (any) {
-          weights();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) pk[i] = 0;
+        for (int i = 0; i < 64; i += 2) {
+          // -inf (hidden) gives exactly 0: m_use is finite
+          const float2 x =
+              f32x2_parts(fma2(f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sl2, nm2));
+          const float e0 = fast_exp2(x.x), e1 = fast_exp2(x.y);
+          rsp[(i >> 1) & 1] = add2(rsp[(i >> 1) & 1], f32x2(e0, e1));
+          pk[i / 2] = pack_bf16x2(e0, e1);
         }
         const float2 rs = f32x2_parts(add2(rsp[0], rsp[1]));
         l_run = l_run * alpha + (rs.x + rs.y);
@@ -807,6 +790,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++jt;
       };
       tile(0, std::true_type{});
+#pragma unroll 1
       for (int j = 1; j < nkt; ++j) tile(j, std::false_type{});
       out_bar = bar_o_done + 8 * (b3 == 0 ? kNS - 1 : b3 - 1);
       out_phase = b3 == 0 ? s_phase ^ 1 : s_phase;
