@@ -198,7 +198,7 @@ struct RopeArgs {
   int interleaved;
 };
 
-constexpr int kMaxWindowSplit = 8;  // portable cluster size
+constexpr int kMaxWindowSplit = 16;  // CTAs of a cluster, where the device allows it
 
 constexpr int kMaxPrefixParts = 4;  // cascade: most CTAs per (group, kv-head subset)
 

@@ -251,31 +251,6 @@ __device__ __forceinline__ int atom_add_acq_rel_gpu(int* p, int v) {
   return old;
 }
 
-// Cluster launch control: a running CTA takes over one that has not started
-// yet.  The request is asynchronous: its 16-byte answer lands in shared memory
-// and completes 16 bytes on `bar`.  No request may follow one that was refused.
-__device__ __forceinline__ void clc_try_cancel(uint32_t answer, uint32_t bar) {
-  asm volatile(
-      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-          answer),
-      "r"(bar)
-      : "memory");
-}
-
-// blockIdx.x of the CTA taken over, or -1.
-__device__ __forceinline__ int clc_answer(uint4 a) {
-  uint32_t x, got;
-  asm volatile(
-      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b64 lo, hi;\n\t"
-      "mov.b64 lo, {%2, %3};\n\tmov.b64 hi, {%4, %5};\n\tmov.b128 h, {lo, hi};\n\t"
-      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-      "selp.u32 %1, 1, 0, p;\n\tmov.u32 %0, 0;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
-      : "=r"(x), "=r"(got)
-      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w));
-  return got ? static_cast<int>(x) : -1;
-}
-
 // Programmatic dependent launch: wait until the previous kernel on the stream
 // has finished and its memory is visible / let the next kernel start launching.
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
