@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libpa.so (include/pa.h).
+"""Thin binding of libpa.so (include/pa.h), through ctypes and, for the
+windowed-attention and norm-rotation calls, a small extension (_pycall).
 
 Argument marshalling only: each function takes torch tensors, checks their
 dtype / device / contiguity, and passes raw pointers, sizes and the current
@@ -20,6 +21,7 @@ if not os.path.exists(_LIB_PATH):
         f"libpa.so not found at {_LIB_PATH}; build it first with "
         "`python -m paged_kv_cache_218_gb300.build` (or __graft_entry__.build())")
 _lib = ctypes.CDLL(_LIB_PATH)
+from . import _pycall  # noqa: E402  (needs libpa.so; built with it)
 
 PA_OK = 0
 PA_ERR_INVALID = -1
@@ -70,17 +72,9 @@ _SIGS = {
     "pa_hybrid_attention_append": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _P,
                                     _P, _P, _P, _P, _P, _I, _P, _I, _P, _L, _L,
                                     _P, _P, _I, _I, _I, _I, _L, _F, _I, _P, _S, _P], _I),
-    "pa_prefill_window": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _L, _I,
-                           _I, _F, _P, _P], _I),
     "pa_test_prefill_window_stalled": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I,
                                         _I, _L, _I, _I, _F, ctypes.c_uint, _P], _I),
     "pa_rope_increments": ([_P, ctypes.POINTER(_F), _I, _D, _I, _D, _D, _D, _D], _I),
-    "pa_qk_norm_rope_cache": ([_P, _P, _P, _P, _P, _L, _L, _L, _P, _P, _F, _P, _P, _I, _I, _F,
-                               _P, _P, _P, _I, _I, _I, _I, _I, _L, _P], _I),
-    "pa_qk_norm_rope_cache_fp8": ([_P, _P, _P, _P, _P, _L, _L, _L, _P, _P, _F, _P, _P, _I, _I, _F,
-                                   _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _L, _P], _I),
-    "pa_decode_window": ([_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _L, _I, _I, _F, _P, _P],
-                         _I),
     "pa_test_decode_stalled": ([_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _L, _F, _I, _P,
                                 _S, ctypes.c_uint, _P], _I),
     "pa_test_prefill_stalled": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I,
@@ -98,6 +92,11 @@ class PAError(RuntimeError):
     def __init__(self, fn: str, status: int):
         super().__init__(f"{fn} failed: {pa_status_string(status)} ({status})")
         self.status = status
+
+
+_pycall.setup(torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
+              getattr(torch._C, "_cuda_getCurrentRawStream", None),
+              getattr(torch._C, "_cuda_getDevice", None), PAError)
 
 
 def _check(fn: str, rc: int) -> None:
@@ -126,58 +125,6 @@ def _need(t: torch.Tensor, name: str, dtype, dims: Optional[int] = None, contigu
         raise ValueError(f"{name} must have {dims} dims, got {t.dim()}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-
-
-def _refuse(t, name: str, dtype, shape, device: int) -> None:
-    """The reason why _arg takes this tensor for no such argument."""
-    _need(t, name, dtype, len(shape))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name} is on {t.device}, and other arguments on cuda:{device}")
-
-
-def _arg(t, name: str, dtype, shape, device: int) -> int:
-    """The address of a contiguous tensor of this type and shape on this device.
-    (One pass of cheap checks: a small call spends most of its time here.)"""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device and
-            t.shape == shape and t.is_contiguous()):
-        return t.data_ptr()
-    return _refuse(t, name, dtype, shape, device)
-
-
-def _rows(t, name: str, shape, device: int) -> int:
-    """_arg for bf16 rows [tokens, heads, head_dim] at any token stride."""
-    if (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.get_device() == device and
-            t.shape == shape):
-        st = t.stride()
-        if st[2] == 1 and (st[1] == shape[2] or shape[1] == 1):
-            return t.data_ptr()
-        raise ValueError(f"{name} must be contiguous within a token")
-    _need(t, name, torch.bfloat16, 3, contiguous=False)
-    return _refuse(t.contiguous(), name, torch.bfloat16, shape, device)
-
-
-def _queue(first, device: int, stream) -> int:
-    """The stream of a call whose tensors are on `device`, which has to be the
-    current one."""
-    if device != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors on {first.device}, current device "
-                         f"cuda:{torch.cuda.current_device()}")
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
-
-
-def _status(fn: str, rc: int) -> None:
-    if rc:
-        raise PAError(fn, rc)
-
-
-def _int32(name: str, v, least: int) -> int:
-    """An int argument of the C call: ctypes would wrap a larger one silently."""
-    if type(v) is not int:
-        v = int(v)
-    if not least <= v <= 0x7FFFFFFF:
-        raise ValueError(f"{name} must be in [{least}, 2**31 - 1], got {v}")
-    return v
 
 
 def pa_status_string(status: int) -> str:
@@ -367,31 +314,8 @@ def pa_prefill_window(out, q, k_cache, v_cache, block_tables, cu_q_lens, q_start
                       max_q_len, window, sinks, scale, out_lse=None, stream=None) -> None:
     """pa_prefill_chunk under a sliding window: the query at position p sees keys
     j <= p with j < sinks or p - j < window."""
-    _need(q, "q", torch.bfloat16, 3)
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-        _need(k_cache, "k_cache", torch.bfloat16, 4)
-    if not isinstance(cu_q_lens, torch.Tensor) or cu_q_lens.dim() != 1:
-        _need(cu_q_lens, "cu_q_lens", torch.int32, 1)
-    T, Hq, D = shape = q.shape
-    nb, bs, Hkv, _ = k_cache.shape
-    C = cu_q_lens.shape[0] - 1
-    dev = q.get_device()
-    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
-        _need(block_tables, "block_tables", torch.int32, 2)
-    mb = block_tables.shape[1]
-    if C < 0:
-        raise ValueError("cu_q_lens must hold one more entry than there are chunks")
-    args = (_arg(out, "out", torch.bfloat16, shape, dev), q.data_ptr(),
-            _arg(k_cache, "k_cache", torch.bfloat16, (nb, bs, Hkv, D), dev),
-            _arg(v_cache, "v_cache", torch.bfloat16, (nb, bs, Hkv, D), dev),
-            _arg(block_tables, "block_tables", torch.int32, (C, mb), dev), mb,
-            _arg(cu_q_lens, "cu_q_lens", torch.int32, (C + 1,), dev),
-            _arg(q_start_pos, "q_start_pos", torch.int32, (C,), dev),
-            _arg(seq_lens, "seq_lens", torch.int32, (C,), dev), C, T,
-            _int32("max_q_len", max_q_len, 0), Hq, Hkv, D, bs, nb, _int32("window", window, 1),
-            _int32("sinks", sinks, 0), scale,
-            None if out_lse is None else _arg(out_lse, "out_lse", torch.float32, (T, Hq), dev))
-    _status("pa_prefill_window", _lib.pa_prefill_window(*args, _queue(q, dev, stream)))
+    _pycall.prefill_window(out, q, k_cache, v_cache, block_tables, cu_q_lens, q_start_pos, seq_lens,
+                           max_q_len, window, sinks, scale, out_lse, stream)
 
 
 ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
@@ -406,56 +330,15 @@ def pa_rope_increments(rot_dim, base=10000.0, scaling="none", factor=1.0, origin
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}, got {scaling!r}")
     p0, p1 = params if params is not None else {"yarn": (32.0, 1.0), "wavelength": (1.0, 4.0)}.get(
         scaling, (0.0, 0.0))
-    rot_dim = _int32("rot_dim", rot_dim, 0)
+    rot_dim = int(rot_dim)
+    if not 0 <= rot_dim <= 0x7FFFFFFF:
+        raise ValueError(f"rot_dim must be in [0, 2**31 - 1], got {rot_dim}")
     inc = torch.empty(rot_dim // 2, dtype=torch.int64)
     f = _F(0.0)
     _check("pa_rope_increments", _lib.pa_rope_increments(
         inc.data_ptr(), ctypes.byref(f), rot_dim, float(base), ROPE_SCALINGS[scaling],
         float(factor), float(original_context), float(p0), float(p1)))
     return inc, float(f.value)
-
-
-def _norm_rope(fn, pool_dtype, q_out, q, k, v, positions, increments, k_cache, v_cache,
-               slot_mapping, scales, q_weight, k_weight, eps, interleaved, rope_factor, k_out,
-               stream):
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        _need(q, "q", torch.bfloat16, 3, contiguous=False)
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        _need(k, "k", torch.bfloat16, 3, contiguous=False)
-    T, Hq, D = shape = q.shape
-    Hkv = k.shape[1]
-    kv_shape = (T, Hkv, D)
-    dev = q.get_device()
-    qp, kp = _rows(q, "q", shape, dev), _rows(k, "k", kv_shape, dev)
-    q_row, k_row = Hq * D, Hkv * D
-    # (a single token's stride is never used: any view of one row will do)
-    q_stride, k_stride = (q.stride(0), k.stride(0)) if T > 1 else (q_row, k_row)
-    vp, v_stride, kcp, vcp, slots, bs, nb = None, k_row, None, None, None, 0, 0
-    if k_cache is not None or v_cache is not None or scales:
-        if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-            _need(k_cache, "k_cache", pool_dtype, 4)
-        nb, bs = k_cache.shape[:2]
-        vp = _rows(v, "v", kv_shape, dev)
-        if T > 1:
-            v_stride = v.stride(0)
-        kcp = _arg(k_cache, "k_cache", pool_dtype, (nb, bs, Hkv, D), dev)
-        vcp = _arg(v_cache, "v_cache", pool_dtype, (nb, bs, Hkv, D), dev)
-        slots = _arg(slot_mapping, "slot_mapping", torch.int64, (T,), dev)
-    rot, pp, ip = 0, None, None
-    if increments is not None:
-        _need(increments, "increments", torch.int64, 1)
-        rot = 2 * increments.shape[0]
-        ip = _arg(increments, "increments", torch.int64, (rot // 2,), dev)
-        pp = _arg(positions, "positions", torch.int64, (T,), dev)
-    args = [_arg(q_out, "q_out", torch.bfloat16, shape, dev),
-            None if k_out is None else _arg(k_out, "k_out", torch.bfloat16, kv_shape, dev),
-            qp, kp, vp, q_stride, k_stride, v_stride,
-            None if q_weight is None else _arg(q_weight, "q_weight", torch.float32, (D,), dev),
-            None if k_weight is None else _arg(k_weight, "k_weight", torch.float32, (D,), dev),
-            eps, pp, ip, rot, 1 if interleaved else 0, rope_factor, kcp, vcp, slots]
-    for t, n in zip(scales, ("k_scales", "v_scales")):
-        args.append(_arg(t, n, torch.float32, (Hkv,), dev))
-    _status(fn.__name__, fn(*args, T, Hq, Hkv, D, bs, nb, _queue(q, dev, stream)))
 
 
 def pa_qk_norm_rope_cache(q_out, q, k, v, positions, increments, k_cache, v_cache, slot_mapping,
@@ -465,9 +348,8 @@ def pa_qk_norm_rope_cache(q_out, q, k, v, positions, increments, k_cache, v_cach
     no norm), rotation of the first 2 * len(increments) columns (None: none),
     q -> q_out, k -> its slots of k_cache and k_out, v -> its slots of v_cache.
     With both pools None: no scatter, k_out required."""
-    _norm_rope(_lib.pa_qk_norm_rope_cache, torch.bfloat16, q_out, q, k, v, positions, increments,
-               k_cache, v_cache, slot_mapping, (), q_weight, k_weight, eps, interleaved,
-               rope_factor, k_out, stream)
+    _pycall.norm_rope(q_out, k_out, q, k, v, positions, increments, k_cache, v_cache, slot_mapping,
+                      None, None, q_weight, k_weight, eps, interleaved, rope_factor, stream, False)
 
 
 def pa_qk_norm_rope_cache_fp8(q_out, q, k, v, positions, increments, k_cache, v_cache,
@@ -475,32 +357,17 @@ def pa_qk_norm_rope_cache_fp8(q_out, q, k, v, positions, increments, k_cache, v_
                               eps=1e-6, interleaved=False, rope_factor=1.0, k_out=None,
                               stream=None) -> None:
     """pa_qk_norm_rope_cache into uint8 E4M3 pools with per-kv-head fp32 scales."""
-    _norm_rope(_lib.pa_qk_norm_rope_cache_fp8, torch.uint8, q_out, q, k, v, positions, increments,
-               k_cache, v_cache, slot_mapping, (k_scales, v_scales), q_weight, k_weight, eps,
-               interleaved, rope_factor, k_out, stream)
+    _pycall.norm_rope(q_out, k_out, q, k, v, positions, increments, k_cache, v_cache, slot_mapping,
+                      k_scales, v_scales, q_weight, k_weight, eps, interleaved, rope_factor, stream,
+                      True)
 
 
 def pa_decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, window, sinks, scale,
                      out_lse=None, stream=None) -> None:
     """Decode over each sequence's last `window` keys and first `sinks` keys;
     table entries of blocks without a visible key are not read."""
-    _need(q, "q", torch.bfloat16, 3)
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-        _need(k_cache, "k_cache", torch.bfloat16, 4)
-    S, Hq, D = shape = q.shape
-    nb, bs, Hkv, _ = k_cache.shape
-    dev = q.get_device()
-    if not isinstance(block_tables, torch.Tensor) or block_tables.dim() != 2:
-        _need(block_tables, "block_tables", torch.int32, 2)
-    mb = block_tables.shape[1]
-    args = (_arg(out, "out", torch.bfloat16, shape, dev), q.data_ptr(),
-            _arg(k_cache, "k_cache", torch.bfloat16, (nb, bs, Hkv, D), dev),
-            _arg(v_cache, "v_cache", torch.bfloat16, (nb, bs, Hkv, D), dev),
-            _arg(block_tables, "block_tables", torch.int32, (S, mb), dev), mb,
-            _arg(seq_lens, "seq_lens", torch.int32, (S,), dev), S, Hq, Hkv, D, bs, nb,
-            _int32("window", window, 1), _int32("sinks", sinks, 0), scale,
-            None if out_lse is None else _arg(out_lse, "out_lse", torch.float32, (S, Hq), dev))
-    _status("pa_decode_window", _lib.pa_decode_window(*args, _queue(q, dev, stream)))
+    _pycall.decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, window, sinks, scale,
+                          out_lse, stream)
 
 
 def pa_decode_noalloc(out, q, k_cache, v_cache, block_tables, seq_lens, scale, out_lse=None,

@@ -1,4 +1,5 @@
-"""Build libpa.so (the C-ABI library) from csrc/ with nvcc for sm_103a.
+"""Build libpa.so (the C-ABI library) from csrc/ with nvcc for sm_103a, and
+the extension that marshals some of its calls' arguments (_pycall.so).
 
 Each translation unit compiles in parallel to an object file under
 ``_build/`` at the repository root, then nvcc links the shared library into
@@ -11,12 +12,14 @@ import concurrent.futures
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpa.so")
+PYCALL = os.path.join(PKG, "_pycall.so")  # CPython extension: argument marshalling
 SOURCES = ["pa_api.cu", "pa_decode.cu", "pa_prefill.cu", "pa_hybrid.cu", "pa_cascade.cu",
            "pa_rope.cu", "pa_window_decode.cu",
            "pa_window_prefill.cu", "pa_block_manager.cpp"]
@@ -70,6 +73,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
         os.replace(tmp, LIB)
+    src = os.path.join(CSRC, "pa_pycall.cpp")
+    if force or _stale(PYCALL, [src, os.path.join(CSRC, "..", "..", "include", "pa.h")]):
+        tmp = PYCALL + f".tmp{os.getpid()}"
+        subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+                        "-I" + sysconfig.get_paths()["include"], src, "-o", tmp, "-L" + PKG,
+                        "-l:libpa.so", "-Wl,-rpath,$ORIGIN"], check=True)
+        os.replace(tmp, PYCALL)
     return LIB
 
 

@@ -200,6 +200,42 @@ def test_whole_sequence_matches_pa_decode(pa, cuda_device):
     assert torch.allclose(lse, ref_lse, atol=1e-4, rtol=1e-5)
 
 
+def test_argument_forms(pa, cuda_device):
+    """An explicit stream, whole numbers of numpy, parameters in place of tensors."""
+    x = make([100, 7], 4, 2, 64, 50, 2, 10, cuda_device)
+    want, want_lse = call(pa, *x, 50, 2, 0.1)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    out, lse = call(pa, *x, np.int64(50), np.int32(2), np.float64(0.1), stream=side)
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    q = torch.nn.Parameter(x[0])
+    out, lse = call(pa, q, *x[1:], 50, 2, 0.1)
+    assert torch.equal(out, want)
+    with torch.cuda.stream(side):
+        side.wait_stream(torch.cuda.default_stream())
+        out, lse = call(pa, *x, 50, 2, 0.1)
+    side.synchronize()
+    assert torch.equal(out, want)
+    for bad in (50.0, "50", None):
+        with pytest.raises(TypeError):
+            call(pa, *x, bad, 2, 0.1)
+
+
+def test_no_sequence_and_no_reference_kept(pa, cuda_device):
+    import sys
+    q, kc, vc, bt, sl = make([40], 4, 2, 64, 30, 2, 11, cuda_device)
+    pa.pa_decode_window(q[:0], q[:0], kc, vc, bt[:0], sl[:0], 30, 2, 0.1)
+    before = [sys.getrefcount(t) for t in (q, kc, bt, torch.bfloat16)]
+    out = torch.empty_like(q)
+    for _ in range(50):
+        pa.pa_decode_window(out, q, kc, vc, bt, sl, 30, 2, 0.1)
+        with pytest.raises(ValueError):
+            pa.pa_decode_window(out, q, kc, vc, bt, sl, 0, 2, 0.1)
+    assert [sys.getrefcount(t) for t in (q, kc, bt, torch.bfloat16)] == before
+
+
 def test_refusals(pa, cuda_device):
     q, kc, vc, bt, sl = make([40, 50], 4, 2, 64, 30, 2, 9, cuda_device)
     out = torch.full_like(q, 3.0)
