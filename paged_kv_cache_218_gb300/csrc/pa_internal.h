@@ -226,7 +226,7 @@ bool cascade_shape(int num_kv_heads, int group, int max_group, int* kv_per_cta, 
 cudaError_t launch_cascade_prefix(const CascadeArgs& a, const CUtensorMap* tm_k,
                                   const CUtensorMap* tm_v, cudaStream_t stream);
 cudaError_t launch_norm_rope(const RopeArgs& a, bool kv_fp8, int num_sms, cudaStream_t stream);
-cudaError_t launch_decode_window(WindowDecodeArgs a, int head_dim, int num_sms,
+cudaError_t launch_decode_window(const WindowDecodeArgs& a, int head_dim, int num_sms,
                                  cudaStream_t stream);
 // One launch for a hybrid batch: the balanced decode (bf16, head_dim 128) on
 // its first decode_ctas CTAs and the prefill's CTA pairs on the rest.

@@ -215,6 +215,23 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
                : "memory");
 }
 
+// 16 bytes past L1, or zeros where `bytes` is 0 (then nothing is read); groups
+// of them, and the wait until at most N of this thread's groups are pending.
+__device__ __forceinline__ void cp_async_16_zfill(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes)
+               : "memory");
+}
+
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ void cp_async_wait_all() {
   asm volatile("cp.async.wait_all;" ::: "memory");
 }

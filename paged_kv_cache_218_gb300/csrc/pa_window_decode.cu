@@ -9,35 +9,39 @@
 //
 // What bounds it: HBM.  Every visible K/V row is read once (4 D bytes per key
 // and kv head against 4 D G multiply-adds), so the kernel's job is to keep
-// enough bytes in flight.  A warp owns one kv head and walks 16-token blocks;
-// the block's K and V rows go from global memory straight into registers (64
-// registers = 8 KB per warp in flight at head_dim 128), with the next block's
-// K loads issued as soon as this block's scores are done and its V loads as
-// soon as its P V is.  There is no shared-memory staging, because the
-// contraction order of a dot product is free: a lane hands the tensor core the
-// pieces it loaded, and the query operand is permuted the same way.  Loads are
-// 32 bytes a lane, so that each covers whole 128-byte lines: with 16 bytes (64
-// of a K row at a time) 256 sequences x 4096 keys took 675 us instead of 645
-// (6.77 TB/s, the measured copy rate).  A ring of asynchronous copies in shared
-// memory, 192 KB in flight per SM instead of at most 128, took 742.
+// enough bytes in flight, in requests that memory likes.  A warp owns one kv
+// head and walks 16-token blocks (8 KB of K and V at head_dim 128) through a
+// ring of three in shared memory, filled by asynchronous copies: a copy
+// instruction takes whole rows (two of 256 bytes), so each 128-byte line is
+// asked for once.  The ring is the warp's own, so the warp alone waits for it,
+// and 192 KB per SM are on their way.  At 256 sequences x 4096 keys this reads
+// 7.2 TB/s (measured copy rate: 6.8).  What it replaced, at the same case: rows
+// loaded straight into the MMA's registers, 16 bytes a lane and so 64 of a K
+// row at a time, 688 us; 32 bytes a lane 645; lane-private copies of 16 bytes
+// through shared memory, again 64 of a row at a time, 742; this 590.
 //
 //   scores  S^T (16 keys x 8 heads) = K (A, 16 keys x 16 d) Q^T (B)
 //           lane (g, t) = (lane / 4, lane % 4) holds keys g and g + 8, columns
-//           [16 (4 j + t), + 16) for j < D / 64;
+//           [8 (4 j + t), + 8) for j < D / 32, as it reads them (16 bytes):
+//           the order of a contraction is free, and the query operand is
+//           permuted the same way;
 //   output  O^T (16 d x 8 heads) = V^T (A, 16 d x 16 keys) P^T (B)
 //           lane (g, t) holds keys 2t, 2t + 1, 2t + 8, 2t + 9, columns
-//           [g D / 8, + D / 8); byte permutes pair two keys of one column into
-//           an A register.
+//           [8 (8 h + g), + 8) for h < D / 64; byte permutes pair two keys of
+//           one column into an A register.
+//
+// In the ring, 16-byte column c of row r sits at c ^ 4 (r & 1) for K and at
+// c ^ (r & 6) for V, which spreads both read patterns over all banks.
 //
 // P enters the tensor core as a sum of two bf16 numbers (p = hi + lo, relative
 // error 2^-17), so that the output is rounded to bf16 once, at the end; the
 // second product costs 8 of 24 MMAs of a block that waits for memory anyway.
 // Scores, statistics and accumulators are fp32.
 //
-// Split over the key axis: the warps of a CTA, and the CTAs of a cluster (up
-// to kMaxWindowSplit), take a sequence's blocks in turn; their (m, l, O) are joined
-// in shared memory, then across the cluster through distributed shared memory.
-// So the call needs no workspace, and its result does not depend on timing.
+// Split over the key axis: the warps of a CTA, and the CTAs of a cluster, take
+// a sequence's blocks in turn; their (m, l, O) are joined in shared memory,
+// then across the cluster through distributed shared memory, always in the same
+// order: the call needs no workspace, and its bits do not depend on timing.
 #include <math.h>
 
 #include <algorithm>
@@ -58,27 +62,6 @@ constexpr float kFloor = -1e30f;
 constexpr float kMoveThreshold = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-struct Piece32 {
-  uint32_t w[8];
-};
-
-__device__ __forceinline__ Piece32 ld_stream32(const void* p) {
-  Piece32 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]),
-                 "=r"(v.w[6]), "=r"(v.w[7])
-               : "l"(reinterpret_cast<uint64_t>(p)));
-  return v;
-}
-
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(reinterpret_cast<uint64_t>(p)));
-  return v;
-}
-
 __device__ __forceinline__ float ld_dsmem(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
@@ -89,24 +72,33 @@ __device__ __forceinline__ float bf16_round(float x) {
   return __bfloat162float(__float2bfloat16(x));
 }
 
-// Shared memory: the warps' partial outputs [warps][8 heads][D], their maxima
-// and sums [warps][8] each, then the CTA's joined output [8][D], maxima [8]
-// and sums [8] (read by the cluster's other CTAs).
-template <int D>
-__host__ __device__ constexpr int window_smem_floats(int warps) {
-  return warps * (8 * D + 16) + 8 * D + 16;
-}
+constexpr int kStages = 3;  // blocks in flight per warp
+
+// Shared memory: the warps' rings [W][kStages][K, V][16 rows][D]; once a warp
+// has read its last block its outputs [8 heads][D] (fp32) take the front of its
+// ring, and those of the whole CTA the next part of warp 0's; maxima and sums
+// [W][8], and the CTA's [8], behind the rings.
+template <int D, int W>
+struct DecodePlan {
+  static constexpr int kStage = 2 * kBlockSize * D * 2;
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kStatOff = W * kRing;
+  static constexpr int kBytes = kStatOff + (W + 1) * 16 * 4;
+  static_assert(2 * 8 * D * 4 <= kRing, "outputs in the ring");
+};
 
 template <int D, int W>
-__global__ void __launch_bounds__(32 * W, 16 / W) decode_window_kernel(const WindowDecodeArgs a) {
-  constexpr int KJ = D / 64;  // 32-byte pieces of a K row per lane
-  constexpr int VW = D / 16;  // 32-bit words of a V row per lane
-  extern __shared__ __align__(16) float sm[];
-  float* const sm_o = sm;
-  float* const sm_m = sm_o + W * 8 * D;
+__global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecodeArgs a) {
+  using P = DecodePlan<D, W>;
+  constexpr int KJ = D / 32;  // 16-byte pieces of a K row per lane
+  constexpr int VH = D / 64;  // 16-byte pieces of a V row per lane
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kPart = P::kRing / 4;  // floats from one warp's outputs to the next
+  float* const sm_o = reinterpret_cast<float*>(smem);
+  float* const sm_m = reinterpret_cast<float*>(smem + P::kStatOff);
   float* const sm_l = sm_m + W * 8;
-  float* const cta_o = sm_l + W * 8;
-  float* const cta_m = cta_o + 8 * D;
+  float* const cta_o = sm_o + 8 * D;
+  float* const cta_m = sm_l + W * 8;
   float* const cta_l = cta_m + 8;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -122,16 +114,14 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_window_kernel(const Win
   griddep_wait();
 
   // q: head g of the group, the columns of this lane's K pieces
-  uint4 qf[KJ][2];
+  uint4 qf[KJ];
   const __nv_bfloat16* qrow =
       a.q + (static_cast<int64_t>(s) * a.num_q_heads + kvh * G + (g < G ? g : 0)) * D;
 #pragma unroll
-  for (int j = 0; j < KJ; ++j)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      qf[j][e] = *reinterpret_cast<const uint4*>(qrow + 16 * (4 * j + t) + 8 * e);
-      if (g >= G) qf[j][e] = make_uint4(0, 0, 0, 0);
-    }
+  for (int j = 0; j < KJ; ++j) {
+    qf[j] = *reinterpret_cast<const uint4*>(qrow + 8 * (4 * j + t));
+    if (g >= G) qf[j] = make_uint4(0, 0, 0, 0);
+  }
 
   int n = a.seq_lens[s];
   const int cap = a.max_blocks * kBlockSize;
@@ -149,13 +139,13 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_window_kernel(const Win
   const int first = rank * W + warp;
 
   const int64_t tok_bytes = static_cast<int64_t>(a.num_kv_heads) * D * 2;
-  const char* const kbase = reinterpret_cast<const char*>(a.k) + kvh * (D * 2) + t * 32;
-  const char* const vbase = reinterpret_cast<const char*>(a.v) + kvh * (D * 2) + g * (D / 4);
+  const char* const kbase = reinterpret_cast<const char*>(a.k) + kvh * (D * 2) + (lane % (D / 8)) * 16;
+  const char* const vbase = reinterpret_cast<const char*>(a.v) + kvh * (D * 2) + (lane % (D / 8)) * 16;
   const int32_t* const table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks;
 
-  float o[VW][4];
+  float o[4 * VH][4];
 #pragma unroll
-  for (int i = 0; i < VW; ++i)
+  for (int i = 0; i < 4 * VH; ++i)
 #pragma unroll
     for (int c = 0; c < 4; ++c) o[i][c] = 0.f;
   float m0 = kFloor, m1 = kFloor, l0 = 0.f, l1 = 0.f;  // heads 2t, 2t + 1
@@ -175,77 +165,72 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_window_kernel(const Win
       }
     }
   };
-  Piece32 kr[2][KJ];
-  uint32_t vr[4][VW];
-  auto load_k = [&](int id) {
-    const char* p = kbase + (static_cast<int64_t>(id) * kBlockSize + g) * tok_bytes;
-#pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-      for (int j = 0; j < KJ; ++j) {
-        if (id < 0)
-          kr[r][j] = Piece32{};
-        else
-          kr[r][j] = ld_stream32(p + r * 8 * tok_bytes + j * 128);
+  // Copies of this warp's next block into stage `st` (an empty group past its
+  // last one, so that the count of groups runs on).
+  const uint32_t ring = smem_u32(smem) + warp * P::kRing;
+  constexpr int kRowBytes = D * 2, kChunks = D / 8, kRowsPerCopy = 32 / kChunks;
+  const int crow = lane / kChunks, cchunk = lane % kChunks;
+  int load_vb = first, load_it = 0;
+  auto issue = [&](int st) {
+    if (load_vb < nv) {
+      if (load_it == 32) {
+        read_ids(load_vb);
+        load_it = 0;
       }
-  };
-  auto load_v = [&](int id) {
-    const char* p = vbase + (static_cast<int64_t>(id) * kBlockSize + 2 * t) * tok_bytes;
+      const int id = __shfl_sync(0xffffffffu, ids, load_it++);
+      load_vb += stride;
+      const int bytes = id < 0 ? 0 : 16;
+      const int64_t off = (static_cast<int64_t>(id < 0 ? 0 : id) * kBlockSize + crow) * tok_bytes;
+      const char* pk = kbase + off;
+      const char* pv = vbase + off;
+      const uint32_t dst = ring + st * P::kStage;
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const char* row = p + ((r & 1) + (r >> 1) * 8) * tok_bytes;
-      if constexpr (D == 128) {
-        const Piece32 x = id < 0 ? Piece32{} : ld_stream32(row);
+      for (int i = 0; i < kBlockSize / kRowsPerCopy; ++i) {
+        const int row = kRowsPerCopy * i + crow;
+        cp_async_16_zfill(dst + row * kRowBytes + ((cchunk ^ ((row & 1) << 2)) << 4),
+                          pk + i * kRowsPerCopy * tok_bytes, bytes);
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) vr[r][i] = x.w[i];
-      } else {
-        const uint4 x = id < 0 ? make_uint4(0, 0, 0, 0) : ld_stream(row);
-        vr[r][0] = x.x;
-        vr[r][1] = x.y;
-        vr[r][2] = x.z;
-        vr[r][3] = x.w;
+      for (int i = 0; i < kBlockSize / kRowsPerCopy; ++i) {
+        const int row = kRowsPerCopy * i + crow;
+        cp_async_16_zfill(dst + kBlockSize * kRowBytes + row * kRowBytes + ((cchunk ^ (row & 6)) << 4),
+                          pv + i * kRowsPerCopy * tok_bytes, bytes);
       }
     }
+    cp_async_commit();
   };
+  if (first < nv) read_ids(first);
+#pragma unroll
+  for (int st = 0; st < kStages; ++st) issue(st);
 
-  if (first < nv) {
-    read_ids(first);
-    int id = __shfl_sync(0xffffffffu, ids, 0);
-    load_k(id);
-    load_v(id);
-  }
-  int it = 0;  // position of this block's id in the batch of 32
+  int stage = 0;
   for (int vb = first; vb < nv; vb += stride) {
     const int j0 = real_block(vb) * kBlockSize;
+    cp_async_wait_group<kStages - 1>();
+    __syncwarp();
+    const uint32_t src = ring + stage * P::kStage + g * kRowBytes;
+    const uint32_t srcv = ring + stage * P::kStage + (kBlockSize + 2 * t) * kRowBytes;
     // ---- scores of 16 keys x 8 heads
-    float sc[4] = {0.f, 0.f, 0.f, 0.f};
+    float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < KJ; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t(&x)[8] = kr[0][j].w;
-        const uint32_t(&y)[8] = kr[1][j].w;
-        const uint32_t a0[4] = {x[4 * e], y[4 * e], x[4 * e + 1], y[4 * e + 1]};
-        mma_bf16_16816(sc, a0, qf[j][e].x, qf[j][e].y);
-        const uint32_t a1[4] = {x[4 * e + 2], y[4 * e + 2], x[4 * e + 3], y[4 * e + 3]};
-        mma_bf16_16816(sc, a1, qf[j][e].z, qf[j][e].w);
-      }
-    // ---- the next block's K
-    const int next = vb + stride;
-    int id = 0;
-    if (next < nv) {
-      if (++it == 32) {
-        read_ids(next);
-        it = 0;
-      }
-      id = __shfl_sync(0xffffffffu, ids, it);
-      load_k(id);
+    for (int j = 0; j < KJ; ++j) {
+      const uint32_t at = ((4 * j + t) ^ ((g & 1) << 2)) << 4;
+      const uint4 k0 = lds128(src + at), k1 = lds128(src + 8 * kRowBytes + at);
+      const uint32_t a0[4] = {k0.x, k1.x, k0.y, k1.y};
+      mma_bf16_16816(sc, a0, qf[j].x, qf[j].y);
+      const uint32_t a1[4] = {k0.z, k1.z, k0.w, k1.w};
+      mma_bf16_16816(sd, a1, qf[j].z, qf[j].w);
     }
+    uint4 vr[4][VH];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int h = 0; h < VH; ++h) vr[r][h] = lds128(srcv + ((r & 1) + (r >> 1) * 8) * kRowBytes + (((8 * h + g) ^ (2 * t)) << 4));
     // ---- mask (first or last block of the window, last block of the sinks):
     // hidden keys get weight 0 and their V rows, which may hold anything, 0
     const bool edge = !(j0 + kBlockSize <= n && (j0 >= lo || j0 + kBlockSize <= ns));
-    float x0 = sc[0] * a.scale_log2, x1 = sc[1] * a.scale_log2;
-    float x2 = sc[2] * a.scale_log2, x3 = sc[3] * a.scale_log2;
+    float x0 = (sc[0] + sd[0]) * a.scale_log2, x1 = (sc[1] + sd[1]) * a.scale_log2;
+    float x2 = (sc[2] + sd[2]) * a.scale_log2, x3 = (sc[3] + sd[3]) * a.scale_log2;
     if (edge) {
       auto seen = [&](int j) { return j < n && (j >= lo || j < ns); };
       if (!seen(j0 + g)) x0 = x1 = -INFINITY;
@@ -254,7 +239,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_window_kernel(const Win
       for (int r = 0; r < 4; ++r)
         if (!seen(j0 + 2 * t + (r & 1) + (r >> 1) * 8))
 #pragma unroll
-          for (int i = 0; i < VW; ++i) vr[r][i] = 0;
+          for (int h = 0; h < VH; ++h) vr[r][h] = make_uint4(0, 0, 0, 0);
     }
     // ---- reference maximum
     float b0 = fmaxf(x0, x2), b1 = fmaxf(x1, x3);
@@ -272,7 +257,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_window_kernel(const Win
       l0 *= s0;
       l1 *= s1;
 #pragma unroll
-      for (int i = 0; i < VW; ++i) {
+      for (int i = 0; i < 4 * VH; ++i) {
         o[i][0] *= s0;
         o[i][1] *= s1;
         o[i][2] *= s0;
@@ -289,17 +274,28 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_window_kernel(const Win
     const uint32_t lo0 = movmatrix_trans(pack_bf16x2(p0 - bf16_round(p0), p1 - bf16_round(p1)));
     const uint32_t lo1 = movmatrix_trans(pack_bf16x2(p2 - bf16_round(p2), p3 - bf16_round(p3)));
 #pragma unroll
-    for (int i = 0; i < VW; ++i) {
-      const uint32_t av[4] = {prmt(vr[0][i], vr[1][i], 0x5410), prmt(vr[0][i], vr[1][i], 0x7632),
-                              prmt(vr[2][i], vr[3][i], 0x5410), prmt(vr[2][i], vr[3][i], 0x7632)};
-      mma_bf16_16816(o[i], av, hi0, hi1);
-      mma_bf16_16816(o[i], av, lo0, lo1);
+    for (int h = 0; h < VH; ++h) {
+      const uint32_t r0[4] = {vr[0][h].x, vr[0][h].y, vr[0][h].z, vr[0][h].w};
+      const uint32_t r1[4] = {vr[1][h].x, vr[1][h].y, vr[1][h].z, vr[1][h].w};
+      const uint32_t r2[4] = {vr[2][h].x, vr[2][h].y, vr[2][h].z, vr[2][h].w};
+      const uint32_t r3[4] = {vr[3][h].x, vr[3][h].y, vr[3][h].z, vr[3][h].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t av[4] = {prmt(r0[i], r1[i], 0x5410), prmt(r0[i], r1[i], 0x7632),
+                                prmt(r2[i], r3[i], 0x5410), prmt(r2[i], r3[i], 0x7632)};
+        mma_bf16_16816(o[4 * h + i], av, hi0, hi1);
+        mma_bf16_16816(o[4 * h + i], av, lo0, lo1);
+      }
     }
-    // ---- the next block's V
-    if (next < nv) load_v(id);
+    // ---- the stage's next block (what was read from it is in registers)
+    __syncwarp();
+    issue(stage);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
   }
 
   // ---- join the CTA's warps
+  cp_async_wait_all();
+  __syncwarp();
 #pragma unroll
   for (int off = 4; off < 32; off <<= 1) {
     l0 += __shfl_xor_sync(0xffffffffu, l0, off);
@@ -312,13 +308,15 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_window_kernel(const Win
     sm_l[warp * 8 + 2 * t + 1] = l1;
   }
 #pragma unroll
-  for (int i = 0; i < VW; ++i) {
-    // rows g, g + 8 of the tile are columns (D / 8) g + 2 i, + 1
-    const int d = D / 8 * g + 2 * i;
-    float2* dst = reinterpret_cast<float2*>(sm_o + (warp * 8 + 2 * t) * D + d);
-    dst[0] = make_float2(o[i][0], o[i][2]);
-    dst[D / 2] = make_float2(o[i][1], o[i][3]);
-  }
+  for (int h = 0; h < VH; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // rows g, g + 8 of the tile are columns 8 (8 h + g) + 2 i, + 1
+      const int d = 8 * (8 * h + g) + 2 * i;
+      float2* dst = reinterpret_cast<float2*>(sm_o + warp * kPart + 2 * t * D + d);
+      dst[0] = make_float2(o[4 * h + i][0], o[4 * h + i][2]);
+      dst[D / 2] = make_float2(o[4 * h + i][1], o[4 * h + i][3]);
+    }
   __syncthreads();
   for (int e = threadIdx.x; e < G * D; e += 32 * W) {
     const int h = e / D, d = e % D;
@@ -329,7 +327,7 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_window_kernel(const Win
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       const float f = fast_exp2(sm_m[w * 8 + h] - m);
-      acc += f * sm_o[(w * 8 + h) * D + d];
+      acc += f * sm_o[w * kPart + h * D + d];
       l += f * sm_l[w * 8 + h];
     }
     if (splits == 1) {
@@ -368,11 +366,26 @@ __global__ void __launch_bounds__(32 * W, 16 / W) decode_window_kernel(const Win
 
 template <int D, int W>
 cudaError_t launch(const WindowDecodeArgs& a, cudaStream_t stream) {
+  {  // raise the kernel's shared-memory limit once per device
+    static std::mutex mu;
+    static bool set_for[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set_for[dev]) {
+      e = cudaFuncSetAttribute(decode_window_kernel<D, W>,
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, DecodePlan<D, W>::kBytes);
+      if (e != cudaSuccess) return e;
+      set_for[dev] = true;
+    }
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * a.num_kv_heads *
                                            a.splits));
   cfg.blockDim = dim3(32 * W);
-  cfg.dynamicSmemBytes = window_smem_floats<D>(W) * sizeof(float);
+  cfg.dynamicSmemBytes = DecodePlan<D, W>::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -387,88 +400,105 @@ cudaError_t launch(const WindowDecodeArgs& a, cudaStream_t stream) {
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-// Opts the eight-warp kernel into clusters of 16; whether one would fit.
+// How many clusters of 1, 2, 4, 8 and 16 eight-warp CTAs the device runs at
+// once (the last is not portable: 0 where the device or a partition of it
+// cannot); asked once per device.
+struct Residency {
+  bool ready = false;
+  int clusters[5] = {};
+};
+
 template <int D>
-bool allow_16() {
-  if (cudaFuncSetAttribute(decode_window_kernel<D, 8>, cudaFuncAttributeNonPortableClusterSizeAllowed,
-                           1) != cudaSuccess)
-    return false;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(16);
-  cfg.blockDim = dim3(32 * 8);
-  cfg.dynamicSmemBytes = window_smem_floats<D>(8) * sizeof(float);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 16;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int clusters = 0;
-  return cudaOccupancyMaxActiveClusters(&clusters, decode_window_kernel<D, 8>, &cfg) ==
-             cudaSuccess &&
-         clusters > 0;
-}
-
-}  // namespace
-
-cudaError_t launch_decode_window(WindowDecodeArgs a, int head_dim, int num_sms,
-                                 cudaStream_t stream) {
-  // Largest cluster that this device runs: 16, if the kernels that use it have
-  // opted in and a cluster fits; else the portable 8.  Asked once per device.
+cudaError_t residency(int num_sms, Residency* out) {
   static std::mutex mu;
-  static int most_for[64] = {};
-  int dev = 0, most_split = 0;
+  static Residency by_device[64];
+  int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  {
-    std::lock_guard<std::mutex> lock(mu);
-    if (most_for[dev] == 0) {
-      const bool ok = allow_16<128>() && allow_16<64>();
-      cudaGetLastError();
-      most_for[dev] = ok ? kMaxWindowSplit : 8;
+  std::lock_guard<std::mutex> lock(mu);
+  Residency& r = by_device[dev];
+  if (!r.ready) {
+    constexpr int smem = DecodePlan<D, 8>::kBytes;
+    const auto kernel = decode_window_kernel<D, 8>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    int ctas = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&ctas, kernel, 32 * 8, smem);
+    if (e != cudaSuccess) return e;
+    r.clusters[0] = ctas * num_sms;
+    const bool wide = cudaFuncSetAttribute(
+                          kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+    for (int k = 1; k < 5; ++k) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(1 << k);
+      cfg.blockDim = dim3(32 * 8);
+      cfg.dynamicSmemBytes = smem;
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = 1 << k;
+      attr[0].val.clusterDim.y = 1;
+      attr[0].val.clusterDim.z = 1;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      int n = 0;
+      if ((k == 4 && !wide) || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+      r.clusters[k] = n;
     }
-    most_split = most_for[dev];
+    cudaGetLastError();  // (a size that the device refuses is no error here)
+    r.ready = true;
   }
+  *out = r;
+  return cudaSuccess;
+}
+
+template <int D>
+cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
+  Residency res;
+  const cudaError_t e = residency<D>(num_sms, &res);
+  if (e != cudaSuccess) return e;
   // Blocks that a sequence can attend at most.
   const int64_t visible = std::min<int64_t>(
       a.max_blocks, (static_cast<int64_t>(a.sinks) + kBlockSize - 1) / kBlockSize +
                         (static_cast<int64_t>(a.window) + kBlockSize - 1) / kBlockSize + 1);
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
-  const int64_t slots = static_cast<int64_t>(num_sms) * 16;  // warps, at 128 registers a thread
-  int w = 8;
   a.splits = 1;
-  if (units * 16 > slots - 64) {
-    // Many units: as many warps each as let all of them run at once, for a unit
-    // costs 4 us before its first block arrives (256 sequences x 8 heads x 1024
-    // keys: 163 us with one warp per unit, 176 with two, 189 with eight; 64
-    // sequences: 94, 70, 49 with four, 53 with eight).  Windows of many blocks
-    // pay that less, and lengths that differ spread further over them: eight
-    // (256 x 4096: one warp 617 us, eight 648; with lengths from 300 on, 446 and
-    // 343).
-    if (visible <= 160)
-      while (w > 1 && (units * w > slots || w >= 2 * visible)) w /= 2;
-  } else {
-    // Few units: clusters of CTAs, as many warps as there are slots or blocks,
-    // in small CTAs while 16 warps do (148 units of 64 blocks: 4 x 4 warps 6.4
-    // us, 2 x 8 6.9, 1 x 8 8.0; 32 units of 2050 blocks: 8 x 8 88 us, 4 x 8 130).
-    // Clusters of 16 where one CTA per SM suffices and eight CTAs' warps would
-    // have four blocks or more each (8 units of 2050 blocks: 40 us, with 8 CTAs
-    // 61; but 16 units 77 and 70, and 8 units of 66 blocks 8.0 and 6.9).
-    const int64_t warps = std::min<int64_t>(visible, slots / units);
-    w = warps > 16 ? 8 : 4;
-    while (a.splits * w < visible && 2 * a.splits * w * units <= slots &&
-           (a.splits < 8 || (a.splits < most_split && 2 * a.splits * units <= num_sms &&
-                             4 * a.splits * w <= visible)))
-      a.splits *= 2;
+  if (units <= res.clusters[0]) {
+    // Few units: eight warps each, and as large clusters of such CTAs as all run
+    // at once and find a block for every warp; none for a few blocks, whose
+    // joining costs more (us, at 8 / 16 / 32 / 64 units: 17 blocks 4.7 / 4.8 /
+    // 4.8 / 4.8 with one CTA, 4.8 to 5.7 with clusters; 66 blocks 8.6 / 9.0 /
+    // 8.9 / 9.8 with one, 5.8 / 6.2 / 6.4 / 9.3 with clusters of 8, 4, 4, 2).
+    if (visible > 24)
+      for (int k = 1; k < 5; ++k)
+        if (units <= res.clusters[k] && (8 << k) <= visible) a.splits = 1 << k;
+    return launch<D, 8>(a, stream);
+  }
+  // Many units: a unit costs some 4 us before its first block arrives, which
+  // many short units at once hide better than few long ones; long units hide it
+  // themselves, and eight warps on each spread lengths that differ.  (us, with
+  // 1 / 2 / 4 / 8 warps: 1024 units of 17 blocks 28 / 29 / 33 / 39; of 66 90 /
+  // 82 / 85 / 88, with lengths from 300 keys on 75 / 72 / 69 / 70; 2048 units of
+  // 258 622 / 600 / 601 / 588, ragged 328 / 313 / 298 / 291.)
+  const int64_t slots = static_cast<int64_t>(res.clusters[0]) * 8;
+  int w = 8;
+  if (visible < 120) {
+    const int least = visible > 32 ? 2 : 1;
+    while (w > least && units * w > slots) w /= 2;
   }
   switch (w) {
-    case 1: return head_dim == 128 ? launch<128, 1>(a, stream) : launch<64, 1>(a, stream);
-    case 2: return head_dim == 128 ? launch<128, 2>(a, stream) : launch<64, 2>(a, stream);
-    case 4: return head_dim == 128 ? launch<128, 4>(a, stream) : launch<64, 4>(a, stream);
-    default: return head_dim == 128 ? launch<128, 8>(a, stream) : launch<64, 8>(a, stream);
+    case 1: return launch<D, 1>(a, stream);
+    case 2: return launch<D, 2>(a, stream);
+    case 4: return launch<D, 4>(a, stream);
+    default: return launch<D, 8>(a, stream);
   }
+}
+
+}  // namespace
+
+cudaError_t launch_decode_window(const WindowDecodeArgs& a, int head_dim, int num_sms,
+                                 cudaStream_t stream) {
+  return head_dim == 128 ? choose<128>(a, num_sms, stream) : choose<64>(a, num_sms, stream);
 }
 
 }  // namespace pa
