@@ -21,9 +21,9 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpa.so")
 PYCALL = os.path.join(PKG, "_pycall.so")  # CPython extension: argument marshalling
 SOURCES = ["pa_api.cu", "pa_decode.cu", "pa_prefill.cu", "pa_hybrid.cu", "pa_cascade.cu",
-           "pa_rope.cu", "pa_window_decode.cu",
-           "pa_window_prefill.cu", "pa_block_manager.cpp"]
-HEADERS = ["pa_internal.h", "pa_ptx.cuh", "pa_decode_body.cuh", "pa_prefill_body.cuh", os.path.join("..", "..", "include", "pa.h"),
+           "pa_rope.cu", "pa_window_decode.cu", "pa_window_prefill.cu", "pa_block_manager.cpp"]
+HEADERS = ["pa_internal.h", "pa_ptx.cuh", "pa_decode_body.cuh", "pa_prefill_body.cuh",
+           "pa_window.h", "pa_window_ptx.cuh", os.path.join("..", "..", "include", "pa.h"),
            os.path.join("..", "..", "include", "pa_block_manager.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]

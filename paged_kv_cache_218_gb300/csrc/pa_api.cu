@@ -15,6 +15,7 @@
 #include "../../include/pa.h"
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
+#include "pa_window.h"
 
 namespace pa {
 namespace {

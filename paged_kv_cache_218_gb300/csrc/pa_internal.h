@@ -114,12 +114,6 @@ struct PrefillArgs {
   __nv_bfloat16* v_pool;
 };
 
-// Prefill chunks under a sliding window and sinks (pa_prefill_window).
-struct WindowPrefillArgs : PrefillArgs {
-  int window;  // a query at p sees keys (p - window, p]
-  int sinks;   // and keys [0, sinks)
-};
-
 struct CascadeArgs {
   const __nv_bfloat16* q;        // [S, Hq, 128]
   const int32_t* seq_lens;       // [S]
@@ -147,59 +141,6 @@ struct CascadeArgs {
   float scale_log2;
 };
 
-// Decode over a sliding window and sinks (pa_decode_window).
-struct WindowDecodeArgs {
-  __nv_bfloat16* out;           // [S, Hq, D]
-  const __nv_bfloat16* q;       // [S, Hq, D]
-  const __nv_bfloat16* k;       // pools
-  const __nv_bfloat16* v;
-  const int32_t* block_tables;  // [S, max_blocks]
-  const int32_t* seq_lens;      // [S]
-  float* out_lse;               // [S, Hq] or null
-  unsigned int* err;
-  int64_t num_blocks;
-  int max_blocks;
-  int num_seqs;
-  int num_q_heads;
-  int num_kv_heads;
-  int group;
-  int window;  // keys [len - window, len) are visible,
-  int sinks;   // and keys [0, sinks)
-  float scale_log2;
-  int splits;  // CTAs (a cluster) per (sequence, kv head); set by the launcher
-};
-
-// Norms, position rotation and slot scatter (pa_qk_norm_rope_cache).
-struct RopeArgs {
-  __nv_bfloat16* q_out;      // [T, Hq, D]
-  __nv_bfloat16* k_out;      // [T, Hkv, D] or null
-  const __nv_bfloat16* q;    // rows at token strides (elements)
-  const __nv_bfloat16* k;
-  const __nv_bfloat16* v;
-  int64_t q_stride, k_stride, v_stride;
-  const float* q_weight;     // [D] or null (no norm)
-  const float* k_weight;
-  const int64_t* positions;  // [T]
-  const int64_t* increments; // [rot_dim / 2], 2^-64 turns per position
-  const int64_t* slots;      // [T]
-  void* k_cache;             // pools, or both null
-  void* v_cache;
-  const float* k_scales;     // E4M3 pools: [Hkv]
-  const float* v_scales;
-  unsigned int* err;
-  int64_t num_slots;
-  float eps;
-  float rope_factor;
-  int num_tokens;
-  int num_q_heads;
-  int num_kv_heads;
-  int head_dim;
-  int rot_dim;
-  int interleaved;
-};
-
-constexpr int kMaxWindowSplit = 16;  // CTAs of a cluster, where the device allows it
-
 constexpr int kMaxPrefixParts = 4;  // cascade: most CTAs per (group, kv-head subset)
 
 // Balanced-mode workspace layout (shared by the size query and the launch):
@@ -216,18 +157,11 @@ bool decode_supported(int head_dim, int num_kv_heads, int num_q_heads, int mode,
 cudaError_t launch_merge(const MergeArgs& a, cudaStream_t stream);
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
                            const CUtensorMap* tm_v, int grid_tiles, cudaStream_t stream);
-cudaError_t launch_prefill_window(const WindowPrefillArgs& a, const CUtensorMap* tm_q,
-                                  const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                  const CUtensorMap* tm_o, int64_t max_items, int num_sms,
-                                  cudaStream_t stream);
 size_t prefill_smem_bytes();
 bool cascade_shape(int num_kv_heads, int group, int max_group, int* kv_per_cta, int* warps_per_kv,
                    int* stages);
 cudaError_t launch_cascade_prefix(const CascadeArgs& a, const CUtensorMap* tm_k,
                                   const CUtensorMap* tm_v, cudaStream_t stream);
-cudaError_t launch_norm_rope(const RopeArgs& a, bool kv_fp8, int num_sms, cudaStream_t stream);
-cudaError_t launch_decode_window(const WindowDecodeArgs& a, int head_dim, int num_sms,
-                                 cudaStream_t stream);
 // One launch for a hybrid batch: the balanced decode (bf16, head_dim 128) on
 // its first decode_ctas CTAs and the prefill's CTA pairs on the rest.
 // append: the decode role writes its sequences' new tokens (d.new_k) and the

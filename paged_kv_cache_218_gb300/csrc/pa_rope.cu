@@ -30,8 +30,8 @@
 #include <math.h>
 
 #include "../../include/pa.h"
-#include "pa_internal.h"
-#include "pa_ptx.cuh"
+#include "pa_window.h"
+#include "pa_window_ptx.cuh"
 
 namespace pa {
 namespace {

@@ -48,8 +48,8 @@
 #include <mutex>
 
 #include "../../include/pa.h"
-#include "pa_internal.h"
-#include "pa_ptx.cuh"
+#include "pa_window.h"
+#include "pa_window_ptx.cuh"
 
 namespace pa {
 namespace {
@@ -407,6 +407,7 @@ struct Residency {
   bool ready = false;
   int clusters[5] = {};
 };
+static_assert(kMaxWindowSplit == 1 << 4, "cluster sizes");
 
 template <int D>
 cudaError_t residency(int num_sms, Residency* out) {

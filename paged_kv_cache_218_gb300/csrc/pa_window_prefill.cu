@@ -41,6 +41,8 @@
 #include <type_traits>
 
 #include "pa_prefill_body.cuh"
+#include "pa_window.h"
+#include "pa_window_ptx.cuh"
 
 namespace pa {
 namespace pre {
