@@ -414,7 +414,7 @@ const char* pa_status_string(int status) {
   }
 }
 
-int pa_version(void) { return (1 << 16) | 0; }
+int pa_version(void) { return (1 << 16) | 1; }
 
 int pa_reshape_and_cache(const void* key, const void* value, int64_t key_token_stride,
                          int64_t value_token_stride, void* k_cache, void* v_cache,
@@ -1463,16 +1463,14 @@ static int prefill_window_impl(void* out, const void* q, const void* k_cache, co
   if ((static_cast<int64_t>(total_q_tokens) + 2 * tokens_per_tile - 1) / (2 * tokens_per_tile) *
           num_kv_heads > INT32_MAX)
     return PA_ERR_UNSUPPORTED;
-  CUtensorMap tm_q, tm_k, tm_v, tm_o;
-  // outputs leave in a warp's 32 rows at a time
+  CUtensorMap tm_q, tm_k, tm_v;
   if (encode_q_map(&tm_q, q, total_q_tokens, num_q_heads, head_dim, a.group, tokens_per_tile) ||
-      encode_q_map(&tm_o, out, total_q_tokens, num_q_heads, head_dim, a.group, 32 / a.group) ||
       encode_pool_map(&tm_k, k_cache, num_blocks, num_kv_heads, head_dim, kPoolKeyTile) ||
       encode_pool_map(&tm_v, v_cache, num_blocks, num_kv_heads, head_dim, kPool2D))
     return PA_ERR_CUDA;
   const int64_t items = (static_cast<int64_t>(max_q_len) + 2 * tokens_per_tile - 1) /
                                  (2 * tokens_per_tile) * num_chunks * num_kv_heads;
-  return launch_prefill_window(a, &tm_q, &tm_k, &tm_v, &tm_o, items, d->num_sms,
+  return launch_prefill_window(a, &tm_q, &tm_k, &tm_v, items, d->num_sms,
                                         static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;

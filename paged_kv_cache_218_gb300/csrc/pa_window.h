@@ -72,7 +72,6 @@ cudaError_t launch_decode_window(const WindowDecodeArgs& a, int head_dim, int nu
                                  cudaStream_t stream);
 cudaError_t launch_prefill_window(const WindowPrefillArgs& a, const CUtensorMap* tm_q,
                                   const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                  const CUtensorMap* tm_o, int64_t max_items, int num_sms,
-                                  cudaStream_t stream);
+                                  int64_t max_items, int num_sms, cudaStream_t stream);
 
 }  // namespace pa

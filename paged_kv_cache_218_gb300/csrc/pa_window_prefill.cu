@@ -30,9 +30,10 @@
 //    the other roles read.  Block ids of the next item are fetched while the
 //    last one's tiles load, and the softmax writes P of an item's first tile
 //    before it turns to the output of the item before, whose last product is
-//    then done.  Outputs leave through shared memory and a tensor store per warp
-//    (written straight from the registers, a row per lane, they took 1.6 us per
-//    item).
+//    then done.  Outputs are turned around in shared memory, so that a store
+//    instruction covers whole 128-byte lines (written straight from the
+//    registers, a row per lane, they took 1.6 us per item; as a tensor store
+//    per warp, 0.8, half of it the proxy fence and the issue).
 //
 // What bounds it: the tensor pipe and, at 128 x 128 tiles, the softmax that
 // feeds it (one exponential per score).
@@ -191,8 +192,7 @@ __device__ __forceinline__ uint64_t low_bits(int k) {
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_window_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
-                          const __grid_constant__ CUtensorMap tm_v,
-                          const __grid_constant__ CUtensorMap tm_o, const WindowPrefillArgs a) {
+                          const __grid_constant__ CUtensorMap tm_v, const WindowPrefillArgs a) {
   using P = WPlan;
   constexpr int kNK = P::kNK, kNV = P::kNV;
   extern __shared__ uint8_t smem_raw[];
@@ -620,17 +620,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // The output of an item, written once its last PV is done: O / l -> bf16,
     // and lse.  The next item's first PV, which overwrites O, waits for this
-    // warp's arrival on p_full behind these loads of O.  A warp's 32 rows, if
-    // all are tokens of the chunk, go to its part of the staging tile and from
-    // there by one tensor store.  The barrier in it also hands over the key
-    // tiles of the item after the one at hand (go_flag 0 .. 7; -1: not
-    // published yet).
+    // warp's arrival on p_full behind these loads of O.  The barrier in it also
+    // hands over the key tiles of the item after the one at hand (go_flag 0 ..
+    // 7; -1: not published yet).
     const int tok = r / G, warp_toks = 32 / G;
     const uint32_t stage = sbase + P::kOutOff + hc * kHalf + qd * 32 * 128;
     bool pending = false;
-    int64_t out_row = 0;       // of the pending item's row; < 0: not stored
-    bool out_whole = false;    // all rows of this warp are
-    int out_y = 0, out_z = 0;  // first head and token of this warp's rows
+    int64_t out_row = 0;            // of the pending item: the warp's first row, [token][head],
+    int out_toks = 0;               // and how many of its tokens exist (<= 0: none)
     float out_m = 0.f, out_l = 0.f;
     uint32_t out_bar = 0, out_phase = 0;  // PV of its last tile
     auto write_out = [&](int k) {
@@ -646,32 +643,36 @@ __global__ void __launch_bounds__(kThreads, 1)
       named_barrier(1 + qd, 64);
       const float l_tot = out_l + red_sum[(hc ^ 1) * 128 + r];
       const float inv = l_tot == 0.f ? 0.f : 1.f / l_tot;  // a NaN sum stays visible
-      uint32_t pk[32];
+      const uint64_t inv2 = f32x2(inv, inv);
+      // 16-byte column q of row `lane` goes to q ^ (lane & 7)
 #pragma unroll
-      for (int i = 0; i < 64; i += 2)
-        pk[i / 2] = pack_bf16x2(__uint_as_float(v[i]) * inv, __uint_as_float(v[i + 1]) * inv);
-      const bool good = !warp_flag(abort_flag);
-      if (out_whole && good) {
-        if (lane == 0) bulk_wait_read();  // the last item's store, long done
-        __syncwarp();
+      for (int q = 0; q < 8; ++q) {
+        uint32_t pk[4];
 #pragma unroll
-        for (int q = 0; q < 8; ++q)  // 16-byte columns in the 128-byte swizzle
-          sts128(stage + lane * 128 + ((q ^ (lane & 7)) << 4),
-                 make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]));
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          tma_store_3d(&tm_o, hc * 64, out_y, out_z, stage);
-          bulk_commit_group();
+        for (int i = 0; i < 4; ++i) {
+          const int e = 8 * q + 2 * i;
+          const float2 x =
+              f32x2_parts(mul2(f32x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), inv2));
+          pk[i] = pack_bf16x2(x.x, x.y);
         }
-      } else if (out_row >= 0 && good) {
-        uint4* dst = reinterpret_cast<uint4*>(a.out + out_row * 128 + hc * 64);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          dst[q] = make_uint4(pk[4 * q], pk[4 * q + 1], pk[4 * q + 2], pk[4 * q + 3]);
+        sts128(stage + lane * 128 + ((q ^ (lane & 7)) << 4), make_uint4(pk[0], pk[1], pk[2], pk[3]));
       }
-      if (out_row >= 0 && good && hc == 0 && a.out_lse)
-        a.out_lse[out_row] = l_tot == 0.f ? -INFINITY : (out_m + __log2f(l_tot)) * kLn2;
+      __syncwarp();
+      const bool good = !warp_flag(abort_flag);
+      // four rows at a time, eight lanes on the 128 bytes of each
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = 4 * i + lane / 8, t = row / G;
+        const uint4 x = lds128(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
+        if (good && t < out_toks)
+          *reinterpret_cast<uint4*>(
+              a.out + (out_row + static_cast<int64_t>(t) * a.num_q_heads + (row - t * G)) * 128 +
+              hc * 64 + (lane & 7) * 8) = x;
+      }
+      if (good && hc == 0 && a.out_lse && lane / G < out_toks)
+        a.out_lse[out_row + static_cast<int64_t>(lane / G) * a.num_q_heads + lane % G] =
+            l_tot == 0.f ? -INFINITY : (out_m + __log2f(l_tot)) * kLn2;
+      __syncwarp();  // the staging rows may be written again
       return *go;
     };
 
@@ -697,10 +698,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int shift = (it.b_first - it.nsb) * kBlockSize;
       const int pos = p0 + t0 + tok;
       const int tv = min(it.qlen - t0, tpt);  // tokens of this tile (<= 0: none)
-      const int row_y = it.kvh * G, row_z = it.q0 + t0 + qd * warp_toks;
+      const int first_tok = t0 + qd * warp_toks;  // of this warp
       const int64_t row =
-          tok < tv ? static_cast<int64_t>(it.q0 + t0 + tok) * a.num_q_heads + row_y + (r - tok * G)
-                   : -1;
+          static_cast<int64_t>(it.q0 + first_tok) * a.num_q_heads + it.kvh * G;
       // last and first visible virtual key of the row's window
       const int hi = min(pos, kmax - 1) - shift;
       const int lo = max(0, pos - (a.window - 1)) - shift;
@@ -798,15 +798,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       out_phase = b3 == 0 ? s_phase ^ 1 : s_phase;
       pending = true;
       out_row = row;
-      out_whole = (qd + 1) * warp_toks <= tv;
-      out_y = row_y;
-      out_z = row_z;
+      out_toks = tv - qd * warp_toks;
       out_m = m_run;
       out_l = l_run;
       nkt = next_nkt;
     }
     if (pending) write_out(0);
-    if (lane == 0) bulk_wait_done();
   }
   tc_fence_before();
   cluster_sync();  // neither CTA leaves while the other may still report to it
@@ -820,8 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 using namespace pre;
 
 cudaError_t launch_prefill_window(const WindowPrefillArgs& args, const CUtensorMap* tm_q,
-                                  const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                  const CUtensorMap* tm_o, int64_t max_items, int num_sms, cudaStream_t stream) {
+                                  const CUtensorMap* tm_k, const CUtensorMap* tm_v, int64_t max_items, int num_sms, cudaStream_t stream) {
   WindowPrefillArgs a = args;
   if (a.wait_ns == 0) a.wait_ns = kWaitLimitNs;
   constexpr int smem = WPlan::kSmemBytes + 1024;
@@ -855,7 +851,7 @@ cudaError_t launch_prefill_window(const WindowPrefillArgs& args, const CUtensorM
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, prefill_window_kernel, *tm_q, *tm_k, *tm_v, *tm_o, a);
+  e = cudaLaunchKernelEx(&cfg, prefill_window_kernel, *tm_q, *tm_k, *tm_v, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -1,33 +1,11 @@
 // pa_window_ptx.cuh -- inline-PTX wrappers of the windowed-attention and
-// norm-rotation kernels, beside pa_ptx.cuh's: packed fp32 arithmetic, tensor
-// stores, groups of asynchronous copies.
+// norm-rotation kernels, beside pa_ptx.cuh's: packed fp32 arithmetic, groups
+// of asynchronous copies.
 #pragma once
 
 #include "pa_ptx.cuh"
 
 namespace pa {
-
-// 3-D tiled tensor store from shared memory, in the thread's bulk group; the
-// commit that closes the group; and the waits until every committed group has
-// read its shared memory, or is complete.
-__device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int z, uint32_t src) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-                   reinterpret_cast<uint64_t>(tmap)),
-               "r"(x), "r"(y), "r"(z), "r"(src)
-               : "memory");
-}
-
-__device__ __forceinline__ void bulk_commit_group() {
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-
-__device__ __forceinline__ void bulk_wait_read() {
-  asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-
-__device__ __forceinline__ void bulk_wait_done() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
 
 // 16 bytes past L1, or zeros where `bytes` is 0 (then nothing is read); groups
 // of them, and the wait until at most N of this thread's groups are pending.
