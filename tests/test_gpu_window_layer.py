@@ -134,3 +134,36 @@ def test_chunks_then_decode_steps(pa, cuda_device, Hq, Hkv, window, sinks, inter
     assert pa.pa_device_error_flags() == 0
     # the prompts' middles were given back on the way
     assert (man.tables[0, :(done[0] - window) // 16] < 0).sum() > 0
+
+
+def test_first_calls_of_a_process_may_be_captured(cuda_device):
+    """Nothing that a first call sets up is forbidden while a graph is captured."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from paged_kv_cache_218_gb300 import binding as pa
+T, Hq, Hkv, D = 64, 8, 2, 128
+r = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+q, k, kc, vc = r(T, Hq, D), r(T, Hkv, D), r(8, 16, Hkv, D), r(8, 16, Hkv, D)
+bt, pos = torch.arange(4, dtype=torch.int32, device="cuda")[None], torch.arange(T, device="cuda")
+inc = pa.pa_rope_increments(D)[0].cuda()
+lens, cu, start = i(T), i(0, T), i(0)
+outs = [torch.zeros_like(q), torch.zeros_like(q), torch.zeros_like(q[:1])]
+last = q[-1:].contiguous()
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    pa.pa_decode_window(outs[2], last, kc, vc, bt, lens, 33, 2, 0.1)
+    pa.pa_prefill_window(outs[1], q, kc, vc, bt, cu, start, lens, T, 33, 2, 0.1)
+    pa.pa_qk_norm_rope_cache(outs[0], q, k, k, pos, inc, kc, vc, pos)
+g.replay()
+torch.cuda.synchronize()
+assert all(o.abs().sum() > 0 for o in outs) and pa.pa_device_error_flags() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
