@@ -488,7 +488,7 @@ int pa_rope_increments(int64_t *increments, float *rope_factor, int rot_dim, dou
  *              Both pools NULL: no scatter (v and slot_mapping unused), and
  *              k_out is required
  * head_dim: a multiple of 16 up to 256; rot_dim: a multiple of 16 up to
- * head_dim; any head counts.  Outputs may not overlap inputs otherwise than
+ * head_dim; up to 32768 heads of each kind.  Outputs may not overlap inputs otherwise than
  * as stated (PA_ERR_INVALID).
  */
 int pa_qk_norm_rope_cache(void *q_out, void *k_out, const void *q, const void *k, const void *v,

@@ -42,6 +42,7 @@
 // a sequence's blocks in turn; their (m, l, O) are joined in shared memory,
 // then across the cluster through distributed shared memory, always in the same
 // order: the call needs no workspace, and its bits do not depend on timing.
+#include <float.h>
 #include <math.h>
 
 #include <algorithm>
@@ -54,9 +55,9 @@
 namespace pa {
 namespace {
 
-// Lowest reference maximum (log2 units): a row whose scores are all -inf keeps
-// it, so its weights are 0 rather than NaN.
-constexpr float kFloor = -1e30f;
+// Lowest reference maximum (log2 units), the lowest finite fp32: a row whose
+// scores are all -inf keeps it, so its weights are 0 rather than NaN.
+constexpr float kFloor = -FLT_MAX;
 // The reference maximum moves only when a score passes it by this much (log2
 // units): p stays below 2^8 and most blocks need no cross-lane maximum.
 constexpr float kMoveThreshold = 8.f;

@@ -95,6 +95,18 @@ def test_scores_that_fall_far(pa, cuda_device):
     check(pa, [330], 2, 1, 64, 330, 0, cuda_device, scale=1.0, mutate=fall)
 
 
+@pytest.mark.parametrize("ahead", [0, 1])
+def test_scores_near_the_lowest_fp32(pa, cuda_device, ahead):
+    """All products and sums are powers of two, so equal scores (-2^126) stay
+    equal: weights 1 each, or all on the one key whose score is half as low."""
+    def low(q, kc, vc, bt, sl):
+        q.fill_(2.0**100)
+        kc[:] = -2.0**20
+        if ahead:
+            kc[bt[0, 2].long(), 5] = -2.0**19
+    check(pa, [64], 2, 1, 64, 64, 0, cuda_device, scale=1.0, mutate=low)
+
+
 def test_infinite_keys_take_or_lose_all_weight(pa, cuda_device):
     x = make([40], 2, 1, 64, 40, 0, 1, cuda_device)
     q, kc, vc, bt, sl = x

@@ -136,6 +136,44 @@ def test_chunks_then_decode_steps(pa, cuda_device, Hq, Hkv, window, sinks, inter
     assert (man.tables[0, :(done[0] - window) // 16] < 0).sum() > 0
 
 
+def test_offsets_past_32_bits(pa, cuda_device):
+    """Pools of more than 2^32 elements, of which the layer uses the last
+    blocks, and a query tensor whose used rows lie past 2^31 elements: the
+    bits of the same calls on a few blocks and rows."""
+    Hq, Hkv, D, T, window, sinks = 16, 8, 128, 90, 40, 3
+    g = torch.Generator(device=cuda_device)
+    g.manual_seed(12)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=cuda_device).bfloat16()  # noqa: E731
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    q, k, v, w = rnd(T, Hq, D), rnd(T, Hkv, D), rnd(T, Hkv, D), torch.ones(D, device=cuda_device)
+    pos = torch.arange(T, device=cuda_device)
+    inc = pa.pa_rope_increments(D)[0].to(cuda_device)
+
+    def run(blocks, first, stride):
+        kc = torch.empty(blocks, 16, Hkv, D, dtype=torch.bfloat16, device=cuda_device)
+        vc = torch.empty_like(kc)
+        tail = blocks - 6
+        kc[tail:], vc[tail:] = 0, 0
+        table = torch.arange(blocks - 1, tail - 1, -1, dtype=torch.int32, device=cuda_device)[None]
+        slots = table[0, pos // 16].long() * 16 + pos % 16
+        wide = torch.empty(T, stride, dtype=torch.bfloat16, device=cuda_device)
+        qs = wide[:, first:first + Hq * D].unflatten(1, (Hq, D))
+        qs.copy_(q)
+        rot, out, last = torch.empty_like(q), torch.empty_like(q), torch.empty_like(q[:1])
+        pa.pa_qk_norm_rope_cache(rot, qs, k, v, pos, inc, kc, vc, slots, w, w)
+        pa.pa_prefill_window(out, rot, kc, vc, table, i32(0, T), i32(0), i32(T), T, window, sinks,
+                             0.09)
+        pa.pa_decode_window(last, rot[-1:].contiguous(), kc, vc, table, i32(T), window, sinks, 0.09)
+        torch.cuda.synchronize()
+        return rot, kc[tail:].clone(), vc[tail:].clone(), out, last
+
+    small = run(6, 0, Hq * D)
+    far = run(2**18 + 100, 2**24, 2**25)
+    assert pa.pa_device_error_flags() == 0
+    for a, b in zip(small, far):
+        assert torch.equal(a, b)
+
+
 def test_first_calls_of_a_process_may_be_captured(cuda_device):
     """Nothing that a first call sets up is forbidden while a graph is captured."""
     import os
