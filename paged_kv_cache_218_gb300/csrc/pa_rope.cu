@@ -234,8 +234,8 @@ __global__ void __launch_bounds__(128, F8 ? 5 : 6) norm_rope_kernel(const RopeAr
     float c[NA], s[NA];
 #pragma unroll
     for (int e = 0; e < NA; ++e) {
-      const uint64_t inc = rot ? static_cast<uint64_t>(a.increments[i * 8 + (sub * NA + e) % 8]) : 0;
-      const uint64_t phase = static_cast<uint64_t>(pos) * inc;
+      const int64_t inc = rot ? a.increments[i * 8 + (sub * NA + e) % 8] : 0;
+      const uint64_t phase = static_cast<uint64_t>(pos) * static_cast<uint64_t>(inc);
       __sincosf(static_cast<float>(static_cast<int32_t>(phase >> 32)) * kPiOver2to31, &s[e], &c[e]);
       c[e] *= a.rope_factor;
       s[e] *= a.rope_factor;

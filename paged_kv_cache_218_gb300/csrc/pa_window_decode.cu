@@ -15,10 +15,10 @@
 // instruction takes whole rows (two of 256 bytes), so each 128-byte line is
 // asked for once.  The ring is the warp's own, so the warp alone waits for it,
 // and 192 KB per SM are on their way.  At 256 sequences x 4096 keys this reads
-// 7.2 TB/s (measured copy rate: 6.8).  What it replaced, at the same case: rows
+// 7.1 TB/s (measured copy rate: 6.8).  What it replaced, at the same case: rows
 // loaded straight into the MMA's registers, 16 bytes a lane and so 64 of a K
 // row at a time, 688 us; 32 bytes a lane 645; lane-private copies of 16 bytes
-// through shared memory, again 64 of a row at a time, 742; this 590.
+// through shared memory, again 64 of a row at a time, 742; this 590 to 613.
 //
 //   scores  S^T (16 keys x 8 heads) = K (A, 16 keys x 16 d) Q^T (B)
 //           lane (g, t) = (lane / 4, lane % 4) holds keys g and g + 8, columns
@@ -140,8 +140,9 @@ __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecod
   const int first = rank * W + warp;
 
   const int64_t tok_bytes = static_cast<int64_t>(a.num_kv_heads) * D * 2;
-  const char* const kbase = reinterpret_cast<const char*>(a.k) + kvh * (D * 2) + (lane % (D / 8)) * 16;
-  const char* const vbase = reinterpret_cast<const char*>(a.v) + kvh * (D * 2) + (lane % (D / 8)) * 16;
+  const int head_bytes = kvh * (D * 2) + (lane % (D / 8)) * 16;
+  const char* const kbase = reinterpret_cast<const char*>(a.k) + head_bytes;
+  const char* const vbase = reinterpret_cast<const char*>(a.v) + head_bytes;
   const int32_t* const table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks;
 
   float o[4 * VH][4];
@@ -194,8 +195,9 @@ __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecod
 #pragma unroll
       for (int i = 0; i < kBlockSize / kRowsPerCopy; ++i) {
         const int row = kRowsPerCopy * i + crow;
-        cp_async_16_zfill(dst + kBlockSize * kRowBytes + row * kRowBytes + ((cchunk ^ (row & 6)) << 4),
-                          pv + i * kRowsPerCopy * tok_bytes, bytes);
+        cp_async_16_zfill(
+            dst + (kBlockSize + row) * kRowBytes + ((cchunk ^ (row & 6)) << 4),
+            pv + i * kRowsPerCopy * tok_bytes, bytes);
       }
     }
     cp_async_commit();
@@ -226,7 +228,9 @@ __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecod
 #pragma unroll
     for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int h = 0; h < VH; ++h) vr[r][h] = lds128(srcv + ((r & 1) + (r >> 1) * 8) * kRowBytes + (((8 * h + g) ^ (2 * t)) << 4));
+      for (int h = 0; h < VH; ++h)
+        vr[r][h] = lds128(srcv + ((r & 1) + (r >> 1) * 8) * kRowBytes +
+                          (((8 * h + g) ^ (2 * t)) << 4));
     // ---- mask (first or last block of the window, last block of the sinks):
     // hidden keys get weight 0 and their V rows, which may hold anything, 0
     const bool edge = !(j0 + kBlockSize <= n && (j0 >= lo || j0 + kBlockSize <= ns));
@@ -377,7 +381,8 @@ cudaError_t launch(const WindowDecodeArgs& a, cudaStream_t stream) {
     std::lock_guard<std::mutex> lock(mu);
     if (!set_for[dev]) {
       e = cudaFuncSetAttribute(decode_window_kernel<D, W>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, DecodePlan<D, W>::kBytes);
+                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               DecodePlan<D, W>::kBytes);
       if (e != cudaSuccess) return e;
       set_for[dev] = true;
     }
@@ -444,7 +449,8 @@ cudaError_t residency(int num_sms, Residency* out) {
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       int n = 0;
-      if ((k == 4 && !wide) || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) n = 0;
+      if ((k == 4 && !wide) || cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess)
+        n = 0;
       r.clusters[k] = n;
     }
     cudaGetLastError();  // (a size that the device refuses is no error here)

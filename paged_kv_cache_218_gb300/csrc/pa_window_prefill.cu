@@ -35,8 +35,18 @@
 //    registers, a row per lane, they took 1.6 us per item; as a tensor store
 //    per warp, 0.8, half of it the proxy fence and the issue).
 //
-// What bounds it: the tensor pipe and, at 128 x 128 tiles, the softmax that
-// feeds it (one exponential per score).
+// What bounds it.  In long windows the tensor pipe: 0.73 us per pair and key
+// tile, 1.66 PFLOP/s over the device where cuBLAS sustains 1.70; 8192 queries x
+// 4096 keys take 395 us (1.43 PFLOP/s of the products that the masks leave).  In
+// short ones instruction fetches: the roles' loops go through 50 KB of code per
+// item, more than an SM caches, and the cache behind it serves a whole GPC.  So
+// each role is one loop with one copy of each step, the masks are a loop over
+// tensor memory in front of a tile's only softmax, waits share their slow path,
+// and divisions by the group are shifts.  With 124 KB of code (a first tile and
+// masked tiles of their own, three searches for the next item) that cache was at
+// 78 % of its request rate, SMs of full GPCs took 20 % longer than others, and an
+// item's ends took 3.9 us; now 2.7.  Only the products stay unrolled: their
+// issue is on the critical path (0.89 us a tile rolled by two).
 // Every mbarrier wait is bounded, as in pa_prefill_body.cuh.
 #include <mutex>
 #include <type_traits>
@@ -82,20 +92,27 @@ struct Item {
   int nvb;          // virtual blocks
   int edge[3];      // tiles with rows that no row of the pair sees, or -1
 };
+// Blocks of an item's key tile j: eight, fewer in the last one.
+__device__ __forceinline__ int tile_blocks(int nvb, int j) { return min(8, nvb - 8 * j); }
+
 constexpr int kItemRing = 8;
 static_assert(sizeof(Item) <= 64, "ring slot");
 
 // Walks a pair's items: every `stride`-th of the list.
 struct Cursor {
-  int64_t want;    // list index of the next item
-  int64_t before;  // items of the chunks before `chunk`
+  int want;    // list index of the next item
+  int before;  // items of the chunks before `chunk`
   int chunk;
 };
 
-__device__ __forceinline__ bool chunk_ok(const WindowPrefillArgs& a, int q0, int q1, int p0, int n) {
+__device__ __forceinline__ bool chunk_ok(const WindowPrefillArgs& a, int q0, int q1, int p0,
+                                         int n) {
   return q0 >= 0 && q1 <= a.total_q && q1 >= q0 && p0 >= 0 && n >= 0 && q1 - q0 <= n &&
          p0 <= n - (q1 - q0) && n <= a.max_blocks * kBlockSize;
 }
+
+static_assert(kBlockSize == 16, "shifts below");
+__device__ __forceinline__ int blocks_of(int keys) { return (keys + 15) >> 4; }
 
 // Rows of virtual blocks that no row of the pair sees: at most three ranges.
 struct Hidden {
@@ -116,9 +133,9 @@ struct Hidden {
       set(0, it.nsb - 1, min(sinks, it.kmax) - base, min(kBlockSize, it.lo - base));
     }
     // before the window, in its first block
-    if (it.lo / kBlockSize >= it.nsb) set(1, it.nsb, 0, it.lo % kBlockSize);
+    if (it.lo >> 4 >= it.nsb) set(1, it.nsb, 0, it.lo & 15);
     // behind the last key
-    if (it.kmax % kBlockSize) set(2, it.nvb - 1, it.kmax % kBlockSize, kBlockSize);
+    if (it.kmax & 15) set(2, it.nvb - 1, it.kmax & 15, kBlockSize);
   }
 };
 
@@ -128,7 +145,8 @@ __device__ __forceinline__ Item next_item(const WindowPrefillArgs& a, Cursor& cu
                                           int lane, bool flag) {
   Item it;
   it.nkt = 0;
-  const int rows = 2 * (kTileKeys / a.group);  // query tokens per item
+  const int rs = 9 - __ffs(a.group);  // log2 of the query tokens per item (a group divides 128)
+  const int rows = 1 << rs;
   while (cur.chunk < a.num_chunks) {
     // items of 32 chunks at a time, and their inclusive sums
     const int c = cur.chunk + lane;
@@ -138,14 +156,14 @@ __device__ __forceinline__ Item next_item(const WindowPrefillArgs& a, Cursor& cu
       q1 = a.cu_q_lens[c + 1];
       p0 = a.q_start_pos[c];
       if (chunk_ok(a, q0, q1, p0, a.seq_lens[c]))
-        items = (q1 - q0 + rows - 1) / rows * a.num_kv_heads;
+        items = ((q1 - q0 + rows - 1) >> rs) * a.num_kv_heads;
       else if (flag)
         atomicOr(a.err, PA_DEVERR_CHUNK);
     }
-    int64_t sum = items;
+    int sum = items;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, sum, off);
+      const int o = __shfl_up_sync(0xffffffffu, sum, off);
       if (lane >= off) sum += o;
     }
     const unsigned past = __ballot_sync(0xffffffffu, cur.before + sum > cur.want);
@@ -156,8 +174,7 @@ __device__ __forceinline__ Item next_item(const WindowPrefillArgs& a, Cursor& cu
     }
     const int w = __ffs(past) - 1;
     cur.before += __shfl_sync(0xffffffffu, sum - items, w);
-    const int at = static_cast<int>(cur.want - cur.before);
-    const int count = __shfl_sync(0xffffffffu, items, w);
+    const int at = cur.want - cur.before;
     cur.chunk += w;
     cur.want += stride;
     it.c = cur.chunk;
@@ -167,21 +184,74 @@ __device__ __forceinline__ Item next_item(const WindowPrefillArgs& a, Cursor& cu
     const int tile = at / a.num_kv_heads;
     it.kvh = at - tile * a.num_kv_heads;
     // last query tiles first: where the window has not closed they are longest
-    it.tc0 = (count / a.num_kv_heads - 1 - tile) * rows;
+    it.tc0 = (((it.qlen + rows - 1) >> rs) - 1 - tile) << rs;
     it.kmax = it.p0 + min(it.qlen, it.tc0 + rows);
     it.lo = max(0, it.p0 + it.tc0 - (a.window - 1));
     const int ns = min(a.sinks, it.kmax);
-    it.nsb = (ns + kBlockSize - 1) / kBlockSize;
-    it.b_first = max(it.lo / kBlockSize, it.nsb);
-    const int nb = (it.kmax + kBlockSize - 1) / kBlockSize;
-    it.nvb = it.nsb + max(0, nb - it.b_first);
-    it.nkt = (it.nvb + 7) / 8;
+    it.nsb = blocks_of(ns);
+    it.b_first = max(it.lo >> 4, it.nsb);
+    it.nvb = it.nsb + max(0, blocks_of(it.kmax) - it.b_first);
+    it.nkt = (it.nvb + 7) >> 3;
     const Hidden hid(it, a.sinks);
 #pragma unroll
-    for (int e = 0; e < 3; ++e) it.edge[e] = hid.vb[e] < 0 ? -1 : hid.vb[e] / 8;
+    for (int e = 0; e < 3; ++e) it.edge[e] = hid.vb[e] >> 3;  // (-1 stays)
     break;
   }
   return it;
+}
+
+// The waits of pa_prefill_body.cuh with one copy of what follows a first
+// attempt: code size decides how long an item's ends take.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort,
+                                     unsigned int* err, uint64_t limit_ns) {
+  if (*abort) return false;
+  if (mbar_wait(bar, parity, limit_ns)) return true;
+  *abort = 1;
+  atomicOr(err, PA_DEVERR_TIMEOUT);
+  return false;
+}
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                     const WindowPrefillArgs& a) {
+  return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort, a.err, a.wait_ns);
+}
+
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          const WindowPrefillArgs& a) {
+  bool ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+  if (!ok) {
+    ok = wait_on(bar, parity, abort, a.err, a.wait_ns);
+    __syncwarp();
+    ok = __all_sync(0xffffffffu, ok);
+  }
+  return ok;
+}
+
+// Ids of an item's virtual blocks [8 t_first, + 8 kIdBatch) into a loader's
+// ring, where the ids of the warp's tile T are at slot T % kIdRing and `base` is
+// the number of the item's tile 0.  A slot is rewritten only when its tile's
+// loads have been issued.  Ids past the list are -1, a box outside the pool,
+// which reads as zeros.  Called by a whole warp.
+__device__ __noinline__ void fetch_ids(const int32_t* table, int64_t num_blocks, unsigned int* err,
+                                       int* ids, int nsb, int b_first, int nvb, int t_first,
+                                       unsigned base) {
+  const int lane = threadIdx.x & 31;
+  int v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int vb = t_first * 8 + lane + 32 * i;
+    v[i] = vb < nvb ? table[vb < nsb ? vb : vb - nsb + b_first] : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int vb = t_first * 8 + lane + 32 * i;
+    if (vb < nvb && (v[i] < 0 || v[i] >= num_blocks)) {
+      atomicOr(err, PA_DEVERR_BLOCK_ID);
+      v[i] = -1;
+    }
+    ids[(base * 8 + vb) % (kIdRing * 8)] = v[i];
+  }
+  __syncwarp();
 }
 
 // Bits [0, k) of 64.
@@ -214,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P::kBarOff + 336);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 340);
   volatile int* go_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 352);
-  auto ring_item = [&](int k) {
+  auto ring_item = [&](unsigned k) {
     return reinterpret_cast<Item*>(smem + P::kItemsOff + 64 * (k % kItemRing));
   };
   int* ids_smem = reinterpret_cast<int*>(smem + P::kIdsOff) +
@@ -223,8 +293,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* red_sum = reinterpret_cast<float*>(smem + P::kRedOff2);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int G = a.group;
-  const int tpt = kTileKeys / G;
+  const int G = a.group, gs = __ffs(G) - 1;  // (a group divides 128)
+  const int tpt = kTileKeys >> gs;
   const int rank = static_cast<int>(blockIdx.x) & 1;
   const bool issuer = rank == 0;
 
@@ -264,42 +334,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kLoadKWarp || warp == kLoadVWarp) {
     // ------------------------------------------------------------ loaders
     const uint64_t pol = l2_policy_evict_last();
-    IdleClock clk(a.wait_ns);
-    auto timed_out = [&](bool progressed) {
-      if (progressed) {
-        clk.progress();
-        return false;
-      }
-      if (!clk.expired()) return false;
-      if (lane == 0) {
-        *abort_flag = 1;
-        atomicOr(a.err, PA_DEVERR_TIMEOUT);
-      }
-      return true;
-    };
-    // ids of virtual blocks [8 t_first, + 8 kIdBatch) of an item whose tile 0
-    // is this warp's tile `base`, into the ring (tile T at slot T % kIdRing);
-    // a slot is rewritten only when its tile's loads have been issued.  Ids
-    // past the list read as zeros (-1: a box outside the pool).
-    auto fetch_ids = [&](const Item& x, int t_first, int base) {
-      int v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int vb = t_first * 8 + lane + 32 * i;
-        const int b = vb < x.nsb ? vb : vb - x.nsb + x.b_first;
-        v[i] = vb < x.nvb ? a.block_tables[static_cast<int64_t>(x.c) * a.max_blocks + b] : -1;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int vb = t_first * 8 + lane + 32 * i;
-        if (vb < x.nvb && (v[i] < 0 || v[i] >= a.num_blocks)) {
-          atomicOr(a.err, PA_DEVERR_BLOCK_ID);
-          v[i] = -1;
-        }
-        ids_smem[(static_cast<unsigned>(base) * 8 + vb) % (kIdRing * 8)] = v[i];
-      }
-      __syncwarp();
-    };
     unsigned total = 0;  // tiles loaded by this warp, over all items
     // after a timeout: let the copies in flight land before the CTA may exit
     auto settle = [&]() {
@@ -312,10 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_prefetch_desc(&tm_q);
         tma_prefetch_desc(&tm_k);
       }
-      Cursor cur{static_cast<int64_t>(blockIdx.x) / 2, 0, 0};
-      int published = 0;
+      Cursor cur{static_cast<int>(blockIdx.x >> 1), 0, 0};
+      unsigned published = 0;
       auto publish = [&]() {
-        const Item x = next_item(a, cur, static_cast<int>(gridDim.x) / 2, lane, blockIdx.x == 0);
+        const Item x = next_item(a, cur, static_cast<int>(gridDim.x >> 1), lane, blockIdx.x == 0);
         if (lane == 0) {
           *ring_item(published) = x;
           mbar_arrive(bar_item + 8 * (published % kItemRing));
@@ -323,186 +357,183 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++published;
         return x;
       };
-      Item it = publish();
-      if (it.nkt) fetch_ids(it, 0, 0);
-      bool stop = a.stall_loads != 0;  // a stalled test launch issues no load
-      for (int qi = 0; it.nkt && !stop; ++qi) {
-        const int qb = qi & 1;
-        int jf = kIdBatch, jk = 0;
-        bool q_loaded = false, next_known = false, next_ids = false;
-        Item next = it;
-        while (jk < it.nkt && !stop) {
-          bool progressed = false;
-          if (!q_loaded) {
-            bool ok = qi < 2;
-            if (!ok && lane == 0) ok = mbar_test_wait(bar_q_empty + 8 * qb, ((qi >> 1) - 1) & 1);
-            if (__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
-              if (lane == 0) {
-                const uint32_t bar = bar_q + 8 * qb;
-                if (issuer) mbar_arrive_expect_tx(bar, 4 * kHalf);  // both Q tiles of the pair
-                for (int h = 0; h < 2; ++h) {
-                  const uint32_t dst = sbase + P::kQOff + (2 * qb + h) * kHalf;
-                  const int row = it.q0 + it.tc0 + rank * tpt;
-                  if (issuer)
-                    tma_load_3d(dst, &tm_q, h * 64, it.kvh * G, row, bar, pol);
-                  else
-                    tma_load_3d_pair(dst, &tm_q, h * 64, it.kvh * G, row, mapa_shared(bar, 0), pol);
-                }
-              }
-              __syncwarp();
-              q_loaded = true;
-              progressed = true;
-            }
-          }
-          if (jf < it.nkt && jk + kIdBatch / 2 >= jf) {
-            fetch_ids(it, jf, total - jk);
-            jf += kIdBatch;
-            progressed = true;
-          }
-          const int slot = total % kNK;
-          bool free_slot = total < kNK;
-          if (!free_slot && lane == 0)
-            free_slot = mbar_test_wait(bar_k_empty + 8 * slot, ((total / kNK) - 1) & 1);
-          if (q_loaded && jk < jf && __shfl_sync(0xffffffffu, free_slot ? 1 : 0, 0)) {
-            const uint32_t bar = bar_k_full + 8 * slot;
-            if (lane == 0 && issuer) mbar_arrive_expect_tx(bar, 2 * kHalf);
-            __syncwarp();
-            if (lane < 4) {  // CTA r takes keys 64 r .. 64 r + 63: blocks 4 r .. 4 r + 3
-              const int id = ids_smem[(total % kIdRing) * 8 + 4 * rank + lane];
-              const uint32_t dst = sbase + P::kKOff + slot * P::kKSlot + lane * 2 * kBlockBytes;
-              if (issuer)
-                tma_load_4d(dst, &tm_k, 0, 0, 2 * it.kvh, 2 * id, bar, pol);
-              else
-                tma_load_4d_pair(dst, &tm_k, 0, 0, 2 * it.kvh, 2 * id, mapa_shared(bar, 0), pol);
-            }
-            __syncwarp();
-            ++jk;
-            ++total;
-            progressed = true;
-          } else if (q_loaded && !next_known) {
-            next = publish();
-            next_known = progressed = true;
-          } else if (next_known && !next_ids && next.nkt && jf >= it.nkt &&
-                     it.nkt - jk <= kIdBatch) {
-            fetch_ids(next, 0, total + it.nkt - jk);
-            next_ids = progressed = true;
-          }
-          stop = timed_out(progressed) || warp_flag(abort_flag);
+      // (One place for each step: the code of all roles has to stay small.)
+      Item it, next;
+      it.nkt = 0;
+      int jf = 0, jk = 0;  // tiles of `it` with ids, and loaded
+      int lead = 0;        // tiles of `it` to load before the next item is looked for
+      bool next_ids = true;
+      unsigned qi = 0;     // items begun
+      while (true) {
+        if (jk == lead) {
+          next = publish();
+          if (a.stall_loads) break;  // a stalled test launch issues no load
+          next_ids = next.nkt == 0;
+          lead = -1;
         }
-        if (stop) break;
-        if (!next_known) next = publish();
-        if (!next_ids && next.nkt) fetch_ids(next, 0, total);
-        it = next;
+        const bool more = jf < it.nkt && jk + kIdBatch / 2 >= jf;
+        if (more || (!next_ids && jf >= it.nkt && it.nkt - jk <= kIdBatch)) {
+          const Item& x = more ? it : next;
+          fetch_ids(a.block_tables + static_cast<int64_t>(x.c) * a.max_blocks, a.num_blocks, a.err,
+                    ids_smem, x.nsb, x.b_first, x.nvb, more ? jf : 0,
+                    total - jk + (more ? 0 : it.nkt));
+          if (more)
+            jf += kIdBatch;
+          else
+            next_ids = true;
+        }
+        if (jk == it.nkt) {  // on to the next item
+          if (next.nkt == 0) break;
+          it = next;
+          jf = kIdBatch;
+          jk = 0;
+          const unsigned qb = qi & 1;
+          if (qi >= 2 &&
+              !wait_warp(bar_q_empty + 8 * qb, ((qi >> 1) - 1) & 1, abort_flag, a))
+            break;
+          lead = qi == 0 ? min(it.nkt, kNK) : 0;
+          ++qi;
+          if (lane < 2) {  // a half each
+            const uint32_t bar = bar_q + 8 * qb;
+            if (issuer && lane == 0) mbar_arrive_expect_tx(bar, 4 * kHalf);  // the pair's Q tiles
+            const uint32_t dst = sbase + P::kQOff + (2 * qb + lane) * kHalf;
+            const int row = it.q0 + it.tc0 + rank * tpt;
+            if (issuer)
+              tma_load_3d(dst, &tm_q, lane * 64, it.kvh * G, row, bar, pol);
+            else
+              tma_load_3d_pair(dst, &tm_q, lane * 64, it.kvh * G, row, mapa_shared(bar, 0), pol);
+          }
+          __syncwarp();
+          if (lead == 0) continue;
+        }
+        const unsigned slot = total % kNK;
+        if (total >= kNK &&
+            !wait_warp(bar_k_empty + 8 * slot, ((total / kNK) - 1) & 1, abort_flag, a))
+          break;
+        const uint32_t bar = bar_k_full + 8 * slot;
+        // each CTA takes half of the tile's blocks, their number made even (an
+        // id past the list loads zeros)
+        const int half = (tile_blocks(it.nvb, jk) + 1) / 2;
+        if (lane == 0 && issuer) mbar_arrive_expect_tx(bar, half * 4 * kBlockBytes);
+        __syncwarp();
+        if (lane < half) {
+          const int id = ids_smem[(total % kIdRing) * 8 + half * rank + lane];
+          const uint32_t dst = sbase + P::kKOff + slot * P::kKSlot + lane * 2 * kBlockBytes;
+          if (issuer)
+            tma_load_4d(dst, &tm_k, 0, 0, 2 * it.kvh, 2 * id, bar, pol);
+          else
+            tma_load_4d_pair(dst, &tm_k, 0, 0, 2 * it.kvh, 2 * id, mapa_shared(bar, 0), pol);
+        }
+        __syncwarp();
+        ++jk;
+        ++total;
       }
       // every load's slot has been released, and so has landed, before exit
-      if (lane == 0)
-        for (int sl = 0; sl < kNK && sl < total; ++sl)
-          wait_or_abort<2>(bar_k_empty + 8 * sl, ((total - 1 - sl) / kNK) & 1, abort_flag, a);
+      if (lane == 0) {
+        for (unsigned b = 0; b < 2 && b < qi; ++b)
+          wait(bar_q_empty + 8 * b, ((qi - 1 - b) >> 1) & 1, abort_flag, a);
+        for (unsigned sl = 0; sl < kNK && sl < total; ++sl)
+          wait(bar_k_empty + 8 * sl, ((total - 1 - sl) / kNK) & 1, abort_flag, a);
+      }
       settle();
     } else {
       if (lane == 0) tma_prefetch_desc(&tm_v);
+      Item it;
+      it.nkt = 0;
+      int jf = 0, jv = 0;  // tiles of `it` with ids, and loaded
+      bool next_ids = false;
+      unsigned k = 0;           // items begun
       unsigned full_phase = 0;  // bit s: parity of v_full[s]'s next use
       int edge_slot = -1;       // slot of the edge tile whose rows are still to be zeroed
-      int edge_tile = 0;
-      bool stop = a.stall_loads != 0;
-      bool have_ids = false;
-      for (int k = 0; !stop; ++k) {
-        if (!wait_or_abort_warp<2>(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1, abort_flag,
-                                   a))
-          break;
-        const Item it = *ring_item(k);
-        if (it.nkt == 0) break;
-        if (!have_ids) fetch_ids(it, 0, total);
-        have_ids = false;
-        const Hidden hid(it, a.sinks);
-        const uint32_t next_bar = bar_item + 8 * ((k + 1) % kItemRing);
-        const uint32_t next_phase = ((k + 1) / kItemRing) & 1;
-        int jf = kIdBatch, jv = 0;
-        while ((jv < it.nkt || edge_slot >= 0) && !stop) {
-          bool progressed = false;
-          if (jf < it.nkt && jv + kIdBatch / 2 >= jf) {
-            fetch_ids(it, jf, total - jv);
-            jf += kIdBatch;
-            progressed = true;
-          }
-          const bool edge = jv == it.edge[0] || jv == it.edge[1] || jv == it.edge[2];
-          if (jv < it.nkt && jv < jf && !(edge && edge_slot >= 0)) {
-            const int slot = total % kNV;
-            bool free_slot = total < kNV;
-            if (!free_slot && lane == 0)
-              free_slot = mbar_test_wait(bar_o_done + 8 * slot, ((total / kNV) - 1) & 1);
-            if (__shfl_sync(0xffffffffu, free_slot ? 1 : 0, 0)) {
-              const bool remote = !issuer && !edge;
-              const uint32_t bar = edge ? bar_v_full + 8 * slot
-                                        : (remote ? mapa_shared(bar_v_ready + 8 * slot, 0)
-                                                  : bar_v_ready + 8 * slot);
-              if (lane == 0) {
-                if (remote)
-                  mbar_arrive_expect_tx_remote(bar, P::kVSlot);
-                else
-                  mbar_arrive_expect_tx(bar, P::kVSlot);
-              }
-              __syncwarp();
-              if (lane < 8) {  // CTA r takes columns 64 r .. 64 r + 63 of every key
-                const int id = ids_smem[(total % kIdRing) * 8 + lane];
-                const uint32_t dst = sbase + P::kVOff + slot * P::kVSlot + lane * kBlockBytes;
-                const int x = it.kvh * 128 + rank * 64, y = id * kBlockSize;
-                if (remote)
-                  tma_load_2d_pair(dst, &tm_v, x, y, bar, pol);
-                else
-                  tma_load_2d(dst, &tm_v, x, y, bar, pol);
-              }
-              __syncwarp();
-              if (edge) {
-                edge_slot = slot;
-                edge_tile = jv;
-              }
-              ++jv;
-              ++total;
-              progressed = true;
-            }
-          }
-          if (edge_slot >= 0) {
-            bool landed = false;
-            if (lane == 0)
-              landed = mbar_test_wait(bar_v_full + 8 * edge_slot, (full_phase >> edge_slot) & 1);
-            if (__shfl_sync(0xffffffffu, landed ? 1 : 0, 0)) {
-              const uint32_t vt = sbase + P::kVOff + edge_slot * P::kVSlot;
+      while (!a.stall_loads) {
+        if (edge_slot >= 0) {
+          if (!wait_warp(bar_v_full + 8 * edge_slot, (full_phase >> edge_slot) & 1, abort_flag, a))
+            break;
+          const uint32_t vt = sbase + P::kVOff + edge_slot * P::kVSlot;
+          const Hidden hid(it, a.sinks);
 #pragma unroll
-              for (int h = 0; h < 3; ++h) {
-                if (it.edge[h] != edge_tile) continue;
-                const uint32_t blk = vt + (hid.vb[h] % 8) * kBlockBytes;
-                for (int e = lane + 8 * hid.r0[h]; e < 8 * hid.r1[h]; e += 32)
-                  st_shared_zero16(blk + e * 16);
-              }
-              fence_proxy_async_smem();
-              __syncwarp();
-              if (lane == 0) {
-                if (!issuer)
-                  mbar_arrive_remote_release(mapa_shared(bar_v_ready + 8 * edge_slot, 0));
-                else
-                  mbar_arrive(bar_v_ready + 8 * edge_slot);
-              }
-              full_phase ^= 1u << edge_slot;
-              edge_slot = -1;
-              progressed = true;
-            }
+          for (int h = 0; h < 3; ++h) {
+            if (it.edge[h] != jv - 1) continue;
+            const uint32_t blk = vt + (hid.vb[h] & 7) * kBlockBytes;
+#pragma unroll 1
+            for (int e = lane + 8 * hid.r0[h]; e < 8 * hid.r1[h]; e += 32)
+              st_shared_zero16(blk + e * 16);
           }
-          if (!progressed && !have_ids && jf >= it.nkt && it.nkt - jv <= kIdBatch) {
-            bool there = false;
-            if (lane == 0) there = mbar_test_wait(next_bar, next_phase);
-            if (__shfl_sync(0xffffffffu, there ? 1 : 0, 0)) {
-              const Item next = *ring_item(k + 1);
-              if (next.nkt) fetch_ids(next, 0, total + it.nkt - jv);
-              have_ids = progressed = true;
-            }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (!issuer)
+              mbar_arrive_remote_release(mapa_shared(bar_v_ready + 8 * edge_slot, 0));
+            else
+              mbar_arrive(bar_v_ready + 8 * edge_slot);
           }
-          stop = timed_out(progressed) || warp_flag(abort_flag);
+          full_phase ^= 1u << edge_slot;
+          edge_slot = -1;
         }
+        const bool more = jf < it.nkt && jv + kIdBatch / 2 >= jf;
+        bool fetch = more;
+        if (!more && !next_ids && jf >= it.nkt && it.nkt - jv <= kIdBatch) {
+          // the next item: waited for at the end of this one, taken before if it is there
+          const uint32_t bar = bar_item + 8 * (k % kItemRing), parity = (k / kItemRing) & 1;
+          if (jv == it.nkt) {
+            if (!wait_warp(bar, parity, abort_flag, a)) break;
+            fetch = true;
+          } else {
+            fetch = __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+          }
+        }
+        if (fetch) {
+          const Item* x = ring_item(more ? k - 1 : k);
+          if (x->nkt)
+            fetch_ids(a.block_tables + static_cast<int64_t>(x->c) * a.max_blocks, a.num_blocks,
+                      a.err, ids_smem, x->nsb, x->b_first, x->nvb, more ? jf : 0,
+                      total - jv + (more ? 0 : it.nkt));
+          if (more)
+            jf += kIdBatch;
+          else
+            next_ids = true;
+        }
+        if (jv == it.nkt) {  // on to the next item
+          it = *ring_item(k++);
+          if (it.nkt == 0) break;
+          jf = kIdBatch;
+          jv = 0;
+          next_ids = false;
+        }
+        const unsigned slot = total % kNV;
+        if (total >= kNV &&
+            !wait_warp(bar_o_done + 8 * slot, ((total / kNV) - 1) & 1, abort_flag, a))
+          break;
+        const bool edge = jv == it.edge[0] || jv == it.edge[1] || jv == it.edge[2];
+        const bool remote = !issuer && !edge;
+        const uint32_t bar = edge ? bar_v_full + 8 * slot
+                                  : (remote ? mapa_shared(bar_v_ready + 8 * slot, 0)
+                                            : bar_v_ready + 8 * slot);
+        const int blocks = tile_blocks(it.nvb, jv);
+        if (lane == 0) {
+          if (remote)
+            mbar_arrive_expect_tx_remote(bar, blocks * kBlockBytes);
+          else
+            mbar_arrive_expect_tx(bar, blocks * kBlockBytes);
+        }
+        __syncwarp();
+        if (lane < blocks) {  // CTA r takes columns 64 r .. 64 r + 63 of every key
+          const int id = ids_smem[(total % kIdRing) * 8 + lane];
+          const uint32_t dst = sbase + P::kVOff + slot * P::kVSlot + lane * kBlockBytes;
+          const int x = it.kvh * 128 + rank * 64, y = id * kBlockSize;
+          if (remote)
+            tma_load_2d_pair(dst, &tm_v, x, y, bar, pol);
+          else
+            tma_load_2d(dst, &tm_v, x, y, bar, pol);
+        }
+        __syncwarp();
+        if (edge) edge_slot = slot;
+        ++jv;
+        ++total;
       }
       if (lane == 0)
-        for (int sl = 0; sl < kNV && sl < total; ++sl)
-          wait_or_abort<2>(bar_o_done + 8 * sl, ((total - 1 - sl) / kNV) & 1, abort_flag, a);
+        for (unsigned sl = 0; sl < kNV && sl < total; ++sl)
+          wait(bar_o_done + 8 * sl, ((total - 1 - sl) / kNV) & 1, abort_flag, a);
       settle();
     }
     __syncwarp();
@@ -510,43 +541,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ tensor-core issue
     // Two threads of the even CTA, as in pa_prefill_body.cuh.
     if (lane == 0 && issuer) {
-      auto commit = [&](uint32_t bar) {
-        tc_commit<2>(mapa_shared(bar, 1));
-        tc_commit<2>(bar);
-      };
-      IdleClock clk(a.wait_ns);
-      auto give_up = [&]() {
-        if (!*abort_flag) {
-          *abort_flag = 1;
-          atomicOr(a.err, PA_DEVERR_TIMEOUT);
-        }
-      };
       bool ok = true;
       if (warp == kMmaWarp) {
-        const uint32_t idesc_s = instr_desc(0, 256);
+        const uint32_t idesc_s = instr_desc(0, 256) & ~(0x3fu << 17);  // (columns / 8 left out)
         const uint64_t dk0 = smem_desc(sbase + P::kKOff, 16, kKGroupStride);
         const uint64_t dq0 = smem_desc(sbase + P::kQOff, 16, 1024);
         int s_buf = 0, s_round = 0, s_kslot = 0, s_kphase = 0;
-        for (int k = 0; ok; ++k) {
-          ok = wait_or_abort<2>(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1, abort_flag, a);
+        for (unsigned k = 0; ok; ++k) {
+          ok = wait(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1, abort_flag, a);
           const int nkt = ok ? ring_item(k)->nkt : 0;
           if (nkt == 0) break;
+          const int nvb = ring_item(k)->nvb;
           const uint64_t dq = dq0 + static_cast<uint64_t>(((k & 1) * 2 * kHalf) >> 4);
-          ok = wait_or_abort<2>(bar_q + 8 * (k & 1), (k >> 1) & 1, abort_flag, a);
+          ok = wait(bar_q + 8 * (k & 1), (k >> 1) & 1, abort_flag, a);
           int js = 0;
           while (ok && js < nkt) {
-            if (mbar_test_wait(bar_k_full + 8 * s_kslot, s_kphase) &&
-                (s_round == 0 || mbar_test_wait(bar_o_done + 8 * s_buf, (s_round + 1) & 1))) {
+            const uint64_t dk = dk0 + static_cast<uint64_t>((s_kslot * P::kKSlot) >> 4);
+            const uint32_t dst = tmem + s_buf * 128;
+            // 32 columns for every two blocks
+            const uint32_t idesc = idesc_s | (((tile_blocks(nvb, js) + 1) / 2 * 4) << 17);
+            ok = wait(bar_k_full + 8 * s_kslot, s_kphase, abort_flag, a) &&
+                 (s_round == 0 || wait(bar_o_done + 8 * s_buf, (s_round + 1) & 1, abort_flag, a));
+            if (ok) {
               tc_fence_after();
-              const uint64_t dk = dk0 + static_cast<uint64_t>((s_kslot * P::kKSlot) >> 4);
-              const uint32_t dst = tmem + s_buf * 128;
 #pragma unroll
               for (int ks = 0; ks < 8; ++ks)
                 tc_mma_f16<2>(dst, dq + (((ks >> 2) * kHalf + (ks & 3) * 32) >> 4),
-                              dk + (((ks >> 2) * kKHalfOffset + (ks & 3) * 32) >> 4), idesc_s,
+                              dk + (((ks >> 2) * kKHalfOffset + (ks & 3) * 32) >> 4), idesc,
                               ks > 0);
-              commit(bar_s_full + 8 * s_buf);
-              commit(bar_k_empty + 8 * s_kslot);
+              tc_commit_pair(bar_s_full + 8 * s_buf);
+              tc_commit_pair(bar_k_empty + 8 * s_kslot);
               ++js;
               if (++s_buf == kNS) {
                 s_buf = 0;
@@ -556,38 +580,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s_kslot = 0;
                 s_kphase ^= 1;
               }
-              clk.progress();
-            } else if (*abort_flag || clk.expired()) {
-              give_up();
-              ok = false;
             }
           }
-          if (ok) commit(bar_q_empty + 8 * (k & 1));
+          if (ok) tc_commit_pair(bar_q_empty + 8 * (k & 1));
         }
       } else {
         const uint32_t idesc_o = instr_desc(1, 256);
         const uint64_t dv0 = smem_desc(sbase + P::kVOff, kHalf, 1024);
         int p_buf = 0, p_phase = 0, p_vslot = 0, p_vphase = 0;
-        for (int k = 0; ok; ++k) {
-          ok = wait_or_abort<2>(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1, abort_flag, a);
+        for (unsigned k = 0; ok; ++k) {
+          ok = wait(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1, abort_flag, a);
           const int nkt = ok ? ring_item(k)->nkt : 0;
           if (nkt == 0) break;
           const int e0 = ring_item(k)->edge[0], e1 = ring_item(k)->edge[1],
                     e2 = ring_item(k)->edge[2];
+          const int nvb = ring_item(k)->nvb;
           int jp = 0;
           while (ok && jp < nkt) {
-            if (mbar_test_wait(bar_p_full + 8 * p_buf, p_phase) &&
-                mbar_test_wait(bar_v_ready + 8 * p_vslot, p_vphase)) {
-              if (jp == e0 || jp == e1 || jp == e2) fence_acq_rel_cluster();  // the peer's zeroed rows
+            const uint64_t dv = dv0 + static_cast<uint64_t>((p_vslot * P::kVSlot) >> 4);
+            const uint32_t ta = tmem + p_buf * 128;
+            const int blocks = tile_blocks(nvb, jp);
+            const bool zeroed = jp == e0 || jp == e1 || jp == e2;
+            ok = wait(bar_v_ready + 8 * p_vslot, p_vphase, abort_flag, a) &&
+                 wait(bar_p_full + 8 * p_buf, p_phase, abort_flag, a);
+            if (ok) {
+              if (zeroed) fence_acq_rel_cluster();  // the peer's zeroed rows
               tc_fence_after();
-              const uint64_t dv = dv0 + static_cast<uint64_t>((p_vslot * P::kVSlot) >> 4);
-              const uint32_t ta = tmem + p_buf * 128;
+              if (blocks == 8) {
 #pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                tc_mma_f16_tmem_a<2>(tmem + kTmemO, ta + (ks >> 2) * 64 + (ks & 3) * 8,
-                                     dv + ((ks * kBlockBytes) >> 4), idesc_o,
-                                     (jp > 0 || ks > 0) ? 1u : 0u);
-              commit(bar_o_done + 8 * p_buf);
+                for (int ks = 0; ks < 8; ++ks)
+                  tc_mma_f16_tmem_a<2>(tmem + kTmemO, ta + (ks >> 2) * 64 + (ks & 3) * 8,
+                                       dv + ((ks * kBlockBytes) >> 4), idesc_o,
+                                       (jp > 0 || ks > 0) ? 1u : 0u);
+              } else {
+#pragma unroll 1
+                for (int ks = 0; ks < blocks; ++ks)
+                  tc_mma_f16_tmem_a<2>(tmem + kTmemO, ta + (ks >> 2) * 64 + (ks & 3) * 8,
+                                       dv + ((ks * kBlockBytes) >> 4), idesc_o,
+                                       (jp > 0 || ks > 0) ? 1u : 0u);
+              }
+              tc_commit_pair(bar_o_done + 8 * p_buf);
               ++jp;
               if (++p_buf == kNS) {
                 p_buf = 0;
@@ -597,10 +629,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 p_vslot = 0;
                 p_vphase ^= 1;
               }
-              clk.progress();
-            } else if (*abort_flag || clk.expired()) {
-              give_up();
-              ok = false;
             }
           }
         }
@@ -623,54 +651,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     // warp's arrival on p_full behind these loads of O.  The barrier in it also
     // hands over the key tiles of the item after the one at hand (go_flag 0 ..
     // 7; -1: not published yet).
-    const int tok = r / G, warp_toks = 32 / G;
+    const int tok = r >> gs, warp_toks = 32 >> gs;
     const uint32_t stage = sbase + P::kOutOff + hc * kHalf + qd * 32 * 128;
     bool pending = false;
     int64_t out_row = 0;            // of the pending item: the warp's first row, [token][head],
     int out_toks = 0;               // and how many of its tokens exist (<= 0: none)
     float out_m = 0.f, out_l = 0.f;
     uint32_t out_bar = 0, out_phase = 0;  // PV of its last tile
-    auto write_out = [&](int k) {
+    auto write_out = [&](unsigned k) {
       volatile int* go = go_flag + (k & 1) * 4 + qd;
       if (hc == 0 && lane == 0)
         *go = mbar_test_wait(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1)
                   ? ring_item(k)->nkt
                   : -1;
-      wait_or_abort_warp<2>(out_bar, out_phase, abort_flag, a);
+      wait_warp(out_bar, out_phase, abort_flag, a);
       tc_fence_after();
       red_sum[hc * 128 + r] = out_l;
-      tmem_ld64(ocol, v);
       named_barrier(1 + qd, 64);
       const float l_tot = out_l + red_sum[(hc ^ 1) * 128 + r];
       const float inv = l_tot == 0.f ? 0.f : 1.f / l_tot;  // a NaN sum stays visible
       const uint64_t inv2 = f32x2(inv, inv);
-      // 16-byte column q of row `lane` goes to q ^ (lane & 7)
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t (&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
+        tmem_ld32(ocol + 32 * c, w);
+        // 16-byte column q of row `lane` goes to q ^ (lane & 7)
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        uint32_t pk[4];
+        for (int q = 0; q < 4; ++q) {
+          uint32_t pk[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = 8 * q + 2 * i;
-          const float2 x =
-              f32x2_parts(mul2(f32x2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), inv2));
-          pk[i] = pack_bf16x2(x.x, x.y);
+          for (int i = 0; i < 4; ++i) {
+            const int e = 8 * q + 2 * i;
+            const float2 x =
+                f32x2_parts(mul2(f32x2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])), inv2));
+            pk[i] = pack_bf16x2(x.x, x.y);
+          }
+          sts128(stage + lane * 128 + (((4 * c + q) ^ (lane & 7)) << 4),
+                 make_uint4(pk[0], pk[1], pk[2], pk[3]));
         }
-        sts128(stage + lane * 128 + ((q ^ (lane & 7)) << 4), make_uint4(pk[0], pk[1], pk[2], pk[3]));
       }
       __syncwarp();
       const bool good = !warp_flag(abort_flag);
       // four rows at a time, eight lanes on the 128 bytes of each
-#pragma unroll
+#pragma unroll 2
       for (int i = 0; i < 8; ++i) {
-        const int row = 4 * i + lane / 8, t = row / G;
+        const int row = 4 * i + lane / 8, t = row >> gs;
         const uint4 x = lds128(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4));
         if (good && t < out_toks)
           *reinterpret_cast<uint4*>(
-              a.out + (out_row + static_cast<int64_t>(t) * a.num_q_heads + (row - t * G)) * 128 +
+              a.out + (out_row + static_cast<int64_t>(t) * a.num_q_heads + (row & (G - 1))) * 128 +
               hc * 64 + (lane & 7) * 8) = x;
       }
-      if (good && hc == 0 && a.out_lse && lane / G < out_toks)
-        a.out_lse[out_row + static_cast<int64_t>(lane / G) * a.num_q_heads + lane % G] =
+      if (good && hc == 0 && a.out_lse && lane >> gs < out_toks)
+        a.out_lse[out_row + static_cast<int64_t>(lane >> gs) * a.num_q_heads + (lane & (G - 1))] =
             l_tot == 0.f ? -INFINITY : (out_m + __log2f(l_tot)) * kLn2;
       __syncwarp();  // the staging rows may be written again
       return *go;
@@ -680,18 +713,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     // item: they meet at a named barrier for every tile, also after a timeout
     // (when the waits are skipped and what they compute is not stored).
     int nkt = -1;
-    for (int k = 0;; ++k) {
+    for (unsigned k = 0;; ++k) {
       const uint32_t item_bar = bar_item + 8 * (k % kItemRing);
       if (nkt < 0) {
         volatile int* go = go_flag + 8 + (k & 1) * 4 + qd;
         if (hc == 0) {
-          const bool got = wait_or_abort_warp<2>(item_bar, (k / kItemRing) & 1, abort_flag, a);
+          const bool got = wait_warp(item_bar, (k / kItemRing) & 1, abort_flag, a);
           if (lane == 0) *go = got ? ring_item(k)->nkt : 0;
         }
         named_barrier(1 + qd, 64);
         nkt = *go;
       }
-      if (nkt == 0) break;
+      const bool last = nkt == 0;  // the list's end: the pending output only
+      if (last && !pending) break;
       int next_nkt = -1;
       const Item& it = *ring_item(k);
       const int kmax = it.kmax, p0 = it.p0, t0 = it.tc0 + rank * tpt;
@@ -705,78 +739,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int hi = min(pos, kmax - 1) - shift;
       const int lo = max(0, pos - (a.window - 1)) - shift;
       float m_run = kFloor, l_run = 0.f;
-      // (The first tile apart, and one copy of the exponentials in each body:
-      // instruction fetches bound this loop.  Everything in one body measured
-      // 0.85 us a tile, two more copies 0.78, this 0.755; a first tile is
-      // masked in nearly every item, so it takes the masks always.)
-      auto tile = [&](int j, auto is_first) {
-        constexpr bool first = decltype(is_first)::value;
-        const int b = jt & 1;
-        wait_or_abort_warp<2>(bar_s_full + 8 * b3, s_phase, abort_flag, a);
-        tc_fence_after();
-        const int kb = j * kTileKeys + hc * 64;
-        const bool whole = hi >= kb + 63 && (lo <= kb || a.sinks >= kb + 64);
-        const bool full = !first && __all_sync(0xffffffffu, whole);
-        float mloc;
-        if (full) {
-          tmem_ld64_max(tmem + lane_off + b3 * 128 + hc * 64, v, mloc);
-        } else {
-          const uint64_t seen =
-              low_bits(hi - kb + 1) &
-              (low_bits(a.sinks > kb ? min(a.sinks - kb, 64) : 0) | ~low_bits(lo - kb));
-          const uint32_t seen0 = static_cast<uint32_t>(seen);
-          const uint32_t seen1 = static_cast<uint32_t>(seen >> 32);
-          tmem_ld64(tmem + lane_off + b3 * 128 + hc * 64, v);
-          float mp[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            // a hidden score, whatever it holds, becomes -inf
-            v[i] = (((i < 32 ? seen0 : seen1) >> (i & 31)) & 1u) ? v[i] : 0xff800000u;
-            mp[i & 3] = fmaxf(mp[i & 3], __uint_as_float(v[i]));
-          }
-          mloc = fmaxf(fmaxf(mp[0], mp[1]), fmaxf(mp[2], mp[3]));
-        }
-        mloc = mloc * sl;  // scale > 0 keeps the order
-        red_max[(b * 2 + hc) * 128 + r] = mloc;
-        named_barrier(1 + qd, 64);
-        const float mx = fmaxf(mloc, red_max[(b * 2 + (hc ^ 1)) * 128 + r]);
-        const float m_new = fmaxf(m_run, mx);
-        const bool move = m_new > m_run + kRescaleThreshold;
-        const float m_use = move ? m_new : m_run;
-        const float alpha = move ? fast_exp2(m_run - m_use) : 1.f;
-        uint64_t rsp[2] = {0, 0};
-        uint32_t pk[32];
-        const uint64_t sl2 = f32x2(sl, sl), nm2 = f32x2(-m_use, -m_use);
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) {
-          // -inf (hidden) gives exactly 0: m_use is finite
-          const float2 x =
-              f32x2_parts(fma2(f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sl2, nm2));
-          const float e0 = fast_exp2(x.x), e1 = fast_exp2(x.y);
-          rsp[(i >> 1) & 1] = add2(rsp[(i >> 1) & 1], f32x2(e0, e1));
-          pk[i / 2] = pack_bf16x2(e0, e1);
-        }
-        const float2 rs = f32x2_parts(add2(rsp[0], rsp[1]));
-        l_run = l_run * alpha + (rs.x + rs.y);
-        m_run = m_use;
-        // O is rescaled only when a row maximum moved; PV of the previous
-        // tile must have landed first (tile 0's PV overwrites O)
-        if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
-          const int pb = b3 == 0 ? kNS - 1 : b3 - 1;
-          wait_or_abort_warp<2>(bar_o_done + 8 * pb, b3 == 0 ? s_phase ^ 1 : s_phase, abort_flag,
-                                a);
+#pragma unroll 1
+      for (int j = 0; j < nkt || last; ++j) {
+        const bool first = j == 0;
+        if (!last) {
+          const int b = jt & 1;
+          wait_warp(bar_s_full + 8 * b3, s_phase, abort_flag, a);
           tc_fence_after();
+          const int kb = j * kTileKeys + hc * 64;
+          const bool whole = hi >= kb + 63 && (lo <= kb || a.sinks >= kb + 64);
+          float mloc;
+          const uint32_t sc = tmem + lane_off + b3 * 128 + hc * 64;
+          if (!__all_sync(0xffffffffu, whole)) {
+            // hidden scores, whatever they hold, become -inf in tensor memory
+            const uint64_t seen =
+                low_bits(hi - kb + 1) &
+                (low_bits(a.sinks > kb ? min(a.sinks - kb, 64) : 0) | ~low_bits(lo - kb));
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t m = static_cast<uint32_t>(seen >> (32 * c));
+              if (__all_sync(0xffffffffu, m == 0xffffffffu)) continue;
+              uint32_t (&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
+              tmem_ld32(sc + 32 * c, w);
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            uint32_t (&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[32 * cc]);
-            tmem_ld32(ocol + 32 * cc, w);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
-            tmem_st32(ocol + 32 * cc, w);
+              for (int i = 0; i < 32; ++i) w[i] = ((m >> i) & 1u) ? w[i] : 0xff800000u;
+              tmem_st32(sc + 32 * c, w);
+            }
           }
+          tmem_ld64_max(sc, v, mloc);
+          mloc = mloc * sl;  // scale > 0 keeps the order
+          red_max[(b * 2 + hc) * 128 + r] = mloc;
+          named_barrier(1 + qd, 64);
+          const float mx = fmaxf(mloc, red_max[(b * 2 + (hc ^ 1)) * 128 + r]);
+          const float m_new = fmaxf(m_run, mx);
+          const bool move = m_new > m_run + kRescaleThreshold;
+          const float m_use = move ? m_new : m_run;
+          const float alpha = move ? fast_exp2(m_run - m_use) : 1.f;
+          uint64_t rsp[2] = {0, 0};
+          uint32_t pk[32];
+          const uint64_t sl2 = f32x2(sl, sl), nm2 = f32x2(-m_use, -m_use);
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            // -inf (hidden) gives exactly 0: m_use is finite
+            const uint64_t s2 = f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            const float2 x = f32x2_parts(fma2(s2, sl2, nm2));
+            const float e0 = fast_exp2(x.x), e1 = fast_exp2(x.y);
+            rsp[(i >> 1) & 1] = add2(rsp[(i >> 1) & 1], f32x2(e0, e1));
+            pk[i / 2] = pack_bf16x2(e0, e1);
+          }
+          const float2 rs = f32x2_parts(add2(rsp[0], rsp[1]));
+          l_run = l_run * alpha + (rs.x + rs.y);
+          m_run = m_use;
+          // O is rescaled only when a row maximum moved; PV of the previous
+          // tile must have landed first (tile 0's PV overwrites O)
+          if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+            const int pb = b3 == 0 ? kNS - 1 : b3 - 1;
+            wait_warp(bar_o_done + 8 * pb, b3 == 0 ? s_phase ^ 1 : s_phase, abort_flag, a);
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < 2; ++cc) {
+              uint32_t (&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
+              tmem_ld32(ocol + 32 * cc, w);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+              tmem_st32(ocol + 32 * cc, w);
+            }
+          }
+          tmem_st32(sc, pk);
         }
-        tmem_st32(tmem + lane_off + b3 * 128 + hc * 64, pk);
         if (first && pending) next_nkt = write_out(k + 1);
+        if (last) break;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
@@ -790,10 +822,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           s_phase ^= 1;
         }
         ++jt;
-      };
-      tile(0, std::true_type{});
-#pragma unroll 1
-      for (int j = 1; j < nkt; ++j) tile(j, std::false_type{});
+      }
+      if (last) break;
       out_bar = bar_o_done + 8 * (b3 == 0 ? kNS - 1 : b3 - 1);
       out_phase = b3 == 0 ? s_phase ^ 1 : s_phase;
       pending = true;
@@ -803,10 +833,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       out_l = l_run;
       nkt = next_nkt;
     }
-    if (pending) write_out(0);
   }
   tc_fence_before();
-  cluster_sync();  // neither CTA leaves while the other may still report to it
+  // Neither CTA leaves while the other may still report to it.  No data changes
+  // hands here, so outputs need not have landed: a release would wait for them
+  // (0.6 us).
+  cluster_sync_relaxed();
   tc_fence_after();
   if (warp == 0) tmem_dealloc<2>(tmem, kTmemCols);
 }
@@ -817,7 +849,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 using namespace pre;
 
 cudaError_t launch_prefill_window(const WindowPrefillArgs& args, const CUtensorMap* tm_q,
-                                  const CUtensorMap* tm_k, const CUtensorMap* tm_v, int64_t max_items, int num_sms, cudaStream_t stream) {
+                                  const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                                  int64_t max_items, int num_sms, cudaStream_t stream) {
   WindowPrefillArgs a = args;
   if (a.wait_ns == 0) a.wait_ns = kWaitLimitNs;
   constexpr int smem = WPlan::kSmemBytes + 1024;

@@ -1,6 +1,6 @@
 // pa_window_ptx.cuh -- inline-PTX wrappers of the windowed-attention and
 // norm-rotation kernels, beside pa_ptx.cuh's: packed fp32 arithmetic, groups
-// of asynchronous copies.
+// of asynchronous copies, a pair's commit, a barrier without memory order.
 #pragma once
 
 #include "pa_ptx.cuh"
@@ -22,6 +22,22 @@ __device__ __forceinline__ void cp_async_commit() {
 template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The pair's earlier tcgen05 work done: one arrival on the barrier at this
+// address in each of its two CTAs.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+      " [%0], %1;" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+// All threads of a cluster meet; orders no memory.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::
+                   : "memory");
 }
 
 // Two fp32 values in one 64-bit register, and arithmetic on both at once

@@ -86,6 +86,13 @@ def test_many_ragged_chunks(pa, cuda_device):
     Chunks(chunks, 4, 1, 37, 3, cuda_device).check(pa)
 
 
+def test_dozens_of_items_per_pair(pa, cuda_device):
+    """Every ring of the kernel goes around several times."""
+    rng = np.random.default_rng(6)
+    chunks = [(int(rng.integers(0, 300)), int(rng.integers(1, 60))) for _ in range(600)]
+    Chunks(chunks, 32, 4, 150, 3, cuda_device).check(pa)
+
+
 def test_a_long_window_needs_several_batches_of_block_ids(pa, cuda_device):
     Chunks([(9000, 70)], 2, 1, 10**6, 0, cuda_device).check(pa)
     Chunks([(14000, 33)], 2, 1, 8400, 700, cuda_device).check(pa)
