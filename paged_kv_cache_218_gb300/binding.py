@@ -94,9 +94,7 @@ class PAError(RuntimeError):
         self.status = status
 
 
-_pycall.setup(torch.Tensor, torch.bfloat16, torch.float32, torch.int32, torch.int64, torch.uint8,
-              getattr(torch._C, "_cuda_getCurrentRawStream", None),
-              getattr(torch._C, "_cuda_getDevice", None), PAError)
+_pycall.setup(PAError)
 
 
 def _check(fn: str, rc: int) -> None:

@@ -9,6 +9,7 @@ the runtime's entry-point query, so no -lcuda is needed.
 from __future__ import annotations
 
 import concurrent.futures
+import importlib.util
 import os
 import subprocess
 import sys
@@ -36,6 +37,14 @@ def _nvcc() -> str:
     return "nvcc"
 
 
+def _torch() -> str:
+    """torch's folder, found without importing it."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None:
+        raise RuntimeError("torch is not installed: _pycall needs its headers")
+    return spec.submodule_search_locations[0]
+
+
 def _stale(target: str, deps) -> bool:
     if not os.path.exists(target):
         return True
@@ -59,6 +68,20 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
                 cmd.insert(1, "-Xptxas=-v")
             jobs.append(cmd)
 
+    relink = force or bool(jobs)
+    # the extension's one source, beside them: torch's headers take it a while
+    torch = _torch()
+    cxx = os.environ.get("CXX", "g++")
+    py_src = os.path.join(CSRC, "pa_pycall.cpp")
+    py_obj = os.path.join(BUILD, "pa_pycall.o")
+    cuda = os.path.dirname(os.path.dirname(nvcc)) if os.path.sep in nvcc else "/usr/local/cuda"
+    if force or _stale(py_obj, [py_src, os.path.join(CSRC, "..", "..", "include", "pa.h"),
+                                os.path.join(torch, "version.py")]):
+        jobs.append([cxx, "-O2", "-std=c++17", "-fPIC", "-Wall",
+                     "-I" + sysconfig.get_paths()["include"],
+                     "-isystem", os.path.join(torch, "include"),
+                     "-isystem", os.path.join(cuda, "include"), "-c", py_src, "-o", py_obj])
+
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
@@ -68,17 +91,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             if verbose or r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
             if r.returncode != 0:
-                raise RuntimeError("nvcc failed: " + " ".join(cmd))
-    if force or jobs or _stale(LIB, objs):
+                raise RuntimeError("compiler failed: " + " ".join(cmd))
+    if relink or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs], check=True)
         os.replace(tmp, LIB)
-    src = os.path.join(CSRC, "pa_pycall.cpp")
-    if force or _stale(PYCALL, [src, os.path.join(CSRC, "..", "..", "include", "pa.h")]):
+    if force or _stale(PYCALL, [py_obj]):
         tmp = PYCALL + f".tmp{os.getpid()}"
-        subprocess.run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-                        "-I" + sysconfig.get_paths()["include"], src, "-o", tmp, "-L" + PKG,
-                        "-l:libpa.so", "-Wl,-rpath,$ORIGIN"], check=True)
+        lib = os.path.join(torch, "lib")
+        subprocess.run([cxx, "-shared", py_obj, "-o", tmp, "-L" + PKG, "-l:libpa.so", "-L" + lib,
+                        "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+                        "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib], check=True)
         os.replace(tmp, PYCALL)
     return LIB
 
