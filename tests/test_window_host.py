@@ -180,3 +180,20 @@ def test_stalled_prefill_refuses_its_limit(lib, limit):
     args = {n: PREFILL[n] for n in names} | {"limit": limit, "stream": None}
     types = {n: PREFILL_T[n] for n in names} | {"limit": ctypes.c_uint, "stream": V}
     assert call(lib.pa_test_prefill_window_stalled, args, types) == INVALID
+
+
+@pytest.mark.parametrize("bad,error", [
+    (lambda t: None, TypeError), (lambda t: 3, TypeError), (lambda t: t.half(), TypeError),
+    (lambda t: t, ValueError), (lambda t: t.to("meta"), ValueError),
+    (lambda t: t.to_sparse(), ValueError), (lambda t: t[0], ValueError)])
+def test_python_calls_refuse_what_is_no_cuda_tensor(lib, bad, error):
+    torch = pytest.importorskip("torch")
+    from paged_kv_cache_218_gb300 import binding as pa
+    x = bad(torch.zeros(2, 4, 64, dtype=torch.bfloat16))
+    for call_it in (lambda: pa.pa_decode_window(x, x, x, x, x, x, 8, 0, 0.1),
+                    lambda: pa.pa_prefill_window(x, x, x, x, x, x, x, x, 1, 8, 0, 0.1),
+                    lambda: pa.pa_qk_norm_rope_cache(x, x, x, x, None, None, None, None, None,
+                                                     k_out=x),
+                    lambda: pa.pa_qk_norm_rope_cache_fp8(x, x, x, x, None, None, x, x, x, x, x)):
+        with pytest.raises(error):
+            call_it()
