@@ -414,7 +414,8 @@ int pa_decode_window(void *out, const void *q, const void *k_cache, const void *
  * sees may hold anything (the K/V of keys that some see must be finite).
  * Arguments, shapes (head_dim 128, a group dividing 128), outputs and the
  * treatment of inconsistent chunks as pa_prefill_chunk; window and sinks as
- * pa_decode_window.  No workspace; equal calls give equal bits.
+ * pa_decode_window.  No workspace; equal calls give equal bits (calls of few
+ * query tokens run on the decode kernel, whose weights are not rounded to bf16).
  */
 int pa_prefill_window(void *out, const void *q, const void *k_cache, const void *v_cache,
                       const int32_t *block_tables, int max_blocks_per_seq,

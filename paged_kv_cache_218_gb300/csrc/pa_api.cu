@@ -1439,6 +1439,39 @@ static int prefill_window_impl(void* out, const void* q, const void* k_cache, co
     return PA_ERR_INVALID;
   DeviceInfo* d;
   if (int rc = current_device_info(&d)) return rc;
+  // Few queries go through the decode kernel one by one: up to a CTA of eight
+  // warps on every SM, keys read again for each query of a chunk cost less than
+  // tiles that hold few rows (us, at 8 / 32 / 128 (token, kv head) pairs: window
+  // 128 4.5 / 4.6 / 4.8 against 6.9 / 7.0 / 7.0 in tiles, 1024 6.2 / 6.7 / 9.4
+  // against 12.7 / 12.7 / 12.9, 4096 8.3 / 10.7 / 25.5 against 30.0 / 30.1 / 31.9;
+  // at 192 pairs 8.6, 15.6 and 31.8 against 7.1, 12.9 and 31.9).
+  if (!stall_loads && static_cast<int64_t>(total_q_tokens) * num_kv_heads <= d->num_sms) {
+    WindowDecodeArgs w{};
+    w.out = static_cast<__nv_bfloat16*>(out);
+    w.q = static_cast<const __nv_bfloat16*>(q);
+    w.k = static_cast<const __nv_bfloat16*>(k_cache);
+    w.v = static_cast<const __nv_bfloat16*>(v_cache);
+    w.block_tables = block_tables;
+    w.seq_lens = seq_lens;
+    w.out_lse = out_lse;
+    w.err = d->err;
+    w.num_blocks = num_blocks;
+    w.max_blocks = max_blocks_per_seq;
+    w.num_seqs = total_q_tokens;
+    w.num_q_heads = num_q_heads;
+    w.num_kv_heads = num_kv_heads;
+    w.group = num_q_heads / num_kv_heads;
+    w.window = window;
+    w.sinks = sinks;
+    w.scale_log2 = scale * 1.4426950408889634f;
+    w.cu_q_lens = cu_q_lens;
+    w.q_start_pos = q_start_pos;
+    w.num_chunks = num_chunks;
+    return launch_decode_window_chunks(w, d->num_sms, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+  }
   WindowPrefillArgs a{};
   a.out = static_cast<__nv_bfloat16*>(out);
   a.block_tables = block_tables;

@@ -29,7 +29,20 @@ struct WindowDecodeArgs {
   int sinks;   // and keys [0, sinks)
   float scale_log2;
   int splits;  // CTAs (a cluster) per (sequence, kv head); set by the launcher
+  // Chunks of queries (pa_prefill_window's few tokens): a "sequence" is a query
+  // token, and num_seqs the number of tokens; tables and lengths are the chunks'.
+  const int32_t* cu_q_lens;    // [num_chunks + 1]
+  const int32_t* q_start_pos;  // [num_chunks]
+  int num_chunks;
 };
+
+// Whether a chunk's query rows [q0, q1), first position and length agree with
+// one another and with the call.
+__device__ __forceinline__ bool chunk_ok(int q0, int q1, int p0, int n, int total_q,
+                                         int max_blocks) {
+  return q0 >= 0 && q1 <= total_q && q1 >= q0 && p0 >= 0 && n >= 0 && q1 - q0 <= n &&
+         p0 <= n - (q1 - q0) && n <= max_blocks * kBlockSize;
+}
 
 // Norms, position rotation and slot scatter (pa_qk_norm_rope_cache).
 struct RopeArgs {
@@ -70,6 +83,8 @@ struct WindowPrefillArgs : PrefillArgs {
 cudaError_t launch_norm_rope(const RopeArgs& a, bool kv_fp8, int num_sms, cudaStream_t stream);
 cudaError_t launch_decode_window(const WindowDecodeArgs& a, int head_dim, int num_sms,
                                  cudaStream_t stream);
+cudaError_t launch_decode_window_chunks(const WindowDecodeArgs& a, int num_sms,
+                                        cudaStream_t stream);  // head_dim 128
 cudaError_t launch_prefill_window(const WindowPrefillArgs& a, const CUtensorMap* tm_q,
                                   const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                   int64_t max_items, int num_sms, cudaStream_t stream);

@@ -42,6 +42,9 @@
 // a sequence's blocks in turn; their (m, l, O) are joined in shared memory,
 // then across the cluster through distributed shared memory, always in the same
 // order: the call needs no workspace, and its bits do not depend on timing.
+//
+// A prefill call of few query tokens comes here too, a token as a sequence of
+// its own that ends with it, and finds its chunk with one more round trip.
 #include <float.h>
 #include <math.h>
 
@@ -88,7 +91,30 @@ struct DecodePlan {
   static_assert(2 * 8 * D * 4 <= kRing, "outputs in the ring");
 };
 
-template <int D, int W>
+// The chunk that holds query token s: its table's row, and the number of keys
+// up to the token's own; -1 where no consistent chunk does.  Called by a whole
+// warp.
+__device__ __forceinline__ int find_chunk(const WindowDecodeArgs& a, int s, int lane, int& n) {
+  for (int c0 = 0; c0 < a.num_chunks; c0 += 32) {
+    const int c = c0 + lane;
+    int q0 = 0, q1 = 0, p0 = 0;
+    bool mine = false;
+    if (c < a.num_chunks) {
+      q0 = a.cu_q_lens[c];
+      q1 = a.cu_q_lens[c + 1];
+      p0 = a.q_start_pos[c];
+      mine = q0 <= s && s < q1 && chunk_ok(q0, q1, p0, a.seq_lens[c], a.num_seqs, a.max_blocks);
+    }
+    const unsigned at = __ballot_sync(0xffffffffu, mine);
+    if (at == 0) continue;
+    n = __shfl_sync(0xffffffffu, p0 + s - q0 + 1, __ffs(at) - 1);
+    return c0 + __ffs(at) - 1;
+  }
+  return -1;
+}
+
+// C: the queries are those of chunks (see WindowDecodeArgs).
+template <int D, int W, bool C>
 __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecodeArgs a) {
   using P = DecodePlan<D, W>;
   constexpr int KJ = D / 32;  // 16-byte pieces of a K row per lane
@@ -124,11 +150,22 @@ __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecod
     if (g >= G) qf[j] = make_uint4(0, 0, 0, 0);
   }
 
-  int n = a.seq_lens[s];
-  const int cap = a.max_blocks * kBlockSize;
-  if (n < 0 || n > cap) {
-    if (threadIdx.x == 0 && rank == 0 && kvh == 0) atomicOr(a.err, PA_DEVERR_SEQ_LEN);
-    n = n < 0 ? 0 : cap;
+  int n, table_row = s;
+  if constexpr (C) {
+    if (blockIdx.x == 0 && warp == 0)
+      for (int c = lane; c < a.num_chunks; c += 32)
+        if (!chunk_ok(a.cu_q_lens[c], a.cu_q_lens[c + 1], a.q_start_pos[c], a.seq_lens[c],
+                      a.num_seqs, a.max_blocks))
+          atomicOr(a.err, PA_DEVERR_CHUNK);
+    table_row = find_chunk(a, s, lane, n);
+    if (table_row < 0) return;  // (every CTA of the cluster) a row of no chunk stays
+  } else {
+    n = a.seq_lens[s];
+    const int cap = a.max_blocks * kBlockSize;
+    if (n < 0 || n > cap) {
+      if (threadIdx.x == 0 && rank == 0 && kvh == 0) atomicOr(a.err, PA_DEVERR_SEQ_LEN);
+      n = n < 0 ? 0 : cap;
+    }
   }
   const int lo = n > a.window ? n - a.window : 0;  // first key of the window
   const int ns = a.sinks < n ? a.sinks : n;        // visible sinks
@@ -143,7 +180,7 @@ __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecod
   const int head_bytes = kvh * (D * 2) + (lane % (D / 8)) * 16;
   const char* const kbase = reinterpret_cast<const char*>(a.k) + head_bytes;
   const char* const vbase = reinterpret_cast<const char*>(a.v) + head_bytes;
-  const int32_t* const table = a.block_tables + static_cast<int64_t>(s) * a.max_blocks;
+  const int32_t* const table = a.block_tables + static_cast<int64_t>(table_row) * a.max_blocks;
 
   float o[4 * VH][4];
 #pragma unroll
@@ -369,7 +406,7 @@ __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecod
   cluster_sync();  // no CTA leaves while another may still read its shared memory
 }
 
-template <int D, int W>
+template <int D, int W, bool C = false>
 cudaError_t launch(const WindowDecodeArgs& a, cudaStream_t stream) {
   {  // raise the kernel's shared-memory limit once per device
     static std::mutex mu;
@@ -380,7 +417,7 @@ cudaError_t launch(const WindowDecodeArgs& a, cudaStream_t stream) {
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!set_for[dev]) {
-      e = cudaFuncSetAttribute(decode_window_kernel<D, W>,
+      e = cudaFuncSetAttribute(decode_window_kernel<D, W, C>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                DecodePlan<D, W>::kBytes);
       if (e != cudaSuccess) return e;
@@ -402,7 +439,7 @@ cudaError_t launch(const WindowDecodeArgs& a, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.splits > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_window_kernel<D, W>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_window_kernel<D, W, C>, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -415,7 +452,7 @@ struct Residency {
 };
 static_assert(kMaxWindowSplit == 1 << 4, "cluster sizes");
 
-template <int D>
+template <int D, bool C>
 cudaError_t residency(int num_sms, Residency* out) {
   static std::mutex mu;
   static Residency by_device[64];
@@ -427,7 +464,7 @@ cudaError_t residency(int num_sms, Residency* out) {
   Residency& r = by_device[dev];
   if (!r.ready) {
     constexpr int smem = DecodePlan<D, 8>::kBytes;
-    const auto kernel = decode_window_kernel<D, 8>;
+    const auto kernel = decode_window_kernel<D, 8, C>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     int ctas = 0;
@@ -460,10 +497,10 @@ cudaError_t residency(int num_sms, Residency* out) {
   return cudaSuccess;
 }
 
-template <int D>
+template <int D, bool C = false>
 cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
   Residency res;
-  const cudaError_t e = residency<D>(num_sms, &res);
+  const cudaError_t e = residency<D, C>(num_sms, &res);
   if (e != cudaSuccess) return e;
   // Blocks that a sequence can attend at most.
   const int64_t visible = std::min<int64_t>(
@@ -471,7 +508,7 @@ cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
                         (static_cast<int64_t>(a.window) + kBlockSize - 1) / kBlockSize + 1);
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   a.splits = 1;
-  if (units <= res.clusters[0]) {
+  if (C || units <= res.clusters[0]) {
     // Few units: eight warps each, and as large clusters of such CTAs as all run
     // at once and find a block for every warp; none for a few blocks, whose
     // joining costs more (us, at 8 / 16 / 32 / 64 units: 17 blocks 4.7 / 4.8 /
@@ -480,7 +517,7 @@ cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
     if (visible > 24)
       for (int k = 1; k < 5; ++k)
         if (units <= res.clusters[k] && (8 << k) <= visible) a.splits = 1 << k;
-    return launch<D, 8>(a, stream);
+    return launch<D, 8, C>(a, stream);
   }
   // Many units: a unit costs some 4 us before its first block arrives, which
   // many short units at once hide better than few long ones; long units hide it
@@ -503,6 +540,11 @@ cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
 }
 
 }  // namespace
+
+cudaError_t launch_decode_window_chunks(const WindowDecodeArgs& a, int num_sms,
+                                        cudaStream_t stream) {
+  return choose<128, true>(a, num_sms, stream);
+}
 
 cudaError_t launch_decode_window(const WindowDecodeArgs& a, int head_dim, int num_sms,
                                  cudaStream_t stream) {

@@ -49,7 +49,6 @@
 // issue is on the critical path (0.89 us a tile rolled by two).
 // Every mbarrier wait is bounded, as in pa_prefill_body.cuh.
 #include <mutex>
-#include <type_traits>
 
 #include "pa_prefill_body.cuh"
 #include "pa_window.h"
@@ -105,12 +104,6 @@ struct Cursor {
   int chunk;
 };
 
-__device__ __forceinline__ bool chunk_ok(const WindowPrefillArgs& a, int q0, int q1, int p0,
-                                         int n) {
-  return q0 >= 0 && q1 <= a.total_q && q1 >= q0 && p0 >= 0 && n >= 0 && q1 - q0 <= n &&
-         p0 <= n - (q1 - q0) && n <= a.max_blocks * kBlockSize;
-}
-
 static_assert(kBlockSize == 16, "shifts below");
 __device__ __forceinline__ int blocks_of(int keys) { return (keys + 15) >> 4; }
 
@@ -155,7 +148,7 @@ __device__ __forceinline__ Item next_item(const WindowPrefillArgs& a, Cursor& cu
       q0 = a.cu_q_lens[c];
       q1 = a.cu_q_lens[c + 1];
       p0 = a.q_start_pos[c];
-      if (chunk_ok(a, q0, q1, p0, a.seq_lens[c]))
+      if (chunk_ok(q0, q1, p0, a.seq_lens[c], a.total_q, a.max_blocks))
         items = ((q1 - q0 + rows - 1) >> rs) * a.num_kv_heads;
       else if (flag)
         atomicOr(a.err, PA_DEVERR_CHUNK);

@@ -1,4 +1,5 @@
-"""pa_prefill_window against its fp64 definition: window, sink and chunk edges
+"""pa_prefill_window against its fp64 definition (calls of few and of many
+query tokens and kv heads, which take different kernels): window, sink and chunk edges
 on both sides of block and tile borders, every group size, more items than CTA
 pairs, ragged and empty chunks, garbage in everything that no query sees,
 inconsistent metadata, the bounded waits, streams, graphs and refusals."""
@@ -58,6 +59,9 @@ class Chunks:
         R.assert_within(out, ro, to, "out")
 
 
+# Few (token, kv head) pairs in a call, and many: more than there are SMs.
+both = pytest.mark.parametrize("hkv", [1, 8])
+
 MIX = [(0, 1), (0, 40), (24, 72), (1000, 5), (513, 260), (300, 0), (17, 130)]
 
 
@@ -73,6 +77,25 @@ def test_window_edges(pa, cuda_device, window, sinks, Hq, Hkv):
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 1), (4, 1), (8, 1), (3, 3), (16, 2), (6, 3)])
 def test_groups(pa, cuda_device, Hq, Hkv):
     Chunks([(70, 300), (5, 33)], Hq, Hkv, 100, 4, cuda_device, seed=Hq).check(pa)
+
+
+FEW = {"one": [(1000, 1)], "first": [(0, 1)], "some": [(5, 3), (0, 0), (700, 7), (31, 2)],
+       "draft": [(2047, 8)], "many": [(17 * i % 400, i % 3) for i in range(70)]}
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (17, 5), (64, 0), (200, 16),
+                                          (1500, 700), (2**31 - 1, 2**31 - 1)])
+@pytest.mark.parametrize("name", FEW)
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (1, 1), (16, 2)])
+def test_few_queries(pa, cuda_device, window, sinks, name, Hq, Hkv):
+    Chunks(FEW[name], Hq, Hkv, window, sinks, cuda_device, seed=window % 1000).check(pa)
+
+
+@pytest.mark.parametrize("Hkv", [1, 2, 3])
+def test_around_the_number_of_sms(pa, cuda_device, Hkv):
+    sms = torch.cuda.get_device_properties(cuda_device).multi_processor_count
+    for tokens in (sms // Hkv - 1, sms // Hkv, sms // Hkv + 1):
+        Chunks([(300, tokens - 40), (2, 40)], 4 * Hkv, Hkv, 90, 3, cuda_device).check(pa)
 
 
 @pytest.mark.parametrize("window,sinks", [(300, 4), (1024, 40), (50, 0)])
@@ -99,13 +122,15 @@ def test_a_long_window_needs_several_batches_of_block_ids(pa, cuda_device):
 
 
 @pytest.mark.parametrize("beyond", [1, 9, 16, 100])
-def test_later_keys_of_the_sequence_stay_unseen(pa, cuda_device, beyond):
+@both
+def test_later_keys_of_the_sequence_stay_unseen(pa, cuda_device, beyond, hkv):
     """The cache holds keys behind the chunk's: their slots are NaN here, their blocks no ids."""
-    Chunks([(100, 77), (32, 16)], 4, 1, 60, 2, cuda_device, beyond=beyond).check(pa)
+    Chunks([(100, 77), (32, 16)], 4 * hkv, hkv, 60, 2, cuda_device, beyond=beyond).check(pa)
 
 
-def test_scores_that_climb_along_the_keys(pa, cuda_device):
-    c = Chunks([(700, 130)], 4, 1, 600, 4, cuda_device)
+@both
+def test_scores_that_climb_along_the_keys(pa, cuda_device, hkv):
+    c = Chunks([(700, 130)], 4 * hkv, hkv, 600, 4, cuda_device)
     c.q = c.q.abs().clamp(min=0.5)
     for b in range(c.bt.shape[1]):
         i = int(c.bt[0, b])
@@ -117,8 +142,9 @@ def test_scores_that_climb_along_the_keys(pa, cuda_device):
     c.check(pa)
 
 
-def test_infinite_scores(pa, cuda_device):
-    c = Chunks([(0, 60)], 2, 1, 20, 0, cuda_device)
+@both
+def test_infinite_scores(pa, cuda_device, hkv):
+    c = Chunks([(0, 60)], 2 * hkv, hkv, 20, 0, cuda_device)
     c.q[:] = 1.0
     i = int(c.bt[0, 1])
     c.kc[i, 3] = -float("inf")  # key 19: weight exactly 0
@@ -148,8 +174,9 @@ def test_whole_sequence_gives_pa_prefill_chunks_result(pa, cuda_device):
     R.assert_within(lse, R.to64(ref_lse), 2 * tl, "lse")
 
 
-def test_inconsistent_chunks_are_skipped_and_flagged(pa, cuda_device):
-    c = Chunks([(10, 40), (0, 30), (50, 20), (7, 33)], 4, 1, 25, 2, cuda_device)
+@both
+def test_inconsistent_chunks_are_skipped_and_flagged(pa, cuda_device, hkv):
+    c = Chunks([(10, 40), (0, 30), (50, 20), (7, 33)], 4 * hkv, hkv, 25, 2, cuda_device)
     good, good_lse = c.call(pa)
     rows = [slice(0, 40), slice(40, 70), slice(70, 90), slice(90, 123)]
     cap = c.bt.shape[1] * 16
@@ -177,8 +204,9 @@ def test_inconsistent_chunks_are_skipped_and_flagged(pa, cuda_device):
 
 
 @pytest.mark.parametrize("bad", [-1, -2**31, 2**31 - 1])
-def test_bad_block_reads_as_zeros_and_is_flagged(pa, cuda_device, bad):
-    c = Chunks([(40, 50)], 4, 2, 60, 4, cuda_device)
+@both
+def test_bad_block_reads_as_zeros_and_is_flagged(pa, cuda_device, bad, hkv):
+    c = Chunks([(40, 50)], 2 * hkv, hkv, 60, 4, cuda_device)
     zero = c.kc.shape[0] - 1
     c.kc[zero], c.vc[zero] = 0, 0
     c.bt[0, 3] = zero
@@ -217,10 +245,33 @@ def test_equal_bits_on_streams_and_graph_replays(pa, cuda_device):
     assert torch.equal(got[1][0], want) and torch.equal(got[1][1], want_lse)
 
 
-def test_rows_outside_the_chunks_stay(pa, cuda_device):
-    c = Chunks([(30, 40), (0, 20)], 4, 1, 25, 2, cuda_device)
-    out = torch.full((70, 4, D), 7.0, dtype=torch.bfloat16, device=cuda_device)
-    lse = torch.full((70, 4), 7.0, device=cuda_device)
+def test_few_queries_in_a_graph_see_new_chunks(pa, cuda_device):
+    """A replay reads the chunks' positions and lengths anew."""
+    c = Chunks([(50, 3), (7, 2)], 8, 2, 30, 2, cuda_device)
+    want, want_lse = c.call(pa)
+    o, l = torch.empty_like(want), torch.empty_like(want_lse)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.call(pa, o, l)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(l, want_lse)
+    c.start.sub_(1)
+    c.lens.sub_(1)
+    c.kc.nan_to_num_()
+    c.vc.nan_to_num_()
+    c.bt.clamp_(0, c.kc.shape[0] - 1)
+    want, want_lse = c.call(pa)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o, want) and torch.equal(l, want_lse)
+
+
+@both
+def test_rows_outside_the_chunks_stay(pa, cuda_device, hkv):
+    c = Chunks([(30, 40), (0, 20)], 4 * hkv, hkv, 25, 2, cuda_device)
+    out = torch.full((70, 4 * hkv, D), 7.0, dtype=torch.bfloat16, device=cuda_device)
+    lse = torch.full((70, 4 * hkv), 7.0, device=cuda_device)
     c.q = torch.cat([c.q, c.q[:10]])  # ten more query rows, of no chunk
     c.call(pa, out, lse)
     torch.cuda.synchronize()
