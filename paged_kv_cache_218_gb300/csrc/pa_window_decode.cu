@@ -519,17 +519,32 @@ cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
         if (units <= res.clusters[k] && (8 << k) <= visible) a.splits = 1 << k;
     return launch<D, 8, C>(a, stream);
   }
-  // Many units: a unit costs some 4 us before its first block arrives, which
-  // many short units at once hide better than few long ones; long units hide it
-  // themselves, and eight warps on each spread lengths that differ.  (us, with
-  // 1 / 2 / 4 / 8 warps: 1024 units of 17 blocks 28 / 29 / 33 / 39; of 66 90 /
-  // 82 / 85 / 88, with lengths from 300 keys on 75 / 72 / 69 / 70; 2048 units of
-  // 258 622 / 600 / 601 / 588, ragged 328 / 313 / 298 / 291.)
-  const int64_t slots = static_cast<int64_t>(res.clusters[0]) * 8;
+  // Many units: few warps on each keep more units at once and hide what a unit
+  // costs before its first block arrives; many warps spread units of different
+  // lengths.  The number with the least estimated time (us): units come in
+  // rounds of as many as run at once; a round's blocks share the memory's 7.1
+  // TB/s, a block takes a warp 0.4 us at least, a further round costs 2, and a
+  // quarter of a block's time on each of a warp's blocks stands for lengths that
+  // differ.  Over 160 to 1760 units of 14 to 108 blocks, head_dim 64 and 128, its
+  // choices take 2.7 % longer than the best one's for equal lengths and 6 % for
+  // lengths from nothing on, on average; eight warps always 16 and 15, four 7 and
+  // 9, two 12 and 41, one 21 and 83.  (us, with 1 / 2 / 4 / 8 warps: 1024 units
+  // of 66 blocks, some shorter, 76.3 / 71.5 / 69.3 / 69.5; 2048 of 258 629 / 609 /
+  // 605 / 600.)
+  const double slots = static_cast<double>(res.clusters[0]) * 8;  // warps at once
+  const double block_us = slots * (2 * kBlockSize * D * 2) / 7.1e6;
   int w = 8;
-  if (visible < 120) {
-    const int least = visible > 32 ? 2 : 1;
-    while (w > least && units * w > slots) w /= 2;
+  double least = 0;
+  for (int k = 8; k > 0; k /= 2) {
+    const int64_t at_once = static_cast<int64_t>(slots) / k;
+    const int64_t full = units / at_once, rest = units % at_once;
+    const double blocks = static_cast<double>(visible) / k;
+    double us = blocks * (0.25 + full * block_us) + 2.0 * (full + (rest > 0 ? 1 : 0));
+    if (rest > 0) us += blocks * std::max(0.4, block_us * rest / at_once);
+    if (k == 8 || us < least) {
+      w = k;
+      least = us;
+    }
   }
   switch (w) {
     case 1: return launch<D, 1>(a, stream);
