@@ -521,12 +521,12 @@ cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
   }
   // Many units: few warps on each keep more units at once and hide what a unit
   // costs before its first block arrives; many warps spread units of different
-  // lengths.  The number with the least estimated time (us): units come in
-  // rounds of as many as run at once; a round's blocks share the memory's 7.1
-  // TB/s, a block takes a warp 0.4 us at least, a further round costs 2, and a
-  // quarter of a block's time on each of a warp's blocks stands for lengths that
-  // differ.  Over 160 to 1760 units of 14 to 108 blocks, head_dim 64 and 128, its
-  // choices take 2.7 % longer than the best one's for equal lengths and 6 % for
+  // lengths.  The number with the least estimated time (us; fewer only where that
+  // saves a percent): units come in rounds of as many as run at once; a round's
+  // blocks share the memory's 7.1 TB/s, a block takes a warp 0.4 us at least, a
+  // further round costs 2, and a quarter of a block's time on each of a warp's
+  // blocks stands for lengths that differ.  Over 160 to 1760 units of 14 to 108 blocks, head_dim 64 and 128, its
+  // choices take 3.3 % longer than the best one's for equal lengths and 6 % for
   // lengths from nothing on, on average; eight warps always 16 and 15, four 7 and
   // 9, two 12 and 41, one 21 and 83.  (us, with 1 / 2 / 4 / 8 warps: 1024 units
   // of 66 blocks, some shorter, 76.3 / 71.5 / 69.3 / 69.5; 2048 of 258 629 / 609 /
@@ -541,7 +541,7 @@ cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
     const double blocks = static_cast<double>(visible) / k;
     double us = blocks * (0.25 + full * block_us) + 2.0 * (full + (rest > 0 ? 1 : 0));
     if (rest > 0) us += blocks * std::max(0.4, block_us * rest / at_once);
-    if (k == 8 || us < least) {
+    if (k == 8 || us < 0.99 * least) {
       w = k;
       least = us;
     }
