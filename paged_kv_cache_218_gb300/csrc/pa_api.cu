@@ -1444,8 +1444,12 @@ static int prefill_window_impl(void* out, const void* q, const void* k_cache, co
   // tiles that hold few rows (us, at 8 / 32 / 128 (token, kv head) pairs: window
   // 128 4.5 / 4.6 / 4.8 against 6.9 / 7.0 / 7.0 in tiles, 1024 6.2 / 6.7 / 9.4
   // against 12.7 / 12.7 / 12.9, 4096 8.3 / 10.7 / 25.5 against 30.0 / 30.1 / 31.9;
-  // at 192 pairs 8.6, 15.6 and 31.8 against 7.1, 12.9 and 31.9).
-  if (!stall_loads && static_cast<int64_t>(total_q_tokens) * num_kv_heads <= d->num_sms) {
+  // at 192 pairs 15.3 against 12.9 and 31.8 against 31.9 in the last two).  In
+  // short windows up to two CTAs of four warps (304 pairs: window 32 4.7 against
+  // 6.5, 128 5.9 against 7.1, 512 10.1 against 10.0; 400 pairs 5.9, 7.9 and 18.9).
+  const int64_t pairs = static_cast<int64_t>(total_q_tokens) * num_kv_heads;
+  const int64_t visible = static_cast<int64_t>(window) / kBlockSize + sinks / kBlockSize;
+  if (!stall_loads && (pairs <= d->num_sms || (pairs <= 2 * d->num_sms && visible <= 20))) {
     WindowDecodeArgs w{};
     w.out = static_cast<__nv_bfloat16*>(out);
     w.q = static_cast<const __nv_bfloat16*>(q);

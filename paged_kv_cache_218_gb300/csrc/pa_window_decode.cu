@@ -508,7 +508,7 @@ cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
                         (static_cast<int64_t>(a.window) + kBlockSize - 1) / kBlockSize + 1);
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   a.splits = 1;
-  if (C || units <= res.clusters[0]) {
+  if (units <= res.clusters[0]) {
     // Few units: eight warps each, and as large clusters of such CTAs as all run
     // at once and find a block for every warp; none for a few blocks, whose
     // joining costs more (us, at 8 / 16 / 32 / 64 units: 17 blocks 4.7 / 4.8 /
@@ -519,6 +519,7 @@ cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
         if (units <= res.clusters[k] && (8 << k) <= visible) a.splits = 1 << k;
     return launch<D, 8, C>(a, stream);
   }
+  if constexpr (C) return launch<D, 4, C>(a, stream);
   // Many units: few warps on each keep more units at once and hide what a unit
   // costs before its first block arrives; many warps spread units of different
   // lengths.  The number with the least estimated time (us; fewer only where that

@@ -59,7 +59,7 @@ class Chunks:
         R.assert_within(out, ro, to, "out")
 
 
-# Few (token, kv head) pairs in a call, and many: more than there are SMs.
+# Few (token, kv head) pairs in a call, and many: more than two for each SM.
 both = pytest.mark.parametrize("hkv", [1, 8])
 
 MIX = [(0, 1), (0, 40), (24, 72), (1000, 5), (513, 260), (300, 0), (17, 130)]
@@ -92,10 +92,12 @@ def test_few_queries(pa, cuda_device, window, sinks, name, Hq, Hkv):
 
 
 @pytest.mark.parametrize("Hkv", [1, 2, 3])
-def test_around_the_number_of_sms(pa, cuda_device, Hkv):
-    sms = torch.cuda.get_device_properties(cuda_device).multi_processor_count
+@pytest.mark.parametrize("times", [1, 2])
+@pytest.mark.parametrize("window,sinks", [(90, 3), (400, 20)])
+def test_around_the_number_of_sms(pa, cuda_device, Hkv, times, window, sinks):
+    sms = times * torch.cuda.get_device_properties(cuda_device).multi_processor_count
     for tokens in (sms // Hkv - 1, sms // Hkv, sms // Hkv + 1):
-        Chunks([(300, tokens - 40), (2, 40)], 4 * Hkv, Hkv, 90, 3, cuda_device).check(pa)
+        Chunks([(300, tokens - 40), (2, 40)], 4 * Hkv, Hkv, window, sinks, cuda_device).check(pa)
 
 
 @pytest.mark.parametrize("window,sinks", [(300, 4), (1024, 40), (50, 0)])
