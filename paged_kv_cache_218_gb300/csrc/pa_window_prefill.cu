@@ -48,6 +48,8 @@
 // item's ends took 3.9 us; now 2.7.  Only the products stay unrolled: their
 // issue is on the critical path (0.89 us a tile rolled by two).
 // Every mbarrier wait is bounded, as in pa_prefill_body.cuh.
+#include <float.h>
+
 #include <mutex>
 
 #include "pa_prefill_body.cuh"
@@ -59,7 +61,9 @@ namespace pre {
 namespace {
 
 constexpr uint64_t kSettleNs = 1000000;  // far longer than any copy takes
-constexpr float kFloor = -1e30f;  // reference maximum of a row that saw nothing yet
+// Reference maximum (log2 units) of a row that saw nothing yet: the lowest finite
+// fp32, so that no visible score lies below it; hidden scores (-inf) weigh 0.
+constexpr float kFloor = -FLT_MAX;
 
 // Shared memory of one CTA of a pair: two Q tiles, four K and three V half
 // tiles, an output tile, block ids of both loaders, the softmax's exchange, barriers.

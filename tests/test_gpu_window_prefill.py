@@ -315,3 +315,37 @@ def test_refusals(pa, cuda_device):
         assert e.value.status == pa.PA_ERR_INVALID
     torch.cuda.synchronize()
     assert (out == 3).all() and (lse == 3).all() and pa.pa_device_error_flags() == 0
+
+
+def equal_scores(pa, device, hkv, q, k, ahead):
+    """300 queries of q over keys of k, 128 columns each, at scale 1; `ahead`:
+    key 200 has half of k.  All partial sums are exact, so scores are equal:
+    weights 1 on every visible key, from query 200 on with `ahead` on that one
+    alone (the others lose by more than 2^7 in log2 units).  Out: one rounding
+    to bf16, 300 fp32 additions of values, a division.  lse: the rounding of
+    the score in base 2 and back, four steps of 2^-24."""
+    c = Chunks([(0, 300)], 2 * hkv, hkv, 300, 0, device)
+    c.scale = 1.0
+    c.q[:] = q
+    c.kc[:] = k
+    if ahead:
+        c.kc[int(c.bt[0, 200 // 16]), 200 % 16] = k / 2
+    out, lse = c.call(pa)
+    torch.cuda.synchronize()
+    assert pa.pa_device_error_flags() == 0
+    v = R.to64(c.vc[c.bt[0, :19].long()]).reshape(-1, hkv, D)[:300].repeat(2, 1)
+    count = np.arange(1.0, 301)[:, None, None]
+    ref, score = v.cumsum(0) / count, np.full((300, 2 * hkv), float(D * q * k))
+    ref_lse = score + np.log(count[:, :, 0])
+    if ahead:
+        ref[200:], ref_lse[200:] = v[200], score[200:] / 2
+    R.assert_within(lse, ref_lse, 2.0**-22 * np.abs(ref_lse), "lse")
+    R.assert_within(out, ref, (2.0**-8 + 2.0**-21) * np.abs(ref) + 300 * 2.0**-23 * np.abs(v).max(),
+                    "out")
+
+
+@pytest.mark.parametrize("ahead", [0, 1])
+@both
+def test_scores_near_the_lowest_fp32(pa, cuda_device, ahead, hkv):
+    """Scores of -2^126: lower than any reference maximum but the lowest fp32."""
+    equal_scores(pa, cuda_device, hkv, 2.0**99, -2.0**20, ahead)
