@@ -48,8 +48,6 @@
 // item's ends took 3.9 us; now 2.7.  Only the products stay unrolled: their
 // issue is on the critical path (0.89 us a tile rolled by two).
 // Every mbarrier wait is bounded, as in pa_prefill_body.cuh.
-#include <float.h>
-
 #include <mutex>
 
 #include "pa_prefill_body.cuh"
@@ -61,9 +59,10 @@ namespace pre {
 namespace {
 
 constexpr uint64_t kSettleNs = 1000000;  // far longer than any copy takes
-// Reference maximum (log2 units) of a row that saw nothing yet: the lowest finite
+// Reference maximum (log2 units) of a row that saw nothing yet: next to the lowest
 // fp32, so that no visible score lies below it; hidden scores (-inf) weigh 0.
-constexpr float kFloor = -FLT_MAX;
+constexpr float kFloor = -0x1.fffff0p127f;
+constexpr float kFarScore = 0x1p31f;  // (log2 units)
 
 // Shared memory of one CTA of a pair: two Q tiles, four K and three V half
 // tiles, an output tile, block ids of both loaders, the softmax's exchange, barriers.
@@ -638,6 +637,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = qd * 32 + lane;  // query row = tensor-memory lane
     const uint32_t lane_off = static_cast<uint32_t>(qd * 32) << 16;
     const float sl = a.scale_log2;
+    const float sl_pow2 = __uint_as_float(__float_as_uint(sl) & 0x7f800000u);  // in (sl / 2, sl]
+    const float floor_score = sl > 1.f ? kFloor / sl : kFloor, floor2 = floor_score * sl;
+    const float floor_n = fabsf(floor2) >= kFarScore ? floor_score * sl_pow2 : floor2;
     const uint32_t ocol = tmem + lane_off + kTmemO + hc * 64;
     uint32_t v[64];
     int jt = 0;                // tiles, over all items
@@ -735,7 +737,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // last and first visible virtual key of the row's window
       const int hi = min(pos, kmax - 1) - shift;
       const int lo = max(0, pos - (a.window - 1)) - shift;
-      float m_run = kFloor, l_run = 0.f;
+      // reference maximum: a score, in log2 units, and as the softmax subtracts it
+      float m_run = floor_score, m_run2 = floor2, n_run = floor_n;
+      float l_run = 0.f;
 #pragma unroll 1
       for (int j = 0; j < nkt || last; ++j) {
         const bool first = j == 0;
@@ -764,20 +768,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           tmem_ld64_max(sc, v, mloc);
-          mloc = mloc * sl;  // scale > 0 keeps the order
           red_max[(b * 2 + hc) * 128 + r] = mloc;
           named_barrier(1 + qd, 64);
-          const float mx = fmaxf(mloc, red_max[(b * 2 + (hc ^ 1)) * 128 + r]);
-          const float m_new = fmaxf(m_run, mx);
-          const bool move = m_new > m_run + kRescaleThreshold;
-          const float m_use = move ? m_new : m_run;
-          const float alpha = move ? fast_exp2(m_run - m_use) : 1.f;
+          // (scale > 0 keeps the order of scores)
+          const float m_new = fmaxf(m_run, fmaxf(mloc, red_max[(b * 2 + (hc ^ 1)) * 128 + r]));
+          const float m_new2 = m_new * sl;
+          const bool move = m_new2 > m_run2 + kRescaleThreshold;
+          const float alpha = move ? fast_exp2(m_run2 - m_new2) : 1.f;
+          // x = s sl - m sl by one fused multiply-add, whose product is exact and so
+          // differs from m_run2, which is rounded, by up to half a step of it: a
+          // common factor of a row's weights, within 2^64 below kFarScore.  From there
+          // on the factor leaves fp32, and neighbouring scores are 2^7 apart: any
+          // multiplier near sl tells them apart, and a power of two is exact.  (m_new2
+          // is far where m_run2 is: they differ by less than that step, or it moves.)
+          const bool far = fabsf(m_new2) >= kFarScore;
+          const float slx = far ? sl_pow2 : sl, n_new = far ? m_new * sl_pow2 : m_new2;
+          m_run = move ? m_new : m_run;
+          m_run2 = move ? m_new2 : m_run2;
+          n_run = move ? n_new : n_run;
           uint64_t rsp[2] = {0, 0};
           uint32_t pk[32];
-          const uint64_t sl2 = f32x2(sl, sl), nm2 = f32x2(-m_use, -m_use);
+          const uint64_t sl2 = f32x2(slx, slx), nm2 = f32x2(-n_run, -n_run);
 #pragma unroll
           for (int i = 0; i < 64; i += 2) {
-            // -inf (hidden) gives exactly 0: m_use is finite
+            // -inf (hidden) gives exactly 0: n_run is finite
             const uint64_t s2 = f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
             const float2 x = f32x2_parts(fma2(s2, sl2, nm2));
             const float e0 = fast_exp2(x.x), e1 = fast_exp2(x.y);
@@ -786,7 +800,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float2 rs = f32x2_parts(add2(rsp[0], rsp[1]));
           l_run = l_run * alpha + (rs.x + rs.y);
-          m_run = m_use;
           // O is rescaled only when a row maximum moved; PV of the previous
           // tile must have landed first (tile 0's PV overwrites O)
           if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -826,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       pending = true;
       out_row = row;
       out_toks = tv - qd * warp_toks;
-      out_m = m_run;
+      out_m = m_run2;
       out_l = l_run;
       nkt = next_nkt;
     }

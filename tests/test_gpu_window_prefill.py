@@ -317,12 +317,14 @@ def test_refusals(pa, cuda_device):
     assert (out == 3).all() and (lse == 3).all() and pa.pa_device_error_flags() == 0
 
 
-def equal_scores(pa, device, hkv, q, k, ahead):
+def equal_scores(pa, device, hkv, q, k, ahead, factor=0.0):
     """300 queries of q over keys of k, 128 columns each, at scale 1; `ahead`:
     key 200 has half of k.  All partial sums are exact, so scores are equal:
     weights 1 on every visible key, from query 200 on with `ahead` on that one
     alone (the others lose by more than 2^7 in log2 units).  Out: one rounding
-    to bf16, 300 fp32 additions of values, a division.  lse: the rounding of
+    to bf16, 300 fp32 additions of values, a division; and, where weights may
+    differ from 1 by a common factor that the normalizer has unrounded, their
+    rounding to bf16, 2^-8 (`factor`).  lse: the rounding of
     the score in base 2 and back, four steps of 2^-24."""
     c = Chunks([(0, 300)], 2 * hkv, hkv, 300, 0, device)
     c.scale = 1.0
@@ -340,8 +342,8 @@ def equal_scores(pa, device, hkv, q, k, ahead):
     if ahead:
         ref[200:], ref_lse[200:] = v[200], score[200:] / 2
     R.assert_within(lse, ref_lse, 2.0**-22 * np.abs(ref_lse), "lse")
-    R.assert_within(out, ref, (2.0**-8 + 2.0**-21) * np.abs(ref) + 300 * 2.0**-23 * np.abs(v).max(),
-                    "out")
+    R.assert_within(out, ref, (2.0**-8 + factor + 2.0**-21) * np.abs(ref) +
+                    300 * 2.0**-23 * np.abs(v).max(), "out")
 
 
 @pytest.mark.parametrize("ahead", [0, 1])
@@ -349,3 +351,24 @@ def equal_scores(pa, device, hkv, q, k, ahead):
 def test_scores_near_the_lowest_fp32(pa, cuda_device, ahead, hkv):
     """Scores of -2^126: lower than any reference maximum but the lowest fp32."""
     equal_scores(pa, cuda_device, hkv, 2.0**99, -2.0**20, ahead)
+
+
+@pytest.mark.parametrize("q,k,ahead", [
+    (1.25 * 2.0**98, 1.125 * 2.0**20, 0), (1.25 * 2.0**98, -1.125 * 2.0**20, 0),
+    (1.25 * 2.0**98, -1.125 * 2.0**20, 1), (1.25 * 2.0**12, 1.125 * 2.0**12, 0),
+    (1.25 * 2.0**12, -1.125 * 2.0**12, 0), (1.25 * 2.0**12, -1.125 * 2.0**12, 1),
+    (1.25 * 2.0**8, 1.125 * 2.0**9, 0), (1.25 * 2.0**8, -1.125 * 2.0**9, 1)])
+@both
+def test_scores_whose_base_2_product_is_rounded_far(pa, cuda_device, q, k, ahead, hkv):
+    """The product of such a score with log2(e) is off by 2^102, 248 and 1.9
+    from the nearest fp32: the reference maximum and the score's distance from
+    it may differ by no more than a factor that fp32 holds."""
+    equal_scores(pa, cuda_device, hkv, q, k, ahead, factor=2.0**-8)
+
+
+@pytest.mark.parametrize("scale", [1e-38, 1e-36, 1e-20])
+@both
+def test_scales_that_leave_every_weight_alike(pa, cuda_device, scale, hkv):
+    c = Chunks([(0, 300), (900, 40)], 2 * hkv, hkv, 200, 4, cuda_device)
+    c.scale = scale
+    c.check(pa)
