@@ -205,3 +205,41 @@ assert all(o.abs().sum() > 0 for o in outs) and pa.pa_device_error_flags() == 0
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("Hq,Hkv,window,sinks,interleaved", [
+    (16, 16, 100, 4, False), (16, 8, 33, 0, True), (64, 8, 64, 20, False)])
+def test_a_layer_of_many_kv_heads(pa, cuda_device, Hq, Hkv, window, sinks, interleaved):
+    """The same, with enough (token, kv head) pairs for tiles in most chunk steps."""
+    test_chunks_then_decode_steps(pa, cuda_device, Hq, Hkv, window, sinks, interleaved)
+
+
+@pytest.mark.parametrize("Hkv", [1, 8])
+def test_first_prefill_of_a_process_may_be_captured(cuda_device, Hkv):
+    """On both sides of the choice between queries one by one and in tiles (64
+    and 512 (token, kv head) pairs)."""
+    import os
+    import subprocess
+    import sys
+    code = f"""
+import torch
+from paged_kv_cache_218_gb300 import binding as pa
+T, Hkv, D = 64, {Hkv}, 128
+r = lambda *s: torch.randn(*s, device="cuda").bfloat16()
+i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+q, kc, vc = r(T, 2 * Hkv, D), r(8, 16, Hkv, D), r(8, 16, Hkv, D)
+bt, lens, cu, start = torch.arange(4, dtype=torch.int32, device="cuda")[None], i(T), i(0, T), i(0)
+out, again = torch.zeros_like(q), torch.zeros_like(q)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    pa.pa_prefill_window(out, q, kc, vc, bt, cu, start, lens, T, 33, 2, 0.1)
+g.replay()
+pa.pa_prefill_window(again, q, kc, vc, bt, cu, start, lens, T, 33, 2, 0.1)
+torch.cuda.synchronize()
+assert out.abs().sum() > 0 and torch.equal(out, again) and pa.pa_device_error_flags() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -372,3 +372,15 @@ def test_scales_that_leave_every_weight_alike(pa, cuda_device, scale, hkv):
     c = Chunks([(0, 300), (900, 40)], 2 * hkv, hkv, 200, 4, cuda_device)
     c.scale = scale
     c.check(pa)
+
+
+@pytest.mark.parametrize("chunks,Hq,Hkv,window,sinks", [
+    # up to 72 key tiles an item: the ring of ids goes around
+    ([(9000, 70), (8500, 40)], 8, 8, 10**6, 0), ([(14000, 60)], 16, 8, 8400, 700),
+    # 35 key tiles, and another such item behind most
+    ([(5000, 330), (4700, 320)], 64, 8, 4300, 40)])
+def test_items_of_several_batches_of_block_ids(pa, cuda_device, chunks, Hq, Hkv, window, sinks):
+    """More than two (token, kv head) pairs for each SM, as for `both`."""
+    assert sum(n for _, n in chunks) * Hkv > 2 * torch.cuda.get_device_properties(
+        cuda_device).multi_processor_count
+    Chunks(chunks, Hq, Hkv, window, sinks, cuda_device).check(pa)
