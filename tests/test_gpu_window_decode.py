@@ -271,3 +271,62 @@ def test_refusals(pa, cuda_device):
     torch.cuda.synchronize()
     assert (out == 3).all()
     assert pa.pa_device_error_flags() == 0
+
+
+@pytest.mark.parametrize("q,k", [(1.25 * 2.0**98, 1.125 * 2.0**20),
+                                 (1.25 * 2.0**98, -1.125 * 2.0**20),
+                                 (1.25 * 2.0**12, 1.125 * 2.0**12),
+                                 (1.25 * 2.0**12, -1.125 * 2.0**12)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_equal_scores_whose_base_2_product_is_rounded_far(pa, cuda_device, q, k, D):
+    """All partial sums are exact, so scores are equal and every weight is 1.
+    Out: one rounding to bf16, 200 fp32 additions of values, a division.  lse:
+    the rounding of the score in base 2 and back, four steps of 2^-24."""
+    x = make([200, 1, 3000], 2, 1, D, 200, 0, 1, cuda_device)
+    x[0][:], x[1][:] = q, k
+    out, lse = call(pa, *x, 200, 0, 1.0)
+    torch.cuda.synchronize()
+    assert pa.pa_device_error_flags() == 0
+    vc, bt = R.to64(x[2]), x[3].cpu().numpy()
+    for s, (first, n) in enumerate([(0, 200), (0, 1), (2800, 200)]):
+        j = np.arange(first, first + n)
+        v = vc[bt[s, j // 16], j % 16, 0]
+        ref = np.tile(v.mean(0), (2, 1))
+        ref_lse = np.full(2, D * q * k + np.log(n))
+        R.assert_within(lse[s], ref_lse, 2.0**-22 * np.abs(ref_lse), "lse")
+        R.assert_within(out[s], ref, (2.0**-8 + 2.0**-21) * np.abs(ref) +
+                        200 * 2.0**-23 * np.abs(v).max(), "out")
+
+
+@pytest.mark.parametrize("D,units,blocks", [
+    # (sequence, kv head) pairs and visible blocks for which the launcher takes,
+    # on 152 SMs, one warp a pair
+    (128, 640, 14), (64, 2048, 8),
+    # two; 34 to 36 blocks a warp, whose ids come in batches of 32
+    (128, 400, 14), (64, 800, 14), (128, 2432, 70),
+    # four; 32 and 33 blocks a warp
+    (128, 1024, 66), (64, 1024, 66), (64, 1600, 130),
+    # eight; up to 38 blocks a warp
+    (128, 320, 130), (64, 400, 100), (128, 320, 300)])
+def test_more_units_than_run_at_once(pa, cuda_device, D, units, blocks):
+    """Sequences that share the blocks of one small pool in random orders."""
+    rng = np.random.default_rng(units + blocks)
+    g = torch.Generator(device=cuda_device)
+    g.manual_seed(units)
+    Hkv, pool = 8, 40
+    S, window, sinks = units // Hkv, 16 * (blocks - 2), 4
+    lens = rng.integers(0, window + 100, S)
+    lens[rng.permutation(S)[:S // 2]] += window  # half of them past their window
+    lens[:3] = 0, 1, window + sinks
+    width = int(lens.max()) // 16 + 1
+    rnd = lambda *s: torch.randn(*s, generator=g, device=cuda_device).bfloat16()  # noqa: E731
+    q = rnd(S, Hkv * (1 if units * blocks > 60000 else 3), D)
+    kc, vc = rnd(pool, 16, Hkv, D), rnd(pool, 16, Hkv, D)
+    bt = torch.from_numpy(rng.integers(0, pool, (S, width)).astype(np.int32)).to(cuda_device)
+    sl = torch.from_numpy(lens.astype(np.int32)).to(cuda_device)
+    out, lse = call(pa, q, kc, vc, bt, sl, window, sinks, D**-0.5)
+    torch.cuda.synchronize()
+    assert pa.pa_device_error_flags() == 0
+    ro, rl, to, tl = R.decode(q, kc, vc, bt, sl, window, sinks, D**-0.5)
+    R.assert_within(lse, rl, tl, "lse")
+    R.assert_within(out, ro, to, "out")
