@@ -5,7 +5,7 @@ Argument marshalling only: each function takes torch tensors, checks their
 dtype / device / contiguity, and passes raw pointers, sizes and the current
 CUDA stream to the C function of the same name.  Every step of the paged
 attention path runs in the library's CUDA kernels; there is no fallback.
-Importing this module raises if libpa.so has not been built.
+Importing this module raises if libpa.so or the extension has not been built.
 """
 from __future__ import annotations
 
@@ -21,7 +21,12 @@ if not os.path.exists(_LIB_PATH):
         f"libpa.so not found at {_LIB_PATH}; build it first with "
         "`python -m paged_kv_cache_218_gb300.build` (or __graft_entry__.build())")
 _lib = ctypes.CDLL(_LIB_PATH)
-from . import _pycall  # noqa: E402  (needs libpa.so; built with it)
+try:
+    from . import _pycall  # (needs libpa.so; built with it)
+except ImportError as e:
+    raise ImportError(
+        "the extension _pycall is missing, or was built for another Python or torch; build it "
+        "with torch installed: `python -m paged_kv_cache_218_gb300.build`") from e
 
 PA_OK = 0
 PA_ERR_INVALID = -1
