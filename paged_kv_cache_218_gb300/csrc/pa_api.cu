@@ -1297,8 +1297,8 @@ static int norm_rope_impl(void* q_out, void* k_out, const void* q, const void* k
         return PA_ERR_INVALID;
     }
   if (k_out && overlap(q_out, out[0].bytes, k_out, out[1].bytes)) return PA_ERR_INVALID;
+  const int64_t pool = pools ? num_blocks * kBlockSize * k_row * (fp8 ? 1 : 2) : 0;
   if (pools) {
-    const int64_t pool = num_blocks * kBlockSize * k_row * (fp8 ? 1 : 2);
     for (const void* p : {k_cache, v_cache}) {
       for (const Span& x : in)
         if (x.bytes && overlap(p, pool, x.p, x.bytes)) return PA_ERR_INVALID;
@@ -1306,6 +1306,24 @@ static int norm_rope_impl(void* q_out, void* k_out, const void* q, const void* k
         if (x.bytes && overlap(p, pool, x.p, x.bytes)) return PA_ERR_INVALID;
     }
     if (overlap(k_cache, pool, v_cache, pool)) return PA_ERR_INVALID;
+  }
+  // weights, positions, frequencies, slots and scales
+  const struct {
+    const void* p;
+    int64_t bytes;
+  } small[] = {{q_weight, q_weight ? D * int64_t{4} : 0},
+               {k_weight, k_weight ? D * int64_t{4} : 0},
+               {positions, rot_dim > 0 ? num_tokens * int64_t{8} : 0},
+               {increments, rot_dim * int64_t{4}},
+               {slots, pools ? num_tokens * int64_t{8} : 0},
+               {k_scales, fp8 ? Hkv * int64_t{4} : 0},
+               {v_scales, fp8 ? Hkv * int64_t{4} : 0}};
+  for (const auto& x : small) {
+    if (x.bytes == 0) continue;
+    for (const Span& o : out)
+      if (o.bytes && overlap(o.p, o.bytes, x.p, x.bytes)) return PA_ERR_INVALID;
+    if (pools && (overlap(k_cache, pool, x.p, x.bytes) || overlap(v_cache, pool, x.p, x.bytes)))
+      return PA_ERR_INVALID;
   }
   DeviceInfo* d;
   if (int rc = current_device_info(&d)) return rc;

@@ -197,3 +197,24 @@ def test_python_calls_refuse_what_is_no_cuda_tensor(lib, bad, error):
                     lambda: pa.pa_qk_norm_rope_cache_fp8(x, x, x, x, None, None, x, x, x, x, x)):
         with pytest.raises(error):
             call_it()
+
+
+@pytest.mark.parametrize("out", ["q_out", "k_out", "kc", "vc"])
+@pytest.mark.parametrize("name,size", [("qw", 512), ("kw", 512), ("pos", 32), ("inc", 512),
+                                       ("slots", 32), ("kscale", 8), ("vscale", 8)])
+def test_norm_rope_refuses_outputs_over_its_small_inputs(lib, out, name, size):
+    """Weights, positions, increments, slots and scales are inputs too: an
+    output that begins on their last element, or ends on their first one."""
+    names = list(ROPE)
+    at = names.index("slots") + 1
+    full = {k: ROPE[k] for k in names[:at]} | {"kscale": 50 * B, "vscale": 51 * B} | {
+        k: ROPE[k] for k in names[at:]}
+    full |= dict(k_out=60 * B, qw=52 * B, kw=53 * B)
+    types = {**ROPE_T, "kscale": V, "vscale": V}
+    bytes_ = dict(q_out=4 * 1024 * 2, k_out=4 * 256 * 2, kc=64 * 16 * 256, vc=64 * 16 * 256)[out]
+    for where in (full[out] - size + 16, full[out] + bytes_ - 16):
+        where -= where % 16
+        assert call(lib.pa_qk_norm_rope_cache_fp8, full, types, **{name: where}) == INVALID, where
+        if name not in ("kscale", "vscale"):
+            bf16 = {k: x for k, x in full.items() if k not in ("kscale", "vscale")}
+            assert call(lib.pa_qk_norm_rope_cache, bf16, ROPE_T, **{name: where}) == INVALID
