@@ -11,11 +11,12 @@
 // on pass through.  Everything is fp32 and rounded once, on the way out.
 //
 // Angles.  A frequency comes as a 64-bit fixed-point number of turns per
-// position, so that position * increment mod 2^64 is the exact phase: one
-// integer multiply, with no loss at far positions (in fp32, position 10^6
-// would be off by 0.06 rad).  The top 32 bits, as a signed angle in [-pi, pi],
-// go to the special-function unit, whose sine and cosine are within 2^-21
-// there: 1/8000 of a bf16 step of a value of the pair's size.
+// position, so that position * increment mod 2^64 is its phase: one integer
+// multiply, and at far positions no error but the frequency's own (in fp32,
+// position 10^6 would be off by 0.06 rad).  The top 32 bits become an fp32
+// angle in [-pi, pi], within 6e-7, and the special-function unit's sine and
+// cosine are within 2^-21.4 there: together under 2^-20, a 4000th of the half
+// step of bf16 of a value of the pair's size.
 //
 // What bounds it: HBM at large batches (each element is read and written
 // once), latency at a decode step's.  A warp takes one token and a few steps

@@ -218,3 +218,28 @@ def test_norm_rope_refuses_outputs_over_its_small_inputs(lib, out, name, size):
         if name not in ("kscale", "vscale"):
             bf16 = {k: x for k, x in full.items() if k not in ("kscale", "vscale")}
             assert call(lib.pa_qk_norm_rope_cache, bf16, ROPE_T, **{name: where}) == INVALID
+
+
+@pytest.mark.parametrize("base", [3.7, 1e4, 5e5, 1e7])
+@pytest.mark.parametrize("scaling,factor", [(0, 1.0), (1, 3.3), (2, 7.7)])
+@pytest.mark.parametrize("rot", [16, 48, 64, 112, 128, 256])
+def test_rope_increments_are_as_near_as_stated(lib, base, scaling, factor, rot):
+    """Against 60 digits: (3 + ln base) 2^-53 relative and half a unit (the
+    exponent's rounding grows by ln base; pow, quotient and constant)."""
+    from decimal import Decimal, localcontext
+    out = (ctypes.c_int64 * (rot // 2))()
+    f = ctypes.c_float(0)
+    fn = lib.pa_rope_increments
+    fn.argtypes = [V, V, I] + [ctypes.c_double, I] + [ctypes.c_double] * 4
+    fn.restype = ctypes.c_int
+    assert fn(out, ctypes.byref(f), rot, base, scaling, factor, 0.0, 0.0, 0.0) == OK
+    with localcontext() as ctx:
+        ctx.prec = 60
+        two_pi = 2 * Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+        b = Decimal(base)
+        if scaling == 2:
+            b *= Decimal(factor) ** (Decimal(rot) / Decimal(rot - 2))
+        for i, got in enumerate(out):
+            want = (b.ln() * Decimal(-2 * i) / Decimal(rot)).exp() * 2**64 / two_pi
+            want /= Decimal(factor) if scaling == 1 else 1
+            assert abs(got - want) <= Decimal("0.5") + want * (3 + b.ln()) / 2**53, (i, got, want)
