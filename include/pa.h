@@ -391,7 +391,8 @@ int pa_decode_append(void *out, const void *q, const void *key, const void *valu
  * Only the blocks that hold a visible key are read, and only their entries of
  * block_tables: a cache manager may free the blocks between the sinks and the
  * window and leave anything in their entries.  Slots without a visible key
- * may hold anything, NaN included.
+ * may hold anything, NaN included; the V of visible keys must be finite (an
+ * infinite one gives NaN in its column).
  *   window  >= 1 (the query's own key counts); sinks >= 0; together they may
  *           exceed the sequence, which is then attended whole
  * Head dims 64 and 128, groups, outputs and device errors as pa_decode.  No

@@ -330,3 +330,15 @@ def test_more_units_than_run_at_once(pa, cuda_device, D, units, blocks):
     ro, rl, to, tl = R.decode(q, kc, vc, bt, sl, window, sinks, D**-0.5)
     R.assert_within(lse, rl, tl, "lse")
     R.assert_within(out, ro, to, "out")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_value_that_is_not_finite_stays_in_its_column(pa, cuda_device, D):
+    x = make([60, 40], 4, 2, D, 40, 3, 12, cuda_device)
+    want, want_lse = call(pa, *x, 40, 3, 0.1)
+    x[2][int(x[3][0, 2]), 5, 1, 7] = float("inf")  # key 37 of sequence 0, kv head 1
+    out, lse = call(pa, *x, 40, 3, 0.1)
+    hit = torch.zeros_like(out, dtype=torch.bool)
+    hit[0, 2:, 7] = True
+    assert not out[hit].isfinite().any()
+    assert torch.equal(out[~hit], want[~hit]) and torch.equal(lse, want_lse)
