@@ -35,9 +35,17 @@
 //    registers, a row per lane, they took 1.6 us per item; as a tensor store
 //    per warp, 0.8, half of it the proxy fence and the issue).
 //
-// What bounds it.  In long windows the tensor pipe: 0.73 us per pair and key
-// tile, 1.66 PFLOP/s over the device where cuBLAS sustains 1.70; 8192 queries x
-// 4096 keys take 395 us (1.43 PFLOP/s of the products that the masks leave).  In
+// Weights enter the second product rounded to bf16, as tensor memory holds them for
+// it, each within 2^-8 of itself (the normalizer sums them unrounded): the output is
+// within 0.0023 of 64 bits (root mean square, relative) where rounding only at the
+// end gives 0.0017.  The low halves in a product of their own, as in the decode
+// kernel, would take this kernel's bound, the tensor pipe, half as long again.
+//
+// What bounds it.  In long windows the tensor pipe and its hand-overs: 0.75 us per
+// pair and key tile (8192 queries, windows of 2048 and 4096), 1.70 PFLOP/s over the
+// device at 1.93 GHz, where cuBLAS reaches 1.92 in a burst and the products alone
+// would take 0.53 us; 8192 queries x 4096 keys take 390 us in a graph (1.45 PFLOP/s
+// of the products that the masks leave), 405 to 414 called one by one.  In
 // short ones instruction fetches: the roles' loops go through 50 KB of code per
 // item, more than an SM caches, and the cache behind it serves a whole GPC.  So
 // each role is one loop with one copy of each step, the masks are a loop over
@@ -46,7 +54,7 @@
 // masked tiles of their own, three searches for the next item) that cache was at
 // 78 % of its request rate, SMs of full GPCs took 20 % longer than others, and an
 // item's ends took 3.9 us; now 2.7.  Only the products stay unrolled: their
-// issue is on the critical path (0.89 us a tile rolled by two).
+// issue is on the critical path (a tile rolled by two took 0.16 us more).
 // Every mbarrier wait is bounded, as in pa_prefill_body.cuh.
 #include <mutex>
 
