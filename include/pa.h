@@ -69,6 +69,7 @@ typedef enum pa_status {
 #define PA_DEVERR_TIMEOUT 8u   /* a pipeline wait ran past its iteration limit */
 #define PA_DEVERR_CHUNK 16u    /* prefill chunk metadata inconsistent (skipped) */
 #define PA_DEVERR_GROUP 32u    /* cascade group / shared-block metadata out of range (clamped) */
+#define PA_DEVERR_BEAM 64u     /* beam parent outside [-1, num_beams) (taken as -1) */
 
 /* Human-readable name of a pa_status value.  Never NULL. */
 const char *pa_status_string(int status);
@@ -520,6 +521,82 @@ int pa_qk_norm_rope_cache_fp8(void *q_out, void *k_out, const void *q, const voi
                               const float *v_scales, int num_tokens, int num_q_heads,
                               int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
                               void *stream);
+
+/*
+ * Beam search: the num_choices best continuations of each request, over its
+ * num_beams beams and the vocabulary.  Beam w with score s_w (a sum of
+ * log-probabilities) and logits x_w proposes token v with the value
+ *   s_w + x_wv - ln sum_u exp(x_wu),
+ * a finished beam proposes end_token alone, with the value s_w.  Outputs are the
+ * best first, equal values in the order of (beam, token); places without a
+ * candidate get parent -1, token -1, score -inf and no mark.
+ *   parents, tokens  device int32 [num_requests, num_choices]: a candidate's beam
+ *              (within its request) and token
+ *   out_scores device fp32 [num_requests, num_choices]: its value, rounded once
+ *   out_finished  device uint8 [num_requests, num_choices] or NULL: 1 where the
+ *              beam was finished or the token is end_token
+ *   logits     device bf16, or fp32 where logits_fp32 is non-zero: beam w of
+ *              request r at + r * request_stride + w * beam_stride (elements, not
+ *              negative), vocab_size entries, from any element on.  -inf is a
+ *              forbidden token; NaN and +inf count as -inf
+ *   scores     device fp32 [num_requests, num_beams]; a beam whose score is -inf
+ *              (or not finite) proposes nothing, and its logits are not read
+ *   finished   device uint8 [num_requests, num_beams] or NULL (none is); a finished
+ *              beam's logits are not read
+ *   end_token  in [0, vocab_size); -1 (none) where finished is NULL
+ * Values are compared to 1e-9 (in a row by the logits alone, so exactly); beams of
+ * equal logits, in whatever order, have equal sums.  out_scores are within 5e-6
+ * of the value, and a rounding of it.  num_beams up to 32, num_choices up
+ * to 64, num_beams * vocab_size up to 2^30.  With num_choices == num_beams,
+ * out_scores and out_finished may be scores and finished themselves; outputs may
+ * not overlap anything otherwise (PA_ERR_INVALID).  No workspace; equal calls give
+ * equal bits, and calls may overlap freely.
+ */
+int pa_beam_select(int32_t *parents, int32_t *tokens, float *out_scores, uint8_t *out_finished,
+                   const void *logits, int logits_fp32, int64_t request_stride,
+                   int64_t beam_stride, const float *scores, const uint8_t *finished,
+                   int end_token, int num_requests, int num_beams, int num_choices,
+                   int vocab_size, void *stream);
+
+/*
+ * The paged cache after a beam selection: new beam i of request r continues its
+ * beam p = parents[r][i] of n = seq_lens[r * num_beams + p] tokens.  Blocks
+ * [0, n / 16) of a beam's table row are its history, which beams may share; the
+ * blocks from n / 16 on are its own, and hold, or will hold, its next tokens.
+ *   history   of out_tables' row r * num_beams + i: p's
+ *   its own   p's, where i is p's first child; otherwise those of a beam without
+ *             children (in order; new beams without a parent come last), after the
+ *             n % 16 tokens of p's block n / 16 are copied into the first of them,
+ *             in both pools of every layer.  A beam's own blocks thus pass to
+ *             exactly one new beam, and none is needed from elsewhere
+ *   out_lens  n; 0 for a new beam without a parent (parents[r][i] = -1)
+ * Own blocks move to the columns from n / 16 on; columns without one get -1, and
+ * those past max_blocks_per_seq are dropped.  The same copies as
+ * pa_bm_fork and pa_copy_blocks make, without the host: the caller gives each
+ * beam blocks of its own up front, and keeps a request's blocks until it ends.
+ *   out_tables, block_tables  device int32 [num_requests * num_beams, max_blocks_per_seq]
+ *   out_lens, seq_lens        device int32 [num_requests * num_beams]
+ *   parents                   device int32 [num_requests, num_beams]
+ *   k_cache, v_cache  device bf16, layer l at + l * layer_stride (elements, a
+ *              multiple of 8): [num_blocks, block_size, num_kv_heads, head_dim];
+ *              num_layers 0: tables and lengths alone (pools may be NULL)
+ * Outputs may not overlap inputs or pools (PA_ERR_INVALID); num_beams up to 32;
+ * head_dim a multiple of 8.  A parent outside [-1, num_beams) sets PA_DEVERR_BEAM
+ * and counts as -1, a length outside its row PA_DEVERR_SEQ_LEN and is clamped; a
+ * copy from or to a block outside the pool sets PA_DEVERR_BLOCK_ID and is left out.
+ */
+int pa_beam_reorder(int32_t *out_tables, int32_t *out_lens, const int32_t *block_tables,
+                    const int32_t *seq_lens, const int32_t *parents, int num_requests,
+                    int num_beams, int max_blocks_per_seq, void *k_cache, void *v_cache,
+                    int num_layers, int64_t layer_stride, int num_kv_heads, int head_dim,
+                    int block_size, int64_t num_blocks, void *stream);
+
+/* The same for E4M3 pools (bytes; head_dim and layer_stride multiples of 16). */
+int pa_beam_reorder_fp8(int32_t *out_tables, int32_t *out_lens, const int32_t *block_tables,
+                        const int32_t *seq_lens, const int32_t *parents, int num_requests,
+                        int num_beams, int max_blocks_per_seq, void *k_cache, void *v_cache,
+                        int num_layers, int64_t layer_stride, int num_kv_heads, int head_dim,
+                        int block_size, int64_t num_blocks, void *stream);
 
 /*
  * Size of the static device scratch behind pa_decode_noalloc (8 MiB).

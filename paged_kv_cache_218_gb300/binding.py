@@ -1,5 +1,6 @@
 """Thin binding of libpa.so (include/pa.h), through ctypes and, for the
-windowed-attention and norm-rotation calls, a small extension (_pycall).
+windowed-attention, norm-rotation and beam-search calls, a small extension
+(_pycall).
 
 Argument marshalling only: each function takes torch tensors, checks their
 dtype / device / contiguity, and passes raw pointers, sizes and the current
@@ -40,6 +41,7 @@ PA_DEVERR_SLOT = 4
 PA_DEVERR_TIMEOUT = 8
 PA_DEVERR_CHUNK = 16
 PA_DEVERR_GROUP = 32
+PA_DEVERR_BEAM = 64
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -371,6 +373,32 @@ def pa_decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, window, s
     table entries of blocks without a visible key are not read."""
     _pycall.decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, window, sinks, scale,
                           out_lse, stream)
+
+
+def pa_beam_select(parents, tokens, out_scores, logits, scores, finished=None, out_finished=None,
+                   end_token=-1, stream=None) -> None:
+    """The best continuations of each request: logits [requests, beams, vocabulary] (bf16 or
+    fp32, any strides over requests and beams), scores [requests, beams]; parents, tokens and
+    out_scores [requests, choices], best first.  finished / out_finished: bool or uint8."""
+    _pycall.beam_select(parents, tokens, out_scores, logits, scores, finished, out_finished,
+                        end_token, stream)
+
+
+def pa_beam_reorder(out_tables, out_lens, block_tables, seq_lens, parents, k_cache, v_cache,
+                    stream=None) -> None:
+    """Block tables, lengths and partly filled blocks after a selection with these parents
+    [requests, beams]; rows of the tables and lengths are requests * beams.  k_cache and
+    v_cache: [layers, num_blocks, 16, kv_heads, head_dim] (layers at any stride), one layer
+    without the first dimension, or both None (tables and lengths alone)."""
+    _pycall.beam_reorder(out_tables, out_lens, block_tables, seq_lens, parents, k_cache, v_cache,
+                         stream, False)
+
+
+def pa_beam_reorder_fp8(out_tables, out_lens, block_tables, seq_lens, parents, k_cache, v_cache,
+                        stream=None) -> None:
+    """pa_beam_reorder for E4M3 pools (uint8)."""
+    _pycall.beam_reorder(out_tables, out_lens, block_tables, seq_lens, parents, k_cache, v_cache,
+                         stream, True)
 
 
 def pa_decode_noalloc(out, q, k_cache, v_cache, block_tables, seq_lens, scale, out_lse=None,

@@ -13,6 +13,7 @@
 #include <unordered_set>
 
 #include "../../include/pa.h"
+#include "pa_beam.h"
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
 #include "pa_window.h"
@@ -1560,6 +1561,167 @@ int pa_test_prefill_window_stalled(void* out, const void* q, const void* k_cache
                              max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
                              num_blocks, window, sinks, scale, nullptr, stream, 1,
                              static_cast<uint64_t>(wait_limit_us) * 1000u);
+}
+
+int pa_beam_select(int32_t* parents, int32_t* tokens, float* out_scores, uint8_t* out_finished,
+                   const void* logits, int logits_fp32, int64_t request_stride,
+                   int64_t beam_stride, const float* scores, const uint8_t* finished,
+                   int end_token, int num_requests, int num_beams, int num_choices,
+                   int vocab_size, void* stream) {
+  if (num_requests < 0 || num_beams < 1 || num_choices < 1 || vocab_size < 1)
+    return PA_ERR_INVALID;
+  if (num_beams > kMaxBeams || num_choices > kMaxChoices ||
+      static_cast<int64_t>(num_beams) * vocab_size > (int64_t{1} << 30) ||
+      num_requests > (1 << 24))
+    return PA_ERR_UNSUPPORTED;
+  if (end_token < (finished ? 0 : -1) || end_token >= vocab_size) return PA_ERR_INVALID;
+  const int64_t most = int64_t{1} << 36;  // (keeps every offset within 64 bits)
+  if (request_stride < 0 || beam_stride < 0 || request_stride > most || beam_stride > most)
+    return PA_ERR_INVALID;
+  if (num_requests == 0) return PA_OK;
+  if (!parents || !tokens || !out_scores || !logits || !scores) return PA_ERR_INVALID;
+  const int elem = logits_fp32 ? 4 : 2;
+  if (!aligned(parents, 4) || !aligned(tokens, 4) || !aligned(out_scores, 4) ||
+      !aligned(scores, 4) || !aligned(logits, elem))
+    return PA_ERR_INVALID;
+  // outputs touch nothing else; scores and marks may be replaced where they are
+  const int64_t rows = static_cast<int64_t>(num_requests) * num_beams;
+  const int64_t picks = static_cast<int64_t>(num_requests) * num_choices;
+  const bool in_place = num_beams == num_choices;
+  struct Span {
+    const void* p;
+    int64_t bytes;
+  };
+  const Span out[4] = {{parents, picks * 4},
+                       {tokens, picks * 4},
+                       {out_scores, picks * 4},
+                       {out_finished, out_finished ? picks : 0}};
+  const Span in[3] = {{logits, ((num_requests - 1) * request_stride +
+                                (num_beams - 1) * beam_stride + vocab_size) * elem},
+                      {scores, rows * 4},
+                      {finished, finished ? rows : 0}};
+  for (int o = 0; o < 4; ++o) {
+    if (out[o].bytes == 0) continue;
+    for (int i = 0; i < 3; ++i) {
+      if (in[i].bytes == 0 || (in_place && o == i + 1 && o >= 2 && out[o].p == in[i].p)) continue;
+      if (overlap(out[o].p, out[o].bytes, in[i].p, in[i].bytes)) return PA_ERR_INVALID;
+    }
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[o].p, out[o].bytes, out[i].p, out[i].bytes)) return PA_ERR_INVALID;
+  }
+  DeviceInfo* d;
+  if (int rc = current_device_info(&d)) return rc;
+  BeamSelectArgs a{};
+  a.parents = parents;
+  a.tokens = tokens;
+  a.out_scores = out_scores;
+  a.out_finished = out_finished;
+  a.logits = logits;
+  a.scores = scores;
+  a.finished = finished;
+  a.request_stride = request_stride;
+  a.beam_stride = beam_stride;
+  a.end_token = end_token;
+  a.num_requests = num_requests;
+  a.num_beams = num_beams;
+  a.num_choices = num_choices;
+  a.vocab = vocab_size;
+  return launch_beam_select(a, logits_fp32 != 0, d->num_sms, static_cast<cudaStream_t>(stream)) ==
+                 cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+static int beam_reorder_impl(int32_t* out_tables, int32_t* out_lens, const int32_t* block_tables,
+                             const int32_t* seq_lens, const int32_t* parents, int num_requests,
+                             int num_beams, int max_blocks_per_seq, void* k_cache, void* v_cache,
+                             int num_layers, int64_t layer_stride, int num_kv_heads, int head_dim,
+                             int block_size, int64_t num_blocks, int elem, void* stream) {
+  if (num_requests < 0 || num_beams < 1 || max_blocks_per_seq < 1 || num_layers < 0 ||
+      block_size <= 0)
+    return PA_ERR_INVALID;
+  if (num_beams > kMaxBeams || num_requests > (1 << 24) ||
+      max_blocks_per_seq > INT32_MAX / kBlockSize || block_size != kBlockSize)
+    return PA_ERR_UNSUPPORTED;
+  const int64_t rows = static_cast<int64_t>(num_requests) * num_beams;
+  int64_t pool = 0, token_bytes = 0;  // bytes of a pool's layers from first to last
+  if (num_layers > 0) {
+    if (num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0 || layer_stride < 0)
+      return PA_ERR_INVALID;
+    if ((static_cast<int64_t>(head_dim) * elem) % 16 != 0 || num_layers > (1 << 16))
+      return PA_ERR_UNSUPPORTED;
+    token_bytes = static_cast<int64_t>(num_kv_heads) * head_dim * elem;
+    const int64_t most = int64_t{1} << 44;
+    if (num_blocks > most / kBlockSize / token_bytes || layer_stride > most / elem)
+      return PA_ERR_INVALID;
+    const int64_t layer = num_blocks * kBlockSize * token_bytes;
+    if (num_layers > 1 && (layer_stride * elem < layer || (layer_stride * elem) % 16 != 0))
+      return PA_ERR_INVALID;
+    pool = (num_layers - 1) * layer_stride * elem + layer;
+  }
+  if (num_requests == 0) return PA_OK;
+  if (!out_tables || !out_lens || !block_tables || !seq_lens || !parents) return PA_ERR_INVALID;
+  if (num_layers > 0 && (!k_cache || !v_cache)) return PA_ERR_INVALID;
+  if (!aligned(out_tables, 4) || !aligned(out_lens, 4) || !aligned(block_tables, 4) ||
+      !aligned(seq_lens, 4) || !aligned(parents, 4) ||
+      (num_layers > 0 && (!aligned(k_cache, 16) || !aligned(v_cache, 16))))
+    return PA_ERR_INVALID;
+  struct Span {
+    const void* p;
+    int64_t bytes;
+  };
+  const Span all[7] = {{out_tables, rows * max_blocks_per_seq * 4}, {out_lens, rows * 4},
+                       {k_cache, pool}, {v_cache, pool},  // (written)
+                       {block_tables, rows * max_blocks_per_seq * 4}, {seq_lens, rows * 4},
+                       {parents, rows * 4}};
+  for (int o = 0; o < 4; ++o)
+    for (int i = o + 1; i < 7; ++i)
+      if (all[o].bytes && all[i].bytes &&
+          overlap(all[o].p, all[o].bytes, all[i].p, all[i].bytes))
+        return PA_ERR_INVALID;
+  DeviceInfo* d;
+  if (int rc = current_device_info(&d)) return rc;
+  BeamReorderArgs a{};
+  a.out_tables = out_tables;
+  a.out_lens = out_lens;
+  a.tables = block_tables;
+  a.lens = seq_lens;
+  a.parents = parents;
+  a.k = static_cast<char*>(k_cache);
+  a.v = static_cast<char*>(v_cache);
+  a.err = d->err;
+  a.num_blocks = num_blocks;
+  a.layer_bytes = layer_stride * elem;
+  a.token_bytes = token_bytes;
+  a.num_requests = num_requests;
+  a.num_beams = num_beams;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_layers = num_layers;
+  return launch_beam_reorder(a, d->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+int pa_beam_reorder(int32_t* out_tables, int32_t* out_lens, const int32_t* block_tables,
+                    const int32_t* seq_lens, const int32_t* parents, int num_requests,
+                    int num_beams, int max_blocks_per_seq, void* k_cache, void* v_cache,
+                    int num_layers, int64_t layer_stride, int num_kv_heads, int head_dim,
+                    int block_size, int64_t num_blocks, void* stream) {
+  return beam_reorder_impl(out_tables, out_lens, block_tables, seq_lens, parents, num_requests,
+                           num_beams, max_blocks_per_seq, k_cache, v_cache, num_layers,
+                           layer_stride, num_kv_heads, head_dim, block_size, num_blocks, 2,
+                           stream);
+}
+
+int pa_beam_reorder_fp8(int32_t* out_tables, int32_t* out_lens, const int32_t* block_tables,
+                        const int32_t* seq_lens, const int32_t* parents, int num_requests,
+                        int num_beams, int max_blocks_per_seq, void* k_cache, void* v_cache,
+                        int num_layers, int64_t layer_stride, int num_kv_heads, int head_dim,
+                        int block_size, int64_t num_blocks, void* stream) {
+  return beam_reorder_impl(out_tables, out_lens, block_tables, seq_lens, parents, num_requests,
+                           num_beams, max_blocks_per_seq, k_cache, v_cache, num_layers,
+                           layer_stride, num_kv_heads, head_dim, block_size, num_blocks, 1,
+                           stream);
 }
 
 int pa_test_decode_stalled(void* out, const void* q, const void* k_cache, const void* v_cache,

@@ -1,0 +1,162 @@
+// pa_beam_reorder.cu -- block tables, lengths and partly filled blocks of a
+// paged cache after a beam selection (sm_103a).
+//
+// New beam i of a request continues old beam p = parents[i], of n tokens: the
+// blocks [0, n / 16) of its table are history, which beams share, and block
+// n / 16 and those behind it are a beam's own (the next tokens go there).
+// Of a parent's children the first keeps the parent's own blocks; every other
+// one takes those of a childless beam, the n % 16 tokens already in the block
+// copied over in every layer.  A childless beam's blocks are no child's
+// source, so all copies of a request run at once, in any order, in place.
+// There are as many childless beams as beams in want of blocks, since each
+// beam with children gives up one of W and takes one of W.
+//
+// What bounds it: HBM, by the bytes copied.  A beam's filled slots of one
+// layer are contiguous in each pool, so a copy is a run of up to 15 token
+// rows; a CTA reads its share of a run, 16 bytes a thread and eight of them
+// under way, before it writes.  The mapping is a few ballots of a warp, which
+// every warp makes for itself rather than wait for another.
+#include <algorithm>
+
+#include "../../include/pa.h"
+#include "pa_beam.h"
+#include "pa_ptx.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVecs = 8;  // 16-byte vectors a thread has under way
+
+__device__ __forceinline__ unsigned low_lanes(int n) { return n >= 32 ? ~0u : (1u << n) - 1; }
+
+// Place of the k-th set bit (from 0) of a mask that has one.
+__device__ __forceinline__ int nth_bit(unsigned mask, int k) {
+  for (; k > 0; --k) mask &= mask - 1;
+  return __ffs(mask) - 1;
+}
+
+__global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorderArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.x, W = a.num_beams;
+  griddep_launch_dependents();
+  griddep_wait();
+
+  // ---- lane i: old beam i, and new beam i
+  const int64_t row = static_cast<int64_t>(r) * W + lane;
+  const bool here = lane < W;
+  int parent = here ? a.parents[row] : -1;
+  int len = here ? a.lens[row] : 0;
+  const bool reports = blockIdx.y == 0 && threadIdx.x < 32;
+  if (parent < -1 || parent >= W) {
+    if (reports) atomicOr(a.err, PA_DEVERR_BEAM);
+    parent = -1;
+  }
+  const int cap = a.max_blocks * kBlockSize;
+  if (len < 0 || len > cap) {
+    if (reports) atomicOr(a.err, PA_DEVERR_SEQ_LEN);
+    len = len < 0 ? 0 : cap;
+  }
+  const unsigned before = (1u << lane) - 1;
+  const unsigned siblings = __match_any_sync(0xffffffffu, parent);
+  const bool child = here && parent >= 0;
+  const bool first = child && (siblings & before) == 0;
+  const unsigned chosen = __reduce_or_sync(0xffffffffu, child ? 1u << parent : 0u);
+  const unsigned idle = low_lanes(W) & ~chosen;
+  const unsigned extra = __ballot_sync(0xffffffffu, child && !first);
+  const unsigned orphan = __ballot_sync(0xffffffffu, here && !child);
+  int owner = parent;  // whose own blocks this beam takes
+  if (here && !first)
+    owner = nth_bit(idle, child ? __popc(extra & before)
+                                : __popc(extra) + __popc(orphan & before));
+  if (!here) owner = 0;
+  const int from = parent < 0 ? 0 : parent;
+  const int parent_len = __shfl_sync(0xffffffffu, len, from);
+  const int owner_len = __shfl_sync(0xffffffffu, len, owner);
+  const int new_len = child ? parent_len : 0;
+  const int keep = new_len / kBlockSize;         // blocks of history
+  const int shift = owner_len / kBlockSize - keep;  // own block of column c: the owner's c + shift
+  if (reports && here) a.out_lens[row] = new_len;
+
+  // ---- tables: the request's CTAs take columns in turn
+  const int32_t* const tables = a.tables + static_cast<int64_t>(r) * W * a.max_blocks;
+  int32_t* const out = a.out_tables + static_cast<int64_t>(r) * W * a.max_blocks;
+  for (int i = 0; i < W; ++i) {
+    const int p = __shfl_sync(0xffffffffu, from, i), o = __shfl_sync(0xffffffffu, owner, i);
+    const int k = __shfl_sync(0xffffffffu, keep, i), d = __shfl_sync(0xffffffffu, shift, i);
+    for (int c = blockIdx.y * kThreads + threadIdx.x; c < a.max_blocks;
+         c += gridDim.y * kThreads) {
+      int id = -1;
+      if (c < k)
+        id = tables[static_cast<int64_t>(p) * a.max_blocks + c];
+      else if (c + d < a.max_blocks)
+        id = tables[static_cast<int64_t>(o) * a.max_blocks + c + d];
+      out[static_cast<int64_t>(i) * a.max_blocks + c] = id;
+    }
+  }
+
+  // ---- copies
+  const int filled = new_len % kBlockSize;
+  int src = 0, dst = 0;
+  bool copy = child && !first && filled > 0 && a.num_layers > 0;
+  if (copy) {
+    const int own_col = owner_len / kBlockSize;
+    src = tables[static_cast<int64_t>(parent) * a.max_blocks + keep];
+    dst = own_col < a.max_blocks ? tables[static_cast<int64_t>(owner) * a.max_blocks + own_col]
+                                 : -1;
+    if (src < 0 || src >= a.num_blocks || dst < 0 || dst >= a.num_blocks) {
+      if (reports) atomicOr(a.err, PA_DEVERR_BLOCK_ID);
+      copy = false;
+    }
+  }
+  const int64_t block_bytes = a.token_bytes * kBlockSize;
+  for (unsigned todo = __ballot_sync(0xffffffffu, copy); todo; todo &= todo - 1) {
+    const int i = __ffs(todo) - 1;
+    const int64_t so = __shfl_sync(0xffffffffu, src, i) * block_bytes;
+    const int64_t to = __shfl_sync(0xffffffffu, dst, i) * block_bytes;
+    const int64_t vecs = __shfl_sync(0xffffffffu, filled, i) * a.token_bytes / 16;
+    // units: layer, pool, part of the run
+    for (int u = blockIdx.y; u < 2 * a.num_layers * a.parts; u += gridDim.y) {
+      const int run = u / a.parts, part = u - run * a.parts;
+      char* const pool = ((run & 1) ? a.v : a.k) + (run >> 1) * a.layer_bytes;
+      const uint4* const s = reinterpret_cast<const uint4*>(pool + so);
+      uint4* const d = reinterpret_cast<uint4*>(pool + to);
+      const int64_t end = vecs * (part + 1) / a.parts;
+      for (int64_t v = vecs * part / a.parts + threadIdx.x; v < end; v += kThreads * kVecs) {
+        uint4 x[kVecs];
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+          if (v + j * kThreads < end) x[j] = s[v + j * kThreads];
+#pragma unroll
+        for (int j = 0; j < kVecs; ++j)
+          if (v + j * kThreads < end) d[v + j * kThreads] = x[j];
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_beam_reorder(BeamReorderArgs a, int num_sms, cudaStream_t stream) {
+  // CTAs per request: one for each layer's pool, or a part of it where requests are few,
+  // or several where they are many; eight CTAs of 256 threads fit an SM.
+  const int64_t want = (8ll * num_sms + a.num_requests - 1) / a.num_requests;
+  const int64_t runs = 2ll * a.num_layers;
+  a.parts = 1;
+  while (a.parts < 4 && runs * a.parts * 2 <= want) a.parts *= 2;
+  const int64_t units = std::max<int64_t>(runs * a.parts, (a.max_blocks + kThreads - 1) / kThreads);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.num_requests),
+                     static_cast<unsigned>(std::max<int64_t>(1, std::min(units, want))));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, beam_reorder_kernel, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace pa

@@ -1,5 +1,5 @@
-// pa_pycall.cpp -- argument marshalling of the windowed-attention and
-// norm-rotation calls, as a CPython extension (_pycall.so).
+// pa_pycall.cpp -- argument marshalling of the windowed-attention,
+// norm-rotation and beam-search calls, as a CPython extension (_pycall.so).
 //
 // These calls are made per layer and step, and the smallest run for a few
 // microseconds on the GPU: checked and passed on in Python, a call's arguments
@@ -326,6 +326,118 @@ PyObject* norm_rope(PyObject* const* a, Py_ssize_t n) {
   return done(fp8 ? "pa_qk_norm_rope_cache_fp8" : "pa_qk_norm_rope_cache", rc);
 }
 
+// A contiguous tensor of truth values or bytes of this shape and device, or None.
+bool marks(PyObject* o, const char* name, Shape want, int device, void** p) {
+  *p = nullptr;
+  if (o == Py_None) return true;
+  const bool truth = THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kBool;
+  return tensor(o, name, truth ? at::kBool : kU8, want, device, p);
+}
+
+// beam_select(parents, tokens, out_scores, logits, scores, finished, out_finished, end_token,
+//             stream)
+PyObject* beam_select(PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 9)) return nullptr;
+  const bool fp32 = THPVariable_Check(a[3]) && THPVariable_Unpack(a[3]).scalar_type() == kF32;
+  const at::Tensor *tl, *tp;
+  if (!(tl = look(a[3], "logits", fp32 ? kF32 : kBf16, 3)) ||
+      !(tp = look(a[0], "parents", kI32, 2)))
+    return nullptr;
+  const Shape ls = tl->sizes(), st = tl->strides();
+  const int dev = static_cast<int>(tl->get_device());
+  const int64_t R = ls[0], W = ls[1], V = ls[2], K = tp->size(1);
+  if (V > 1 && st[2] != 1) {
+    PyErr_SetString(PyExc_ValueError, "logits must be contiguous within a beam");
+    return nullptr;
+  }
+  int end;
+  void *parents, *tokens, *out_scores, *scores, *finished, *out_finished, *stream;
+  if (!tensor(a[0], "parents", kI32, {R, K}, dev, &parents) ||
+      !tensor(a[1], "tokens", kI32, {R, K}, dev, &tokens) ||
+      !tensor(a[2], "out_scores", kF32, {R, K}, dev, &out_scores) ||
+      !tensor(a[4], "scores", kF32, {R, W}, dev, &scores) ||
+      !marks(a[5], "finished", {R, W}, dev, &finished) ||
+      !marks(a[6], "out_finished", {R, K}, dev, &out_finished) ||
+      !whole(a[7], "end_token", -1, INT_MAX, &end) || !fits(R, "logits") || !fits(W, "logits") ||
+      !fits(V, "logits") || !fits(K, "parents") || !queue(a[8], dev, &stream))
+    return nullptr;
+  const void* logits = tl->data_ptr();
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = pa_beam_select(static_cast<int32_t*>(parents), static_cast<int32_t*>(tokens),
+                      static_cast<float*>(out_scores), static_cast<uint8_t*>(out_finished), logits,
+                      fp32, R > 1 ? st[0] : 0, W > 1 ? st[1] : 0,
+                      static_cast<const float*>(scores), static_cast<const uint8_t*>(finished),
+                      end, static_cast<int>(R), static_cast<int>(W), static_cast<int>(K),
+                      static_cast<int>(V), stream);
+  Py_END_ALLOW_THREADS;
+  return done("pa_beam_select", rc);
+}
+
+// beam_reorder(out_tables, out_lens, block_tables, seq_lens, parents, k_cache, v_cache, stream,
+//              e4m3)
+PyObject* beam_reorder(PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 9)) return nullptr;
+  const int fp8 = PyObject_IsTrue(a[8]);
+  if (fp8 < 0) return nullptr;
+  const at::Tensor *tt, *tp;
+  if (!(tt = look(a[2], "block_tables", kI32, 2)) || !(tp = look(a[4], "parents", kI32, 2)))
+    return nullptr;
+  const int dev = static_cast<int>(tt->get_device());
+  const int64_t rows = tt->size(0), blocks = tt->size(1), R = tp->size(0), W = tp->size(1);
+  if (R * W != rows) {
+    PyErr_SetString(PyExc_ValueError, "block_tables must have a row for each entry of parents");
+    return nullptr;
+  }
+  void *out_tables, *out_lens, *tables, *lens, *parents, *stream, *k = nullptr, *v = nullptr;
+  int64_t layers = 0, stride = 0, nb = 0, bs = 16, Hkv = 1, D = 16;
+  if (a[5] != Py_None || a[6] != Py_None) {
+    // [layers, blocks, block size, heads, head_dim], layers at any stride, or one layer
+    const at::ScalarType type = fp8 ? kU8 : kBf16;
+    const bool one = THPVariable_Check(a[5]) && THPVariable_Unpack(a[5]).dim() == 4;
+    const int at = one ? 0 : 1;
+    const at::Tensor *tk, *tv;
+    if (!(tk = look(a[5], "k_cache", type, 4 + at)) || !(tv = look(a[6], "v_cache", type, 4 + at)))
+      return nullptr;
+    const Shape s = tk->sizes();
+    layers = one ? 1 : s[0];
+    nb = s[at];
+    bs = s[at + 1];
+    Hkv = s[at + 2];
+    D = s[at + 3];
+    stride = layers > 1 ? tk->stride(0) : nb * bs * Hkv * D;
+    if (!same(*tk, "k_cache", s, dev) || !same(*tv, "v_cache", s, dev)) return nullptr;
+    if (layers > 1 && tv->stride(0) != stride) {
+      PyErr_SetString(PyExc_ValueError, "k_cache and v_cache must have the same layer stride");
+      return nullptr;
+    }
+    if (layers > 0 && (!contiguous(one ? *tk : tk->select(0, 0), "a layer of k_cache") ||
+                       !contiguous(one ? *tv : tv->select(0, 0), "a layer of v_cache")))
+      return nullptr;
+    k = tk->data_ptr();
+    v = tv->data_ptr();
+  }
+  if (!tensor(a[0], "out_tables", kI32, {rows, blocks}, dev, &out_tables) ||
+      !tensor(a[1], "out_lens", kI32, {rows}, dev, &out_lens) ||
+      !tensor(a[2], "block_tables", kI32, {rows, blocks}, dev, &tables) ||
+      !tensor(a[3], "seq_lens", kI32, {rows}, dev, &lens) ||
+      !tensor(a[4], "parents", kI32, {R, W}, dev, &parents) || !fits(R, "parents") ||
+      !fits(W, "parents") || !fits(blocks, "block_tables") || !fits(layers, "k_cache") ||
+      !fits(bs, "k_cache") || !fits(Hkv, "k_cache") || !fits(D, "k_cache") ||
+      !queue(a[7], dev, &stream))
+    return nullptr;
+  const auto call = fp8 ? pa_beam_reorder_fp8 : pa_beam_reorder;
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = call(static_cast<int32_t*>(out_tables), static_cast<int32_t*>(out_lens),
+            static_cast<const int32_t*>(tables), static_cast<const int32_t*>(lens),
+            static_cast<const int32_t*>(parents), static_cast<int>(R), static_cast<int>(W),
+            static_cast<int>(blocks), k, v, static_cast<int>(layers), stride,
+            static_cast<int>(Hkv), static_cast<int>(D), static_cast<int>(bs), nb, stream);
+  Py_END_ALLOW_THREADS;
+  return done(fp8 ? "pa_beam_reorder_fp8" : "pa_beam_reorder", rc);
+}
+
 // No C++ exception (of a tensor without storage, say) leaves for the interpreter.
 template <PyObject* (*f)(PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -355,6 +467,8 @@ PyMethodDef methods[] = {
     {"decode_window", method(guarded<decode_window>), METH_FASTCALL, nullptr},
     {"prefill_window", method(guarded<prefill_window>), METH_FASTCALL, nullptr},
     {"norm_rope", method(guarded<norm_rope>), METH_FASTCALL, nullptr},
+    {"beam_select", method(guarded<beam_select>), METH_FASTCALL, nullptr},
+    {"beam_reorder", method(guarded<beam_reorder>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pycall", nullptr, -1, methods,
