@@ -12,14 +12,16 @@
 // near behind (11 elements per cycle and SM arrive, 16 exponentials leave).  So
 // the pass does as little as it can per element: its exponential for the sum, and
 // a maximum.  A cluster serves a request, its CTAs take a share of every row,
-// a warp 512 bf16 (256 fp32) elements at a time, 32 bytes a lane; the maxima of
+// a warp 1024 bf16 (512 fp32) elements at a time, twice 32 bytes a lane; the maxima of
 // such blocks and the rows' (maximum, sum) go to the cluster's first CTA.
 //
-// Selection, in that CTA: the K best candidates lie in the K blocks with the best
-// (s_w - lse_w + block maximum), ties to the first: each other block's best
-// candidate comes behind K blocks' best.  So K blocks are read again (from L2),
-// and of them the candidates that are not below the K-th block's best: a few more
-// than K.  Lists are kept sorted in a warp's registers, a lane each.
+// Selection, in that CTA: with 128 groups of blocks, the (K + 1)-th best group's best
+// candidate is a bound that K + 1 candidates reach.  The blocks that reach it, a few
+// more than K, are read again (from L2), the candidates that reach it are gathered
+// and put in order by counting.  Where more than 256 blocks or candidates do (many
+// equal logits), lists that are kept sorted in a warp's registers find first the
+// K + 1 best blocks, equal ones in their order, which hold the K + 1 best candidates
+// (each other block's best comes behind theirs), then those.
 //
 // Exactness.  Within a row the logits themselves give the order.  Between rows it
 // hangs on lse_w, which the pass knows to `margin` / 2: values are kept as sums
@@ -41,9 +43,11 @@
 namespace pa {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kUnroll = 4;     // loads a warp has under way
+constexpr int kVecs = 2;       // 32-byte vectors of a lane in a warp load
+constexpr int kAhead = 2;      // warp loads under way
+constexpr float kMove = 5.5f;  // a lane's reference moves when passed by this much
 constexpr int kMaxCtas = 16;   // of a cluster
 constexpr int kMaxEntries = 8192;  // block maxima of a request
 constexpr float kLog2e = 1.4426950408889634f;
@@ -79,10 +83,6 @@ struct Elem<__nv_bfloat16> {
   static __device__ __forceinline__ float load(const void* row, int64_t e) {
     return __bfloat162float(static_cast<const __nv_bfloat16*>(row)[e]);
   }
-  static __device__ __forceinline__ void put(uint32_t (&v)[8], int i, float x) {
-    const uint32_t b = __float_as_uint(x) >> 16;  // (x is a bf16 value)
-    v[i / 2] = (i & 1) ? (v[i / 2] & 0xffffu) | (b << 16) : (v[i / 2] & 0xffff0000u) | b;
-  }
   static __device__ __forceinline__ float max(const uint32_t (&v)[8]) {
     auto two = [&](int i) { return *reinterpret_cast<const __nv_bfloat162*>(&v[i]); };
     const __nv_bfloat162 a = __hmax2(__hmax2(two(0), two(1)), __hmax2(two(2), two(3)));
@@ -100,9 +100,6 @@ struct Elem<float> {
   static __device__ __forceinline__ float load(const void* row, int64_t e) {
     return static_cast<const float*>(row)[e];
   }
-  static __device__ __forceinline__ void put(uint32_t (&v)[8], int i, float x) {
-    v[i] = __float_as_uint(x);
-  }
   static __device__ __forceinline__ float max(const uint32_t (&v)[8]) {
     float m = __uint_as_float(v[0]);
 #pragma unroll
@@ -112,45 +109,80 @@ struct Elem<float> {
 };
 
 // A beam's logits in vectors of 32 aligned bytes: vector i holds the elements
-// [kVec * i - lead, + kVec), as far as the row has them.
+// [kVec * i - lead, + kVec), as far as the row has them.  Warp load t takes vectors
+// [64 t, 64 t + 64), a lane the ones at its own number and 32 behind.
 template <typename T>
 struct Row {
   using E = Elem<T>;
+  static constexpr int kLoad = 32 * kVecs * E::kVec;  // elements
   const T* p;
   int lead;
-  int vecs;
-  int vocab;
   __device__ __forceinline__ Row(const BeamSelectArgs& a, int r, int w) {
     p = static_cast<const T*>(a.logits) + r * a.request_stride + w * a.beam_stride;
-    vocab = a.vocab;
     lead = static_cast<int>(reinterpret_cast<uintptr_t>(p) & 31) / static_cast<int>(sizeof(T));
-    vecs = (lead + vocab + E::kVec - 1) / E::kVec;
   }
-  // Vector i, -inf outside the row.  The first and the last one may be partial: they
-  // go through `edges`, 64 bytes of the warp's.
-  __device__ __forceinline__ void load(int i, uint32_t (&v)[8], uint4* edges) const {
-    const int e = i * E::kVec - lead;
-    const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // (-inf)
-    if (i < vecs && e >= 0 && e <= vocab - E::kVec) {
-      ldg32(p + e, v);
-    } else if (i < vecs) {
-      uint4* const mine = edges + (i == 0 ? 0 : 2);
-      T* const t = reinterpret_cast<T*>(mine);
+  // Loads [first, last) have none but elements of the row.
+  __device__ __forceinline__ int first() const { return lead ? 1 : 0; }
+  __device__ __forceinline__ int last(int vocab) const { return (lead + vocab) / kLoad; }
+};
+
+template <typename T>
+__device__ __forceinline__ void load_whole(const T* at, uint32_t (&v)[kVecs][8]) {
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) ldg32(at + u * 32 * Elem<T>::kVec, v[u]);
+}
+
+// (Rare work is kept out of line and its loops rolled: a CTA runs each step but a few
+// times, and fetching instructions decides how long they take.  With everything in line,
+// 113 KB of code, finding the bound of a choice took 3.6 us of which 0.1 was work.)
+
+// A vector of a row's first or last elements, -inf where they end.
+template <typename T>
+__device__ __noinline__ void gather_edge(const T* p, int vocab, int e, uint4* to) {
+  T t[Elem<T>::kVec];
+#pragma unroll
+  for (int j = 0; j < Elem<T>::kVec; ++j)
+    t[j] = e + j >= 0 && e + j < vocab ? p[e + j] : static_cast<T>(-INFINITY);
+  T* const out = reinterpret_cast<T*>(to);
+#pragma unroll
+  for (int j = 0; j < Elem<T>::kVec; ++j) out[j] = t[j];
+}
+
+// NaN and +inf of a vector become -inf.
+template <typename T>
+__device__ __noinline__ void clean_vector(uint4* v) {
+  T* const t = reinterpret_cast<T*>(v);
 #pragma unroll 1
-      for (int j = 0; j < E::kVec; ++j)
-        t[j] = e + j >= 0 && e + j < vocab ? p[e + j] : static_cast<T>(-INFINITY);
-      const uint4 lo = mine[0], hi = mine[1];
-      v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
-      v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+  for (int j = 0; j < Elem<T>::kVec; ++j)
+    if (!(static_cast<float>(t[j]) < INFINITY)) t[j] = static_cast<T>(-INFINITY);
+}
+
+__device__ __forceinline__ void unpack(const uint4* from, uint32_t (&v)[8]) {
+  const uint4 lo = from[0], hi = from[1];
+  v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w;
+  v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
+}
+
+// Any load, partial vectors through `edges`, the lane's own 32 bytes.
+template <typename T>
+__device__ __forceinline__ void load_edge(const T* p, int vocab, int e0, uint4* edges,
+                                          uint32_t (&v)[kVecs][8]) {
+  constexpr int kVec = Elem<T>::kVec;
+  constexpr uint32_t kNone = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // (-inf)
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    const int e = e0 + u * 32 * kVec;
+    if (e >= 0 && e <= vocab - kVec) {
+      ldg32(p + e, v[u]);
+    } else if (e > -kVec && e < vocab) {
+      gather_edge(p, vocab, e, edges);
+      unpack(edges, v[u]);
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = none;
+      for (int i = 0; i < 8; ++i) v[u][i] = kNone;
     }
   }
-  __device__ __forceinline__ int blocks(int shift) const {
-    return (((vecs + 31) >> 5) + (1 << shift) - 1) >> shift;
-  }
-};
+}
 
 // A value as a sum of two floats, the second below half a step of the first: one
 // 64-bit number in the order of such values, 0 below all.
@@ -164,6 +196,11 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 __device__ __forceinline__ float2 two_sum(float a, float b) {  // (exact)
   const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
   return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
+}
+// score - top - ln
+__device__ __forceinline__ float2 base_of(float score, float top, float2 ln) {
+  const float2 a = two_sum(score, -top), b = two_sum(a.x, -ln.x);
+  return two_sum(b.x, (b.y + a.y) - ln.y);
 }
 __device__ __forceinline__ uint64_t value_key(float2 base, float x) {
   const float2 s = two_sum(base.x, x);
@@ -259,22 +296,35 @@ __device__ __forceinline__ void add_exp(FixedSum& sum, const ExpTable& tab, floa
   sum.add(static_cast<uint64_t>(__float2ll_rn(hi) + __float2ll_rn(__fmaf_rn(hi, p, b.y * scale))));
 }
 
+constexpr int kGroups = 128;     // of block maxima, whose best bound the choice
+constexpr int kMaxPicked = 256;  // blocks, and candidates, that are gathered unsorted
+
 // Shared memory besides the block maxima.
 template <int KL>
 struct SelectSmem {
-  uint4 edges[kWarps][4];            // of rows, elements on their way to registers
+  uint4 edges[kThreads][2];          // of rows, elements on their way to registers
   float2 part[kMaxBeams][kMaxCtas];  // rows' (maximum, sum) of each CTA
   float2 red[kMaxBeams][kWarps];     // and of each warp
   float2 base[kMaxBeams];            // s - lse in two floats
-  float top[kMaxBeams];              // rows' maxima
-  uint64_t list_key[kWarps][32 * KL];
-  uint32_t list_idx[kWarps][32 * KL];
-  uint64_t key[32 * KL];  // the lists' best, in order
-  uint32_t idx[32 * KL];
-  uint64_t floor[kWarps];
-  FixedSum sum[kWarps];
+  float group[kThreads / kGroups][kGroups];
+  uint32_t group_key[4][kGroups / 4 + 4];  // (quarters in different banks)
+  union {
+    struct {
+      uint64_t key[kMaxPicked];
+      uint32_t idx[kMaxPicked];
+      uint32_t block[kMaxPicked];
+    } pick;
+    struct {
+      uint64_t key[kWarps][32 * KL];
+      uint32_t idx[kWarps][32 * KL];
+    } list;
+  };
+  uint64_t key[kMaxPicked];  // candidates in order
+  uint32_t idx[kMaxPicked];
+  uint64_t sum_hi[kWarps], sum_lo[kWarps];
+  float bound;        // no candidate below it is chosen
   unsigned doubtful;  // rows whose sums are to be taken again
-  int found;
+  int found, blocks, picked;
   ExpTable table;
 };
 
@@ -285,15 +335,15 @@ __device__ __forceinline__ void join_lists(SelectSmem<KL>& sm, const WarpList<KL
                                            int warp, int lane) {
 #pragma unroll
   for (int r = 0; r < KL; ++r) {
-    sm.list_key[warp][32 * r + lane] = mine.key[r];
-    sm.list_idx[warp][32 * r + lane] = mine.idx[r];
+    sm.list.key[warp][32 * r + lane] = mine.key[r];
+    sm.list.idx[warp][32 * r + lane] = mine.idx[r];
   }
   if (threadIdx.x == 0) sm.found = 0;
   __syncthreads();
   for (int t = threadIdx.x; t < kWarps * n; t += kThreads) {
     const int w = t / n, at = t - w * n;
-    const uint64_t k = sm.list_key[w][at];
-    const uint32_t i = sm.list_idx[w][at];
+    const uint64_t k = sm.list.key[w][at];
+    const uint32_t i = sm.list.idx[w][at];
     if (k == 0) continue;
     int rank = at;
 #pragma unroll
@@ -302,7 +352,7 @@ __device__ __forceinline__ void join_lists(SelectSmem<KL>& sm, const WarpList<KL
       int lo = 0, hi = n;  // how many of list l come before
       while (lo < hi) {
         const int mid = (lo + hi) >> 1;
-        if (better(sm.list_key[l][mid], sm.list_idx[l][mid], k, i))
+        if (better(sm.list.key[l][mid], sm.list.idx[l][mid], k, i))
           lo = mid + 1;
         else
           hi = mid;
@@ -320,8 +370,182 @@ __device__ __forceinline__ void join_lists(SelectSmem<KL>& sm, const WarpList<KL
 
 enum BeamState : int { kDead = 0, kLive = 1, kEnded = 2 };
 
+// The beam of entry e of the block maxima.
+__device__ __forceinline__ int beam_of(const BeamSelectArgs& a, int e) {
+  return a.blocks_per_row == 1 ? e : static_cast<int>(__umulhi(e, a.blocks_inverse));
+}
+
+// What the first CTA's threads know of the choice.
 template <typename T, int KL>
-__global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSelectArgs a) {
+struct Choice {
+  using E = Elem<T>;
+  const BeamSelectArgs& a;
+  SelectSmem<KL>& sm;
+  float* block_max;
+  int r;
+  unsigned live, ended;
+  unsigned exact;  // rows whose base is known to 1e-9
+  float bound;     // no candidate below it is chosen, and what sums and roundings are off
+  float slack;
+
+  // the value of a block's best candidate
+  __device__ __forceinline__ uint64_t entry_key(int e) const {
+    return value_key(sm.base[beam_of(a, e)], block_max[e]);
+  }
+  // Load number `part` of block e: f(key, index) for the candidates that may reach the
+  // bound, the whole warp together (key 0: this lane has none).
+  template <typename F>
+  __device__ __forceinline__ void scan(int e, int part, int lane, F f) const {
+    const int V = a.vocab, w = beam_of(a, e);
+    const float2 base = sm.base[w];
+    const uint32_t index0 = static_cast<uint32_t>(w) * V;
+    if ((ended >> w) & 1) {
+      f(lane == 0 && part == 0 ? value_key(base, 0.f) : 0, index0 + a.end_token);
+      return;
+    }
+    const Row<T> row(a, r, w);
+    const int t = ((e - w * a.blocks_per_row) << a.block_shift) + part;
+    const int e0 = t * Row<T>::kLoad + lane * E::kVec - row.lead;
+    uint32_t v[kVecs][8];
+    if (t >= row.first() && t < row.last(V))
+      load_whole(row.p + e0, v);
+    else
+      load_edge(row.p, V, e0, sm.edges[threadIdx.x], v);
+    unsigned hits = 0;
+    const float least = fmaxf((bound - base.x) - slack, -FLT_MAX);
+#pragma unroll
+    for (int i = 0; i < kVecs * E::kVec / 2; ++i) {
+      const float2 x = E::pair(v[i / (E::kVec / 2)], i % (E::kVec / 2));
+      hits |= (x.x >= least ? 1u : 0u) << (2 * i) | (x.y >= least ? 1u : 0u) << (2 * i + 1);
+    }
+#pragma unroll 1
+    while (__any_sync(0xffffffffu, hits != 0)) {
+      uint64_t k = 0;
+      int token = 0;
+      if (hits) {
+        const int j = __ffs(hits) - 1;
+        token = e0 + (j / E::kVec) * 32 * E::kVec + j % E::kVec;
+        hits &= hits - 1;
+        k = value_key(base, sane(E::load(row.p, token)));
+      }
+      f(k, index0 + token);
+      __syncwarp();
+    }
+  }
+  __device__ __forceinline__ void doubt(int w0, int w1) const {
+    const unsigned both = 1u << w0 | 1u << w1;
+    if (w0 != w1 && (both & ~exact)) atomicOr(&sm.doubtful, both);
+  }
+};
+
+// The K + 1 best by sorted lists: first the blocks, then of these the candidates; and which
+// rows' order is in doubt.  Called by the whole CTA.
+template <typename T, int KL>
+__device__ __noinline__ void choose_by_lists(const Choice<T, KL>& c) {
+  SelectSmem<KL>& sm = c.sm;
+  const BeamSelectArgs& a = c.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int K = a.num_choices, L = K + 1, V = a.vocab;
+  const int entries = a.num_beams * a.blocks_per_row, sh = a.block_shift;
+  uint64_t floor = static_cast<uint64_t>(ordered(c.bound)) << 32;
+  WarpList<KL> list;
+#pragma unroll 1
+  for (int round = 0; round < 2; ++round) {
+    list.clear();
+    const int chosen = round == 0 ? entries : sm.found << sh;
+    if (round == 1) floor = sm.found == L ? sm.key[L - 1] : 0;
+#pragma unroll 1
+    for (int t = round == 0 ? warp * 32 : warp; t < chosen; t += round == 0 ? kThreads : kWarps) {
+      auto offer = [&](uint64_t k, uint32_t i) { list.offer(k, i, floor, lane); };
+      if (round == 0)
+        offer(t + lane < entries ? c.entry_key(t + lane) : 0, t + lane);
+      else
+        c.scan(sm.idx[t >> sh], t & ((1 << sh) - 1), lane, offer);
+    }
+    __syncthreads();  // sm.idx and sm.found have been read
+    join_lists(sm, list, L, warp, lane);
+  }
+  const int found = sm.found;
+  for (int i = threadIdx.x; i < K && i + 1 < found; i += kThreads)
+    if (key_gap(sm.key[i], sm.key[i + 1]) < a.margin) c.doubt(sm.idx[i] / V, sm.idx[i + 1] / V);
+  if (found < L) return;
+  const uint64_t last = sm.key[K - 1];
+  const int w0 = sm.idx[K - 1] / V;
+  if (static_cast<int>(sm.idx[K] / V) != w0 || key_gap(last, sm.key[K]) >= a.margin) return;
+  // Another row's candidate next to the last choice, displaced by candidates of that
+  // choice's own row?
+#pragma unroll 1
+  for (int e0 = warp * 32; e0 < entries; e0 += kThreads) {
+    const int e = e0 + lane;
+    const int w = e < entries ? beam_of(a, e) : w0;
+    const uint64_t k = e < entries ? c.entry_key(e) : 0;
+    const bool look = w != w0 && ((1u << w0 | 1u << w) & ~c.exact) && k != 0 &&
+                      key_gap(last, k) < a.margin;
+    if (look && k < last) c.doubt(w0, w);
+#pragma unroll 1
+    for (unsigned todo = __ballot_sync(0xffffffffu, look && k >= last); todo; todo &= todo - 1) {
+      const int from = e0 + __ffs(todo) - 1;
+#pragma unroll 1
+      for (int part = 0; part < 1 << sh; ++part)
+        c.scan(from, part, lane, [&](uint64_t kx, uint32_t i) {
+          if (kx != 0 && kx < last && key_gap(last, kx) < a.margin) c.doubt(w0, beam_of(a, from));
+        });
+    }
+  }
+}
+
+// The bases of these rows, to 1e-9.  Called by the whole CTA.
+template <typename T, int KL>
+__device__ __noinline__ void sum_again(const Choice<T, KL>& c, unsigned rows, float score) {
+  SelectSmem<KL>& sm = c.sm;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int V = c.a.vocab, NB = c.a.blocks_per_row;
+  if (threadIdx.x < 64) {
+    const double t = exp2(threadIdx.x / 64.0);
+    const float hi = static_cast<float>(t);
+    sm.table.t[threadIdx.x] = make_float2(hi, static_cast<float>(t - hi));
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (; rows; rows &= rows - 1) {
+    const int w = __ffs(rows) - 1;
+    const Row<T> row(c.a, c.r, w);
+    // (the row's maximum: a reference that the order of the logits does not change)
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int b = lane; b < NB; b += 32) top = fmaxf(top, c.block_max[w * NB + b]);
+    top = warp_max(top);
+    FixedSum sum;
+#pragma unroll 2
+    for (int x = threadIdx.x; x < V; x += kThreads)
+      add_exp(sum, sm.table, sane(Elem<T>::load(row.p, x)), top);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      sum.hi += __shfl_xor_sync(0xffffffffu, sum.hi, off);
+      sum.lo += __shfl_xor_sync(0xffffffffu, sum.lo, off);
+    }
+    if (lane == 0) {
+      sm.sum_hi[warp] = sum.hi;
+      sm.sum_lo[warp] = sum.lo;
+    }
+    __syncthreads();
+    const float mine = __shfl_sync(0xffffffffu, score, w);
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < kWarps; ++i) {
+        sum.hi += sm.sum_hi[i];
+        sum.lo += sm.sum_lo[i];
+      }
+      const double ln = log(static_cast<double>(sum.hi) * 0x1p-18 +
+                            static_cast<double>(sum.lo) * 0x1p-50);
+      const float hi = static_cast<float>(ln);
+      sm.base[w] = base_of(mine, top, make_float2(hi, static_cast<float>(ln - hi)));
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, int KL>
+__global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSelectArgs a) {
   using E = Elem<T>;
   extern __shared__ float block_max[];  // [beams][blocks_per_row], of the first CTA
   __shared__ SelectSmem<KL> sm;
@@ -332,8 +556,12 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSele
   const int C = static_cast<int>(ctas);
   const int r = static_cast<int>(blockIdx.x) / C;
   const int W = a.num_beams, V = a.vocab, NB = a.blocks_per_row, sh = a.block_shift;
-  // the first CTA runs before its shared memory is written
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  // the first CTA clears its shared memory before others write there
+  if (rank == 0)
+    for (int e = threadIdx.x; e < W * NB; e += kThreads) block_max[e] = -INFINITY;
+  for (int e = threadIdx.x; e < W * kWarps; e += kThreads)
+    sm.red[e / kWarps][e % kWarps] = make_float2(-FLT_MAX, 0.f);
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   griddep_launch_dependents();
   griddep_wait();
 
@@ -348,296 +576,268 @@ __global__ void __launch_bounds__(kThreads, 3) beam_select_kernel(const BeamSele
   }
   const unsigned live = __ballot_sync(0xffffffffu, state == kLive);
   const unsigned ended = __ballot_sync(0xffffffffu, state == kEnded);
-  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 
-  // ---- the pass over the logits
+  // ---- the pass over the logits: the CTA's blocks [b0, b1) of every live beam, one
+  // row behind another, in a range of them for each warp
   const uint32_t remote_max = mapa_shared(smem_u32(block_max), 0);
-  for (unsigned todo = live; todo; todo &= todo - 1) {
-    const int w = __ffs(todo) - 1;
-    const Row<T> row(a, r, w);
-    const int blocks = row.blocks(sh);
-    const int b0 = static_cast<int>(static_cast<int64_t>(blocks) * rank / C);
-    const int b1 = static_cast<int>(static_cast<int64_t>(blocks) * (rank + 1) / C);
-    // this warp's blocks b0 + warp, + kWarps ..., a warp load at a time
-    const int mine = b1 - b0 > warp ? ((b1 - b0 - warp + kWarps - 1) / kWarps) << sh : 0;
-    float m = -INFINITY, s = 0.f, bm = -INFINITY;
-    for (int q0 = 0; q0 < mine; q0 += kUnroll) {
-      uint32_t v[kUnroll][8];
-      auto step_of = [&](int q) {
-        return ((b0 + warp + kWarps * (q >> sh)) << sh) + (q & ((1 << sh) - 1));
-      };
-#pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int q = q0 + u;
-        row.load(q < mine ? step_of(q) * 32 + lane : row.vecs, v[u], sm.edges[warp]);
+  const int t0 = (NB * rank / C) << sh, t1 = (NB * (rank + 1) / C) << sh;  // loads of a row
+  const int per_row = t1 - t0, all = __popc(live) * (per_row >> sh);
+  const int first = (all * warp / kWarps) << sh;
+  int left = ((all * (warp + 1) / kWarps) << sh) - first;  // to be fetched
+  if (left > 0) {
+    const int part_mask = (1 << sh) - 1;
+    unsigned get_rows = live;  // beams from the one fetched on
+    int skip = first;
+    for (; skip >= per_row; skip -= per_row) get_rows &= get_rows - 1;
+    int get = t0 + skip;       // load fetched next, and the row's whole ones
+    int whole0 = 0, whole1 = 0;
+    const T* row = nullptr;    // the lane's first element of the row's load 0
+    auto begin = [&]() {
+      const Row<T> x(a, r, __ffs(get_rows) - 1);
+      row = x.p - x.lead + lane * E::kVec;
+      whole0 = x.first();
+      whole1 = x.last(V);
+    };
+    begin();
+    uint32_t v[kAhead][kVecs][8];
+    auto fetch = [&](uint32_t (&to)[kVecs][8]) {
+      if (get >= whole0 && get < whole1) {
+        load_whole(row + static_cast<int64_t>(get) * Row<T>::kLoad, to);
+      } else {
+        const Row<T> x(a, r, __ffs(get_rows) - 1);
+        load_edge(x.p, V, get * Row<T>::kLoad + lane * E::kVec - x.lead, sm.edges[threadIdx.x],
+                  to);
       }
-      float mx[kUnroll], total = 0.f, ref = 0.f, m_new = m;
-      bool clean = false;
-      while (true) {
-        m_new = m;
+      --left;
+      if (++get == t1 && left > 0) {
+        get = t0;
+        get_rows &= get_rows - 1;
+        begin();
+      }
+    };
+    unsigned use_rows = get_rows;
+    int use = get, todo = left;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          mx[u] = E::max(v[u]);
-          m_new = fmaxf(m_new, mx[u]);
-        }
-        ref = fmaxf(m_new, -FLT_MAX);  // finite
-        const uint64_t nref = f32x2(-ref, -ref), scale = f32x2(kLog2e, kLog2e);
-        uint64_t acc = 0;
+    for (int u = 0; u < kAhead; ++u)
+      if (left > 0) fetch(v[u]);
+    // sum of 2^((x - ref) log2 e) of the lane's elements of this row; ref is finite, and
+    // at most kMove below the largest
+    float ref = -FLT_MAX, sum = 0.f, block = -INFINITY;
+    while (todo > 0) {
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+      for (int u = 0; u < kAhead; ++u) {
+        if (todo == 0) break;
+        float mx, more;
+        bool clean = false;
+        while (true) {
+          mx = E::max(v[u][0]);
+#pragma unroll
+          for (int c = 1; c < kVecs; ++c) mx = fmaxf(mx, E::max(v[u][c]));
+          if (mx > ref + kMove && mx < INFINITY) {
+            sum *= fast_exp2((ref - mx) * kLog2e);
+            ref = mx;
+          }
+          const uint64_t nref = f32x2(-ref, -ref), scale = f32x2(kLog2e, kLog2e);
           uint64_t sums[2] = {0, 0};
 #pragma unroll
-          for (int i = 0; i < E::kVec / 2; ++i) {
-            const float2 x = E::pair(v[u], i);
+          for (int i = 0; i < kVecs * E::kVec / 2; ++i) {
+            const float2 x = E::pair(v[u][i / (E::kVec / 2)], i % (E::kVec / 2));
             const float2 d = f32x2_parts(mul2(add2(f32x2(x.x, x.y), nref), scale));
             sums[i & 1] = add2(sums[i & 1], f32x2(fast_exp2(d.x), fast_exp2(d.y)));
           }
-          acc = add2(acc, add2(sums[0], sums[1]));
-        }
-        const float2 two = f32x2_parts(acc);
-        total = two.x + two.y;
-        // NaN or +inf among them: once more without
-        if (clean || (m_new < INFINITY && total == total)) break;
-        clean = true;
+          const float2 two = f32x2_parts(add2(sums[0], sums[1]));
+          more = two.x + two.y;
+          if (clean || (mx < INFINITY && more == more)) break;
+          // NaN or +inf among them: once more without
+          clean = true;
+          uint4* const edges = sm.edges[threadIdx.x];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u)
-#pragma unroll
-          for (int i = 0; i < E::kVec / 2; ++i) {
-            const float2 x = E::pair(v[u], i);
-            E::put(v[u], 2 * i, sane(x.x));
-            E::put(v[u], 2 * i + 1, sane(x.y));
+          for (int c = 0; c < kVecs; ++c) {
+            uint32_t (&x)[8] = v[u][c];
+            edges[0] = make_uint4(x[0], x[1], x[2], x[3]);
+            edges[1] = make_uint4(x[4], x[5], x[6], x[7]);
+            clean_vector<T>(edges);
+            unpack(edges, x);
           }
-      }
-      s = s * fast_exp2((m - ref) * kLog2e) + total;  // (s is 0 where m is -inf)
-      m = m_new;
-      __syncwarp();
+        }
+        if (left > 0) fetch(v[u]);
+        sum += more;
+        --todo;
+        __syncwarp();
+        block = fmaxf(block, warp_max(mx));
+        const int w = __ffs(use_rows) - 1;
+        if ((use & part_mask) == part_mask) {
+          if (lane == 0) st_remote(remote_max + 4 * (w * NB + (use >> sh)), block);
+          block = -INFINITY;
+        }
+        if (++use == t1 || todo == 0) {  // the warp's share of this row is done
+          const float top = warp_max(ref);
+          sum *= fast_exp2((ref - top) * kLog2e);
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int q = q0 + u;
-        bm = fmaxf(bm, warp_max(mx[u]));
-        if (q < mine && ((q + 1) & ((1 << sh) - 1)) == 0) {
-          if (lane == 0)
-            st_remote(remote_max + 4 * (w * NB + b0 + warp + kWarps * (q >> sh)), bm);
-          bm = -INFINITY;
+          for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+          if (lane == 0) sm.red[w][warp] = make_float2(top, sum);
+          ref = -FLT_MAX;
+          sum = 0.f;
+          use = t0;
+          use_rows &= use_rows - 1;
         }
       }
     }
-    const float top = warp_max(m);
-    s *= fast_exp2((m - fmaxf(top, -FLT_MAX)) * kLog2e);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    if (lane == 0) sm.red[w][warp] = make_float2(top, s);
   }
   __syncthreads();
-  if (threadIdx.x < W && ((live >> threadIdx.x) & 1)) {
-    const int w = threadIdx.x;
-    float top = -INFINITY;
+  // a row's share of this CTA, a half warp for each
+  {
+    static_assert(kThreads / kWarps == kMaxBeams, "rows at once");
+    const int w = threadIdx.x / kWarps;
+    const float2 x = sm.red[w][threadIdx.x % kWarps];
+    float top = x.x;
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) top = fmaxf(top, sm.red[w][i].x);
-    float s[kWarps];
+    for (int off = kWarps / 2; off > 0; off >>= 1)
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    float sum = x.y * fast_exp2((x.x - top) * kLog2e);
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i)
-      s[i] = sm.red[w][i].y * fast_exp2((sm.red[w][i].x - fmaxf(top, -FLT_MAX)) * kLog2e);
-#pragma unroll
-    for (int h = kWarps / 2; h > 0; h >>= 1)
-#pragma unroll
-      for (int i = 0; i < h; ++i) s[i] += s[i + h];
-    const uint32_t at = mapa_shared(smem_u32(&sm.part[w][rank]), 0);
-    st_remote(at, top);
-    st_remote(at + 4, s[0]);
+    for (int off = kWarps / 2; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (w < W && threadIdx.x % kWarps == 0) {
+      const uint32_t at = mapa_shared(smem_u32(&sm.part[w][rank]), 0);
+      st_remote(at, top);
+      st_remote(at + 4, sum);
+    }
   }
   cluster_sync();
   if (rank != 0) return;
 
   // ---- the first CTA: s - lse of each row
   for (int w = warp; w < W; w += kWarps) {
-    if (!((live >> w) & 1)) continue;
-    const float2 x = lane < C ? sm.part[w][lane] : make_float2(-INFINITY, 0.f);
-    const float top = warp_max(x.x);
-    float s = x.y * fast_exp2((x.x - fmaxf(top, -FLT_MAX)) * kLog2e);
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
     const float mine = __shfl_sync(0xffffffffu, score, w);
-    if (lane == 0) {
+    float2 base = make_float2(mine, 0.f);
+    if ((live >> w) & 1) {
+      const float2 x = lane < C ? sm.part[w][lane] : make_float2(-FLT_MAX, 0.f);
+      const float top = warp_max(x.x);
+      float s = x.y * fast_exp2((x.x - top) * kLog2e);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
       // (a row of -inf: no candidates, whatever the base)
-      const double b = s > 0.f ? (mine - static_cast<double>(top)) - log(static_cast<double>(s))
-                               : 0.0;
-      const float hi = static_cast<float>(b);
-      sm.base[w] = make_float2(hi, static_cast<float>(b - hi));
-      sm.top[w] = top;
+      if (s > 0.f) base = base_of(mine, top, make_float2(logf(s), 0.f));
+    } else if (((ended >> w) & 1) && lane == 0) {
+      const Row<T> row(a, r, w);  // one candidate, in its token's block
+      block_max[w * NB + ((a.end_token + row.lead) / Row<T>::kLoad >> sh)] = 0.f;
     }
+    if (lane == 0) sm.base[w] = base;
   }
-  if (warp == 0 && state == kEnded) sm.base[lane] = make_float2(score, 0.f);
-  const int K = a.num_choices, L = K + 1;
-  unsigned exact = ended;  // rows whose base is known to 1e-9
+  const int K = a.num_choices, L = K + 1, entries = W * NB;
+  Choice<T, KL> c{a, sm, block_max, r, live, ended, ended, 0.f, 0.f};
   __syncthreads();
 
-  // the value of a row's block's best candidate
-  auto entry_key = [&](int w, int b) -> uint64_t {
-    if ((live >> w) & 1) {
-      const Row<T> row(a, r, w);
-      return b < row.blocks(sh) ? value_key(sm.base[w], block_max[w * NB + b]) : 0;
-    }
-    if ((ended >> w) & 1) {
-      const Row<T> row(a, r, w);
-      return b == (((a.end_token + row.lead) / E::kVec) >> 5) >> sh
-                 ? value_key(sm.base[w], 0.f)
-                 : 0;
-    }
-    return 0;
+  // f(entry, value in fp32) for this thread's blocks, those of group threadIdx.x % 128
+  auto each_entry = [&](auto f) {
+#pragma unroll 4
+    for (int e = threadIdx.x; e < entries; e += kThreads)
+      f(e, sm.base[beam_of(a, e)].x + block_max[e]);
   };
 
   while (true) {
-    WarpList<KL> list;
-    // ---- the L best blocks
-    const int entries = W * NB;
-    uint64_t best = 0;
-    for (int e = threadIdx.x; e < entries; e += kThreads) {
-      const uint64_t k = entry_key(e / NB, e % NB);
-      best = k > best ? k : best;
+    // ---- a bound: the L-th best of 128 groups' best blocks, less what sums and
+    // roundings may be off
+    if (threadIdx.x == 0) {
+      sm.blocks = sm.picked = sm.found = 0;
+      sm.doubtful = 0;
+      sm.bound = -INFINITY;
     }
-    uint64_t floor = 0;
-    if (L <= 32) {
-      // L lanes of a warp have a block that is as good as its L-th lane's
+    float best = -INFINITY;
+    each_entry([&](int, float v) { best = fmaxf(best, v); });
+    sm.group[threadIdx.x / kGroups][threadIdx.x % kGroups] = best;
+    __syncthreads();
+    constexpr int kQuarter = kGroups / 4;
+    static_assert(kThreads / kGroups == 4, "a thread for each quarter");
+    if (threadIdx.x < kGroups) {
 #pragma unroll
-      for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-        for (int off = size / 2; off > 0; off >>= 1) {
-          const uint64_t o = __shfl_xor_sync(0xffffffffu, best, off);
-          const bool up = ((lane & off) == 0) == ((lane & size) == 0 || size == 32);
-          best = (o > best) == up ? o : best;
+      for (int i = 1; i < 4; ++i) best = fmaxf(best, sm.group[i][threadIdx.x]);
+      // (the last bits tell equal groups apart; the value is rounded down)
+      sm.group_key[threadIdx.x / kQuarter][threadIdx.x % kQuarter] =
+          best > -INFINITY ? (ordered(best) & ~(kGroups - 1u)) | threadIdx.x : threadIdx.x;
+    }
+    __syncthreads();
+    {
+      // thread 4 g + h: how many of quarter h come before group g
+      const int g = threadIdx.x >> 2, h = threadIdx.x & 3;
+      const uint32_t mine = sm.group_key[g / kQuarter][g % kQuarter];
+      int place = 0;
+#pragma unroll 2
+      for (int i = 0; i < kQuarter; i += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(&sm.group_key[h][i]);
+        place += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+      }
+      place += __shfl_xor_sync(0xffffffffu, place, 1);
+      place += __shfl_xor_sync(0xffffffffu, place, 2);
+      if (place == L - 1 && h == 0 && mine >= kGroups)
+        sm.bound = unordered(mine & ~(kGroups - 1u));
+    }
+    float far = lane < W ? fabsf(sm.base[lane].x) : 0.f;
+    far = warp_max(far < INFINITY ? far : 0.f);
+    __syncthreads();
+    c.slack = (fabsf(sm.bound) + far) * 0x1p-20f + 2 * a.margin;
+    c.bound = sm.bound > -INFINITY ? sm.bound - c.slack : -FLT_MAX;
+    // ---- the blocks that reach it, and of them the candidates
+    each_entry([&](int e, float v) {
+      if (v >= c.bound) {
+        const int at = atomicAdd(&sm.blocks, 1);
+        if (at < kMaxPicked) sm.pick.block[at] = e;
+      }
+    });
+    __syncthreads();
+    const int blocks = sm.blocks;
+    if (blocks <= kMaxPicked) {
+#pragma unroll 1
+      for (int t = warp; t < blocks << sh; t += kWarps)
+        c.scan(sm.pick.block[t >> sh], t & ((1 << sh) - 1), lane, [&](uint64_t k, uint32_t i) {
+          if (k == 0) return;
+          const int at = atomicAdd(&sm.picked, 1);
+          if (at < kMaxPicked) {
+            sm.pick.key[at] = k;
+            sm.pick.idx[at] = i;
+          }
+        });
+    }
+    __syncthreads();
+    const int picked = sm.picked;
+    if (blocks <= kMaxPicked && picked <= kMaxPicked) {
+      // in order: eight lanes compare one with all
+#pragma unroll 1
+      for (int i0 = 0; i0 < picked; i0 += kThreads / 8) {
+        const int i = i0 + threadIdx.x / 8;
+        int place = 0;
+        if (i < picked) {
+          const uint64_t k = sm.pick.key[i];
+          const uint32_t id = sm.pick.idx[i];
+#pragma unroll 1
+          for (int o = threadIdx.x & 7; o < picked; o += 8)
+            place += better(sm.pick.key[o], sm.pick.idx[o], k, id);
         }
-      if (lane == L - 1) sm.floor[warp] = best;
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1) place += __shfl_xor_sync(0xffffffffu, place, off);
+        if (i < picked && (threadIdx.x & 7) == 0) {
+          sm.key[place] = sm.pick.key[i];
+          sm.idx[place] = sm.pick.idx[i];
+        }
+      }
+      if (threadIdx.x == 0) sm.found = picked;
       __syncthreads();
-#pragma unroll
-      for (int i = 0; i < kWarps; ++i) floor = sm.floor[i] > floor ? sm.floor[i] : floor;
-    }
-    list.clear();
-    for (int e0 = warp * 32; e0 < entries; e0 += kThreads) {
-      const int e = e0 + lane;
-      list.offer(e < entries ? entry_key(e / NB, e % NB) : 0, e, floor, lane);
-    }
-    join_lists(sm, list, L, warp, lane);
-    // ---- the L best candidates of these blocks
-    const int chosen = sm.found;
-    floor = chosen == L ? sm.key[L - 1] : 0;
-    const float floor_value = floor ? unordered(static_cast<uint32_t>(floor >> 32)) : -FLT_MAX;
-    list.clear();
-    for (int t = warp; t < chosen << sh; t += kWarps) {
-      const int e = sm.idx[t >> sh];
-      const int w = e / NB, b = e % NB;
-      const float2 base = sm.base[w];
-      if ((ended >> w) & 1) {
-        if ((t & ((1 << sh) - 1)) == 0)
-          list.offer(lane == 0 ? value_key(base, 0.f) : 0,
-                     static_cast<uint32_t>(w) * V + a.end_token, floor, lane);
-        continue;
-      }
-      const Row<T> row(a, r, w);
-      const int i = ((b << sh) + (t & ((1 << sh) - 1))) * 32 + lane;
-      uint32_t v[8];
-      row.load(i, v, sm.edges[warp]);
-      // logits from here on may reach the floor (two roundings of the sums)
-      const float slack = (fabsf(floor_value) + fabsf(base.x)) * 0x1p-21f;
-      const float least = (floor_value - base.x) - slack;
-      unsigned hits = 0;
-#pragma unroll
-      for (int j = 0; j < E::kVec / 2; ++j) {
-        const float2 x = E::pair(v, j);
-        hits |= (x.x >= least ? 1u : 0u) << (2 * j) | (x.y >= least ? 1u : 0u) << (2 * j + 1);
-      }
-      while (__any_sync(0xffffffffu, hits != 0)) {
-        uint64_t k = 0;
-        uint32_t id = 0;
-        if (hits) {
-          const int x = i * E::kVec - row.lead + __ffs(hits) - 1;
-          hits &= hits - 1;
-          if (x >= 0 && x < V) {
-            k = value_key(base, sane(E::load(row.p, x)));
-            id = static_cast<uint32_t>(w) * V + x;
-          }
-        }
-        __syncwarp();
-        list.offer(k, id, floor, lane);
-      }
-    }
-    __syncthreads();  // sm.idx has been read
-    join_lists(sm, list, L, warp, lane);
-    // ---- order between rows, where their sums may not tell
-    if (threadIdx.x == 0) sm.doubtful = 0;
-    __syncthreads();
-    const int found = sm.found;
-    for (int i = threadIdx.x; i < K && i + 1 < found; i += kThreads) {
-      const int w0 = sm.idx[i] / V, w1 = sm.idx[i + 1] / V;
-      const unsigned both = 1u << w0 | 1u << w1;
-      if (w0 != w1 && (both & ~exact) && key_gap(sm.key[i], sm.key[i + 1]) < a.margin)
-        atomicOr(&sm.doubtful, both);
-    }
-    if (found == L) {
-      // Another row's candidate next to the last choice, displaced by candidates of
-      // that choice's own row?
-      const uint64_t last = sm.key[K - 1];
-      const int w0 = sm.idx[K - 1] / V;
-      if (static_cast<int>(sm.idx[K] / V) == w0 && key_gap(last, sm.key[K]) < a.margin) {
-        for (int e = threadIdx.x; e < entries; e += kThreads) {
-          const int w = e / NB, b = e % NB;
-          const unsigned both = 1u << w0 | 1u << w;
-          if (w == w0 || !(both & ~exact)) continue;
-          const uint64_t k = entry_key(w, b);
-          if (k == 0 || key_gap(last, k) >= a.margin) continue;
-          bool near = k < last;
-          if (!near && ((live >> w) & 1)) {
-            const Row<T> row(a, r, w);
-            const int x0 = ((b << sh) * 32) * E::kVec - row.lead;
-            const int x1 = min(V, x0 + (32 << sh) * E::kVec);
-            for (int x = max(0, x0); x < x1 && !near; ++x) {
-              const uint64_t kx = value_key(sm.base[w], sane(E::load(row.p, x)));
-              near = kx != 0 && kx < last && key_gap(last, kx) < a.margin;
-            }
-          }
-          if (near) atomicOr(&sm.doubtful, both);
-        }
-      }
+      // order between rows, where their sums may not tell
+      if (threadIdx.x < K)
+#pragma unroll 1
+        for (int i = threadIdx.x, j = i + 1;
+             j < picked && key_gap(sm.key[i], sm.key[j]) < a.margin; ++j)
+          c.doubt(sm.idx[i] / V, sm.idx[j] / V);
+    } else {
+      __syncthreads();  // (sm.pick ends here)
+      choose_by_lists(c);
     }
     __syncthreads();
-    const unsigned again = sm.doubtful & ~exact;
+    const unsigned again = sm.doubtful & ~c.exact;
     if (!again) break;
-    // ---- those rows' sums once more
-    if (threadIdx.x < 64) {
-      const double t = exp2(threadIdx.x / 64.0);
-      const float hi = static_cast<float>(t);
-      sm.table.t[threadIdx.x] = make_float2(hi, static_cast<float>(t - hi));
-    }
-    __syncthreads();
-    for (unsigned todo = again; todo; todo &= todo - 1) {
-      const int w = __ffs(todo) - 1;
-      const Row<T> row(a, r, w);
-      const float top = sm.top[w];
-      FixedSum sum;
-      for (int x = threadIdx.x; x < V; x += kThreads)
-        add_exp(sum, sm.table, sane(E::load(row.p, x)), top);
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        sum.hi += __shfl_xor_sync(0xffffffffu, sum.hi, off);
-        sum.lo += __shfl_xor_sync(0xffffffffu, sum.lo, off);
-      }
-      if (lane == 0) sm.sum[warp] = sum;
-      __syncthreads();
-      const float mine = __shfl_sync(0xffffffffu, score, w);
-      if (threadIdx.x == 0) {
-        for (int i = 1; i < kWarps; ++i) {
-          sum.hi += sm.sum[i].hi;
-          sum.lo += sm.sum[i].lo;
-        }
-        const double s = static_cast<double>(sum.hi) * 0x1p-18 +
-                         static_cast<double>(sum.lo) * 0x1p-50;
-        const double b = (mine - static_cast<double>(top)) - log(s);
-        const float hi = static_cast<float>(b);
-        sm.base[w] = make_float2(hi, static_cast<float>(b - hi));
-      }
-      __syncthreads();
-    }
-    exact |= again;
+    sum_again(c, again, score);
+    c.exact |= again;
   }
 
   // ---- the choices
@@ -700,22 +900,29 @@ cudaError_t launch(const BeamSelectArgs& a, int ctas, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_beam_select(BeamSelectArgs a, bool fp32, int num_sms, cudaStream_t stream) {
-  const int elems = 32 * (fp32 ? 8 : 16);  // of a warp load
-  // a row may begin anywhere in its first 32 bytes
-  const int64_t steps = (static_cast<int64_t>(a.vocab) + elems / 32 - 1 + elems - 1) / elems;
+  const int lead = fp32 ? 7 : 15;  // a row may begin anywhere in its first 32 bytes
+  const int elems = 32 * kVecs * (lead + 1);  // of a warp load
+  const int64_t steps = (static_cast<int64_t>(a.vocab) + lead + elems - 1) / elems;
   int sh = 0;
   while (((steps + (1 << sh) - 1) >> sh) * a.num_beams > kMaxEntries) ++sh;
   a.block_shift = sh;
   a.blocks_per_row = static_cast<int>((steps + (1 << sh) - 1) >> sh);
-  const int ctas = kMaxCtas / 2;
-  // Twice the error of a row's sum in the pass, relative, all roundings adding up:
-  // exponentials 2^-22, their arguments 1.3 * 2^-24 |x - m| (a weighted mean of which is
-  // at most ln V), the additions of a lane (9 in a step of 4 loads, 3 more for each step),
-  // a warp, the CTA and the cluster, a rescaling by an exponential at each of the three.
-  const double chain = 9 + static_cast<double>((steps + ctas * kWarps * kUnroll - 1) /
-                                               (ctas * kWarps * kUnroll)) * 3 + 5 + 3 + 5;
-  const double err = 0x1p-22 * 4 + 1.3 * 0x1p-24 * (4 + log(static_cast<double>(a.vocab))) +
-                     chain * 0x1p-24;
+  // e / blocks_per_row = e * inverse / 2^32 for e < kMaxEntries
+  a.blocks_inverse = static_cast<uint32_t>(((int64_t{1} << 32) - 1) / a.blocks_per_row + 1);
+  // As many CTAs per request as run at once, two on an SM.
+  int ctas = kMaxCtas;
+  while (ctas > 1 && static_cast<int64_t>(a.num_requests) * ctas > 2 * num_sms) ctas /= 2;
+  // Twice the error of a row's sum in the pass, relative, all roundings adding up (a step
+  // of fp32 is 2^-24): exponentials 4 steps, their arguments 1.3 |x - m| (a weighted mean of
+  // which is at most ln V, and kMove); the additions of a lane, 10 and one for each load, a
+  // warp, a CTA and a cluster; rescalings by an exponential, 5 and its argument's, once for
+  // a lane (a moved reference shrinks what came before) and at each of the three; the
+  // logarithm's 2 ln V.
+  const int64_t lane_loads =
+      (static_cast<int64_t>(a.num_beams) * (a.blocks_per_row / ctas + 1) / kWarps + 1) << sh;
+  const double ln_v = log(static_cast<double>(a.vocab));
+  const double err = 0x1p-24 * (4 + 1.3 * (kMove + ln_v) + 10 + static_cast<double>(lane_loads) +
+                                5 + 4 + 4 + 4 * (5 + 1.3 * kMove) + 2 * ln_v);
   a.margin = static_cast<float>(2 * err);
   const bool wide = a.num_choices + 1 > 32;
   if (fp32) return wide ? launch<float, 3>(a, ctas, stream) : launch<float, 1>(a, ctas, stream);

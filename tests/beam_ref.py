@@ -17,7 +17,7 @@ import numpy as np
 
 def score_tolerance(value, vocab, fp32):
     steps = math.ceil(vocab / (8 * 8 * 4 * 32 * (8 if fp32 else 16))) + 1
-    err = 2.0**-20 + 1.3 * 2.0**-24 * (4 + math.log(vocab)) + (25 + 3 * steps) * 2.0**-24
+    err = 2.0**-20 + 2.0**-23 * math.log(vocab) + 1.3 * 2.0**-24 * (4 + math.log(vocab)) + (25 + 3 * steps) * 2.0**-24
     return err + 2.0**-24 * np.abs(value)
 
 
@@ -41,8 +41,8 @@ def select(logits, scores, finished, end_token, num_choices):
             top = x[r, w].max()
             if top == -np.inf:
                 continue
-            lse = top + math.log(math.fsum(np.exp(x[r, w] - top)))
-            value[w] = x[r, w] + (s - lse)
+            # (in this order: s and the logarithm vanish next to a far logit)
+            value[w] = (x[r, w] - top) + (s - math.log(math.fsum(np.exp(x[r, w] - top))))
         flat = value.ravel()
         best = np.argsort(-flat, kind="stable")[:num_choices]
         best = best[flat[best] > -np.inf]
