@@ -523,6 +523,41 @@ int pa_qk_norm_rope_cache_fp8(void *q_out, void *k_out, const void *q, const voi
                               void *stream);
 
 /*
+ * Decode of sequences that share long prefixes, a group's prefix attended once for all
+ * its members: the beams of a prompt, or every request behind one system prompt.  The
+ * attention is pa_decode's (same formula, same outputs); the prefix's part of it is a
+ * dense product of all the members' queries on tcgen05 tensor cores, cut along the keys
+ * over the whole device, and joined with each sequence's own part by log-sum-exp.
+ * Where pa_cascade_decode takes up to 32 query rows per kv head and group, a group may
+ * have any number of members here.
+ *   group_offsets  device int32 [num_groups + 1], rising: sequences
+ *              [group_offsets[g], group_offsets[g + 1]) are group g.  A sequence in no
+ *              group shares nothing
+ *   max_group_size  host int, at least every group's number of members
+ *   shared_blocks  device int32 [num_groups]: the members' first shared_blocks[g] table
+ *              entries name the same blocks (the caller guarantees it; they are read
+ *              from the first member's row).  A member may end inside them
+ *   workspace  device, pa_decode_shared_workspace_size bytes, 256-byte aligned, with
+ *              any content; one call in flight per workspace
+ * head_dim must be 128; the V of tokens that some member of the group sees must be
+ * finite; other slots may hold anything.  Equal calls give equal bits.  Weights over
+ * the prefix are rounded to bf16 (each within 2^-8 of itself), as in the prefill.
+ * Groups or shared_blocks out of range set PA_DEVERR_GROUP and are clamped: members
+ * past max_group_size attend all their blocks on their own.  Other device errors as
+ * pa_decode.
+ */
+size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int max_group_size,
+                                       int num_q_heads, int num_kv_heads, int head_dim,
+                                       int block_size);
+int pa_decode_shared(void *out, const void *q, const void *k_cache, const void *v_cache,
+                     const int32_t *block_tables, int max_blocks_per_seq,
+                     const int32_t *seq_lens, int num_seqs, const int32_t *group_offsets,
+                     int num_groups, int max_group_size, const int32_t *shared_blocks,
+                     int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                     int64_t num_blocks, float scale, float *out_lse, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
  * Beam search: the num_choices best continuations of each request, over its
  * num_beams beams and the vocabulary.  Beam w with score s_w (a sum of
  * log-probabilities) and logits x_w proposes token v with the value
@@ -656,7 +691,7 @@ int pa_device_error_flags(unsigned int *flags, int reset);
  * Test entry points of the failure path (no product call needs them).  Each
  * makes one launch of the kernel its name gives, with the same arguments as
  * pa_decode (workspace and mode included; no lse) / pa_prefill_chunk /
- * pa_prefill_window (no lse), in which the producer / loader warps issue no load at all and every
+ * pa_prefill_window / pa_decode_shared (its prefix pass; no lse), in which the producer / loader warps issue no load at all and every
  * mbarrier wait is bounded by wait_limit_us (1 .. 2,000,000 us) instead of
  * the default two seconds.  Every wait therefore runs out with no copy in
  * flight: the kernel sets PA_DEVERR_TIMEOUT, skips the rest of its waits,
@@ -688,6 +723,15 @@ int pa_test_prefill_window_stalled(void *out, const void *q, const void *k_cache
                                    int num_q_heads, int num_kv_heads, int head_dim,
                                    int block_size, int64_t num_blocks, int window, int sinks,
                                    float scale, unsigned int wait_limit_us, void *stream);
+int pa_test_decode_shared_stalled(void *out, const void *q, const void *k_cache,
+                                  const void *v_cache, const int32_t *block_tables,
+                                  int max_blocks_per_seq, const int32_t *seq_lens, int num_seqs,
+                                  const int32_t *group_offsets, int num_groups,
+                                  int max_group_size, const int32_t *shared_blocks,
+                                  int num_q_heads, int num_kv_heads, int head_dim,
+                                  int block_size, int64_t num_blocks, float scale,
+                                  void *workspace, size_t workspace_bytes,
+                                  unsigned int wait_limit_us, void *stream);
 
 #ifdef __cplusplus
 }

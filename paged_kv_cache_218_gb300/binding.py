@@ -1,6 +1,6 @@
 """Thin binding of libpa.so (include/pa.h), through ctypes and, for the
-windowed-attention, norm-rotation and beam-search calls, a small extension
-(_pycall).
+windowed-attention, norm-rotation, shared-prefix and beam-search calls, a small
+extension (_pycall).
 
 Argument marshalling only: each function takes torch tensors, checks their
 dtype / device / contiguity, and passes raw pointers, sizes and the current
@@ -81,6 +81,9 @@ _SIGS = {
                                     _P, _P, _I, _I, _I, _I, _L, _F, _I, _P, _S, _P], _I),
     "pa_test_prefill_window_stalled": ([_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _I, _I, _I, _I, _I,
                                         _I, _L, _I, _I, _F, ctypes.c_uint, _P], _I),
+    "pa_decode_shared_workspace_size": ([_I, _I, _I, _I, _I, _I, _I], _S),
+    "pa_test_decode_shared_stalled": ([_P, _P, _P, _P, _P, _I, _P, _I, _P, _I, _I, _P, _I, _I, _I,
+                                       _I, _L, _F, _P, _S, ctypes.c_uint, _P], _I),
     "pa_rope_increments": ([_P, ctypes.POINTER(_F), _I, _D, _I, _D, _D, _D, _D], _I),
     "pa_test_decode_stalled": ([_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _L, _F, _I, _P,
                                 _S, ctypes.c_uint, _P], _I),
@@ -375,6 +378,22 @@ def pa_decode_window(out, q, k_cache, v_cache, block_tables, seq_lens, window, s
                           out_lse, stream)
 
 
+def pa_decode_shared_workspace_size(num_seqs, num_groups, max_group_size, num_q_heads,
+                                    num_kv_heads, head_dim, block_size=16) -> int:
+    return int(_lib.pa_decode_shared_workspace_size(num_seqs, num_groups, max_group_size,
+                                                    num_q_heads, num_kv_heads, head_dim,
+                                                    block_size))
+
+
+def pa_decode_shared(out, q, k_cache, v_cache, block_tables, seq_lens, group_offsets,
+                     max_group_size, shared_blocks, scale, workspace, out_lse=None,
+                     stream=None) -> None:
+    """Decode of sequences in groups whose first shared_blocks[g] blocks are the same: the
+    prefix is attended once for all members (any number of them)."""
+    _pycall.decode_shared(out, q, k_cache, v_cache, block_tables, seq_lens, group_offsets,
+                          max_group_size, shared_blocks, scale, workspace, out_lse, stream)
+
+
 def pa_beam_select(parents, tokens, out_scores, logits, scores, finished=None, out_finished=None,
                    end_token=-1, stream=None) -> None:
     """The best continuations of each request: logits [requests, beams, vocabulary] (bf16 or
@@ -632,3 +651,25 @@ def pa_test_prefill_window_stalled(out, q, k_cache, v_cache, block_tables, cu_q_
         block_tables.shape[1], _ptr(cu_q_lens), _ptr(q_start_pos), _ptr(seq_lens),
         q_start_pos.shape[0], T, int(max_q_len), Hq, Hkv, D, bs, nb, int(window), int(sinks),
         float(scale), int(wait_limit_us), _stream(stream)))
+
+
+def pa_test_decode_shared_stalled(out, q, k_cache, v_cache, block_tables, seq_lens, group_offsets,
+                                  max_group_size, shared_blocks, scale, workspace,
+                                  wait_limit_us=1000, stream=None) -> None:
+    """One shared-prefix decode whose prefix loaders issue no load, every wait bounded by
+    wait_limit_us: the kernel must report PA_DEVERR_TIMEOUT and return."""
+    _need(out, "out", torch.bfloat16, 3)
+    _need(q, "q", torch.bfloat16, 3)
+    _need(k_cache, "k_cache", torch.bfloat16, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, 4)
+    _need(block_tables, "block_tables", torch.int32, 2)
+    for t, name in ((seq_lens, "seq_lens"), (group_offsets, "group_offsets"),
+                    (shared_blocks, "shared_blocks")):
+        _need(t, name, torch.int32, 1)
+    S, Hq, D = q.shape
+    nb, bs, Hkv, _ = k_cache.shape
+    _check("pa_test_decode_shared_stalled", _lib.pa_test_decode_shared_stalled(
+        _ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+        block_tables.shape[1], _ptr(seq_lens), S, _ptr(group_offsets), shared_blocks.shape[0],
+        int(max_group_size), _ptr(shared_blocks), Hq, Hkv, D, bs, nb, float(scale),
+        _ptr(workspace), workspace.numel(), int(wait_limit_us), _stream(stream)))

@@ -16,6 +16,7 @@
 #include "pa_beam.h"
 #include "pa_internal.h"
 #include "pa_ptx.cuh"
+#include "pa_shared.h"
 #include "pa_window.h"
 
 namespace pa {
@@ -1561,6 +1562,162 @@ int pa_test_prefill_window_stalled(void* out, const void* q, const void* k_cache
                              max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
                              num_blocks, window, sinks, scale, nullptr, stream, 1,
                              static_cast<uint64_t>(wait_limit_us) * 1000u);
+}
+
+// Slots, teams and workspace of a shared-prefix decode.
+struct SharedPlan {
+  SharedLayout lay;
+  size_t ml_off, info_off, bytes;
+  bool fits;
+};
+
+static SharedPlan shared_plan(int num_seqs, int num_groups, int max_group_size, int num_kv_heads,
+                              int group, int num_sms) {
+  SharedPlan p{};
+  const int pairs = num_sms / 2 < 1 ? 1 : num_sms / 2;
+  p.lay.team_pairs = num_kv_heads < pairs ? num_kv_heads : pairs;
+  p.lay.teams = pairs / p.lay.team_pairs;
+  p.lay.tile_tokens = 128 / group;
+  const int rows = 2 * p.lay.tile_tokens;
+  const int members = max_group_size < num_seqs ? max_group_size : num_seqs;
+  p.lay.slot_rows = (members < rows ? members : rows) * group;
+  // every group may begin a unit, and every `rows` sequences
+  const int64_t units = static_cast<int64_t>(num_groups) + num_seqs / rows;
+  const int64_t out_rows = (units + p.lay.teams) * num_kv_heads * p.lay.slot_rows;
+  p.lay.max_units = static_cast<int>(units < (1 << 24) ? units : 1 << 24);
+  p.fits = units < (1 << 24) && out_rows < (int64_t{1} << 40);
+  p.ml_off = round256(static_cast<size_t>(out_rows) * 128 * sizeof(float));
+  p.info_off = p.ml_off + round256(static_cast<size_t>(out_rows) * sizeof(float2));
+  p.bytes = p.info_off + round256((static_cast<size_t>(num_groups) + 1) * sizeof(int4));
+  return p;
+}
+
+size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int max_group_size,
+                                       int num_q_heads, int num_kv_heads, int head_dim,
+                                       int block_size) {
+  if (check_shape(num_q_heads, num_kv_heads, head_dim, block_size) != PA_OK || head_dim != 128 ||
+      num_seqs < 0 || num_groups < 0 || max_group_size < 1)
+    return 0;
+  DeviceInfo* d;
+  if (current_device_info(&d) != PA_OK) return 0;
+  const SharedPlan p = shared_plan(num_seqs, num_groups, max_group_size, num_kv_heads,
+                                   num_q_heads / num_kv_heads, d->num_sms);
+  return p.fits ? p.bytes : 0;
+}
+
+static int decode_shared_impl(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* seq_lens, int num_seqs, const int32_t* group_offsets,
+                              int num_groups, int max_group_size, const int32_t* shared_blocks,
+                              int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                              int64_t num_blocks, float scale, float* out_lse, void* workspace,
+                              size_t workspace_bytes, void* stream, int stall_loads = 0,
+                              uint64_t wait_ns = 0) {
+  if (int rc = check_shape(num_q_heads, num_kv_heads, head_dim, block_size)) return rc;
+  if (num_seqs < 0 || max_blocks_per_seq <= 0 || num_blocks <= 0 || num_groups < 0 ||
+      max_group_size < 1)
+    return PA_ERR_INVALID;
+  if (head_dim != 128 || num_blocks * kBlockSize > (int64_t)INT32_MAX ||
+      max_blocks_per_seq > INT32_MAX / kBlockSize ||
+      static_cast<int64_t>(num_seqs) * num_kv_heads > INT32_MAX / kMaxWindowSplit)
+    return PA_ERR_UNSUPPORTED;
+  if (!(scale > 0.f) || !isfinite(scale)) return PA_ERR_INVALID;
+  if (num_seqs == 0) return PA_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !seq_lens || !group_offsets ||
+      (num_groups > 0 && !shared_blocks))
+    return PA_ERR_INVALID;
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(group_offsets, 4) ||
+      (num_groups > 0 && !aligned(shared_blocks, 4)) || (out_lse && !aligned(out_lse, 4)))
+    return PA_ERR_INVALID;
+  DeviceInfo* d;
+  if (int rc = current_device_info(&d)) return rc;
+  const int group = num_q_heads / num_kv_heads;
+  const SharedPlan p =
+      shared_plan(num_seqs, num_groups, max_group_size, num_kv_heads, group, d->num_sms);
+  const int64_t unit_tiles = (max_blocks_per_seq + 7) / 8;
+  if (!p.fits || p.lay.max_units > INT32_MAX / unit_tiles) return PA_ERR_UNSUPPORTED;
+  if (!workspace || workspace_bytes < p.bytes || !aligned(workspace, 256))
+    return PA_ERR_WORKSPACE;
+  SharedDecodeArgs a{};
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k_cache);
+  a.v = static_cast<const __nv_bfloat16*>(v_cache);
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.out_lse = out_lse;
+  a.err = d->err;
+  a.num_blocks = num_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.group = group;
+  a.window = INT32_MAX;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  SharedArgs& x = a.shared;
+  x.block_tables = block_tables;
+  x.seq_lens = seq_lens;
+  x.group_offsets = group_offsets;
+  x.shared_blocks = shared_blocks;
+  x.err = d->err;
+  x.num_blocks = num_blocks;
+  x.max_blocks = max_blocks_per_seq;
+  x.num_seqs = num_seqs;
+  x.num_groups = num_groups;
+  x.max_group = max_group_size;
+  x.num_q_heads = num_q_heads;
+  x.num_kv_heads = num_kv_heads;
+  x.group = group;
+  x.scale_log2 = a.scale_log2;
+  x.stall_loads = stall_loads;
+  x.wait_ns = wait_ns;
+  x.lay = p.lay;
+  char* const ws = static_cast<char*>(workspace);
+  x.lay.part_o = reinterpret_cast<float*>(ws);
+  x.lay.part_ml = reinterpret_cast<float2*>(ws + p.ml_off);
+  x.lay.info = reinterpret_cast<int4*>(ws + p.info_off);
+  CUtensorMap tm_q, tm_k, tm_v;
+  if (encode_q_map(&tm_q, q, num_seqs, num_q_heads, head_dim, group, p.lay.tile_tokens) ||
+      encode_pool_map(&tm_k, k_cache, num_blocks, num_kv_heads, head_dim, kPoolKeyTile) ||
+      encode_pool_map(&tm_v, v_cache, num_blocks, num_kv_heads, head_dim, kPool2D))
+    return PA_ERR_CUDA;
+  if (launch_shared_prefix(x, &tm_q, &tm_k, &tm_v, static_cast<cudaStream_t>(stream)) !=
+          cudaSuccess ||
+      launch_shared_decode(a, d->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return PA_OK;
+}
+
+int pa_decode_shared(void* out, const void* q, const void* k_cache, const void* v_cache,
+                     const int32_t* block_tables, int max_blocks_per_seq, const int32_t* seq_lens,
+                     int num_seqs, const int32_t* group_offsets, int num_groups,
+                     int max_group_size, const int32_t* shared_blocks, int num_q_heads,
+                     int num_kv_heads, int head_dim, int block_size, int64_t num_blocks,
+                     float scale, float* out_lse, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  return decode_shared_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
+                            num_seqs, group_offsets, num_groups, max_group_size, shared_blocks,
+                            num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                            out_lse, workspace, workspace_bytes, stream);
+}
+
+int pa_test_decode_shared_stalled(void* out, const void* q, const void* k_cache,
+                                  const void* v_cache, const int32_t* block_tables,
+                                  int max_blocks_per_seq, const int32_t* seq_lens, int num_seqs,
+                                  const int32_t* group_offsets, int num_groups,
+                                  int max_group_size, const int32_t* shared_blocks,
+                                  int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                  int64_t num_blocks, float scale, void* workspace,
+                                  size_t workspace_bytes, unsigned int wait_limit_us,
+                                  void* stream) {
+  if (wait_limit_us < 1 || wait_limit_us > 2000000u) return PA_ERR_INVALID;
+  return decode_shared_impl(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, seq_lens,
+                            num_seqs, group_offsets, num_groups, max_group_size, shared_blocks,
+                            num_q_heads, num_kv_heads, head_dim, block_size, num_blocks, scale,
+                            nullptr, workspace, workspace_bytes, stream, 1,
+                            static_cast<uint64_t>(wait_limit_us) * 1000u);
 }
 
 int pa_beam_select(int32_t* parents, int32_t* tokens, float* out_scores, uint8_t* out_finished,

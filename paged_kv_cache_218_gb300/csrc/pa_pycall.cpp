@@ -1,5 +1,5 @@
-// pa_pycall.cpp -- argument marshalling of the windowed-attention,
-// norm-rotation and beam-search calls, as a CPython extension (_pycall.so).
+// pa_pycall.cpp -- argument marshalling of the windowed-attention, norm-rotation,
+// shared-prefix and beam-search calls, as a CPython extension (_pycall.so).
 //
 // These calls are made per layer and step, and the smallest run for a few
 // microseconds on the GPU: checked and passed on in Python, a call's arguments
@@ -326,6 +326,50 @@ PyObject* norm_rope(PyObject* const* a, Py_ssize_t n) {
   return done(fp8 ? "pa_qk_norm_rope_cache_fp8" : "pa_qk_norm_rope_cache", rc);
 }
 
+// decode_shared(out, q, k_cache, v_cache, block_tables, seq_lens, group_offsets, max_group_size,
+//               shared_blocks, scale, workspace, out_lse, stream)
+PyObject* decode_shared(PyObject* const* a, Py_ssize_t n) {
+  if (!count(n, 13)) return nullptr;
+  const at::Tensor *tq, *tk, *tb, *tg, *tw;
+  if (!(tq = look(a[1], "q", kBf16, 3)) || !contiguous(*tq, "q") ||
+      !(tk = look(a[2], "k_cache", kBf16, 4)) || !(tb = look(a[4], "block_tables", kI32, 2)) ||
+      !(tg = look(a[8], "shared_blocks", kI32, 1)) || !(tw = look(a[10], "workspace", kU8, 1)))
+    return nullptr;
+  const Shape qs = tq->sizes(), ks = tk->sizes();
+  const int dev = static_cast<int>(tq->get_device());
+  const int64_t blocks = tb->size(1), groups = tg->size(0), bytes = tw->size(0);
+  int members;
+  void *out, *k, *v, *bt, *sl, *go, *sb, *ws, *lse, *stream;
+  float scale;
+  if (!tensor(a[2], "k_cache", kBf16, {ks[0], ks[1], ks[2], qs[2]}, dev, &k) ||
+      !tensor(a[0], "out", kBf16, qs, dev, &out) ||
+      !tensor(a[3], "v_cache", kBf16, ks, dev, &v) ||
+      !tensor(a[4], "block_tables", kI32, {qs[0], blocks}, dev, &bt) ||
+      !tensor(a[5], "seq_lens", kI32, {qs[0]}, dev, &sl) ||
+      !tensor(a[6], "group_offsets", kI32, {groups + 1}, dev, &go) ||
+      !whole(a[7], "max_group_size", 1, INT_MAX, &members) ||
+      !tensor(a[8], "shared_blocks", kI32, {groups}, dev, &sb) || !real(a[9], &scale) ||
+      !tensor(a[10], "workspace", kU8, {bytes}, dev, &ws) ||
+      !optional(a[11], "out_lse", kF32, {qs[0], qs[1]}, dev, &lse) || !fits(qs[0], "q") ||
+      !fits(qs[1], "q") || !fits(qs[2], "q") || !fits(blocks, "block_tables") ||
+      !fits(ks[1], "k_cache") || !fits(ks[2], "k_cache") || !fits(groups, "shared_blocks") ||
+      !queue(a[12], dev, &stream))
+    return nullptr;
+  const void* q = tq->data_ptr();
+  const int S = static_cast<int>(qs[0]), Hq = static_cast<int>(qs[1]), D = static_cast<int>(qs[2]),
+            bs = static_cast<int>(ks[1]), Hkv = static_cast<int>(ks[2]);
+  const int64_t nb = ks[0];
+  int rc;
+  Py_BEGIN_ALLOW_THREADS;
+  rc = pa_decode_shared(out, q, k, v, static_cast<const int32_t*>(bt), static_cast<int>(blocks),
+                        static_cast<const int32_t*>(sl), S, static_cast<const int32_t*>(go),
+                        static_cast<int>(groups), members, static_cast<const int32_t*>(sb), Hq,
+                        Hkv, D, bs, nb, scale, static_cast<float*>(lse), ws,
+                        static_cast<size_t>(bytes), stream);
+  Py_END_ALLOW_THREADS;
+  return done("pa_decode_shared", rc);
+}
+
 // A contiguous tensor of truth values or bytes of this shape and device, or None.
 bool marks(PyObject* o, const char* name, Shape want, int device, void** p) {
   *p = nullptr;
@@ -467,6 +511,7 @@ PyMethodDef methods[] = {
     {"decode_window", method(guarded<decode_window>), METH_FASTCALL, nullptr},
     {"prefill_window", method(guarded<prefill_window>), METH_FASTCALL, nullptr},
     {"norm_rope", method(guarded<norm_rope>), METH_FASTCALL, nullptr},
+    {"decode_shared", method(guarded<decode_shared>), METH_FASTCALL, nullptr},
     {"beam_select", method(guarded<beam_select>), METH_FASTCALL, nullptr},
     {"beam_reorder", method(guarded<beam_reorder>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

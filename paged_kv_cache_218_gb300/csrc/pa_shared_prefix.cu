@@ -1,0 +1,865 @@
+// pa_shared_prefix.cu -- attention of the sequences of a group over the prefix that
+// they share, read once for all of them, on tcgen05 tensor cores (sm_103a).
+//
+// The queries of a group's members, G heads a kv head, are the rows of one dense
+// product with the prefix's keys: no mask but the members' lengths.  What is left
+// of each sequence is decoded by pa_window_decode.cu, which joins both.
+//
+// The tensor-core pipeline of a key tile (128 keys) is that of the windowed prefill:
+// a CTA pair (cta_group::2) on two query tiles of up to 128 rows, K and V halves
+// loaded by each CTA, three score buffers in tensor memory, online softmax with P
+// written back over its scores, bounded waits.  What differs:
+//
+//  * Work is cut along the keys, so that a single long prefix fills the device: teams
+//    of pairs, one pair for each kv head, take equal ranges of all key tiles.  The
+//    pairs of a team read the same blocks at the same time, each its own head's 256
+//    bytes of a token's row; together they read whole rows, which memory serves faster.
+//  * A piece (a unit's key tiles in a team's range) leaves its reference maximum, sum
+//    and weighted values, in fp32 and undivided, for the decode to join.
+//  * Warps whose 32 rows no member fills wait for scores and pass them on unread.
+//
+// What bounds it: with up to 256 rows a kv head, HBM: a pair takes 0.75 us for a tile's
+// 64 KB, which is both its share of the memory's rate and what its two products and
+// their hand-overs take; with more rows, the tensor pipe.
+#include <mutex>
+
+#include "pa_prefill_body.cuh"
+#include "pa_shared.h"
+#include "pa_window_ptx.cuh"
+
+namespace pa {
+namespace pre {
+namespace {
+
+constexpr uint64_t kSettleNs = 1000000;  // far longer than any copy takes
+// Reference maximum (log2 units) of a row that saw nothing yet: next to the lowest
+// fp32, so that no visible score lies below it; hidden scores (-inf) weigh 0.
+constexpr float kFloor = -0x1.fffff0p127f;
+constexpr float kFarScore = 0x1p31f;  // (log2 units)
+
+// Shared memory of one CTA of a pair: two Q tiles, four K and three V half
+// tiles, block ids of both loaders, the softmax's exchange, barriers.
+struct SPlan {
+  static constexpr int kNK = 4, kNV = 3;
+  static constexpr int kKSlot = kHalf, kVSlot = kHalf;
+  static constexpr int kQOff = 0;  // [2][2 * kHalf]
+  static constexpr int kKOff = kQOff + 4 * kHalf;
+  static constexpr int kVOff = kKOff + kNK * kKSlot;
+  static constexpr int kIdsOff = kVOff + kNV * kVSlot;
+  static constexpr int kRedOff = kIdsOff + 2 * kIdRing * 8 * 4;
+  static constexpr int kRedOff2 = kRedOff + 2 * 2 * 128 * 4;
+  static constexpr int kBarOff = kRedOff2 + 2 * 128 * 4;
+  static constexpr int kItemsOff = kBarOff + 448;  // [kItemRing]
+  static constexpr int kSmemBytes = kItemsOff + 8 * 64;
+};
+static_assert(SPlan::kSmemBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
+
+// One work item of a pair: a piece of a unit's key tiles, one kv head.
+struct Item {
+  int nkt;         // key tiles; 0 ends the list
+  int row;         // table row that names the prefix's blocks: the first member's
+  int kvh;
+  int q0, tokens;  // the unit's first member, and how many
+  int block0;      // first block of the piece
+  int nvb;         // blocks to read
+  int keys;        // keys [0, keys) of the sequence are the prefix
+  int hidden;      // rows of the last block from this one on are seen by no member; or 16
+  int slot;        // of the results
+};
+// Blocks of an item's key tile j: eight, fewer in the last one.
+__device__ __forceinline__ int tile_blocks(int nvb, int j) { return min(8, nvb - 8 * j); }
+
+constexpr int kItemRing = 8;
+static_assert(sizeof(Item) <= 64, "ring slot");
+static_assert(kBlockSize == 16, "shifts below");
+
+// Units and key tiles of 32 groups at a time, a lane each, and their sums, with
+// `before` units in front of them.  Groups that overlap could make more units than
+// there are slots: what is too many is left out.
+struct Groups {
+  SharedGroup g;
+  int units, tiles;          // of the lane's group
+  int units_sum, tiles_sum;  // up to and with it
+  __device__ __forceinline__ Groups(const SharedArgs& a, int g0, int before, int lane) {
+    g = SharedGroup{0, 0, 0, true};
+    if (g0 + lane < a.num_groups) g = shared_group(a, g0 + lane);
+    const int rows = 2 * a.lay.tile_tokens;
+    units = g.blocks > 0 ? (g.members + rows - 1) / rows : 0;
+    units_sum = units;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, units_sum, off);
+      if (lane >= off) units_sum = min(units_sum + u, 1 << 30);
+    }
+    if (__any_sync(0xffffffffu, before + units_sum > a.lay.max_units)) {
+      const int room = max(a.lay.max_units - before, 0);
+      const int start = units_sum - units;
+      if (units_sum > room) {
+        units = 0;
+        g.sound = false;
+      }
+      units_sum = __reduce_max_sync(0xffffffffu, start + units <= room ? start + units : 0);
+      units_sum = min(start + units, units_sum);
+    }
+    tiles = units * ((g.blocks + 7) >> 3);
+    tiles_sum = tiles;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, tiles_sum, off);
+      if (lane >= off) tiles_sum += t;
+    }
+  }
+};
+
+// Walks a pair's pieces.
+struct Cursor {
+  int pos, end;      // key tiles of the team's range that are left
+  int group0;        // groups looked at, 32 at a time,
+  int units, tiles;  // and units and key tiles before them
+  int team, kvh;
+};
+
+// The next item (nkt 0 at the end of the list).  Called by a whole warp.
+__device__ __forceinline__ Item next_item(const SharedArgs& a, Cursor& cur, int lane) {
+  Item it;
+  it.nkt = 0;
+  while (cur.pos < cur.end && cur.group0 < a.num_groups) {
+    const Groups x(a, cur.group0, cur.units, lane);
+    const unsigned past = __ballot_sync(0xffffffffu, cur.tiles + x.tiles_sum > cur.pos);
+    if (past == 0) {
+      cur.units += __shfl_sync(0xffffffffu, x.units_sum, 31);
+      cur.tiles += __shfl_sync(0xffffffffu, x.tiles_sum, 31);
+      cur.group0 += 32;
+      continue;
+    }
+    const int w = __ffs(past) - 1;
+    const int at = cur.pos - cur.tiles - __shfl_sync(0xffffffffu, x.tiles_sum - x.tiles, w);
+    const int unit0 = cur.units + __shfl_sync(0xffffffffu, x.units_sum - x.units, w);
+    const int first = __shfl_sync(0xffffffffu, x.g.first, w);
+    const int members = __shfl_sync(0xffffffffu, x.g.members, w);
+    const int blocks = __shfl_sync(0xffffffffu, x.g.blocks, w);
+    const int nkt = (blocks + 7) >> 3;
+    const int u = at / nkt, tile0 = at - u * nkt;
+    const int n = min(nkt - tile0, cur.end - cur.pos);
+    cur.pos += n;
+    const int rows = 2 * a.lay.tile_tokens;
+    it.row = first;
+    it.kvh = cur.kvh;
+    it.q0 = first + u * rows;
+    it.tokens = min(members - u * rows, rows);
+    it.block0 = 8 * tile0;
+    it.slot = (cur.team + unit0 + u) * a.num_kv_heads + cur.kvh;
+    it.keys = blocks * kBlockSize;
+    // the last key that some member sees
+    int seen = 0;
+    for (int i = lane; i < it.tokens; i += 32) seen = max(seen, __ldcg(a.seq_lens + it.q0 + i));
+    seen = min(__reduce_max_sync(0xffffffffu, seen), it.keys);
+    // (one block at least, so that there are scores)
+    const int left = ((seen + 15) >> 4) - it.block0;
+    it.nvb = min(max(left, 1), min(8 * n, blocks - it.block0));
+    it.nkt = (it.nvb + 7) >> 3;
+    it.hidden = min(max(seen - (it.block0 + it.nvb - 1) * kBlockSize, 0), kBlockSize);
+    break;
+  }
+  return it;
+}
+
+// The waits of pa_prefill_body.cuh with one copy of what follows a first
+// attempt: code size decides how long an item's ends take.
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, volatile int* abort,
+                                     unsigned int* err, uint64_t limit_ns) {
+  if (*abort) return false;
+  if (mbar_wait(bar, parity, limit_ns)) return true;
+  *abort = 1;
+  atomicOr(err, PA_DEVERR_TIMEOUT);
+  return false;
+}
+
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, volatile int* abort,
+                                     const SharedArgs& a) {
+  return mbar_try_wait(bar, parity) || wait_on(bar, parity, abort, a.err, a.wait_ns);
+}
+
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int* abort,
+                                          const SharedArgs& a) {
+  bool ok = __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+  if (!ok) {
+    ok = wait_on(bar, parity, abort, a.err, a.wait_ns);
+    __syncwarp();
+    ok = __all_sync(0xffffffffu, ok);
+  }
+  return ok;
+}
+
+// Ids of an item's blocks [8 t_first, + 8 kIdBatch) into a loader's
+// ring, where the ids of the warp's tile T are at slot T % kIdRing and `base` is
+// the number of the item's tile 0.  A slot is rewritten only when its tile's
+// loads have been issued.  Ids past the list are -1, a box outside the pool,
+// which reads as zeros.  Called by a whole warp.
+__device__ __noinline__ void fetch_ids(const int32_t* table, int64_t num_blocks, unsigned int* err,
+                                       int* ids, int nvb, int t_first, unsigned base) {
+  const int lane = threadIdx.x & 31;
+  int v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int vb = t_first * 8 + lane + 32 * i;
+    v[i] = vb < nvb ? __ldcg(table + vb) : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int vb = t_first * 8 + lane + 32 * i;
+    if (vb < nvb && (v[i] < 0 || v[i] >= num_blocks)) {
+      atomicOr(err, PA_DEVERR_BLOCK_ID);
+      v[i] = -1;
+    }
+    ids[(base * 8 + vb) % (kIdRing * 8)] = v[i];
+  }
+  __syncwarp();
+}
+
+// Bits [0, k) of 64.
+__device__ __forceinline__ uint64_t low_bits(int k) {
+  return k <= 0 ? 0ull : (k >= 64 ? ~0ull : (1ull << k) - 1);
+}
+
+// 32 bytes to memory.
+__device__ __forceinline__ void stg32(float* p, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                   reinterpret_cast<uint64_t>(p)),
+               "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_q,
+                          const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const SharedArgs a) {
+  using P = SPlan;
+  constexpr int kNK = P::kNK, kNV = P::kNV;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  const uint32_t bar_q = sbase + P::kBarOff;         // [2]: Q of the pair landed
+  const uint32_t bar_q_empty = bar_q + 16;           // [2]: its score products are done
+  const uint32_t bar_k_full = bar_q_empty + 16;      // [kNK]
+  const uint32_t bar_k_empty = bar_k_full + 8 * kNK;
+  const uint32_t bar_v_full = bar_k_empty + 8 * kNK;   // [kNV]: this CTA's V landed (edge tiles)
+  const uint32_t bar_v_ready = bar_v_full + 8 * kNV;   // [kNV]: V of the pair ready
+  const uint32_t bar_s_full = bar_v_ready + 8 * kNV;   // [kNS]: scores of a tile
+  const uint32_t bar_p_full = bar_s_full + 8 * kNS;    // [kNS]: softmax done
+  const uint32_t bar_o_done = bar_p_full + 8 * kNS;    // [kNS]: PV done, and so V slot free
+  const uint32_t bar_item = bar_o_done + 8 * kNS;      // [kItemRing]: item published
+  static_assert(32 + 8 * (2 * kNK + 2 * kNV + 3 * kNS + kItemRing) <= 336, "barrier area");
+  static_assert(kNV == kNS, "V slot of a tile = its score buffer");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P::kBarOff + 336);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 340);
+  volatile int* go_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 352);
+  auto ring_item = [&](unsigned k) {
+    return reinterpret_cast<Item*>(smem + P::kItemsOff + 64 * (k % kItemRing));
+  };
+  int* ids_smem = reinterpret_cast<int*>(smem + P::kIdsOff) +
+                  ((threadIdx.x >> 5) == kLoadVWarp ? kIdRing * 8 : 0);
+  float* red_max = reinterpret_cast<float*>(smem + P::kRedOff);
+  float* red_sum = reinterpret_cast<float*>(smem + P::kRedOff2);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.group, tpt = a.lay.tile_tokens;
+  const int rank = static_cast<int>(blockIdx.x) & 1;
+  const bool issuer = rank == 0;
+
+  if (tid == 0) {
+    for (int k = 0; k < 2; ++k) {
+      mbar_init(bar_q + 8 * k, 1);
+      mbar_init(bar_q_empty + 8 * k, 1);
+    }
+    for (int k = 0; k < kNK; ++k) {
+      mbar_init(bar_k_full + 8 * k, 1);
+      mbar_init(bar_k_empty + 8 * k, 1);
+    }
+    for (int k = 0; k < kNV; ++k) {
+      mbar_init(bar_v_full + 8 * k, 1);
+      mbar_init(bar_v_ready + 8 * k, 2);
+    }
+    for (int k = 0; k < kNS; ++k) {
+      mbar_init(bar_s_full + 8 * k, 1);
+      mbar_init(bar_p_full + 8 * k, kSoftmaxWarps * 2);
+      mbar_init(bar_o_done + 8 * k, 1);
+    }
+    for (int k = 0; k < kItemRing; ++k) mbar_init(bar_item + 8 * k, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc<2>(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish<2>();
+  }
+  tc_fence_before();
+  cluster_sync();  // both CTAs' barriers exist before either reports to the other
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  if (warp == kLoadKWarp || warp == kLoadVWarp) {
+    // ------------------------------------------------------------ loaders
+    const uint64_t pol = l2_policy_evict_last();
+    unsigned total = 0;  // tiles loaded by this warp, over all items
+    // after a timeout: let the copies in flight land before the CTA may exit
+    auto settle = [&]() {
+      if (!*abort_flag) return;
+      const uint64_t t = global_ns();
+      while (global_ns() - t < kSettleNs) __nanosleep(1000);
+    };
+    if (warp == kLoadKWarp) {
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+      }
+      // all key tiles, and where each group's begin (the first pair writes it down)
+      int units = 0, tiles = 0;
+      for (int g0 = 0; g0 < a.num_groups; g0 += 32) {
+        const Groups x(a, g0, units, lane);
+        if (blockIdx.x == 0 && g0 + lane < a.num_groups) {
+          a.lay.info[g0 + lane] =
+              make_int4(units + x.units_sum - x.units, tiles + x.tiles_sum - x.tiles,
+                        x.units > 0 ? (x.g.blocks + 7) >> 3 : 0, x.g.first);
+          if (!x.g.sound) atomicOr(a.err, PA_DEVERR_GROUP);
+        }
+        units += __shfl_sync(0xffffffffu, x.units_sum, 31);
+        tiles += __shfl_sync(0xffffffffu, x.tiles_sum, 31);
+      }
+      if (blockIdx.x == 0 && lane == 0) a.lay.info[a.num_groups] = make_int4(units, tiles, 0, 0);
+      const int pair = static_cast<int>(blockIdx.x >> 1);
+      const int team = pair / a.lay.team_pairs;
+      const int teams = shared_teams(a.lay, tiles);
+      const int from = team < teams ? static_cast<int>(static_cast<int64_t>(tiles) * team / teams) : 0;
+      const int to =
+          team < teams ? static_cast<int>(static_cast<int64_t>(tiles) * (team + 1) / teams) : 0;
+      Cursor cur{from, to, 0, 0, 0, team, pair - team * a.lay.team_pairs};
+      unsigned published = 0;
+      auto publish = [&]() {
+        if (cur.pos == cur.end && cur.kvh + a.lay.team_pairs < a.num_kv_heads)
+          cur = Cursor{from, to, 0, 0, 0, team, cur.kvh + a.lay.team_pairs};
+        const Item x = next_item(a, cur, lane);
+        if (lane == 0) {
+          *ring_item(published) = x;
+          mbar_arrive(bar_item + 8 * (published % kItemRing));
+        }
+        ++published;
+        return x;
+      };
+      // (One place for each step: the code of all roles has to stay small.)
+      Item it, next;
+      it.nkt = 0;
+      int jf = 0, jk = 0;  // tiles of `it` with ids, and loaded
+      int lead = 0;        // tiles of `it` to load before the next item is looked for
+      bool next_ids = true;
+      unsigned qi = 0;     // items begun
+      while (true) {
+        if (jk == lead) {
+          next = publish();
+          if (a.stall_loads) break;  // a stalled test launch issues no load
+          next_ids = next.nkt == 0;
+          lead = -1;
+        }
+        const bool more = jf < it.nkt && jk + kIdBatch / 2 >= jf;
+        if (more || (!next_ids && jf >= it.nkt && it.nkt - jk <= kIdBatch)) {
+          const Item& x = more ? it : next;
+          fetch_ids(a.block_tables + static_cast<int64_t>(x.row) * a.max_blocks + x.block0,
+                    a.num_blocks, a.err, ids_smem, x.nvb, more ? jf : 0,
+                    total - jk + (more ? 0 : it.nkt));
+          if (more)
+            jf += kIdBatch;
+          else
+            next_ids = true;
+        }
+        if (jk == it.nkt) {  // on to the next item
+          if (next.nkt == 0) break;
+          it = next;
+          jf = kIdBatch;
+          jk = 0;
+          const unsigned qb = qi & 1;
+          if (qi >= 2 &&
+              !wait_warp(bar_q_empty + 8 * qb, ((qi >> 1) - 1) & 1, abort_flag, a))
+            break;
+          lead = qi == 0 ? min(it.nkt, kNK) : 0;
+          ++qi;
+          if (lane < 2) {  // a half each
+            const uint32_t bar = bar_q + 8 * qb;
+            // (both CTAs' query tiles, tpt tokens of G heads, two halves)
+            if (issuer && lane == 0) mbar_arrive_expect_tx(bar, 4 * tpt * G * 128);
+            const uint32_t dst = sbase + P::kQOff + (2 * qb + lane) * kHalf;
+            const int row = it.q0 + rank * tpt;
+            if (issuer)
+              tma_load_3d(dst, &tm_q, lane * 64, it.kvh * G, row, bar, pol);
+            else
+              tma_load_3d_pair(dst, &tm_q, lane * 64, it.kvh * G, row, mapa_shared(bar, 0), pol);
+          }
+          __syncwarp();
+          if (lead == 0) continue;
+        }
+        const unsigned slot = total % kNK;
+        if (total >= kNK &&
+            !wait_warp(bar_k_empty + 8 * slot, ((total / kNK) - 1) & 1, abort_flag, a))
+          break;
+        const uint32_t bar = bar_k_full + 8 * slot;
+        // each CTA takes half of the tile's blocks, their number made even (an
+        // id past the list loads zeros)
+        const int half = (tile_blocks(it.nvb, jk) + 1) / 2;
+        if (lane == 0 && issuer) mbar_arrive_expect_tx(bar, half * 4 * kBlockBytes);
+        __syncwarp();
+        if (lane < half) {
+          const int id = ids_smem[(total % kIdRing) * 8 + half * rank + lane];
+          const uint32_t dst = sbase + P::kKOff + slot * P::kKSlot + lane * 2 * kBlockBytes;
+          if (issuer)
+            tma_load_4d(dst, &tm_k, 0, 0, 2 * it.kvh, 2 * id, bar, pol);
+          else
+            tma_load_4d_pair(dst, &tm_k, 0, 0, 2 * it.kvh, 2 * id, mapa_shared(bar, 0), pol);
+        }
+        __syncwarp();
+        ++jk;
+        ++total;
+      }
+      // every load's slot has been released, and so has landed, before exit
+      if (lane == 0) {
+        for (unsigned b = 0; b < 2 && b < qi; ++b)
+          wait(bar_q_empty + 8 * b, ((qi - 1 - b) >> 1) & 1, abort_flag, a);
+        for (unsigned sl = 0; sl < kNK && sl < total; ++sl)
+          wait(bar_k_empty + 8 * sl, ((total - 1 - sl) / kNK) & 1, abort_flag, a);
+      }
+      settle();
+    } else {
+      if (lane == 0) tma_prefetch_desc(&tm_v);
+      Item it;
+      it.nkt = 0;
+      int jf = 0, jv = 0;  // tiles of `it` with ids, and loaded
+      bool next_ids = false;
+      unsigned k = 0;           // items begun
+      unsigned full_phase = 0;  // bit s: parity of v_full[s]'s next use
+      int edge_slot = -1;       // slot of the edge tile whose rows are still to be zeroed
+      while (!a.stall_loads) {
+        if (edge_slot >= 0) {
+          if (!wait_warp(bar_v_full + 8 * edge_slot, (full_phase >> edge_slot) & 1, abort_flag, a))
+            break;
+          const uint32_t vt = sbase + P::kVOff + edge_slot * P::kVSlot;
+          const uint32_t blk = vt + ((it.nvb - 1) & 7) * kBlockBytes;
+#pragma unroll 1
+          for (int e = lane + 8 * it.hidden; e < 8 * kBlockSize; e += 32)
+            st_shared_zero16(blk + e * 16);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (!issuer)
+              mbar_arrive_remote_release(mapa_shared(bar_v_ready + 8 * edge_slot, 0));
+            else
+              mbar_arrive(bar_v_ready + 8 * edge_slot);
+          }
+          full_phase ^= 1u << edge_slot;
+          edge_slot = -1;
+        }
+        const bool more = jf < it.nkt && jv + kIdBatch / 2 >= jf;
+        bool fetch = more;
+        if (!more && !next_ids && jf >= it.nkt && it.nkt - jv <= kIdBatch) {
+          // the next item: waited for at the end of this one, taken before if it is there
+          const uint32_t bar = bar_item + 8 * (k % kItemRing), parity = (k / kItemRing) & 1;
+          if (jv == it.nkt) {
+            if (!wait_warp(bar, parity, abort_flag, a)) break;
+            fetch = true;
+          } else {
+            fetch = __all_sync(0xffffffffu, mbar_test_wait(bar, parity));
+          }
+        }
+        if (fetch) {
+          const Item* x = ring_item(more ? k - 1 : k);
+          if (x->nkt)
+            fetch_ids(a.block_tables + static_cast<int64_t>(x->row) * a.max_blocks + x->block0,
+                      a.num_blocks, a.err, ids_smem, x->nvb, more ? jf : 0,
+                      total - jv + (more ? 0 : it.nkt));
+          if (more)
+            jf += kIdBatch;
+          else
+            next_ids = true;
+        }
+        if (jv == it.nkt) {  // on to the next item
+          it = *ring_item(k++);
+          if (it.nkt == 0) break;
+          jf = kIdBatch;
+          jv = 0;
+          next_ids = false;
+        }
+        const unsigned slot = total % kNV;
+        if (total >= kNV &&
+            !wait_warp(bar_o_done + 8 * slot, ((total / kNV) - 1) & 1, abort_flag, a))
+          break;
+        const bool edge = jv == it.nkt - 1 && it.hidden < kBlockSize;
+        const bool remote = !issuer && !edge;
+        const uint32_t bar = edge ? bar_v_full + 8 * slot
+                                  : (remote ? mapa_shared(bar_v_ready + 8 * slot, 0)
+                                            : bar_v_ready + 8 * slot);
+        const int blocks = tile_blocks(it.nvb, jv);
+        if (lane == 0) {
+          if (remote)
+            mbar_arrive_expect_tx_remote(bar, blocks * kBlockBytes);
+          else
+            mbar_arrive_expect_tx(bar, blocks * kBlockBytes);
+        }
+        __syncwarp();
+        if (lane < blocks) {  // CTA r takes columns 64 r .. 64 r + 63 of every key
+          const int id = ids_smem[(total % kIdRing) * 8 + lane];
+          const uint32_t dst = sbase + P::kVOff + slot * P::kVSlot + lane * kBlockBytes;
+          const int x = it.kvh * 128 + rank * 64, y = id * kBlockSize;
+          if (remote)
+            tma_load_2d_pair(dst, &tm_v, x, y, bar, pol);
+          else
+            tma_load_2d(dst, &tm_v, x, y, bar, pol);
+        }
+        __syncwarp();
+        if (edge) edge_slot = slot;
+        ++jv;
+        ++total;
+      }
+      if (lane == 0)
+        for (unsigned sl = 0; sl < kNV && sl < total; ++sl)
+          wait(bar_o_done + 8 * sl, ((total - 1 - sl) / kNV) & 1, abort_flag, a);
+      settle();
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp || warp == kPvWarp) {
+    // ------------------------------------------------------------ tensor-core issue
+    // Two threads of the even CTA, as in pa_prefill_body.cuh.
+    if (lane == 0 && issuer) {
+      bool ok = true;
+      if (warp == kMmaWarp) {
+        const uint32_t idesc_s = instr_desc(0, 256) & ~(0x3fu << 17);  // (columns / 8 left out)
+        const uint64_t dk0 = smem_desc(sbase + P::kKOff, 16, kKGroupStride);
+        const uint64_t dq0 = smem_desc(sbase + P::kQOff, 16, 1024);
+        int s_buf = 0, s_round = 0, s_kslot = 0, s_kphase = 0;
+        for (unsigned k = 0; ok; ++k) {
+          ok = wait(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1, abort_flag, a);
+          const int nkt = ok ? ring_item(k)->nkt : 0;
+          if (nkt == 0) break;
+          const int nvb = ring_item(k)->nvb;
+          const uint64_t dq = dq0 + static_cast<uint64_t>(((k & 1) * 2 * kHalf) >> 4);
+          ok = wait(bar_q + 8 * (k & 1), (k >> 1) & 1, abort_flag, a);
+          int js = 0;
+          while (ok && js < nkt) {
+            const uint64_t dk = dk0 + static_cast<uint64_t>((s_kslot * P::kKSlot) >> 4);
+            const uint32_t dst = tmem + s_buf * 128;
+            // 32 columns for every two blocks
+            const uint32_t idesc = idesc_s | (((tile_blocks(nvb, js) + 1) / 2 * 4) << 17);
+            ok = wait(bar_k_full + 8 * s_kslot, s_kphase, abort_flag, a) &&
+                 (s_round == 0 || wait(bar_o_done + 8 * s_buf, (s_round + 1) & 1, abort_flag, a));
+            if (ok) {
+              tc_fence_after();
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                tc_mma_f16<2>(dst, dq + (((ks >> 2) * kHalf + (ks & 3) * 32) >> 4),
+                              dk + (((ks >> 2) * kKHalfOffset + (ks & 3) * 32) >> 4), idesc,
+                              ks > 0);
+              tc_commit_pair(bar_s_full + 8 * s_buf);
+              tc_commit_pair(bar_k_empty + 8 * s_kslot);
+              ++js;
+              if (++s_buf == kNS) {
+                s_buf = 0;
+                ++s_round;
+              }
+              if (++s_kslot == kNK) {
+                s_kslot = 0;
+                s_kphase ^= 1;
+              }
+            }
+          }
+          if (ok) tc_commit_pair(bar_q_empty + 8 * (k & 1));
+        }
+      } else {
+        const uint32_t idesc_o = instr_desc(1, 256);
+        const uint64_t dv0 = smem_desc(sbase + P::kVOff, kHalf, 1024);
+        int p_buf = 0, p_phase = 0, p_vslot = 0, p_vphase = 0;
+        for (unsigned k = 0; ok; ++k) {
+          ok = wait(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1, abort_flag, a);
+          const int nkt = ok ? ring_item(k)->nkt : 0;
+          if (nkt == 0) break;
+          const bool hides = ring_item(k)->hidden < kBlockSize;
+          const int nvb = ring_item(k)->nvb;
+          int jp = 0;
+          while (ok && jp < nkt) {
+            const uint64_t dv = dv0 + static_cast<uint64_t>((p_vslot * P::kVSlot) >> 4);
+            const uint32_t ta = tmem + p_buf * 128;
+            const int blocks = tile_blocks(nvb, jp);
+            const bool zeroed = hides && jp == nkt - 1;
+            ok = wait(bar_v_ready + 8 * p_vslot, p_vphase, abort_flag, a) &&
+                 wait(bar_p_full + 8 * p_buf, p_phase, abort_flag, a);
+            if (ok) {
+              if (zeroed) fence_acq_rel_cluster();  // the peer's zeroed rows
+              tc_fence_after();
+              if (blocks == 8) {
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                  tc_mma_f16_tmem_a<2>(tmem + kTmemO, ta + (ks >> 2) * 64 + (ks & 3) * 8,
+                                       dv + ((ks * kBlockBytes) >> 4), idesc_o,
+                                       (jp > 0 || ks > 0) ? 1u : 0u);
+              } else {
+#pragma unroll 1
+                for (int ks = 0; ks < blocks; ++ks)
+                  tc_mma_f16_tmem_a<2>(tmem + kTmemO, ta + (ks >> 2) * 64 + (ks & 3) * 8,
+                                       dv + ((ks * kBlockBytes) >> 4), idesc_o,
+                                       (jp > 0 || ks > 0) ? 1u : 0u);
+              }
+              tc_commit_pair(bar_o_done + 8 * p_buf);
+              ++jp;
+              if (++p_buf == kNS) {
+                p_buf = 0;
+                p_phase ^= 1;
+              }
+              if (++p_vslot == kNV) {
+                p_vslot = 0;
+                p_vphase ^= 1;
+              }
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax warps
+    const int qd = warp & 3, hc = warp >> 2;
+    const int r = qd * 32 + lane;  // query row = tensor-memory lane
+    const uint32_t lane_off = static_cast<uint32_t>(qd * 32) << 16;
+    const float sl = a.scale_log2;
+    const float sl_pow2 = __uint_as_float(__float_as_uint(sl) & 0x7f800000u);  // in (sl / 2, sl]
+    const float floor_score = sl > 1.f ? kFloor / sl : kFloor, floor2 = floor_score * sl;
+    const float floor_n = fabsf(floor2) >= kFarScore ? floor_score * sl_pow2 : floor2;
+    const uint32_t ocol = tmem + lane_off + kTmemO + hc * 64;
+    uint32_t v[64];
+    int jt = 0;                // tiles, over all items
+    int b3 = 0, s_phase = 0;   // score buffer of tile jt and its parity
+
+    // The results of an item, written once its last PV is done: O undivided, maximum and
+    // sum.  The next item's first PV, which overwrites O, waits for this
+    // warp's arrival on p_full behind these loads of O.  The barrier in it also
+    // hands over the key tiles of the item after the one at hand (go_flag 0 ..
+    // 7; -1: not published yet).
+    const int tok = r / G;
+    bool pending = false;
+    int64_t out_row = 0;            // of the pending item: this lane's row of the results,
+    bool out_here = false;          // and whether a member has it
+    float out_m = 0.f, out_l = 0.f;
+    uint32_t out_bar = 0, out_phase = 0;  // PV of its last tile
+    auto write_out = [&](unsigned k) {
+      volatile int* go = go_flag + (k & 1) * 4 + qd;
+      if (hc == 0 && lane == 0)
+        *go = mbar_test_wait(bar_item + 8 * (k % kItemRing), (k / kItemRing) & 1)
+                  ? ring_item(k)->nkt
+                  : -1;
+      wait_warp(out_bar, out_phase, abort_flag, a);
+      tc_fence_after();
+      red_sum[hc * 128 + r] = out_l;
+      named_barrier(1 + qd, 64);
+      const float l_tot = out_l + red_sum[(hc ^ 1) * 128 + r];
+      const bool sound = !warp_flag(abort_flag);  // (asked by the whole warp)
+      const bool good = sound && out_here;
+      float* const to = a.lay.part_o + out_row * 128 + hc * 64;
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t (&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
+        tmem_ld32(ocol + 32 * c, w);
+        if (good) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) stg32(to + 32 * c + 8 * q, &w[8 * q]);
+        }
+        __syncwarp();
+      }
+      if (good && hc == 0) a.lay.part_ml[out_row] = make_float2(out_m, l_tot);
+      __syncwarp();
+      return *go;
+    };
+
+    // Both warps of a quadrant act on what the first one found of the next
+    // item: they meet at a named barrier for every tile, also after a timeout
+    // (when the waits are skipped and what they compute is not stored).
+    int nkt = -1;
+    for (unsigned k = 0;; ++k) {
+      const uint32_t item_bar = bar_item + 8 * (k % kItemRing);
+      if (nkt < 0) {
+        volatile int* go = go_flag + 8 + (k & 1) * 4 + qd;
+        if (hc == 0) {
+          const bool got = wait_warp(item_bar, (k / kItemRing) & 1, abort_flag, a);
+          if (lane == 0) *go = got ? ring_item(k)->nkt : 0;
+        }
+        named_barrier(1 + qd, 64);
+        nkt = *go;
+      }
+      const bool last = nkt == 0;  // the list's end: the pending output only
+      if (last && !pending) break;
+      int next_nkt = -1;
+      const Item& it = *ring_item(k);
+      const int mine = rank * tpt + tok;  // member of the unit
+      const bool here = !last && tok < tpt && mine < it.tokens;
+      const bool active = __any_sync(0xffffffffu, here);
+      // last key of the piece that the row sees
+      int hi = -1;
+      if (here)
+        hi = min(__ldcg(a.seq_lens + it.q0 + mine), it.keys) - 1 - it.block0 * kBlockSize;
+      const int64_t row =
+          static_cast<int64_t>(it.slot) * a.lay.slot_rows + rank * tpt * G + r;
+      // reference maximum: a score, in log2 units, and as the softmax subtracts it
+      float m_run = floor_score, m_run2 = floor2, n_run = floor_n;
+      float l_run = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < nkt || last; ++j) {
+        const bool first = j == 0;
+        if (!last) wait_warp(bar_s_full + 8 * b3, s_phase, abort_flag, a);
+        if (active) {
+          const int b = jt & 1;
+          tc_fence_after();
+          const int kb = j * kTileKeys + hc * 64;
+          const bool whole = hi >= kb + 63;
+          float mloc;
+          const uint32_t sc = tmem + lane_off + b3 * 128 + hc * 64;
+          if (!__all_sync(0xffffffffu, whole)) {
+            // hidden scores, whatever they hold, become -inf in tensor memory
+            const uint64_t seen = low_bits(hi - kb + 1);
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t m = static_cast<uint32_t>(seen >> (32 * c));
+              if (__all_sync(0xffffffffu, m == 0xffffffffu)) continue;
+              uint32_t (&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
+              tmem_ld32(sc + 32 * c, w);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) w[i] = ((m >> i) & 1u) ? w[i] : 0xff800000u;
+              tmem_st32(sc + 32 * c, w);
+            }
+          }
+          tmem_ld64_max(sc, v, mloc);
+          red_max[(b * 2 + hc) * 128 + r] = mloc;
+          named_barrier(1 + qd, 64);
+          // (scale > 0 keeps the order of scores)
+          const float m_new = fmaxf(m_run, fmaxf(mloc, red_max[(b * 2 + (hc ^ 1)) * 128 + r]));
+          const float m_new2 = m_new * sl;
+          const bool move = m_new2 > m_run2 + kRescaleThreshold;
+          const float alpha = move ? fast_exp2(m_run2 - m_new2) : 1.f;
+          // x = s sl - m sl by one fused multiply-add, whose product is exact and so
+          // differs from m_run2, which is rounded, by up to half a step of it: a
+          // common factor of a row's weights, within 2^64 below kFarScore.  From there
+          // on the factor leaves fp32, and neighbouring scores are 2^7 apart: any
+          // multiplier near sl tells them apart, and a power of two is exact.  (m_new2
+          // is far where m_run2 is: they differ by less than that step, or it moves.)
+          const bool far = fabsf(m_new2) >= kFarScore;
+          const float slx = far ? sl_pow2 : sl, n_new = far ? m_new * sl_pow2 : m_new2;
+          m_run = move ? m_new : m_run;
+          m_run2 = move ? m_new2 : m_run2;
+          n_run = move ? n_new : n_run;
+          uint64_t rsp[2] = {0, 0};
+          uint32_t pk[32];
+          const uint64_t sl2 = f32x2(slx, slx), nm2 = f32x2(-n_run, -n_run);
+#pragma unroll
+          for (int i = 0; i < 64; i += 2) {
+            // -inf (hidden) gives exactly 0: n_run is finite
+            const uint64_t s2 = f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            const float2 x = f32x2_parts(fma2(s2, sl2, nm2));
+            const float e0 = fast_exp2(x.x), e1 = fast_exp2(x.y);
+            rsp[(i >> 1) & 1] = add2(rsp[(i >> 1) & 1], f32x2(e0, e1));
+            pk[i / 2] = pack_bf16x2(e0, e1);
+          }
+          const float2 rs = f32x2_parts(add2(rsp[0], rsp[1]));
+          l_run = l_run * alpha + (rs.x + rs.y);
+          // O is rescaled only when a row maximum moved; PV of the previous
+          // tile must have landed first (tile 0's PV overwrites O)
+          if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+            const int pb = b3 == 0 ? kNS - 1 : b3 - 1;
+            wait_warp(bar_o_done + 8 * pb, b3 == 0 ? s_phase ^ 1 : s_phase, abort_flag, a);
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < 2; ++cc) {
+              uint32_t (&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
+              tmem_ld32(ocol + 32 * cc, w);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+              tmem_st32(ocol + 32 * cc, w);
+            }
+          }
+          tmem_st32(sc, pk);
+        }
+        if (first && pending) next_nkt = write_out(k + 1);
+        if (last) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (!issuer)
+            mbar_arrive_remote(mapa_shared(bar_p_full + 8 * b3, 0));
+          else
+            mbar_arrive(bar_p_full + 8 * b3);
+        }
+        if (++b3 == kNS) {
+          b3 = 0;
+          s_phase ^= 1;
+        }
+        ++jt;
+      }
+      if (last) break;
+      out_bar = bar_o_done + 8 * (b3 == 0 ? kNS - 1 : b3 - 1);
+      out_phase = b3 == 0 ? s_phase ^ 1 : s_phase;
+      pending = active;
+      out_row = row;
+      out_here = here;
+      out_m = m_run2;
+      out_l = l_run;
+      nkt = next_nkt;
+    }
+  }
+  tc_fence_before();
+  // Neither CTA leaves while the other may still report to it.  No data changes
+  // hands here, so outputs need not have landed: a release would wait for them
+  // (0.6 us).
+  cluster_sync_relaxed();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc<2>(tmem, kTmemCols);
+}
+
+}  // namespace
+}  // namespace pre
+
+using namespace pre;
+
+cudaError_t launch_shared_prefix(const SharedArgs& args, const CUtensorMap* tm_q,
+                                 const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                                 cudaStream_t stream) {
+  SharedArgs a = args;
+  if (a.wait_ns == 0) a.wait_ns = kWaitLimitNs;
+  constexpr int smem = SPlan::kSmemBytes + 1024;
+  static std::mutex mu;
+  static bool set_for[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!set_for[dev]) {
+      e = cudaFuncSetAttribute(shared_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               smem);
+      if (e != cudaSuccess) return e;
+      set_for[dev] = true;
+    }
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(a.lay.teams * a.lay.team_pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  e = cudaLaunchKernelEx(&cfg, shared_prefix_kernel, *tm_q, *tm_k, *tm_v, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace pa

@@ -45,6 +45,11 @@
 //
 // A prefill call of few query tokens comes here too, a token as a sequence of
 // its own that ends with it, and finds its chunk with one more round trip.
+//
+// So does the decode of sequences that share prefixes, for what is each one's own:
+// the blocks behind its group's prefix, joined at the end with the results that
+// pa_shared_prefix.cu left for the prefix.  Its CTAs may start before that kernel is
+// done (which waits for all work before it), and wait for it where they join.
 #include <float.h>
 #include <math.h>
 
@@ -52,7 +57,7 @@
 #include <mutex>
 
 #include "../../include/pa.h"
-#include "pa_window.h"
+#include "pa_shared.h"
 #include "pa_window_ptx.cuh"
 
 namespace pa {
@@ -113,9 +118,47 @@ __device__ __forceinline__ int find_chunk(const WindowDecodeArgs& a, int s, int 
   return -1;
 }
 
-// C: the queries are those of chunks (see WindowDecodeArgs).
-template <int D, int W, bool C>
-__global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecodeArgs a) {
+// What the queries are: a sequence's last token each, those of chunks (see
+// WindowDecodeArgs), or a sequence's last token behind a shared prefix.
+enum DecodeKind : int { kSequences = 0, kChunks = 1, kShared = 2 };
+
+template <int M>
+struct KindArgs {
+  using type = WindowDecodeArgs;
+};
+template <>
+struct KindArgs<kShared> {
+  using type = SharedDecodeArgs;
+};
+
+// The group of sequence s (-1: none), its first member and its prefix's blocks.  Called
+// by a whole warp.
+__device__ __forceinline__ int find_group(const SharedArgs& a, int s, int lane, int& first,
+                                          int& blocks) {
+  // offsets rise: 32 of them at a time narrow the range [lo, hi) whose group holds s
+  first = blocks = 0;
+  if (a.num_groups == 0) return -1;
+  int lo = 0, hi = a.num_groups;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const bool below = at < hi && __ldcg(a.group_offsets + at) <= s;
+    // (at least the first one: sequences before every group have none, seen below)
+    const int n = max(__popc(__ballot_sync(0xffffffffu, below)), 1);
+    const int next = lo + (n - 1) * step;
+    hi = min(hi, next + step);
+    lo = next;
+  }
+  const SharedGroup g = shared_group(a, lo);
+  first = g.first;
+  blocks = g.blocks;
+  return s >= g.first && s < g.first + g.members ? lo : -1;
+}
+
+template <int D, int W, int M>
+__global__ void __launch_bounds__(32 * W)
+    decode_window_kernel(const typename KindArgs<M>::type a) {
+  constexpr bool C = M == kChunks;
   using P = DecodePlan<D, W>;
   constexpr int KJ = D / 32;  // 16-byte pieces of a K row per lane
   constexpr int VH = D / 64;  // 16-byte pieces of a V row per lane
@@ -138,7 +181,7 @@ __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecod
   const int G = a.group;
 
   griddep_launch_dependents();
-  griddep_wait();
+  if constexpr (M != kShared) griddep_wait();
 
   // q: head g of the group, the columns of this lane's K pieces
   uint4 qf[KJ];
@@ -146,7 +189,8 @@ __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecod
       a.q + (static_cast<int64_t>(s) * a.num_q_heads + kvh * G + (g < G ? g : 0)) * D;
 #pragma unroll
   for (int j = 0; j < KJ; ++j) {
-    qf[j] = *reinterpret_cast<const uint4*>(qrow + 8 * (4 * j + t));
+    const uint4* const at = reinterpret_cast<const uint4*>(qrow + 8 * (4 * j + t));
+    qf[j] = M == kShared ? __ldcg(at) : *at;
     if (g >= G) qf[j] = make_uint4(0, 0, 0, 0);
   }
 
@@ -160,15 +204,22 @@ __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecod
     table_row = find_chunk(a, s, lane, n);
     if (table_row < 0) return;  // (every CTA of the cluster) a row of no chunk stays
   } else {
-    n = a.seq_lens[s];
+    n = M == kShared ? __ldcg(a.seq_lens + s) : a.seq_lens[s];
     const int cap = a.max_blocks * kBlockSize;
     if (n < 0 || n > cap) {
       if (threadIdx.x == 0 && rank == 0 && kvh == 0) atomicOr(a.err, PA_DEVERR_SEQ_LEN);
       n = n < 0 ? 0 : cap;
     }
   }
-  const int lo = n > a.window ? n - a.window : 0;  // first key of the window
-  const int ns = a.sinks < n ? a.sinks : n;        // visible sinks
+  int lo = n > a.window ? n - a.window : 0;        // first key of the window
+  int ns = a.sinks < n ? a.sinks : n;              // visible sinks
+  int group = -1, group_first = 0;
+  if constexpr (M == kShared) {
+    int blocks;
+    group = find_group(a.shared, s, lane, group_first, blocks);
+    lo = group >= 0 ? blocks * kBlockSize : 0;     // first key of the sequence's own
+    ns = 0;
+  }
   const int nsb = (ns + kBlockSize - 1) / kBlockSize;
   const int b_first = max(lo / kBlockSize, nsb);   // first block behind the sinks'
   const int nb = (n + kBlockSize - 1) / kBlockSize;
@@ -197,7 +248,7 @@ __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecod
     const int mine = vb + lane * stride;
     ids = 0;
     if (mine < nv) {
-      ids = table[real_block(mine)];
+      ids = M == kShared ? __ldcg(table + real_block(mine)) : table[real_block(mine)];
       if (ids < 0 || ids >= a.num_blocks) {
         atomicOr(a.err, PA_DEVERR_BLOCK_ID);
         ids = -1;  // reads as zeros
@@ -359,6 +410,55 @@ __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecod
       dst[0] = make_float2(o[4 * h + i][0], o[4 * h + i][2]);
       dst[D / 2] = make_float2(o[4 * h + i][1], o[4 * h + i][3]);
     }
+  // The prefix's results for this sequence: those of its slots, `span` rows apart, from
+  // `part0` on.
+  int parts = 0;
+  int64_t part0 = 0, span = 0;
+  if constexpr (M == kShared) {
+    griddep_wait();
+    const SharedLayout& lay = a.shared.lay;
+    if (group >= 0) {
+      const int4 info = __ldcg(lay.info + group);
+      const int tiles = __ldcg(lay.info + a.shared.num_groups).y;
+      if (info.z > 0) {
+        const int rows = 2 * lay.tile_tokens;
+        const int at = s - group_first, u = at / rows;
+        const int t0 = info.y + u * info.z;
+        const int teams = shared_teams(lay, tiles);
+        const int j0 = shared_team(t0, tiles, teams);
+        parts = shared_team(t0 + info.z - 1, tiles, teams) - j0 + 1;
+        span = static_cast<int64_t>(a.num_kv_heads) * lay.slot_rows;
+        part0 = (static_cast<int64_t>(j0 + info.x + u) * a.num_kv_heads + kvh) * lay.slot_rows +
+                (at - u * rows) * G;
+      }
+    }
+  }
+  // An output element, of head h: the softmax's maximum, sum and weighted values over
+  // the sequence's own keys, joined with those over its prefix.
+  auto emit = [&](int h, int d, float m, float l, float acc) {
+    if constexpr (M == kShared) {
+      if (parts > 0) {
+        const float2* const ml = a.shared.lay.part_ml + part0 + h;
+        const float* const o = a.shared.lay.part_o + (part0 + h) * D + d;
+        float top = m;
+        for (int p = 0; p < parts; ++p) top = fmaxf(top, __ldcg(ml + p * span).x);
+        const float own = fast_exp2(m - top);
+        acc *= own;
+        l *= own;
+#pragma unroll 4
+        for (int p = 0; p < parts; ++p) {
+          const float2 x = __ldcg(ml + p * span);
+          const float f = fast_exp2(x.x - top);
+          acc += f * __ldcg(o + p * span * D);
+          l += f * x.y;
+        }
+        m = top;
+      }
+    }
+    const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + kvh * G + h;
+    a.out[row * D + d] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
+    if (d == 0 && a.out_lse) a.out_lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  };
   __syncthreads();
   for (int e = threadIdx.x; e < G * D; e += 32 * W) {
     const int h = e / D, d = e % D;
@@ -373,9 +473,7 @@ __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecod
       l += f * sm_l[w * 8 + h];
     }
     if (splits == 1) {
-      const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + kvh * G + h;
-      a.out[row * D + d] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
-      if (d == 0 && a.out_lse) a.out_lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      emit(h, d, m, l, acc);
     } else {
       cta_o[e] = acc;
       if (d == 0) {
@@ -399,15 +497,13 @@ __global__ void __launch_bounds__(32 * W) decode_window_kernel(const WindowDecod
       acc += f * ld_dsmem(mapa_shared(ro + 4 * e, c));
       l += f * ld_dsmem(mapa_shared(rl + 4 * h, c));
     }
-    const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + kvh * G + h;
-    a.out[row * D + d] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
-    if (d == 0 && a.out_lse) a.out_lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    emit(h, d, m, l, acc);
   }
   cluster_sync();  // no CTA leaves while another may still read its shared memory
 }
 
-template <int D, int W, bool C = false>
-cudaError_t launch(const WindowDecodeArgs& a, cudaStream_t stream) {
+template <int D, int W, int M>
+cudaError_t launch(const typename KindArgs<M>::type& a, cudaStream_t stream) {
   {  // raise the kernel's shared-memory limit once per device
     static std::mutex mu;
     static bool set_for[64] = {};
@@ -417,7 +513,7 @@ cudaError_t launch(const WindowDecodeArgs& a, cudaStream_t stream) {
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!set_for[dev]) {
-      e = cudaFuncSetAttribute(decode_window_kernel<D, W, C>,
+      e = cudaFuncSetAttribute(decode_window_kernel<D, W, M>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                DecodePlan<D, W>::kBytes);
       if (e != cudaSuccess) return e;
@@ -439,7 +535,7 @@ cudaError_t launch(const WindowDecodeArgs& a, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = a.splits > 1 ? 2 : 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_window_kernel<D, W, C>, a);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_window_kernel<D, W, M>, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -452,7 +548,7 @@ struct Residency {
 };
 static_assert(kMaxWindowSplit == 1 << 4, "cluster sizes");
 
-template <int D, bool C>
+template <int D, int M>
 cudaError_t residency(int num_sms, Residency* out) {
   static std::mutex mu;
   static Residency by_device[64];
@@ -464,7 +560,7 @@ cudaError_t residency(int num_sms, Residency* out) {
   Residency& r = by_device[dev];
   if (!r.ready) {
     constexpr int smem = DecodePlan<D, 8>::kBytes;
-    const auto kernel = decode_window_kernel<D, 8, C>;
+    const auto kernel = decode_window_kernel<D, 8, M>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     int ctas = 0;
@@ -497,10 +593,10 @@ cudaError_t residency(int num_sms, Residency* out) {
   return cudaSuccess;
 }
 
-template <int D, bool C = false>
+template <int D, int M>
 cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
   Residency res;
-  const cudaError_t e = residency<D, C>(num_sms, &res);
+  const cudaError_t e = residency<D, M>(num_sms, &res);
   if (e != cudaSuccess) return e;
   // Blocks that a sequence can attend at most.
   const int64_t visible = std::min<int64_t>(
@@ -517,9 +613,9 @@ cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
     if (visible > 24)
       for (int k = 1; k < 5; ++k)
         if (units <= res.clusters[k] && (8 << k) <= visible) a.splits = 1 << k;
-    return launch<D, 8, C>(a, stream);
+    return launch<D, 8, M>(a, stream);
   }
-  if constexpr (C) return launch<D, 4, C>(a, stream);
+  if constexpr (M == kChunks) return launch<D, 4, M>(a, stream);
   // Many units: few warps on each keep more units at once and hide what a unit
   // costs before its first block arrives; many warps spread units of different
   // lengths.  The number with the least estimated time (us; fewer only where that
@@ -548,10 +644,10 @@ cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
     }
   }
   switch (w) {
-    case 1: return launch<D, 1>(a, stream);
-    case 2: return launch<D, 2>(a, stream);
-    case 4: return launch<D, 4>(a, stream);
-    default: return launch<D, 8>(a, stream);
+    case 1: return launch<D, 1, M>(a, stream);
+    case 2: return launch<D, 2, M>(a, stream);
+    case 4: return launch<D, 4, M>(a, stream);
+    default: return launch<D, 8, M>(a, stream);
   }
 }
 
@@ -559,12 +655,23 @@ cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
 
 cudaError_t launch_decode_window_chunks(const WindowDecodeArgs& a, int num_sms,
                                         cudaStream_t stream) {
-  return choose<128, true>(a, num_sms, stream);
+  return choose<128, kChunks>(a, num_sms, stream);
 }
 
 cudaError_t launch_decode_window(const WindowDecodeArgs& a, int head_dim, int num_sms,
                                  cudaStream_t stream) {
-  return head_dim == 128 ? choose<128>(a, num_sms, stream) : choose<64>(a, num_sms, stream);
+  return head_dim == 128 ? choose<128, kSequences>(a, num_sms, stream)
+                         : choose<64, kSequences>(a, num_sms, stream);
+}
+
+cudaError_t launch_shared_decode(const SharedDecodeArgs& args, int num_sms, cudaStream_t stream) {
+  SharedDecodeArgs a = args;
+  a.splits = 1;
+  const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
+  // How long a sequence's own part is, the host does not know: eight warps on each where
+  // all units run at once, four where they come in rounds.
+  if (units <= num_sms) return launch<128, 8, kShared>(a, stream);
+  return launch<128, 4, kShared>(a, stream);
 }
 
 }  // namespace pa
