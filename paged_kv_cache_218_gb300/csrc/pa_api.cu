@@ -1567,7 +1567,7 @@ int pa_test_prefill_window_stalled(void* out, const void* q, const void* k_cache
 // Slots, teams and workspace of a shared-prefix decode.
 struct SharedPlan {
   SharedLayout lay;
-  size_t ml_off, info_off, bytes;
+  size_t ml_off, info_off, member_off, bytes;
   bool fits;
 };
 
@@ -1588,7 +1588,8 @@ static SharedPlan shared_plan(int num_seqs, int num_groups, int max_group_size, 
   p.fits = units < (1 << 24) && out_rows < (int64_t{1} << 40);
   p.ml_off = round256(static_cast<size_t>(out_rows) * 128 * sizeof(float));
   p.info_off = p.ml_off + round256(static_cast<size_t>(out_rows) * sizeof(float2));
-  p.bytes = p.info_off + round256((static_cast<size_t>(num_groups) + 1) * sizeof(int4));
+  p.member_off = p.info_off + round256((static_cast<size_t>(num_groups) + 1) * sizeof(int4));
+  p.bytes = p.member_off + round256(static_cast<size_t>(num_seqs) * sizeof(int4));
   return p;
 }
 
@@ -1678,6 +1679,7 @@ static int decode_shared_impl(void* out, const void* q, const void* k_cache, con
   x.lay.part_o = reinterpret_cast<float*>(ws);
   x.lay.part_ml = reinterpret_cast<float2*>(ws + p.ml_off);
   x.lay.info = reinterpret_cast<int4*>(ws + p.info_off);
+  x.lay.member = reinterpret_cast<int4*>(ws + p.member_off);
   CUtensorMap tm_q, tm_k, tm_v;
   if (encode_q_map(&tm_q, q, num_seqs, num_q_heads, head_dim, group, p.lay.tile_tokens) ||
       encode_pool_map(&tm_k, k_cache, num_blocks, num_kv_heads, head_dim, kPoolKeyTile) ||

@@ -23,6 +23,9 @@ struct SharedLayout {
   // [num_groups + 1]: a group's first unit, its first key tile, key tiles of each of its
   // units, first member; last entry: .y all key tiles.  Written by the prefix pass.
   int4* info;
+  // [num_seqs]: a sequence's group (-1: none), its number in it, its prefix's blocks.
+  // Written by the prefix pass.
+  int4* member;
 };
 
 struct SharedArgs {
@@ -59,6 +62,27 @@ __device__ __forceinline__ SharedGroup shared_group(const SharedArgs& a, int g) 
   x.blocks = min(max(b, 0), a.max_blocks);
   x.sound = f == x.first && e == f + x.members && b == x.blocks;
   return x;
+}
+
+// The group of sequence s (-1: none), s's number in it, its prefix's blocks.  Called by a
+// whole warp.
+__device__ __forceinline__ int4 find_group(const SharedArgs& a, int s, int lane) {
+  if (a.num_groups == 0) return make_int4(-1, 0, 0, 0);
+  // offsets rise: 32 of them at a time narrow the range [lo, hi) whose group holds s
+  int lo = 0, hi = a.num_groups;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + lane * step;
+    const bool below = at < hi && __ldcg(a.group_offsets + at) <= s;
+    // (at least the first one: sequences before every group have none, seen below)
+    const int n = max(__popc(__ballot_sync(0xffffffffu, below)), 1);
+    const int next = lo + (n - 1) * step;
+    hi = min(hi, next + step);
+    lo = next;
+  }
+  const SharedGroup g = shared_group(a, lo);
+  if (s < g.first || s >= g.first + g.members) return make_int4(-1, 0, 0, 0);
+  return make_int4(lo, s - g.first, g.blocks, 0);
 }
 
 // Teams that take part: none has an empty range.

@@ -21,6 +21,8 @@
 // What bounds it: with up to 256 rows a kv head, HBM: a pair takes 0.75 us for a tile's
 // 64 KB, which is both its share of the memory's rate and what its two products and
 // their hand-overs take; with more rows, the tensor pipe.
+#include <limits.h>
+
 #include <mutex>
 
 #include "pa_prefill_body.cuh"
@@ -37,10 +39,10 @@ constexpr uint64_t kSettleNs = 1000000;  // far longer than any copy takes
 constexpr float kFloor = -0x1.fffff0p127f;
 constexpr float kFarScore = 0x1p31f;  // (log2 units)
 
-// Shared memory of one CTA of a pair: two Q tiles, four K and three V half
+// Shared memory of one CTA of a pair: two Q tiles, four K and five V half
 // tiles, block ids of both loaders, the softmax's exchange, barriers.
 struct SPlan {
-  static constexpr int kNK = 4, kNV = 3;
+  static constexpr int kNK = 4, kNV = 5;
   static constexpr int kKSlot = kHalf, kVSlot = kHalf;
   static constexpr int kQOff = 0;  // [2][2 * kHalf]
   static constexpr int kKOff = kQOff + 4 * kHalf;
@@ -49,7 +51,7 @@ struct SPlan {
   static constexpr int kRedOff = kIdsOff + 2 * kIdRing * 8 * 4;
   static constexpr int kRedOff2 = kRedOff + 2 * 2 * 128 * 4;
   static constexpr int kBarOff = kRedOff2 + 2 * 128 * 4;
-  static constexpr int kItemsOff = kBarOff + 448;  // [kItemRing]
+  static constexpr int kItemsOff = kBarOff + 512;  // [kItemRing]
   static constexpr int kSmemBytes = kItemsOff + 8 * 64;
 };
 static_assert(SPlan::kSmemBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
@@ -65,6 +67,7 @@ struct Item {
   int keys;        // keys [0, keys) of the sequence are the prefix
   int hidden;      // rows of the last block from this one on are seen by no member; or 16
   int slot;        // of the results
+  int whole;       // every member sees the whole prefix
 };
 // Blocks of an item's key tile j: eight, fewer in the last one.
 __device__ __forceinline__ int tile_blocks(int nvb, int j) { return min(8, nvb - 8 * j); }
@@ -114,22 +117,23 @@ struct Groups {
 // Walks a pair's pieces.
 struct Cursor {
   int pos, end;      // key tiles of the team's range that are left
-  int group0;        // groups looked at, 32 at a time,
+  int group0;        // groups at hand, 32 at a time,
   int units, tiles;  // and units and key tiles before them
   int team, kvh;
 };
 
-// The next item (nkt 0 at the end of the list).  Called by a whole warp.
-__device__ __forceinline__ Item next_item(const SharedArgs& a, Cursor& cur, int lane) {
+// The next item (nkt 0 at the end of the list); x: the groups at hand.  Called by a
+// whole warp.
+__device__ __forceinline__ Item next_item(const SharedArgs& a, Cursor& cur, Groups& x, int lane) {
   Item it;
   it.nkt = 0;
   while (cur.pos < cur.end && cur.group0 < a.num_groups) {
-    const Groups x(a, cur.group0, cur.units, lane);
     const unsigned past = __ballot_sync(0xffffffffu, cur.tiles + x.tiles_sum > cur.pos);
     if (past == 0) {
       cur.units += __shfl_sync(0xffffffffu, x.units_sum, 31);
       cur.tiles += __shfl_sync(0xffffffffu, x.tiles_sum, 31);
       cur.group0 += 32;
+      x = Groups(a, cur.group0, cur.units, lane);
       continue;
     }
     const int w = __ffs(past) - 1;
@@ -150,10 +154,15 @@ __device__ __forceinline__ Item next_item(const SharedArgs& a, Cursor& cur, int 
     it.block0 = 8 * tile0;
     it.slot = (cur.team + unit0 + u) * a.num_kv_heads + cur.kvh;
     it.keys = blocks * kBlockSize;
-    // the last key that some member sees
-    int seen = 0;
-    for (int i = lane; i < it.tokens; i += 32) seen = max(seen, __ldcg(a.seq_lens + it.q0 + i));
+    // the last key that some member sees, and whether all see the last one
+    int seen = 0, least = INT_MAX;
+    for (int i = lane; i < it.tokens; i += 32) {
+      const int n = __ldcg(a.seq_lens + it.q0 + i);
+      seen = max(seen, n);
+      least = min(least, n);
+    }
     seen = min(__reduce_max_sync(0xffffffffu, seen), it.keys);
+    it.whole = __reduce_min_sync(0xffffffffu, least) >= it.keys;
     // (one block at least, so that there are scores)
     const int left = ((seen + 15) >> 4) - it.block0;
     it.nvb = min(max(left, 1), min(8 * n, blocks - it.block0));
@@ -248,13 +257,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t bar_v_ready = bar_v_full + 8 * kNV;   // [kNV]: V of the pair ready
   const uint32_t bar_s_full = bar_v_ready + 8 * kNV;   // [kNS]: scores of a tile
   const uint32_t bar_p_full = bar_s_full + 8 * kNS;    // [kNS]: softmax done
-  const uint32_t bar_o_done = bar_p_full + 8 * kNS;    // [kNS]: PV done, and so V slot free
+  const uint32_t bar_o_done = bar_p_full + 8 * kNS;    // [kNS]: PV done
   const uint32_t bar_item = bar_o_done + 8 * kNS;      // [kItemRing]: item published
-  static_assert(32 + 8 * (2 * kNK + 2 * kNV + 3 * kNS + kItemRing) <= 336, "barrier area");
-  static_assert(kNV == kNS, "V slot of a tile = its score buffer");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P::kBarOff + 336);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 340);
-  volatile int* go_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 352);
+  const uint32_t bar_v_empty = bar_item + 8 * kItemRing;  // [kNV]: PV done, slot free
+  static_assert(32 + 8 * (2 * kNK + 3 * kNV + 3 * kNS + kItemRing) <= 384, "barrier area");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P::kBarOff + 384);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 388);
+  volatile int* go_flag = reinterpret_cast<volatile int*>(smem + P::kBarOff + 400);
   auto ring_item = [&](unsigned k) {
     return reinterpret_cast<Item*>(smem + P::kItemsOff + 64 * (k % kItemRing));
   };
@@ -280,6 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k < kNV; ++k) {
       mbar_init(bar_v_full + 8 * k, 1);
       mbar_init(bar_v_ready + 8 * k, 2);
+      mbar_init(bar_v_empty + 8 * k, 1);
     }
     for (int k = 0; k < kNS; ++k) {
       mbar_init(bar_s_full + 8 * k, 1);
@@ -318,8 +328,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // all key tiles, and where each group's begin (the first pair writes it down)
       int units = 0, tiles = 0;
+      const Groups head(a, 0, 0, lane);
       for (int g0 = 0; g0 < a.num_groups; g0 += 32) {
-        const Groups x(a, g0, units, lane);
+        const Groups x = g0 == 0 ? head : Groups(a, g0, units, lane);
         if (blockIdx.x == 0 && g0 + lane < a.num_groups) {
           a.lay.info[g0 + lane] =
               make_int4(units + x.units_sum - x.units, tiles + x.tiles_sum - x.tiles,
@@ -337,11 +348,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int to =
           team < teams ? static_cast<int>(static_cast<int64_t>(tiles) * (team + 1) / teams) : 0;
       Cursor cur{from, to, 0, 0, 0, team, pair - team * a.lay.team_pairs};
+      Groups at_hand = head;
       unsigned published = 0;
       auto publish = [&]() {
-        if (cur.pos == cur.end && cur.kvh + a.lay.team_pairs < a.num_kv_heads)
+        if (cur.pos == cur.end && cur.kvh + a.lay.team_pairs < a.num_kv_heads) {
           cur = Cursor{from, to, 0, 0, 0, team, cur.kvh + a.lay.team_pairs};
-        const Item x = next_item(a, cur, lane);
+          if (a.num_groups > 32) at_hand = Groups(a, 0, 0, lane);
+        }
+        const Item x = next_item(a, cur, at_hand, lane);
         if (lane == 0) {
           *ring_item(published) = x;
           mbar_arrive(bar_item + 8 * (published % kItemRing));
@@ -490,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const unsigned slot = total % kNV;
         if (total >= kNV &&
-            !wait_warp(bar_o_done + 8 * slot, ((total / kNV) - 1) & 1, abort_flag, a))
+            !wait_warp(bar_v_empty + 8 * slot, ((total / kNV) - 1) & 1, abort_flag, a))
           break;
         const bool edge = jv == it.nkt - 1 && it.hidden < kBlockSize;
         const bool remote = !issuer && !edge;
@@ -521,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (lane == 0)
         for (unsigned sl = 0; sl < kNV && sl < total; ++sl)
-          wait(bar_o_done + 8 * sl, ((total - 1 - sl) / kNV) & 1, abort_flag, a);
+          wait(bar_v_empty + 8 * sl, ((total - 1 - sl) / kNV) & 1, abort_flag, a);
       settle();
     }
     __syncwarp();
@@ -607,6 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                        (jp > 0 || ks > 0) ? 1u : 0u);
               }
               tc_commit_pair(bar_o_done + 8 * p_buf);
+              tc_commit_pair(bar_v_empty + 8 * p_vslot);
               ++jp;
               if (++p_buf == kNS) {
                 p_buf = 0;
@@ -633,6 +648,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float floor_n = fabsf(floor2) >= kFarScore ? floor_score * sl_pow2 : floor2;
     const uint32_t ocol = tmem + lane_off + kTmemO + hc * 64;
     uint32_t v[64];
+    // (until the first scores are there) which group each sequence is in, for the decode
+    for (int x = static_cast<int>(blockIdx.x) * kSoftmaxWarps + warp; x < a.num_seqs;
+         x += static_cast<int>(gridDim.x) * kSoftmaxWarps) {
+      const int4 g = find_group(a, x, lane);
+      if (lane == 0) a.lay.member[x] = g;
+    }
     int jt = 0;                // tiles, over all items
     int b3 = 0, s_phase = 0;   // score buffer of tile jt and its parity
 
@@ -701,7 +722,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // last key of the piece that the row sees
       int hi = -1;
       if (here)
-        hi = min(__ldcg(a.seq_lens + it.q0 + mine), it.keys) - 1 - it.block0 * kBlockSize;
+        hi = (it.whole ? it.keys : min(__ldcg(a.seq_lens + it.q0 + mine), it.keys)) - 1 -
+             it.block0 * kBlockSize;
       const int64_t row =
           static_cast<int64_t>(it.slot) * a.lay.slot_rows + rank * tpt * G + r;
       // reference maximum: a score, in log2 units, and as the softmax subtracts it
@@ -715,7 +737,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int b = jt & 1;
           tc_fence_after();
           const int kb = j * kTileKeys + hc * 64;
-          const bool whole = hi >= kb + 63;
+          const bool whole = !here || hi >= kb + 63;  // (rows of no member hold anything)
           float mloc;
           const uint32_t sc = tmem + lane_off + b3 * 128 + hc * 64;
           if (!__all_sync(0xffffffffu, whole)) {

@@ -48,8 +48,7 @@
 //
 // So does the decode of sequences that share prefixes, for what is each one's own:
 // the blocks behind its group's prefix, joined at the end with the results that
-// pa_shared_prefix.cu left for the prefix.  Its CTAs may start before that kernel is
-// done (which waits for all work before it), and wait for it where they join.
+// pa_shared_prefix.cu left for the prefix.
 #include <float.h>
 #include <math.h>
 
@@ -131,30 +130,6 @@ struct KindArgs<kShared> {
   using type = SharedDecodeArgs;
 };
 
-// The group of sequence s (-1: none), its first member and its prefix's blocks.  Called
-// by a whole warp.
-__device__ __forceinline__ int find_group(const SharedArgs& a, int s, int lane, int& first,
-                                          int& blocks) {
-  // offsets rise: 32 of them at a time narrow the range [lo, hi) whose group holds s
-  first = blocks = 0;
-  if (a.num_groups == 0) return -1;
-  int lo = 0, hi = a.num_groups;
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32;
-    const int at = lo + lane * step;
-    const bool below = at < hi && __ldcg(a.group_offsets + at) <= s;
-    // (at least the first one: sequences before every group have none, seen below)
-    const int n = max(__popc(__ballot_sync(0xffffffffu, below)), 1);
-    const int next = lo + (n - 1) * step;
-    hi = min(hi, next + step);
-    lo = next;
-  }
-  const SharedGroup g = shared_group(a, lo);
-  first = g.first;
-  blocks = g.blocks;
-  return s >= g.first && s < g.first + g.members ? lo : -1;
-}
-
 template <int D, int W, int M>
 __global__ void __launch_bounds__(32 * W)
     decode_window_kernel(const typename KindArgs<M>::type a) {
@@ -181,7 +156,7 @@ __global__ void __launch_bounds__(32 * W)
   const int G = a.group;
 
   griddep_launch_dependents();
-  if constexpr (M != kShared) griddep_wait();
+  griddep_wait();
 
   // q: head g of the group, the columns of this lane's K pieces
   uint4 qf[KJ];
@@ -189,8 +164,7 @@ __global__ void __launch_bounds__(32 * W)
       a.q + (static_cast<int64_t>(s) * a.num_q_heads + kvh * G + (g < G ? g : 0)) * D;
 #pragma unroll
   for (int j = 0; j < KJ; ++j) {
-    const uint4* const at = reinterpret_cast<const uint4*>(qrow + 8 * (4 * j + t));
-    qf[j] = M == kShared ? __ldcg(at) : *at;
+    qf[j] = *reinterpret_cast<const uint4*>(qrow + 8 * (4 * j + t));
     if (g >= G) qf[j] = make_uint4(0, 0, 0, 0);
   }
 
@@ -204,7 +178,7 @@ __global__ void __launch_bounds__(32 * W)
     table_row = find_chunk(a, s, lane, n);
     if (table_row < 0) return;  // (every CTA of the cluster) a row of no chunk stays
   } else {
-    n = M == kShared ? __ldcg(a.seq_lens + s) : a.seq_lens[s];
+    n = a.seq_lens[s];
     const int cap = a.max_blocks * kBlockSize;
     if (n < 0 || n > cap) {
       if (threadIdx.x == 0 && rank == 0 && kvh == 0) atomicOr(a.err, PA_DEVERR_SEQ_LEN);
@@ -213,11 +187,10 @@ __global__ void __launch_bounds__(32 * W)
   }
   int lo = n > a.window ? n - a.window : 0;        // first key of the window
   int ns = a.sinks < n ? a.sinks : n;              // visible sinks
-  int group = -1, group_first = 0;
+  int4 member{-1, 0, 0, 0};
   if constexpr (M == kShared) {
-    int blocks;
-    group = find_group(a.shared, s, lane, group_first, blocks);
-    lo = group >= 0 ? blocks * kBlockSize : 0;     // first key of the sequence's own
+    member = a.shared.lay.member[s];
+    lo = member.z * kBlockSize;                    // first key of the sequence's own
     ns = 0;
   }
   const int nsb = (ns + kBlockSize - 1) / kBlockSize;
@@ -248,7 +221,7 @@ __global__ void __launch_bounds__(32 * W)
     const int mine = vb + lane * stride;
     ids = 0;
     if (mine < nv) {
-      ids = M == kShared ? __ldcg(table + real_block(mine)) : table[real_block(mine)];
+      ids = table[real_block(mine)];
       if (ids < 0 || ids >= a.num_blocks) {
         atomicOr(a.err, PA_DEVERR_BLOCK_ID);
         ids = -1;  // reads as zeros
@@ -293,6 +266,29 @@ __global__ void __launch_bounds__(32 * W)
   if (first < nv) read_ids(first);
 #pragma unroll
   for (int st = 0; st < kStages; ++st) issue(st);
+
+  // The prefix's results for this sequence: those of its slots, `span` rows apart, from
+  // `part0` on.
+  int parts = 0;
+  int64_t part0 = 0, span = 0;
+  if constexpr (M == kShared) {
+    const SharedLayout& lay = a.shared.lay;
+    if (member.x >= 0) {
+      const int4 info = lay.info[member.x];
+      const int tiles = lay.info[a.shared.num_groups].y;
+      if (info.z > 0) {
+        const int rows = 2 * lay.tile_tokens;
+        const int u = member.y / rows;
+        const int t0 = info.y + u * info.z;
+        const int teams = shared_teams(lay, tiles);
+        const int j0 = shared_team(t0, tiles, teams);
+        parts = shared_team(t0 + info.z - 1, tiles, teams) - j0 + 1;
+        span = static_cast<int64_t>(a.num_kv_heads) * lay.slot_rows;
+        part0 = (static_cast<int64_t>(j0 + info.x + u) * a.num_kv_heads + kvh) * lay.slot_rows +
+                (member.y - u * rows) * G;
+      }
+    }
+  }
 
   int stage = 0;
   for (int vb = first; vb < nv; vb += stride) {
@@ -410,56 +406,60 @@ __global__ void __launch_bounds__(32 * W)
       dst[0] = make_float2(o[4 * h + i][0], o[4 * h + i][2]);
       dst[D / 2] = make_float2(o[4 * h + i][1], o[4 * h + i][3]);
     }
-  // The prefix's results for this sequence: those of its slots, `span` rows apart, from
-  // `part0` on.
-  int parts = 0;
-  int64_t part0 = 0, span = 0;
-  if constexpr (M == kShared) {
-    griddep_wait();
-    const SharedLayout& lay = a.shared.lay;
-    if (group >= 0) {
-      const int4 info = __ldcg(lay.info + group);
-      const int tiles = __ldcg(lay.info + a.shared.num_groups).y;
-      if (info.z > 0) {
-        const int rows = 2 * lay.tile_tokens;
-        const int at = s - group_first, u = at / rows;
-        const int t0 = info.y + u * info.z;
-        const int teams = shared_teams(lay, tiles);
-        const int j0 = shared_team(t0, tiles, teams);
-        parts = shared_team(t0 + info.z - 1, tiles, teams) - j0 + 1;
-        span = static_cast<int64_t>(a.num_kv_heads) * lay.slot_rows;
-        part0 = (static_cast<int64_t>(j0 + info.x + u) * a.num_kv_heads + kvh) * lay.slot_rows +
-                (at - u * rows) * G;
-      }
-    }
-  }
-  // An output element, of head h: the softmax's maximum, sum and weighted values over
-  // the sequence's own keys, joined with those over its prefix.
-  auto emit = [&](int h, int d, float m, float l, float acc) {
-    if constexpr (M == kShared) {
-      if (parts > 0) {
-        const float2* const ml = a.shared.lay.part_ml + part0 + h;
-        const float* const o = a.shared.lay.part_o + (part0 + h) * D + d;
-        float top = m;
-        for (int p = 0; p < parts; ++p) top = fmaxf(top, __ldcg(ml + p * span).x);
-        const float own = fast_exp2(m - top);
-        acc *= own;
-        l *= own;
-#pragma unroll 4
-        for (int p = 0; p < parts; ++p) {
-          const float2 x = __ldcg(ml + p * span);
-          const float f = fast_exp2(x.x - top);
-          acc += f * __ldcg(o + p * span * D);
-          l += f * x.y;
-        }
-        m = top;
-      }
-    }
-    const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + kvh * G + h;
-    a.out[row * D + d] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
-    if (d == 0 && a.out_lse) a.out_lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-  };
   __syncthreads();
+  if constexpr (M == kShared) {
+    // four columns of a head: the CTA's warps, then the prefix's pieces
+    for (int e = 4 * threadIdx.x; e < G * D; e += 4 * 32 * W) {
+      const int h = e / D, d = e % D;
+      float m = kFloor;
+#pragma unroll
+      for (int w = 0; w < W; ++w) m = fmaxf(m, sm_m[w * 8 + h]);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      float l = 0.f;
+      auto add = [&](float f, float4 x, float sum) {
+        acc.x += f * x.x;
+        acc.y += f * x.y;
+        acc.z += f * x.z;
+        acc.w += f * x.w;
+        l += f * sum;
+      };
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        add(fast_exp2(sm_m[w * 8 + h] - m),
+            *reinterpret_cast<const float4*>(sm_o + w * kPart + h * D + d), sm_l[w * 8 + h]);
+      const float2* const ml = a.shared.lay.part_ml + part0 + h;
+      const float* const o = a.shared.lay.part_o + (part0 + h) * D + d;
+      // (four at a time: their loads are under way together)
+#pragma unroll 1
+      for (int p0 = 0; p0 < parts; p0 += 4) {
+        float2 x[4];
+        float4 y[4];
+        float top = m;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int p = min(p0 + i, parts - 1);
+          x[i] = ml[p * span];
+          y[i] = *reinterpret_cast<const float4*>(o + p * span * D);
+          top = fmaxf(top, x[i].x);
+        }
+        const float own = fast_exp2(m - top);
+        acc = make_float4(acc.x * own, acc.y * own, acc.z * own, acc.w * own);
+        l *= own;
+        m = top;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (p0 + i < parts) add(fast_exp2(x[i].x - top), y[i], x[i].y);
+      }
+      const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + kvh * G + h;
+      const bool none = l == 0.f;
+      uint2 out;
+      out.x = none ? 0u : pack_bf16x2(acc.x / l, acc.y / l);
+      out.y = none ? 0u : pack_bf16x2(acc.z / l, acc.w / l);
+      *reinterpret_cast<uint2*>(a.out + row * D + d) = out;
+      if (d == 0 && a.out_lse) a.out_lse[row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+    return;
+  }
   for (int e = threadIdx.x; e < G * D; e += 32 * W) {
     const int h = e / D, d = e % D;
     float m = kFloor;
@@ -473,7 +473,9 @@ __global__ void __launch_bounds__(32 * W)
       l += f * sm_l[w * 8 + h];
     }
     if (splits == 1) {
-      emit(h, d, m, l, acc);
+      const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + kvh * G + h;
+      a.out[row * D + d] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
+      if (d == 0 && a.out_lse) a.out_lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     } else {
       cta_o[e] = acc;
       if (d == 0) {
@@ -497,7 +499,9 @@ __global__ void __launch_bounds__(32 * W)
       acc += f * ld_dsmem(mapa_shared(ro + 4 * e, c));
       l += f * ld_dsmem(mapa_shared(rl + 4 * h, c));
     }
-    emit(h, d, m, l, acc);
+    const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + kvh * G + h;
+    a.out[row * D + d] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
+    if (d == 0 && a.out_lse) a.out_lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
   cluster_sync();  // no CTA leaves while another may still read its shared memory
 }
@@ -667,11 +671,15 @@ cudaError_t launch_decode_window(const WindowDecodeArgs& a, int head_dim, int nu
 cudaError_t launch_shared_decode(const SharedDecodeArgs& args, int num_sms, cudaStream_t stream) {
   SharedDecodeArgs a = args;
   a.splits = 1;
+  // How long a sequence's own part is, the host does not know.  As many warps on each as
+  // run at once, nine on an SM: more would only come in rounds, which cost a unit's
+  // latency each.
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
-  // How long a sequence's own part is, the host does not know: eight warps on each where
-  // all units run at once, four where they come in rounds.
-  if (units <= num_sms) return launch<128, 8, kShared>(a, stream);
-  return launch<128, 4, kShared>(a, stream);
+  const int64_t warps = 9ll * num_sms / units;
+  if (warps >= 8) return launch<128, 8, kShared>(a, stream);
+  if (warps >= 4) return launch<128, 4, kShared>(a, stream);
+  if (warps >= 2) return launch<128, 2, kShared>(a, stream);
+  return launch<128, 1, kShared>(a, stream);
 }
 
 }  // namespace pa
