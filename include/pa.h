@@ -543,8 +543,9 @@ int pa_qk_norm_rope_cache_fp8(void *q_out, void *k_out, const void *q, const voi
  * finite; other slots may hold anything.  Equal calls give equal bits.  Weights over
  * the prefix are rounded to bf16 (each within 2^-8 of itself), as in the prefill.
  * Groups or shared_blocks out of range set PA_DEVERR_GROUP and are clamped: members
- * past max_group_size attend all their blocks on their own.  Other device errors as
- * pa_decode.
+ * past max_group_size attend all their blocks on their own.  (Batches whose tables
+ * name up to 96 MB of keys and values do not look at the groups: each sequence is
+ * attended through its own row, in one launch.)  Other device errors as pa_decode.
  */
 size_t pa_decode_shared_workspace_size(int num_seqs, int num_groups, int max_group_size,
                                        int num_q_heads, int num_kv_heads, int head_dim,
@@ -615,8 +616,8 @@ int pa_beam_select(int32_t *parents, int32_t *tokens, float *out_scores, uint8_t
  *   k_cache, v_cache  device bf16, layer l at + l * layer_stride (elements, a
  *              multiple of 8): [num_blocks, block_size, num_kv_heads, head_dim];
  *              num_layers 0: tables and lengths alone (pools may be NULL)
- * Outputs may not overlap inputs or pools (PA_ERR_INVALID); num_beams up to 32;
- * head_dim a multiple of 8.  A parent outside [-1, num_beams) sets PA_DEVERR_BEAM
+ * Outputs may not overlap inputs or pools (PA_ERR_INVALID); num_beams up to 32,
+ * num_beams * max_blocks_per_seq up to 2^30; head_dim a multiple of 8.  A parent outside [-1, num_beams) sets PA_DEVERR_BEAM
  * and counts as -1, a length outside its row PA_DEVERR_SEQ_LEN and is clamped; a
  * copy from or to a block outside the pool sets PA_DEVERR_BLOCK_ID and is left out.
  */

@@ -1657,6 +1657,17 @@ static int decode_shared_impl(void* out, const void* q, const void* k_cache, con
   a.group = group;
   a.window = INT32_MAX;
   a.scale_log2 = scale * 1.4426950408889634f;
+  // A small batch takes one launch, each sequence reading all its keys: the second
+  // pass costs more than the prefixes read again from L2.  Bytes of keys and values are
+  // bounded by the tables' width.  (us, this way / with the prefix apart: 17 MB 6.0 /
+  // 12.0 to 13.6; 70 MB 9.1 to 10.3 / 12.6 to 14.9; 117 and 140 MB in many groups 16 and
+  // 17 / 36 and 24, 134 MB in one of two 25.5 / 22.0; 270 MB 24 to 28 / 15 to 22.)
+  const int64_t bytes = static_cast<int64_t>(num_seqs) * max_blocks_per_seq * num_kv_heads * 8192;
+  if (!stall_loads && bytes <= int64_t{96} << 20)
+    return launch_decode_window(a, head_dim, d->num_sms, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
   SharedArgs& x = a.shared;
   x.block_tables = block_tables;
   x.seq_lens = seq_lens;
@@ -1800,7 +1811,8 @@ static int beam_reorder_impl(int32_t* out_tables, int32_t* out_lens, const int32
       block_size <= 0)
     return PA_ERR_INVALID;
   if (num_beams > kMaxBeams || num_requests > (1 << 24) ||
-      max_blocks_per_seq > INT32_MAX / kBlockSize || block_size != kBlockSize)
+      max_blocks_per_seq > INT32_MAX / kBlockSize || block_size != kBlockSize ||
+      static_cast<int64_t>(num_beams) * max_blocks_per_seq > (int64_t{1} << 30))
     return PA_ERR_UNSUPPORTED;
   const int64_t rows = static_cast<int64_t>(num_requests) * num_beams;
   int64_t pool = 0, token_bytes = 0;  // bytes of a pool's layers from first to last

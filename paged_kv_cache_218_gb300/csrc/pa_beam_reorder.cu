@@ -13,7 +13,7 @@
 //
 // What bounds it: HBM, by the bytes copied.  A beam's filled slots of one
 // layer are contiguous in each pool, so a copy is a run of up to 15 token
-// rows; a CTA reads its share of a run, 16 bytes a thread and eight of them
+// rows; a warp reads its share of a run, 16 bytes a lane and eight of them
 // under way, before it writes.  The mapping is a few ballots of a warp, which
 // every warp makes for itself rather than wait for another.
 #include <algorithm>
@@ -78,24 +78,9 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
   const int shift = owner_len / kBlockSize - keep;  // own block of column c: the owner's c + shift
   if (reports && here) a.out_lens[row] = new_len;
 
-  // ---- tables: the request's CTAs take columns in turn
+  // ---- copies: lane i's source and destination block, and vectors to copy
   const int32_t* const tables = a.tables + static_cast<int64_t>(r) * W * a.max_blocks;
   int32_t* const out = a.out_tables + static_cast<int64_t>(r) * W * a.max_blocks;
-  for (int i = 0; i < W; ++i) {
-    const int p = __shfl_sync(0xffffffffu, from, i), o = __shfl_sync(0xffffffffu, owner, i);
-    const int k = __shfl_sync(0xffffffffu, keep, i), d = __shfl_sync(0xffffffffu, shift, i);
-    for (int c = blockIdx.y * kThreads + threadIdx.x; c < a.max_blocks;
-         c += gridDim.y * kThreads) {
-      int id = -1;
-      if (c < k)
-        id = tables[static_cast<int64_t>(p) * a.max_blocks + c];
-      else if (c + d < a.max_blocks)
-        id = tables[static_cast<int64_t>(o) * a.max_blocks + c + d];
-      out[static_cast<int64_t>(i) * a.max_blocks + c] = id;
-    }
-  }
-
-  // ---- copies
   const int filled = new_len % kBlockSize;
   int src = 0, dst = 0;
   bool copy = child && !first && filled > 0 && a.num_layers > 0;
@@ -109,28 +94,57 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
       copy = false;
     }
   }
+  // what every thread needs of each beam
+  __shared__ int4 row_of[kMaxBeams];  // history's row, own row, history's blocks, shift
+  __shared__ int2 copy_of[kMaxBeams];
+  __shared__ int filled_of[kMaxBeams];
+  const unsigned copies = __ballot_sync(0xffffffffu, copy);
+  if (threadIdx.x < 32) {
+    row_of[lane] = make_int4(from, owner, keep, shift);
+    if (copy) {
+      const int at = __popc(copies & before);
+      copy_of[at] = make_int2(src, dst);
+      filled_of[at] = filled;
+    }
+  }
+  __syncthreads();
+
+  // ---- tables: the request's CTAs take entries in turn
+  const int entries = W * a.max_blocks, step = gridDim.y * kThreads;
+  for (int e = blockIdx.y * kThreads + threadIdx.x; e < entries; e += step) {
+    const int i = e / a.max_blocks, c = e - i * a.max_blocks;
+    const int4 x = row_of[i];
+    int id = -1;
+    if (c < x.z)
+      id = tables[static_cast<int64_t>(x.x) * a.max_blocks + c];
+    else if (c + x.w < a.max_blocks)
+      id = tables[static_cast<int64_t>(x.y) * a.max_blocks + c + x.w];
+    out[e] = id;
+  }
+
+  // ---- units of the copies: beam, layer, pool, part of the run of filled slots; a warp
+  // each, so that a CTA has eight on their way
   const int64_t block_bytes = a.token_bytes * kBlockSize;
-  for (unsigned todo = __ballot_sync(0xffffffffu, copy); todo; todo &= todo - 1) {
-    const int i = __ffs(todo) - 1;
-    const int64_t so = __shfl_sync(0xffffffffu, src, i) * block_bytes;
-    const int64_t to = __shfl_sync(0xffffffffu, dst, i) * block_bytes;
-    const int64_t vecs = __shfl_sync(0xffffffffu, filled, i) * a.token_bytes / 16;
-    // units: layer, pool, part of the run
-    for (int u = blockIdx.y; u < 2 * a.num_layers * a.parts; u += gridDim.y) {
-      const int run = u / a.parts, part = u - run * a.parts;
-      char* const pool = ((run & 1) ? a.v : a.k) + (run >> 1) * a.layer_bytes;
-      const uint4* const s = reinterpret_cast<const uint4*>(pool + so);
-      uint4* const d = reinterpret_cast<uint4*>(pool + to);
-      const int64_t end = vecs * (part + 1) / a.parts;
-      for (int64_t v = vecs * part / a.parts + threadIdx.x; v < end; v += kThreads * kVecs) {
-        uint4 x[kVecs];
+  const int runs = 2 * a.num_layers * a.parts;
+  const int64_t units = static_cast<int64_t>(__popc(copies)) * runs;
+  const int warps = gridDim.y * (kThreads / 32);
+  for (int64_t u = blockIdx.y * (kThreads / 32) + threadIdx.x / 32; u < units; u += warps) {
+    const int at = static_cast<int>(u / runs), run = static_cast<int>(u - at * runs);
+    const int pool_run = run / a.parts, part = run - pool_run * a.parts;
+    char* const pool = ((pool_run & 1) ? a.v : a.k) + (pool_run >> 1) * a.layer_bytes;
+    const int2 ids = copy_of[at];
+    const uint4* const s = reinterpret_cast<const uint4*>(pool + ids.x * block_bytes);
+    uint4* const d = reinterpret_cast<uint4*>(pool + ids.y * block_bytes);
+    const int64_t vecs = filled_of[at] * a.token_bytes / 16;
+    const int64_t end = vecs * (part + 1) / a.parts;
+    for (int64_t v = vecs * part / a.parts + lane; v < end; v += 32 * kVecs) {
+      uint4 x[kVecs];
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j)
-          if (v + j * kThreads < end) x[j] = s[v + j * kThreads];
+      for (int j = 0; j < kVecs; ++j)
+        if (v + j * 32 < end) x[j] = s[v + j * 32];
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j)
-          if (v + j * kThreads < end) d[v + j * kThreads] = x[j];
-      }
+      for (int j = 0; j < kVecs; ++j)
+        if (v + j * 32 < end) d[v + j * 32] = x[j];
     }
   }
 }
@@ -138,13 +152,15 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
 }  // namespace
 
 cudaError_t launch_beam_reorder(BeamReorderArgs a, int num_sms, cudaStream_t stream) {
-  // CTAs per request: one for each layer's pool, or a part of it where requests are few,
-  // or several where they are many; eight CTAs of 256 threads fit an SM.
+  // A run of one layer's pool is up to 15 token rows; four warps share one of 2 KB rows.
+  // CTAs of eight warps: for every run of all beams but one, at most as many as fit the
+  // device, eight on an SM.
+  a.parts = static_cast<int>(std::min<int64_t>(std::max<int64_t>(a.token_bytes / 512, 1), 8));
   const int64_t want = (8ll * num_sms + a.num_requests - 1) / a.num_requests;
-  const int64_t runs = 2ll * a.num_layers;
-  a.parts = 1;
-  while (a.parts < 4 && runs * a.parts * 2 <= want) a.parts *= 2;
-  const int64_t units = std::max<int64_t>(runs * a.parts, (a.max_blocks + kThreads - 1) / kThreads);
+  const int64_t runs = (2ll * a.num_layers * a.parts * std::max(1, a.num_beams - 1) + 7) / 8;
+  const int64_t columns =
+      (static_cast<int64_t>(a.num_beams) * a.max_blocks + kThreads - 1) / kThreads;
+  const int64_t units = std::max(runs, columns);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(a.num_requests),
                      static_cast<unsigned>(std::max<int64_t>(1, std::min(units, want))));

@@ -80,16 +80,22 @@ __device__ __forceinline__ float bf16_round(float x) {
   return __bfloat162float(__float2bfloat16(x));
 }
 
-constexpr int kStages = 3;  // blocks in flight per warp
+// Blocks in flight per warp; two where a warp has a unit to itself behind a shared prefix,
+// so that thirteen of them and not nine run on an SM: as many bytes on their way, and
+// fewer rounds of a unit's latency.
+template <int W, int M>
+constexpr int kStages = 3;
+template <>
+constexpr int kStages<1, 2> = 2;
 
 // Shared memory: the warps' rings [W][kStages][K, V][16 rows][D]; once a warp
 // has read its last block its outputs [8 heads][D] (fp32) take the front of its
 // ring, and those of the whole CTA the next part of warp 0's; maxima and sums
 // [W][8], and the CTA's [8], behind the rings.
-template <int D, int W>
+template <int D, int W, int M>
 struct DecodePlan {
   static constexpr int kStage = 2 * kBlockSize * D * 2;
-  static constexpr int kRing = kStages * kStage;
+  static constexpr int kRing = kStages<W, M> * kStage;
   static constexpr int kStatOff = W * kRing;
   static constexpr int kBytes = kStatOff + (W + 1) * 16 * 4;
   static_assert(2 * 8 * D * 4 <= kRing, "outputs in the ring");
@@ -134,7 +140,8 @@ template <int D, int W, int M>
 __global__ void __launch_bounds__(32 * W)
     decode_window_kernel(const typename KindArgs<M>::type a) {
   constexpr bool C = M == kChunks;
-  using P = DecodePlan<D, W>;
+  using P = DecodePlan<D, W, M>;
+  constexpr int kStages = pa::kStages<W, M>;
   constexpr int KJ = D / 32;  // 16-byte pieces of a K row per lane
   constexpr int VH = D / 64;  // 16-byte pieces of a V row per lane
   extern __shared__ __align__(16) uint8_t smem[];
@@ -519,7 +526,7 @@ cudaError_t launch(const typename KindArgs<M>::type& a, cudaStream_t stream) {
     if (!set_for[dev]) {
       e = cudaFuncSetAttribute(decode_window_kernel<D, W, M>,
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               DecodePlan<D, W>::kBytes);
+                               DecodePlan<D, W, M>::kBytes);
       if (e != cudaSuccess) return e;
       set_for[dev] = true;
     }
@@ -528,7 +535,7 @@ cudaError_t launch(const typename KindArgs<M>::type& a, cudaStream_t stream) {
   cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(a.num_seqs) * a.num_kv_heads *
                                            a.splits));
   cfg.blockDim = dim3(32 * W);
-  cfg.dynamicSmemBytes = DecodePlan<D, W>::kBytes;
+  cfg.dynamicSmemBytes = DecodePlan<D, W, M>::kBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -563,7 +570,7 @@ cudaError_t residency(int num_sms, Residency* out) {
   std::lock_guard<std::mutex> lock(mu);
   Residency& r = by_device[dev];
   if (!r.ready) {
-    constexpr int smem = DecodePlan<D, 8>::kBytes;
+    constexpr int smem = DecodePlan<D, 8, M>::kBytes;
     const auto kernel = decode_window_kernel<D, 8, M>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -672,7 +679,7 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& args, int num_sms, cuda
   SharedDecodeArgs a = args;
   a.splits = 1;
   // How long a sequence's own part is, the host does not know.  As many warps on each as
-  // run at once, nine on an SM: more would only come in rounds, which cost a unit's
+  // run at once, nine or more on an SM: more would only come in rounds, which cost a unit's
   // latency each.
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   const int64_t warps = 9ll * num_sms / units;

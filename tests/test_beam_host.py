@@ -62,6 +62,7 @@ REORDER_T = dict(zip(REORDER, [V, V, V, V, V, I, I, I, V, V, I, L, I, I, I, L, V
     (dict(Hkv=0), INVALID), (dict(D=0), INVALID), (dict(nb=0), INVALID), (dict(bs=0), INVALID),
     (dict(stride=-8), INVALID), (dict(nb=1 << 60), INVALID), (dict(W=33), UNSUPPORTED),
     (dict(bs=32), UNSUPPORTED), (dict(D=4), UNSUPPORTED), (dict(mb=1 << 28), UNSUPPORTED),
+    (dict(W=32, mb=(1 << 25) + 1), UNSUPPORTED),
     (dict(R=1 << 25), UNSUPPORTED), (dict(layers=1 << 20), UNSUPPORTED),
     (dict(stride=64 * 16 * 2 * 64 - 16), INVALID), (dict(stride=64 * 16 * 2 * 64 + 4), INVALID),
     (dict(R=0), OK), (dict(R=0, ot=None, k=None), OK),

@@ -19,13 +19,16 @@ def pa(cuda_device):
 
 class Case:
     """groups: (shared blocks, [lengths of the members]).  Every slot that no sequence sees is
-    NaN, and table entries of blocks without one are ids outside the pool."""
+    NaN, and table entries of blocks without one are ids outside the pool.  Tables are so
+    wide that the call takes the prefix apart; small: as narrow as they can be."""
 
-    def __init__(self, seed, groups, Hq, Hkv, loose=0, scale=None, amp=1.0):
+    def __init__(self, seed, groups, Hq, Hkv, loose=0, scale=None, amp=1.0, small=False):
         rng = np.random.default_rng(seed)
         lens = [n for _, m in groups for n in m] + [int(rng.integers(0, 90)) for _ in range(loose)]
         S = len(lens)
         width = max([1] + [p for p, m in groups] + [(n + 15) // 16 for n in lens]) + 1
+        if not small:  # more than 96 MB
+            width = max(width, (96 << 20) // (S * Hkv * 8192) + 1)
         tables = np.full((S, width), -7, dtype=np.int64)
         tables[:, 1::2] = 2**31 - 1
         seen = []  # of each block given out
@@ -132,6 +135,21 @@ def test_groups_past_a_tile_and_a_pair(pa, members):
     c.run(pa)
     c.check(rows=sorted({0, 1, 30, members - 1, members // 2, min(31, members - 1),
                          min(32, members - 1), min(63, members - 1), min(64, members - 1)}))
+
+
+@pytest.mark.parametrize("groups", [[(9, [150, 160, 144])], [(3, [0, 20, 48, 49]), (0, [70]), (5, [])],
+                                    [(60, [1000, 961, 3])]])
+def test_small_batches(pa, groups):
+    """One launch, each sequence through its own row; no matter what the groups say."""
+    c = Case(30, groups, 8, 2, loose=2, small=True)
+    c.run(pa)
+    c.check()
+    c.shared.fill_(-5)
+    c.offsets.fill_(10**6)
+    c.out.zero_()
+    c.run(pa)
+    c.check()
+    assert pa.pa_device_error_flags() == 0
 
 
 def test_many_ragged_groups(pa):
