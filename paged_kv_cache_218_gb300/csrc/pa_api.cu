@@ -1567,19 +1567,22 @@ int pa_test_prefill_window_stalled(void* out, const void* q, const void* k_cache
 // Slots, teams and workspace of a shared-prefix decode.
 struct SharedPlan {
   SharedLayout lay;
-  size_t ml_off, info_off, member_off, bytes;
+  size_t ml_off, info_off, member_off, own_off, own_ml_off, bytes;
   bool fits;
 };
 
 static SharedPlan shared_plan(int num_seqs, int num_groups, int max_group_size, int num_kv_heads,
                               int group, int num_sms) {
   SharedPlan p{};
-  const int pairs = num_sms / 2 < 1 ? 1 : num_sms / 2;
-  p.lay.team_pairs = num_kv_heads < pairs ? num_kv_heads : pairs;
-  p.lay.teams = pairs / p.lay.team_pairs;
-  p.lay.tile_tokens = 128 / group;
-  const int rows = 2 * p.lay.tile_tokens;
   const int members = max_group_size < num_seqs ? max_group_size : num_seqs;
+  p.lay.tile_tokens = 128 / group;
+  p.lay.worker_ctas = members > p.lay.tile_tokens && num_sms >= 2 ? 2 : 1;
+  p.lay.unit_tokens = p.lay.worker_ctas * p.lay.tile_tokens;
+  p.lay.box_tokens = members < p.lay.tile_tokens ? members : p.lay.tile_tokens;
+  const int workers = num_sms / p.lay.worker_ctas;
+  p.lay.team_workers = num_kv_heads < workers ? num_kv_heads : workers;
+  p.lay.teams = workers / p.lay.team_workers;
+  const int rows = p.lay.unit_tokens;
   p.lay.slot_rows = (members < rows ? members : rows) * group;
   // every group may begin a unit, and every `rows` sequences
   const int64_t units = static_cast<int64_t>(num_groups) + num_seqs / rows;
@@ -1589,7 +1592,10 @@ static SharedPlan shared_plan(int num_seqs, int num_groups, int max_group_size, 
   p.ml_off = round256(static_cast<size_t>(out_rows) * 128 * sizeof(float));
   p.info_off = p.ml_off + round256(static_cast<size_t>(out_rows) * sizeof(float2));
   p.member_off = p.info_off + round256((static_cast<size_t>(num_groups) + 1) * sizeof(int4));
-  p.bytes = p.member_off + round256(static_cast<size_t>(num_seqs) * sizeof(int4));
+  p.own_off = p.member_off + round256(static_cast<size_t>(num_seqs) * sizeof(int4));
+  const size_t own_rows = static_cast<size_t>(num_seqs) * num_kv_heads * group;
+  p.own_ml_off = p.own_off + round256(own_rows * 128 * sizeof(float));
+  p.bytes = p.own_ml_off + round256(own_rows * sizeof(float2));
   return p;
 }
 
@@ -1691,14 +1697,17 @@ static int decode_shared_impl(void* out, const void* q, const void* k_cache, con
   x.lay.part_ml = reinterpret_cast<float2*>(ws + p.ml_off);
   x.lay.info = reinterpret_cast<int4*>(ws + p.info_off);
   x.lay.member = reinterpret_cast<int4*>(ws + p.member_off);
+  x.lay.own_o = reinterpret_cast<float*>(ws + p.own_off);
+  x.lay.own_ml = reinterpret_cast<float2*>(ws + p.own_ml_off);
   CUtensorMap tm_q, tm_k, tm_v;
-  if (encode_q_map(&tm_q, q, num_seqs, num_q_heads, head_dim, group, p.lay.tile_tokens) ||
+  if (encode_q_map(&tm_q, q, num_seqs, num_q_heads, head_dim, group, p.lay.box_tokens) ||
       encode_pool_map(&tm_k, k_cache, num_blocks, num_kv_heads, head_dim, kPoolKeyTile) ||
       encode_pool_map(&tm_v, v_cache, num_blocks, num_kv_heads, head_dim, kPool2D))
     return PA_ERR_CUDA;
   if (launch_shared_prefix(x, &tm_q, &tm_k, &tm_v, static_cast<cudaStream_t>(stream)) !=
           cudaSuccess ||
-      launch_shared_decode(a, d->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      launch_shared_decode(a, d->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess ||
+      launch_shared_join(x, a.out, out_lse, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return PA_ERR_CUDA;
   return PA_OK;
 }

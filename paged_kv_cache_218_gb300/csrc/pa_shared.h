@@ -7,15 +7,19 @@
 
 namespace pa {
 
-// The prefix pass cuts its work into teams of CTA pairs, one pair for each kv head.
-// Units are (group, rows of up to two query tiles), in order; a team takes a range of
-// the units' key tiles, all units behind one another, and leaves a partial result
-// (maximum, sum, weighted values) for each unit that it meets: that of team j and
-// unit u in slot (j + u) * kv heads + kv head, so that a unit's slots are neighbours.
+// The prefix pass cuts its work into teams of workers (CTAs, or pairs of them), one worker
+// for each kv head.  Units are (group, rows of a worker's query tiles), in order; a team
+// takes a range of the units' key tiles, all units behind one another, and leaves a
+// partial result (maximum, sum, weighted values) for each unit that it meets: that of
+// team j and unit u in slot (j + u) * kv heads + kv head, so that a unit's slots are
+// neighbours.
 struct SharedLayout {
+  int worker_ctas;   // 1, or 2 for groups of more than 128 query rows per kv head
   int teams;
-  int team_pairs;   // pairs of a team; a pair takes every team_pairs-th kv head
-  int tile_tokens;  // members (query tokens) of a query tile, 128 / group
+  int team_workers;  // of a team; a worker takes every team_workers-th kv head
+  int tile_tokens;   // members (query tokens) of a query tile, 128 / group
+  int unit_tokens;   // and of a unit, worker_ctas tiles
+  int box_tokens;    // and of a load of one: no group has more
   int slot_rows;    // query rows of a slot
   int max_units;    // that the slots have room for
   float* part_o;    // [slots][slot_rows][128], not divided by the sum
@@ -23,9 +27,12 @@ struct SharedLayout {
   // [num_groups + 1]: a group's first unit, its first key tile, key tiles of each of its
   // units, first member; last entry: .y all key tiles.  Written by the prefix pass.
   int4* info;
-  // [num_seqs]: a sequence's group (-1: none), its number in it, its prefix's blocks.
-  // Written by the prefix pass.
+  // Of the decode of each sequence's own part: [num_seqs] its group (-1: none), its number
+  // in it, its prefix's blocks; [num_seqs][q heads][128] weighted values, and [num_seqs]
+  // [q heads] maximum and sum, as above.
   int4* member;
+  float* own_o;
+  float2* own_ml;
 };
 
 struct SharedArgs {
@@ -96,7 +103,7 @@ __device__ __forceinline__ int shared_team(int t, int tiles, int teams) {
   return static_cast<int>(((static_cast<int64_t>(t) + 1) * teams - 1) / tiles);
 }
 
-// Decode over each sequence's own blocks, joined with the prefix pass's results.
+// Decode over each sequence's own blocks.
 struct SharedDecodeArgs : WindowDecodeArgs {
   SharedArgs shared;
 };
@@ -105,5 +112,7 @@ cudaError_t launch_shared_prefix(const SharedArgs& a, const CUtensorMap* tm_q,
                                  const CUtensorMap* tm_k, const CUtensorMap* tm_v,
                                  cudaStream_t stream);
 cudaError_t launch_shared_decode(const SharedDecodeArgs& a, int num_sms, cudaStream_t stream);
+cudaError_t launch_shared_join(const SharedArgs& a, __nv_bfloat16* out, float* out_lse,
+                               cudaStream_t stream);
 
 }  // namespace pa

@@ -3,24 +3,27 @@
 //
 // The queries of a group's members, G heads a kv head, are the rows of one dense
 // product with the prefix's keys: no mask but the members' lengths.  What is left
-// of each sequence is decoded by pa_window_decode.cu, which joins both.
+// of each sequence is decoded by pa_window_decode.cu beside it; a third kernel, below,
+// joins both.
 //
 // The tensor-core pipeline of a key tile (128 keys) is that of the windowed prefill:
-// a CTA pair (cta_group::2) on two query tiles of up to 128 rows, K and V halves
-// loaded by each CTA, three score buffers in tensor memory, online softmax with P
+// K and V tiles by TMA, three score buffers in tensor memory, online softmax with P
 // written back over its scores, bounded waits.  What differs:
 //
+//  * Groups of up to 128 query rows a kv head are a lone CTA's (cta_group::1), larger ones
+//    a pair's, 256 rows at a time (cta_group::2, K and V halves loaded by each CTA): 128
+//    rows fill but half of a pair's products, and those of a tile would then take as
+//    long as its bytes.
 //  * Work is cut along the keys, so that a single long prefix fills the device: teams
-//    of pairs, one pair for each kv head, take equal ranges of all key tiles.  The
-//    pairs of a team read the same blocks at the same time, each its own head's 256
+//    of workers (CTAs or pairs), one for each kv head, take equal ranges of all key tiles.
+//    The workers of a team read the same blocks at the same time, each its own head's 256
 //    bytes of a token's row; together they read whole rows, which memory serves faster.
 //  * A piece (a unit's key tiles in a team's range) leaves its reference maximum, sum
-//    and weighted values, in fp32 and undivided, for the decode to join.
+//    and weighted values, in fp32 and undivided, for the join behind.
 //  * Warps whose 32 rows no member fills wait for scores and pass them on unread.
 //
-// What bounds it: with up to 256 rows a kv head, HBM: a pair takes 0.75 us for a tile's
-// 64 KB, which is both its share of the memory's rate and what its two products and
-// their hand-overs take; with more rows, the tensor pipe.
+// What bounds it: with up to 256 rows a kv head, HBM: a pair takes 0.72 us for a tile's
+// 64 KB, 6.5 TB/s over 72 pairs; with more rows, the tensor pipe and its hand-overs, 0.79.
 #include <limits.h>
 
 #include <mutex>
@@ -39,13 +42,18 @@ constexpr uint64_t kSettleNs = 1000000;  // far longer than any copy takes
 constexpr float kFloor = -0x1.fffff0p127f;
 constexpr float kFarScore = 0x1p31f;  // (log2 units)
 
-// Shared memory of one CTA of a pair: two Q tiles, four K and five V half
-// tiles, block ids of both loaders, the softmax's exchange, barriers.
+// Shared memory of one CTA: Q tiles of two items, K and V tiles (a pair's CTAs hold half
+// of each), block ids of both loaders, the softmax's exchange, barriers.  An operand tile
+// has 128 rows; the second Q tile lies kQRows behind the first, whose other rows no member
+// has.  (What is left of an SM holds CTAs of the decode of the sequences' own parts.)
+template <int CG, int kQRows>
 struct SPlan {
-  static constexpr int kNK = 4, kNV = 5;
-  static constexpr int kKSlot = kHalf, kVSlot = kHalf;
-  static constexpr int kQOff = 0;  // [2][2 * kHalf]
-  static constexpr int kKOff = kQOff + 4 * kHalf;
+  static constexpr int kNK = CG == 2 ? 3 : 2, kNV = CG == 2 ? 4 : 2;
+  static constexpr int kKSlot = 2 * kHalf / CG, kVSlot = 2 * kHalf / CG;
+  static constexpr int kQNext = kQRows * 128;           // to the next Q tile
+  static constexpr int kQHalf = kQNext + kHalf;         // to the other 64 columns
+  static constexpr int kQOff = 0;
+  static constexpr int kKOff = kQOff + 2 * kQHalf;
   static constexpr int kVOff = kKOff + kNK * kKSlot;
   static constexpr int kIdsOff = kVOff + kNV * kVSlot;
   static constexpr int kRedOff = kIdsOff + 2 * kIdRing * 8 * 4;
@@ -53,10 +61,12 @@ struct SPlan {
   static constexpr int kBarOff = kRedOff2 + 2 * 128 * 4;
   static constexpr int kItemsOff = kBarOff + 512;  // [kItemRing]
   static constexpr int kSmemBytes = kItemsOff + 8 * 64;
+  static_assert(kSmemBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
+  static_assert(kQNext % 1024 == 0, "swizzle atoms");
 };
-static_assert(SPlan::kSmemBytes + 1024 <= 227 * 1024, "shared memory of one CTA");
 
-// One work item of a pair: a piece of a unit's key tiles, one kv head.
+// One work item of a worker (a CTA, or a pair of them): a piece of a unit's key tiles,
+// one kv head.
 struct Item {
   int nkt;         // key tiles; 0 ends the list
   int row;         // table row that names the prefix's blocks: the first member's
@@ -86,7 +96,7 @@ struct Groups {
   __device__ __forceinline__ Groups(const SharedArgs& a, int g0, int before, int lane) {
     g = SharedGroup{0, 0, 0, true};
     if (g0 + lane < a.num_groups) g = shared_group(a, g0 + lane);
-    const int rows = 2 * a.lay.tile_tokens;
+    const int rows = a.lay.unit_tokens;
     units = g.blocks > 0 ? (g.members + rows - 1) / rows : 0;
     units_sum = units;
 #pragma unroll
@@ -114,7 +124,7 @@ struct Groups {
   }
 };
 
-// Walks a pair's pieces.
+// Walks a worker's pieces.
 struct Cursor {
   int pos, end;      // key tiles of the team's range that are left
   int group0;        // groups at hand, 32 at a time,
@@ -146,7 +156,7 @@ __device__ __forceinline__ Item next_item(const SharedArgs& a, Cursor& cur, Grou
     const int u = at / nkt, tile0 = at - u * nkt;
     const int n = min(nkt - tile0, cur.end - cur.pos);
     cur.pos += n;
-    const int rows = 2 * a.lay.tile_tokens;
+    const int rows = a.lay.unit_tokens;
     it.row = first;
     it.kvh = cur.kvh;
     it.q0 = first + u * rows;
@@ -239,11 +249,13 @@ __device__ __forceinline__ void stg32(float* p, const uint32_t* x) {
                : "memory");
 }
 
+// CG: CTAs of a worker.  Two of them (a tcgen05 pair) take 256 query rows, one 128.
+template <int CG, int kQRows>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const SharedArgs a) {
-  using P = SPlan;
+  using P = SPlan<CG, kQRows>;
   constexpr int kNK = P::kNK, kNV = P::kNV;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -274,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.group, tpt = a.lay.tile_tokens;
-  const int rank = static_cast<int>(blockIdx.x) & 1;
+  const int rank = CG == 2 ? static_cast<int>(blockIdx.x) & 1 : 0;
   const bool issuer = rank == 0;
 
   if (tid == 0) {
@@ -288,12 +300,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int k = 0; k < kNV; ++k) {
       mbar_init(bar_v_full + 8 * k, 1);
-      mbar_init(bar_v_ready + 8 * k, 2);
+      mbar_init(bar_v_ready + 8 * k, CG);
       mbar_init(bar_v_empty + 8 * k, 1);
     }
     for (int k = 0; k < kNS; ++k) {
       mbar_init(bar_s_full + 8 * k, 1);
-      mbar_init(bar_p_full + 8 * k, kSoftmaxWarps * 2);
+      mbar_init(bar_p_full + 8 * k, kSoftmaxWarps * CG);
       mbar_init(bar_o_done + 8 * k, 1);
     }
     for (int k = 0; k < kItemRing; ++k) mbar_init(bar_item + 8 * k, 1);
@@ -301,11 +313,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 0) {
-    tmem_alloc<2>(smem_u32(tmem_slot), kTmemCols);
-    tmem_relinquish<2>();
+    tmem_alloc<CG>(smem_u32(tmem_slot), kTmemCols);
+    tmem_relinquish<CG>();
   }
   tc_fence_before();
-  cluster_sync();  // both CTAs' barriers exist before either reports to the other
+  if constexpr (CG == 2)
+    cluster_sync();  // both CTAs' barriers exist before either reports to the other
+  else
+    __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
@@ -341,18 +356,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         tiles += __shfl_sync(0xffffffffu, x.tiles_sum, 31);
       }
       if (blockIdx.x == 0 && lane == 0) a.lay.info[a.num_groups] = make_int4(units, tiles, 0, 0);
-      const int pair = static_cast<int>(blockIdx.x >> 1);
-      const int team = pair / a.lay.team_pairs;
+      const int worker = static_cast<int>(blockIdx.x) / CG;
+      const int team = worker / a.lay.team_workers;
       const int teams = shared_teams(a.lay, tiles);
       const int from = team < teams ? static_cast<int>(static_cast<int64_t>(tiles) * team / teams) : 0;
       const int to =
           team < teams ? static_cast<int>(static_cast<int64_t>(tiles) * (team + 1) / teams) : 0;
-      Cursor cur{from, to, 0, 0, 0, team, pair - team * a.lay.team_pairs};
+      Cursor cur{from, to, 0, 0, 0, team, worker - team * a.lay.team_workers};
       Groups at_hand = head;
       unsigned published = 0;
       auto publish = [&]() {
-        if (cur.pos == cur.end && cur.kvh + a.lay.team_pairs < a.num_kv_heads) {
-          cur = Cursor{from, to, 0, 0, 0, team, cur.kvh + a.lay.team_pairs};
+        if (cur.pos == cur.end && cur.kvh + a.lay.team_workers < a.num_kv_heads) {
+          cur = Cursor{from, to, 0, 0, 0, team, cur.kvh + a.lay.team_workers};
           if (a.num_groups > 32) at_hand = Groups(a, 0, 0, lane);
         }
         const Item x = next_item(a, cur, at_hand, lane);
@@ -401,9 +416,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++qi;
           if (lane < 2) {  // a half each
             const uint32_t bar = bar_q + 8 * qb;
-            // (both CTAs' query tiles, tpt tokens of G heads, two halves)
-            if (issuer && lane == 0) mbar_arrive_expect_tx(bar, 4 * tpt * G * 128);
-            const uint32_t dst = sbase + P::kQOff + (2 * qb + lane) * kHalf;
+            // (the CTAs' query tiles, two halves of box_tokens tokens of G heads)
+            if (issuer && lane == 0)
+              mbar_arrive_expect_tx(bar, CG * 2 * a.lay.box_tokens * G * 128);
+            const uint32_t dst = sbase + P::kQOff + qb * P::kQNext + lane * P::kQHalf;
             const int row = it.q0 + rank * tpt;
             if (issuer)
               tma_load_3d(dst, &tm_q, lane * 64, it.kvh * G, row, bar, pol);
@@ -418,13 +434,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             !wait_warp(bar_k_empty + 8 * slot, ((total / kNK) - 1) & 1, abort_flag, a))
           break;
         const uint32_t bar = bar_k_full + 8 * slot;
-        // each CTA takes half of the tile's blocks, their number made even (an
+        // each CTA takes its share of the tile's blocks, their number made even (an
         // id past the list loads zeros)
         const int half = (tile_blocks(it.nvb, jk) + 1) / 2;
+        const int mine = half * 2 / CG;
         if (lane == 0 && issuer) mbar_arrive_expect_tx(bar, half * 4 * kBlockBytes);
         __syncwarp();
-        if (lane < half) {
-          const int id = ids_smem[(total % kIdRing) * 8 + half * rank + lane];
+        if (lane < mine) {
+          const int id = ids_smem[(total % kIdRing) * 8 + mine * rank + lane];
           const uint32_t dst = sbase + P::kKOff + slot * P::kKSlot + lane * 2 * kBlockBytes;
           if (issuer)
             tma_load_4d(dst, &tm_k, 0, 0, 2 * it.kvh, 2 * id, bar, pol);
@@ -459,8 +476,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t vt = sbase + P::kVOff + edge_slot * P::kVSlot;
           const uint32_t blk = vt + ((it.nvb - 1) & 7) * kBlockBytes;
 #pragma unroll 1
-          for (int e = lane + 8 * it.hidden; e < 8 * kBlockSize; e += 32)
+          for (int e = lane + 8 * it.hidden; e < 8 * kBlockSize; e += 32) {
             st_shared_zero16(blk + e * 16);
+            if constexpr (CG == 1) st_shared_zero16(blk + kHalf + e * 16);
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -516,13 +535,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (remote)
             mbar_arrive_expect_tx_remote(bar, blocks * kBlockBytes);
           else
-            mbar_arrive_expect_tx(bar, blocks * kBlockBytes);
+            mbar_arrive_expect_tx(bar, blocks * kBlockBytes * (2 / CG));
         }
         __syncwarp();
-        if (lane < blocks) {  // CTA r takes columns 64 r .. 64 r + 63 of every key
-          const int id = ids_smem[(total % kIdRing) * 8 + lane];
-          const uint32_t dst = sbase + P::kVOff + slot * P::kVSlot + lane * kBlockBytes;
-          const int x = it.kvh * 128 + rank * 64, y = id * kBlockSize;
+        // 64 columns of a block each: CTA r of a pair takes columns 64 r .. 64 r + 63 of
+        // every key, a lone CTA both halves
+        const int blk = lane & 7, h = CG == 2 ? rank : lane >> 3;
+        if (lane < 16 / CG && blk < blocks) {
+          const int id = ids_smem[(total % kIdRing) * 8 + blk];
+          const uint32_t dst = sbase + P::kVOff + slot * P::kVSlot + blk * kBlockBytes +
+                               (CG == 1 ? h * kHalf : 0);
+          const int x = it.kvh * 128 + h * 64, y = id * kBlockSize;
           if (remote)
             tma_load_2d_pair(dst, &tm_v, x, y, bar, pol);
           else
@@ -544,8 +567,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Two threads of the even CTA, as in pa_prefill_body.cuh.
     if (lane == 0 && issuer) {
       bool ok = true;
+      auto commit = [&](uint32_t bar) {
+        if constexpr (CG == 2)
+          tc_commit_pair(bar);
+        else
+          tc_commit<1>(bar);
+      };
       if (warp == kMmaWarp) {
-        const uint32_t idesc_s = instr_desc(0, 256) & ~(0x3fu << 17);  // (columns / 8 left out)
+        const uint32_t idesc_s = instr_desc(0, 128 * CG) & ~(0x3fu << 17);  // (columns / 8 left out)
         const uint64_t dk0 = smem_desc(sbase + P::kKOff, 16, kKGroupStride);
         const uint64_t dq0 = smem_desc(sbase + P::kQOff, 16, 1024);
         int s_buf = 0, s_round = 0, s_kslot = 0, s_kphase = 0;
@@ -554,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int nkt = ok ? ring_item(k)->nkt : 0;
           if (nkt == 0) break;
           const int nvb = ring_item(k)->nvb;
-          const uint64_t dq = dq0 + static_cast<uint64_t>(((k & 1) * 2 * kHalf) >> 4);
+          const uint64_t dq = dq0 + static_cast<uint64_t>(((k & 1) * P::kQNext) >> 4);
           ok = wait(bar_q + 8 * (k & 1), (k >> 1) & 1, abort_flag, a);
           int js = 0;
           while (ok && js < nkt) {
@@ -568,11 +597,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               tc_fence_after();
 #pragma unroll
               for (int ks = 0; ks < 8; ++ks)
-                tc_mma_f16<2>(dst, dq + (((ks >> 2) * kHalf + (ks & 3) * 32) >> 4),
+                tc_mma_f16<CG>(dst, dq + (((ks >> 2) * P::kQHalf + (ks & 3) * 32) >> 4),
                               dk + (((ks >> 2) * kKHalfOffset + (ks & 3) * 32) >> 4), idesc,
                               ks > 0);
-              tc_commit_pair(bar_s_full + 8 * s_buf);
-              tc_commit_pair(bar_k_empty + 8 * s_kslot);
+              commit(bar_s_full + 8 * s_buf);
+              commit(bar_k_empty + 8 * s_kslot);
               ++js;
               if (++s_buf == kNS) {
                 s_buf = 0;
@@ -584,10 +613,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (ok) tc_commit_pair(bar_q_empty + 8 * (k & 1));
+          if (ok) commit(bar_q_empty + 8 * (k & 1));
         }
       } else {
-        const uint32_t idesc_o = instr_desc(1, 256);
+        const uint32_t idesc_o = instr_desc(1, 128 * CG);
         const uint64_t dv0 = smem_desc(sbase + P::kVOff, kHalf, 1024);
         int p_buf = 0, p_phase = 0, p_vslot = 0, p_vphase = 0;
         for (unsigned k = 0; ok; ++k) {
@@ -610,18 +639,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (blocks == 8) {
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                  tc_mma_f16_tmem_a<2>(tmem + kTmemO, ta + (ks >> 2) * 64 + (ks & 3) * 8,
+                  tc_mma_f16_tmem_a<CG>(tmem + kTmemO, ta + (ks >> 2) * 64 + (ks & 3) * 8,
                                        dv + ((ks * kBlockBytes) >> 4), idesc_o,
                                        (jp > 0 || ks > 0) ? 1u : 0u);
               } else {
 #pragma unroll 1
                 for (int ks = 0; ks < blocks; ++ks)
-                  tc_mma_f16_tmem_a<2>(tmem + kTmemO, ta + (ks >> 2) * 64 + (ks & 3) * 8,
+                  tc_mma_f16_tmem_a<CG>(tmem + kTmemO, ta + (ks >> 2) * 64 + (ks & 3) * 8,
                                        dv + ((ks * kBlockBytes) >> 4), idesc_o,
                                        (jp > 0 || ks > 0) ? 1u : 0u);
               }
-              tc_commit_pair(bar_o_done + 8 * p_buf);
-              tc_commit_pair(bar_v_empty + 8 * p_vslot);
+              commit(bar_o_done + 8 * p_buf);
+              commit(bar_v_empty + 8 * p_vslot);
               ++jp;
               if (++p_buf == kNS) {
                 p_buf = 0;
@@ -648,12 +677,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float floor_n = fabsf(floor2) >= kFarScore ? floor_score * sl_pow2 : floor2;
     const uint32_t ocol = tmem + lane_off + kTmemO + hc * 64;
     uint32_t v[64];
-    // (until the first scores are there) which group each sequence is in, for the decode
-    for (int x = static_cast<int>(blockIdx.x) * kSoftmaxWarps + warp; x < a.num_seqs;
-         x += static_cast<int>(gridDim.x) * kSoftmaxWarps) {
-      const int4 g = find_group(a, x, lane);
-      if (lane == 0) a.lay.member[x] = g;
-    }
     int jt = 0;                // tiles, over all items
     int b3 = 0, s_phase = 0;   // score buffer of tile jt and its parity
 
@@ -835,9 +858,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Neither CTA leaves while the other may still report to it.  No data changes
   // hands here, so outputs need not have landed: a release would wait for them
   // (0.6 us).
-  cluster_sync_relaxed();
+  if constexpr (CG == 2)
+    cluster_sync_relaxed();
+  else
+    __syncthreads();
   tc_fence_after();
-  if (warp == 0) tmem_dealloc<2>(tmem, kTmemCols);
+  if (warp == 0) tmem_dealloc<CG>(tmem, kTmemCols);
 }
 
 }  // namespace
@@ -845,12 +871,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 using namespace pre;
 
-cudaError_t launch_shared_prefix(const SharedArgs& args, const CUtensorMap* tm_q,
-                                 const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                 cudaStream_t stream) {
-  SharedArgs a = args;
-  if (a.wait_ns == 0) a.wait_ns = kWaitLimitNs;
-  constexpr int smem = SPlan::kSmemBytes + 1024;
+namespace {
+
+template <int CG, int kQRows>
+cudaError_t launch_workers(const SharedArgs& a, const CUtensorMap* tm_q, const CUtensorMap* tm_k,
+                           const CUtensorMap* tm_v, cudaStream_t stream) {
+  constexpr int smem = SPlan<CG, kQRows>::kSmemBytes + 1024;
+  const auto kernel = shared_prefix_kernel<CG, kQRows>;
   static std::mutex mu;
   static bool set_for[64] = {};
   int dev = 0;
@@ -860,14 +887,16 @@ cudaError_t launch_shared_prefix(const SharedArgs& args, const CUtensorMap* tm_q
   {
     std::lock_guard<std::mutex> lock(mu);
     if (!set_for[dev]) {
-      e = cudaFuncSetAttribute(shared_prefix_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               smem);
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+      if (e != cudaSuccess) return e;
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               cudaSharedmemCarveoutMaxShared);
       if (e != cudaSuccess) return e;
       set_for[dev] = true;
     }
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * static_cast<unsigned>(a.lay.teams * a.lay.team_pairs));
+  cfg.gridDim = dim3(CG * static_cast<unsigned>(a.lay.teams * a.lay.team_workers));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -875,12 +904,114 @@ cudaError_t launch_shared_prefix(const SharedArgs& args, const CUtensorMap* tm_q
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = 2;
+  attr[1].val.clusterDim.x = CG;
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  e = cudaLaunchKernelEx(&cfg, shared_prefix_kernel, *tm_q, *tm_k, *tm_v, a);
+  cfg.numAttrs = CG == 2 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kernel, *tm_q, *tm_k, *tm_v, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_shared_prefix(const SharedArgs& args, const CUtensorMap* tm_q,
+                                 const CUtensorMap* tm_k, const CUtensorMap* tm_v,
+                                 cudaStream_t stream) {
+  SharedArgs a = args;
+  if (a.wait_ns == 0) a.wait_ns = kWaitLimitNs;
+  if (a.lay.worker_ctas == 2) return launch_workers<2, 128>(a, tm_q, tm_k, tm_v, stream);
+  if (a.lay.box_tokens * a.group <= 64) return launch_workers<1, 64>(a, tm_q, tm_k, tm_v, stream);
+  return launch_workers<1, 128>(a, tm_q, tm_k, tm_v, stream);
+}
+
+namespace {
+
+constexpr int kJoinWarps = 8;
+
+// A warp for each (sequence, head): four columns a lane of the own part and of each of
+// the prefix's pieces, weighted by their sums, in the pieces' order.
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    shared_join_kernel(const SharedArgs a, __nv_bfloat16* out, float* out_lse) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= static_cast<int64_t>(a.num_seqs) * a.num_q_heads) return;
+  const int s = static_cast<int>(row / a.num_q_heads);
+  const int head = static_cast<int>(row - static_cast<int64_t>(s) * a.num_q_heads);
+  const int kvh = head / a.group, h = head - kvh * a.group;
+  const SharedLayout& lay = a.lay;
+  const int4 member = lay.member[s];
+  float4 acc = reinterpret_cast<const float4*>(lay.own_o + row * 128)[lane];
+  float2 ml = lay.own_ml[row];
+  if (member.x >= 0) {
+    const int4 info = lay.info[member.x];
+    const int tiles = lay.info[a.num_groups].y;
+    if (info.z > 0) {
+      const int rows = lay.unit_tokens;
+      const int u = member.y / rows;
+      const int t0 = info.y + u * info.z;
+      const int teams = shared_teams(lay, tiles);
+      const int j0 = shared_team(t0, tiles, teams);
+      const int parts = shared_team(t0 + info.z - 1, tiles, teams) - j0 + 1;
+      const int64_t span = static_cast<int64_t>(a.num_kv_heads) * lay.slot_rows;
+      const int64_t part0 =
+          (static_cast<int64_t>(j0 + info.x + u) * a.num_kv_heads + kvh) * lay.slot_rows +
+          (member.y - u * rows) * a.group + h;
+      // (four at a time: their loads are under way together)
+#pragma unroll 1
+      for (int p0 = 0; p0 < parts; p0 += 4) {
+        float2 x[4];
+        float4 y[4];
+        float top = ml.x;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t at = part0 + min(p0 + i, parts - 1) * span;
+          x[i] = lay.part_ml[at];
+          y[i] = reinterpret_cast<const float4*>(lay.part_o + at * 128)[lane];
+          top = fmaxf(top, x[i].x);
+        }
+        const float own = fast_exp2(ml.x - top);
+        acc = make_float4(acc.x * own, acc.y * own, acc.z * own, acc.w * own);
+        ml = make_float2(top, ml.y * own);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (p0 + i >= parts) continue;
+          const float f = fast_exp2(x[i].x - top);
+          acc.x += f * y[i].x;
+          acc.y += f * y[i].y;
+          acc.z += f * y[i].z;
+          acc.w += f * y[i].w;
+          ml.y += f * x[i].y;
+        }
+      }
+    }
+  }
+  const bool none = ml.y == 0.f;
+  uint2 o;
+  o.x = none ? 0u : pack_bf16x2(acc.x / ml.y, acc.y / ml.y);
+  o.y = none ? 0u : pack_bf16x2(acc.z / ml.y, acc.w / ml.y);
+  reinterpret_cast<uint2*>(out + row * 128)[lane] = o;
+  if (lane == 0 && out_lse)
+    out_lse[row] = none ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
+}
+
+}  // namespace
+
+cudaError_t launch_shared_join(const SharedArgs& a, __nv_bfloat16* out, float* out_lse,
+                               cudaStream_t stream) {
+  const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_join_kernel, a, out, out_lse);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

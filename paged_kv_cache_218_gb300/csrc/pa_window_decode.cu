@@ -47,8 +47,9 @@
 // its own that ends with it, and finds its chunk with one more round trip.
 //
 // So does the decode of sequences that share prefixes, for what is each one's own:
-// the blocks behind its group's prefix, joined at the end with the results that
-// pa_shared_prefix.cu left for the prefix.
+// the blocks behind its group's prefix.  It runs beside the prefix pass, whose CTAs leave
+// room for two warps' rings on each SM, and reads nothing of it; a third kernel joins
+// both (pa_shared_prefix.cu).
 #include <float.h>
 #include <math.h>
 
@@ -163,7 +164,9 @@ __global__ void __launch_bounds__(32 * W)
   const int G = a.group;
 
   griddep_launch_dependents();
-  griddep_wait();
+  // (beside the prefix pass: what that waited for before it let this kernel start is
+  // there, and read past L1)
+  if constexpr (M != kShared) griddep_wait();
 
   // q: head g of the group, the columns of this lane's K pieces
   uint4 qf[KJ];
@@ -171,7 +174,8 @@ __global__ void __launch_bounds__(32 * W)
       a.q + (static_cast<int64_t>(s) * a.num_q_heads + kvh * G + (g < G ? g : 0)) * D;
 #pragma unroll
   for (int j = 0; j < KJ; ++j) {
-    qf[j] = *reinterpret_cast<const uint4*>(qrow + 8 * (4 * j + t));
+    const uint4* const at = reinterpret_cast<const uint4*>(qrow + 8 * (4 * j + t));
+    qf[j] = M == kShared ? __ldcg(at) : *at;
     if (g >= G) qf[j] = make_uint4(0, 0, 0, 0);
   }
 
@@ -185,7 +189,7 @@ __global__ void __launch_bounds__(32 * W)
     table_row = find_chunk(a, s, lane, n);
     if (table_row < 0) return;  // (every CTA of the cluster) a row of no chunk stays
   } else {
-    n = a.seq_lens[s];
+    n = M == kShared ? __ldcg(a.seq_lens + s) : a.seq_lens[s];
     const int cap = a.max_blocks * kBlockSize;
     if (n < 0 || n > cap) {
       if (threadIdx.x == 0 && rank == 0 && kvh == 0) atomicOr(a.err, PA_DEVERR_SEQ_LEN);
@@ -194,9 +198,9 @@ __global__ void __launch_bounds__(32 * W)
   }
   int lo = n > a.window ? n - a.window : 0;        // first key of the window
   int ns = a.sinks < n ? a.sinks : n;              // visible sinks
-  int4 member{-1, 0, 0, 0};
   if constexpr (M == kShared) {
-    member = a.shared.lay.member[s];
+    const int4 member = find_group(a.shared, s, lane);
+    if (kvh == 0 && threadIdx.x == 0) a.shared.lay.member[s] = member;
     lo = member.z * kBlockSize;                    // first key of the sequence's own
     ns = 0;
   }
@@ -228,7 +232,7 @@ __global__ void __launch_bounds__(32 * W)
     const int mine = vb + lane * stride;
     ids = 0;
     if (mine < nv) {
-      ids = table[real_block(mine)];
+      ids = M == kShared ? __ldcg(table + real_block(mine)) : table[real_block(mine)];
       if (ids < 0 || ids >= a.num_blocks) {
         atomicOr(a.err, PA_DEVERR_BLOCK_ID);
         ids = -1;  // reads as zeros
@@ -273,29 +277,6 @@ __global__ void __launch_bounds__(32 * W)
   if (first < nv) read_ids(first);
 #pragma unroll
   for (int st = 0; st < kStages; ++st) issue(st);
-
-  // The prefix's results for this sequence: those of its slots, `span` rows apart, from
-  // `part0` on.
-  int parts = 0;
-  int64_t part0 = 0, span = 0;
-  if constexpr (M == kShared) {
-    const SharedLayout& lay = a.shared.lay;
-    if (member.x >= 0) {
-      const int4 info = lay.info[member.x];
-      const int tiles = lay.info[a.shared.num_groups].y;
-      if (info.z > 0) {
-        const int rows = 2 * lay.tile_tokens;
-        const int u = member.y / rows;
-        const int t0 = info.y + u * info.z;
-        const int teams = shared_teams(lay, tiles);
-        const int j0 = shared_team(t0, tiles, teams);
-        parts = shared_team(t0 + info.z - 1, tiles, teams) - j0 + 1;
-        span = static_cast<int64_t>(a.num_kv_heads) * lay.slot_rows;
-        part0 = (static_cast<int64_t>(j0 + info.x + u) * a.num_kv_heads + kvh) * lay.slot_rows +
-                (member.y - u * rows) * G;
-      }
-    }
-  }
 
   int stage = 0;
   for (int vb = first; vb < nv; vb += stride) {
@@ -415,7 +396,7 @@ __global__ void __launch_bounds__(32 * W)
     }
   __syncthreads();
   if constexpr (M == kShared) {
-    // four columns of a head: the CTA's warps, then the prefix's pieces
+    // four columns of a head, left undivided
     for (int e = 4 * threadIdx.x; e < G * D; e += 4 * 32 * W) {
       const int h = e / D, d = e % D;
       float m = kFloor;
@@ -434,83 +415,58 @@ __global__ void __launch_bounds__(32 * W)
       for (int w = 0; w < W; ++w)
         add(fast_exp2(sm_m[w * 8 + h] - m),
             *reinterpret_cast<const float4*>(sm_o + w * kPart + h * D + d), sm_l[w * 8 + h]);
-      const float2* const ml = a.shared.lay.part_ml + part0 + h;
-      const float* const o = a.shared.lay.part_o + (part0 + h) * D + d;
-      // (four at a time: their loads are under way together)
-#pragma unroll 1
-      for (int p0 = 0; p0 < parts; p0 += 4) {
-        float2 x[4];
-        float4 y[4];
-        float top = m;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int p = min(p0 + i, parts - 1);
-          x[i] = ml[p * span];
-          y[i] = *reinterpret_cast<const float4*>(o + p * span * D);
-          top = fmaxf(top, x[i].x);
-        }
-        const float own = fast_exp2(m - top);
-        acc = make_float4(acc.x * own, acc.y * own, acc.z * own, acc.w * own);
-        l *= own;
-        m = top;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (p0 + i < parts) add(fast_exp2(x[i].x - top), y[i], x[i].y);
-      }
       const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + kvh * G + h;
-      const bool none = l == 0.f;
-      uint2 out;
-      out.x = none ? 0u : pack_bf16x2(acc.x / l, acc.y / l);
-      out.y = none ? 0u : pack_bf16x2(acc.z / l, acc.w / l);
-      *reinterpret_cast<uint2*>(a.out + row * D + d) = out;
-      if (d == 0 && a.out_lse) a.out_lse[row] = none ? -INFINITY : (m + log2f(l)) * kLn2;
+      *reinterpret_cast<float4*>(a.shared.lay.own_o + row * D + d) = acc;
+      if (d == 0) a.shared.lay.own_ml[row] = make_float2(m, l);
     }
-    return;
-  }
-  for (int e = threadIdx.x; e < G * D; e += 32 * W) {
-    const int h = e / D, d = e % D;
-    float m = kFloor;
-#pragma unroll
-    for (int w = 0; w < W; ++w) m = fmaxf(m, sm_m[w * 8 + h]);
-    float acc = 0.f, l = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float f = fast_exp2(sm_m[w * 8 + h] - m);
-      acc += f * sm_o[w * kPart + h * D + d];
-      l += f * sm_l[w * 8 + h];
+    // (who waits for this kernel waits for the prefix pass, too)
+    if (blockIdx.x == 0) griddep_wait();
+  } else {
+    for (int e = threadIdx.x; e < G * D; e += 32 * W) {
+      const int h = e / D, d = e % D;
+      float m = kFloor;
+  #pragma unroll
+      for (int w = 0; w < W; ++w) m = fmaxf(m, sm_m[w * 8 + h]);
+      float acc = 0.f, l = 0.f;
+  #pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = fast_exp2(sm_m[w * 8 + h] - m);
+        acc += f * sm_o[w * kPart + h * D + d];
+        l += f * sm_l[w * 8 + h];
+      }
+      if (splits == 1) {
+        const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + kvh * G + h;
+        a.out[row * D + d] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
+        if (d == 0 && a.out_lse) a.out_lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+      } else {
+        cta_o[e] = acc;
+        if (d == 0) {
+          cta_m[h] = m;
+          cta_l[h] = l;
+        }
+      }
     }
-    if (splits == 1) {
+    if (splits == 1) return;
+
+    // ---- join the cluster's CTAs: CTA r writes every splits-th element
+    cluster_sync();
+    const uint32_t ro = smem_u32(cta_o), rm = smem_u32(cta_m), rl = smem_u32(cta_l);
+    for (int e = rank * 32 * W + threadIdx.x; e < G * D; e += splits * 32 * W) {
+      const int h = e / D, d = e % D;
+      float m = kFloor;
+      for (int c = 0; c < splits; ++c) m = fmaxf(m, ld_dsmem(mapa_shared(rm + 4 * h, c)));
+      float acc = 0.f, l = 0.f;
+      for (int c = 0; c < splits; ++c) {
+        const float f = fast_exp2(ld_dsmem(mapa_shared(rm + 4 * h, c)) - m);
+        acc += f * ld_dsmem(mapa_shared(ro + 4 * e, c));
+        l += f * ld_dsmem(mapa_shared(rl + 4 * h, c));
+      }
       const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + kvh * G + h;
       a.out[row * D + d] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
       if (d == 0 && a.out_lse) a.out_lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-    } else {
-      cta_o[e] = acc;
-      if (d == 0) {
-        cta_m[h] = m;
-        cta_l[h] = l;
-      }
     }
+    cluster_sync();  // no CTA leaves while another may still read its shared memory
   }
-  if (splits == 1) return;
-
-  // ---- join the cluster's CTAs: CTA r writes every splits-th element
-  cluster_sync();
-  const uint32_t ro = smem_u32(cta_o), rm = smem_u32(cta_m), rl = smem_u32(cta_l);
-  for (int e = rank * 32 * W + threadIdx.x; e < G * D; e += splits * 32 * W) {
-    const int h = e / D, d = e % D;
-    float m = kFloor;
-    for (int c = 0; c < splits; ++c) m = fmaxf(m, ld_dsmem(mapa_shared(rm + 4 * h, c)));
-    float acc = 0.f, l = 0.f;
-    for (int c = 0; c < splits; ++c) {
-      const float f = fast_exp2(ld_dsmem(mapa_shared(rm + 4 * h, c)) - m);
-      acc += f * ld_dsmem(mapa_shared(ro + 4 * e, c));
-      l += f * ld_dsmem(mapa_shared(rl + 4 * h, c));
-    }
-    const int64_t row = static_cast<int64_t>(s) * a.num_q_heads + kvh * G + h;
-    a.out[row * D + d] = __float2bfloat16(l == 0.f ? 0.f : acc / l);
-    if (d == 0 && a.out_lse) a.out_lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-  }
-  cluster_sync();  // no CTA leaves while another may still read its shared memory
 }
 
 template <int D, int W, int M>
@@ -528,6 +484,14 @@ cudaError_t launch(const typename KindArgs<M>::type& a, cudaStream_t stream) {
                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                DecodePlan<D, W, M>::kBytes);
       if (e != cudaSuccess) return e;
+      if (M == kShared) {
+        // (an SM keeps its split of memory while a CTA runs: the prefix pass's, so that
+        // CTAs of both share SMs)
+        e = cudaFuncSetAttribute(decode_window_kernel<D, W, M>,
+                                 cudaFuncAttributePreferredSharedMemoryCarveout,
+                                 cudaSharedmemCarveoutMaxShared);
+        if (e != cudaSuccess) return e;
+      }
       set_for[dev] = true;
     }
   }

@@ -127,14 +127,28 @@ def test_prefix_and_group_sizes(pa, prefix, members):
     c.check()
 
 
-@pytest.mark.parametrize("members", [31, 32, 63, 64, 65, 129, 200])
+@pytest.mark.parametrize("members", [16, 17, 31, 32, 33, 63, 64, 65, 129, 200])
 def test_groups_past_a_tile_and_a_pair(pa, members):
-    """32 members of four heads fill a query tile, 64 a pair's two."""
+    """32 members of four heads fill a query tile, 64 a pair's two (16 and fewer leave half
+    a tile free)."""
     rng = np.random.default_rng(members)
     c = Case(members, [(11, lengths(rng, members, 11, 30))], 8, 2)
     c.run(pa)
-    c.check(rows=sorted({0, 1, 30, members - 1, members // 2, min(31, members - 1),
-                         min(32, members - 1), min(63, members - 1), min(64, members - 1)}))
+    c.check(rows=sorted({0, 1, min(30, members - 1), members - 1, members // 2,
+                         min(31, members - 1), min(32, members - 1), min(63, members - 1), min(64, members - 1)}))
+
+
+@pytest.mark.parametrize("G,members", [(1, 128), (1, 129), (3, 21), (3, 42), (3, 50), (5, 12),
+                                       (5, 13), (5, 26), (6, 60), (7, 9), (7, 18), (7, 40)])
+def test_tiles_that_heads_do_not_fill(pa, G, members):
+    """floor(128 / G) members to a tile, with rows to spare; several items for a worker."""
+    rng = np.random.default_rng(100 * G + members)
+    groups = [(p, lengths(rng, members, p, 20)) for p in (3, 12, 20)]
+    c = Case(G, groups, 2 * G, 2)
+    c.run(pa)
+    n = 3 * members
+    c.check(rows=sorted({0, 1, members - 1, members, 128 // G - 1, min(128 // G, n - 1),
+                         min(2 * (128 // G), n - 1), n - 1}))
 
 
 @pytest.mark.parametrize("groups", [[(9, [150, 160, 144])], [(3, [0, 20, 48, 49]), (0, [70]), (5, [])],
