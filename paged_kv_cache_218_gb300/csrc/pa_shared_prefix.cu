@@ -42,13 +42,17 @@ constexpr uint64_t kSettleNs = 1000000;  // far longer than any copy takes
 constexpr float kFloor = -0x1.fffff0p127f;
 constexpr float kFarScore = 0x1p31f;  // (log2 units)
 
-// Shared memory of one CTA: Q tiles of two items, K and V tiles (a pair's CTAs hold half
-// of each), block ids of both loaders, the softmax's exchange, barriers.  An operand tile
-// has 128 rows; the second Q tile lies kQRows behind the first, whose other rows no member
-// has.  (What is left of an SM holds CTAs of the decode of the sequences' own parts.)
+// Shared memory of one CTA: Q tiles, K and V tiles (a pair's CTAs hold half of each), block
+// ids of both loaders, the softmax's exchange, barriers.  Small groups (kQRows > 0: at most
+// so many query rows), of which a worker has many short items, have the next item's Q
+// tile beside; an operand tile has 128 rows, and the second one lies kQRows behind the
+// first, whose other rows no member has.  Otherwise an item's Q waits for the scores of
+// the one before.  (What is left of an SM holds CTAs of the decode of the sequences' own
+// parts.)
 template <int CG, int kQRows>
 struct SPlan {
-  static constexpr int kNK = CG == 2 ? 3 : 2, kNV = CG == 2 ? 4 : 2;
+  static constexpr int kNQ = kQRows > 0 ? 2 : 1;
+  static constexpr int kNK = 2, kNV = CG == 2 ? 3 : 2;
   static constexpr int kKSlot = 2 * kHalf / CG, kVSlot = 2 * kHalf / CG;
   static constexpr int kQNext = kQRows * 128;           // to the next Q tile
   static constexpr int kQHalf = kQNext + kHalf;         // to the other 64 columns
@@ -250,13 +254,15 @@ __device__ __forceinline__ void stg32(float* p, const uint32_t* x) {
 }
 
 // CG: CTAs of a worker.  Two of them (a tcgen05 pair) take 256 query rows, one 128.
+// (The bound of 512 threads is one of 128 registers: three warps of this kernel on a
+// quarter of an SM then leave room for one of the decode's beside it.)
 template <int CG, int kQRows>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(512, 1)
     shared_prefix_kernel(const __grid_constant__ CUtensorMap tm_q,
                           const __grid_constant__ CUtensorMap tm_k,
                           const __grid_constant__ CUtensorMap tm_v, const SharedArgs a) {
   using P = SPlan<CG, kQRows>;
-  constexpr int kNK = P::kNK, kNV = P::kNV;
+  constexpr int kNK = P::kNK, kNV = P::kNV, kNQ = P::kNQ;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -408,9 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           it = next;
           jf = kIdBatch;
           jk = 0;
-          const unsigned qb = qi & 1;
-          if (qi >= 2 &&
-              !wait_warp(bar_q_empty + 8 * qb, ((qi >> 1) - 1) & 1, abort_flag, a))
+          const unsigned qb = qi % kNQ;
+          if (qi >= kNQ &&
+              !wait_warp(bar_q_empty + 8 * qb, ((qi / kNQ) - 1) & 1, abort_flag, a))
             break;
           lead = qi == 0 ? min(it.nkt, kNK) : 0;
           ++qi;
@@ -454,8 +460,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // every load's slot has been released, and so has landed, before exit
       if (lane == 0) {
-        for (unsigned b = 0; b < 2 && b < qi; ++b)
-          wait(bar_q_empty + 8 * b, ((qi - 1 - b) >> 1) & 1, abort_flag, a);
+        for (unsigned b = 0; b < kNQ && b < qi; ++b)
+          wait(bar_q_empty + 8 * b, ((qi - 1 - b) / kNQ) & 1, abort_flag, a);
         for (unsigned sl = 0; sl < kNK && sl < total; ++sl)
           wait(bar_k_empty + 8 * sl, ((total - 1 - sl) / kNK) & 1, abort_flag, a);
       }
@@ -583,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int nkt = ok ? ring_item(k)->nkt : 0;
           if (nkt == 0) break;
           const int nvb = ring_item(k)->nvb;
-          const uint64_t dq = dq0 + static_cast<uint64_t>(((k & 1) * P::kQNext) >> 4);
-          ok = wait(bar_q + 8 * (k & 1), (k >> 1) & 1, abort_flag, a);
+          const uint64_t dq = dq0 + static_cast<uint64_t>(((k % kNQ) * P::kQNext) >> 4);
+          ok = wait(bar_q + 8 * (k % kNQ), (k / kNQ) & 1, abort_flag, a);
           int js = 0;
           while (ok && js < nkt) {
             const uint64_t dk = dk0 + static_cast<uint64_t>((s_kslot * P::kKSlot) >> 4);
@@ -613,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
           }
-          if (ok) commit(bar_q_empty + 8 * (k & 1));
+          if (ok) commit(bar_q_empty + 8 * (k % kNQ));
         }
       } else {
         const uint32_t idesc_o = instr_desc(1, 128 * CG);
@@ -920,90 +926,122 @@ cudaError_t launch_shared_prefix(const SharedArgs& args, const CUtensorMap* tm_q
                                  cudaStream_t stream) {
   SharedArgs a = args;
   if (a.wait_ns == 0) a.wait_ns = kWaitLimitNs;
-  if (a.lay.worker_ctas == 2) return launch_workers<2, 128>(a, tm_q, tm_k, tm_v, stream);
+  if (a.lay.worker_ctas == 2) return launch_workers<2, 0>(a, tm_q, tm_k, tm_v, stream);
   if (a.lay.box_tokens * a.group <= 64) return launch_workers<1, 64>(a, tm_q, tm_k, tm_v, stream);
-  return launch_workers<1, 128>(a, tm_q, tm_k, tm_v, stream);
+  return launch_workers<1, 0>(a, tm_q, tm_k, tm_v, stream);
 }
 
 namespace {
 
 constexpr int kJoinWarps = 8;
 
-// A warp for each (sequence, head): four columns a lane of the own part and of each of
-// the prefix's pieces, weighted by their sums, in the pieces' order.
-__global__ void __launch_bounds__(32 * kJoinWarps)
+// What a warp has of a row: four columns a lane, the maximum and the sum.
+struct Joined {
+  float4 o;
+  float m, l;
+  __device__ __forceinline__ void move(float top) {
+    const float f = fast_exp2(m - top);
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+    l *= f;
+    m = top;
+  }
+  __device__ __forceinline__ void add(float4 x, float2 ml) {  // (m is not below ml.x)
+    const float f = fast_exp2(ml.x - m);
+    o.x += f * x.x;
+    o.y += f * x.y;
+    o.z += f * x.z;
+    o.w += f * x.w;
+    l += f * ml.y;
+  }
+};
+
+// kRowWarps warps for each (sequence, head): the own part and the prefix's pieces,
+// weighted by their sums, always in the same order.
+template <int kRowWarps>
+__global__ void __launch_bounds__(32 * kJoinWarps, 7)
     shared_join_kernel(const SharedArgs a, __nv_bfloat16* out, float* out_lse) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= static_cast<int64_t>(a.num_seqs) * a.num_q_heads) return;
+  constexpr int kRows = kJoinWarps / kRowWarps;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part_of = warp % kRowWarps;
+  const int64_t all = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
+  const int64_t at = static_cast<int64_t>(blockIdx.x) * kRows + warp / kRowWarps;
+  const int64_t row = at < all ? at : all - 1;
   const int s = static_cast<int>(row / a.num_q_heads);
   const int head = static_cast<int>(row - static_cast<int64_t>(s) * a.num_q_heads);
   const int kvh = head / a.group, h = head - kvh * a.group;
   const SharedLayout& lay = a.lay;
+  griddep_launch_dependents();
+  griddep_wait();
   const int4 member = lay.member[s];
-  float4 acc = reinterpret_cast<const float4*>(lay.own_o + row * 128)[lane];
-  float2 ml = lay.own_ml[row];
-  if (member.x >= 0) {
-    const int4 info = lay.info[member.x];
-    const int tiles = lay.info[a.num_groups].y;
-    if (info.z > 0) {
-      const int rows = lay.unit_tokens;
-      const int u = member.y / rows;
-      const int t0 = info.y + u * info.z;
-      const int teams = shared_teams(lay, tiles);
-      const int j0 = shared_team(t0, tiles, teams);
-      const int parts = shared_team(t0 + info.z - 1, tiles, teams) - j0 + 1;
-      const int64_t span = static_cast<int64_t>(a.num_kv_heads) * lay.slot_rows;
-      const int64_t part0 =
-          (static_cast<int64_t>(j0 + info.x + u) * a.num_kv_heads + kvh) * lay.slot_rows +
-          (member.y - u * rows) * a.group + h;
-      // (four at a time: their loads are under way together)
+  const int4 info = lay.info[max(member.x, 0)];  // (of any group where there is none)
+  const int tiles = lay.info[a.num_groups].y;
+  Joined x{make_float4(0.f, 0.f, 0.f, 0.f), kFloor, 0.f};
+  if (part_of == 0) {
+    x.o = reinterpret_cast<const float4*>(lay.own_o + row * 128)[lane];
+    const float2 ml = lay.own_ml[row];
+    x.m = ml.x;
+    x.l = ml.y;
+  }
+  if (member.x >= 0 && info.z > 0) {
+    const int rows = lay.unit_tokens;
+    const int u = member.y / rows;
+    const int t0 = info.y + u * info.z;
+    const int teams = shared_teams(lay, tiles);
+    const int j0 = shared_team(t0, tiles, teams);
+    const int parts = shared_team(t0 + info.z - 1, tiles, teams) - j0 + 1;
+    const int64_t span = static_cast<int64_t>(a.num_kv_heads) * lay.slot_rows;
+    const int64_t first =
+        (static_cast<int64_t>(j0 + info.x + u) * a.num_kv_heads + kvh) * lay.slot_rows +
+        (member.y - u * rows) * a.group + h;
+    // (a few at a time: their loads are under way together)
+    constexpr int kAhead = 2;
 #pragma unroll 1
-      for (int p0 = 0; p0 < parts; p0 += 4) {
-        float2 x[4];
-        float4 y[4];
-        float top = ml.x;
+    for (int p0 = part_of; p0 < parts; p0 += kAhead * kRowWarps) {
+      float2 ml[kAhead];
+      float4 o[kAhead];
+      float top = x.m;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int64_t at = part0 + min(p0 + i, parts - 1) * span;
-          x[i] = lay.part_ml[at];
-          y[i] = reinterpret_cast<const float4*>(lay.part_o + at * 128)[lane];
-          top = fmaxf(top, x[i].x);
-        }
-        const float own = fast_exp2(ml.x - top);
-        acc = make_float4(acc.x * own, acc.y * own, acc.z * own, acc.w * own);
-        ml = make_float2(top, ml.y * own);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (p0 + i >= parts) continue;
-          const float f = fast_exp2(x[i].x - top);
-          acc.x += f * y[i].x;
-          acc.y += f * y[i].y;
-          acc.z += f * y[i].z;
-          acc.w += f * y[i].w;
-          ml.y += f * x[i].y;
-        }
+      for (int i = 0; i < kAhead; ++i) {
+        const int64_t r = first + min(p0 + i * kRowWarps, parts - 1) * span;
+        ml[i] = lay.part_ml[r];
+        o[i] = reinterpret_cast<const float4*>(lay.part_o + r * 128)[lane];
+        top = fmaxf(top, ml[i].x);
       }
+      x.move(top);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (p0 + i * kRowWarps < parts) x.add(o[i], ml[i]);
     }
   }
-  const bool none = ml.y == 0.f;
+  if constexpr (kRowWarps > 1) {
+    __shared__ float4 others[kJoinWarps][32];
+    __shared__ float2 others_ml[kJoinWarps];
+    others[warp][lane] = x.o;
+    if (lane == 0) others_ml[warp] = make_float2(x.m, x.l);
+    __syncthreads();
+    if (part_of != 0) return;
+    float top = x.m;
+#pragma unroll
+    for (int i = 1; i < kRowWarps; ++i) top = fmaxf(top, others_ml[warp + i].x);
+    x.move(top);
+#pragma unroll
+    for (int i = 1; i < kRowWarps; ++i) x.add(others[warp + i][lane], others_ml[warp + i]);
+  }
+  if (at >= all) return;
+  const bool none = x.l == 0.f;
   uint2 o;
-  o.x = none ? 0u : pack_bf16x2(acc.x / ml.y, acc.y / ml.y);
-  o.y = none ? 0u : pack_bf16x2(acc.z / ml.y, acc.w / ml.y);
+  o.x = none ? 0u : pack_bf16x2(x.o.x / x.l, x.o.y / x.l);
+  o.y = none ? 0u : pack_bf16x2(x.o.z / x.l, x.o.w / x.l);
   reinterpret_cast<uint2*>(out + row * 128)[lane] = o;
-  if (lane == 0 && out_lse)
-    out_lse[row] = none ? -INFINITY : (ml.x + log2f(ml.y)) * kLn2;
+  if (lane == 0 && out_lse) out_lse[row] = none ? -INFINITY : (x.m + log2f(x.l)) * kLn2;
 }
 
-}  // namespace
-
-cudaError_t launch_shared_join(const SharedArgs& a, __nv_bfloat16* out, float* out_lse,
-                               cudaStream_t stream) {
+template <int kRowWarps>
+cudaError_t launch_join(const SharedArgs& a, __nv_bfloat16* out, float* out_lse,
+                        cudaStream_t stream) {
+  constexpr int kRows = kJoinWarps / kRowWarps;
   const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kRows - 1) / kRows));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1011,8 +1049,18 @@ cudaError_t launch_shared_join(const SharedArgs& a, __nv_bfloat16* out, float* o
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_join_kernel, a, out, out_lse);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, shared_join_kernel<kRowWarps>, a, out, out_lse);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_shared_join(const SharedArgs& a, __nv_bfloat16* out, float* out_lse,
+                               cudaStream_t stream) {
+  // Few rows behind a long prefix have a piece from every team: four warps on each.
+  const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
+  return rows <= 2048 ? launch_join<4>(a, out, out_lse, stream)
+                      : launch_join<1>(a, out, out_lse, stream);
 }
 
 }  // namespace pa

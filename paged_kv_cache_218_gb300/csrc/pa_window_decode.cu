@@ -81,13 +81,12 @@ __device__ __forceinline__ float bf16_round(float x) {
   return __bfloat162float(__float2bfloat16(x));
 }
 
-// Blocks in flight per warp; two where a warp has a unit to itself behind a shared prefix,
-// so that thirteen of them and not nine run on an SM: as many bytes on their way, and
-// fewer rounds of a unit's latency.
+// Blocks in flight per warp; two where two warps have a unit behind a shared prefix, so
+// that both fit beside the prefix pass.
 template <int W, int M>
 constexpr int kStages = 3;
 template <>
-constexpr int kStages<1, 2> = 2;
+constexpr int kStages<2, 2> = 2;
 
 // Shared memory: the warps' rings [W][kStages][K, V][16 rows][D]; once a warp
 // has read its last block its outputs [8 heads][D] (fp32) take the front of its
@@ -137,8 +136,10 @@ struct KindArgs<kShared> {
   using type = SharedDecodeArgs;
 };
 
+// (Behind a shared prefix at most 128 registers: what three warps of the prefix pass leave
+// of a quarter of an SM.)
 template <int D, int W, int M>
-__global__ void __launch_bounds__(32 * W)
+__global__ void __launch_bounds__(32 * W, M == kShared ? 16 / W : 0)
     decode_window_kernel(const typename KindArgs<M>::type a) {
   constexpr bool C = M == kChunks;
   using P = DecodePlan<D, W, M>;
@@ -619,10 +620,10 @@ cudaError_t choose(WindowDecodeArgs a, int num_sms, cudaStream_t stream) {
     }
   }
   switch (w) {
-    case 1: return launch<D, 1, M>(a, stream);
-    case 2: return launch<D, 2, M>(a, stream);
-    case 4: return launch<D, 4, M>(a, stream);
-    default: return launch<D, 8, M>(a, stream);
+    case 1: return launch<D, 1, kSequences>(a, stream);
+    case 2: return launch<D, 2, kSequences>(a, stream);
+    case 4: return launch<D, 4, kSequences>(a, stream);
+    default: return launch<D, 8, kSequences>(a, stream);
   }
 }
 
@@ -642,14 +643,12 @@ cudaError_t launch_decode_window(const WindowDecodeArgs& a, int head_dim, int nu
 cudaError_t launch_shared_decode(const SharedDecodeArgs& args, int num_sms, cudaStream_t stream) {
   SharedDecodeArgs a = args;
   a.splits = 1;
-  // How long a sequence's own part is, the host does not know.  As many warps on each as
-  // run at once, nine or more on an SM: more would only come in rounds, which cost a unit's
-  // latency each.
+  // How long a sequence's own part is, the host does not know.  Eight warps on each up to
+  // one on every SM; above, as many as run at once, and few enough to start beside the
+  // prefix pass.
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
-  const int64_t warps = 9ll * num_sms / units;
-  if (warps >= 8) return launch<128, 8, kShared>(a, stream);
-  if (warps >= 4) return launch<128, 4, kShared>(a, stream);
-  if (warps >= 2) return launch<128, 2, kShared>(a, stream);
+  if (units <= num_sms) return launch<128, 8, kShared>(a, stream);
+  if (units <= 6 * num_sms) return launch<128, 2, kShared>(a, stream);
   return launch<128, 1, kShared>(a, stream);
 }
 
