@@ -46,7 +46,6 @@ namespace {
 constexpr int kWarps = 16;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kVecs = 2;       // 32-byte vectors of a lane in a warp load
-constexpr int kAhead = 2;      // warp loads under way
 constexpr float kMove = 5.5f;  // a lane's reference moves when passed by this much
 constexpr int kMaxCtas = 16;   // of a cluster
 constexpr int kMaxEntries = 8192;  // block maxima of a request
@@ -392,25 +391,45 @@ struct Choice {
   __device__ __forceinline__ uint64_t entry_key(int e) const {
     return value_key(sm.base[beam_of(a, e)], block_max[e]);
   }
+  // The lane's elements of load number `part` of block e, a live beam w's.
+  __device__ __forceinline__ int fetch(const Row<T>& row, int w, int e, int part, int lane,
+                                       uint32_t (&v)[kVecs][8]) const {
+    const int t = ((e - w * a.blocks_per_row) << a.block_shift) + part;
+    const int e0 = t * Row<T>::kLoad + lane * E::kVec - row.lead;
+    if (t >= row.first() && t < row.last(a.vocab))
+      load_whole(row.p + e0, v);
+    else
+      load_edge(row.p, a.vocab, e0, sm.edges[threadIdx.x], v);
+    return e0;
+  }
+  // Best value among them, in fp32.
+  __device__ __forceinline__ float best_of(int e, int part, int lane) const {
+    const int w = beam_of(a, e);
+    if ((ended >> w) & 1) return lane == 0 && part == 0 ? sm.base[w].x : -INFINITY;
+    uint32_t v[kVecs][8];
+    fetch(Row<T>(a, r, w), w, e, part, lane, v);
+    float best = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kVecs * E::kVec / 2; ++i) {
+      const float2 x = E::pair(v[i / (E::kVec / 2)], i % (E::kVec / 2));
+      best = fmaxf(best, fmaxf(sane(x.x), sane(x.y)));
+    }
+    return sm.base[w].x + best;
+  }
   // Load number `part` of block e: f(key, index) for the candidates that may reach the
   // bound, the whole warp together (key 0: this lane has none).
   template <typename F>
   __device__ __forceinline__ void scan(int e, int part, int lane, F f) const {
-    const int V = a.vocab, w = beam_of(a, e);
+    const int w = beam_of(a, e);
     const float2 base = sm.base[w];
-    const uint32_t index0 = static_cast<uint32_t>(w) * V;
+    const uint32_t index0 = static_cast<uint32_t>(w) * a.vocab;
     if ((ended >> w) & 1) {
       f(lane == 0 && part == 0 ? value_key(base, 0.f) : 0, index0 + a.end_token);
       return;
     }
     const Row<T> row(a, r, w);
-    const int t = ((e - w * a.blocks_per_row) << a.block_shift) + part;
-    const int e0 = t * Row<T>::kLoad + lane * E::kVec - row.lead;
     uint32_t v[kVecs][8];
-    if (t >= row.first() && t < row.last(V))
-      load_whole(row.p + e0, v);
-    else
-      load_edge(row.p, V, e0, sm.edges[threadIdx.x], v);
+    const int e0 = fetch(row, w, e, part, lane, v);
     unsigned hits = 0;
     const float least = fmaxf((bound - base.x) - slack, -FLT_MAX);
 #pragma unroll
@@ -437,6 +456,40 @@ struct Choice {
     if (w0 != w1 && (both & ~exact)) atomicOr(&sm.doubtful, both);
   }
 };
+
+// The n-th best of 128 groups' best values, of which each thread brings a share of group
+// threadIdx.x % 128's, rounded down; -inf where fewer groups have one.  Called by the
+// whole CTA.
+template <int KL>
+__device__ __noinline__ float group_bound(SelectSmem<KL>& sm, float best, int n) {
+  constexpr int kQuarter = kGroups / 4;
+  static_assert(kThreads / kGroups == 4, "a thread for each quarter");
+  sm.group[threadIdx.x / kGroups][threadIdx.x % kGroups] = best;
+  if (threadIdx.x == 0) sm.bound = -INFINITY;
+  __syncthreads();
+  if (threadIdx.x < kGroups) {
+#pragma unroll
+    for (int i = 1; i < 4; ++i) best = fmaxf(best, sm.group[i][threadIdx.x]);
+    // (the last bits tell equal groups apart)
+    sm.group_key[threadIdx.x / kQuarter][threadIdx.x % kQuarter] =
+        best > -INFINITY ? (ordered(best) & ~(kGroups - 1u)) | threadIdx.x : threadIdx.x;
+  }
+  __syncthreads();
+  // thread 4 g + h: how many of quarter h come before group g
+  const int g = threadIdx.x >> 2, h = threadIdx.x & 3;
+  const uint32_t mine = sm.group_key[g / kQuarter][g % kQuarter];
+  int place = 0;
+#pragma unroll 2
+  for (int i = 0; i < kQuarter; i += 4) {
+    const uint4 o = *reinterpret_cast<const uint4*>(&sm.group_key[h][i]);
+    place += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+  }
+  place += __shfl_xor_sync(0xffffffffu, place, 1);
+  place += __shfl_xor_sync(0xffffffffu, place, 2);
+  if (place == n - 1 && h == 0 && mine >= kGroups) sm.bound = unordered(mine & ~(kGroups - 1u));
+  __syncthreads();
+  return sm.bound;
+}
 
 // The K + 1 best by sorted lists: first the blocks, then of these the candidates; and which
 // rows' order is in doubt.  Called by the whole CTA.
@@ -600,14 +653,14 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
       whole1 = x.last(V);
     };
     begin();
-    uint32_t v[kAhead][kVecs][8];
-    auto fetch = [&](uint32_t (&to)[kVecs][8]) {
+    uint32_t v[kVecs][8];
+    auto fetch = [&]() {
       if (get >= whole0 && get < whole1) {
-        load_whole(row + static_cast<int64_t>(get) * Row<T>::kLoad, to);
+        load_whole(row + static_cast<int64_t>(get) * Row<T>::kLoad, v);
       } else {
         const Row<T> x(a, r, __ffs(get_rows) - 1);
         load_edge(x.p, V, get * Row<T>::kLoad + lane * E::kVec - x.lead, sm.edges[threadIdx.x],
-                  to);
+                  v);
       }
       --left;
       if (++get == t1 && left > 0) {
@@ -618,70 +671,64 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
     };
     unsigned use_rows = get_rows;
     int use = get, todo = left;
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (left > 0) fetch(v[u]);
+    fetch();
     // sum of 2^((x - ref) log2 e) of the lane's elements of this row; ref is finite, and
     // at most kMove below the largest
     float ref = -FLT_MAX, sum = 0.f, block = -INFINITY;
     while (todo > 0) {
+      float mx, more;
+      bool clean = false;
+      while (true) {
+        mx = E::max(v[0]);
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        if (todo == 0) break;
-        float mx, more;
-        bool clean = false;
-        while (true) {
-          mx = E::max(v[u][0]);
-#pragma unroll
-          for (int c = 1; c < kVecs; ++c) mx = fmaxf(mx, E::max(v[u][c]));
-          if (mx > ref + kMove && mx < INFINITY) {
-            sum *= fast_exp2((ref - mx) * kLog2e);
-            ref = mx;
-          }
-          const uint64_t nref = f32x2(-ref, -ref), scale = f32x2(kLog2e, kLog2e);
-          uint64_t sums[2] = {0, 0};
-#pragma unroll
-          for (int i = 0; i < kVecs * E::kVec / 2; ++i) {
-            const float2 x = E::pair(v[u][i / (E::kVec / 2)], i % (E::kVec / 2));
-            const float2 d = f32x2_parts(mul2(add2(f32x2(x.x, x.y), nref), scale));
-            sums[i & 1] = add2(sums[i & 1], f32x2(fast_exp2(d.x), fast_exp2(d.y)));
-          }
-          const float2 two = f32x2_parts(add2(sums[0], sums[1]));
-          more = two.x + two.y;
-          if (clean || (mx < INFINITY && more == more)) break;
-          // NaN or +inf among them: once more without
-          clean = true;
-          uint4* const edges = sm.edges[threadIdx.x];
-#pragma unroll
-          for (int c = 0; c < kVecs; ++c) {
-            uint32_t (&x)[8] = v[u][c];
-            edges[0] = make_uint4(x[0], x[1], x[2], x[3]);
-            edges[1] = make_uint4(x[4], x[5], x[6], x[7]);
-            clean_vector<T>(edges);
-            unpack(edges, x);
-          }
+        for (int c = 1; c < kVecs; ++c) mx = fmaxf(mx, E::max(v[c]));
+        if (mx > ref + kMove && mx < INFINITY) {
+          sum *= fast_exp2((ref - mx) * kLog2e);
+          ref = mx;
         }
-        if (left > 0) fetch(v[u]);
-        sum += more;
-        --todo;
-        __syncwarp();
-        block = fmaxf(block, warp_max(mx));
-        const int w = __ffs(use_rows) - 1;
-        if ((use & part_mask) == part_mask) {
-          if (lane == 0) st_remote(remote_max + 4 * (w * NB + (use >> sh)), block);
-          block = -INFINITY;
-        }
-        if (++use == t1 || todo == 0) {  // the warp's share of this row is done
-          const float top = warp_max(ref);
-          sum *= fast_exp2((ref - top) * kLog2e);
+        const uint64_t nref = f32x2(-ref, -ref), scale = f32x2(kLog2e, kLog2e);
+        uint64_t sums[2] = {0, 0};
 #pragma unroll
-          for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-          if (lane == 0) sm.red[w][warp] = make_float2(top, sum);
-          ref = -FLT_MAX;
-          sum = 0.f;
-          use = t0;
-          use_rows &= use_rows - 1;
+        for (int i = 0; i < kVecs * E::kVec / 2; ++i) {
+          const float2 x = E::pair(v[i / (E::kVec / 2)], i % (E::kVec / 2));
+          const float2 d = f32x2_parts(mul2(add2(f32x2(x.x, x.y), nref), scale));
+          sums[i & 1] = add2(sums[i & 1], f32x2(fast_exp2(d.x), fast_exp2(d.y)));
         }
+        const float2 two = f32x2_parts(add2(sums[0], sums[1]));
+        more = two.x + two.y;
+        if (clean || (mx < INFINITY && more == more)) break;
+        // NaN or +inf among them: once more without
+        clean = true;
+        uint4* const edges = sm.edges[threadIdx.x];
+#pragma unroll
+        for (int c = 0; c < kVecs; ++c) {
+          uint32_t (&x)[8] = v[c];
+          edges[0] = make_uint4(x[0], x[1], x[2], x[3]);
+          edges[1] = make_uint4(x[4], x[5], x[6], x[7]);
+          clean_vector<T>(edges);
+          unpack(edges, x);
+        }
+      }
+      if (left > 0) fetch();  // (the next one: this one's elements are used up)
+      sum += more;
+      --todo;
+      __syncwarp();
+      block = fmaxf(block, warp_max(mx));
+      const int w = __ffs(use_rows) - 1;
+      if ((use & part_mask) == part_mask) {
+        if (lane == 0) st_remote(remote_max + 4 * (w * NB + (use >> sh)), block);
+        block = -INFINITY;
+      }
+      if (++use == t1 || todo == 0) {  // the warp's share of this row is done
+        const float top = warp_max(ref);
+        sum *= fast_exp2((ref - top) * kLog2e);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (lane == 0) sm.red[w][warp] = make_float2(top, sum);
+        ref = -FLT_MAX;
+        sum = 0.f;
+        use = t0;
+        use_rows &= use_rows - 1;
       }
     }
   }
@@ -742,42 +789,18 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
     if (threadIdx.x == 0) {
       sm.blocks = sm.picked = sm.found = 0;
       sm.doubtful = 0;
-      sm.bound = -INFINITY;
     }
     float best = -INFINITY;
     each_entry([&](int, float v) { best = fmaxf(best, v); });
-    sm.group[threadIdx.x / kGroups][threadIdx.x % kGroups] = best;
-    __syncthreads();
-    constexpr int kQuarter = kGroups / 4;
-    static_assert(kThreads / kGroups == 4, "a thread for each quarter");
-    if (threadIdx.x < kGroups) {
-#pragma unroll
-      for (int i = 1; i < 4; ++i) best = fmaxf(best, sm.group[i][threadIdx.x]);
-      // (the last bits tell equal groups apart; the value is rounded down)
-      sm.group_key[threadIdx.x / kQuarter][threadIdx.x % kQuarter] =
-          best > -INFINITY ? (ordered(best) & ~(kGroups - 1u)) | threadIdx.x : threadIdx.x;
-    }
-    __syncthreads();
-    {
-      // thread 4 g + h: how many of quarter h come before group g
-      const int g = threadIdx.x >> 2, h = threadIdx.x & 3;
-      const uint32_t mine = sm.group_key[g / kQuarter][g % kQuarter];
-      int place = 0;
-#pragma unroll 2
-      for (int i = 0; i < kQuarter; i += 4) {
-        const uint4 o = *reinterpret_cast<const uint4*>(&sm.group_key[h][i]);
-        place += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
-      }
-      place += __shfl_xor_sync(0xffffffffu, place, 1);
-      place += __shfl_xor_sync(0xffffffffu, place, 2);
-      if (place == L - 1 && h == 0 && mine >= kGroups)
-        sm.bound = unordered(mine & ~(kGroups - 1u));
-    }
+    float least = group_bound(sm, best, L);
     float far = lane < W ? fabsf(sm.base[lane].x) : 0.f;
     far = warp_max(far < INFINITY ? far : 0.f);
-    __syncthreads();
-    c.slack = (fabsf(sm.bound) + far) * 0x1p-20f + 2 * a.margin;
-    c.bound = sm.bound > -INFINITY ? sm.bound - c.slack : -FLT_MAX;
+    auto set_bound = [&]() {
+      c.slack = (fabsf(least) + far) * 0x1p-20f + 2 * a.margin;
+      c.bound = least > -INFINITY ? least - c.slack : -FLT_MAX;
+      if (least == -INFINITY) c.slack = INFINITY;
+    };
+    set_bound();
     // ---- the blocks that reach it, and of them the candidates
     each_entry([&](int e, float v) {
       if (v >= c.bound) {
@@ -788,6 +811,15 @@ __global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSele
     __syncthreads();
     const int blocks = sm.blocks;
     if (blocks <= kMaxPicked) {
+      if (least == -INFINITY) {
+        // (too few blocks for a bound: that of lanes' best candidates)
+        best = -INFINITY;
+#pragma unroll 1
+        for (int t = warp; t < blocks << sh; t += kWarps)
+          best = fmaxf(best, c.best_of(sm.pick.block[t >> sh], t & ((1 << sh) - 1), lane));
+        least = group_bound(sm, best, L);
+        set_bound();
+      }
 #pragma unroll 1
       for (int t = warp; t < blocks << sh; t += kWarps)
         c.scan(sm.pick.block[t >> sh], t & ((1 << sh) - 1), lane, [&](uint64_t k, uint32_t i) {
