@@ -597,8 +597,11 @@ __device__ __noinline__ void sum_again(const Choice<T, KL>& c, unsigned rows, fl
   }
 }
 
+// (__grid_constant__: the arguments' address goes to functions out of line, and a copy of
+// them in local memory cost a fifth of the time.)
 template <typename T, int KL>
-__global__ void __launch_bounds__(kThreads, 2) beam_select_kernel(const BeamSelectArgs a) {
+__global__ void __launch_bounds__(kThreads, 2)
+    beam_select_kernel(const __grid_constant__ BeamSelectArgs a) {
   using E = Elem<T>;
   extern __shared__ float block_max[];  // [beams][blocks_per_row], of the first CTA
   __shared__ SelectSmem<KL> sm;
@@ -941,9 +944,15 @@ cudaError_t launch_beam_select(BeamSelectArgs a, bool fp32, int num_sms, cudaStr
   a.blocks_per_row = static_cast<int>((steps + (1 << sh) - 1) >> sh);
   // e / blocks_per_row = e * inverse / 2^32 for e < kMaxEntries
   a.blocks_inverse = static_cast<uint32_t>(((int64_t{1} << 32) - 1) / a.blocks_per_row + 1);
-  // As many CTAs per request as run at once, two on an SM.
+  // As many CTAs per request as run at once, two on an SM; one on an SM where that leaves
+  // a warp at most four loads, since a second one delays the choice more than it speeds
+  // the pass (us, one / two: 37 requests of 3 x 50001 10.4 / 12.6, 64 of 4 x 131072
+  // 27.0 / 19.4, 16 of 16 x 131072 in fp32 88 / 34.6).
+  const int64_t loads = (static_cast<int64_t>(a.num_beams) * a.blocks_per_row << sh) *
+                        a.num_requests;
+  const int64_t most = (loads <= 4ll * kWarps * num_sms ? 1 : 2) * static_cast<int64_t>(num_sms);
   int ctas = kMaxCtas;
-  while (ctas > 1 && static_cast<int64_t>(a.num_requests) * ctas > 2 * num_sms) ctas /= 2;
+  while (ctas > 1 && a.num_requests * static_cast<int64_t>(ctas) > most) ctas /= 2;
   // Twice the error of a row's sum in the pass, relative, all roundings adding up (a step
   // of fp32 is 2^-24): exponentials 4 steps, their arguments 1.3 |x - m| (a weighted mean of
   // which is at most ln V, and kMove); the additions of a lane, 10 and one for each load, a
