@@ -962,11 +962,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 7)
     shared_join_kernel(const SharedArgs a, __nv_bfloat16* out, float* out_lse) {
   constexpr int kRows = kJoinWarps / kRowWarps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part_of = warp % kRowWarps;
-  const int64_t all = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kRows + warp / kRowWarps;
-  const int64_t row = at < all ? at : all - 1;
-  const int s = static_cast<int>(row / a.num_q_heads);
-  const int head = static_cast<int>(row - static_cast<int64_t>(s) * a.num_q_heads);
+  // (rows fit 31 bits, as the call checks)
+  const int all = a.num_seqs * a.num_q_heads;
+  const int at = static_cast<int>(blockIdx.x) * kRows + warp / kRowWarps;
+  const int row = at < all ? at : all - 1;
+  const int s = row / a.num_q_heads;
+  const int head = row - s * a.num_q_heads;
   const int kvh = head / a.group, h = head - kvh * a.group;
   const SharedLayout& lay = a.lay;
   griddep_launch_dependents();
@@ -976,7 +977,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 7)
   const int tiles = lay.info[a.num_groups].y;
   Joined x{make_float4(0.f, 0.f, 0.f, 0.f), kFloor, 0.f};
   if (part_of == 0) {
-    x.o = reinterpret_cast<const float4*>(lay.own_o + row * 128)[lane];
+    x.o = reinterpret_cast<const float4*>(lay.own_o)[static_cast<int64_t>(row) * 32 + lane];
     const float2 ml = lay.own_ml[row];
     x.m = ml.x;
     x.l = ml.y;
@@ -1031,7 +1032,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 7)
   uint2 o;
   o.x = none ? 0u : pack_bf16x2(x.o.x / x.l, x.o.y / x.l);
   o.y = none ? 0u : pack_bf16x2(x.o.z / x.l, x.o.w / x.l);
-  reinterpret_cast<uint2*>(out + row * 128)[lane] = o;
+  reinterpret_cast<uint2*>(out)[static_cast<int64_t>(row) * 32 + lane] = o;
   if (lane == 0 && out_lse) out_lse[row] = none ? -INFINITY : (x.m + log2f(x.l)) * kLn2;
 }
 
