@@ -27,7 +27,7 @@
 // hangs on lse_w, which the pass knows to `margin` / 2: values are kept as sums
 // of two floats (48 bits), and where two beams' candidates around the choice are
 // nearer than `margin`, those rows' sums are taken again, to 1e-9: exponentials by
-// table and short polynomial (Tang's method) in two floats, added as whole numbers,
+// table and short polynomial (Tang's method), added as whole numbers,
 // so that equal logits in whatever order and place give equal sums.
 //
 // NaN and +inf logits count as -inf: no candidates, no part of the sum.
@@ -261,9 +261,9 @@ struct WarpList {
   }
 };
 
-// 2^(j / 64), as a sum of two floats, j < 64: for sums that need more than fp32.
+// 2^(j / 64) in units of 2^-31, j < 64: for sums that need more than fp32.
 struct ExpTable {
-  float2 t[64];
+  uint32_t t[64];
 };
 
 // A sum in units of 2^-50, whole numbers in two parts: no order of its terms changes it.
@@ -288,11 +288,12 @@ __device__ __forceinline__ void add_exp(FixedSum& sum, const ExpTable& tab, floa
   // 2^f - 1 = sum (f ln 2)^k / k!
   const float g = f * 0.69314718055994530942f;
   const float p = g * __fmaf_rn(g, __fmaf_rn(g, __fmaf_rn(g, 1.f / 24.f, 1.f / 6.f), 0.5f), 1.f);
+  // in whole numbers from here on, a conversion to 64 bits costs eight of these: p in units
+  // of 2^-38 (|p| < 0.006, so 31 bits hold it)
   const int k = static_cast<int>(n);
-  const float2 b = tab.t[k & 63];
-  const float scale = __uint_as_float(static_cast<uint32_t>((k >> 6) + 127 + 50) << 23);
-  const float hi = b.x * scale;
-  sum.add(static_cast<uint64_t>(__float2ll_rn(hi) + __float2ll_rn(__fmaf_rn(hi, p, b.y * scale))));
+  const uint32_t e = tab.t[k & 63];
+  const int64_t ep = static_cast<int64_t>(e) * __float2int_rn(p * 0x1p38f);
+  sum.add(((static_cast<uint64_t>(e) << 19) + (ep >> 19)) >> -(k >> 6));
 }
 
 constexpr int kGroups = 128;     // of block maxima, whose best bound the choice
@@ -464,7 +465,10 @@ template <int KL>
 __device__ __noinline__ float group_bound(SelectSmem<KL>& sm, float best, int n) {
   constexpr int kQuarter = kGroups / 4;
   static_assert(kThreads / kGroups == 4, "a thread for each quarter");
-  sm.group[threadIdx.x / kGroups][threadIdx.x % kGroups] = best;
+  // (turned by a quarter: short rows, which fill only their warps' first lanes, fill more groups)
+  static_assert(kGroups == 4 * 32, "four warps side by side");
+  const int turned = (threadIdx.x + 8 * (threadIdx.x / kGroups)) & 31;
+  sm.group[threadIdx.x / kGroups][(threadIdx.x & (kGroups - 32)) | turned] = best;
   if (threadIdx.x == 0) sm.bound = -INFINITY;
   __syncthreads();
   if (threadIdx.x < kGroups) {
@@ -553,11 +557,8 @@ __device__ __noinline__ void sum_again(const Choice<T, KL>& c, unsigned rows, fl
   SelectSmem<KL>& sm = c.sm;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int V = c.a.vocab, NB = c.a.blocks_per_row;
-  if (threadIdx.x < 64) {
-    const double t = exp2(threadIdx.x / 64.0);
-    const float hi = static_cast<float>(t);
-    sm.table.t[threadIdx.x] = make_float2(hi, static_cast<float>(t - hi));
-  }
+  if (threadIdx.x < 64)
+    sm.table.t[threadIdx.x] = __double2uint_rn(exp2(threadIdx.x / 64.0) * 0x1p31);
   __syncthreads();
 #pragma unroll 1
   for (; rows; rows &= rows - 1) {
@@ -569,9 +570,16 @@ __device__ __noinline__ void sum_again(const Choice<T, KL>& c, unsigned rows, fl
     for (int b = lane; b < NB; b += 32) top = fmaxf(top, c.block_max[w * NB + b]);
     top = warp_max(top);
     FixedSum sum;
-#pragma unroll 2
-    for (int x = threadIdx.x; x < V; x += kThreads)
-      add_exp(sum, sm.table, sane(Elem<T>::load(row.p, x)), top);
+    // (eight loads under way: two rows of 50497 alone took 80 us with two)
+#pragma unroll 1
+    for (int x0 = threadIdx.x; x0 < V; x0 += 8 * kThreads) {
+      float x[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        x[i] = x0 + i * kThreads < V ? sane(Elem<T>::load(row.p, x0 + i * kThreads)) : -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) add_exp(sum, sm.table, x[i], top);
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       sum.hi += __shfl_xor_sync(0xffffffffu, sum.hi, off);
@@ -814,27 +822,36 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
     const int blocks = sm.blocks;
     if (blocks <= kMaxPicked) {
-      if (least == -INFINITY) {
-        // (too few blocks for a bound: that of lanes' best candidates)
-        best = -INFINITY;
+      // where blocks are too few for a bound, or give too low a one (a few beams far above
+      // the others have all the candidates): that of lanes' best candidates
+      bool lanes = least == -INFINITY;
+      while (true) {
+        if (lanes) {
+          best = -INFINITY;
+#pragma unroll 1
+          for (int t = warp; t < blocks << sh; t += kWarps)
+            best = fmaxf(best, c.best_of(sm.pick.block[t >> sh], t & ((1 << sh) - 1), lane));
+          least = fmaxf(least, group_bound(sm, best, L));
+          set_bound();
+        }
 #pragma unroll 1
         for (int t = warp; t < blocks << sh; t += kWarps)
-          best = fmaxf(best, c.best_of(sm.pick.block[t >> sh], t & ((1 << sh) - 1), lane));
-        least = group_bound(sm, best, L);
-        set_bound();
+          c.scan(sm.pick.block[t >> sh], t & ((1 << sh) - 1), lane, [&](uint64_t k, uint32_t i) {
+            if (k == 0) return;
+            const int at = atomicAdd(&sm.picked, 1);
+            if (at < kMaxPicked) {
+              sm.pick.key[at] = k;
+              sm.pick.idx[at] = i;
+            }
+          });
+        __syncthreads();
+        const bool enough = lanes || sm.picked <= kMaxPicked;
+        __syncthreads();
+        if (enough) break;
+        lanes = true;
+        if (threadIdx.x == 0) sm.picked = 0;
       }
-#pragma unroll 1
-      for (int t = warp; t < blocks << sh; t += kWarps)
-        c.scan(sm.pick.block[t >> sh], t & ((1 << sh) - 1), lane, [&](uint64_t k, uint32_t i) {
-          if (k == 0) return;
-          const int at = atomicAdd(&sm.picked, 1);
-          if (at < kMaxPicked) {
-            sm.pick.key[at] = k;
-            sm.pick.idx[at] = i;
-          }
-        });
     }
-    __syncthreads();
     const int picked = sm.picked;
     if (blocks <= kMaxPicked && picked <= kMaxPicked) {
       // in order: eight lanes compare one with all

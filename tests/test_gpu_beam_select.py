@@ -71,6 +71,21 @@ def test_sizes(pa, R, W, V, K, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("R,W,V,K", [
+    (8, 27, 2123, 54), (1, 32, 16705, 64), (20, 17, 65, 43), (5, 9, 131, 54), (70, 6, 50497, 57)])
+def test_many_choices(pa, R, W, V, K, dtype):
+    """Many choices out of few parts of the rows; the candidates of one beam, of two beams
+    and of all of them far above the others'."""
+    c = make(gen(V), R, W, V, K, dtype)
+    c.scores[0, 1:] -= 60.0
+    if R > 3:
+        c.scores[1, 2:] -= 60.0
+        c.scores[2, :] = c.scores[2, :1]
+    c.run(pa)
+    c.check()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("offset,pad", [(0, 1), (1, 0), (3, 5), (8, 8), (13, 31)])
 def test_strides_and_alignment(pa, dtype, offset, pad):
     """Rows that begin anywhere, of a wider matrix, requests apart, beams in another order."""
