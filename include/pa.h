@@ -581,9 +581,9 @@ int pa_decode_shared(void *out, const void *q, const void *k_cache, const void *
  *              beam's logits are not read
  *   end_token  in [0, vocab_size); -1 (none) where finished is NULL
  * Values are compared to 1e-9 (in a row by the logits alone, so exactly); beams of
- * equal logits, in whatever order, have equal sums.  out_scores are within 5e-6
- * of the value, and a rounding of it.  num_beams up to 32, num_choices up
- * to 64, num_beams * vocab_size up to 2^30.  With num_choices == num_beams,
+ * equal logits, in whatever order, have equal sums.  out_scores are within 2^-24 of
+ * their size and 6e-6 + 5e-11 vocab_size of the value.  num_beams up to 32, num_choices
+ * up to 64, num_beams * vocab_size up to 2^30.  With num_choices == num_beams,
  * out_scores and out_finished may be scores and finished themselves; outputs may
  * not overlap anything otherwise (PA_ERR_INVALID).  No workspace; equal calls give
  * equal bits, and calls may overlap freely.
@@ -617,9 +617,10 @@ int pa_beam_select(int32_t *parents, int32_t *tokens, float *out_scores, uint8_t
  *              multiple of 8): [num_blocks, block_size, num_kv_heads, head_dim];
  *              num_layers 0: tables and lengths alone (pools may be NULL)
  * Outputs may not overlap inputs or pools (PA_ERR_INVALID); num_beams up to 32,
- * num_beams * max_blocks_per_seq up to 2^30; head_dim a multiple of 8.  A parent outside [-1, num_beams) sets PA_DEVERR_BEAM
- * and counts as -1, a length outside its row PA_DEVERR_SEQ_LEN and is clamped; a
- * copy from or to a block outside the pool sets PA_DEVERR_BLOCK_ID and is left out.
+ * num_beams * max_blocks_per_seq up to 2^30; head_dim a multiple of 8.  A parent
+ * outside [-1, num_beams) sets PA_DEVERR_BEAM and counts as -1, a length outside its
+ * row PA_DEVERR_SEQ_LEN and is clamped; a copy from or to a block outside the pool
+ * sets PA_DEVERR_BLOCK_ID and is left out.
  */
 int pa_beam_reorder(int32_t *out_tables, int32_t *out_lens, const int32_t *block_tables,
                     const int32_t *seq_lens, const int32_t *parents, int num_requests,
@@ -692,8 +693,8 @@ int pa_device_error_flags(unsigned int *flags, int reset);
  * Test entry points of the failure path (no product call needs them).  Each
  * makes one launch of the kernel its name gives, with the same arguments as
  * pa_decode (workspace and mode included; no lse) / pa_prefill_chunk /
- * pa_prefill_window / pa_decode_shared (its prefix pass; no lse), in which the producer / loader warps issue no load at all and every
- * mbarrier wait is bounded by wait_limit_us (1 .. 2,000,000 us) instead of
+ * pa_prefill_window / pa_decode_shared (its prefix pass; no lse), in which the
+ * producer / loader warps issue no load at all and every mbarrier wait is bounded by wait_limit_us (1 .. 2,000,000 us) instead of
  * the default two seconds.  Every wait therefore runs out with no copy in
  * flight: the kernel sets PA_DEVERR_TIMEOUT, skips the rest of its waits,
  * frees its tensor memory and returns; the outputs are unspecified.  The

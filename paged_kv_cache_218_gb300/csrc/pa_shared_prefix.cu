@@ -249,7 +249,8 @@ __device__ __forceinline__ uint64_t low_bits(int k) {
 __device__ __forceinline__ void stg32(float* p, const uint32_t* x) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
                    reinterpret_cast<uint64_t>(p)),
-               "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]),
+               "r"(x[7])
                : "memory");
 }
 
@@ -365,7 +366,8 @@ __global__ void __launch_bounds__(512, 1)
       const int worker = static_cast<int>(blockIdx.x) / CG;
       const int team = worker / a.lay.team_workers;
       const int teams = shared_teams(a.lay, tiles);
-      const int from = team < teams ? static_cast<int>(static_cast<int64_t>(tiles) * team / teams) : 0;
+      const int from =
+          team < teams ? static_cast<int>(static_cast<int64_t>(tiles) * team / teams) : 0;
       const int to =
           team < teams ? static_cast<int>(static_cast<int64_t>(tiles) * (team + 1) / teams) : 0;
       Cursor cur{from, to, 0, 0, 0, team, worker - team * a.lay.team_workers};
@@ -580,7 +582,8 @@ __global__ void __launch_bounds__(512, 1)
           tc_commit<1>(bar);
       };
       if (warp == kMmaWarp) {
-        const uint32_t idesc_s = instr_desc(0, 128 * CG) & ~(0x3fu << 17);  // (columns / 8 left out)
+        // (columns / 8 left out)
+        const uint32_t idesc_s = instr_desc(0, 128 * CG) & ~(0x3fu << 17);
         const uint64_t dk0 = smem_desc(sbase + P::kKOff, 16, kKGroupStride);
         const uint64_t dq0 = smem_desc(sbase + P::kQOff, 16, 1024);
         int s_buf = 0, s_round = 0, s_kslot = 0, s_kphase = 0;

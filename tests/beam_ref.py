@@ -17,7 +17,8 @@ import numpy as np
 
 def score_tolerance(value, vocab, fp32):
     steps = math.ceil(vocab / (8 * 8 * 4 * 32 * (8 if fp32 else 16))) + 1
-    err = 2.0**-20 + 2.0**-23 * math.log(vocab) + 1.3 * 2.0**-24 * (4 + math.log(vocab)) + (25 + 3 * steps) * 2.0**-24
+    err = 2.0**-20 + 2.0**-23 * math.log(vocab) + 1.3 * 2.0**-24 * (4 + math.log(vocab))
+    err += (25 + 3 * steps) * 2.0**-24
     return err + 2.0**-24 * np.abs(value)
 
 

@@ -104,6 +104,17 @@ def test_strides_and_alignment(pa, dtype, offset, pad):
     t.check()
 
 
+def test_offsets_past_32_bits(pa):
+    """Beams and requests beyond 2^32 bytes, and 2^32 elements, of one another."""
+    base = torch.empty(((1 << 32) + (1 << 31) + 60000,), device="cuda", dtype=BF16)
+    x = torch.as_strided(base, (2, 2, 50021), (1 << 32, (1 << 31) + 7, 1), 3)
+    x.copy_(3 * torch.randn((2, 2, 50021), generator=gen(21), device="cuda"))
+    s = -torch.rand((2, 2), generator=gen(22), device="cuda")
+    c = Case(x, s, 6)
+    c.run(pa)
+    c.check()
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_ties(pa, dtype):
     """Few distinct logits, many of them equal; whole rows equal; beams equal to one another."""

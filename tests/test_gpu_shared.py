@@ -253,6 +253,24 @@ def test_agrees_with_plain_decode_and_equal_bits(pa):
     assert (lse - c.lse).abs().max() < 1e-4
 
 
+def test_offsets_past_32_bits(pa):
+    """Pools of 4.8 GB each, prefixes and own blocks at their end; then the small call."""
+    for small in (False, True):
+        rng = np.random.default_rng(13)
+        c = Case(13, [(20, lengths(rng, 5, 20, 90)), (9, lengths(rng, 40, 9, 60))], 16, 8, loose=2,
+                 small=small)
+        n, nb = c.kc.shape[0], 150000
+        big = [torch.empty((nb, 16, 8, D), device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+        for pool, part in zip(big, (c.kc, c.vc)):
+            pool[nb - n:] = part
+        here = (c.tables >= 0) & (c.tables < n)
+        c.tables = torch.where(here, c.tables + (nb - n), c.tables).contiguous()
+        c.kc, c.vc = big
+        c.run(pa)
+        c.check()
+        assert pa.pa_device_error_flags() == 0
+
+
 def test_bad_metadata_is_flagged(pa):
     """Offsets that overlap, fall or leave the batch, groups larger than said, prefixes longer
     than a row, ids outside the pool, lengths outside the row: flagged, nothing faults."""
