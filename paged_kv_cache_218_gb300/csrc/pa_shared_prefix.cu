@@ -930,7 +930,11 @@ cudaError_t launch_shared_prefix(const SharedArgs& args, const CUtensorMap* tm_q
   SharedArgs a = args;
   if (a.wait_ns == 0) a.wait_ns = kWaitLimitNs;
   if (a.lay.worker_ctas == 2) return launch_workers<2, 0>(a, tm_q, tm_k, tm_v, stream);
-  if (a.lay.box_tokens * a.group <= 64) return launch_workers<1, 64>(a, tm_q, tm_k, tm_v, stream);
+  // Up to 16 query rows: the next item's Q tile in front of its turn.  (us with 4 query
+  // heads a kv head, with / without: 200 groups of 4 sequences behind 256 tokens 76.8 /
+  // 83.8, 64 of 4 behind 1024 59.6 / 61.8, 12 of 4 behind 2048 25.7 / 26.0; with room for
+  // 64 rows, 40 groups of 8 behind 256 28.8 / 27.9, 20 of 8 behind 2048 42.3 / 41.2.)
+  if (a.lay.box_tokens * a.group <= 16) return launch_workers<1, 16>(a, tm_q, tm_k, tm_v, stream);
   return launch_workers<1, 0>(a, tm_q, tm_k, tm_v, stream);
 }
 
@@ -1061,7 +1065,9 @@ cudaError_t launch_join(const SharedArgs& a, __nv_bfloat16* out, float* out_lse,
 
 cudaError_t launch_shared_join(const SharedArgs& a, __nv_bfloat16* out, float* out_lse,
                                cudaStream_t stream) {
-  // Few rows behind a long prefix have a piece from every team: four warps on each.
+  // Few rows behind a long prefix have a piece from every team: four warps on each.  (us
+  // of a call, four warps / one: 512 rows behind 16384 tokens 20.4 / 21.8, 608 behind
+  // 32768 36.6 / 38.7; 5120 rows 47.7 / 45.6, 8192 64.8 / 60.0, 3200 the same.)
   const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
   return rows <= 2048 ? launch_join<4>(a, out, out_lse, stream)
                       : launch_join<1>(a, out, out_lse, stream);

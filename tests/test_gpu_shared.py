@@ -135,7 +135,21 @@ def test_groups_past_a_tile_and_a_pair(pa, members):
     c = Case(members, [(11, lengths(rng, members, 11, 30))], 8, 2)
     c.run(pa)
     c.check(rows=sorted({0, 1, min(30, members - 1), members - 1, members // 2,
-                         min(31, members - 1), min(32, members - 1), min(63, members - 1), min(64, members - 1)}))
+                         min(31, members - 1), min(32, members - 1), min(63, members - 1),
+                         min(64, members - 1)}))
+
+
+@pytest.mark.parametrize("G,members", [(4, 1), (4, 4), (4, 5), (8, 2), (8, 3), (1, 16), (1, 17)])
+def test_many_small_groups(pa, G, members):
+    """Up to 16 query rows have the next group's queries loaded ahead: many groups of a few
+    key tiles for each worker, on both sides of that."""
+    rng = np.random.default_rng(50 * G + members)
+    groups = [(p, lengths(rng, members, p, 20)) for p in rng.integers(1, 30, 160)]
+    c = Case(G, groups, 2 * G, 2)
+    c.run(pa)
+    c.check(rows=sorted({int(x) for x in rng.integers(0, 160 * members, 60)}
+                        | {0, 160 * members - 1}))
+    assert pa.pa_device_error_flags() == 0
 
 
 @pytest.mark.parametrize("G,members", [(1, 128), (1, 129), (3, 21), (3, 42), (3, 50), (5, 12),
