@@ -53,7 +53,8 @@ struct BeamReorderArgs {
 };
 
 // Kernel launchers (return cudaError_t of the launch).
-cudaError_t launch_beam_select(BeamSelectArgs a, bool fp32, int num_sms, cudaStream_t stream);
+cudaError_t launch_beam_select(const BeamSelectArgs& a, bool fp32, int num_sms,
+                               cudaStream_t stream);
 cudaError_t launch_beam_reorder(BeamReorderArgs a, int num_sms, cudaStream_t stream);
 
 }  // namespace pa

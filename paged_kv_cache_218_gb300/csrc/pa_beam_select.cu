@@ -911,48 +911,64 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 template <typename T, int KL>
-cudaError_t launch(const BeamSelectArgs& a, int ctas, cudaStream_t stream) {
-  const int smem = a.num_beams * a.blocks_per_row * 4;
-  {  // allow clusters of 16, once per device
-    static std::mutex mu;
-    static bool set_for[64] = {};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!set_for[dev]) {
-      e = cudaFuncSetAttribute(beam_select_kernel<T, KL>,
-                               cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-      if (e != cudaSuccess) return e;
-      e = cudaFuncSetAttribute(beam_select_kernel<T, KL>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxEntries * 4);
-      if (e != cudaSuccess) return e;
-      set_for[dev] = true;
-    }
-  }
+struct Launch {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.num_requests) * static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, beam_select_kernel<T, KL>, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  Launch(int requests, int ctas, int smem, cudaStream_t stream) {
+    cfg.gridDim = dim3(static_cast<unsigned>(requests) * static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
+// The largest cluster, up to *ctas, of which as many as there are requests run at once: a
+// cluster lies within one part of the device, and parts differ in size.  (At two CTAs an
+// SM 14 clusters of 16 run at once, 19 of 13, 36 of 8, 74 of 4: sixteen requests of
+// 16 x 131072 in fp32 took 35.3 us in clusters of 16, of which two began 13 us late, and
+// take 32.8 in clusters of 13.)  What the device answers for a size is asked once.
+template <typename T, int KL>
+cudaError_t fit_cluster(int requests, int* ctas) {
+  const auto kernel = beam_select_kernel<T, KL>;
+  static std::mutex mu;
+  static bool set_for[64] = {};
+  static int at_once[64][kMaxCtas + 1] = {};  // 0: not asked yet
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!set_for[dev]) {  // allow clusters of 16
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kMaxEntries * 4);
+    if (e != cudaSuccess) return e;
+    set_for[dev] = true;
+  }
+  for (; *ctas > 1; --*ctas) {
+    int& n = at_once[dev][*ctas];
+    if (n == 0) {
+      const Launch<T, KL> one(1, *ctas, kMaxEntries * 4, nullptr);
+      e = cudaOccupancyMaxActiveClusters(&n, kernel, &one.cfg);
+      if (e != cudaSuccess) return e;
+    }
+    if (n >= requests) break;
+  }
+  return cudaSuccess;
 }
 
-}  // namespace
-
-cudaError_t launch_beam_select(BeamSelectArgs a, bool fp32, int num_sms, cudaStream_t stream) {
-  const int lead = fp32 ? 7 : 15;  // a row may begin anywhere in its first 32 bytes
+template <typename T, int KL>
+cudaError_t launch(BeamSelectArgs a, int num_sms, cudaStream_t stream) {
+  const int lead = Elem<T>::kVec - 1;  // a row may begin anywhere in its first 32 bytes
   const int elems = 32 * kVecs * (lead + 1);  // of a warp load
   const int64_t steps = (static_cast<int64_t>(a.vocab) + lead + elems - 1) / elems;
   int sh = 0;
@@ -962,14 +978,17 @@ cudaError_t launch_beam_select(BeamSelectArgs a, bool fp32, int num_sms, cudaStr
   // e / blocks_per_row = e * inverse / 2^32 for e < kMaxEntries
   a.blocks_inverse = static_cast<uint32_t>(((int64_t{1} << 32) - 1) / a.blocks_per_row + 1);
   // As many CTAs per request as run at once, two on an SM; one on an SM where that leaves
-  // a warp at most four loads, since a second one delays the choice more than it speeds
-  // the pass (us, one / two: 37 requests of 3 x 50001 10.4 / 12.6, 64 of 4 x 131072
-  // 27.0 / 19.4, 16 of 16 x 131072 in fp32 88 / 34.6).
+  // a warp at most two loads, since a second one delays the choice more than it speeds
+  // the pass (us, one / two: 1.6 loads a warp, 100 requests of 4 x 10000 10.2 / 11.2; 1.9,
+  // 150 of 5 x 3000 in fp32 12.1 / 13.5; 2.3, 37 of 3 x 50001 10.3 / 9.8; 3.2, 60 of
+  // 4 x 32000 12.4 / 11.9; 64 of 4 x 131072 27.0 / 19.3, 16 of 16 x 131072 in fp32
+  // 36.6 / 32.8).
   const int64_t loads = (static_cast<int64_t>(a.num_beams) * a.blocks_per_row << sh) *
                         a.num_requests;
-  const int64_t most = (loads <= 4ll * kWarps * num_sms ? 1 : 2) * static_cast<int64_t>(num_sms);
-  int ctas = kMaxCtas;
-  while (ctas > 1 && a.num_requests * static_cast<int64_t>(ctas) > most) ctas /= 2;
+  const int64_t most = (loads <= 2ll * kWarps * num_sms ? 1 : 2) * static_cast<int64_t>(num_sms);
+  int ctas = static_cast<int>(std::min<int64_t>(std::max<int64_t>(most / a.num_requests, 1),
+                                                kMaxCtas));
+  if (const cudaError_t e = fit_cluster<T, KL>(a.num_requests, &ctas)) return e;
   // Twice the error of a row's sum in the pass, relative, all roundings adding up (a step
   // of fp32 is 2^-24): exponentials 4 steps, their arguments 1.3 |x - m| (a weighted mean of
   // which is at most ln V, and kMove); the additions of a lane, 10 and one for each load, a
@@ -982,10 +1001,20 @@ cudaError_t launch_beam_select(BeamSelectArgs a, bool fp32, int num_sms, cudaStr
   const double err = 0x1p-24 * (4 + 1.3 * (kMove + ln_v) + 10 + static_cast<double>(lane_loads) +
                                 5 + 4 + 4 + 4 * (5 + 1.3 * kMove) + 2 * ln_v);
   a.margin = static_cast<float>(2 * err);
+  const Launch<T, KL> l(a.num_requests, ctas, a.num_beams * a.blocks_per_row * 4, stream);
+  const cudaError_t e = cudaLaunchKernelEx(&l.cfg, beam_select_kernel<T, KL>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_beam_select(const BeamSelectArgs& a, bool fp32, int num_sms,
+                               cudaStream_t stream) {
   const bool wide = a.num_choices + 1 > 32;
-  if (fp32) return wide ? launch<float, 3>(a, ctas, stream) : launch<float, 1>(a, ctas, stream);
-  return wide ? launch<__nv_bfloat16, 3>(a, ctas, stream)
-              : launch<__nv_bfloat16, 1>(a, ctas, stream);
+  if (fp32)
+    return wide ? launch<float, 3>(a, num_sms, stream) : launch<float, 1>(a, num_sms, stream);
+  return wide ? launch<__nv_bfloat16, 3>(a, num_sms, stream)
+              : launch<__nv_bfloat16, 1>(a, num_sms, stream);
 }
 
 }  // namespace pa
