@@ -11,7 +11,10 @@
 // What bounds it: HBM, one pass over the logits; at bf16 the exponential unit is
 // near behind (11 elements per cycle and SM arrive, 16 exponentials leave).  So
 // the pass does as little as it can per element: its exponential for the sum, and
-// a maximum.  A cluster serves a request, its CTAs take a share of every row,
+// a maximum.  Behind it comes a chain of short steps on one SM.  64 requests of
+// 4 x 131072 in bf16 (67 MB) take 19.3 us, 12.7 of them the pass (6.3 TB/s once it
+// runs) and 5.6 the choice; 16 of 16 x 131072 in fp32 (134 MB) 32.8; one of 4 x 32000
+// 6.4, a launch and some eight dependent round trips.  A cluster serves a request, its CTAs take a share of every row,
 // a warp 1024 bf16 (512 fp32) elements at a time, twice 32 bytes a lane; the maxima of
 // such blocks and the rows' (maximum, sum) go to the cluster's first CTA.
 //
