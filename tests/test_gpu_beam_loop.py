@@ -3,6 +3,10 @@ selection, reordering, scatter of the chosen tokens, attention behind the shared
 eagerly and as one captured step.  After every step each beam's cache holds its own
 history token for token, the attention is that of 64 bits over it, and the choice that of
 the logits it was made from."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -148,3 +152,60 @@ def test_beams_keep_their_histories(pa, captured, wide):
                             window_ref.assert_within(s.out[layer, r * W + i, h], out, tol,
                                                      (n, r, i, layer, h))
             assert len(tails) == W  # the next tokens go to blocks of the beams' own
+
+
+FIRST = """
+import torch
+from paged_kv_cache_218_gb300 import binding as pa
+dev = dict(device="cuda")
+R, W, V, Hq, Hkv, D = 16, 4, 5000, 8, 2, 128
+x = torch.randn((R, W, V), **dev)
+scores = torch.zeros((R, W), **dev)
+kc, vc = (torch.randn((2 * R * W + R, 16, Hkv, D), **dev).bfloat16() for _ in range(2))
+tables = torch.full((R * W, (96 << 20) // (R * W * Hkv * 8192) + 1), -1, dtype=torch.int32, **dev)
+tables[:, 0] = torch.arange(R, **dev).repeat_interleave(W)
+tables[:, 1:3] = R + torch.arange(2 * R * W, **dev).view(-1, 2)
+lens = torch.full((R * W,), 27, dtype=torch.int32, **dev)
+q = torch.randn((R * W, Hq, D), **dev).bfloat16()
+offsets = torch.arange(R + 1, dtype=torch.int32, **dev) * W
+shared = torch.ones(R, dtype=torch.int32, **dev)
+made = []
+for members in (W, 20, R * W):  # the kernels of 16 query rows, of 128, of pairs
+    out = torch.zeros_like(q)
+    ws = torch.empty(pa.pa_decode_shared_workspace_size(R * W, R, members, Hq, Hkv, D),
+                     dtype=torch.uint8, **dev)
+    made.append((pa.pa_decode_shared, (out, q, kc, vc, tables, lens, offsets, members, shared,
+                                       D ** -0.5, ws), (out,)))
+for dtype in (torch.bfloat16, torch.float32):
+    for choices in (4, 40):
+        out = (torch.zeros((R, choices), dtype=torch.int32, **dev),
+               torch.zeros((R, choices), dtype=torch.int32, **dev), torch.zeros((R, choices), **dev))
+        made.append((pa.pa_beam_select, (*out, x.to(dtype), scores), out))
+parents = torch.randint(0, W, (R, W), dtype=torch.int32, **dev)
+out = (torch.zeros_like(tables), torch.zeros_like(lens))
+made.append((pa.pa_beam_reorder, (*out, tables, lens, parents, None, None), out))
+torch.cuda.synchronize()
+for call, args, out in made:
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(*args)
+    graph.replay()
+    torch.cuda.synchronize()
+    captured = [t.clone() for t in out]
+    for t in out:
+        t.zero_()
+    call(*args)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(captured, out)), call.__name__
+    assert any(t.ne(0).any() for t in out), call.__name__
+assert pa.pa_device_error_flags() == 0
+"""
+
+
+def test_first_calls_captured(pa):
+    """In a process of its own: a kernel's first launch sets its attributes, and asks how many
+    of its clusters run at once."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST], cwd=root, capture_output=True, text=True,
+                          timeout=120)
+    assert done.returncode == 0, done.stdout + done.stderr
