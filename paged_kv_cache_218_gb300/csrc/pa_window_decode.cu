@@ -50,7 +50,7 @@
 // the blocks behind its group's prefix.  It runs beside the prefix pass, whose CTAs leave
 // room for two warps' rings on each SM, and reads nothing of it; a third kernel joins
 // both (pa_shared_prefix.cu).  Alone it reads 294 MB of 256 sequences in 54 us; beside the
-// pass a block takes a warp 2 us instead of 1, since its products wait behind the pass's.
+// pass a block takes a warp 2 us instead of 1.
 #include <float.h>
 #include <math.h>
 
