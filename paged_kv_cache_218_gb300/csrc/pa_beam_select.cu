@@ -406,19 +406,21 @@ struct Choice {
       load_edge(row.p, a.vocab, e0, sm.edges[threadIdx.x], v);
     return e0;
   }
-  // Best value among them, in fp32.
-  __device__ __forceinline__ float best_of(int e, int part, int lane) const {
+  // Best values among quarters of them (every fourth pair), in fp32.
+  __device__ __forceinline__ void best_of(int e, int part, int lane, float (&best)[4]) const {
     const int w = beam_of(a, e);
-    if ((ended >> w) & 1) return lane == 0 && part == 0 ? sm.base[w].x : -INFINITY;
+    if ((ended >> w) & 1) {
+      if (lane == 0 && part == 0) best[0] = fmaxf(best[0], sm.base[w].x);
+      return;
+    }
     uint32_t v[kVecs][8];
     fetch(Row<T>(a, r, w), w, e, part, lane, v);
-    float best = -INFINITY;
+    const float base = sm.base[w].x;
 #pragma unroll
     for (int i = 0; i < kVecs * E::kVec / 2; ++i) {
       const float2 x = E::pair(v[i / (E::kVec / 2)], i % (E::kVec / 2));
-      best = fmaxf(best, fmaxf(sane(x.x), sane(x.y)));
+      best[i % 4] = fmaxf(best[i % 4], base + fmaxf(sane(x.x), sane(x.y)));
     }
-    return sm.base[w].x + best;
   }
   // Load number `part` of block e: f(key, index) for the candidates that may reach the
   // bound, the whole warp together (key 0: this lane has none).
@@ -468,10 +470,7 @@ template <int KL>
 __device__ __noinline__ float group_bound(SelectSmem<KL>& sm, float best, int n) {
   constexpr int kQuarter = kGroups / 4;
   static_assert(kThreads / kGroups == 4, "a thread for each quarter");
-  // (turned by a quarter: short rows, which fill only their warps' first lanes, fill more groups)
-  static_assert(kGroups == 4 * 32, "four warps side by side");
-  const int turned = (threadIdx.x + 8 * (threadIdx.x / kGroups)) & 31;
-  sm.group[threadIdx.x / kGroups][(threadIdx.x & (kGroups - 32)) | turned] = best;
+  sm.group[threadIdx.x / kGroups][threadIdx.x % kGroups] = best;
   if (threadIdx.x == 0) sm.bound = -INFINITY;
   __syncthreads();
   if (threadIdx.x < kGroups) {
@@ -826,14 +825,27 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int blocks = sm.blocks;
     if (blocks <= kMaxPicked) {
       // where blocks are too few for a bound, or give too low a one (a few beams far above
-      // the others have all the candidates): that of lanes' best candidates
+      // the others have all the candidates): that of the best candidates in quarters of
+      // lanes' shares, so that one block fills the 128 groups
       bool lanes = least == -INFINITY;
       while (true) {
         if (lanes) {
-          best = -INFINITY;
+          float quarter[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
           for (int t = warp; t < blocks << sh; t += kWarps)
-            best = fmaxf(best, c.best_of(sm.pick.block[t >> sh], t & ((1 << sh) - 1), lane));
+            c.best_of(sm.pick.block[t >> sh], t & ((1 << sh) - 1), lane, quarter);
+          __syncthreads();  // (no load uses sm.edges any more)
+          float* const all = reinterpret_cast<float*>(sm.edges);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) all[q * kThreads + threadIdx.x] = quarter[q];
+          __syncthreads();
+          // group 32 q + l: quarter q of lane l, of the next warp's lane l + 8, and so on,
+          // since short rows fill but their warps' first lanes
+          best = -INFINITY;
+          if (warp < 4)
+#pragma unroll 4
+            for (int w = 0; w < kWarps; ++w)
+              best = fmaxf(best, all[warp * kThreads + 32 * w + ((lane + 8 * w) & 31)]);
           least = fmaxf(least, group_bound(sm, best, L));
           set_bound();
         }
