@@ -12,16 +12,18 @@
 // near behind (11 elements per cycle and SM arrive, 16 exponentials leave).  So
 // the pass does as little as it can per element: its exponential for the sum, and
 // a maximum.  Behind it comes a chain of short steps on one SM.  64 requests of
-// 4 x 131072 in bf16 (67 MB) take 19.3 us, 12.7 of them the pass (6.3 TB/s once it
-// runs) and 5.6 the choice; 16 of 16 x 131072 in fp32 (134 MB) 32.8; one of 4 x 32000
-// 6.4, a launch and some eight dependent round trips.  A cluster serves a request, its CTAs take a share of every row,
+// 4 x 131072 in bf16 (67 MB) take 19.0 us, 12.7 of them the pass (6.3 TB/s once it
+// runs) and 5.6 the choice; 16 of 16 x 131072 in fp32 (134 MB) 32.2; one of 4 x 32000
+// 6.3, a launch and some eight dependent round trips.  A cluster serves a request, its CTAs take a share of every row,
 // a warp 1024 bf16 (512 fp32) elements at a time, twice 32 bytes a lane; the maxima of
 // such blocks and the rows' (maximum, sum) go to the cluster's first CTA.
 //
 // Selection, in that CTA: with 128 groups of blocks, the (K + 1)-th best group's best
 // candidate is a bound that K + 1 candidates reach.  The blocks that reach it, a few
 // more than K, are read again (from L2), the candidates that reach it are gathered
-// and put in order by counting.  Where more than 256 blocks or candidates do (many
+// and put in order by counting.  Few blocks, or a beam far above the others, make a finer
+// bound of the best in 128 shares of the candidates themselves (109 requests of 20 beams, 53
+// choices of 931 tokens: 24 us instead of 139).  Where more than 256 blocks or candidates do (many
 // equal logits), lists that are kept sorted in a warp's registers find first the
 // K + 1 best blocks, equal ones in their order, which hold the K + 1 best candidates
 // (each other block's best comes behind theirs), then those.
@@ -572,15 +574,23 @@ __device__ __noinline__ void sum_again(const Choice<T, KL>& c, unsigned rows, fl
     for (int b = lane; b < NB; b += 32) top = fmaxf(top, c.block_max[w * NB + b]);
     top = warp_max(top);
     FixedSum sum;
-    // (eight loads under way: two rows of 50497 alone took 80 us with two)
-#pragma unroll 1
-    for (int x0 = threadIdx.x; x0 < V; x0 += 8 * kThreads) {
-      float x[8];
+    // (eight loads are under way behind the eight at hand: 103 requests of 6 x 50497, of
+    // which one or two sum a few rows again, 75 us; without, 88; with two loads and 64-bit
+    // conversions 110; with no row in doubt 35)
+    auto get = [&](int x0, float (&x)[8]) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        x[i] = x0 + i * kThreads < V ? sane(Elem<T>::load(row.p, x0 + i * kThreads)) : -INFINITY;
+        x[i] = x0 + i * kThreads < V ? Elem<T>::load(row.p, x0 + i * kThreads) : -INFINITY;
+    };
+    float x[8], next[8];
+    get(threadIdx.x, next);
+#pragma unroll 1
+    for (int x0 = threadIdx.x; x0 < V; x0 += 8 * kThreads) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) add_exp(sum, sm.table, x[i], top);
+      for (int i = 0; i < 8; ++i) x[i] = next[i];
+      get(x0 + 8 * kThreads, next);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) add_exp(sum, sm.table, sane(x[i]), top);
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
