@@ -574,7 +574,8 @@ int pa_decode_shared(void *out, const void *q, const void *k_cache, const void *
  *   logits     device bf16, or fp32 where logits_fp32 is non-zero: beam w of
  *              request r at + r * request_stride + w * beam_stride (elements, not
  *              negative), vocab_size entries, from any element on.  -inf is a
- *              forbidden token; NaN and +inf count as -inf
+ *              forbidden token; NaN and +inf count as -inf, and so does a logit whose
+ *              value lies below the lowest fp32
  *   scores     device fp32 [num_requests, num_beams]; a beam whose score is -inf
  *              (or not finite) proposes nothing, and its logits are not read
  *   finished   device uint8 [num_requests, num_beams] or NULL (none is); a finished
@@ -694,9 +695,9 @@ int pa_device_error_flags(unsigned int *flags, int reset);
  * makes one launch of the kernel its name gives, with the same arguments as
  * pa_decode (workspace and mode included; no lse) / pa_prefill_chunk /
  * pa_prefill_window / pa_decode_shared (its prefix pass; no lse), in which the
- * producer / loader warps issue no load at all and every mbarrier wait is bounded by wait_limit_us (1 .. 2,000,000 us) instead of
- * the default two seconds.  Every wait therefore runs out with no copy in
- * flight: the kernel sets PA_DEVERR_TIMEOUT, skips the rest of its waits,
+ * producer / loader warps issue no load at all and every mbarrier wait is bounded by
+ * wait_limit_us (1 .. 2,000,000 us) instead of the default two seconds.  Every wait
+ * therefore runs out with no copy in flight: the kernel sets PA_DEVERR_TIMEOUT, skips the rest of its waits,
  * frees its tensor memory and returns; the outputs are unspecified.  The
  * call itself returns PA_OK once launched (PA_ERR_INVALID for a limit out of
  * range, or any status the plain call would return).  A decode's balanced-

@@ -14,9 +14,11 @@
 // a maximum.  Behind it comes a chain of short steps on one SM.  64 requests of
 // 4 x 131072 in bf16 (67 MB) take 19.0 us, 12.7 of them the pass (6.3 TB/s once it
 // runs) and 5.6 the choice; 16 of 16 x 131072 in fp32 (134 MB) 32.2; one of 4 x 32000
-// 6.3, a launch and some eight dependent round trips.  A cluster serves a request, its CTAs take a share of every row,
-// a warp 1024 bf16 (512 fp32) elements at a time, twice 32 bytes a lane; the maxima of
-// such blocks and the rows' (maximum, sum) go to the cluster's first CTA.
+// 6.3, a launch and some eight dependent round trips.
+//
+// A cluster serves a request, its CTAs take a share of every row, a warp 1024 bf16 (512
+// fp32) elements at a time, twice 32 bytes a lane; the maxima of such blocks and the rows'
+// (maximum, sum) go to the cluster's first CTA.
 //
 // Selection, in that CTA: with 128 groups of blocks, the (K + 1)-th best group's best
 // candidate is a bound that K + 1 candidates reach.  The blocks that reach it, a few
@@ -326,7 +328,6 @@ struct SelectSmem {
   };
   uint64_t key[kMaxPicked];  // candidates in order
   uint32_t idx[kMaxPicked];
-  uint64_t sum_hi[kWarps], sum_lo[kWarps];
   float bound;        // no candidate below it is chosen
   unsigned doubtful;  // rows whose sums are to be taken again
   int found, blocks, picked;
@@ -459,6 +460,39 @@ struct Choice {
       __syncwarp();
     }
   }
+  // Load number `part` of block e: the candidates that may reach the bound into sm.pick,
+  // their number added to sm.picked; no lane's that are more than sm.pick takes (one at a
+  // time, a thousand of them took 35 us).
+  __device__ __forceinline__ void gather(int e, int part, int lane) const {
+    const int w = beam_of(a, e);
+    const float2 base = sm.base[w];
+    const uint32_t index0 = static_cast<uint32_t>(w) * a.vocab;
+    const bool over = (ended >> w) & 1;
+    const Row<T> row(a, r, w);
+    unsigned hits = over && lane == 0 && part == 0;
+    int e0 = 0;
+    if (!over) {
+      uint32_t v[kVecs][8];
+      e0 = fetch(row, w, e, part, lane, v);
+      const float least = fmaxf((bound - base.x) - slack, -FLT_MAX);
+#pragma unroll
+      for (int i = 0; i < kVecs * E::kVec / 2; ++i) {
+        const float2 x = E::pair(v[i / (E::kVec / 2)], i % (E::kVec / 2));
+        hits |= (x.x >= least && x.x < INFINITY ? 1u : 0u) << (2 * i) |
+                (x.y >= least && x.y < INFINITY ? 1u : 0u) << (2 * i + 1);
+      }
+    }
+    if (hits == 0) return;
+    int at = atomicAdd(&sm.picked, __popc(hits));
+    if (at + __popc(hits) > kMaxPicked) return;
+#pragma unroll 1
+    for (; hits; hits &= hits - 1, ++at) {
+      const int j = __ffs(hits) - 1;
+      const int token = over ? a.end_token : e0 + (j / E::kVec) * 32 * E::kVec + j % E::kVec;
+      sm.pick.key[at] = value_key(base, over ? 0.f : E::load(row.p, token));
+      sm.pick.idx[at] = index0 + token;
+    }
+  }
   __device__ __forceinline__ void doubt(int w0, int w1) const {
     const unsigned both = 1u << w0 | 1u << w1;
     if (w0 != w1 && (both & ~exact)) atomicOr(&sm.doubtful, both);
@@ -564,9 +598,16 @@ __device__ __noinline__ void sum_again(const Choice<T, KL>& c, unsigned rows, fl
   if (threadIdx.x < 64)
     sm.table.t[threadIdx.x] = __double2uint_rn(exp2(threadIdx.x / 64.0) * 0x1p31);
   __syncthreads();
+  // (the rows' sums one behind another, by all threads; then a lane takes each row's logarithm)
+  struct Sums {
+    uint64_t hi[kMaxBeams][kWarps], lo[kMaxBeams][kWarps];
+    float top[kMaxBeams];
+  };
+  static_assert(sizeof(Sums) <= sizeof(sm.edges), "no load uses it meanwhile");
+  Sums& all = *reinterpret_cast<Sums*>(sm.edges);
 #pragma unroll 1
-  for (; rows; rows &= rows - 1) {
-    const int w = __ffs(rows) - 1;
+  for (unsigned todo = rows; todo; todo &= todo - 1) {
+    const int w = __ffs(todo) - 1;
     const Row<T> row(c.a, c.r, w);
     // (the row's maximum: a reference that the order of the logits does not change)
     float top = -INFINITY;
@@ -598,23 +639,26 @@ __device__ __noinline__ void sum_again(const Choice<T, KL>& c, unsigned rows, fl
       sum.lo += __shfl_xor_sync(0xffffffffu, sum.lo, off);
     }
     if (lane == 0) {
-      sm.sum_hi[warp] = sum.hi;
-      sm.sum_lo[warp] = sum.lo;
+      all.hi[w][warp] = sum.hi;
+      all.lo[w][warp] = sum.lo;
+      all.top[w] = top;
     }
-    __syncthreads();
-    const float mine = __shfl_sync(0xffffffffu, score, w);
-    if (threadIdx.x == 0) {
-      for (int i = 1; i < kWarps; ++i) {
-        sum.hi += sm.sum_hi[i];
-        sum.lo += sm.sum_lo[i];
-      }
-      const double ln = log(static_cast<double>(sum.hi) * 0x1p-18 +
-                            static_cast<double>(sum.lo) * 0x1p-50);
-      const float hi = static_cast<float>(ln);
-      sm.base[w] = base_of(mine, top, make_float2(hi, static_cast<float>(ln - hi)));
-    }
-    __syncthreads();
   }
+  __syncthreads();
+  if (threadIdx.x < kMaxBeams && (rows >> lane & 1)) {
+    FixedSum sum;
+#pragma unroll 1
+    for (int i = 0; i < kWarps; ++i) {
+      sum.hi += all.hi[lane][i];
+      sum.lo += all.lo[lane][i];
+    }
+    const double ln = log(static_cast<double>(sum.hi) * 0x1p-18 +
+                          static_cast<double>(sum.lo) * 0x1p-50);
+    const float hi = static_cast<float>(ln);
+    sm.base[lane] =
+        base_of(score, all.top[lane], make_float2(hi, static_cast<float>(ln - hi)));
+  }
+  __syncthreads();
 }
 
 // (__grid_constant__: the arguments' address goes to functions out of line, and a copy of
@@ -861,14 +905,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
 #pragma unroll 1
         for (int t = warp; t < blocks << sh; t += kWarps)
-          c.scan(sm.pick.block[t >> sh], t & ((1 << sh) - 1), lane, [&](uint64_t k, uint32_t i) {
-            if (k == 0) return;
-            const int at = atomicAdd(&sm.picked, 1);
-            if (at < kMaxPicked) {
-              sm.pick.key[at] = k;
-              sm.pick.idx[at] = i;
-            }
-          });
+          c.gather(sm.pick.block[t >> sh], t & ((1 << sh) - 1), lane);
         __syncthreads();
         const bool enough = lanes || sm.picked <= kMaxPicked;
         __syncthreads();
@@ -922,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int64_t at = static_cast<int64_t>(r) * K + i;
     int w = -1, token = -1;
     float value = -INFINITY;
-    if (i < sm.found) {
+    if (i < sm.found && sm.key[i] != 0) {  // (key 0: its value lies past fp32)
       w = sm.idx[i] / V;
       token = sm.idx[i] - static_cast<uint32_t>(w) * V;
       value = unordered(static_cast<uint32_t>(sm.key[i] >> 32));

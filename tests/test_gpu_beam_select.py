@@ -261,6 +261,26 @@ def test_far_logits(pa, scale):
     c.check()
 
 
+@pytest.mark.parametrize("V", [40, 3000])
+def test_values_past_fp32(pa, V):
+    """Logits of -3e38 behind a score of -1e38 have no value in fp32: no candidates, in few
+    blocks as in lists."""
+    x = torch.full((2, 2, V), -3e38, device="cuda")
+    x[:, :, 5:8] = torch.tensor([1.0, 3.0, 2.0], device="cuda")
+    x[1, 0] = -3e38
+    s = torch.full((2, 2), -1e38, device="cuda")
+    s[1, 1] = -1.0
+    c = Case(x, s, 16)
+    c.run(pa)
+    par, tok = c.parents.cpu().tolist(), c.tokens.cpu().tolist()
+    # (the logits tell -1e38 + 3 from -1e38 + 2: a value's second float holds them)
+    assert par[0] == [0, 1] * 3 + [-1] * 10 and tok[0] == [6, 6, 7, 7, 5, 5] + [-1] * 10
+    # (beam 0 of request 1: every logit the same, -3e38 - ln V behind the sum; beam 1's
+    # -3e38 - 1 are values)
+    assert par[1] == [1] * 3 + [0] * 13 and tok[1] == [6, 7, 5] + list(range(13))
+    assert torch.isinf(c.out_scores[0, 6:]).all() and (c.out_scores[0, :6] < -9e37).all()
+
+
 def test_scores_in_place_and_a_few_steps(pa):
     """Outputs over the inputs they replace, as a loop keeps them."""
     g = gen(12)
