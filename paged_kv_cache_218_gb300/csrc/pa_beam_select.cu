@@ -12,8 +12,8 @@
 // near behind (11 elements per cycle and SM arrive, 16 exponentials leave).  So
 // the pass does as little as it can per element: its exponential for the sum, and
 // a maximum.  Behind it comes a chain of short steps on one SM.  64 requests of
-// 4 x 131072 in bf16 (67 MB) take 19.0 us, 12.7 of them the pass (6.3 TB/s once it
-// runs) and 5.6 the choice; 16 of 16 x 131072 in fp32 (134 MB) 32.2; one of 4 x 32000
+// 4 x 131072 in bf16 (67 MB) take 19.3 us, 12.7 of them the pass (6.3 TB/s once it
+// runs) and 5.6 the choice; 16 of 16 x 131072 in fp32 (134 MB) 33.0; one of 4 x 32000
 // 6.3, a launch and some eight dependent round trips.
 //
 // A cluster serves a request, its CTAs take a share of every row, a warp 1024 bf16 (512
