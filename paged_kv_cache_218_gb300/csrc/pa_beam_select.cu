@@ -24,11 +24,12 @@
 // candidate is a bound that K + 1 candidates reach.  The blocks that reach it, a few
 // more than K, are read again (from L2), the candidates that reach it are gathered
 // and put in order by counting.  Few blocks, or a beam far above the others, make a finer
-// bound of the best in 128 shares of the candidates themselves (109 requests of 20 beams, 53
-// choices of 931 tokens: 24 us instead of 139).  Where more than 256 blocks or candidates do (many
-// equal logits), lists that are kept sorted in a warp's registers find first the
-// K + 1 best blocks, equal ones in their order, which hold the K + 1 best candidates
-// (each other block's best comes behind theirs), then those.
+// bound of the best in 128 shares of the candidates themselves (109 requests of 20 beams,
+// 53 choices of 931 tokens: 24 us instead of 139).  Where more than 256 blocks or
+// candidates reach the bound all the same (many equal logits), lists that are kept
+// sorted in a warp's registers find first the K + 1 best blocks, equal ones in their
+// order, which hold the K + 1 best candidates (each other block's best comes behind
+// theirs), then those.
 //
 // Exactness.  Within a row the logits themselves give the order.  Between rows it
 // hangs on lse_w, which the pass knows to `margin` / 2: values are kept as sums
