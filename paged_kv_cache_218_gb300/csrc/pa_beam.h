@@ -29,6 +29,7 @@ struct BeamSelectArgs {
   int block_shift;     // log2 of the warp loads per block of a row
   int blocks_per_row;  // entries of the block maxima for each beam
   uint32_t blocks_inverse;  // 2^32 / blocks_per_row, rounded up
+  int all_sum;         // the whole cluster takes sums again
   float margin;        // values nearer than this are compared again, more exactly
 };
 

@@ -72,6 +72,9 @@ __device__ __forceinline__ float warp_max(float x) {
   return m;
 }
 
+__device__ __forceinline__ void st_remote(uint32_t addr, uint64_t x) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(x) : "memory");
+}
 __device__ __forceinline__ void st_remote(uint32_t addr, float x) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
 }
@@ -333,6 +336,12 @@ struct SelectSmem {
   unsigned doubtful;  // rows whose sums are to be taken again
   int found, blocks, picked;
   ExpTable table;
+  // Rows that the whole cluster is to sum again (0: the choice is made), and their maxima, a
+  // reference that the order of the logits does not change.  The first CTA writes every CTA's.
+  struct Call {
+    unsigned rows;
+    float top[kMaxBeams];
+  } call;
 };
 
 // The best `n` of the warps' lists into sm.key / sm.idx, their number into sm.found.
@@ -590,47 +599,43 @@ __device__ __noinline__ void choose_by_lists(const Choice<T, KL>& c) {
   }
 }
 
-// The bases of these rows, to 1e-9.  Called by the whole CTA.
+// A CTA's share of the sums that sm.call names, in whole numbers, to the first CTA's sm.part
+// (upper halves) and sm.red, which nothing else needs any more.  Called by the whole CTA.
 template <typename T, int KL>
-__device__ __noinline__ void sum_again(const Choice<T, KL>& c, unsigned rows, float score) {
-  SelectSmem<KL>& sm = c.sm;
+__device__ __noinline__ void sum_share(const BeamSelectArgs& a, SelectSmem<KL>& sm, int r, int rank,
+                                       int ctas) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int V = c.a.vocab, NB = c.a.blocks_per_row;
+  const int V = a.vocab, step = ctas * kThreads;
+  struct Sums {
+    uint64_t hi[kMaxBeams][kWarps], lo[kMaxBeams][kWarps];
+  };
+  static_assert(sizeof(Sums) <= sizeof(sm.edges), "no load uses it meanwhile");
+  static_assert(sizeof(sm.part) == 8 * kMaxBeams * kMaxCtas && sizeof(sm.red) == sizeof(sm.part),
+                "a number for each row and CTA");
+  Sums& all = *reinterpret_cast<Sums*>(sm.edges);
   if (threadIdx.x < 64)
     sm.table.t[threadIdx.x] = __double2uint_rn(exp2(threadIdx.x / 64.0) * 0x1p31);
   __syncthreads();
-  // (the rows' sums one behind another, by all threads; then a lane takes each row's logarithm)
-  struct Sums {
-    uint64_t hi[kMaxBeams][kWarps], lo[kMaxBeams][kWarps];
-    float top[kMaxBeams];
-  };
-  static_assert(sizeof(Sums) <= sizeof(sm.edges), "no load uses it meanwhile");
-  Sums& all = *reinterpret_cast<Sums*>(sm.edges);
 #pragma unroll 1
-  for (unsigned todo = rows; todo; todo &= todo - 1) {
+  for (unsigned todo = sm.call.rows; todo; todo &= todo - 1) {
     const int w = __ffs(todo) - 1;
-    const Row<T> row(c.a, c.r, w);
-    // (the row's maximum: a reference that the order of the logits does not change)
-    float top = -INFINITY;
-#pragma unroll 1
-    for (int b = lane; b < NB; b += 32) top = fmaxf(top, c.block_max[w * NB + b]);
-    top = warp_max(top);
+    const Row<T> row(a, r, w);
+    const float top = sm.call.top[w];
     FixedSum sum;
-    // (eight loads are under way behind the eight at hand: 103 requests of 6 x 50497, of
-    // which one or two sum a few rows again, 75 us; without, 88; with two loads and 64-bit
-    // conversions 110; with no row in doubt 35)
-    auto get = [&](int x0, float (&x)[8]) {
+    // (eight loads are under way behind the eight at hand)
+    auto get = [&](int x0, float (&x)[8]) {  // (a row has up to 2^30 elements)
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        x[i] = x0 + i * kThreads < V ? Elem<T>::load(row.p, x0 + i * kThreads) : -INFINITY;
+        x[i] = x0 + i * step < V ? Elem<T>::load(row.p, x0 + i * step) : -INFINITY;
     };
     float x[8], next[8];
-    get(threadIdx.x, next);
+    int x0 = rank * kThreads + threadIdx.x;
+    get(x0, next);
 #pragma unroll 1
-    for (int x0 = threadIdx.x; x0 < V; x0 += 8 * kThreads) {
+    for (; x0 < V; x0 += 8 * step) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) x[i] = next[i];
-      get(x0 + 8 * kThreads, next);
+      get(x0 + 8 * step, next);
 #pragma unroll
       for (int i = 0; i < 8; ++i) add_exp(sum, sm.table, sane(x[i]), top);
     }
@@ -642,22 +647,81 @@ __device__ __noinline__ void sum_again(const Choice<T, KL>& c, unsigned rows, fl
     if (lane == 0) {
       all.hi[w][warp] = sum.hi;
       all.lo[w][warp] = sum.lo;
-      all.top[w] = top;
     }
   }
   __syncthreads();
-  if (threadIdx.x < kMaxBeams && (rows >> lane & 1)) {
+  if (threadIdx.x < kMaxBeams && (sm.call.rows >> lane & 1)) {
     FixedSum sum;
 #pragma unroll 1
     for (int i = 0; i < kWarps; ++i) {
       sum.hi += all.hi[lane][i];
       sum.lo += all.lo[lane][i];
     }
+    st_remote(mapa_shared(smem_u32(&sm.part[lane][rank]), 0), sum.hi);
+    st_remote(mapa_shared(smem_u32(&sm.red[lane][rank]), 0), sum.lo);
+  }
+  __syncwarp();
+}
+
+// Every other CTA of the cluster learns of sm.call.  Called by the whole first CTA.
+template <int KL>
+__device__ __forceinline__ void pass_on_call(SelectSmem<KL>& sm, int ctas) {
+  constexpr int kWords = sizeof(sm.call) / 4;
+  __syncthreads();
+  const float* const word = reinterpret_cast<const float*>(&sm.call);
+  for (int t = threadIdx.x; t < kWords * (ctas - 1); t += kThreads)
+    st_remote(mapa_shared(smem_u32(word + t % kWords), 1 + t / kWords), word[t % kWords]);
+  __syncwarp();
+}
+
+// The bases of these rows, to 1e-9, by so many CTAs of the cluster: the first one's part in
+// it.  What has been gathered gets its keys anew: it has the choices all the same, since the
+// sums move by less than its bound allows for.
+template <typename T, int KL>
+__device__ __noinline__ void sum_again(const Choice<T, KL>& c, unsigned rows, float score,
+                                       int ctas, int picked) {
+  SelectSmem<KL>& sm = c.sm;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int NB = c.a.blocks_per_row;
+  if (threadIdx.x == 0) sm.call.rows = rows;
+#pragma unroll 1
+  for (int w = warp; w < c.a.num_beams; w += kWarps) {
+    if (!(rows >> w & 1)) continue;
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int b = lane; b < NB; b += 32) top = fmaxf(top, c.block_max[w * NB + b]);
+    top = warp_max(top);
+    if (lane == 0) sm.call.top[w] = top;
+  }
+  pass_on_call(sm, ctas);
+  if (ctas > 1) cluster_sync();
+  sum_share<T, KL>(c.a, sm, c.r, 0, ctas);
+  if (ctas > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (threadIdx.x < kMaxBeams && (rows >> lane & 1)) {
+    const uint64_t* const his = reinterpret_cast<const uint64_t*>(sm.part[lane]);
+    const uint64_t* const los = reinterpret_cast<const uint64_t*>(sm.red[lane]);
+    FixedSum sum;
+#pragma unroll 1
+    for (int i = 0; i < ctas; ++i) {
+      sum.hi += his[i];
+      sum.lo += los[i];
+    }
     const double ln = log(static_cast<double>(sum.hi) * 0x1p-18 +
                           static_cast<double>(sum.lo) * 0x1p-50);
     const float hi = static_cast<float>(ln);
     sm.base[lane] =
-        base_of(score, all.top[lane], make_float2(hi, static_cast<float>(ln - hi)));
+        base_of(score, sm.call.top[lane], make_float2(hi, static_cast<float>(ln - hi)));
+  }
+  if (threadIdx.x == 0) sm.doubtful = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < picked; i += kThreads) {
+    const int w = sm.pick.idx[i] / c.a.vocab;
+    const int token = static_cast<int>(sm.pick.idx[i]) - w * c.a.vocab;
+    if (rows >> w & 1)
+      sm.pick.key[i] = value_key(sm.base[w], Elem<T>::load(Row<T>(c.a, c.r, w).p, token));
   }
   __syncthreads();
 }
@@ -682,6 +746,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int e = threadIdx.x; e < W * NB; e += kThreads) block_max[e] = -INFINITY;
   for (int e = threadIdx.x; e < W * kWarps; e += kThreads)
     sm.red[e / kWarps][e % kWarps] = make_float2(-FLT_MAX, 0.f);
+  if (threadIdx.x == 0) sm.call.rows = 0;
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   griddep_launch_dependents();
   griddep_wait();
@@ -820,7 +886,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   }
   cluster_sync();
-  if (rank != 0) return;
+  const int hands = a.all_sum ? C : 1;
+  if (rank != 0) {  // a hand with rows whose sums are taken again, until the choice is made
+    while (a.all_sum) {
+      cluster_sync();
+      if (sm.call.rows == 0) return;
+      sum_share<T, KL>(a, sm, r, rank, C);
+      cluster_sync();
+    }
+    return;
+  }
 
   // ---- the first CTA: s - lse of each row
   for (int w = warp; w < W; w += kWarps) {
@@ -916,43 +991,55 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     const int picked = sm.picked;
-    if (blocks <= kMaxPicked && picked <= kMaxPicked) {
-      // in order: eight lanes compare one with all
+    const bool few = blocks <= kMaxPicked && picked <= kMaxPicked;
+    unsigned again;
+    do {
+      if (few) {
+        // in order: eight lanes compare one with all
 #pragma unroll 1
-      for (int i0 = 0; i0 < picked; i0 += kThreads / 8) {
-        const int i = i0 + threadIdx.x / 8;
-        int place = 0;
-        if (i < picked) {
-          const uint64_t k = sm.pick.key[i];
-          const uint32_t id = sm.pick.idx[i];
+        for (int i0 = 0; i0 < picked; i0 += kThreads / 8) {
+          const int i = i0 + threadIdx.x / 8;
+          int place = 0;
+          if (i < picked) {
+            const uint64_t k = sm.pick.key[i];
+            const uint32_t id = sm.pick.idx[i];
 #pragma unroll 1
-          for (int o = threadIdx.x & 7; o < picked; o += 8)
-            place += better(sm.pick.key[o], sm.pick.idx[o], k, id);
-        }
+            for (int o = threadIdx.x & 7; o < picked; o += 8)
+              place += better(sm.pick.key[o], sm.pick.idx[o], k, id);
+          }
 #pragma unroll
-        for (int off = 1; off < 8; off <<= 1) place += __shfl_xor_sync(0xffffffffu, place, off);
-        if (i < picked && (threadIdx.x & 7) == 0) {
-          sm.key[place] = sm.pick.key[i];
-          sm.idx[place] = sm.pick.idx[i];
+          for (int off = 1; off < 8; off <<= 1) place += __shfl_xor_sync(0xffffffffu, place, off);
+          if (i < picked && (threadIdx.x & 7) == 0) {
+            sm.key[place] = sm.pick.key[i];
+            sm.idx[place] = sm.pick.idx[i];
+          }
         }
-      }
-      if (threadIdx.x == 0) sm.found = picked;
-      __syncthreads();
-      // order between rows, where their sums may not tell
-      if (threadIdx.x < K)
+        if (threadIdx.x == 0) sm.found = picked;
+        __syncthreads();
+        // order between rows, where their sums may not tell
+        if (threadIdx.x < K)
 #pragma unroll 1
-        for (int i = threadIdx.x, j = i + 1;
-             j < picked && key_gap(sm.key[i], sm.key[j]) < a.margin; ++j)
-          c.doubt(sm.idx[i] / V, sm.idx[j] / V);
-    } else {
-      __syncthreads();  // (sm.pick ends here)
-      choose_by_lists(c);
-    }
-    __syncthreads();
-    const unsigned again = sm.doubtful & ~c.exact;
+          for (int i = threadIdx.x, j = i + 1;
+               j < picked && key_gap(sm.key[i], sm.key[j]) < a.margin; ++j)
+            c.doubt(sm.idx[i] / V, sm.idx[j] / V);
+      } else {
+        __syncthreads();  // (sm.pick ends here)
+        choose_by_lists(c);
+      }
+      __syncthreads();
+      again = sm.doubtful & ~c.exact;
+      if (!again) break;
+      sum_again(c, again, score, hands, few ? picked : 0);
+      c.exact |= again;
+    } while (few);
     if (!again) break;
-    sum_again(c, again, score);
-    c.exact |= again;
+  }
+  if (hands > 1) {  // the others may go
+    if (c.exact != ended) {
+      if (threadIdx.x == 0) sm.call.rows = 0;
+      pass_on_call(sm, hands);
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   }
 
   // ---- the choices
@@ -971,6 +1058,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (a.out_finished)
       a.out_finished[at] = w >= 0 && (((ended >> w) & 1) || token == a.end_token);
   }
+  __syncwarp();
+  if (hands > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <typename T, int KL>
@@ -1064,6 +1153,10 @@ cudaError_t launch(BeamSelectArgs a, int num_sms, cudaStream_t stream) {
   const double err = 0x1p-24 * (4 + 1.3 * (kMove + ln_v) + 10 + static_cast<double>(lane_loads) +
                                 5 + 4 + 4 + 4 * (5 + 1.3 * kMove) + 2 * ln_v);
   a.margin = static_cast<float>(2 * err);
+  // Where a second sum of two rows is likely (neighbours among the best candidates nearer
+  // than the margin, one pair in a thousand or so) or takes long, the cluster stays for it: 0.5
+  // us of every call, against 53 us of one CTA's time for rows of 131072 in fp32.
+  a.all_sum = static_cast<int64_t>(a.num_requests) * a.num_choices * a.vocab >= 1 << 21;
   const Launch<T, KL> l(a.num_requests, ctas, a.num_beams * a.blocks_per_row * 4, stream);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, beam_select_kernel<T, KL>, a);
   return e != cudaSuccess ? e : cudaGetLastError();
