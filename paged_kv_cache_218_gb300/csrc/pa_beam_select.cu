@@ -12,9 +12,9 @@
 // near behind (11 elements per cycle and SM arrive, 16 exponentials leave).  So
 // the pass does as little as it can per element: its exponential for the sum, and
 // a maximum.  Behind it comes a chain of short steps on one SM.  64 requests of
-// 4 x 131072 in bf16 (67 MB) take 19.3 us, 12.7 of them the pass (6.3 TB/s once it
-// runs) and 5.6 the choice; 16 of 16 x 131072 in fp32 (134 MB) 33.0; one of 4 x 32000
-// 6.3, a launch and some eight dependent round trips.
+// 4 x 131072 in bf16 (67 MB) take 19.8 us, 12.7 of them the pass (6.3 TB/s once it
+// runs) and 5.6 the choice; 16 of 16 x 131072 in fp32 (134 MB) 32.9; one of 4 x 32000
+// 6.6, a launch and some eight dependent round trips.
 //
 // A cluster serves a request, its CTAs take a share of every row, a warp 1024 bf16 (512
 // fp32) elements at a time, twice 32 bytes a lane; the maxima of such blocks and the rows'
@@ -35,8 +35,10 @@
 // hangs on lse_w, which the pass knows to `margin` / 2: values are kept as sums
 // of two floats (48 bits), and where two beams' candidates around the choice are
 // nearer than `margin`, those rows' sums are taken again, to 1e-9: exponentials by
-// table and short polynomial (Tang's method), added as whole numbers,
-// so that equal logits in whatever order and place give equal sums.
+// table and short polynomial (Tang's method), added as whole numbers, so that equal
+// logits in whatever order and place give equal sums.  The cluster's CTAs wait for their
+// share of that where it is likely (two rows of 131072 in fp32: 9 us more, one CTA 53;
+// 103 requests of 6 x 50497, two CTAs each, 58 us, of which 35 without doubts).
 //
 // NaN and +inf logits count as -inf: no candidates, no part of the sum.
 #include <float.h>
@@ -1028,7 +1030,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       __syncthreads();
       again = sm.doubtful & ~c.exact;
-      if (!again) break;
+      if (__builtin_expect(!again, 1)) break;
       sum_again(c, again, score, hands, few ? picked : 0);
       c.exact |= again;
     } while (few);
@@ -1154,8 +1156,9 @@ cudaError_t launch(BeamSelectArgs a, int num_sms, cudaStream_t stream) {
                                 5 + 4 + 4 + 4 * (5 + 1.3 * kMove) + 2 * ln_v);
   a.margin = static_cast<float>(2 * err);
   // Where a second sum of two rows is likely (neighbours among the best candidates nearer
-  // than the margin, one pair in a thousand or so) or takes long, the cluster stays for it: 0.5
-  // us of every call, against 53 us of one CTA's time for rows of 131072 in fp32.
+  // than the margin, one pair in a thousand or so) or takes long, the cluster stays for it:
+  // 0.5 us of every call (64 of 4 x 131072 19.8 / 19.3, 37 of 3 x 50001 10.3 / 9.7),
+  // against 53 us of one CTA's time for two rows of 131072 in fp32.
   a.all_sum = static_cast<int64_t>(a.num_requests) * a.num_choices * a.vocab >= 1 << 21;
   const Launch<T, KL> l(a.num_requests, ctas, a.num_beams * a.blocks_per_row * 4, stream);
   const cudaError_t e = cudaLaunchKernelEx(&l.cfg, beam_select_kernel<T, KL>, a);

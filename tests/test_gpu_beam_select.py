@@ -163,6 +163,36 @@ def test_beams_a_rounding_apart(pa, dtype, steps):
     c.check()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("R", [1, 3, 40, 160])
+@pytest.mark.parametrize("few", [True, False])
+def test_sums_taken_again_by_whole_clusters(pa, dtype, R, few):
+    """Beams of the same logits in another order, a rounding apart or equal, in calls large
+    enough for every CTA of a cluster (of 16, 13, 7, 1) to take its share; few: candidates that
+    are gathered, or so many equal ones that lists find them.  Some requests have no doubt."""
+    V, K = 70001, 33
+    g = gen(R)
+    row = 2 * torch.randn(V, generator=g, device="cuda") if few else \
+        torch.randint(-3, 2, (V,), generator=g, device="cuda").float()
+    x = torch.stack([row[torch.randperm(V, generator=g, device="cuda")]
+                     for _ in range(4)]).to(dtype)[None].expand(R, 4, V).contiguous()
+    s = torch.full((R, 4), -7.0, device="cuda")
+    s[:, 1] = torch.nextafter(s[:, 1], torch.zeros_like(s[:, 1]))
+    s[::3, 1:] -= torch.tensor([20.0, 40.0, 60.0], device="cuda")
+    c = Case(x, s, K)
+    c.run(pa)
+    # (one request of each kind, and that all of a kind are the same)
+    for i in range(R):
+        first = 0 if i % 3 == 0 else 1
+        for t in (c.parents, c.tokens, c.out_scores):
+            assert torch.equal(t[i], t[first])
+    n = min(R, 2)
+    c.logits, c.scores = x[:n], s[:n]
+    c.parents, c.tokens, c.out_scores, c.marks = (
+        t[:n] for t in (c.parents, c.tokens, c.out_scores, c.marks))
+    c.check()
+
+
 def test_displaced_by_the_last_choice_s_own_row(pa):
     """Beam 1's best lies a rounding above beam 0's K-th candidate, which ties with more of
     its own row: the K + 1 best of an fp32 pass may all be beam 0's."""
