@@ -45,6 +45,9 @@ constexpr uint64_t kSettleNs = 1000000;  // far longer than any copy takes
 // fp32, so that no visible score lies below it; hidden scores (-inf) weigh 0.
 constexpr float kFloor = -0x1.fffff0p127f;
 constexpr float kFarScore = 0x1p31f;  // (log2 units)
+// Weights, each the sum of two bf16 numbers, lie over their scores: of 64 columns the upper
+// parts of 64 keys take the first 32, the lower ones the others.
+constexpr uint32_t kLowCols = 32;
 
 // Shared memory of one CTA: Q tiles, K and V tiles (a pair's CTAs hold half of each), block
 // ids of both loaders, the softmax's exchange, barriers.  Small groups (kQRows > 0: at most
@@ -268,6 +271,10 @@ __global__ void __launch_bounds__(512, 1)
                           const __grid_constant__ CUtensorMap tm_v, const SharedArgs a) {
   using P = SPlan<CG, kQRows>;
   constexpr int kNK = P::kNK, kNV = P::kNV, kNQ = P::kNQ;
+  // Up to 16 query rows: the lower parts of row r's weights are row r + 16, so that one
+  // product takes both, and that row's lane computes half of the weights.
+  constexpr bool kFold = kQRows > 0;
+  static_assert(kQRows <= 16, "rows of a half warp");
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
@@ -649,18 +656,24 @@ __global__ void __launch_bounds__(512, 1)
             if (ok) {
               if (zeroed) fence_acq_rel_cluster();  // the peer's zeroed rows
               tc_fence_after();
-              if (blocks == 8) {
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                  tc_mma_f16_tmem_a<CG>(tmem + kTmemO, ta + (ks >> 2) * 64 + (ks & 3) * 8,
-                                       dv + ((ks * kBlockBytes) >> 4), idesc_o,
-                                       (jp > 0 || ks > 0) ? 1u : 0u);
-              } else {
+              // (upper parts, then lower ones; where those are other rows, all at once)
 #pragma unroll 1
-                for (int ks = 0; ks < blocks; ++ks)
-                  tc_mma_f16_tmem_a<CG>(tmem + kTmemO, ta + (ks >> 2) * 64 + (ks & 3) * 8,
-                                       dv + ((ks * kBlockBytes) >> 4), idesc_o,
-                                       (jp > 0 || ks > 0) ? 1u : 0u);
+              for (int part = 0; part < (kFold ? 1 : 2); ++part) {
+                const uint32_t tp = ta + part * kLowCols;
+                const bool more = jp > 0 || part > 0;
+                if (blocks == 8) {
+#pragma unroll
+                  for (int ks = 0; ks < 8; ++ks)
+                    tc_mma_f16_tmem_a<CG>(tmem + kTmemO, tp + (ks >> 2) * 64 + (ks & 3) * 8,
+                                         dv + ((ks * kBlockBytes) >> 4), idesc_o,
+                                         (more || ks > 0) ? 1u : 0u);
+                } else {
+#pragma unroll 1
+                  for (int ks = 0; ks < blocks; ++ks)
+                    tc_mma_f16_tmem_a<CG>(tmem + kTmemO, tp + (ks >> 2) * 64 + (ks & 3) * 8,
+                                         dv + ((ks * kBlockBytes) >> 4), idesc_o,
+                                         (more || ks > 0) ? 1u : 0u);
+                }
               }
               commit(bar_o_done + 8 * p_buf);
               commit(bar_v_empty + 8 * p_vslot);
@@ -712,6 +725,7 @@ __global__ void __launch_bounds__(512, 1)
                   : -1;
       wait_warp(out_bar, out_phase, abort_flag, a);
       tc_fence_after();
+      if constexpr (kFold) out_l += __shfl_xor_sync(0xffffffffu, out_l, 16);
       red_sum[hc * 128 + r] = out_l;
       named_barrier(1 + qd, 64);
       const float l_tot = out_l + red_sum[(hc ^ 1) * 128 + r];
@@ -722,6 +736,12 @@ __global__ void __launch_bounds__(512, 1)
       for (int c = 0; c < 2; ++c) {
         uint32_t (&w)[32] = *reinterpret_cast<uint32_t(*)[32]>(&v[0]);
         tmem_ld32(ocol + 32 * c, w);
+        if constexpr (kFold) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            w[i] = __float_as_uint(__uint_as_float(w[i]) +
+                                   __shfl_xor_sync(0xffffffffu, __uint_as_float(w[i]), 16));
+        }
         if (good) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) stg32(to + 32 * c + 8 * q, &w[8 * q]);
@@ -791,6 +811,7 @@ __global__ void __launch_bounds__(512, 1)
             }
           }
           tmem_ld64_max(sc, v, mloc);
+          if constexpr (kFold) mloc = __shfl_sync(0xffffffffu, mloc, lane & 15);
           red_max[(b * 2 + hc) * 128 + r] = mloc;
           named_barrier(1 + qd, 64);
           // (scale > 0 keeps the order of scores)
@@ -810,16 +831,38 @@ __global__ void __launch_bounds__(512, 1)
           m_run2 = move ? m_new2 : m_run2;
           n_run = move ? n_new : n_run;
           uint64_t rsp[2] = {0, 0};
-          uint32_t pk[32];
+          uint32_t pk[32], low[32];
           const uint64_t sl2 = f32x2(slx, slx), nm2 = f32x2(-n_run, -n_run);
-#pragma unroll
-          for (int i = 0; i < 64; i += 2) {
+          // weights of two keys, their upper and their lower parts
+          auto weigh = [&](uint32_t s0, uint32_t s1, int at, uint32_t& hi, uint32_t& lo) {
             // -inf (hidden) gives exactly 0: n_run is finite
-            const uint64_t s2 = f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            const uint64_t s2 = f32x2(__uint_as_float(s0), __uint_as_float(s1));
             const float2 x = f32x2_parts(fma2(s2, sl2, nm2));
             const float e0 = fast_exp2(x.x), e1 = fast_exp2(x.y);
-            rsp[(i >> 1) & 1] = add2(rsp[(i >> 1) & 1], f32x2(e0, e1));
-            pk[i / 2] = pack_bf16x2(e0, e1);
+            rsp[at] = add2(rsp[at], f32x2(e0, e1));
+            hi = pack_bf16x2(e0, e1);
+            lo = pack_bf16x2(e0 - __uint_as_float(hi << 16),
+                             e1 - __uint_as_float(hi & 0xffff0000u));
+          };
+          if constexpr (kFold) {
+            const bool lower = lane >= 16;  // lower parts, and the second 32 keys
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const uint32_t theirs = __shfl_sync(0xffffffffu, v[32 + i], lane & 15);
+              v[i] = lower ? theirs : v[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              uint32_t hi, lo;
+              weigh(v[2 * i], v[2 * i + 1], i & 1, hi, lo);
+              const uint32_t theirs = __shfl_xor_sync(0xffffffffu, lower ? hi : lo, 16);
+              pk[i] = lower ? theirs : hi;
+              pk[16 + i] = lower ? lo : theirs;
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              weigh(v[2 * i], v[2 * i + 1], i & 1, pk[i], low[i]);
           }
           const float2 rs = f32x2_parts(add2(rsp[0], rsp[1]));
           l_run = l_run * alpha + (rs.x + rs.y);
@@ -839,6 +882,7 @@ __global__ void __launch_bounds__(512, 1)
             }
           }
           tmem_st32(sc, pk);
+          if constexpr (!kFold) tmem_st32(sc + kLowCols, low);
         }
         if (first && pending) next_nkt = write_out(k + 1);
         if (last) break;
