@@ -540,8 +540,8 @@ int pa_qk_norm_rope_cache_fp8(void *q_out, void *k_out, const void *q, const voi
  *   workspace  device, pa_decode_shared_workspace_size bytes, 256-byte aligned, with
  *              any content; one call in flight per workspace
  * head_dim must be 128; the V of tokens that some member of the group sees must be
- * finite; other slots may hold anything.  Equal calls give equal bits.  Weights over
- * the prefix are rounded to bf16 (each within 2^-8 of itself), as in the prefill.
+ * finite; other slots may hold anything.  Equal calls give equal bits.  Weights enter
+ * the tensor cores as sums of two bf16 numbers (each within 2^-16 of itself).
  * Groups or shared_blocks out of range set PA_DEVERR_GROUP and are clamped: members
  * past max_group_size attend all their blocks on their own.  (Batches whose tables
  * name up to 96 MB of keys and values do not look at the groups: each sequence is

@@ -21,13 +21,18 @@
 //  * A piece (a unit's key tiles in a team's range) leaves its reference maximum, sum
 //    and weighted values, in fp32 and undivided, for the join behind.
 //  * Warps whose 32 rows no member fills wait for scores and pass them on unread.
+//  * P is the sum of two bf16 numbers (to 2^-16 of itself), as in the decode of the own
+//    parts, so that the output does not depend on which of both reads a key.  One bf16
+//    took 78 / 81 / 57 us in the cases below.  Of groups of up to 16 rows the lower parts
+//    are rows of their own beside the upper ones, multiplied at no cost, and their lanes
+//    take half of the exponentials (with two products instead 90 us for 82).
 //
 // What bounds it: HBM.  In the steady state lone CTAs read 7.3 TB/s (0.65 us for every
-// 72 tiles of 64 KB), pairs with 256 rows take 0.79 us a tile, the tensor pipe and its
-// hand-overs.  The first 8 us go to round trips: offsets, lengths, block ids, keys.
+// 72 tiles of 64 KB), pairs with 256 rows wait for the tensor pipe and its hand-overs.
+// The first 8 us go to round trips: offsets, lengths, block ids, keys.
 // With 32 query and 8 kv heads of 128: 64 groups of 4 sequences behind 256 to 2048 tokens
-// (392 MB with their own parts) 77 us, 5.1 TB/s; 32 sequences behind 65536 (273 MB) 57 us;
-// 256 behind 8192 (322 MB, of which 294 are own parts) 81 us.
+// (392 MB with their own parts) 82 us, 4.8 TB/s; 32 sequences behind 65536 (273 MB) 59 us;
+// 256 behind 8192 (322 MB, of which 294 are own parts) 88 us.
 #include <limits.h>
 
 #include <mutex>
