@@ -403,7 +403,7 @@ struct Choice {
   int r;
   unsigned live, ended;
   unsigned exact;  // rows whose base is known to 1e-9
-  float bound;     // no candidate below it is chosen, and what sums and roundings are off
+  float bound;     // finite: no candidate below it is chosen; and what sums and roundings are off
   float slack;
 
   // the value of a block's best candidate
@@ -942,11 +942,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     far = warp_max(far < INFINITY ? far : 0.f);
     auto set_bound = [&]() {
       c.slack = (fabsf(least) + far) * 0x1p-20f + 2 * a.margin;
-      c.bound = least > -INFINITY ? least - c.slack : -FLT_MAX;
+      // (finite, so that blocks without a candidate, -inf, lie below it)
+      c.bound = least > -INFINITY ? fmaxf(least - c.slack, -FLT_MAX) : -FLT_MAX;
       if (least == -INFINITY) c.slack = INFINITY;
     };
     set_bound();
-    // ---- the blocks that reach it, and of them the candidates
+    // ---- the blocks that reach it (of an ended beam, its token's alone: each is listed
+    // once, and so is each candidate), and of them the candidates
     each_entry([&](int e, float v) {
       if (v >= c.bound) {
         const int at = atomicAdd(&sm.blocks, 1);
