@@ -30,7 +30,7 @@ struct BeamSelectArgs {
   int blocks_per_row;  // entries of the block maxima for each beam
   uint32_t blocks_inverse;  // 2^32 / blocks_per_row, rounded up
   int all_sum;         // the whole cluster takes sums again
-  float margin;        // values nearer than this are compared again, more exactly
+  float margin;        // (halved) values nearer than this are compared again, more exactly
 };
 
 // Tables, lengths and partly filled blocks after a selection (pa_beam_reorder).

@@ -32,9 +32,9 @@
 // theirs), then those.
 //
 // Exactness.  Within a row the logits themselves give the order.  Between rows it
-// hangs on lse_w, which the pass knows to `margin` / 2: values are kept as sums
+// hangs on lse_w, which the pass knows to a bound: values are kept as sums
 // of two floats (48 bits), and where two beams' candidates around the choice are
-// nearer than `margin`, those rows' sums are taken again, to 1e-9: exponentials by
+// nearer than twice that (`margin`), those rows' sums are taken again, to 1e-9: exponentials by
 // table and short polynomial (Tang's method), added as whole numbers, so that equal
 // logits in whatever order and place give equal sums.  The cluster's CTAs wait for their
 // share of that where it is likely (two rows of 131072 in fp32: 9 us more, one CTA 53;
@@ -60,6 +60,8 @@ constexpr float kMove = 5.5f;  // a lane's reference moves when passed by this m
 constexpr int kMaxCtas = 16;   // of a cluster
 constexpr int kMaxEntries = 8192;  // block maxima of a request
 constexpr float kLog2e = 1.4426950408889634f;
+// Values are kept halved (see base_of): the largest finite one, and a number below all.
+constexpr float kMost = 0.5f * FLT_MAX, kLowest = -0.75f * FLT_MAX;
 
 __device__ __forceinline__ void ldg32(const void* p, uint32_t (&v)[8]) {
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -209,15 +211,15 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {  // (exact)
   const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
   return make_float2(s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t)));
 }
-// score - top - ln
+// Half of score - top - ln: the whole may lie past fp32 where it and a logit do not.
 __device__ __forceinline__ float2 base_of(float score, float top, float2 ln) {
-  const float2 a = two_sum(score, -top), b = two_sum(a.x, -ln.x);
-  return two_sum(b.x, (b.y + a.y) - ln.y);
+  const float2 a = two_sum(0.5f * score, -0.5f * top), b = two_sum(a.x, -0.5f * ln.x);
+  return two_sum(b.x, (b.y + a.y) - 0.5f * ln.y);
 }
 __device__ __forceinline__ uint64_t value_key(float2 base, float x) {
-  const float2 s = two_sum(base.x, x);
+  const float2 s = two_sum(base.x, 0.5f * x);
   const float2 v = two_sum(s.x, __fadd_rn(s.y, base.y));
-  if (!(v.x > -INFINITY && v.x < INFINITY)) return 0;
+  if (!(fabsf(v.x) <= kMost)) return 0;
   return static_cast<uint64_t>(ordered(v.x)) << 32 | ordered(v.y);
 }
 // How far one value lies above another.
@@ -318,7 +320,7 @@ struct SelectSmem {
   uint4 edges[kThreads][2];          // of rows, elements on their way to registers
   float2 part[kMaxBeams][kMaxCtas];  // rows' (maximum, sum) of each CTA
   float2 red[kMaxBeams][kWarps];     // and of each warp
-  float2 base[kMaxBeams];            // s - lse in two floats
+  float2 base[kMaxBeams];            // (s - lse) / 2 in two floats
   float group[kThreads / kGroups][kGroups];
   uint32_t group_key[4][kGroups / 4 + 4];  // (quarters in different banks)
   union {
@@ -434,7 +436,7 @@ struct Choice {
 #pragma unroll
     for (int i = 0; i < kVecs * E::kVec / 2; ++i) {
       const float2 x = E::pair(v[i / (E::kVec / 2)], i % (E::kVec / 2));
-      best[i % 4] = fmaxf(best[i % 4], base + fmaxf(sane(x.x), sane(x.y)));
+      best[i % 4] = fmaxf(best[i % 4], __fmaf_rn(0.5f, fmaxf(sane(x.x), sane(x.y)), base));
     }
   }
   // Load number `part` of block e: f(key, index) for the candidates that may reach the
@@ -452,7 +454,7 @@ struct Choice {
     uint32_t v[kVecs][8];
     const int e0 = fetch(row, w, e, part, lane, v);
     unsigned hits = 0;
-    const float least = fmaxf((bound - base.x) - slack, -FLT_MAX);
+    const float least = fmaxf(2.f * ((bound - base.x) - slack), -FLT_MAX);
 #pragma unroll
     for (int i = 0; i < kVecs * E::kVec / 2; ++i) {
       const float2 x = E::pair(v[i / (E::kVec / 2)], i % (E::kVec / 2));
@@ -486,7 +488,7 @@ struct Choice {
     if (!over) {
       uint32_t v[kVecs][8];
       e0 = fetch(row, w, e, part, lane, v);
-      const float least = fmaxf((bound - base.x) - slack, -FLT_MAX);
+      const float least = fmaxf(2.f * ((bound - base.x) - slack), -FLT_MAX);
 #pragma unroll
       for (int i = 0; i < kVecs * E::kVec / 2; ++i) {
         const float2 x = E::pair(v[i / (E::kVec / 2)], i % (E::kVec / 2));
@@ -899,10 +901,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
 
-  // ---- the first CTA: s - lse of each row
+  // ---- the first CTA: (s - lse) / 2 of each row
   for (int w = warp; w < W; w += kWarps) {
     const float mine = __shfl_sync(0xffffffffu, score, w);
-    float2 base = make_float2(mine, 0.f);
+    float2 base = make_float2(0.5f * mine, 0.f);
     if ((live >> w) & 1) {
       const float2 x = lane < C ? sm.part[w][lane] : make_float2(-FLT_MAX, 0.f);
       const float top = warp_max(x.x);
@@ -925,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   auto each_entry = [&](auto f) {
 #pragma unroll 4
     for (int e = threadIdx.x; e < entries; e += kThreads)
-      f(e, sm.base[beam_of(a, e)].x + block_max[e]);
+      f(e, __fmaf_rn(0.5f, block_max[e], sm.base[beam_of(a, e)].x));
   };
 
   while (true) {
@@ -943,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto set_bound = [&]() {
       c.slack = (fabsf(least) + far) * 0x1p-20f + 2 * a.margin;
       // (finite, so that blocks without a candidate, -inf, lie below it)
-      c.bound = least > -INFINITY ? fmaxf(least - c.slack, -FLT_MAX) : -FLT_MAX;
+      c.bound = least > -INFINITY ? fmaxf(least - c.slack, kLowest) : kLowest;
       if (least == -INFINITY) c.slack = INFINITY;
     };
     set_bound();
@@ -1054,7 +1056,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (i < sm.found && sm.key[i] != 0) {  // (key 0: its value lies past fp32)
       w = sm.idx[i] / V;
       token = sm.idx[i] - static_cast<uint32_t>(w) * V;
-      value = unordered(static_cast<uint32_t>(sm.key[i] >> 32));
+      value = 2.f * unordered(static_cast<uint32_t>(sm.key[i] >> 32));
     }
     a.parents[at] = w;
     a.tokens[at] = token;
@@ -1145,18 +1147,18 @@ cudaError_t launch(BeamSelectArgs a, int num_sms, cudaStream_t stream) {
   int ctas = static_cast<int>(std::min<int64_t>(std::max<int64_t>(most / a.num_requests, 1),
                                                 kMaxCtas));
   if (const cudaError_t e = fit_cluster<T, KL>(a.num_requests, &ctas)) return e;
-  // Twice the error of a row's sum in the pass, relative, all roundings adding up (a step
-  // of fp32 is 2^-24): exponentials 4 steps, their arguments 1.3 |x - m| (a weighted mean of
-  // which is at most ln V, and kMove); the additions of a lane, 10 and one for each load, a
-  // warp, a CTA and a cluster; rescalings by an exponential, 5 and its argument's, once for
-  // a lane (a moved reference shrinks what came before) and at each of the three; the
-  // logarithm's 2 ln V.
+  // The margin of two rows is twice the error of a row's sum in the pass, relative, all
+  // roundings adding up (a step of fp32 is 2^-24): exponentials 4 steps, their arguments
+  // 1.3 |x - m| (a weighted mean of which is at most ln V, and kMove); the additions of a
+  // lane, 10 and one for each load, a warp, a CTA and a cluster; rescalings by an
+  // exponential, 5 and its argument's, once for a lane (a moved reference shrinks what came
+  // before) and at each of the three; the logarithm's 2 ln V.
   const int64_t lane_loads =
       (static_cast<int64_t>(a.num_beams) * (a.blocks_per_row / ctas + 1) / kWarps + 1) << sh;
   const double ln_v = log(static_cast<double>(a.vocab));
   const double err = 0x1p-24 * (4 + 1.3 * (kMove + ln_v) + 10 + static_cast<double>(lane_loads) +
                                 5 + 4 + 4 + 4 * (5 + 1.3 * kMove) + 2 * ln_v);
-  a.margin = static_cast<float>(2 * err);
+  a.margin = static_cast<float>(err);  // (of values that are halved)
   // Where a second sum of two rows is likely (neighbours among the best candidates nearer
   // than the margin, one pair in a thousand or so) or takes long, the cluster stays for it:
   // 0.5 us of every call (64 of 4 x 131072 19.8 / 19.3, 37 of 3 x 50001 10.3 / 9.7),

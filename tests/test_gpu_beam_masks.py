@@ -104,3 +104,25 @@ def test_beams_held_back_by_finite_scores(pa, dtype, low, R, W, V, K):
     c = Case(x, s, K, finished=fin, end=V // 2)
     c.run(pa)
     check(c)
+
+
+@pytest.mark.parametrize("V", [40, 3000, 70000])
+@pytest.mark.parametrize("K", [3, 8, 40])
+def test_far_scores_and_far_logits_together(pa, V, K):
+    """A score and a row's largest logit whose difference leaves fp32 where their candidates'
+    values do not, on either side; beside them an ended and an ordinary beam."""
+    x = torch.full((4, 4, V), -3e38, device="cuda")
+    g = gen(V + K)
+    x[0, 0, 3:9] = torch.tensor([3e38, 2e38, 1e38, 3e38, -1e38, 2.5e38], device="cuda")
+    x[0, 1] = 1e38 * torch.rand(V, generator=g, device="cuda")
+    x[1] = 3.4e38
+    x[1, :, ::2] = 1.7e38
+    x[2] = -3.4e38
+    x[3] = 3e38 * (2 * torch.rand((4, V), generator=g, device="cuda") - 1)
+    s = torch.tensor([[-1e38, -2e38, -5.0, -3e38], [-3.4e38, -3.3e38, -3.4e38, -1.0],
+                      [3e38, 3.4e38, 1e38, -3e38], [-3e38, 3e38, 0.0, -1e38]], device="cuda")
+    fin = torch.zeros((4, 4), dtype=torch.bool, device="cuda")
+    fin[:, 2] = True
+    c = Case(x, s, K, finished=fin, end=1)
+    c.run(pa)
+    check(c)
