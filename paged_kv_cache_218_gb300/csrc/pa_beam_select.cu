@@ -405,9 +405,12 @@ struct Choice {
   int r;
   unsigned live, ended;
   unsigned exact;  // rows whose base is known to 1e-9
-  float bound;     // finite: no candidate below it is chosen; and what sums and roundings are off
-  float slack;
+  float bound;     // finite: no candidate below it is chosen
+  float slack;     // what sums and roundings are off, besides off() of the row
 
+  // What a row's values may be off in fp32 for its base's size.  (The row's own: beams that
+  // are held back by scores of -1e9 leave the others' bound where it is.)
+  static __device__ __forceinline__ float off(float base) { return fabsf(base) * 0x1p-20f; }
   // the value of a block's best candidate
   __device__ __forceinline__ uint64_t entry_key(int e) const {
     return value_key(sm.base[beam_of(a, e)], block_max[e]);
@@ -423,16 +426,17 @@ struct Choice {
       load_edge(row.p, a.vocab, e0, sm.edges[threadIdx.x], v);
     return e0;
   }
-  // Best values among quarters of them (every fourth pair), in fp32.
+  // Best values, at the least, among quarters of them (every fourth pair), in fp32.
   __device__ __forceinline__ void best_of(int e, int part, int lane, float (&best)[4]) const {
     const int w = beam_of(a, e);
     if ((ended >> w) & 1) {
-      if (lane == 0 && part == 0) best[0] = fmaxf(best[0], sm.base[w].x);
+      const float base = sm.base[w].x;
+      if (lane == 0 && part == 0) best[0] = fmaxf(best[0], base - off(base));
       return;
     }
     uint32_t v[kVecs][8];
     fetch(Row<T>(a, r, w), w, e, part, lane, v);
-    const float base = sm.base[w].x;
+    const float base = sm.base[w].x - off(sm.base[w].x);
 #pragma unroll
     for (int i = 0; i < kVecs * E::kVec / 2; ++i) {
       const float2 x = E::pair(v[i / (E::kVec / 2)], i % (E::kVec / 2));
@@ -454,7 +458,7 @@ struct Choice {
     uint32_t v[kVecs][8];
     const int e0 = fetch(row, w, e, part, lane, v);
     unsigned hits = 0;
-    const float least = fmaxf(2.f * ((bound - base.x) - slack), -FLT_MAX);
+    const float least = fmaxf(2.f * ((bound - base.x) - (slack + off(base.x))), -FLT_MAX);
 #pragma unroll
     for (int i = 0; i < kVecs * E::kVec / 2; ++i) {
       const float2 x = E::pair(v[i / (E::kVec / 2)], i % (E::kVec / 2));
@@ -488,7 +492,7 @@ struct Choice {
     if (!over) {
       uint32_t v[kVecs][8];
       e0 = fetch(row, w, e, part, lane, v);
-      const float least = fmaxf(2.f * ((bound - base.x) - slack), -FLT_MAX);
+      const float least = fmaxf(2.f * ((bound - base.x) - (slack + off(base.x))), -FLT_MAX);
 #pragma unroll
       for (int i = 0; i < kVecs * E::kVec / 2; ++i) {
         const float2 x = E::pair(v[i / (E::kVec / 2)], i % (E::kVec / 2));
@@ -923,27 +927,28 @@ __global__ void __launch_bounds__(kThreads, 2)
   Choice<T, KL> c{a, sm, block_max, r, live, ended, ended, 0.f, 0.f};
   __syncthreads();
 
-  // f(entry, value in fp32) for this thread's blocks, those of group threadIdx.x % 128
+  // f(entry, value in fp32, what that may be off) for this thread's blocks, those of group
+  // threadIdx.x % 128
   auto each_entry = [&](auto f) {
 #pragma unroll 4
-    for (int e = threadIdx.x; e < entries; e += kThreads)
-      f(e, __fmaf_rn(0.5f, block_max[e], sm.base[beam_of(a, e)].x));
+    for (int e = threadIdx.x; e < entries; e += kThreads) {
+      const float base = sm.base[beam_of(a, e)].x;
+      f(e, __fmaf_rn(0.5f, block_max[e], base), c.off(base));
+    }
   };
 
   while (true) {
-    // ---- a bound: the L-th best of 128 groups' best blocks, less what sums and
-    // roundings may be off
+    // ---- a bound: the L-th best of 128 groups' best blocks, each at the least that it may
+    // be, less what sums and roundings may be off
     if (threadIdx.x == 0) {
       sm.blocks = sm.picked = sm.found = 0;
       sm.doubtful = 0;
     }
     float best = -INFINITY;
-    each_entry([&](int, float v) { best = fmaxf(best, v); });
+    each_entry([&](int, float v, float off) { best = fmaxf(best, v - off); });
     float least = group_bound(sm, best, L);
-    float far = lane < W ? fabsf(sm.base[lane].x) : 0.f;
-    far = warp_max(far < INFINITY ? far : 0.f);
     auto set_bound = [&]() {
-      c.slack = (fabsf(least) + far) * 0x1p-20f + 2 * a.margin;
+      c.slack = fabsf(least) * 0x1p-20f + 2 * a.margin;
       // (finite, so that blocks without a candidate, -inf, lie below it)
       c.bound = least > -INFINITY ? fmaxf(least - c.slack, kLowest) : kLowest;
       if (least == -INFINITY) c.slack = INFINITY;
@@ -951,8 +956,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     set_bound();
     // ---- the blocks that reach it (of an ended beam, its token's alone: each is listed
     // once, and so is each candidate), and of them the candidates
-    each_entry([&](int e, float v) {
-      if (v >= c.bound) {
+    each_entry([&](int e, float v, float off) {
+      if (v + off >= c.bound) {
         const int at = atomicAdd(&sm.blocks, 1);
         if (at < kMaxPicked) sm.pick.block[at] = e;
       }

@@ -126,3 +126,28 @@ def test_far_scores_and_far_logits_together(pa, V, K):
     c = Case(x, s, K, finished=fin, end=1)
     c.run(pa)
     check(c)
+
+
+@pytest.mark.parametrize("low", [-1e9, float(np.finfo(np.float32).min)])
+def test_held_back_beams_cost_no_more_than_others(pa, low):
+    """Beams 1 .. 3 at a finite lowest score: the call reads their logits, as it does those of
+    ordinary beams, and takes no longer (2 for noise; it took 4.5 times as long)."""
+    R, W, V, K = 64, 4, 131072, 8
+    x = (3 * torch.randn((R, W, V), generator=gen(1), device="cuda")).to(BF16)
+    plain = -5.0 - 3.0 * torch.rand((R, W), generator=gen(2), device="cuda").cumsum(1)
+    held = plain.clone()
+    held[:, 1:] = low
+    best = []
+    for s in (plain, held):
+        c, times = Case(x, s, K), []
+        for _ in range(12):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            c.run(pa)
+            a.record()
+            for _ in range(5):
+                c.run(pa)
+            b.record()
+            b.synchronize()
+            times.append(a.elapsed_time(b))
+        best.append(min(times))
+    assert best[1] < 2 * best[0], best
