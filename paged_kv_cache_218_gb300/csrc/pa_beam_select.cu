@@ -311,6 +311,10 @@ __device__ __forceinline__ void add_exp(FixedSum& sum, const ExpTable& tab, floa
   sum.add(((static_cast<uint64_t>(e) << 19) + (ep >> 19)) >> -(k >> 6));
 }
 
+// e^(x - m) as 2^((x - m) log2 e) in fp32, steps (2^-24) of itself that it may be off for each
+// unit of |x - m|: the difference is rounded, the product is, and log2 e is 0.22 steps off.
+constexpr double kArgSteps = 2.3;
+
 constexpr int kGroups = 128;     // of block maxima, whose best bound the choice
 constexpr int kMaxPicked = 256;  // blocks, and candidates, that are gathered unsorted
 
@@ -1154,15 +1158,16 @@ cudaError_t launch(BeamSelectArgs a, int num_sms, cudaStream_t stream) {
   if (const cudaError_t e = fit_cluster<T, KL>(a.num_requests, &ctas)) return e;
   // The margin of two rows is twice the error of a row's sum in the pass, relative, all
   // roundings adding up (a step of fp32 is 2^-24): exponentials 4 steps, their arguments
-  // 1.3 |x - m| (a weighted mean of which is at most ln V, and kMove); the additions of a
+  // kArgSteps |x - m| (a weighted mean of which is at most ln V, and kMove); additions of a
   // lane, 10 and one for each load, a warp, a CTA and a cluster; rescalings by an
   // exponential, 5 and its argument's, once for a lane (a moved reference shrinks what came
   // before) and at each of the three; the logarithm's 2 ln V.
   const int64_t lane_loads =
       (static_cast<int64_t>(a.num_beams) * (a.blocks_per_row / ctas + 1) / kWarps + 1) << sh;
   const double ln_v = log(static_cast<double>(a.vocab));
-  const double err = 0x1p-24 * (4 + 1.3 * (kMove + ln_v) + 10 + static_cast<double>(lane_loads) +
-                                5 + 4 + 4 + 4 * (5 + 1.3 * kMove) + 2 * ln_v);
+  const double err =
+      0x1p-24 * (4 + kArgSteps * (kMove + ln_v) + 10 + static_cast<double>(lane_loads) + 5 + 4 +
+                 4 + 4 * (5 + kArgSteps * kMove) + 2 * ln_v);
   a.margin = static_cast<float>(err);  // (of values that are halved)
   // Where a second sum of two rows is likely (neighbours among the best candidates nearer
   // than the margin, one pair in a thousand or so) or takes long, the cluster stays for it:
