@@ -581,13 +581,14 @@ int pa_decode_shared(void *out, const void *q, const void *k_cache, const void *
  *   finished   device uint8 [num_requests, num_beams] or NULL (none is); a finished
  *              beam's logits are not read
  *   end_token  in [0, vocab_size); -1 (none) where finished is NULL
- * Values are compared to 1e-9 (in a row by the logits alone, so exactly); beams of
- * equal logits, in whatever order, have equal sums.  out_scores are within 2^-24 of
- * their size and 6e-6 + 5e-11 vocab_size of the value.  num_beams up to 32, num_choices
- * up to 64, num_beams * vocab_size up to 2^30.  With num_choices == num_beams,
- * out_scores and out_finished may be scores and finished themselves; outputs may
- * not overlap anything otherwise (PA_ERR_INVALID).  No workspace; equal calls give
- * equal bits, and calls may overlap freely.
+ * Values are compared to 1e-9 + 1.2e-15 vocab_size + 2^-45 (|s_w| + the row's largest
+ * |x|), in a row as by the logits wherever that tells them apart; beams of equal logits,
+ * in whatever order, have equal sums.  out_scores are within 2^-24 of their size and
+ * 1.3e-5 + 2.5e-10 vocab_size of the value (one fp32 pass, all its roundings adding up).
+ * num_beams up to 32, num_choices up to 64, num_beams * vocab_size up to 2^30.  With
+ * num_choices == num_beams, out_scores and out_finished may be scores and finished
+ * themselves; outputs may not overlap anything otherwise (PA_ERR_INVALID).  No
+ * workspace; equal calls give equal bits, and calls may overlap freely.
  */
 int pa_beam_select(int32_t *parents, int32_t *tokens, float *out_scores, uint8_t *out_finished,
                    const void *logits, int logits_fp32, int64_t request_stride,

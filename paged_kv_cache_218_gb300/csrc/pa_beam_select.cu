@@ -32,11 +32,12 @@
 // theirs), then those.
 //
 // Exactness.  Within a row the logits themselves give the order.  Between rows it
-// hangs on lse_w, which the pass knows to a bound: values are kept as sums
-// of two floats (48 bits), and where two beams' candidates around the choice are
-// nearer than twice that (`margin`), those rows' sums are taken again, to 1e-9: exponentials by
-// table and short polynomial (Tang's method), added as whole numbers, so that equal
-// logits in whatever order and place give equal sums.  The cluster's CTAs wait for their
+// hangs on lse_w, which the pass knows to a bound: values are kept as sums of two floats
+// (48 bits; halved, so that sums of far scores and logits stay within fp32), and where two
+// beams' candidates around the choice are nearer than twice that bound (`margin`), those
+// rows' sums are taken again, to 1e-9 and 1e-15 for each token: exponentials by table and
+// short polynomial (Tang's method), added as whole numbers, so that equal logits in
+// whatever order and place give equal sums.  The cluster's CTAs wait for their
 // share of that where it is likely (two rows of 131072 in fp32: 9 us more, one CTA 53;
 // 103 requests of 6 x 50497, two CTAs each, 58 us, of which 35 without doubts).
 //

@@ -151,3 +151,18 @@ def test_held_back_beams_cost_no_more_than_others(pa, low):
             times.append(a.elapsed_time(b))
         best.append(min(times))
     assert best[1] < 2 * best[0], best
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_scores_within_the_stated_bound(pa, dtype):
+    """One CTA for all 32 rows of a request, so that a lane sums as much as it ever does."""
+    R, W, V, K = 160, 32, 40000, 4
+    x = (3 * torch.randn((R, W, V), generator=gen(3), device="cuda")).to(dtype)
+    s = -5.0 * torch.rand((R, W), generator=gen(4), device="cuda")
+    c = Case(x, s, K)
+    c.run(pa)
+    lse = torch.stack([torch.logsumexp(y.double(), -1) for y in x])
+    at = torch.arange(R, device="cuda")[:, None], c.parents.long(), c.tokens.long()
+    value = s.double()[at[:2]] + x[at].double() - lse[at[:2]]
+    bound = 2.0**-24 * value.abs() + 1.3e-5 + 2.5e-10 * V
+    assert ((c.out_scores.double() - value).abs() <= bound).all()
