@@ -89,7 +89,8 @@ struct Item {
   int kvh;
   int q0, tokens;  // the unit's first member, and how many
   int block0;      // first block of the piece
-  int nvb;         // blocks to read
+  int nvb;         // blocks to load, one at least
+  int ids;         // and how many of them some member sees: no other table entry is read
   int keys;        // keys [0, keys) of the sequence are the prefix
   int hidden;      // rows of the last block from this one on are seen by no member; or 16
   int slot;        // of the results
@@ -191,7 +192,8 @@ __device__ __forceinline__ Item next_item(const SharedArgs& a, Cursor& cur, Grou
     it.whole = __reduce_min_sync(0xffffffffu, least) >= it.keys;
     // (one block at least, so that there are scores)
     const int left = ((seen + 15) >> 4) - it.block0;
-    it.nvb = min(max(left, 1), min(8 * n, blocks - it.block0));
+    it.ids = min(max(left, 0), min(8 * n, blocks - it.block0));
+    it.nvb = max(it.ids, 1);
     it.nkt = (it.nvb + 7) >> 3;
     it.hidden = min(max(seen - (it.block0 + it.nvb - 1) * kBlockSize, 0), kBlockSize);
     break;
@@ -229,21 +231,21 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
 // Ids of an item's blocks [8 t_first, + 8 kIdBatch) into a loader's
 // ring, where the ids of the warp's tile T are at slot T % kIdRing and `base` is
 // the number of the item's tile 0.  A slot is rewritten only when its tile's
-// loads have been issued.  Ids past the list are -1, a box outside the pool,
+// loads have been issued.  Ids past the list (nid of them) are -1, a box outside the pool,
 // which reads as zeros.  Called by a whole warp.
 __device__ __noinline__ void fetch_ids(const int32_t* table, int64_t num_blocks, unsigned int* err,
-                                       int* ids, int nvb, int t_first, unsigned base) {
+                                       int* ids, int nid, int t_first, unsigned base) {
   const int lane = threadIdx.x & 31;
   int v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int vb = t_first * 8 + lane + 32 * i;
-    v[i] = vb < nvb ? __ldcg(table + vb) : -1;
+    v[i] = vb < nid ? __ldcg(table + vb) : -1;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int vb = t_first * 8 + lane + 32 * i;
-    if (vb < nvb && (v[i] < 0 || v[i] >= num_blocks)) {
+    if (vb < nid && (v[i] < 0 || v[i] >= num_blocks)) {
       atomicOr(err, PA_DEVERR_BLOCK_ID);
       v[i] = -1;
     }
@@ -420,7 +422,7 @@ __global__ void __launch_bounds__(512, 1)
         if (more || (!next_ids && jf >= it.nkt && it.nkt - jk <= kIdBatch)) {
           const Item& x = more ? it : next;
           fetch_ids(a.block_tables + static_cast<int64_t>(x.row) * a.max_blocks + x.block0,
-                    a.num_blocks, a.err, ids_smem, x.nvb, more ? jf : 0,
+                    a.num_blocks, a.err, ids_smem, x.ids, more ? jf : 0,
                     total - jk + (more ? 0 : it.nkt));
           if (more)
             jf += kIdBatch;
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(512, 1)
           const Item* x = ring_item(more ? k - 1 : k);
           if (x->nkt)
             fetch_ids(a.block_tables + static_cast<int64_t>(x->row) * a.max_blocks + x->block0,
-                      a.num_blocks, a.err, ids_smem, x->nvb, more ? jf : 0,
+                      a.num_blocks, a.err, ids_smem, x->ids, more ? jf : 0,
                       total - jv + (more ? 0 : it.nkt));
           if (more)
             jf += kIdBatch;
