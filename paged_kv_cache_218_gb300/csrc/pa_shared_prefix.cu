@@ -782,11 +782,12 @@ __global__ void __launch_bounds__(512, 1)
       const int mine = rank * tpt + tok;  // member of the unit
       const bool here = !last && tok < tpt && mine < it.tokens;
       const bool active = __any_sync(0xffffffffu, here);
-      // last key of the piece that the row sees
+      // last key of the piece that the row sees (a length below zero, which the decode of
+      // the own parts reports, is none)
       int hi = -1;
       if (here)
-        hi = (it.whole ? it.keys : min(__ldcg(a.seq_lens + it.q0 + mine), it.keys)) - 1 -
-             it.block0 * kBlockSize;
+        hi = (it.whole ? it.keys : max(min(__ldcg(a.seq_lens + it.q0 + mine), it.keys), 0)) -
+             1 - it.block0 * kBlockSize;
       const int64_t row =
           static_cast<int64_t>(it.slot) * a.lay.slot_rows + rank * tpt * G + r;
       // reference maximum: a score, in log2 units, and as the softmax subtracts it
