@@ -59,6 +59,15 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
     if (reports) atomicOr(a.err, PA_DEVERR_SEQ_LEN);
     len = len < 0 ? 0 : cap;
   }
+  // ---- the beam's first own block, and whether another beam has the same (rows of a fork
+  // do until their last blocks are copied): nobody's to give away
+  const int32_t* const tables = a.tables + static_cast<int64_t>(r) * W * a.max_blocks;
+  const int own_col = len / kBlockSize;
+  const int own = here && own_col < a.max_blocks
+                      ? tables[static_cast<int64_t>(lane) * a.max_blocks + own_col]
+                      : -1;
+  const unsigned like = __match_any_sync(0xffffffffu, own);
+  const int taken = own >= 0 && (like & (like - 1)) != 0;
   const unsigned before = (1u << lane) - 1;
   const unsigned siblings = __match_any_sync(0xffffffffu, parent);
   const bool child = here && parent >= 0;
@@ -81,20 +90,16 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
   if (reports && here) a.out_lens[row] = new_len;
 
   // ---- copies: lane i's source and destination block, and vectors to copy
-  const int32_t* const tables = a.tables + static_cast<int64_t>(r) * W * a.max_blocks;
   int32_t* const out = a.out_tables + static_cast<int64_t>(r) * W * a.max_blocks;
   const int filled = new_len % kBlockSize;
-  int src = 0, dst = 0;
-  bool copy = child && !first && filled > 0 && a.num_layers > 0;
-  if (copy) {
-    const int own_col = owner_len / kBlockSize;
-    src = tables[static_cast<int64_t>(parent) * a.max_blocks + keep];
-    dst = own_col < a.max_blocks ? tables[static_cast<int64_t>(owner) * a.max_blocks + own_col]
-                                 : -1;
-    if (src < 0 || src >= a.num_blocks || dst < 0 || dst >= a.num_blocks) {
-      if (reports) atomicOr(a.err, PA_DEVERR_BLOCK_ID);
-      copy = false;
-    }
+  const int src = __shfl_sync(0xffffffffu, own, from);
+  const int dst = __shfl_sync(0xffffffffu, own, owner);
+  const bool extra_child = child && !first;
+  bool copy = extra_child && filled > 0 && a.num_layers > 0;
+  if ((__shfl_sync(0xffffffffu, taken, owner) && extra_child) ||
+      (copy && (src < 0 || src >= a.num_blocks || dst < 0 || dst >= a.num_blocks))) {
+    if (reports) atomicOr(a.err, PA_DEVERR_BLOCK_ID);
+    copy = false;
   }
   // what every thread needs of each beam
   __shared__ int4 row_of[kMaxBeams];  // history's row, own row, history's blocks, shift
