@@ -622,9 +622,8 @@ int pa_beam_select(int32_t *parents, int32_t *tokens, float *out_scores, uint8_t
  * num_beams * max_blocks_per_seq up to 2^30; head_dim a multiple of 8.  A parent
  * outside [-1, num_beams) sets PA_DEVERR_BEAM and counts as -1, a length outside its
  * row PA_DEVERR_SEQ_LEN and is clamped; a copy from or to a block outside the pool
- * sets PA_DEVERR_BLOCK_ID and is left out, and so is one where a child would get own
- * blocks whose first another beam of the request has as well (flagged with nothing to
- * copy, too: both beams would write their next tokens there).
+ * sets PA_DEVERR_BLOCK_ID and is left out, and so is one into a block that another beam
+ * of the request has as its own, too (with num_layers 0 it is flagged as well).
  */
 int pa_beam_reorder(int32_t *out_tables, int32_t *out_lens, const int32_t *block_tables,
                     const int32_t *seq_lens, const int32_t *parents, int num_requests,

@@ -94,9 +94,9 @@ __global__ void __launch_bounds__(kThreads) beam_reorder_kernel(const BeamReorde
   const int filled = new_len % kBlockSize;
   const int src = __shfl_sync(0xffffffffu, own, from);
   const int dst = __shfl_sync(0xffffffffu, own, owner);
-  const bool extra_child = child && !first;
-  bool copy = extra_child && filled > 0 && a.num_layers > 0;
-  if ((__shfl_sync(0xffffffffu, taken, owner) && extra_child) ||
+  const bool begun = child && !first && filled > 0;
+  bool copy = begun && a.num_layers > 0;
+  if ((__shfl_sync(0xffffffffu, taken, owner) && begun) ||
       (copy && (src < 0 || src >= a.num_blocks || dst < 0 || dst >= a.num_blocks))) {
     if (reports) atomicOr(a.err, PA_DEVERR_BLOCK_ID);
     copy = false;
