@@ -1665,9 +1665,10 @@ static int decode_shared_impl(void* out, const void* q, const void* k_cache, con
   a.scale_log2 = scale * 1.4426950408889634f;
   // A small batch takes one launch, each sequence reading all its keys: the second
   // pass costs more than the prefixes read again from L2.  Bytes of keys and values are
-  // bounded by the tables' width.  (us, this way / with the prefix apart: 17 MB 6.0 /
-  // 12.0 to 13.6; 70 MB 9.1 to 10.3 / 12.6 to 14.9; 117 and 140 MB in many groups 16 and
-  // 17 / 36 and 24, 134 MB in one of two 25.5 / 22.0; 270 MB 24 to 28 / 15 to 22.)
+  // bounded by the tables' width: the host knows no lengths.  (us, this way / with the
+  // prefix apart: 17 MB 5.9 / 11.9; 70 MB 8.9 to 9.9 / 13.1 to 14.5; 110 MB in 20 groups of
+  // 2 18.5 / 23.0, in 12 of 4 18.8 / 16.2; 134 MB in one group 16.9 / 16.5; 270 MB in 16
+  // groups 29.6 / 25.6, in one 28.4 / 17.4.)
   const int64_t bytes = static_cast<int64_t>(num_seqs) * max_blocks_per_seq * num_kv_heads * 8192;
   if (!stall_loads && bytes <= int64_t{96} << 20)
     return launch_decode_window(a, head_dim, d->num_sms, static_cast<cudaStream_t>(stream)) ==

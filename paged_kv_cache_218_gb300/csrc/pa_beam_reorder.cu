@@ -12,9 +12,9 @@
 // beam with children gives up one of W and takes one of W.
 //
 // What bounds it: HBM, by the bytes copied: 64 requests of 4 beams in 32 layers of 8 heads
-// of 128 (84 MB, read and written) take 31.2 us, 5.4 TB/s, 81 % of what a plain copy
-// reaches; one request 4.5 us, a launch and four dependent round trips.  A beam's filled slots of one
-// layer are contiguous in each pool, so a copy is a run of up to 15 token
+// of 128 (84 MB, read and written) take 31.3 us, 5.4 TB/s, 81 % of what a plain copy
+// reaches; one request 4.5 us, a launch and four dependent round trips.  A beam's filled
+// slots of one layer are contiguous in each pool, so a copy is a run of up to 15 token
 // rows; a warp reads its share of a run, 16 bytes a lane and eight of them
 // under way, before it writes.  The mapping is a few ballots of a warp, which
 // every warp makes for itself rather than wait for another.

@@ -12,9 +12,9 @@
 // near behind (11 elements per cycle and SM arrive, 16 exponentials leave).  So
 // the pass does as little as it can per element: its exponential for the sum, and
 // a maximum.  Behind it comes a chain of short steps on one SM.  64 requests of
-// 4 x 131072 in bf16 (67 MB) take 19.8 us, 12.7 of them the pass (6.3 TB/s once it
-// runs) and 5.6 the choice; 16 of 16 x 131072 in fp32 (134 MB) 32.9; one of 4 x 32000
-// 6.6, a launch and some eight dependent round trips.
+// 4 x 131072 in bf16 (67 MB) take 19.6 us, 12.7 of them the pass (6.3 TB/s once it
+// runs) and 5.6 the choice; 16 of 16 x 131072 in fp32 (134 MB) 32.4; one of 4 x 32000
+// 6.5, a launch and some eight dependent round trips.
 //
 // A cluster serves a request, its CTAs take a share of every row, a warp 1024 bf16 (512
 // fp32) elements at a time, twice 32 bytes a lane; the maxima of such blocks and the rows'
@@ -38,7 +38,7 @@
 // rows' sums are taken again, to 1e-9 and 1e-15 for each token: exponentials by table and
 // short polynomial (Tang's method), added as whole numbers, so that equal logits in
 // whatever order and place give equal sums.  The cluster's CTAs wait for their
-// share of that where it is likely (two rows of 131072 in fp32: 9 us more, one CTA 53;
+// share of that where it is likely (two rows of 131072 in fp32: 14 us more, one CTA 53;
 // 103 requests of 6 x 50497, two CTAs each, 58 us, of which 35 without doubts).
 //
 // NaN and +inf logits count as -inf: no candidates, no part of the sum.
@@ -1171,7 +1171,8 @@ cudaError_t launch(BeamSelectArgs a, int num_sms, cudaStream_t stream) {
                  4 + 4 * (5 + kArgSteps * kMove) + 2 * ln_v);
   a.margin = static_cast<float>(err);  // (of values that are halved)
   // Where a second sum of two rows is likely (neighbours among the best candidates nearer
-  // than the margin, one pair in a thousand or so) or takes long, the cluster stays for it:
+  // than the margin: 3 of 100 calls of 16 requests of 16 x 131072, 32 choices; nearly all of
+  // 103 of 6 x 50497, 57 choices) or takes long, the cluster stays for it:
   // 0.5 us of every call (64 of 4 x 131072 19.8 / 19.3, 37 of 3 x 50001 10.3 / 9.7),
   // against 53 us of one CTA's time for two rows of 131072 in fp32.
   a.all_sum = static_cast<int64_t>(a.num_requests) * a.num_choices * a.vocab >= 1 << 21;

@@ -94,7 +94,7 @@ __device__ __forceinline__ int4 find_group(const SharedArgs& a, int s, int lane)
 
 // Teams that take part: with at least four key tiles each where there are as many (the
 // others' SMs are free for the sequences' own parts meanwhile: nine ragged groups of up
-// to 37 blocks 31.8 us, with one tile 34.6, with eight 34.5).  None has an empty range.
+// to 37 blocks 31.6 us, with one tile 34.4, with eight 37.1).  None has an empty range.
 __device__ __forceinline__ int shared_teams(const SharedLayout& lay, int tiles) {
   return min(lay.teams, max((tiles + 3) / 4, 1));
 }

@@ -23,12 +23,14 @@
 //  * Warps whose 32 rows no member fills wait for scores and pass them on unread.
 //  * P is the sum of two bf16 numbers (to 2^-16 of itself), as in the decode of the own
 //    parts, so that the output does not depend on which of both reads a key.  One bf16
-//    took 78 / 81 / 57 us in the cases below.  Of groups of up to 16 rows the lower parts
-//    are rows of their own beside the upper ones, multiplied at no cost, and their lanes
-//    take half of the exponentials (with two products instead 90 us for 82).
+//    took 78 / 57 / 81 us in the cases below, and 0.79 a tile of 256 rows.  Of groups of up
+//    to 16 rows the lower parts are rows of their own beside the upper ones, multiplied at
+//    no cost, and their lanes take half of the exponentials (with two products instead 90
+//    us for 82).
 //
 // What bounds it: HBM.  In the steady state lone CTAs read 7.3 TB/s (0.65 us for every
-// 72 tiles of 64 KB), pairs with 256 rows wait for the tensor pipe and its hand-overs.
+// 72 tiles of 64 KB); pairs take 1.14 us a tile for 256 rows, 1.6 PFLOP/s of their three
+// products (of 1.88 that a library product reaches).
 // The first 8 us go to round trips: offsets, lengths, block ids, keys.
 // With 32 query and 8 kv heads of 128: 64 groups of 4 sequences behind 256 to 2048 tokens
 // (392 MB with their own parts) 82 us, 4.8 TB/s; 32 sequences behind 65536 (273 MB) 59 us;
@@ -986,10 +988,12 @@ cudaError_t launch_shared_prefix(const SharedArgs& args, const CUtensorMap* tm_q
   SharedArgs a = args;
   if (a.wait_ns == 0) a.wait_ns = kWaitLimitNs;
   if (a.lay.worker_ctas == 2) return launch_workers<2, 0>(a, tm_q, tm_k, tm_v, stream);
-  // Up to 16 query rows: the next item's Q tile in front of its turn.  (us with 4 query
-  // heads a kv head, with / without: 200 groups of 4 sequences behind 256 tokens 76.8 /
-  // 83.8, 64 of 4 behind 1024 59.6 / 61.8, 12 of 4 behind 2048 25.7 / 26.0; with room for
-  // 64 rows, 40 groups of 8 behind 256 28.8 / 27.9, 20 of 8 behind 2048 42.3 / 41.2.)
+  // Up to 16 query rows: the next item's Q tile in front of its turn, and the weights' lower
+  // parts as rows of their own.  (us with 4 query heads a kv head, with / without: 200
+  // groups of 4 sequences behind 256 tokens 82.0 / 90.4, 64 of 4 behind 1024 61.3 / 68.5,
+  // 12 of 4 behind 2048 28.6 / 31.2.  A Q tile ahead for up to 64 rows gained nothing: 40
+  // groups of 8 behind 256 28.8 / 27.9, 20 of 8 behind 2048 42.3 / 41.2, when weights were
+  // one bf16.)
   if (a.lay.box_tokens * a.group <= 16) return launch_workers<1, 16>(a, tm_q, tm_k, tm_v, stream);
   return launch_workers<1, 0>(a, tm_q, tm_k, tm_v, stream);
 }
@@ -1122,8 +1126,9 @@ cudaError_t launch_join(const SharedArgs& a, __nv_bfloat16* out, float* out_lse,
 cudaError_t launch_shared_join(const SharedArgs& a, __nv_bfloat16* out, float* out_lse,
                                cudaStream_t stream) {
   // Few rows behind a long prefix have a piece from every team: four warps on each.  (us
-  // of a call, four warps / one: 512 rows behind 16384 tokens 20.4 / 21.8, 608 behind
-  // 32768 36.6 / 38.7; 5120 rows 47.7 / 45.6, 8192 64.8 / 60.0, 3200 the same.)
+  // of a call, four warps / one: 512 rows behind 16384 tokens 26.9 / 27.9, 608 behind
+  // 32768 38.4 / 39.6; 5120 rows behind 2048 31.7 / 29.3, 8192 behind 4096 44.1 / 39.2, 3200
+  // the same.)
   const int64_t rows = static_cast<int64_t>(a.num_seqs) * a.num_q_heads;
   return rows <= 2048 ? launch_join<4>(a, out, out_lse, stream)
                       : launch_join<1>(a, out, out_lse, stream);

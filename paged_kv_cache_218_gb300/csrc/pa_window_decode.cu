@@ -48,9 +48,10 @@
 //
 // So does the decode of sequences that share prefixes, for what is each one's own:
 // the blocks behind its group's prefix.  It runs beside the prefix pass, whose CTAs leave
-// room for two warps' rings on each SM, and reads nothing of it; a third kernel joins
-// both (pa_shared_prefix.cu).  Alone it reads 294 MB of 256 sequences in 54 us; beside the
-// pass a block takes a warp 2 us instead of 1.
+// room on each SM for the rings of two warps (beside a lone CTA) or four (beside one of a
+// pair), and reads nothing of it; a third kernel joins both (pa_shared_prefix.cu).  Alone
+// it reads 294 MB of 256 sequences in 54 us.  Beside the pass a CTA of one warp lives 20 us
+// for 17 blocks, 9 for 4 or 5: 5 us for its chain of round trips, 0.9 a block.
 #include <float.h>
 #include <math.h>
 
@@ -83,7 +84,7 @@ __device__ __forceinline__ float bf16_round(float x) {
 }
 
 // Blocks in flight per warp; two where two warps have a unit behind a shared prefix, so
-// that both fit beside the prefix pass.
+// that both fit beside a lone CTA of the prefix pass.
 template <int W, int M>
 constexpr int kStages = 3;
 template <>
@@ -647,10 +648,10 @@ cudaError_t launch_shared_decode(const SharedDecodeArgs& args, int num_sms, cuda
   // How long a sequence's own part is, the host does not know.  Eight warps on each up to
   // one on every SM; above, as many as run at once, and few enough to start beside the
   // prefix pass.  (us of a call behind 8192 shared tokens, 8 kv heads, with 8 / 4 / 2 / 1
-  // warps: 16 sequences of up to 64 tokens of their own 16.7 / 15.8 / 16.6 / 16.6, 1200
-  // 28.8 / 30.5 / 36.9 / 44.5, 5000 66 / 69 / 105 / 137; 64 of 64 28.2 / 22.3 / 21.4 / 21.0,
-  // of 1200 73.6 / 67.8 / 67.8 / 65.6, of 5000 210 / 204 / 209 / 227; 110 of 300 57.0 /
-  // 45.6 / 43.9 / 47.9; 256 of 40 81.2 / 52.2 / 46.4 / 45.9.)
+  // warps: 16 sequences of 1 to 64 tokens of their own 20.2 / 19.6 / 19.8 / 19.9, to 1200
+  // 27.1 / 30.2 / 37.6 / 45.5, to 5000 49 / 66 / 102 / 135; 64 to 64 34.1 / 27.1 / 25.8 /
+  // 25.2, to 1200 55.1 / 48.8 / 57.6 / 55.8, to 5000 139 / 137 / 162 / 164; 110 to 300 55.2 /
+  // 43.6 / 45.6 / 45.5; 256 to 40 88.8 / 64.7 / 61.9 / 57.5.)
   const int64_t units = static_cast<int64_t>(a.num_seqs) * a.num_kv_heads;
   if (units <= num_sms) return launch<128, 8, kShared>(a, stream);
   if (units <= 6 * num_sms) return launch<128, 2, kShared>(a, stream);
